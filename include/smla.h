@@ -29,6 +29,19 @@
  *   smla_topk_select                  per row (per rank: as global ids)
  *   smla_dcp_topk_merge               top-k of the ranks' candidates
  *
+ * and the rest of a serving step, over the 8-bit or a 4-bit cache:
+ *
+ *   smla_dcp_step_maps                request ids, positions, slots and new
+ *                                     block-table entries from the requests'
+ *                                     lengths
+ *   smla_mla_cache_write              latent norm, rotary positions,
+ *                                     quantisation and scatter into the cache
+ *   smla_mla_cache_gather             cache rows back to bf16 or fp32
+ *   smla_sparse_mla_decode_fp4, smla_dcp_sparse_mla_decode_fused_fp4
+ *                                     step 2 and steps 1-3 over fp4 rows
+ *   smla_dcp_window_mla_decode        the dense decode limited to a sliding
+ *                                     window and a few first tokens (sinks)
+ *
  * Sources (page title, then section):
  *   [P1] "[eldritch] attention: support DCP in SM120 FlashInfer sparse MLA"
  *   [P2] "[Bugfix][Attention] Stabilize sparse-MLA DCP for GLM PCP evals"
@@ -84,10 +97,13 @@ enum {
   SMLA_DEVERR_REQ_ID = 2u,      /* req_id_per_token outside [0, num_reqs)      */
   SMLA_DEVERR_SLOT_RANGE = 4u,  /* local slot >= num_slots                     */
   SMLA_DEVERR_TIMEOUT = 8u,     /* a bounded wait inside a kernel gave up      */
-  SMLA_DEVERR_CONTEXT = 16u,    /* dense decode: a context shorter than its
-                                   request's query tokens or past max_ctx     */
-  SMLA_DEVERR_RANGE = 32u       /* a q or rope value, or a latent group scale,
+  SMLA_DEVERR_CONTEXT = 16u,    /* a context shorter than its request's query
+                                   tokens or past max_ctx; step maps: that, a
+                                   negative length or more rows than T        */
+  SMLA_DEVERR_RANGE = 32u,      /* a q or rope value, or a latent group scale,
                                    that the fp16 keys cannot carry (below)    */
+  SMLA_DEVERR_FREE_BLOCKS = 64u, /* step maps: the free list is too short     */
+  SMLA_DEVERR_POSITION = 128u   /* cache write: a position outside the table  */
 };
 /* The decode kernels compute QK^T and PV on fp16 operands: q and the rope
  * values are converted from bf16 and each latent value is dequantised as
@@ -96,7 +112,9 @@ enum {
  * group scale exceeds 65504 / 448 (its dequantised values would overflow
  * fp16), or when a nonzero scale is below 2^-22 (its keys would be fp16
  * subnormals and lose precision).  The result is still written; the bit says
- * it may be outside the stated tolerances. */
+ * it may be outside the stated tolerances.  An fp4 row's latent values are
+ * exact in fp16; for those rows the bit stands for the q and rope values and
+ * for a NaN scale. */
 /* With SMLA_DEVERR_TIMEOUT, bits 8..31 of the word tell which of the decode
  * kernel's internal waits gave up (a diagnostic bitmask, one bit per site). */
 
@@ -109,6 +127,15 @@ enum {
 #define SMLA_ROW_BYTES 656
 #define SMLA_QK_DIM 576
 #define SMLA_V_DIM 512
+
+/* Packed 4-bit row: 256 bytes of e2m1 codes (byte i holds dim 2i in its low
+ * nibble, dim 2i + 1 in its high one) | 32 e4m3 scales, scale g for dims
+ * 16g .. 16g + 15 | 64 bf16 rope.  Latent dim c = e2m1(code c) *
+ * e4m3(scale[c div 16]); e2m1 is sign, 2 exponent and 1 mantissa bits: 0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives. */
+#define SMLA_FP4_ROW_BYTES 416
+/* Row formats, where a call takes either. */
+enum { SMLA_CACHE_FP8 = 0, SMLA_CACHE_FP4 = 1 };
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* smla_status_string(smla_status status);
@@ -455,6 +482,171 @@ smla_status smla_dcp_lse_merge(const uint16_t* const* outs,
                                const float* const* lses, int32_t D, int32_t T,
                                int32_t H, uint16_t* out, float* lse,
                                void* stream);
+
+/*
+ * Steps 1-3 over fp4 rows (SMLA_FP4_ROW_BYTES each).
+ *
+ * smla_sparse_mla_decode_fp4 is smla_sparse_mla_decode and
+ * smla_dcp_sparse_mla_decode_fused_fp4 is smla_dcp_sparse_mla_decode_fused
+ * with the pools' rows in the 4-bit format: same arguments, results, errors
+ * and workspace rules (smla_fp4_decode_workspace_size gives the size).
+ * smla_dcp_filter_convert_index and smla_dcp_lse_merge do not read cache
+ * rows and serve either format.  The latent keys are exact in the kernel's
+ * fp16 operands.
+ */
+size_t smla_fp4_decode_workspace_size(int32_t T, int32_t H, int32_t K);
+smla_status smla_sparse_mla_decode_fp4(
+    const uint16_t* q, const uint8_t* kv_cache, int64_t num_slots,
+    const int32_t* local_slots, int32_t T, int32_t H, int32_t K,
+    float sm_scale, uint16_t* out, float* lse, void* workspace,
+    size_t workspace_bytes, void* stream);
+smla_status smla_dcp_sparse_mla_decode_fused_fp4(
+    const uint16_t* q, int32_t T, int32_t H, int32_t K, float sm_scale,
+    const int32_t* req_id_per_token, const int32_t* topk_global, int32_t num_reqs,
+    int32_t D, int32_t block_size, int32_t interleave, const uint8_t* const* kv_caches,
+    const int64_t* num_slots, const int32_t* const* block_tables,
+    const int64_t* bt_row_strides, const int32_t* bt_widths, uint16_t* out,
+    float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Windowed decode with sinks: smla_dcp_dense_mla_decode in which token s of
+ * request b, at position p = ctx_lens[b] - S + s, attends the positions
+ * t <= p with t < sinks or t > p - window (the last `window` positions, its
+ * own among them, and the request's first `sinks`).  A window of at least
+ * max_ctx is the dense decode.  Only those positions' block-table entries and
+ * cache rows are read: blocks behind the window may have been given back.
+ *
+ *   window       >= 1
+ *   sinks        >= 0
+ *   format       SMLA_CACHE_FP8 or SMLA_CACHE_FP4: the rows of every pool
+ *   workspace    >= smla_window_decode_workspace_size(B*S, H, max_ctx, window,
+ *                sinks, D, interleave, rank) bytes, same rules as for
+ *                smla_sparse_mla_decode
+ *   the rest     as for smla_dcp_dense_mla_decode; a rank that holds none of
+ *                a token's positions returns (0, -inf) for it
+ * Errors: as smla_dcp_dense_mla_decode, plus INVALID_ARG for window < 1,
+ * sinks < 0 or another format.
+ */
+size_t smla_window_decode_workspace_size(int32_t T, int32_t H, int32_t max_ctx, int32_t window,
+                                         int32_t sinks, int32_t D, int32_t interleave,
+                                         int32_t rank);
+smla_status smla_dcp_window_mla_decode(
+    const uint16_t* q, int32_t B, int32_t S, int32_t H, float sm_scale,
+    const int32_t* ctx_lens, int32_t max_ctx, int32_t window, int32_t sinks, int32_t D,
+    int32_t rank, int32_t block_size, int32_t interleave, int32_t format,
+    const uint8_t* const* kv_caches, const int64_t* num_slots,
+    const int32_t* const* block_tables, const int64_t* bt_row_strides, const int32_t* bt_widths,
+    uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Step maps of one rank, from the requests' lengths: what a prefill, decode
+ * or mixed step needs to write its new tokens' cache rows and to run the
+ * calls above.
+ *
+ * Request b has ctx_lens[b] cached positions, its q_lens[b] new tokens
+ * included (0 <= q_lens[b] <= ctx_lens[b]).  Its rows are row_start[b] ..
+ * row_start[b + 1] - 1, row_start the exclusive sum of q_lens; row i of
+ * request b is position p = ctx_lens[b] - q_lens[b] + (i - row_start[b]).
+ *   req_id[i] = b, positions[i] = p
+ *   slots[i]  = this rank's cache slot of p (through block_table, as
+ *               smla_dcp_filter_convert_index maps it), -1 where another
+ *               rank holds p
+ *   rows i >= row_start[B] up to T (padding of a captured step): req_id 0,
+ *               position 0, slot -1
+ *   local_lens[b] = how many of the request's positions this rank holds
+ * The positions already cached fill the first ceil(count / block_size)
+ * columns of the request's block_table row on this rank; the columns the new
+ * tokens add are taken from free_blocks in request order, column order, and
+ * written to block_table.  *blocks_taken = how many, over all requests: the
+ * caller drops that many from the front of its free list.
+ *
+ *   ctx_lens, q_lens   device int32 [B]
+ *   free_blocks        device int32 [num_free], distinct block ids (NULL when
+ *                      num_free is 0)
+ *   block_table        device int32 [B, bt_row_stride], read and written
+ *   slots              device int32 [T] output; T is at least the sum of
+ *                      q_lens
+ *   row_start [B + 1], req_id [T], positions [T], local_lens [B],
+ *   blocks_taken [1]   device int32 outputs, each may be NULL
+ * No output may alias an input or another output.  A repeated call on the
+ * same lengths and free list writes the same values.
+ * Errors: INVALID_ARG for B < 0, T < 0, D < 1, rank outside [0, D),
+ * block_size < 1, interleave < 1, num_free < 0, bt_width < 1 or
+ * bt_row_stride < bt_width, a NULL array that is needed, misaligned arrays;
+ * UNSUPPORTED for B > SMLA_MAX_STEP_REQS.  B = 0 and T = 0 is a no-op.  On
+ * the device, lengths outside 0 <= q <= ctx count as no new tokens and set
+ * SMLA_DEVERR_CONTEXT, as does a sum of q_lens past T (the rows that fit are
+ * written); a free list that is too short leaves -1 in block_table and slots
+ * and sets SMLA_DEVERR_FREE_BLOCKS; a column past bt_width, an unallocated or
+ * negative block and a slot past 2^31 - 1 give slot -1 and set
+ * SMLA_DEVERR_BLOCK_TABLE.
+ */
+#define SMLA_MAX_STEP_REQS 8192
+smla_status smla_dcp_step_maps(
+    const int32_t* ctx_lens, const int32_t* q_lens, int32_t B, int32_t T, int32_t D, int32_t rank,
+    int32_t block_size, int32_t interleave, const int32_t* free_blocks, int32_t num_free,
+    int32_t* block_table, int64_t bt_row_stride, int32_t bt_width, int32_t* row_start,
+    int32_t* req_id, int32_t* positions, int32_t* slots, int32_t* local_lens,
+    int32_t* blocks_taken, void* stream);
+
+/*
+ * Cache write: a step's latent rows, normalised, rotated and quantised into
+ * the packed cache at their slots.
+ *
+ * For row i with slots[i] >= 0, latent x = kv[i, 0:512] and rope part
+ * z = kv[i, 512:576]:
+ *   y = x * gamma / sqrt(mean(x^2) + eps)  (gamma NULL: y = x)
+ *   fp8 row: scale[g] = fp32(max |y| / 448) over dims 128g .. 128g + 127,
+ *            codes = e4m3(y / scale)
+ *   fp4 row: scale[g] = e4m3(max |y| / 6) over dims 16g .. 16g + 15,
+ *            codes = e2m1(y / scale)
+ *            (nearest, ties to even, past the largest code to the largest)
+ *   rope:    each pair (a, b) becomes (a c - b s, a s + b c), rounded to bf16,
+ *            with c = cos_sin[positions[i], j], s = cos_sin[positions[i],
+ *            32 + j] for pair j (cos_sin NULL: copied as it is); pair j is
+ *            values (2j, 2j + 1) when rope_pairs != 0, else (j, j + 32)
+ * Scales and codes are rounded once, from the quotients above computed to
+ * about 45 bits; a group whose scale is 0 (fp8: or below 2^-126) has zero
+ * codes.  A group with a value that is not finite, and every group of a
+ * normalised row with a latent that is not finite or a sum of squares past
+ * fp32, gets a NaN scale.  Rows with slot -1 write nothing; the slots of one
+ * call are distinct (a slot given twice ends with an undefined mix of its
+ * rows).
+ *
+ *   kv          device bf16, row i at kv + i * kv_row_stride (elements; a
+ *               multiple of 8, at least 576), 16-byte aligned
+ *   gamma       device bf16 [512], 16-byte aligned, or NULL
+ *   positions   device int32 [T] (may be NULL without cos_sin)
+ *   cos_sin     device fp32 [num_positions, 64] or NULL
+ *   slots       device int32 [T]
+ *   format      SMLA_CACHE_FP8 or SMLA_CACHE_FP4
+ *   kv_cache    device uint8 [num_slots, 656 or 416], 16-byte aligned
+ * Errors: INVALID_ARG for T < 0, num_slots < 0, another format, a bad stride,
+ * eps not finite and positive (with gamma), num_positions < 1 (with cos_sin),
+ * NULL or misaligned arrays.  On the device a slot >= num_slots sets
+ * SMLA_DEVERR_SLOT_RANGE and a position outside [0, num_positions) of a row
+ * with a slot sets SMLA_DEVERR_POSITION; such a row writes nothing.
+ */
+smla_status smla_mla_cache_write(
+    const uint16_t* kv, int64_t kv_row_stride, int32_t T, const uint16_t* gamma, float eps,
+    const int32_t* positions, const float* cos_sin, int32_t num_positions, int32_t rope_pairs,
+    const int32_t* slots, int32_t format, uint8_t* kv_cache, int64_t num_slots, void* stream);
+
+/*
+ * Cache gather: row slots[n] of the cache, dequantised, as row n of `out`
+ * (512 latent values, then 64 rope values; bf16, rounded once, or fp32) --
+ * the cached context of a prefill chunk, for instance.  Slot -1 gives a row
+ * of zeros; so does a slot >= num_slots, which sets SMLA_DEVERR_SLOT_RANGE.
+ *
+ *   slots           device int32 [N], any order, repeats allowed
+ *   out             device bf16 (out_fp32 = 0) or fp32 [N, 576], row n at
+ *                   n * out_row_stride elements (at least 576; a multiple of
+ *                   8, of 4 for fp32), 16-byte aligned
+ *   the rest        as for smla_mla_cache_write
+ */
+smla_status smla_mla_cache_gather(const uint8_t* kv_cache, int64_t num_slots, int32_t format,
+                                  const int32_t* slots, int32_t N, void* out,
+                                  int64_t out_row_stride, int32_t out_fp32, void* stream);
 
 #ifdef __cplusplus
 } /* extern "C" */

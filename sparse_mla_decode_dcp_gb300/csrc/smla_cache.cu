@@ -1,0 +1,387 @@
+// The packed cache's other side: writing a step's latent rows into it (norm,
+// rotary positions, quantisation and scatter in one pass) and gathering rows
+// back to bf16 or fp32.
+//
+// Write.  For token t with latent x (512) and rope part z (64):
+//   y = x g / sqrt(mean(x^2) + eps)          (g = gamma; y = x without one)
+//   rope pair (a, b) at angle (c, s) -> (a c - b s, a s + b c)
+//   fp8 row: per 128 dims scale = fp32(max|y| / 448), code = e4m3(y / scale)
+//   fp4 row: per 16 dims scale = e4m3(max|y| / 6), code = e2m1(y / scale)
+// Every rounding to a code or a stored scale is of the exact quotient: the
+// products x g of two bf16 are exact in fp32, and everything else runs in
+// pairs of fp32 (value and remainder), about 45 bits, rounded to odd before
+// the conversion, so that a quotient next to a rounding border lands on the
+// side 64-bit arithmetic puts it.  An fp32 quotient would put about one code
+// in 10^6 on the other side, a whole step of e2m1 (up to a third of the
+// value).  fp64 would do too but runs at about 1/60 of the fp32 rate here.
+//
+// One warp per row: a lane owns 16 consecutive latent dims (one fp4 group, an
+// eighth of an fp8 group) and one rope pair.
+//
+// Gather.  One warp per row, 8 dims per lane and step, so that every store is
+// 16 consecutive bytes a lane; kRows rows at once keep their loads in flight
+// together.  Bound by HBM: row + 4 bytes in, 1152 (bf16) or 2304 (fp32) out.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include "../../include/smla.h"
+#include "smla_internal.h"
+
+namespace smla {
+namespace {
+
+__device__ unsigned int g_cache_error;
+
+constexpr int kWarps = 8;
+
+// A value as the unevaluated sum of two fp32.
+struct Pair {
+  float hi, lo;
+};
+
+// Exact sum of two fp32 (Knuth's two-sum).
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b);
+  const float bb = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
+}
+
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+  const Pair s = two_sum(a.hi, b.hi);
+  const float lo = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo));
+  const float hi = __fadd_rn(s.hi, lo);
+  return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
+}
+
+// a / d for an fp32 divisor; hi is the nearest fp32.
+__device__ __forceinline__ Pair pair_div(Pair a, float d) {
+  const float q = __fdiv_rn(a.hi, d);
+  const float rem = __fadd_rn(__fmaf_rn(-q, d, a.hi), a.lo);  // zero when q is exact
+  const float c = __fdividef(rem, d);
+  const float hi = __fadd_rn(q, c);
+  return {hi, __fsub_rn(c, __fsub_rn(hi, q))};
+}
+
+// x * p for an fp32 factor.
+__device__ __forceinline__ Pair pair_mul(float x, Pair p) {
+  const float v = __fmul_rn(x, p.hi);
+  return {v, __fadd_rn(__fmaf_rn(x, p.hi, -v), __fmul_rn(x, p.lo))};
+}
+
+// hi + lo rounded to odd in fp32: truncated toward zero, last bit set when
+// anything was cut off.  Rounding that once more to a format of at most 22
+// bits equals rounding hi + lo itself.
+__device__ __forceinline__ float round_odd(Pair p) {
+  if (p.lo == 0.f) return p.hi;
+  uint32_t b = __float_as_uint(p.hi);
+  if ((p.lo < 0.f) != (p.hi < 0.f)) --b;  // |hi + lo| < |hi|
+  return __uint_as_float(b | 1u);
+}
+
+// a / d rounded to odd, inv = 1 / d in fp32: the quotient is corrected once,
+// to the nearest fp32, and what is left of a then has the sign of the part
+// that was cut off (zero, exactly, when nothing was).
+__device__ __forceinline__ float quotient_odd(Pair a, float d, float inv) {
+  const float v = __fmul_rn(a.hi, inv);
+  const float q = __fmaf_rn(__fadd_rn(__fmaf_rn(-v, d, a.hi), a.lo), inv, v);
+  return round_odd({q, __fadd_rn(__fmaf_rn(-q, d, a.hi), a.lo)});
+}
+
+// 1 / sqrt(m): one Newton step from the fp32 reciprocal square root, its
+// residual 1 - m r^2 formed exactly enough with fused multiply-adds.
+__device__ __forceinline__ Pair pair_rsqrt(Pair m) {
+  const float r = rsqrtf(m.hi);
+  const float t = __fmul_rn(r, r);
+  const float te = __fmaf_rn(r, r, -t);
+  float u = __fmaf_rn(-m.hi, t, 1.f);
+  u = __fsub_rn(u, __fmaf_rn(m.hi, te, __fmul_rn(m.lo, t)));
+  return {r, 0.5f * r * u};
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <bool kFp4>
+__global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(const CacheWriteArgs a) {
+  constexpr int kRowBytes = kFp4 ? SMLA_FP4_ROW_BYTES : SMLA_ROW_BYTES;
+  constexpr int kRope = kRowBytes - 128;
+  const int lane = threadIdx.x & 31;
+  const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const int32_t slot = __ldg(a.slots + t);
+  const int32_t pos = a.cos_sin ? __ldg(a.positions + t) : 0;
+  if (slot < 0) return;
+  const bool bad_slot = slot >= a.num_slots;
+  const bool bad_pos = a.cos_sin && (pos < 0 || pos >= a.num_positions);
+  if (bad_slot || bad_pos) {
+    if (lane == 0)
+      atomicOr(&g_cache_error, (bad_slot ? SMLA_DEVERR_SLOT_RANGE : 0u) |
+                                   (bad_pos ? SMLA_DEVERR_POSITION : 0u));
+    return;
+  }
+  const uint16_t* src = a.kv + t * a.kv_row_stride;
+  uint8_t* dst = a.kv_cache + int64_t(slot) * kRowBytes;
+
+  // every load of the row first
+  uint32_t x[8], g[8];
+  {
+    const uint4 v0 = __ldg(reinterpret_cast<const uint4*>(src) + 2 * lane);
+    const uint4 v1 = __ldg(reinterpret_cast<const uint4*>(src) + 2 * lane + 1);
+    x[0] = v0.x, x[1] = v0.y, x[2] = v0.z, x[3] = v0.w;
+    x[4] = v1.x, x[5] = v1.y, x[6] = v1.z, x[7] = v1.w;
+  }
+  // the lane's rope pair: values 2 lane, 2 lane + 1, or lane, lane + 32
+  const uint16_t* zs = src + SMLA_V_DIM;
+  uint32_t z;
+  if (a.rope_pairs)
+    z = __ldg(reinterpret_cast<const uint32_t*>(zs) + lane);
+  else
+    z = uint32_t(__ldg(zs + lane)) | uint32_t(__ldg(zs + 32 + lane)) << 16;
+  float co = 1.f, si = 0.f;
+  if (a.cos_sin) {
+    co = __ldg(a.cos_sin + int64_t(pos) * 64 + lane);
+    si = __ldg(a.cos_sin + int64_t(pos) * 64 + 32 + lane);
+  }
+  if (a.gamma) {
+    const uint4 v0 = __ldg(reinterpret_cast<const uint4*>(a.gamma) + 2 * lane);
+    const uint4 v1 = __ldg(reinterpret_cast<const uint4*>(a.gamma) + 2 * lane + 1);
+    g[0] = v0.x, g[1] = v0.y, g[2] = v0.z, g[3] = v0.w;
+    g[4] = v1.x, g[5] = v1.y, g[6] = v1.z, g[7] = v1.w;
+  }
+
+  float y[16];  // x g, exact
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    y[2 * k] = bf16_lo(x[k]);
+    y[2 * k + 1] = bf16_hi(x[k]);
+  }
+  Pair r = {1.f, 0.f};
+  if (a.gamma) {
+    Pair ss = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const Pair s = two_sum(ss.hi, __fmul_rn(y[k], y[k]));
+      ss = {s.hi, __fadd_rn(ss.lo, s.lo)};
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      ss = pair_add(ss, {__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
+    const Pair m = two_sum(__fmul_rn(ss.hi, 1.f / 512.f), a.eps);
+    r = pair_rsqrt({m.hi, __fadd_rn(m.lo, __fmul_rn(ss.lo, 1.f / 512.f))});
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      y[2 * k] = __fmul_rn(y[2 * k], bf16_lo(g[k]));
+      y[2 * k + 1] = __fmul_rn(y[2 * k + 1], bf16_hi(g[k]));
+    }
+  }
+  // the group's largest magnitude; a value that is not finite (an infinite
+  // or NaN input, or a sum of squares past fp32) makes the group's scale NaN
+  float amax = 0.f;
+  bool finite = isfinite(r.hi) && isfinite(r.lo);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    amax = fmaxf(amax, fabsf(y[k]));
+    finite = finite && isfinite(y[k]);
+  }
+  if (!kFp4) {
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const unsigned ok = __ballot_sync(0xffffffffu, finite);
+    finite = ((ok >> (lane & 24)) & 0xffu) == 0xffu;
+    const Pair s = pair_div(pair_mul(amax, r), 448.f);
+    float scale = s.hi;
+    // below the normal fp32 range: the group is stored as zeros
+    if (!(scale >= 0x1p-126f)) scale = 0.f;
+    const float d = scale > 0.f ? scale : 1.f;
+    const float inv = __frcp_rn(d);
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t c = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float2 v = make_float2(quotient_odd(pair_mul(y[4 * k + 2 * h], r), d, inv),
+                                     quotient_odd(pair_mul(y[4 * k + 2 * h + 1], r), d, inv));
+        c |= uint32_t(__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3)) << (16 * h);
+      }
+      w[k] = (scale > 0.f && finite) ? c : 0u;
+    }
+    *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+    if ((lane & 7) == 0)
+      *reinterpret_cast<float*>(dst + 512 + 4 * (lane >> 3)) =
+          finite ? scale : __int_as_float(0x7fc00000);
+  } else {
+    const Pair s = pair_div(pair_mul(amax, r), 6.f);
+    const uint32_t sc = __nv_cvt_float_to_fp8(round_odd(s), __NV_SATFINITE, __NV_E4M3);
+    const float scale = __half2float(__half(__nv_cvt_fp8_to_halfraw(sc, __NV_E4M3)));
+    const float d = scale > 0.f ? scale : 1.f;
+    const float inv = __frcp_rn(d);
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 v = make_float2(quotient_odd(pair_mul(y[2 * k], r), d, inv),
+                                   quotient_odd(pair_mul(y[2 * k + 1], r), d, inv));
+      w[k >> 2] |= uint32_t(__nv_cvt_float2_to_fp4x2(v, __NV_E2M1, cudaRoundNearest)) << (8 * (k & 3));
+    }
+    const bool keep = scale > 0.f && finite;
+    *reinterpret_cast<uint2*>(dst + 8 * lane) = keep ? make_uint2(w[0], w[1]) : make_uint2(0u, 0u);
+    dst[256 + lane] = finite ? uint8_t(sc) : uint8_t(0x7f);
+  }
+
+  // rope
+  const float za = bf16_lo(z), zb = bf16_hi(z);
+  const uint32_t o = a.cos_sin ? bf16x2_bits(__fmaf_rn(za, co, -__fmul_rn(zb, si)),
+                                             __fmaf_rn(za, si, __fmul_rn(zb, co)))
+                               : z;
+  if (a.rope_pairs) {
+    *reinterpret_cast<uint32_t*>(dst + kRope + 4 * lane) = o;
+  } else {
+    *reinterpret_cast<uint16_t*>(dst + kRope + 2 * lane) = uint16_t(o);
+    *reinterpret_cast<uint16_t*>(dst + kRope + 64 + 2 * lane) = uint16_t(o >> 16);
+  }
+}
+
+// 8 consecutive values of a row to its output (bf16 or fp32).
+template <bool kFp32>
+__device__ __forceinline__ void store8(void* out, int64_t at, const float* v) {
+  if (kFp32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+    __stcs(o, make_float4(v[0], v[1], v[2], v[3]));
+    __stcs(o + 1, make_float4(v[4], v[5], v[6], v[7]));
+  } else {
+    __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at),
+           make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]),
+                      bf16x2_bits(v[6], v[7])));
+  }
+}
+
+__device__ __forceinline__ void e4m3x2(uint32_t c, float& a, float& b) {
+  const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(c & 0xffffu), __NV_E4M3));
+  a = __low2float(h);
+  b = __high2float(h);
+}
+
+constexpr int kRows = 4;
+
+template <bool kFp4, bool kFp32>
+__global__ void __launch_bounds__(kWarps * 32) cache_gather_kernel(const CacheGatherArgs a) {
+  constexpr int kRowBytes = kFp4 ? SMLA_FP4_ROW_BYTES : SMLA_ROW_BYTES;
+  constexpr int kRope = kRowBytes - 128;
+  constexpr int kCodeBytes = kFp4 ? 4 : 8;  // 8 dims
+  const int lane = threadIdx.x & 31;
+  const int64_t n0 = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kRows;
+  if (n0 >= a.N) return;
+  int32_t slot[kRows];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    slot[i] = n0 + i < a.N ? __ldg(a.slots + n0 + i) : -1;
+    if (slot[i] >= a.num_slots) {
+      bad = true;
+      slot[i] = -1;
+    }
+  }
+  uint2 code[kRows][2];
+  float scale[kRows][2];
+  uint32_t rope[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    code[i][0] = code[i][1] = make_uint2(0, 0);
+    scale[i][0] = scale[i][1] = 0.f;
+    rope[i] = 0;
+    if (slot[i] >= 0) {
+      const uint8_t* src = a.kv_cache + int64_t(slot[i]) * kRowBytes;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* p = src + kCodeBytes * (32 * h + lane);
+        if (kFp4) {
+          code[i][h].x = __ldg(reinterpret_cast<const uint32_t*>(p));
+          scale[i][h] = __half2float(
+              __half(__nv_cvt_fp8_to_halfraw(__ldg(src + 256 + 16 * h + (lane >> 1)), __NV_E4M3)));
+        } else {
+          code[i][h] = __ldg(reinterpret_cast<const uint2*>(p));
+          scale[i][h] = __ldg(reinterpret_cast<const float*>(src + 512) + 2 * h + (lane >> 4));
+        }
+      }
+      rope[i] = __ldg(reinterpret_cast<const uint32_t*>(src + kRope) + lane);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (n0 + i >= a.N) break;
+    const int64_t row = (n0 + i) * a.out_row_stride;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
+      if (kFp4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __half2 c = __half2(__nv_cvt_fp4x2_to_halfraw2(
+              __nv_fp4x2_storage_t((code[i][h].x >> (8 * k)) & 0xffu), __NV_E2M1));
+          v[2 * k] = __low2float(c) * scale[i][h];
+          v[2 * k + 1] = __high2float(c) * scale[i][h];
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t w = k < 2 ? code[i][h].x : code[i][h].y;
+          e4m3x2(w >> (16 * (k & 1)), v[2 * k], v[2 * k + 1]);
+          v[2 * k] *= scale[i][h];
+          v[2 * k + 1] *= scale[i][h];
+        }
+      }
+      store8<kFp32>(a.out, row + 256 * h + 8 * lane, v);
+    }
+    if (kFp32)
+      __stcs(reinterpret_cast<float2*>(static_cast<float*>(a.out) + row + 512) + lane,
+             make_float2(bf16_lo(rope[i]), bf16_hi(rope[i])));
+    else
+      __stcs(reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row + 512) + lane, rope[i]);
+  }
+  if (bad && lane == 0) atomicOr(&g_cache_error, SMLA_DEVERR_SLOT_RANGE);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const CacheWriteArgs& a, bool fp4, cudaStream_t s) {
+  const unsigned grid = unsigned((int64_t(a.T) + kWarps - 1) / kWarps);
+  if (fp4)
+    cache_write_kernel<true><<<grid, kWarps * 32, 0, s>>>(a);
+  else
+    cache_write_kernel<false><<<grid, kWarps * 32, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_gather(const CacheGatherArgs& a, bool fp4, bool fp32, cudaStream_t s) {
+  const unsigned grid = unsigned((int64_t(a.N) + kWarps * kRows - 1) / (kWarps * kRows));
+  if (fp4 && fp32)
+    cache_gather_kernel<true, true><<<grid, kWarps * 32, 0, s>>>(a);
+  else if (fp4)
+    cache_gather_kernel<true, false><<<grid, kWarps * 32, 0, s>>>(a);
+  else if (fp32)
+    cache_gather_kernel<false, true><<<grid, kWarps * 32, 0, s>>>(a);
+  else
+    cache_gather_kernel<false, false><<<grid, kWarps * 32, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t cache_error_word(uint32_t* flags, bool clear) {
+  unsigned int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_cache_error, sizeof(v));
+  if (e != cudaSuccess) return e;
+  *flags |= v;
+  if (clear) {
+    v = 0;
+    e = cudaMemcpyToSymbol(g_cache_error, &v, sizeof(v));
+  }
+  return e;
+}
+
+}  // namespace smla

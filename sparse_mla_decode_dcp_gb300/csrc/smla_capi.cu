@@ -4,6 +4,7 @@
 // call has no side effect and needs no device.
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/smla.h"
 #include "smla_internal.h"
@@ -41,6 +42,10 @@ smla_status smla_get_device_error(uint32_t* flags, int clear) {
   *flags = 0;
   cudaError_t e = smla::index_error_word(flags, clear != 0);
   if (e == cudaSuccess) e = smla::decode_error_word(flags, clear != 0);
+  if (e == cudaSuccess) e = smla::decode_fp4_error_word(flags, clear != 0);
+  if (e == cudaSuccess) e = smla::decode_window_error_word(flags, clear != 0);
+  if (e == cudaSuccess) e = smla::maps_error_word(flags, clear != 0);
+  if (e == cudaSuccess) e = smla::cache_error_word(flags, clear != 0);
   return from_cuda(e);
 }
 
@@ -83,11 +88,11 @@ size_t smla_decode_workspace_size(int32_t T, int32_t H, int32_t K) {
   return smla::decode_workspace_bytes(T, H, K);
 }
 
-smla_status smla_sparse_mla_decode(
-    const uint16_t* q, const uint8_t* kv_cache, int64_t num_slots,
-    const int32_t* local_slots, int32_t T, int32_t H, int32_t K,
-    float sm_scale, uint16_t* out, float* lse, void* workspace,
-    size_t workspace_bytes, void* stream) {
+// Checks of the per-rank sparse decode's arguments, whatever the rows' format;
+// fills `a` with everything but the workspace.
+static smla_status slots_args(const uint16_t* q, const uint8_t* kv_cache, int64_t num_slots,
+                              const int32_t* local_slots, int32_t T, int32_t H, int32_t K,
+                              float sm_scale, uint16_t* out, float* lse, smla::DecodeArgs& a) {
   if (T < 0 || K < 1 || H < 1 || num_slots < 0 || !std::isfinite(sm_scale) ||
       !(sm_scale > 0.f))
     return SMLA_ERR_INVALID_ARG;
@@ -97,11 +102,7 @@ smla_status smla_sparse_mla_decode(
   if (misaligned(q, 16) || misaligned(kv_cache, 16) || misaligned(out, 16) ||
       misaligned(local_slots, 4) || misaligned(lse, 4))
     return SMLA_ERR_INVALID_ARG;
-  const size_t need = smla::decode_workspace_bytes(T, H, K);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need ||
-                   misaligned(workspace, 256)))
-    return SMLA_ERR_WORKSPACE;
-  smla::DecodeArgs a{};
+  a = smla::DecodeArgs{};
   a.q = q;
   a.kv = kv_cache;
   a.num_slots = num_slots;
@@ -112,37 +113,61 @@ smla_status smla_sparse_mla_decode(
   a.sm_scale = sm_scale;
   a.out = out;
   a.lse = lse;
+  return SMLA_OK;
+}
+
+// Takes the caller's workspace of at least `need` bytes.
+static smla_status take_workspace(void* workspace, size_t workspace_bytes, size_t need,
+                                  smla::DecodeArgs& a) {
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || misaligned(workspace, 256)))
+    return SMLA_ERR_WORKSPACE;
   a.workspace = workspace;
   a.workspace_bytes = workspace_bytes;
+  return SMLA_OK;
+}
+
+smla_status smla_sparse_mla_decode(
+    const uint16_t* q, const uint8_t* kv_cache, int64_t num_slots,
+    const int32_t* local_slots, int32_t T, int32_t H, int32_t K,
+    float sm_scale, uint16_t* out, float* lse, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  smla::DecodeArgs a;
+  smla_status st =
+      slots_args(q, kv_cache, num_slots, local_slots, T, H, K, sm_scale, out, lse, a);
+  if (st != SMLA_OK || T == 0) return st;
+  st = take_workspace(workspace, workspace_bytes, smla::decode_workspace_bytes(T, H, K), a);
+  if (st != SMLA_OK) return st;
   return from_cuda(smla::launch_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t smla_fp4_decode_workspace_size(int32_t T, int32_t H, int32_t K) {
+  return smla_decode_workspace_size(T, H, K);
+}
+
+smla_status smla_sparse_mla_decode_fp4(
+    const uint16_t* q, const uint8_t* kv_cache, int64_t num_slots,
+    const int32_t* local_slots, int32_t T, int32_t H, int32_t K,
+    float sm_scale, uint16_t* out, float* lse, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  smla::DecodeArgs a;
+  smla_status st =
+      slots_args(q, kv_cache, num_slots, local_slots, T, H, K, sm_scale, out, lse, a);
+  if (st != SMLA_OK || T == 0) return st;
+  st = take_workspace(workspace, workspace_bytes, smla_fp4_decode_workspace_size(T, H, K), a);
+  if (st != SMLA_OK) return st;
+  return from_cuda(smla::launch_decode_fp4(a, static_cast<cudaStream_t>(stream)));
 }
 
 smla_status smla_sparse_mla_decode_noalloc(
     const uint16_t* q, const uint8_t* kv_cache, int64_t num_slots,
     const int32_t* local_slots, int32_t T, int32_t H, int32_t K,
     float sm_scale, uint16_t* out, float* lse, void* stream) {
-  if (T < 0 || K < 1 || H < 1 || num_slots < 0 || !std::isfinite(sm_scale) ||
-      !(sm_scale > 0.f))
-    return SMLA_ERR_INVALID_ARG;
-  if (H > SMLA_MAX_HEADS) return SMLA_ERR_UNSUPPORTED;
-  if (T == 0) return SMLA_OK;
-  if (!q || !kv_cache || !local_slots || !out || !lse) return SMLA_ERR_INVALID_ARG;
-  if (misaligned(q, 16) || misaligned(kv_cache, 16) || misaligned(out, 16) ||
-      misaligned(local_slots, 4) || misaligned(lse, 4))
-    return SMLA_ERR_INVALID_ARG;
+  smla::DecodeArgs a;
+  const smla_status st =
+      slots_args(q, kv_cache, num_slots, local_slots, T, H, K, sm_scale, out, lse, a);
+  if (st != SMLA_OK || T == 0) return st;
   if (smla::decode_workspace_bytes(T, H, K) > SMLA_NOALLOC_SCRATCH_BYTES)
     return SMLA_ERR_WORKSPACE;
-  smla::DecodeArgs a{};
-  a.q = q;
-  a.kv = kv_cache;
-  a.num_slots = num_slots;
-  a.slots = local_slots;
-  a.T = T;
-  a.H = H;
-  a.K = K;
-  a.sm_scale = sm_scale;
-  a.out = out;
-  a.lse = lse;
   return from_cuda(smla::launch_decode_noalloc(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -198,22 +223,40 @@ smla_status smla_dcp_sparse_mla_decode_fused(
     const int64_t* bt_row_strides, const int32_t* bt_widths, uint16_t* out,
     float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   smla::DecodeArgs a;
-  const smla_status st =
+  smla_status st =
       fused_args(q, T, H, K, sm_scale, req_id_per_token, topk_global, num_reqs, D, block_size,
                  interleave, kv_caches, num_slots, block_tables, bt_row_strides, bt_widths, out,
                  lse, a);
   if (st != SMLA_OK || T == 0) return st;
-  const size_t need = smla::decode_workspace_bytes(T, H, K);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need ||
-                   misaligned(workspace, 256)))
-    return SMLA_ERR_WORKSPACE;
+  st = take_workspace(workspace, workspace_bytes, smla::decode_workspace_bytes(T, H, K), a);
+  if (st != SMLA_OK) return st;
   a.q = q;
   a.topk = topk_global;
   a.out = out;
   a.lse = lse;
-  a.workspace = workspace;
-  a.workspace_bytes = workspace_bytes;
   return from_cuda(smla::launch_decode_fused(a, static_cast<cudaStream_t>(stream)));
+}
+
+smla_status smla_dcp_sparse_mla_decode_fused_fp4(
+    const uint16_t* q, int32_t T, int32_t H, int32_t K, float sm_scale,
+    const int32_t* req_id_per_token, const int32_t* topk_global, int32_t num_reqs,
+    int32_t D, int32_t block_size, int32_t interleave, const uint8_t* const* kv_caches,
+    const int64_t* num_slots, const int32_t* const* block_tables,
+    const int64_t* bt_row_strides, const int32_t* bt_widths, uint16_t* out,
+    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  smla::DecodeArgs a;
+  smla_status st =
+      fused_args(q, T, H, K, sm_scale, req_id_per_token, topk_global, num_reqs, D, block_size,
+                 interleave, kv_caches, num_slots, block_tables, bt_row_strides, bt_widths, out,
+                 lse, a);
+  if (st != SMLA_OK || T == 0) return st;
+  st = take_workspace(workspace, workspace_bytes, smla_fp4_decode_workspace_size(T, H, K), a);
+  if (st != SMLA_OK) return st;
+  a.q = q;
+  a.topk = topk_global;
+  a.out = out;
+  a.lse = lse;
+  return from_cuda(smla::launch_decode_fused_fp4(a, static_cast<cudaStream_t>(stream)));
 }
 
 smla_status smla_dcp_sparse_mla_decode_fused_host(
@@ -268,26 +311,26 @@ size_t smla_dense_decode_workspace_size(int32_t T, int32_t H, int32_t max_ctx, i
   return smla::decode_workspace_bytes(T, H, dense_entries(max_ctx, D, interleave, rank));
 }
 
-smla_status smla_dcp_dense_mla_decode(
-    const uint16_t* q, int32_t B, int32_t S, int32_t H, float sm_scale,
-    const int32_t* ctx_lens, int32_t max_ctx, int32_t D, int32_t rank,
-    int32_t block_size, int32_t interleave, const uint8_t* const* kv_caches,
-    const int64_t* num_slots, const int32_t* const* block_tables,
-    const int64_t* bt_row_strides, const int32_t* bt_widths, uint16_t* out,
-    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+// Checks of the dense and windowed decode's arguments; fills `a` with
+// everything but K and the workspace.
+static smla_status generated_args(
+    const uint16_t* q, int32_t B, int32_t S, int32_t H, float sm_scale, const int32_t* ctx_lens,
+    int32_t max_ctx, int32_t D, int32_t rank, int32_t block_size, int32_t interleave,
+    const uint8_t* const* kv_caches, const int64_t* num_slots,
+    const int32_t* const* block_tables, const int64_t* bt_row_strides, const int32_t* bt_widths,
+    uint16_t* out, float* lse, smla::DecodeArgs& a) {
   if (B < 0 || S < 1 || H < 1 || max_ctx < 1 || D < 1 || rank < -1 || rank >= D ||
       block_size < 1 || interleave < 1 || !std::isfinite(sm_scale) || !(sm_scale > 0.f))
     return SMLA_ERR_INVALID_ARG;
   if (H > SMLA_MAX_HEADS || D > SMLA_MAX_DCP) return SMLA_ERR_UNSUPPORTED;
   if (int64_t(B) * S > INT32_MAX) return SMLA_ERR_INVALID_ARG;
-  const int32_t T = B * S;
-  if (T == 0) return SMLA_OK;
+  if (B == 0) return SMLA_OK;
   if (!q || !ctx_lens || !out || !lse || !kv_caches || !num_slots || !block_tables ||
       !bt_row_strides || !bt_widths)
     return SMLA_ERR_INVALID_ARG;
   if (misaligned(q, 16) || misaligned(out, 16) || misaligned(lse, 4) || misaligned(ctx_lens, 4))
     return SMLA_ERR_INVALID_ARG;
-  smla::DecodeArgs a{};
+  a = smla::DecodeArgs{};
   for (int d = 0; d < D; ++d) {
     const bool used = rank < 0 || d == rank;
     if (used && (!kv_caches[d] || misaligned(kv_caches[d], 16) || num_slots[d] < 0 ||
@@ -300,20 +343,12 @@ smla_status smla_dcp_dense_mla_decode(
     a.bt_stride[d] = used ? bt_row_strides[d] : 0;
     a.bt_width[d] = used ? bt_widths[d] : 0;
   }
-  const int32_t K = dense_entries(max_ctx, D, interleave, rank);
-  const size_t need = smla::decode_workspace_bytes(T, H, K);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need ||
-                   misaligned(workspace, 256)))
-    return SMLA_ERR_WORKSPACE;
   a.q = q;
-  a.T = T;
+  a.T = B * S;
   a.H = H;
-  a.K = K;
   a.sm_scale = sm_scale;
   a.out = out;
   a.lse = lse;
-  a.workspace = workspace;
-  a.workspace_bytes = workspace_bytes;
   a.D = D;
   a.block_size = block_size;
   a.interleave = interleave;
@@ -322,7 +357,165 @@ smla_status smla_dcp_dense_mla_decode(
   a.S = S;
   a.dense_rank = rank;
   a.max_ctx = max_ctx;
+  return SMLA_OK;
+}
+
+smla_status smla_dcp_dense_mla_decode(
+    const uint16_t* q, int32_t B, int32_t S, int32_t H, float sm_scale,
+    const int32_t* ctx_lens, int32_t max_ctx, int32_t D, int32_t rank,
+    int32_t block_size, int32_t interleave, const uint8_t* const* kv_caches,
+    const int64_t* num_slots, const int32_t* const* block_tables,
+    const int64_t* bt_row_strides, const int32_t* bt_widths, uint16_t* out,
+    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  smla::DecodeArgs a;
+  smla_status st = generated_args(q, B, S, H, sm_scale, ctx_lens, max_ctx, D, rank, block_size,
+                                  interleave, kv_caches, num_slots, block_tables, bt_row_strides,
+                                  bt_widths, out, lse, a);
+  if (st != SMLA_OK || B == 0) return st;
+  a.K = dense_entries(max_ctx, D, interleave, rank);
+  st = take_workspace(workspace, workspace_bytes, smla::decode_workspace_bytes(a.T, H, a.K), a);
+  if (st != SMLA_OK) return st;
   return from_cuda(smla::launch_decode_dense(a, static_cast<cudaStream_t>(stream)));
+}
+
+// Raw entries per row of the windowed decode: the sinks and the window, or
+// the largest count of them one rank holds, and never more than the context.
+static int32_t window_entries(int32_t max_ctx, int32_t window, int32_t sinks, int32_t D,
+                              int32_t interleave, int32_t rank) {
+  const int64_t all = dense_entries(max_ctx, D, interleave, rank);
+  const int64_t kept =
+      int64_t(dense_entries(window < max_ctx ? window : max_ctx, D, interleave, rank)) +
+      dense_entries(sinks < max_ctx ? sinks : max_ctx, D, interleave, rank);
+  return int32_t(kept < all ? kept : all);
+}
+
+size_t smla_window_decode_workspace_size(int32_t T, int32_t H, int32_t max_ctx, int32_t window,
+                                         int32_t sinks, int32_t D, int32_t interleave,
+                                         int32_t rank) {
+  if (T < 0 || H < 1 || H > SMLA_MAX_HEADS || max_ctx < 1 || window < 1 || sinks < 0 || D < 1 ||
+      interleave < 1 || rank < -1 || rank >= D)
+    return 0;
+  return smla::decode_workspace_bytes(
+      T, H, window_entries(max_ctx, window, sinks, D, interleave, rank));
+}
+
+smla_status smla_dcp_window_mla_decode(
+    const uint16_t* q, int32_t B, int32_t S, int32_t H, float sm_scale,
+    const int32_t* ctx_lens, int32_t max_ctx, int32_t window, int32_t sinks, int32_t D,
+    int32_t rank, int32_t block_size, int32_t interleave, int32_t format,
+    const uint8_t* const* kv_caches, const int64_t* num_slots,
+    const int32_t* const* block_tables, const int64_t* bt_row_strides, const int32_t* bt_widths,
+    uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (window < 1 || sinks < 0 || (format != SMLA_CACHE_FP8 && format != SMLA_CACHE_FP4))
+    return SMLA_ERR_INVALID_ARG;
+  smla::DecodeArgs a;
+  smla_status st = generated_args(q, B, S, H, sm_scale, ctx_lens, max_ctx, D, rank, block_size,
+                                  interleave, kv_caches, num_slots, block_tables, bt_row_strides,
+                                  bt_widths, out, lse, a);
+  if (st != SMLA_OK || B == 0) return st;
+  a.window = window;
+  a.sinks = sinks;
+  a.K = window_entries(max_ctx, window, sinks, D, interleave, rank);
+  st = take_workspace(workspace, workspace_bytes, smla::decode_workspace_bytes(a.T, H, a.K), a);
+  if (st != SMLA_OK) return st;
+  return from_cuda(smla::launch_decode_window(a, format == SMLA_CACHE_FP4,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+smla_status smla_dcp_step_maps(
+    const int32_t* ctx_lens, const int32_t* q_lens, int32_t B, int32_t T, int32_t D, int32_t rank,
+    int32_t block_size, int32_t interleave, const int32_t* free_blocks, int32_t num_free,
+    int32_t* block_table, int64_t bt_row_stride, int32_t bt_width, int32_t* row_start,
+    int32_t* req_id, int32_t* positions, int32_t* slots, int32_t* local_lens,
+    int32_t* blocks_taken, void* stream) {
+  if (B < 0 || T < 0 || D < 1 || rank < 0 || rank >= D || block_size < 1 || interleave < 1 ||
+      num_free < 0 || bt_width < 1 || bt_row_stride < bt_width)
+    return SMLA_ERR_INVALID_ARG;
+  if (B > SMLA_MAX_STEP_REQS) return SMLA_ERR_UNSUPPORTED;
+  if (B == 0 && T == 0) return SMLA_OK;
+  if ((B > 0 && (!ctx_lens || !q_lens || !block_table)) || (T > 0 && !slots) ||
+      (num_free > 0 && !free_blocks))
+    return SMLA_ERR_INVALID_ARG;
+  for (const int32_t* p : {ctx_lens, q_lens, free_blocks, static_cast<const int32_t*>(block_table),
+                           static_cast<const int32_t*>(row_start),
+                           static_cast<const int32_t*>(req_id),
+                           static_cast<const int32_t*>(positions),
+                           static_cast<const int32_t*>(slots),
+                           static_cast<const int32_t*>(local_lens),
+                           static_cast<const int32_t*>(blocks_taken)})
+    if (misaligned(p, 4)) return SMLA_ERR_INVALID_ARG;
+  smla::MapsArgs a{};
+  a.ctx_lens = ctx_lens;
+  a.q_lens = q_lens;
+  a.B = B;
+  a.T = T;
+  a.D = D;
+  a.rank = rank;
+  a.block_size = block_size;
+  a.interleave = interleave;
+  a.free_blocks = free_blocks;
+  a.num_free = num_free;
+  a.block_table = block_table;
+  a.bt_row_stride = bt_row_stride;
+  a.bt_width = bt_width;
+  a.row_start = row_start;
+  a.req_id = req_id;
+  a.positions = positions;
+  a.slots = slots;
+  a.local_lens = local_lens;
+  a.blocks_taken = blocks_taken;
+  return from_cuda(smla::launch_step_maps(a, static_cast<cudaStream_t>(stream)));
+}
+
+smla_status smla_mla_cache_write(
+    const uint16_t* kv, int64_t kv_row_stride, int32_t T, const uint16_t* gamma, float eps,
+    const int32_t* positions, const float* cos_sin, int32_t num_positions, int32_t rope_pairs,
+    const int32_t* slots, int32_t format, uint8_t* kv_cache, int64_t num_slots, void* stream) {
+  if (T < 0 || num_slots < 0 || (format != SMLA_CACHE_FP8 && format != SMLA_CACHE_FP4) ||
+      kv_row_stride < SMLA_QK_DIM || kv_row_stride % 8 != 0 ||
+      (gamma && !(std::isfinite(eps) && eps > 0.f)) || (cos_sin && num_positions < 1))
+    return SMLA_ERR_INVALID_ARG;
+  if (T == 0) return SMLA_OK;
+  if (!kv || !slots || !kv_cache || (cos_sin && !positions)) return SMLA_ERR_INVALID_ARG;
+  if (misaligned(kv, 16) || misaligned(gamma, 16) || misaligned(kv_cache, 16) ||
+      misaligned(slots, 4) || misaligned(positions, 4) || misaligned(cos_sin, 4))
+    return SMLA_ERR_INVALID_ARG;
+  smla::CacheWriteArgs a{};
+  a.kv = kv;
+  a.kv_row_stride = kv_row_stride;
+  a.T = T;
+  a.gamma = gamma;
+  a.eps = eps;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.num_positions = num_positions;
+  a.rope_pairs = rope_pairs != 0;
+  a.slots = slots;
+  a.kv_cache = kv_cache;
+  a.num_slots = num_slots;
+  return from_cuda(smla::launch_cache_write(a, format == SMLA_CACHE_FP4,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+smla_status smla_mla_cache_gather(const uint8_t* kv_cache, int64_t num_slots, int32_t format,
+                                  const int32_t* slots, int32_t N, void* out,
+                                  int64_t out_row_stride, int32_t out_fp32, void* stream) {
+  if (N < 0 || num_slots < 0 || (format != SMLA_CACHE_FP8 && format != SMLA_CACHE_FP4) ||
+      out_row_stride < SMLA_QK_DIM || out_row_stride % (out_fp32 ? 4 : 8) != 0)
+    return SMLA_ERR_INVALID_ARG;
+  if (N == 0) return SMLA_OK;
+  if (!kv_cache || !slots || !out) return SMLA_ERR_INVALID_ARG;
+  if (misaligned(kv_cache, 16) || misaligned(slots, 4) || misaligned(out, 16))
+    return SMLA_ERR_INVALID_ARG;
+  smla::CacheGatherArgs a{};
+  a.kv_cache = kv_cache;
+  a.num_slots = num_slots;
+  a.slots = slots;
+  a.N = N;
+  a.out = out;
+  a.out_row_stride = out_row_stride;
+  return from_cuda(smla::launch_cache_gather(a, format == SMLA_CACHE_FP4, out_fp32 != 0,
+                                             static_cast<cudaStream_t>(stream)));
 }
 
 size_t smla_topk_select_workspace_size(int32_t T, int32_t L, int32_t K) {

@@ -1,0 +1,17 @@
+// Windowed decode with sinks over either cache: the launcher of the kernel in
+// smla_decode_kernel.cuh for generated rows with a gap.
+#include "smla_decode_kernel.cuh"
+
+namespace smla {
+
+cudaError_t launch_decode_window(const DecodeArgs& args, bool fp4, cudaStream_t s) {
+  DecodeArgs a = args;
+  set_divisors(a);
+  return fp4 ? launch_impl<kModeWindow, Fp4Rows>(a, s) : launch_impl<kModeWindow, Fp8Rows>(a, s);
+}
+
+cudaError_t decode_window_error_word(uint32_t* flags, bool clear) {
+  return read_error_word(flags, clear);
+}
+
+}  // namespace smla

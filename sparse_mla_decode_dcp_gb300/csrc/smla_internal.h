@@ -76,6 +76,7 @@ struct DecodeArgs {
   // pools) or dense_rank's local positions; max_ctx bounds the positions.
   const int32_t* ctx_lens;
   int32_t S, dense_rank, max_ctx;
+  int32_t window, sinks;  // windowed decode only
   // q [T*H, 576] bf16 for TMA, set by the launcher: boxes of 64 dims x 128
   // head rows (128-byte swizzle) and 32 dims x 128 head rows (64-byte swizzle)
   CUtensorMap q_lat, q_rope;
@@ -108,6 +109,48 @@ struct TopkArgs {
   float* chunk_scores;
 };
 
+struct MapsArgs {
+  const int32_t* ctx_lens;     // [B] cached positions, the new tokens included
+  const int32_t* q_lens;       // [B] new tokens
+  int32_t B, T, D, rank, block_size, interleave;
+  FastDiv div_I, div_D, div_bs, div_ID;  // set by the launcher
+  const int32_t* free_blocks;  // [num_free]
+  int32_t num_free;
+  int32_t* block_table;        // [B, bt_row_stride]
+  int64_t bt_row_stride;
+  int32_t bt_width;
+  int32_t* row_start;          // [B + 1] or null
+  int32_t* req_id;             // [T] or null
+  int32_t* positions;          // [T] or null
+  int32_t* slots;              // [T]
+  int32_t* local_lens;         // [B] or null
+  int32_t* blocks_taken;       // [1] or null
+};
+
+struct CacheWriteArgs {
+  const uint16_t* kv;          // bf16 [T, 576], rows kv_row_stride apart
+  int64_t kv_row_stride;
+  int32_t T;
+  const uint16_t* gamma;       // bf16 [512], or null: no norm
+  float eps;
+  const int32_t* positions;    // [T] (with cos_sin)
+  const float* cos_sin;        // [num_positions, 64]: 32 cosines, 32 sines; null: no rotation
+  int32_t num_positions;
+  int32_t rope_pairs;          // 1: pairs (2i, 2i + 1); 0: pairs (i, i + 32)
+  const int32_t* slots;        // [T], -1 = not this cache's
+  uint8_t* kv_cache;
+  int64_t num_slots;
+};
+
+struct CacheGatherArgs {
+  const uint8_t* kv_cache;
+  int64_t num_slots;
+  const int32_t* slots;        // [N], -1 = a row of zeros
+  int32_t N;
+  void* out;                   // bf16 or fp32 [N, 576], rows out_row_stride apart
+  int64_t out_row_stride;
+};
+
 struct MergeArgs {
   const uint16_t* outs[kMaxMerge];
   const float* lses[kMaxMerge];
@@ -120,6 +163,10 @@ cudaError_t launch_filter_convert(const IndexArgs& a, cudaStream_t s);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_fused(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_dense(const DecodeArgs& a, cudaStream_t s);
+// over 416-byte fp4 rows
+cudaError_t launch_decode_fp4(const DecodeArgs& a, cudaStream_t s);
+cudaError_t launch_decode_fused_fp4(const DecodeArgs& a, cudaStream_t s);
+cudaError_t launch_decode_window(const DecodeArgs& a, bool fp4, cudaStream_t s);
 // Library-owned split-K scratch (no allocation by anyone at call time).
 constexpr size_t kNoAllocScratchBytes = size_t(32) << 20;
 // compacted entries one decode cluster handles (the key list in its shared
@@ -133,6 +180,12 @@ cudaError_t launch_topk_select(const TopkArgs& a, void* workspace, cudaStream_t 
 size_t topk_workspace_bytes(int32_t T, int32_t L, int32_t K);
 cudaError_t launch_topk_merge(const TopkArgs& a, cudaStream_t s);
 size_t decode_workspace_bytes(int32_t T, int32_t H, int32_t K);
+
+cudaError_t launch_step_maps(const MapsArgs& a, cudaStream_t s);
+cudaError_t maps_error_word(uint32_t* flags, bool clear);
+cudaError_t launch_cache_write(const CacheWriteArgs& a, bool fp4, cudaStream_t s);
+cudaError_t launch_cache_gather(const CacheGatherArgs& a, bool fp4, bool fp32, cudaStream_t s);
+cudaError_t cache_error_word(uint32_t* flags, bool clear);
 
 // The fused step from and to host memory (smla_host.cu): the caller's host
 // buffers and the device staging buffers their copies fill (the decode's q
@@ -151,5 +204,7 @@ cudaError_t launch_fused_host(const DecodeArgs& a, const HostBuffers& h, int gro
 // Each kernel translation unit owns one device error word.
 cudaError_t index_error_word(uint32_t* flags, bool clear);
 cudaError_t decode_error_word(uint32_t* flags, bool clear);
+cudaError_t decode_fp4_error_word(uint32_t* flags, bool clear);
+cudaError_t decode_window_error_word(uint32_t* flags, bool clear);
 
 }  // namespace smla
