@@ -84,3 +84,77 @@ class DcpDecodeStep:
         capi.dcp_lse_merge(self.part_out, self.part_lse, out=self.out, lse=self.lse,
                            stream=self.stream)
         return self.out, self.lse
+
+
+class DcpServingStep:
+    """A server's steps over D simulated shards and a cache it fills itself.
+
+    ``prefill`` writes a chunk of any requests' tokens into the caches;
+    ``run`` brings ``tokens_per_req`` new tokens of every request, writes
+    them and attends each token's window and sinks over all D pools.  Both
+    take device tensors, launch on one stream and read nothing back: the
+    block tables grow on the device from each rank's free list.
+    ``take_blocks`` then drops the blocks taken since the last call from the
+    front of the free lists (it reads their counts, so it synchronises); a
+    server that keeps the lengths on the host can do that from them instead.
+    """
+
+    def __init__(self, num_reqs: int, tokens_per_req: int, heads: int, dcp: int, block_size: int,
+                 blocks_per_rank: int, max_ctx: int, window: int, sinks: int, *, fmt: str = "fp4",
+                 gamma: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 cos_sin: Optional[torch.Tensor] = None, rope_pairs: bool = True,
+                 sm_scale: float = 192 ** -0.5, interleave: int = 1, device="cuda",
+                 stream: Optional[torch.cuda.Stream] = None):
+        dev = torch.device(device)
+        self.B, self.S, self.H, self.D = num_reqs, tokens_per_req, heads, dcp
+        self.block_size, self.interleave, self.max_ctx = block_size, interleave, max_ctx
+        self.window, self.sinks, self.sm_scale = window, sinks, sm_scale
+        self.gamma, self.eps, self.cos_sin, self.rope_pairs = gamma, eps, cos_sin, rope_pairs
+        self.stream = stream
+        row = {"fp8": capi.ROW_BYTES, "fp4": capi.FP4_ROW_BYTES}[fmt]
+        width = -(-max_ctx // (interleave * dcp)) * interleave
+        width = max(1, -(-width // block_size))
+        self.pools = [torch.zeros((blocks_per_rank * block_size, row), dtype=torch.uint8, device=dev)
+                      for _ in range(dcp)]
+        self.block_tables = [torch.full((num_reqs, width), -1, dtype=torch.int32, device=dev)
+                             for _ in range(dcp)]
+        self.free_blocks = [torch.arange(blocks_per_rank, dtype=torch.int32, device=dev)
+                            for _ in range(dcp)]
+        T = num_reqs * tokens_per_req
+        self.q_lens = torch.full((num_reqs,), tokens_per_req, dtype=torch.int32, device=dev)
+        self.maps = [capi.alloc_step_maps(num_reqs, T, dev) for _ in range(dcp)]
+        self.out = torch.empty((T, heads, capi.V_DIM), dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty((T, heads), dtype=torch.float32, device=dev)
+        self.workspace = capi.alloc_window_decode_workspace(T, heads, max_ctx, window, sinks, dcp,
+                                                            interleave, -1, dev)
+        self._taken: List[torch.Tensor] = []
+
+    def _append(self, ctx_lens, q_lens, kv, outs):
+        self._taken = []
+        for d in range(self.D):
+            m = capi.dcp_step_maps(ctx_lens, q_lens, self.free_blocks[d], self.block_tables[d],
+                                   kv.shape[0], self.D, d, self.block_size,
+                                   interleave=self.interleave, out=outs[d], stream=self.stream)
+            self._taken.append(m.blocks_taken)
+            capi.mla_cache_write(kv, m.slots, self.pools[d], gamma=self.gamma, eps=self.eps,
+                                 positions=m.positions, cos_sin=self.cos_sin,
+                                 rope_pairs=self.rope_pairs, stream=self.stream)
+
+    def prefill(self, ctx_lens: torch.Tensor, q_lens: torch.Tensor, kv: torch.Tensor):
+        """Write the rows kv [sum(q_lens), 576] of the requests' new tokens."""
+        self._append(ctx_lens, q_lens, kv, [None] * self.D)
+
+    def run(self, ctx_lens: torch.Tensor, kv: torch.Tensor, q: torch.Tensor):
+        """One decode step: rows kv [B*S, 576] go into the caches, q
+        [B*S, H, 576] attends.  Returns (out, lse), reused by the next step."""
+        self._append(ctx_lens, self.q_lens, kv, self.maps)
+        return capi.dcp_window_mla_decode(
+            q, ctx_lens, self.max_ctx, self.S, self.window, self.sinks, self.pools,
+            self.block_tables, self.block_size, self.sm_scale, interleave=self.interleave,
+            out=self.out, lse=self.lse, workspace=self.workspace, stream=self.stream)
+
+    def take_blocks(self):
+        """Drop the blocks the last prefill or run took from the free lists."""
+        for d, taken in enumerate(self._taken):
+            self.free_blocks[d] = self.free_blocks[d][int(taken.item()):]
+        self._taken = []
