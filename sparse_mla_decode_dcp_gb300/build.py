@@ -1,9 +1,11 @@
-"""Build the in-tree CUDA library ``libsmla.so`` for sm_103a with nvcc.
+"""Build the in-tree CUDA library ``libsmla.so`` for sm_103a with nvcc, and the
+compiled part of its Python binding (``_smla_torch.so``) with the host compiler.
 
 Each ``csrc/*.cu`` translation unit compiles in its own nvcc process (in
 parallel), then nvcc links the shared library next to this file.  A unit is
 rebuilt only when it, a header under ``csrc/`` or ``include/smla.h`` is newer
-than its object.
+than its object.  The binding compiles beside them, against the installed
+torch's headers.
 """
 from __future__ import annotations
 
@@ -13,12 +15,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libsmla.so")
+BINDING_SRC = os.path.join(CSRC, "smla_torch.cpp")
+BINDING_PATH = os.path.join(PKG_DIR, "_smla_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "--expt-relaxed-constexpr", "-Xptxas", "-v"]
@@ -54,8 +59,30 @@ def _compile(nvcc, src, obj, log_dir):
     return obj
 
 
+def _compile_binding(obj, log_dir):
+    import torch
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [os.path.join(os.path.dirname(torch.__file__), "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden"]
+    cmd += ["-I" + p for p in inc] + ["-c", BINDING_SRC, "-o", obj]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    with open(os.path.join(log_dir, "smla_torch.cpp.log"), "w") as f:
+        f.write(" ".join(cmd) + "\n" + p.stdout + p.stderr)
+    if p.returncode != 0:
+        raise RuntimeError(f"the binding failed to compile:\n{p.stderr[-6000:]}")
+    return obj
+
+
+def _link(cmd):
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"link failed:\n{p.stderr[-4000:]}")
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
-    """Compile every CUDA unit and link libsmla.so; returns the library path."""
+    """Compile every CUDA unit and link libsmla.so, and compile and link its
+    Python binding; returns the library path."""
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -67,9 +94,13 @@ def build(verbose: bool = False, force: bool = False) -> str:
         objs.append(obj)
         if force or _stale(obj, [src] + hdrs):
             jobs.append((src, obj))
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
-            futs = [ex.submit(_compile, nvcc, s, o, BUILD_DIR) for s, o in jobs]
+    binding_obj = os.path.join(BUILD_DIR, "smla_torch.o")
+    header = os.path.join(ROOT, "include", "smla.h")
+    binding_job = force or _stale(binding_obj, [BINDING_SRC, header])
+    if jobs or binding_job:
+        with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
+            futs = [ex.submit(_compile_binding, binding_obj, BUILD_DIR)] if binding_job else []
+            futs += [ex.submit(_compile, nvcc, s, o, BUILD_DIR) for s, o in jobs]
             for f in futs:
                 f.result()
         if verbose:
@@ -77,10 +108,13 @@ def build(verbose: bool = False, force: bool = False) -> str:
                 with open(os.path.join(BUILD_DIR, os.path.basename(s) + ".log")) as f:
                     sys.stdout.write(f.read())
     if force or jobs or _stale(LIB_PATH, objs):
-        cmd = [nvcc] + ARCH + ["-shared", "-o", LIB_PATH] + objs
-        p = subprocess.run(cmd, capture_output=True, text=True)
-        if p.returncode != 0:
-            raise RuntimeError(f"link failed:\n{p.stderr[-4000:]}")
+        _link([nvcc] + ARCH + ["-shared", "-o", LIB_PATH] + objs)
+    if force or jobs or binding_job or _stale(BINDING_PATH, [binding_obj, LIB_PATH]):
+        import torch
+        _link([os.environ.get("CXX", "g++"), "-shared", "-o", BINDING_PATH, binding_obj,
+               "-L" + PKG_DIR, "-l:libsmla.so", "-Wl,-rpath,$ORIGIN",
+               "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python",
+               "-ltorch_cpu", "-lc10_cuda", "-lc10"])
     return LIB_PATH
 
 

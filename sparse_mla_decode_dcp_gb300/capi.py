@@ -563,21 +563,22 @@ def dcp_lse_merge(outs: Sequence[torch.Tensor], lses: Sequence[torch.Tensor], *,
 
 # --------------------------------------------------------------------------
 # The serving step around the decode: 4-bit cache, windows, maps, write and
-# gather.  These calls launch on their tensors' device whatever the current
-# one is, and allocate what the caller does not pass on the stream they
-# launch on.
+# gather.  Their tensors are checked by the compiled binding (csrc/
+# smla_torch.cpp).  These calls launch on their tensors' device whatever the
+# current one is, and allocate what the caller does not pass on the stream
+# they launch on.
 # --------------------------------------------------------------------------
-def _call(fn: str, dev: torch.device, stream: Optional[torch.cuda.Stream], args):
-    if dev.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, got {dev}")
-    s = _stream_ptr(stream, dev)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        st = getattr(load(), fn)(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            st = getattr(load(), fn)(*args, s)
-    if st != SMLA_OK:
-        raise SmlaError(fn, st)
+_binding = None
+
+
+def _native():
+    """The compiled binding (raises if it was never built)."""
+    global _binding
+    if _binding is None:
+        load()
+        from . import _smla_torch
+        _binding = _smla_torch
+    return _binding
 
 
 def _new(shape, dtype, dev, stream: Optional[torch.cuda.Stream], zero: bool = False):
@@ -588,89 +589,26 @@ def _new(shape, dtype, dev, stream: Optional[torch.cuda.Stream], zero: bool = Fa
         return make(shape, dtype=dtype, device=dev)
 
 
-def _shaped(t: torch.Tensor, name: str, dtype, shape, dev):
-    _need(t, name, dtype, dev)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-
-
-def _cache_format(kv: torch.Tensor, name: str, dev) -> int:
-    _need(kv, name, torch.uint8, dev)
-    if kv.dim() != 2 or kv.shape[1] not in (ROW_BYTES, FP4_ROW_BYTES):
-        raise ValueError(f"{name} must be [num_slots, {ROW_BYTES} or {FP4_ROW_BYTES}] uint8")
-    return CACHE_FP8 if kv.shape[1] == ROW_BYTES else CACHE_FP4
-
-
-def _fp4_cache(kv: torch.Tensor, name: str, dev):
-    _need(kv, name, torch.uint8, dev)
-    if kv.dim() != 2 or kv.shape[1] != FP4_ROW_BYTES:
-        raise ValueError(f"{name} must be [num_slots, {FP4_ROW_BYTES}] uint8")
-
-
-def _q_out_lse(q: torch.Tensor, out, lse, stream):
-    dev = q.device
-    _need(q, "q", torch.bfloat16, dev)
-    if q.dim() != 3 or q.shape[2] != QK_DIM:
+def _out_lse(q: torch.Tensor, out, lse, stream):
+    if q.dim() != 3:
         raise ValueError(f"q must be [T, H, {QK_DIM}]")
-    T, H = q.shape[0], q.shape[1]
     if out is None:
-        out = _new((T, H, V_DIM), torch.bfloat16, dev, stream)
-    else:
-        _shaped(out, "out", torch.bfloat16, (T, H, V_DIM), dev)
+        out = _new((q.shape[0], q.shape[1], V_DIM), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = _new((T, H), torch.float32, dev, stream)
-    else:
-        _shaped(lse, "lse", torch.float32, (T, H), dev)
-    return T, H, out, lse
-
-
-def _workspace(ws: Optional[torch.Tensor], need: int, dev, stream):
-    """(tensor to keep, address, bytes) of the given workspace, or of a
-    zero-filled one of `need` bytes."""
-    if ws is None and need:
-        ws = _new(need, torch.uint8, dev, stream, zero=True)
-    if ws is None:
-        return None, None, 0
-    _need(ws, "workspace", torch.uint8, dev)
-    return ws, ws.data_ptr(), ws.numel()
-
-
-def _pool_arrays(kv_caches, block_tables, bt_widths, dev, used, num_reqs=None):
-    """ctypes arrays (pools, slot counts, tables, strides, widths) of the D
-    shards, the format of the used pools and the tables' common row count."""
-    D = len(kv_caches)
-    if D != len(block_tables) or D < 1:
-        raise ValueError("need one block table per KV pool (>= 1)")
-    pools, nslots = (ctypes.c_void_p * D)(), (ctypes.c_int64 * D)()
-    bts, strides, widths = (ctypes.c_void_p * D)(), (ctypes.c_int64 * D)(), (ctypes.c_int32 * D)()
-    fmt = None
-    for d in used:
-        kv, bt = kv_caches[d], block_tables[d]
-        f = _cache_format(kv, "kv_caches[d]", dev)
-        if fmt is not None and f != fmt:
-            raise ValueError("kv_caches must share one row format")
-        fmt = f
-        if bt.dtype != torch.int32 or bt.device != dev or bt.dim() != 2 or bt.stride(1) != 1:
-            raise ValueError("block_tables[d] must be 2-D int32 with contiguous rows")
-        width = bt.shape[1] if bt_widths is None else int(bt_widths[d])
-        if width > bt.shape[1]:
-            raise ValueError("bt_widths[d] is past the table's columns")
-        num_reqs = bt.shape[0] if num_reqs is None else min(num_reqs, bt.shape[0])
-        pools[d], nslots[d] = kv.data_ptr(), kv.shape[0]
-        # a one-row table's stride means nothing (and may be anything)
-        bts[d], strides[d] = bt.data_ptr(), bt.stride(0) if bt.shape[0] > 1 else bt.shape[1]
-        widths[d] = width
-    return pools, nslots, bts, strides, widths, fmt, num_reqs
+        lse = _new((q.shape[0], q.shape[1]), torch.float32, q.device, stream)
+    return out, lse
 
 
 def fp4_decode_workspace_size(T: int, H: int, K: int) -> int:
     return int(load().smla_fp4_decode_workspace_size(T, H, K))
 
 
-def alloc_fp4_decode_workspace(T: int, H: int, K: int, device) -> Optional[torch.Tensor]:
+def alloc_fp4_decode_workspace(T: int, H: int, K: int, device,
+                               stream: Optional[torch.cuda.Stream] = None
+                               ) -> Optional[torch.Tensor]:
     """Zero-filled workspace of the fp4 sparse decodes (None if none needed)."""
     n = fp4_decode_workspace_size(T, H, K)
-    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+    return _new(n, torch.uint8, device, stream, zero=True) if n else None
 
 
 def sparse_mla_decode_fp4(q: torch.Tensor, kv_cache: torch.Tensor, local_slots: torch.Tensor,
@@ -680,18 +618,13 @@ def sparse_mla_decode_fp4(q: torch.Tensor, kv_cache: torch.Tensor, local_slots: 
                           stream: Optional[torch.cuda.Stream] = None
                           ) -> Tuple[torch.Tensor, torch.Tensor]:
     """sparse_mla_decode over a 4-bit cache [num_slots, 416]."""
-    dev = q.device
-    T, H, out, lse = _q_out_lse(q, out, lse, stream)
-    _fp4_cache(kv_cache, "kv_cache", dev)
-    _need(local_slots, "local_slots", torch.int32, dev)
-    if local_slots.dim() != 2 or local_slots.shape[0] != T:
-        raise ValueError("local_slots must be [T, K]")
-    K = local_slots.shape[1]
-    workspace, ws, ws_bytes = _workspace(
-        workspace, 0 if workspace is not None else fp4_decode_workspace_size(T, H, K), dev, stream)
-    _call("smla_sparse_mla_decode_fp4", dev, stream,
-          (q.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0], local_slots.data_ptr(), T, H, K,
-           float(sm_scale), out.data_ptr(), lse.data_ptr(), ws, ws_bytes))
+    if out is None or lse is None:
+        out, lse = _out_lse(q, out, lse, stream)
+    if workspace is None and q.dim() == 3 and local_slots.dim() == 2:
+        workspace = alloc_fp4_decode_workspace(q.shape[0], q.shape[1], local_slots.shape[1],
+                                               q.device, stream)
+    _check("smla_sparse_mla_decode_fp4",
+           _native().decode_fp4(q, kv_cache, local_slots, sm_scale, out, lse, workspace, stream))
     return out, lse
 
 
@@ -706,24 +639,15 @@ def dcp_sparse_mla_decode_fused_fp4(q: torch.Tensor, req_id_per_token: torch.Ten
                                     stream: Optional[torch.cuda.Stream] = None
                                     ) -> Tuple[torch.Tensor, torch.Tensor]:
     """dcp_sparse_mla_decode_fused over 4-bit pools [num_slots, 416]."""
-    dev = q.device
-    T, H, out, lse = _q_out_lse(q, out, lse, stream)
-    _shaped(req_id_per_token, "req_id_per_token", torch.int32, (T,), dev)
-    _need(topk_global, "topk_global", torch.int32, dev)
-    if topk_global.dim() != 2 or topk_global.shape[0] != T:
-        raise ValueError("topk_global must be [T, K]")
-    K = topk_global.shape[1]
-    D = len(kv_caches)
-    pools, nslots, bts, strides, widths, fmt, num_reqs = _pool_arrays(
-        kv_caches, block_tables, bt_widths, dev, range(D))
-    if fmt != CACHE_FP4:
-        raise ValueError(f"kv_caches[d] must be [num_slots, {FP4_ROW_BYTES}] uint8")
-    workspace, ws, ws_bytes = _workspace(
-        workspace, 0 if workspace is not None else fp4_decode_workspace_size(T, H, K), dev, stream)
-    _call("smla_dcp_sparse_mla_decode_fused_fp4", dev, stream,
-          (q.data_ptr(), T, H, K, float(sm_scale), req_id_per_token.data_ptr(),
-           topk_global.data_ptr(), num_reqs, D, int(block_size), int(interleave), pools, nslots,
-           bts, strides, widths, out.data_ptr(), lse.data_ptr(), ws, ws_bytes))
+    if out is None or lse is None:
+        out, lse = _out_lse(q, out, lse, stream)
+    if workspace is None and q.dim() == 3 and topk_global.dim() == 2:
+        workspace = alloc_fp4_decode_workspace(q.shape[0], q.shape[1], topk_global.shape[1],
+                                               q.device, stream)
+    _check("smla_dcp_sparse_mla_decode_fused_fp4",
+           _native().decode_fused_fp4(q, req_id_per_token, topk_global, kv_caches, block_tables,
+                                      block_size, sm_scale, interleave, bt_widths, out, lse,
+                                      workspace, stream))
     return out, lse
 
 
@@ -734,10 +658,12 @@ def window_decode_workspace_size(T: int, H: int, max_ctx: int, window: int, sink
 
 
 def alloc_window_decode_workspace(T: int, H: int, max_ctx: int, window: int, sinks: int, D: int,
-                                  interleave: int, rank: int, device) -> Optional[torch.Tensor]:
+                                  interleave: int, rank: int, device,
+                                  stream: Optional[torch.cuda.Stream] = None
+                                  ) -> Optional[torch.Tensor]:
     """Zero-filled workspace of dcp_window_mla_decode (None if none needed)."""
     n = window_decode_workspace_size(T, H, max_ctx, window, sinks, D, interleave, rank)
-    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+    return _new(n, torch.uint8, device, stream, zero=True) if n else None
 
 
 def dcp_window_mla_decode(q: torch.Tensor, ctx_lens: torch.Tensor, max_ctx: int, S: int,
@@ -753,26 +679,16 @@ def dcp_window_mla_decode(q: torch.Tensor, ctx_lens: torch.Tensor, max_ctx: int,
     request's first `sinks`, over 8- or 4-bit pools (told by their rows'
     bytes): merged over the D pools (rank = -1) or one rank's partial (only
     its pool and table are read).  q is [B*S, H, 576], rows b*S + s."""
-    dev = q.device
-    T, H, out, lse = _q_out_lse(q, out, lse, stream)
-    _need(ctx_lens, "ctx_lens", torch.int32, dev)
-    B = ctx_lens.shape[0]
-    if ctx_lens.dim() != 1 or T != B * S:
-        raise ValueError(f"q must be [B*S, H, {QK_DIM}] with B = len(ctx_lens)")
-    D = len(kv_caches)
-    if not -1 <= rank < D:
-        raise ValueError("rank must be -1 or one of the pools")
-    pools, nslots, bts, strides, widths, fmt, rows = _pool_arrays(
-        kv_caches, block_tables, bt_widths, dev, range(D) if rank < 0 else [rank])
-    if rows < B:
-        raise ValueError("block_tables need a row per request")
-    need = 0 if workspace is not None else window_decode_workspace_size(
-        T, H, max_ctx, window, sinks, D, interleave, rank)
-    workspace, ws, ws_bytes = _workspace(workspace, need, dev, stream)
-    _call("smla_dcp_window_mla_decode", dev, stream,
-          (q.data_ptr(), B, int(S), H, float(sm_scale), ctx_lens.data_ptr(), int(max_ctx),
-           int(window), int(sinks), D, int(rank), int(block_size), int(interleave), fmt, pools,
-           nslots, bts, strides, widths, out.data_ptr(), lse.data_ptr(), ws, ws_bytes))
+    if out is None or lse is None:
+        out, lse = _out_lse(q, out, lse, stream)
+    if workspace is None and q.dim() == 3:
+        workspace = alloc_window_decode_workspace(q.shape[0], q.shape[1], max_ctx, window, sinks,
+                                                  len(kv_caches), interleave, rank, q.device,
+                                                  stream)
+    _check("smla_dcp_window_mla_decode",
+           _native().decode_window(q, ctx_lens, max_ctx, S, window, sinks, kv_caches, block_tables,
+                                   block_size, sm_scale, rank, interleave, bt_widths, out, lse,
+                                   workspace, stream))
     return out, lse
 
 
@@ -798,30 +714,11 @@ def dcp_step_maps(ctx_lens: torch.Tensor, q_lens: torch.Tensor, free_blocks: tor
                   stream: Optional[torch.cuda.Stream] = None) -> StepMaps:
     """One rank's maps of a step of at most T rows; takes the blocks the new
     tokens need from the front of free_blocks into block_table (in place)."""
-    dev = ctx_lens.device
-    _need(ctx_lens, "ctx_lens", torch.int32, dev)
-    B = ctx_lens.shape[0]
-    if ctx_lens.dim() != 1:
-        raise ValueError("ctx_lens must be [B]")
-    _shaped(q_lens, "q_lens", torch.int32, (B,), dev)
-    _need(free_blocks, "free_blocks", torch.int32, dev)
-    if (block_table.dtype != torch.int32 or block_table.device != dev or block_table.dim() != 2
-            or block_table.stride(1) != 1 or block_table.shape[0] < B):
-        raise ValueError("block_table must be a 2-D int32 tensor with contiguous rows, one per request")
-    width = block_table.shape[1] if bt_width is None else int(bt_width)
-    if width > block_table.shape[1]:
-        raise ValueError("bt_width is past the table's columns")
     if out is None:
-        out = alloc_step_maps(B, T, dev, stream)
-    else:
-        for t, name, n in zip(out, StepMaps._fields, (B + 1, T, T, T, B, 1)):
-            _shaped(t, name, torch.int32, (n,), dev)
-    stride = block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
-    _call("smla_dcp_step_maps", dev, stream,
-          (ctx_lens.data_ptr(), q_lens.data_ptr(), B, int(T), int(D), int(rank), int(block_size),
-           int(interleave), free_blocks.data_ptr(), free_blocks.numel(), block_table.data_ptr(),
-           stride, width, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
-           out[3].data_ptr(), out[4].data_ptr(), out[5].data_ptr()))
+        out = alloc_step_maps(ctx_lens.shape[0], T, ctx_lens.device, stream)
+    _check("smla_dcp_step_maps",
+           _native().step_maps(ctx_lens, q_lens, free_blocks, block_table, T, D, rank, block_size,
+                               interleave, bt_width, out, stream))
     return out
 
 
@@ -834,27 +731,9 @@ def mla_cache_write(kv: torch.Tensor, slots: torch.Tensor, kv_cache: torch.Tenso
     that is a multiple of 8) into kv_cache [num_slots, 656 or 416] at
     slots[T] (-1: skipped).  gamma [512] bf16 (None: no norm), cos_sin
     [P, 64] fp32 with positions [T] (None: no rotation).  Returns kv_cache."""
-    dev = kv_cache.device
-    fmt = _cache_format(kv_cache, "kv_cache", dev)
-    if kv.dtype != torch.bfloat16 or kv.device != dev or kv.dim() != 2 or kv.shape[1] != QK_DIM \
-            or kv.stride(1) != 1:
-        raise ValueError(f"kv must be a bf16 [T, {QK_DIM}] tensor with contiguous rows")
-    T = kv.shape[0]
-    _shaped(slots, "slots", torch.int32, (T,), dev)
-    if gamma is not None:
-        _shaped(gamma, "gamma", torch.bfloat16, (V_DIM,), dev)
-    if cos_sin is not None:
-        if positions is None:
-            raise ValueError("cos_sin needs positions")
-        _shaped(positions, "positions", torch.int32, (T,), dev)
-        _shaped(cos_sin, "cos_sin", torch.float32, (cos_sin.shape[0], 64), dev)
-    _call("smla_mla_cache_write", dev, stream,
-          (kv.data_ptr(), kv.stride(0) if T > 1 else QK_DIM, T,
-           gamma.data_ptr() if gamma is not None else None, float(eps),
-           positions.data_ptr() if cos_sin is not None else None,
-           cos_sin.data_ptr() if cos_sin is not None else None,
-           cos_sin.shape[0] if cos_sin is not None else 0, int(rope_pairs), slots.data_ptr(), fmt,
-           kv_cache.data_ptr(), kv_cache.shape[0]))
+    _check("smla_mla_cache_write",
+           _native().cache_write(kv, slots, kv_cache, gamma, eps, positions, cos_sin, rope_pairs,
+                                 stream))
     return kv_cache
 
 
@@ -863,18 +742,7 @@ def mla_cache_gather(kv_cache: torch.Tensor, slots: torch.Tensor, *,
                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Rows slots[N] of the cache as bf16 or fp32 [N, 576] (-1: zeros).
     `out` may have any row stride that is a multiple of 16 bytes."""
-    dev = kv_cache.device
-    fmt = _cache_format(kv_cache, "kv_cache", dev)
-    _need(slots, "slots", torch.int32, dev)
-    if slots.dim() != 1:
-        raise ValueError("slots must be [N]")
-    N = slots.shape[0]
     if out is None:
-        out = _new((N, QK_DIM), dtype, dev, stream)
-    if out.dtype not in (torch.bfloat16, torch.float32) or out.device != dev \
-            or tuple(out.shape) != (N, QK_DIM) or out.stride(1) != 1:
-        raise ValueError(f"out must be a bf16 or fp32 [N, {QK_DIM}] tensor with contiguous rows")
-    _call("smla_mla_cache_gather", dev, stream,
-          (kv_cache.data_ptr(), kv_cache.shape[0], fmt, slots.data_ptr(), N, out.data_ptr(),
-           out.stride(0) if N > 1 else QK_DIM, int(out.dtype == torch.float32)))
+        out = _new((slots.shape[0], QK_DIM), dtype, kv_cache.device, stream)
+    _check("smla_mla_cache_gather", _native().cache_gather(kv_cache, slots, out, stream))
     return out
