@@ -639,13 +639,17 @@ def test_window_over_splits_long_contexts_and_freed_blocks(cuda_device, fmt):
 
 @pytest.mark.gpu
 def test_window_wide_enough_is_the_dense_decode(cuda_device):
+    """Two kernels, one definition: both within its bounds."""
     dev = cuda_device
     ctx = [300, 77]
     pools, tables = _paged(ctx, 2, 16, 1, "fp8", 8, dev)
     q = _q(4, 32, dev)
-    a = capi.dcp_dense_mla_decode(q, _i32(ctx, dev), 300, 2, pools, tables, 16, SCALE)
-    b = capi.dcp_window_mla_decode(q, _i32(ctx, dev), 300, 2, 300, 0, pools, tables, 16, SCALE)
-    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    npools, ntables, qf = [_np(p) for p in pools], [_np(t) for t in tables], _f64(q)
+    refs = [so.attend(qf[t], _rows_at(npools, ntables, t // 2, range(ctx[t // 2] - 1 + t % 2), 2, 16, 1), SCALE,
+                      2.0 ** -11) for t in range(4)]
+    _check(*capi.dcp_dense_mla_decode(q, _i32(ctx, dev), 300, 2, pools, tables, 16, SCALE), refs, "dense")
+    _check(*capi.dcp_window_mla_decode(q, _i32(ctx, dev), 300, 2, 300, 0, pools, tables, 16, SCALE), refs,
+           "window")
 
 
 @pytest.mark.gpu
