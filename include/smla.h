@@ -113,8 +113,8 @@ enum {
  * fp16), or when a nonzero scale is below 2^-22 (its keys would be fp16
  * subnormals and lose precision).  The result is still written; the bit says
  * it may be outside the stated tolerances.  An fp4 row's latent values are
- * exact in fp16; for those rows the bit stands for the q and rope values and
- * for a NaN scale. */
+ * exact in the kernel's keys and its rope values within 2^-18; for those rows
+ * the bit stands for the q and rope values and for a NaN scale. */
 /* With SMLA_DEVERR_TIMEOUT, bits 8..31 of the word tell which of the decode
  * kernel's internal waits gave up (a diagnostic bitmask, one bit per site). */
 

@@ -133,7 +133,8 @@ def attend(q, rows, sm_scale, key_step=0.0):
     fp16's step is 2^-24, so each of those fp16 roundings is off by up to
     2^-25 as well: a p against a sum that is at least 1 (a key's p is 2^0
     when it sets the reference), a key (where key_step is not 0) and a
-    partial output."""
+    partial output.  The kernel holds fp4 rows' keys times 2^-7, which puts
+    a rope value within 2^-18."""
     H = q.shape[0]
     if len(rows) == 0:
         return np.zeros((H, 512)), np.full(H, -np.inf), np.zeros((H, 512)), np.zeros(H)
@@ -146,6 +147,8 @@ def attend(q, rows, sm_scale, key_step=0.0):
     size = sm_scale * (np.abs(q) @ np.abs(k).T)
     tiny = 2.0 ** -25
     lse_tol = size.max(axis=1) * (42 * 2.0 ** -23 + key_step) + 2.0 ** -19
+    if rows.shape[1] == FP4_ROW_BYTES:
+        lse_tol = lse_tol + sm_scale * np.abs(q[:, 512:]).sum(axis=1) * 2.0 ** -18
     if key_step:
         lse_tol = lse_tol + sm_scale * np.abs(q).sum(axis=1) * tiny
     out = p @ lat

@@ -220,14 +220,15 @@ __device__ __forceinline__ bool scale_out_of_range(float s) {
   return !(s <= 65504.f / 448.f) || (s != 0.f && s < 0x1p-22f);
 }
 
-// 8 bf16 -> 8 fp16 (exact for values in fp16 range)
-__device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v) {
+// 8 bf16 -> 8 fp16 of value * up, up a power of two (exact where the product
+// is in fp16's normal range)
+__device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v, float up = 1.f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t o[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    o[k] = h2_bits(__floats2half2_rn(__uint_as_float(w[k] << 16),
-                                     __uint_as_float(w[k] & 0xffff0000u)));
+    o[k] = h2_bits(__floats2half2_rn(__uint_as_float(w[k] << 16) * up,
+                                     __uint_as_float(w[k] & 0xffff0000u) * up));
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
@@ -278,6 +279,11 @@ __device__ __forceinline__ float ex2(float x) {
 constexpr int kQkDims = 288;
 constexpr int kKSteps = kQkDims / 16;  // MMA K = 16
 
+// Softmax warps with a head row to work on: a warp whose 32 rows are all
+// padding computes, exchanges and stores nothing (its rows of S, P and O hold
+// arbitrary values that no other row sees).
+__device__ __forceinline__ int softmax_warps(int H) { return (H + 31) >> 5; }
+
 struct HalfRt {
   int c;  // CTA rank in the pair
 };
@@ -291,9 +297,11 @@ __device__ __forceinline__ HalfRt half_of(uint32_t c) {
 // A cache row's format.  CTA c stages the bytes of its half of a row, at
 // kRawStride per row, in kPieces pieces of 16 bytes: its code pieces, then
 // its scales, then its four rope pieces.  kCodes: 16-byte code pieces of one
-// converter thread (its 128 dims); kScaleBytes: bytes of its scales.
+// converter thread (its 128 dims).  kKeyScale: the operand tile holds the
+// keys times this; the softmax's scale and O's factor take it out again.
 struct Fp8Rows {
   static constexpr bool kFp4 = false;
+  static constexpr float kKeyScale = 1.f;
   static constexpr int kRowBytes = SMLA_ROW_BYTES;
   // pieces 0..15: codes [256c, 256c + 256) -> raw [0, 256); piece 16: the
   // four fp32 scales [512, 528) -> raw [256, 272); pieces 17..20: rope bf16
@@ -310,6 +318,7 @@ struct Fp8Rows {
 
 struct Fp4Rows {
   static constexpr bool kFp4 = true;
+  static constexpr float kKeyScale = 1.f / 128.f;
   static constexpr int kRowBytes = SMLA_FP4_ROW_BYTES;
   // pieces 0..7: codes [128c, 128c + 128) -> raw [0, 128); piece 8: sixteen
   // e4m3 scales [256 + 16c, 272 + 16c) -> raw [128, 144); pieces 9..12: rope
@@ -376,18 +385,20 @@ __device__ __forceinline__ uint32_t op_addr(uint32_t op, int key, int ldim) {
 }
 
 // 8 e2m1 codes (one 32-bit word, dim i in nibble i) -> 8 fp16 values code *
-// scale, in the order of o_col.  A nibble's sign moves to fp16's sign bit and
-// its exponent and mantissa bits to fp16's bits 11..9, which makes normal and
-// subnormal codes alike land on code * 2^-14 (bias 1 against 15); both
-// products are exact.
-__device__ __forceinline__ uint4 e2m1x8_scaled(uint32_t w, __half2 scale) {
-  const __half2 up = __float2half2_rn(16384.f);
+// scale * 2^-7, in the order of o_col; scale7 = scale * 2^7.  A nibble's sign
+// moves to fp16's sign bit and its exponent and mantissa bits to fp16's bits
+// 11..9, which makes normal and subnormal codes alike land on code * 2^-14
+// (bias 1 against 15); scale * 2^14 itself would overflow fp16, so 2^-7 stays
+// on the keys, and one product does.  It is exact: at most 6 significant
+// bits, a multiple of 2^-17.  (Rope values times 2^-7 are exact down to 2^-10
+// and within 2^-18 of the value below.)
+__device__ __forceinline__ uint4 e2m1x8_scaled(uint32_t w, __half2 scale7) {
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t mag = i < 3 ? w << (9 - 4 * i) : w >> 3;
     const uint32_t bits = (mag & 0x0E000E00u) | ((w << (12 - 4 * i)) & 0x80008000u);
-    o[i] = h2_bits(__hmul2(__hmul2(*reinterpret_cast<const __half2*>(&bits), up), scale));
+    o[i] = h2_bits(__hmul2(*reinterpret_cast<const __half2*>(&bits), scale7));
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -441,7 +452,8 @@ __device__ __forceinline__ bool convert_row(const ConvRegs<F>& r, uint32_t op, i
       const __half2 ss = __half2(sr);
       const uint32_t sb = h2_bits(ss);
       nan |= (sb & 0x7fffu) > 0x7c00u || (sb & 0x7fff0000u) > 0x7c000000u;
-      const __half2 s0 = __low2half2(ss), s1 = __high2half2(ss);
+      const __half2 up = __float2half2_rn(128.f);
+      const __half2 s0 = __hmul2(__low2half2(ss), up), s1 = __hmul2(__high2half2(ss), up);
       const int ldim = 128 * part + 32 * k;
       sts128(op_addr(op, key, ldim), e2m1x8_scaled(r.cur[k].x, s0));
       sts128(op_addr(op, key, ldim + 8), e2m1x8_scaled(r.cur[k].y, s0));
@@ -464,7 +476,8 @@ __device__ __forceinline__ bool convert_row(const ConvRegs<F>& r, uint32_t op, i
 #pragma unroll
   for (int q = 0; q < kRopePerPart; ++q) {
     over |= bf16x8_over_fp16(r.cur[F::kCodes + q]);
-    sts128(op_addr(op, key, 256 + 16 * part + 8 * q), bf16x8_to_f16x8(r.cur[F::kCodes + q]));
+    sts128(op_addr(op, key, 256 + 16 * part + 8 * q), 
+           bf16x8_to_f16x8(r.cur[F::kCodes + q], F::kKeyScale));
   }
   return over != 0 || bad_scale;
 }
@@ -501,9 +514,9 @@ __device__ void loader_loop(const DecodeArgs& a, Ctl* ctl, uint8_t* sm, int n, i
     const int r = int((uint32_t(p) * (F::kFp4 ? 5042u : 3121u)) >> 16);
     const int j = p - r * F::kPieces;
     // a piece past the tile (fp4's last round): row 64, never below a row count
-    pk[k] = p < kPieceCount ? uint32_t(r) << 25 | uint32_t(F::piece_src(c, j)) << 15 |
-                                  uint32_t(r * F::kRawStride + 16 * j)
-                            : uint32_t(kTileN) << 25;
+    pk[k] = uint32_t(r) << 25 | uint32_t(F::piece_src(c, j)) << 15 |
+            uint32_t(r * F::kRawStride + 16 * j);
+    if (kPieceCount % kLoaders != 0 && p >= kPieceCount) pk[k] = uint32_t(kTileN) << 25;
   }
   auto load = [&](int tile) {
     const int base = tile * kTileN;
@@ -586,7 +599,7 @@ __device__ void split_epilogue(const DecodeArgs& a, Ctl* ctl, int C, int64_t t, 
   uint4* wo = reinterpret_cast<uint4*>(a.ws_o + row * SMLA_V_DIM + C * 256);
   const bool has = ok && ntiles > 0;
   if (has) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l > 0.f ? 1.f / (l * F::kKeyScale) : 0.f;
 #pragma unroll 1
     for (int cc = 0; cc < 8; ++cc) {
       uint32_t r[32];
@@ -894,7 +907,10 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
   if (warp < 4) {
     // ------------------------------------------------ softmax + epilogue
     const int h = tid;  // head row == TMEM lane
-    const float scale_log2 = a.sm_scale * kLog2e;
+    const bool live_warp = warp < softmax_warps(a.H);
+    const uint32_t xa_bytes = softmax_warps(a.H) * (kXABytes / 4);
+    const uint32_t xb_bytes = softmax_warps(a.H) * (kXBBytes / 4);
+    const float scale_log2 = a.sm_scale * kLog2e / F::kKeyScale;
     float m_ref = -INFINITY;  // log2-domain reference maximum
     float l = 0.f;
     // Key-column split of the softmax: CTA c finishes the scores of keys
@@ -915,8 +931,8 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
     const uint32_t peer_xb1 = map_to_cta(smem_u32(&ctl->xb[1]), peer);
     if (h == 0) {
       for (int b = 0; b < 2 && b < ntiles; ++b) {
-        mbar_arrive_expect_tx(&ctl->xa[b], kXABytes);
-        mbar_arrive_expect_tx(&ctl->xb[b], kXBBytes);
+        mbar_arrive_expect_tx(&ctl->xa[b], xa_bytes);
+        mbar_arrive_expect_tx(&ctl->xb[b], xb_bytes);
       }
     }
     // The loop is software-pipelined across tiles: while the P of tile i is
@@ -960,10 +976,10 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
     // others' waits give up too, since every wait is an mbarrier wait that
     // sees the CTA's abort flag.  The four warps enter the loop on one
     // reduced decision and meet again only at the epilogue's barrier.
-    bool ok = ntiles == 0 || start_tile(0);
+    bool ok = ntiles == 0 || !live_warp || start_tile(0);
     ok = !named_bar_or(5, 128, !ok);
     int i = 0;
-    for (; i < ntiles && ok; ++i) {
+    for (; i < ntiles && ok && live_warp; ++i) {
       const int b = i & 1;
       const uint32_t xa_l = smem_u32(xbase) + b * kXBytes;  // this CTA's buffer set b
       const uint32_t xa_p = peer_x + b * kXBytes;           // the peer's
@@ -979,7 +995,7 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
         f[4 * j4 + 2] = sown[4 * j4 + 2] + v.z;
         f[4 * j4 + 3] = sown[4 * j4 + 3] + v.w;
       }
-      if (h == 0 && i + 2 < ntiles) mbar_arrive_expect_tx(&ctl->xa[b], kXABytes);
+      if (h == 0 && i + 2 < ntiles) mbar_arrive_expect_tx(&ctl->xa[b], xa_bytes);
       const int valid = min(kTileN, n - i * kTileN) - oc0;  // valid columns of this CTA's 32
       if (valid < 32) {
 #pragma unroll
@@ -1044,7 +1060,7 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
         pp[4 * q + 3] = v.w;
       }
       const float2 peer_rl = ld_shared_f2(xb_l + kXBPBytes + h * 8);
-      if (h == 0 && i + 2 < ntiles) mbar_arrive_expect_tx(&ctl->xb[b], kXBBytes);
+      if (h == 0 && i + 2 < ntiles) mbar_arrive_expect_tx(&ctl->xb[b], xb_bytes);
       // 6) the shared reference moves to the larger of the two (identically
       //    on both CTAs); what was computed against a smaller one is redone
       const float r_new = fmaxf(my_ref, peer_rl.x);
@@ -1110,7 +1126,7 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
       ok = false;
     }
     // epilogue
-    if (ok && ntiles > 0) {
+    if (ok && ntiles > 0 && live_warp) {
       ok = __all_sync(0xffffffffu, wait_bar(&ctl->pv_done, (ntiles - 1) & 1, abort, kWsPvLast));
       tc_fence_after();
     }
@@ -1118,8 +1134,8 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
     // 128-thread named barrier)
     ok = !named_bar_or(4, 128, !ok);
     if (a.splits > 1) {
-      split_epilogue<F>(a, ctl, C, t, split, ntiles, m_ref, l, tb, warp, h, ok);
-    } else if (ok) {
+      split_epilogue<F>(a, ctl, C, t, split, ntiles, m_ref, l, tb, warp, h, ok && live_warp);
+    } else if (ok && live_warp) {
       // tcgen05.ld is warp-collective: every lane loads, only live heads store
       const bool live = h < a.H;
       uint4* dst = reinterpret_cast<uint4*>(a.out + (t * a.H + (live ? h : 0)) * SMLA_V_DIM +
@@ -1130,7 +1146,9 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
           for (int k = 0; k < 32; ++k) dst[k] = make_uint4(0, 0, 0, 0);
         }
       } else {
-        const float inv = 1.f / l;
+        const float inv = 1.f / (l * F::kKeyScale);
+        // 32-byte stores fill whole sectors (`out` itself may be 16-byte aligned)
+        const bool whole = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
 #pragma unroll 1
         for (int cc = 0; cc < 8; ++cc) {
           uint32_t r[32];
@@ -1144,7 +1162,10 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
                                       __uint_as_float(r[o_col<F>(2 * j + 1)]) * inv);
             o[j] = *reinterpret_cast<uint32_t*>(&v);
           }
-          if (live) {
+          if (live && whole) {
+            stg256(dst + cc * 4, o);
+            stg256(dst + cc * 4 + 2, o + 8);
+          } else if (live) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               dst[cc * 4 + k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
@@ -1226,6 +1247,11 @@ struct RowRange {
 // a generated row and places them.  Returns false for -1 / foreign / invalid
 // entries, recording input errors in `err`.
 template <int kMode>
+__device__ __forceinline__ int32_t place_entry(int32_t v, const RowRange& range) {
+  return kMode == kModeWindow && v >= range.first ? v + range.skip : v;
+}
+
+template <int kMode>
 __device__ __forceinline__ bool resolve_entry(const DecodeArgs& a, const Ctl* ctl, const int32_t* bt,
                                               bool staged, bool req_ok, const RowRange& range,
                                               int32_t v, int32_t& slot, int& shard,
@@ -1242,8 +1268,7 @@ __device__ __forceinline__ bool resolve_entry(const DecodeArgs& a, const Ctl* ct
   // Pools: every entry takes the same straight-line path (no branch per
   // check), so the 16 entries of a thread overlap their shared-memory reads.
   const bool live = v >= 0 && req_ok && !(generated(kMode) && v >= range.limit);
-  int32_t vv = live ? v : 0;
-  if (kMode == kModeWindow && vv >= range.first) vv += range.skip;
+  const int32_t vv = place_entry<kMode>(live ? v : 0, range);
   int d;
   int32_t lp;
   if (generated(kMode) && a.dense_rank >= 0) {
@@ -1272,13 +1297,9 @@ __device__ __forceinline__ bool resolve_entry(const DecodeArgs& a, const Ctl* ct
 // How many of the first n positions rank `dense_rank` holds: whole rounds of
 // I*D positions give I each, then the partial round.
 __device__ __forceinline__ int32_t rank_rows(const DecodeArgs& a, int32_t n) {
-  // a round longer than 32 bits never completes
-  const uint64_t round = uint64_t(a.interleave) * uint32_t(a.D);
-  const uint32_t ID = round > 0xffffffffull ? 0xffffffffu : uint32_t(round);
-  const int32_t full = int32_t(uint32_t(n) / ID);
-  const int64_t rem = int64_t(uint32_t(n) - uint32_t(full) * ID);
-  const int64_t mine = rem - int64_t(a.dense_rank) * a.interleave;
-  return full * a.interleave + int32_t(min(max(mine, int64_t(0)), int64_t(a.interleave)));
+  const int32_t ID = a.interleave * a.D;
+  const int32_t full = n / ID, rem = n - full * ID;
+  return full * a.interleave + min(max(rem - a.dense_rank * a.interleave, 0), a.interleave);
 }
 
 // Dense and windowed decode: the request of row t and the range of its raw
@@ -1390,9 +1411,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->freed[st], 1);
     }
     mbar_init(&ctl->s_full, 1);
-    mbar_init(&ctl->s_free, 128);
+    mbar_init(&ctl->s_free, 32 * softmax_warps(a.H));  // one arrival per softmax thread
     mbar_init(&ctl->pv_done, 1);
-    mbar_init(&ctl->p_full, 128);  // one arrival per softmax thread
+    mbar_init(&ctl->p_full, 32 * softmax_warps(a.H));
     for (int st = 0; st < kRawStages; ++st) {
       mbar_init(&ctl->raw_full[st], kLoaders);  // one arrival per loader
       mbar_init(&ctl->raw_empty[st], 4);        // one arrival per converter warp
@@ -1458,7 +1479,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // Q half -> TMEM, overlapping the compaction below
     // the whole q tile landed (issued by thread 0 before the set-up barrier)
     bool qok = wait_bar(&ctl->q_tma, 0, &ctl->abort, kWsQReady);
-    if (q_to_tmem<F>(ctl->tbase, warp, tid, qok && tid < a.H, smem_u32(sm + kOffOp)))
+    if (warp < softmax_warps(a.H) &&
+        q_to_tmem<F>(ctl->tbase, warp, tid, qok && tid < a.H, smem_u32(sm + kOffOp)))
       atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
     tc_fence_before();
     mbar_arrive(&ctl->q_ready);
@@ -1485,67 +1507,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       req_ok = dense_row<kMode>(a, t, r, range, e2);
       if (d == 0) err |= e2;
     }
-    // 1) this thread's kPer raw entries (loaded before the set-up barrier,
-    //    four 16-byte loads when the row allows; a dense row's entries are
-    //    just their indices), and, with D pools, the request's block-table
-    //    rows copied into shared memory by all the compacting threads
-    const int j0 = e_begin + d * kPer;
-    if (generated(kMode)) {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) vs[k] = j0 + k;
-    }
-    int32_t* bt = reinterpret_cast<int32_t*>(sm + kOffX);
-    const bool staged = kPools && ctl->bt_staged;
-    if (staged) {
-      const uint32_t bt0 = smem_u32(bt);
-#pragma unroll 1
-      for (int sd = 0; sd < a.D; ++sd) {
-#pragma unroll 1
-        for (int col = d; col < ctl->meta[sd].bt_width; col += kListThreads)
-          cp_async_4(bt0 + 4u * uint32_t(ctl->meta[sd].bt_off + col), ctl->bt_row[sd] + col);
+    // A window's entries are valid unless an input is not: the threads take
+    // them in turn, each entry at its own place in the list.  One that is not
+    // valid sends the CTA through the compaction below.
+    bool listed = false;
+    if (kMode == kModeWindow) {
+      const int cnt = req_ok ? min(e_end, range.limit) - e_begin : 0;
+      bool all = true;
+#pragma unroll 2
+      for (int j = d; j < cnt; j += kListThreads) {
+        int32_t slot = -1;
+        int sh = 0;
+        unsigned e1 = 0;
+        all = resolve_entry<kMode>(a, ctl, nullptr, false, req_ok, range, e_begin + j, slot, sh, e1) &&
+              all;
+        list[j] = slot;
+        list_shard[j] = uint8_t(sh);
       }
-      cp_async_commit();
-      cp_async_wait<0>();
-      named_bar_sync(3, kListThreads);  // every thread's copies are visible
+      listed = !named_bar_or(3, kListThreads, !all);
+      if (listed && d == 0) ctl->n_list = max(cnt, 0);
     }
-    // 2) resolve the 16 entries from registers and shared memory
-    int shards[kPer];
-    unsigned keep = 0;
+    if (!listed) {
+      // 1) this thread's kPer raw entries (loaded before the set-up barrier,
+      //    four 16-byte loads when the row allows; a dense row's entries are
+      //    just their indices), and, with D pools, the request's block-table
+      //    rows copied into shared memory by all the compacting threads
+      const int j0 = e_begin + d * kPer;
+      if (generated(kMode)) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int32_t v = vs[k];
-      vs[k] = -1;
-      shards[k] = 0;
-      const bool ok = resolve_entry<kMode>(a, ctl, bt, staged, req_ok, range,
-                                           j0 + k < e_end ? v : -1, vs[k], shards[k], err);
-      keep |= unsigned(ok) << k;
-    }
-    const int cnt = __popc(keep);
-    int incl = cnt;  // inclusive warp scan
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += y;
-    }
-    if (lane == 31) ctl->warp_cnt[warp - 4] = incl;
-    named_bar_sync(3, kListThreads);
-    int wbase = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kListThreads / 32; ++w) {
-      const int x = ctl->warp_cnt[w];
-      wbase += (w < warp - 4) ? x : 0;
-      total += x;
-    }
-    int pos = wbase + incl - cnt;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      if (keep & (1u << k)) {
-        list[pos] = vs[k];
-        list_shard[pos] = uint8_t(shards[k]);
-        ++pos;
+        for (int k = 0; k < kPer; ++k) vs[k] = j0 + k;
       }
+      int32_t* bt = reinterpret_cast<int32_t*>(sm + kOffX);
+      const bool staged = kPools && ctl->bt_staged;
+      if (staged) {
+        const uint32_t bt0 = smem_u32(bt);
+#pragma unroll 1
+        for (int sd = 0; sd < a.D; ++sd) {
+#pragma unroll 1
+          for (int col = d; col < ctl->meta[sd].bt_width; col += kListThreads)
+            cp_async_4(bt0 + 4u * uint32_t(ctl->meta[sd].bt_off + col), ctl->bt_row[sd] + col);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        named_bar_sync(3, kListThreads);  // every thread's copies are visible
+      }
+      // 2) resolve the 16 entries from registers and shared memory
+      int shards[kPer];
+      unsigned keep = 0;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int32_t v = vs[k];
+        vs[k] = -1;
+        shards[k] = 0;
+        const bool ok = resolve_entry<kMode>(a, ctl, bt, staged, req_ok, range,
+                                             j0 + k < e_end ? v : -1, vs[k], shards[k], err);
+        keep |= unsigned(ok) << k;
+      }
+      const int cnt = __popc(keep);
+      int incl = cnt;  // inclusive warp scan
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+      }
+      if (lane == 31) ctl->warp_cnt[warp - 4] = incl;
+      named_bar_sync(3, kListThreads);
+      int wbase = 0, total = 0;
+#pragma unroll
+      for (int w = 0; w < kListThreads / 32; ++w) {
+        const int x = ctl->warp_cnt[w];
+        wbase += (w < warp - 4) ? x : 0;
+        total += x;
+      }
+      int pos = wbase + incl - cnt;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        if (keep & (1u << k)) {
+          list[pos] = vs[k];
+          list_shard[pos] = uint8_t(shards[k]);
+          ++pos;
+        }
+      }
+      if (d == 0) ctl->n_list = total;
     }
-    if (d == 0) ctl->n_list = total;
     if (err) atomicOr(&g_decode_error, err);
   }
   tc_fence_before();
