@@ -100,6 +100,42 @@ __device__ __forceinline__ Pair pair_rsqrt(Pair m) {
   return {r, 0.5f * r * u};
 }
 
+// The codes of a lane's 16 values y r / d, packed into kWords words by
+// pack(v0, v1, pair index).  In fp32 alone a quotient is within 2^-21 of its
+// exact value, so where the codes of v (1 - 2^-20) and v (1 + 2^-20) agree they
+// are the exact quotient's; a warp with a value that close to a border (one
+// row in some thousands) takes the exact quotients.  Called by whole warps.
+template <int kWords, class Pack>
+__device__ __forceinline__ void quantise(const float* y, Pair r, float d, float inv, uint32_t* w,
+                                         Pack pack) {
+  constexpr int kPairs = 8 / kWords;  // pairs of values a word
+  const float t = __fmul_rn(r.hi, inv);
+  const float below = __fmul_rn(t, 1.f - 0x1p-20f), above = __fmul_rn(t, 1.f + 0x1p-20f);
+  uint32_t near = 0;
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) {
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const float a = y[2 * (kPairs * k + i)], b = y[2 * (kPairs * k + i) + 1];
+      lo |= pack(__fmul_rn(a, below), __fmul_rn(b, below), i);
+      hi |= pack(__fmul_rn(a, above), __fmul_rn(b, above), i);
+    }
+    w[k] = lo;
+    near |= lo ^ hi;
+  }
+  if (!__any_sync(0xffffffffu, near != 0)) return;
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) {
+    w[k] = 0;
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const float a = y[2 * (kPairs * k + i)], b = y[2 * (kPairs * k + i) + 1];
+      w[k] |= pack(quotient_odd(pair_mul(a, r), d, inv), quotient_odd(pair_mul(b, r), d, inv), i);
+    }
+  }
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -202,18 +238,15 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(const CacheWri
     const float d = scale > 0.f ? scale : 1.f;
     const float inv = __frcp_rn(d);
     uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t c = 0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float2 v = make_float2(quotient_odd(pair_mul(y[4 * k + 2 * h], r), d, inv),
-                                     quotient_odd(pair_mul(y[4 * k + 2 * h + 1], r), d, inv));
-        c |= uint32_t(__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3)) << (16 * h);
-      }
-      w[k] = (scale > 0.f && finite) ? c : 0u;
-    }
-    *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+    quantise<4>(
+        y, r, d, inv, w,
+        [](float a, float b, int i) {
+          return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3))
+                 << (16 * (i & 1));
+        });
+    const bool keep = scale > 0.f && finite;
+    *reinterpret_cast<uint4*>(dst + 16 * lane) =
+        keep ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0u, 0u, 0u, 0u);
     if ((lane & 7) == 0)
       *reinterpret_cast<float*>(dst + 512 + 4 * (lane >> 3)) =
           finite ? scale : __int_as_float(0x7fc00000);
@@ -223,13 +256,13 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(const CacheWri
     const float scale = __half2float(__half(__nv_cvt_fp8_to_halfraw(sc, __NV_E4M3)));
     const float d = scale > 0.f ? scale : 1.f;
     const float inv = __frcp_rn(d);
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 v = make_float2(quotient_odd(pair_mul(y[2 * k], r), d, inv),
-                                   quotient_odd(pair_mul(y[2 * k + 1], r), d, inv));
-      w[k >> 2] |= uint32_t(__nv_cvt_float2_to_fp4x2(v, __NV_E2M1, cudaRoundNearest)) << (8 * (k & 3));
-    }
+    uint32_t w[2];
+    quantise<2>(
+        y, r, d, inv, w,
+        [](float a, float b, int i) {
+          return uint32_t(__nv_cvt_float2_to_fp4x2(make_float2(a, b), __NV_E2M1, cudaRoundNearest))
+                 << (8 * (i & 3));
+        });
     const bool keep = scale > 0.f && finite;
     *reinterpret_cast<uint2*>(dst + 8 * lane) = keep ? make_uint2(w[0], w[1]) : make_uint2(0u, 0u);
     dst[256 + lane] = finite ? uint8_t(sc) : uint8_t(0x7f);
