@@ -150,7 +150,9 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(const CacheWri
   constexpr int kRope = kRowBytes - 128;
   const int lane = threadIdx.x & 31;
   const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  griddep_launch_dependents();
   if (t >= a.T) return;
+  griddep_wait();
   const int32_t slot = __ldg(a.slots + t);
   const int32_t pos = a.cos_sin ? __ldg(a.positions + t) : 0;
   if (slot < 0) return;
@@ -310,7 +312,9 @@ __global__ void __launch_bounds__(kWarps * 32) cache_gather_kernel(const CacheGa
   constexpr int kCodeBytes = kFp4 ? 4 : 8;  // 8 dims
   const int lane = threadIdx.x & 31;
   const int64_t n0 = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kRows;
+  griddep_launch_dependents();
   if (n0 >= a.N) return;
+  griddep_wait();
   int32_t slot[kRows];
   bool bad = false;
 #pragma unroll
@@ -385,24 +389,15 @@ __global__ void __launch_bounds__(kWarps * 32) cache_gather_kernel(const CacheGa
 
 cudaError_t launch_cache_write(const CacheWriteArgs& a, bool fp4, cudaStream_t s) {
   const unsigned grid = unsigned((int64_t(a.T) + kWarps - 1) / kWarps);
-  if (fp4)
-    cache_write_kernel<true><<<grid, kWarps * 32, 0, s>>>(a);
-  else
-    cache_write_kernel<false><<<grid, kWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(fp4 ? cache_write_kernel<true> : cache_write_kernel<false>, grid, kWarps * 32,
+                           0, s, a);
 }
 
 cudaError_t launch_cache_gather(const CacheGatherArgs& a, bool fp4, bool fp32, cudaStream_t s) {
   const unsigned grid = unsigned((int64_t(a.N) + kWarps * kRows - 1) / (kWarps * kRows));
-  if (fp4 && fp32)
-    cache_gather_kernel<true, true><<<grid, kWarps * 32, 0, s>>>(a);
-  else if (fp4)
-    cache_gather_kernel<true, false><<<grid, kWarps * 32, 0, s>>>(a);
-  else if (fp32)
-    cache_gather_kernel<false, true><<<grid, kWarps * 32, 0, s>>>(a);
-  else
-    cache_gather_kernel<false, false><<<grid, kWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  const auto kernel = fp4 ? (fp32 ? cache_gather_kernel<true, true> : cache_gather_kernel<true, false>)
+                          : (fp32 ? cache_gather_kernel<false, true> : cache_gather_kernel<false, false>);
+  return launch_overlapped(kernel, grid, kWarps * 32, 0, s, a);
 }
 
 cudaError_t cache_error_word(uint32_t* flags, bool clear) {

@@ -141,15 +141,6 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Programmatic dependent launch: a grid launched after this one with
-// programmatic stream serialisation may be scheduled once every CTA here has
-// signalled (or exited); it waits for this grid's completion and memory in
-// griddepcontrol.wait.
-__device__ __forceinline__ void griddep_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 __device__ __forceinline__ uint64_t globaltimer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -1364,6 +1355,10 @@ __device__ void publish_empty_split(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, 
   if (ctl->is_last) combine_splits(a, sm, C, t);
 }
 
+// Decodes of the serving step are launched behind the step's short kernels.
+template <int kMode, class F>
+constexpr bool overlapped() { return F::kFp4 || kMode == kModeWindow; }
+
 template <int kMode, class F>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     sparse_mla_decode_kernel(const __grid_constant__ DecodeArgs a) {
@@ -1388,6 +1383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // a separate split combine (if any) may be scheduled on SMs this grid
   // leaves idle
   griddep_launch_dependents();
+  if (overlapped<kMode, F>()) griddep_wait();
   if (generated(kMode)) {
     int32_t r;
     RowRange range;
@@ -1842,22 +1838,18 @@ cudaError_t launch_impl(const DecodeArgs& args, cudaStream_t s) {
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   a.combine_in_kernel = combine_in_kernel(ctas, a.splits, sms) ? 1 : 0;
-  sparse_mla_decode_kernel<kMode, F><<<dim3(unsigned(ctas)), dim3(kThreads), kSmemBytes, s>>>(a);
-  e = cudaGetLastError();
+  if (overlapped<kMode, F>()) {
+    e = launch_overlapped(sparse_mla_decode_kernel<kMode, F>, unsigned(ctas), kThreads, kSmemBytes, s, a);
+  } else {
+    sparse_mla_decode_kernel<kMode, F><<<dim3(unsigned(ctas)), dim3(kThreads), kSmemBytes, s>>>(a);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess || a.splits == 1 || a.T == 0 || a.combine_in_kernel) return e;
   // the separate split combine, scheduled while the decode grid drains
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(int64_t(a.T) * 2 * ((a.H + kCombHeads - 1) / kCombHeads)));
-  cfg.blockDim = dim3(kCombHeads * 32);
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, split_combine_kernel, static_cast<const uint16_t*>(a.ws_o),
-                            static_cast<const float*>(a.ws_ml), a.out, a.lse, a.H, a.splits);
+  const unsigned combine = unsigned(int64_t(a.T) * 2 * ((a.H + kCombHeads - 1) / kCombHeads));
+  return launch_overlapped(split_combine_kernel, combine, kCombHeads * 32, 0, s,
+                           static_cast<const uint16_t*>(a.ws_o), static_cast<const float*>(a.ws_ml),
+                           a.out, a.lse, a.H, a.splits);
 }
 
 // Multiply-shift constants of the divisions by I, D and the block size.

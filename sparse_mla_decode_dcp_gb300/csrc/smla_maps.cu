@@ -55,6 +55,8 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapsArgs a) {
   const int warp = tid >> 5;
   const int lane = tid & 31;
   const bool first_cta = blockIdx.x == 0;
+  griddep_launch_dependents();
+  griddep_wait();
   unsigned err = 0;
 
   // 1) both exclusive sums, requests in chunks of one per thread; 64-bit, so
@@ -195,8 +197,7 @@ cudaError_t launch_step_maps(const MapsArgs& args, cudaStream_t s) {
   }
   const int64_t need = (int64_t(a.T) + kThreads - 1) / kThreads;
   const unsigned grid = unsigned(need < 1 ? 1 : need > 152 ? 152 : need);
-  step_maps_kernel<<<grid, kThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(step_maps_kernel, grid, kThreads, smem, s, a);
 }
 
 cudaError_t maps_error_word(uint32_t* flags, bool clear) {
