@@ -141,7 +141,8 @@ smla_status smla_sparse_mla_decode(
 }
 
 size_t smla_fp4_decode_workspace_size(int32_t T, int32_t H, int32_t K) {
-  return smla_decode_workspace_size(T, H, K);
+  if (T < 0 || H < 1 || H > SMLA_MAX_HEADS || K < 1) return 0;
+  return smla::fp4_decode_workspace_bytes(T, H, K);
 }
 
 smla_status smla_sparse_mla_decode_fp4(
@@ -395,7 +396,7 @@ size_t smla_window_decode_workspace_size(int32_t T, int32_t H, int32_t max_ctx, 
   if (T < 0 || H < 1 || H > SMLA_MAX_HEADS || max_ctx < 1 || window < 1 || sinks < 0 || D < 1 ||
       interleave < 1 || rank < -1 || rank >= D)
     return 0;
-  return smla::decode_workspace_bytes(
+  return smla::window_decode_workspace_bytes(
       T, H, window_entries(max_ctx, window, sinks, D, interleave, rank));
 }
 
@@ -416,7 +417,7 @@ smla_status smla_dcp_window_mla_decode(
   a.window = window;
   a.sinks = sinks;
   a.K = window_entries(max_ctx, window, sinks, D, interleave, rank);
-  st = take_workspace(workspace, workspace_bytes, smla::decode_workspace_bytes(a.T, H, a.K), a);
+  st = take_workspace(workspace, workspace_bytes, smla::window_decode_workspace_bytes(a.T, H, a.K), a);
   if (st != SMLA_OK) return st;
   return from_cuda(smla::launch_decode_window(a, format == SMLA_CACHE_FP4,
                                               static_cast<cudaStream_t>(stream)));

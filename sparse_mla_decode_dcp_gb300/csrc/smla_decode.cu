@@ -6,7 +6,7 @@
 namespace smla {
 
 size_t decode_workspace_bytes(int32_t T, int32_t H, int32_t K) {
-  return ws_layout(T, H, K).total;
+  return ws_layout(T, H, decode_splits(T, K)).total;
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
@@ -58,7 +58,7 @@ cudaError_t noalloc_scratch_ptr(void** ptr) {
 }  // namespace
 
 cudaError_t launch_decode_noalloc(const DecodeArgs& args, cudaStream_t s) {
-  const WsLayout w = ws_layout(args.T, args.H, args.K);
+  const WsLayout w = ws_layout(args.T, args.H, decode_splits(args.T, args.K));
   if (w.total > kNoAllocScratchBytes) return cudaErrorInvalidValue;  // caller checks first
   DecodeArgs a = args;
   a.workspace = nullptr;

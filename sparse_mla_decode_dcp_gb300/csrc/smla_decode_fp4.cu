@@ -4,6 +4,10 @@
 
 namespace smla {
 
+size_t fp4_decode_workspace_bytes(int32_t T, int32_t H, int32_t K) {
+  return ws_layout(T, H, model_splits(T, K)).total;
+}
+
 cudaError_t launch_decode_fp4(const DecodeArgs& a, cudaStream_t s) {
   return launch_impl<kModeSlots, Fp4Rows>(a, s);
 }

@@ -1383,18 +1383,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // a separate split combine (if any) may be scheduled on SMs this grid
   // leaves idle
   griddep_launch_dependents();
-  if (overlapped<kMode, F>()) griddep_wait();
-  if (generated(kMode)) {
+  // a generated row's split without a position: published, nothing to do
+  auto empty_split = [&]() -> bool {
     int32_t r;
     RowRange range;
     unsigned e2 = 0;
     const bool row_ok = dense_row<kMode>(a, t, r, range, e2);
-    if (!row_ok || min(e_end, range.limit) <= e_begin) {
-      if (tid == 0 && e2) atomicOr(&g_decode_error, e2);
-      publish_empty_split(a, sm, ctl, t, split, hr.c);
-      return;
-    }
-  }
+    if (row_ok && min(e_end, range.limit) > e_begin) return false;
+    if (tid == 0 && e2) atomicOr(&g_decode_error, e2);
+    publish_empty_split(a, sm, ctl, t, split, hr.c);
+    return true;
+  };
+  if (kMode == kModeDense && empty_split()) return;
   if (warp == kMmaWarp) {
     tmem_alloc(&ctl->tbase, kTmemCols);
     tmem_relinquish();
@@ -1421,9 +1421,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&ctl->end, 1);
     ctl->abort = 0;
     fence_mbar_init_cluster();
-    // q lands in the (still idle) operand stages while the CTA sets up
-    issue_q_tma(a, t, hr.c, smem_u32(sm + kOffOp), &ctl->q_tma);
   }
+  if (overlapped<kMode, F>()) {
+    griddep_wait();  // set-up so far overlaps the end of the kernel before
+    if (kMode == kModeWindow && empty_split()) {
+      if (warp == kMmaWarp) tmem_dealloc(ctl->tbase, kTmemCols);
+      return;
+    }
+  }
+  // q lands in the (still idle) operand stages while the CTA sets up
+  if (tid == 0) issue_q_tma(a, t, hr.c, smem_u32(sm + kOffOp), &ctl->q_tma);
   // The compacting warps' raw entries (kPer each of the row's split, see the
   // compaction below) are loaded before the set-up barrier, so that their
   // memory round trip overlaps the request id's.
@@ -1736,13 +1743,36 @@ int decode_splits(int32_t T, int32_t K) {
   return max(s, 1);
 }
 
+// The serving step's decodes take the split count that ends first by a model
+// of a launch of one wave of pairs, in 1/100 us, fitted to fp4 decodes of 1-64
+// rows of 128-2048 entries (H = 128): 950 for a pair's set-up and epilogue,
+// 145 a tile of 64 keys, 7 a pair at work on the GPU, and 420 + 12 a split for
+// the kernel that merges splits.  Measured against at least 256 entries a
+// split: 1 row of 512 entries 8 splits 15.8 us (2: 22.8), 1 of 2048 16 splits
+// 18.3 (8: 19.7), 16 of 512 4 splits 19.5 (2: 24.3).  Splits that need a second
+// wave never won (80 rows of 2048: 1 split 117 us, 2 119).  Like decode_splits
+// a function of the shape alone, with at most kMaxList entries per split.
+int model_splits(int32_t T, int32_t K) {
+  const int lo = (K + kMaxList - 1) / kMaxList;
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int s = 1; T > 0 && int64_t(T) * s <= kClusterSlots && (s - 1) * kTileN < K; ++s) {
+    const int tiles = ((K + s - 1) / s + kTileN - 1) / kTileN;
+    const int64_t cost = 950 + 145 * int64_t(tiles) + 7 * T * s + (s > 1 ? 420 + 12 * s : 0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return max(best, lo);
+}
+
 struct WsLayout {
   size_t o_off, ml_off, tick_off, total;
 };
 
-WsLayout ws_layout(int32_t T, int32_t H, int32_t K) {
+WsLayout ws_layout(int32_t T, int32_t H, int32_t S) {
   WsLayout w{0, 0, 0, 0};
-  const int S = decode_splits(T, K);
   if (S == 1 || T <= 0) return w;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   w.o_off = 0;
@@ -1822,8 +1852,10 @@ cudaError_t launch_impl(const DecodeArgs& args, cudaStream_t s) {
     const cudaError_t e = encode_q_maps(a);
     if (e != cudaSuccess) return e;
   }
-  a.splits = a.single_split ? 1 : decode_splits(a.T, a.K);
-  const WsLayout w = a.splits > 1 ? ws_layout(a.T, a.H, a.K) : WsLayout{0, 0, 0, 0};
+  a.splits = a.single_split          ? 1
+             : overlapped<kMode, F>() ? model_splits(a.T, a.K)
+                                      : decode_splits(a.T, a.K);
+  const WsLayout w = ws_layout(a.T, a.H, a.splits);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   a.ws_o = w.total ? reinterpret_cast<uint16_t*>(ws + w.o_off) : nullptr;
   a.ws_ml = w.total ? reinterpret_cast<float*>(ws + w.ml_off) : nullptr;
@@ -1837,7 +1869,10 @@ cudaError_t launch_impl(const DecodeArgs& args, cudaStream_t s) {
   int sms = 0;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  a.combine_in_kernel = combine_in_kernel(ctas, a.splits, sms) ? 1 : 0;
+  // The serving step's decodes merge in a second kernel whenever the grid
+  // leaves SMs idle for it (25 rows of 2048 in 3 splits: 35.7 us against 38.0;
+  // 38 rows in 2, which fill the GPU: 46.8 against 45.1).
+  a.combine_in_kernel = overlapped<kMode, F>() ? ctas >= sms : combine_in_kernel(ctas, a.splits, sms);
   if (overlapped<kMode, F>()) {
     e = launch_overlapped(sparse_mla_decode_kernel<kMode, F>, unsigned(ctas), kThreads, kSmemBytes, s, a);
   } else {

@@ -4,6 +4,10 @@
 
 namespace smla {
 
+size_t window_decode_workspace_bytes(int32_t T, int32_t H, int32_t K) {
+  return ws_layout(T, H, model_splits(T, K)).total;
+}
+
 cudaError_t launch_decode_window(const DecodeArgs& args, bool fp4, cudaStream_t s) {
   DecodeArgs a = args;
   set_divisors(a);

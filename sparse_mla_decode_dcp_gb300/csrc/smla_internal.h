@@ -209,6 +209,8 @@ cudaError_t launch_topk_select(const TopkArgs& a, void* workspace, cudaStream_t 
 size_t topk_workspace_bytes(int32_t T, int32_t L, int32_t K);
 cudaError_t launch_topk_merge(const TopkArgs& a, cudaStream_t s);
 size_t decode_workspace_bytes(int32_t T, int32_t H, int32_t K);
+size_t fp4_decode_workspace_bytes(int32_t T, int32_t H, int32_t K);
+size_t window_decode_workspace_bytes(int32_t T, int32_t H, int32_t K);
 
 cudaError_t launch_step_maps(const MapsArgs& a, cudaStream_t s);
 cudaError_t maps_error_word(uint32_t* flags, bool clear);

@@ -638,6 +638,41 @@ def test_window_over_splits_long_contexts_and_freed_blocks(cuda_device, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_window_rows_longer_than_a_pairs_list(cuda_device, fmt):
+    """Up to 4100 keys a row, over several key ranges.  Then the same with
+    blocks missing."""
+    dev = cuda_device
+    B, S, H, D, bs, window, sinks = 4, 19, 3, 2, 16, 4090, 10
+    ctx = [4150, 2049, 2100, 3000]
+    pools, tables = _paged(ctx, D, bs, 1, fmt, 6, dev)
+    q = _q(B * S, H, dev, 9)
+    npools, qf = [_np(p) for p in pools], _f64(q)
+    step = 2.0 ** -11 if fmt == "fp8" else 0.0
+
+    def refs():
+        nt, out = [_np(t) for t in tables], []
+        for t in range(0, B * S, 7):  # every seventh token
+            b, i = divmod(t, S)
+            ids = [x for x in so.window_positions(ctx[b] - S + i, window, sinks)
+                   if nt[x % D][b, (x // D) // bs] >= 0]
+            out.append(so.attend(qf[t], _rows_at(npools, nt, b, ids, D, bs, 1), SCALE, step))
+        return out
+
+    _err()
+    out, lse = capi.dcp_window_mla_decode(q, _i32(ctx, dev), 4150, S, window, sinks, pools, tables, bs, SCALE)
+    assert _err() == 0
+    _check(out[::7], lse[::7], refs(), "whole")
+    tables[0][0, 3] = tables[1][0, 90] = tables[0][0, 129] = -1
+    tables[0][3], tables[1][3] = -1, -1  # a request without any
+    tables[1][2, 64] = -1  # the last block of a row just longer than the list
+    out, lse = capi.dcp_window_mla_decode(q, _i32(ctx, dev), 4150, S, window, sinks, pools, tables, bs, SCALE)
+    assert _err() == capi.DEVERR_BLOCK_TABLE
+    _check(out[::7], lse[::7], refs(), "holes")
+    assert torch.isneginf(lse[3 * S:]).all() and not out[3 * S:].any()
+
+
+@pytest.mark.gpu
 def test_window_wide_enough_is_the_dense_decode(cuda_device):
     """Two kernels, one definition: both within its bounds."""
     dev = cuda_device
