@@ -485,30 +485,40 @@ static_assert(kTileN * Fp8Rows::kRawStride <= (1 << 15) && Fp8Rows::kRowBytes <=
                   kTileN <= (1 << 7),
               "packed piece offsets fit their fields");
 
+// Each piece's place is the same in every tile: its row r in the tile, its
+// source offset in the cache row and its destination offset in the raw
+// stage, packed once as r << 25 | src << 15 | dst (dst < 2^15, src < 2^10).
+// A loader forms its pieces' places before the set-up barrier, while other
+// warps' first loads are on the way.
+template <class F>
+struct Pieces {
+  static constexpr int kCount = kTileN * F::kPieces;
+  static constexpr int kPer = (kCount + kLoaders - 1) / kLoaders;
+  uint32_t pk[kPer];
+  __device__ __forceinline__ void place(int c, int ld) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int p = ld + kLoaders * k;
+      // p / 21 or p / 13, exact for p < 64 * 21 (p < 9 * 96)
+      const int r = int((uint32_t(p) * (F::kFp4 ? 5042u : 3121u)) >> 16);
+      const int j = p - r * F::kPieces;
+      // a piece past the tile (fp4's last round): row 64, never below a row count
+      pk[k] = uint32_t(r) << 25 | uint32_t(F::piece_src(c, j)) << 15 |
+              uint32_t(r * F::kRawStride + 16 * j);
+      if (kCount % kLoaders != 0 && p >= kCount) pk[k] = uint32_t(kTileN) << 25;
+    }
+  }
+};
+
 template <int kMode, class F>
-__device__ void loader_loop(const DecodeArgs& a, Ctl* ctl, uint8_t* sm, int n, int ntiles, int c,
-                            int ld, volatile int* abort) {
+__device__ void loader_loop(const DecodeArgs& a, Ctl* ctl, uint8_t* sm, int n, int ntiles,
+                            const Pieces<F>& pieces, volatile int* abort) {
   const int* list = reinterpret_cast<const int*>(sm + kOffList);
   const uint8_t* list_shard = sm + kOffListShard;
   const uint32_t raw0 = smem_u32(sm + kOffRaw);
-  constexpr int kPieceCount = kTileN * F::kPieces;
-  constexpr int kPiecesPerLoader = (kPieceCount + kLoaders - 1) / kLoaders;
+  constexpr int kPiecesPerLoader = Pieces<F>::kPer;
+  const uint32_t (&pk)[kPiecesPerLoader] = pieces.pk;
   uint4 buf[kPiecesPerLoader];
-  // Each piece's place is the same in every tile: its row r in the tile, its
-  // source offset in the cache row and its destination offset in the raw
-  // stage, packed once as r << 25 | src << 15 | dst (dst < 2^15, src < 2^10).
-  uint32_t pk[kPiecesPerLoader];
-#pragma unroll
-  for (int k = 0; k < kPiecesPerLoader; ++k) {
-    const int p = ld + kLoaders * k;
-    // p / 21 or p / 13, exact for p < 64 * 21 (p < 9 * 96)
-    const int r = int((uint32_t(p) * (F::kFp4 ? 5042u : 3121u)) >> 16);
-    const int j = p - r * F::kPieces;
-    // a piece past the tile (fp4's last round): row 64, never below a row count
-    pk[k] = uint32_t(r) << 25 | uint32_t(F::piece_src(c, j)) << 15 |
-            uint32_t(r * F::kRawStride + 16 * j);
-    if (kPieceCount % kLoaders != 0 && p >= kPieceCount) pk[k] = uint32_t(kTileN) << 25;
-  }
   auto load = [&](int tile) {
     const int base = tile * kTileN;
     const uint32_t rows = uint32_t(min(kTileN, n - base));
@@ -885,7 +895,7 @@ __device__ __forceinline__ void issue_pv(uint32_t tb, uint32_t op, bool accumula
 
 template <int kMode, class F>
 __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt& hr, int64_t t,
-                        int split, uint32_t peer) {
+                        int split, uint32_t peer, const Pieces<F>& pieces) {
   const int C = hr.c;
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -897,6 +907,7 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
 
   if (warp < 4) {
     // ------------------------------------------------ softmax + epilogue
+    cluster_wait();     // the peer's barriers are initialised
     const int h = tid;  // head row == TMEM lane
     const bool live_warp = warp < softmax_warps(a.H);
     const uint32_t xa_bytes = softmax_warps(a.H) * (kXABytes / 4);
@@ -1175,7 +1186,7 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
     convert_loop<F>(ctl, sm, n, ntiles, d & (kTileN - 1), C, d >> 6, lane, abort);
   } else if (warp >= kLoaderWarp0) {
     // ------------------------------------------------ stage cache rows
-    loader_loop<kMode, F>(a, ctl, sm, n, ntiles, C, tid - 32 * kLoaderWarp0, abort);
+    loader_loop<kMode, F>(a, ctl, sm, n, ntiles, pieces, abort);
   } else if (lane == 0) {
     // ------------------------------------------------ MMA issue (one thread)
     // QK(i) needs its operand stage converted and S(i - 1) read by the
@@ -1431,6 +1442,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   // q lands in the (still idle) operand stages while the CTA sets up
   if (tid == 0) issue_q_tma(a, t, hr.c, smem_u32(sm + kOffOp), &ctl->q_tma);
+  Pieces<F> pieces;
+  if (warp >= kLoaderWarp0) pieces.place(hr.c, tid - 32 * kLoaderWarp0);
   // The compacting warps' raw entries (kPer each of the row's split, see the
   // compaction below) are loaded before the set-up barrier, so that their
   // memory round trip overlaps the request id's.
@@ -1597,11 +1610,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // peer barriers initialised before any remote arrive
+  // The peer's barriers are initialised before any remote store: only the
+  // softmax warps, which send them, wait for that before their loop.
+  cluster_arrive();
   tc_fence_after();
 
-  run_cta<kMode, F>(a, sm, ctl, hr, t, split, peer);
+  run_cta<kMode, F>(a, sm, ctl, hr, t, split, peer, pieces);
 
+  if (warp >= 4) {
+    __syncwarp();
+    cluster_wait();
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the peer no longer writes into this CTA's shared memory
