@@ -70,6 +70,10 @@
  *     treated as -1 and a bit is set in the device error word, readable with
  *     smla_get_device_error.  No kernel traps.
  *   - Index tensors are int32, row-major and contiguous.
+ *   - The serving step's calls (the last list above) launch with programmatic
+ *     stream serialisation: their launch overlaps the end of the kernel before
+ *     them on the stream, and they wait for its completion before they touch
+ *     memory.
  */
 #ifndef SMLA_H_
 #define SMLA_H_
@@ -489,7 +493,9 @@ smla_status smla_dcp_lse_merge(const uint16_t* const* outs,
  * smla_sparse_mla_decode_fp4 is smla_sparse_mla_decode and
  * smla_dcp_sparse_mla_decode_fused_fp4 is smla_dcp_sparse_mla_decode_fused
  * with the pools' rows in the 4-bit format: same arguments, results, errors
- * and workspace rules (smla_fp4_decode_workspace_size gives the size).
+ * and workspace rules (smla_fp4_decode_workspace_size gives the size; key
+ * ranges are chosen by the shape, and merged in a second kernel when the grid
+ * does not fill the GPU); UNSUPPORTED for K > 2^30.
  * smla_dcp_filter_convert_index and smla_dcp_lse_merge do not read cache
  * rows and serve either format.  The latent keys are exact in the kernel's
  * fp16 operands.
@@ -524,8 +530,11 @@ smla_status smla_dcp_sparse_mla_decode_fused_fp4(
  *                smla_sparse_mla_decode
  *   the rest     as for smla_dcp_dense_mla_decode; a rank that holds none of
  *                a token's positions returns (0, -inf) for it
+ * With SMLA_CACHE_FP8 the LSE carries the keys' rounding to fp16 (2^-11 a key
+ * value, so a few 10^-6 of it over a thousand keys); 4-bit keys are exact.
  * Errors: as smla_dcp_dense_mla_decode, plus INVALID_ARG for window < 1,
- * sinks < 0 or another format.
+ * sinks < 0 or another format, and UNSUPPORTED for max_ctx > 2^30 or
+ * interleave * D > 2^31 - 1.
  */
 size_t smla_window_decode_workspace_size(int32_t T, int32_t H, int32_t max_ctx, int32_t window,
                                          int32_t sinks, int32_t D, int32_t interleave,

@@ -140,8 +140,12 @@ smla_status smla_sparse_mla_decode(
   return from_cuda(smla::launch_decode(a, static_cast<cudaStream_t>(stream)));
 }
 
+// Entries of a row the serving step's decodes take (their split arithmetic is
+// 32-bit).
+constexpr int32_t kMaxEntries = 1 << 30;
+
 size_t smla_fp4_decode_workspace_size(int32_t T, int32_t H, int32_t K) {
-  if (T < 0 || H < 1 || H > SMLA_MAX_HEADS || K < 1) return 0;
+  if (T < 0 || H < 1 || H > SMLA_MAX_HEADS || K < 1 || K > kMaxEntries) return 0;
   return smla::fp4_decode_workspace_bytes(T, H, K);
 }
 
@@ -154,6 +158,7 @@ smla_status smla_sparse_mla_decode_fp4(
   smla_status st =
       slots_args(q, kv_cache, num_slots, local_slots, T, H, K, sm_scale, out, lse, a);
   if (st != SMLA_OK || T == 0) return st;
+  if (K > kMaxEntries) return SMLA_ERR_UNSUPPORTED;
   st = take_workspace(workspace, workspace_bytes, smla_fp4_decode_workspace_size(T, H, K), a);
   if (st != SMLA_OK) return st;
   return from_cuda(smla::launch_decode_fp4(a, static_cast<cudaStream_t>(stream)));
@@ -251,6 +256,7 @@ smla_status smla_dcp_sparse_mla_decode_fused_fp4(
                  interleave, kv_caches, num_slots, block_tables, bt_row_strides, bt_widths, out,
                  lse, a);
   if (st != SMLA_OK || T == 0) return st;
+  if (K > kMaxEntries) return SMLA_ERR_UNSUPPORTED;
   st = take_workspace(workspace, workspace_bytes, smla_fp4_decode_workspace_size(T, H, K), a);
   if (st != SMLA_OK) return st;
   a.q = q;
@@ -379,22 +385,36 @@ smla_status smla_dcp_dense_mla_decode(
   return from_cuda(smla::launch_decode_dense(a, static_cast<cudaStream_t>(stream)));
 }
 
-// Raw entries per row of the windowed decode: the sinks and the window, or
-// the largest count of them one rank holds, and never more than the context.
+// The most positions of a run of n that the row's raw entries cover: all of
+// them, or what one rank holds of a run that begins with its share.
+static int64_t held_at_most(int32_t n, int32_t D, int32_t interleave, int32_t rank) {
+  if (rank < 0) return n;
+  const int64_t round = int64_t(interleave) * D;
+  const int64_t rest = n % round;
+  return n / round * interleave + (rest < interleave ? rest : interleave);
+}
+
+// Raw entries per row of the windowed decode: the sinks and the window, and
+// never more than the context.
 static int32_t window_entries(int32_t max_ctx, int32_t window, int32_t sinks, int32_t D,
                               int32_t interleave, int32_t rank) {
-  const int64_t all = dense_entries(max_ctx, D, interleave, rank);
+  const int64_t all = held_at_most(max_ctx, D, interleave, rank);
   const int64_t kept =
-      int64_t(dense_entries(window < max_ctx ? window : max_ctx, D, interleave, rank)) +
-      dense_entries(sinks < max_ctx ? sinks : max_ctx, D, interleave, rank);
+      held_at_most(window < max_ctx ? window : max_ctx, D, interleave, rank) +
+      held_at_most(sinks < max_ctx ? sinks : max_ctx, D, interleave, rank);
   return int32_t(kept < all ? kept : all);
+}
+
+// The windowed decode's positions and rounds of I*D positions are 32-bit.
+static bool window_unsupported(int32_t max_ctx, int32_t D, int32_t interleave) {
+  return max_ctx > kMaxEntries || int64_t(interleave) * D > INT32_MAX;
 }
 
 size_t smla_window_decode_workspace_size(int32_t T, int32_t H, int32_t max_ctx, int32_t window,
                                          int32_t sinks, int32_t D, int32_t interleave,
                                          int32_t rank) {
   if (T < 0 || H < 1 || H > SMLA_MAX_HEADS || max_ctx < 1 || window < 1 || sinks < 0 || D < 1 ||
-      interleave < 1 || rank < -1 || rank >= D)
+      interleave < 1 || rank < -1 || rank >= D || window_unsupported(max_ctx, D, interleave))
     return 0;
   return smla::window_decode_workspace_bytes(
       T, H, window_entries(max_ctx, window, sinks, D, interleave, rank));
@@ -414,6 +434,7 @@ smla_status smla_dcp_window_mla_decode(
                                   interleave, kv_caches, num_slots, block_tables, bt_row_strides,
                                   bt_widths, out, lse, a);
   if (st != SMLA_OK || B == 0) return st;
+  if (window_unsupported(max_ctx, D, interleave)) return SMLA_ERR_UNSUPPORTED;
   a.window = window;
   a.sinks = sinks;
   a.K = window_entries(max_ctx, window, sinks, D, interleave, rank);

@@ -1436,6 +1436,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (overlapped<kMode, F>()) {
     griddep_wait();  // set-up so far overlaps the end of the kernel before
     if (kMode == kModeWindow && empty_split()) {
+      tc_fence_before();
+      __syncthreads();  // tensor memory's address has been written
+      tc_fence_after();
       if (warp == kMmaWarp) tmem_dealloc(ctl->tbase, kTmemCols);
       return;
     }

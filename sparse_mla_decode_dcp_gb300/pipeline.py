@@ -130,7 +130,8 @@ class DcpServingStep:
         self._taken: List[torch.Tensor] = []
 
     def _append(self, ctx_lens, q_lens, kv, outs):
-        self._taken = []
+        if self._taken:
+            raise RuntimeError("the last step's blocks are still in the free lists: take_blocks() first")
         for d in range(self.D):
             m = capi.dcp_step_maps(ctx_lens, q_lens, self.free_blocks[d], self.block_tables[d],
                                    kv.shape[0], self.D, d, self.block_size,
@@ -155,6 +156,8 @@ class DcpServingStep:
 
     def take_blocks(self):
         """Drop the blocks the last prefill or run took from the free lists."""
+        if self.stream is not None:
+            self.stream.synchronize()
         for d, taken in enumerate(self._taken):
             self.free_blocks[d] = self.free_blocks[d][int(taken.item()):]
         self._taken = []

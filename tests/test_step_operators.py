@@ -101,7 +101,8 @@ def _fp4(lib, **kw):
     (dict(T=-1), BAD), (dict(K=0), BAD), (dict(H=0), BAD), (dict(H=129), UNSUP), (dict(ns=-1), BAD),
     (dict(scale=0.0), BAD), (dict(scale=float("nan")), BAD), (dict(q=None), BAD),
     (dict(q=FAKE + 8), BAD), (dict(kv=FAKE + 4), BAD), (dict(out=FAKE + 2), BAD),
-    (dict(K=4096), WS), (dict(T=0, q=None, kv=None, slots=None, out=None, lse=None), OK),
+    (dict(K=4096), WS), (dict(K=2 ** 30 + 1), UNSUP),
+    (dict(T=0, q=None, kv=None, slots=None, out=None, lse=None), OK),
 ])
 def test_fp4_decode_argument_checks(lib, kw, status):
     assert _fp4(lib, **kw) == status
@@ -133,7 +134,8 @@ def test_fused_fp4_argument_checks(lib, D, kw, status):
     (2, dict(window=0), BAD), (2, dict(window=-5), BAD), (2, dict(sinks=-1), BAD), (2, dict(fmt=2), BAD),
     (2, dict(rank=2), BAD), (2, dict(rank=-2), BAD), (2, dict(maxc=0), BAD), (2, dict(S=0), BAD),
     (2, dict(B=-1), BAD), (2, dict(H=129), UNSUP), (17, {}, UNSUP), (2, dict(pools=[FAKE, None]), BAD),
-    (2, dict(maxc=65536, window=8192), WS),
+    (2, dict(maxc=65536, window=8192), WS), (2, dict(maxc=2 ** 30 + 1), UNSUP),
+    (4, dict(I=2 ** 30, rank=0), UNSUP), (2, dict(I=2 ** 30 - 1, maxc=65536, window=8192, rank=0), WS),
     (2, dict(rank=0, maxc=65536, window=2 ** 31 - 1, sinks=2 ** 31 - 1, pools=[FAKE, None]), WS),
     (2, dict(B=0), OK),
 ])
@@ -156,6 +158,8 @@ def test_workspace_sizes(lib):
     assert size(8, 128, 65536, 1024, 64, 4) == size(8, 128, 2048, 1024, 64, 4)
     assert size(8, 128, 65536, 2 ** 31 - 1, 2 ** 31 - 1, 4) == size(8, 128, 65536, 65536, 0, 4)
     assert size(8, 128, 65536, 8192, 0, 4, 1, 0) < size(8, 128, 65536, 8192, 0, 4)
+    # a rank with long runs holds no more than the window
+    assert size(8, 128, 65536, 8192, 0, 2, 2 ** 20, 0) == size(8, 128, 65536, 8192, 0, 1)
 
 
 def test_binding_refuses_what_it_cannot_pass():
@@ -532,7 +536,13 @@ def _paged(ctx, D, bs, I, fmt, seed, dev):
             table[b, :n] = perm[at:at + n]
             at += n
         tables.append(_i32(table, dev))
-        pools.append(_random_cache((sum(nb) + 2) * bs, fmt, seed + d, dev))
+        pool = _random_cache((sum(nb) + 2) * bs, fmt, seed + d, dev)
+        held = np.zeros(pool.shape[0], dtype=bool)
+        for b, c in enumerate(ctx):
+            lp = np.arange(so.rank_rows(int(c), D, d, I))
+            held[table[b, lp // bs] * bs + lp % bs] = True
+        pool[torch.from_numpy(~held).to(dev)] = 0xFF  # NaN scales, codes and rope nobody may read
+        pools.append(pool)
     return pools, tables
 
 
@@ -589,7 +599,8 @@ WINDOWS = [(1, 0), (1, 1), (7, 0), (64, 4), (65, 63), (200, 300), (2 ** 31 - 1, 
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
 @pytest.mark.parametrize("window,sinks", WINDOWS)
-@pytest.mark.parametrize("D,I,bs,S,rank", [(1, 1, 16, 1, -1), (3, 1, 8, 2, -1), (2, 4, 3, 3, 1)])
+@pytest.mark.parametrize("D,I,bs,S,rank", [(1, 1, 16, 1, -1), (3, 1, 8, 2, -1), (2, 4, 3, 3, 1),
+                                           (2, 100, 16, 1, 0)])
 def test_window_matches_float64(cuda_device, fmt, window, sinks, D, I, bs, S, rank):
     dev = cuda_device
     ctx = [S, 5 + S, 64, 131, 430]
@@ -761,6 +772,8 @@ def test_serving_step_runs_together(cuda_device, fmt):
 
     _err()
     step.prefill(_i32(ctx, dev), _i32(ctx, dev), bring(ctx))
+    with pytest.raises(RuntimeError):  # the blocks it took are still listed as free
+        step.run(_i32(ctx, dev), torch.zeros((3 * S, 576), dtype=torch.bfloat16, device=dev), _q(3 * S, H, dev))
     step.take_blocks()
     for i in range(3):
         ctx = ctx + S
