@@ -84,6 +84,8 @@ constexpr int kMmaWarp = 8;
 constexpr int kLoaderWarp0 = 9;   // warps 9..11 stage cache rows
 constexpr int kLoaders = 96;
 constexpr int kMaxList = kDecodeMaxList;  // compacted slots one cluster handles
+// a windowed row's entries need no compaction: what shared memory holds
+constexpr int kWindowList = 2096;
 
 // tensor-memory columns (512 allocated)
 constexpr uint32_t kOCol = 0;     // O half: 256 fp32 columns
@@ -109,9 +111,9 @@ constexpr int kOffRaw = kOffOp + kStages * kOpTileBytes;
 constexpr int kOffX = kOffRaw + kRawStages * kRawTileBytes;
 constexpr int kOffList = kOffX + 2 * kXBytes;  // two buffer sets
 constexpr int kBtStageMax = 2 * kXBytes / 4;    // staged block-table entries (fused prologue)
-constexpr int kOffListShard = kOffList + kMaxList * 4;  // fused step: shard of each key
-constexpr int kOffCtl = kOffListShard + kMaxList;
-constexpr int kCtlBytes = 1024;
+constexpr int kOffListShard = kOffList + kWindowList * 4;  // fused step: shard of each key
+constexpr int kOffCtl = kOffListShard + kWindowList;
+constexpr int kCtlBytes = 784;
 constexpr int kSmemBytes = kOffCtl + kCtlBytes + 1024;  // + control block + alignment slack
 
 // Per shard: its staged block-table row's offset in the staging area, the
@@ -1451,7 +1453,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // compaction below) are loaded before the set-up barrier, so that their
   // memory round trip overlaps the request id's.
   constexpr int kListThreads = kThreads - 128;  // every warp but the softmax warps
-  constexpr int kPer = kMaxList / kListThreads;
+  constexpr int kPer =
+      ((kMode == kModeWindow ? kWindowList : kMaxList) + kListThreads - 1) / kListThreads;
   int32_t vs[kPer];
   if (!generated(kMode) && warp >= 4) {
     const int j0 = e_begin + (tid - 128) * kPer;
@@ -1773,9 +1776,9 @@ int decode_splits(int32_t T, int32_t K) {
 // split: 1 row of 512 entries 8 splits 15.8 us (2: 22.8), 1 of 2048 16 splits
 // 18.3 (8: 19.7), 16 of 512 4 splits 19.5 (2: 24.3).  Splits that need a second
 // wave never won (80 rows of 2048: 1 split 117 us, 2 119).  Like decode_splits
-// a function of the shape alone, with at most kMaxList entries per split.
-int model_splits(int32_t T, int32_t K) {
-  const int lo = (K + kMaxList - 1) / kMaxList;
+// a function of the shape alone, with at most `list` entries per split.
+int model_splits(int32_t T, int32_t K, int list) {
+  const int lo = (K + list - 1) / list;
   int best = 1;
   int64_t best_cost = INT64_MAX;
   for (int s = 1; T > 0 && int64_t(T) * s <= kClusterSlots && (s - 1) * kTileN < K; ++s) {
@@ -1875,7 +1878,7 @@ cudaError_t launch_impl(const DecodeArgs& args, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   a.splits = a.single_split          ? 1
-             : overlapped<kMode, F>() ? model_splits(a.T, a.K)
+             : overlapped<kMode, F>() ? model_splits(a.T, a.K, kMode == kModeWindow ? kWindowList : kMaxList)
                                       : decode_splits(a.T, a.K);
   const WsLayout w = ws_layout(a.T, a.H, a.splits);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
