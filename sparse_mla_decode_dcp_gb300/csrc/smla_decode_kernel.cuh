@@ -45,7 +45,7 @@
 //
 // Warp roles (384 threads): warps 0-3 softmax/epilogue (TMEM lanes 0-127,
 // one head row per thread), warps 4-7 dequantise, warp 8 allocates TMEM and
-// issues every MMA (one thread: QK^T of a tile, then PV of the tile two
+// issues every MMA (one elected lane: QK^T of a tile, then PV of the tile two
 // before it, once the softmax has stored that tile's P), warps 9-11 gather.
 // Every wait is bounded; a wait that runs out sets SMLA_DEVERR_TIMEOUT and
 // the CTA unwinds.
@@ -866,10 +866,9 @@ __device__ bool q_to_tmem(uint32_t tb, int warp, int h, bool live, uint32_t src)
   return over != 0;
 }
 
-// MMA issue, fully unrolled: one thread issues a tcgen05.mma every few tens
-// of cycles at best, and computing each descriptor in the loop about doubles
-// that, which for the N = 64 QK^T steps is slower than the tensor core runs
-// them.  A descriptor's start address field is the byte address / 16, so
+// MMA issue, fully unrolled: computing each descriptor in a loop about
+// doubles the time an issue takes, which for the N = 64 QK^T steps is slower
+// than the tensor core runs them (44 clocks each).  A descriptor's start address field is the byte address / 16, so
 // stepping through a stage adds a constant to the stage's base descriptor
 // (shared-memory addresses stay below 256 KB: no carry leaves the field).
 __device__ __forceinline__ void issue_qk(uint32_t tb, uint32_t op) {
@@ -1189,43 +1188,57 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
   } else if (warp >= kLoaderWarp0) {
     // ------------------------------------------------ stage cache rows
     loader_loop<kMode, F>(a, ctl, sm, n, ntiles, pieces, abort);
-  } else if (lane == 0) {
+  } else {
     // ------------------------------------------------ MMA issue (one thread)
     // QK(i) needs its operand stage converted and S(i - 1) read by the
-    // softmax, PV(i) the softmax's P(i); the thread sleeps on each barrier
+    // softmax, PV(i) the softmax's P(i); the warp sleeps on each barrier
     // until the hardware wakes it at the phase change.  Issuing PV here
-    // rather than from a softmax thread keeps the MMA issue (~57 cycles an
-    // instruction) and a per-tile barrier of the four softmax warps off the
-    // softmax's chain.
-    const uint32_t op0 = smem_u32(sm + kOffOp);
+    // rather than from a softmax thread keeps the MMA issue and a per-tile
+    // barrier of the four softmax warps off the softmax's chain.
+    // The whole warp runs the loop on values that are the same in every lane
+    // and one elected lane issues: descriptors then stay in uniform registers,
+    // and the 18 instructions of QK^T take ~400 clocks to issue (1200 when one
+    // lane ran the loop alone; dense decode 673 -> 645 us, windows of 4,112
+    // entries 153 -> 136).
+    const uint32_t op0 = __shfl_sync(0xffffffffu, smem_u32(sm + kOffOp), 0);
+    const uint32_t tbu = __shfl_sync(0xffffffffu, tb, 0);
+    const int nt = __shfl_sync(0xffffffffu, ntiles, 0);
+    const bool leader = elect_one();
     bool ok = wait_bar(&ctl->q_ready, 0, abort, kWsQReady);
     // QK(j), then PV(j - 2): the softmax stores P(j - 2) after it has read
     // S(j - 1), which frees S for QK(j)
 #pragma unroll 1
-    for (int j = 0; j < ntiles + 2 && ok; ++j) {
-      if (j < ntiles) {
+    for (int j = 0; j < nt + 2; ++j) {
+      if (j < nt) {
         ok = wait_bar(&ctl->full[j % kStages], (j / kStages) & 1, abort, kWsFull) &&
              (j == 0 || wait_bar(&ctl->s_free, (j - 1) & 1, abort, kWsSFree));
-        if (!ok) break;
+        if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        issue_qk(tb, op0 + (j % kStages) * kOpTileBytes);
-        mma_commit(&ctl->s_full);
+        if (leader) {
+          issue_qk(tbu, op0 + (j % kStages) * kOpTileBytes);
+          mma_commit(&ctl->s_full);
+        }
+        __syncwarp();
       }
       const int i = j - 2;
       if (i >= 0) {
         ok = wait_bar(&ctl->p_full, i & 1, abort, kWsPFull);
-        if (!ok) break;
+        if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        issue_pv(tb, op0 + (i % kStages) * kOpTileBytes, i > 0);
-        mma_commit(&ctl->pv_done);
-        mma_commit(&ctl->freed[i % kStages]);
+        if (leader) {
+          issue_pv(tbu, op0 + (i % kStages) * kOpTileBytes, i > 0);
+          mma_commit(&ctl->pv_done);
+          mma_commit(&ctl->freed[i % kStages]);
+        }
+        __syncwarp();
       }
     }
     // drain: every MMA issued above has completed before TMEM is released
     // (waited on even after an abort, with its own bound).  A CTA whose row
     // has no valid slot issued no MMA and has nothing to drain.
     if (ntiles > 0) {
-      mma_commit(&ctl->end);
+      if (leader) mma_commit(&ctl->end);
+      __syncwarp();
       int no_abort = 0;
       wait_bar(&ctl->end, 0, &no_abort, kWsDrain);
     }
