@@ -19,9 +19,10 @@
 //     QK^T contraction is split by key dimension the same way: CTA c
 //     contracts latent dims [256c, 256c + 256) (its value half) and rope dims
 //     [32c, 32c + 32), 288 key dims each, so every cache byte is fetched by
-//     one CTA.  The two fp32 partial score tiles are exchanged through
-//     distributed shared memory each tile, so no FLOP is recomputed.  Both
-//     CTAs then run the identical online softmax.
+//     one CTA.  The fp32 partial scores are exchanged through distributed
+//     shared memory each tile: each CTA finishes half of the tile's keys and
+//     sends the other its P of them, so no FLOP and no exponential is
+//     computed twice.
 //   * Q (this CTA's key-dim half) and P live in tensor memory as the A
 //     operand; K/V tiles are the B operand in shared memory (128-byte
 //     swizzle): one buffer serves as K (K-major) for QK^T and as V
@@ -34,19 +35,20 @@
 //     row's code x scale has at most 6 significant bits and lies in [2^-10,
 //     2688] (or is 0), so its keys are exact in fp16.
 //   * Valid slots are compacted in order in the prologue (-1 never costs a
-//     load or an MMA).  Each gather thread loads its fixed share of every key
-//     row straight into registers one tile ahead and converts it from there;
-//     three operand tiles are in flight.
+//     load or an MMA).  Loader threads hold a tile's rows in registers while
+//     the tile before it is read out of a raw stage in shared memory; four
+//     operand tiles are in flight.
 //   * The partial score tiles travel as asynchronous remote stores counted on
 //     the receiving CTA's mbarrier (st.async + expect_tx).
 //   * Softmax in the log2 domain with a lazily moved reference maximum: the
 //     O accumulator in TMEM is rescaled only when the row maximum grows by
 //     more than 2^8.
 //
-// Warp roles (384 threads): warps 0-3 softmax/epilogue (TMEM lanes 0-127,
-// one head row per thread), warps 4-7 dequantise, warp 8 allocates TMEM and
-// issues every MMA (one elected lane: QK^T of a tile, then PV of the tile two
-// before it, once the softmax has stored that tile's P), warps 9-11 gather.
+// Warp roles: 4 (fp8 rows) or 8 (fp4) warps of softmax and epilogue (TMEM
+// lanes 0-127, one or two threads a head row), 4 that dequantise, one that
+// allocates TMEM and issues every MMA (one elected lane: QK^T of a tile, then
+// PV of the tile two before it, once the softmax has stored that tile's P)
+// and 3 that load cache rows.
 // Every wait is bounded; a wait that runs out sets SMLA_DEVERR_TIMEOUT and
 // the CTA unwinds.
 #pragma once
@@ -77,11 +79,8 @@ enum : int { kModeSlots = 0, kModeTopk = 1, kModeDense = 2, kModeWindow = 3 };
 constexpr bool generated(int mode) { return mode == kModeDense || mode == kModeWindow; }
 
 constexpr int kTileN = 64;        // keys per tile (MMA N of QK^T, K of PV)
-constexpr int kThreads = 384;     // 12 warps
 constexpr int kStages = 4;        // fp16 operand tiles in flight
 constexpr int kRawStages = 1;     // raw cache-row tiles in shared memory (one more in registers)
-constexpr int kMmaWarp = 8;
-constexpr int kLoaderWarp0 = 9;   // warps 9..11 stage cache rows
 constexpr int kLoaders = 96;
 constexpr int kMaxList = kDecodeMaxList;  // compacted slots one cluster handles
 // a windowed row's entries need no compaction: what shared memory holds
@@ -92,7 +91,20 @@ constexpr uint32_t kOCol = 0;     // O half: 256 fp32 columns
 constexpr uint32_t kSCol = 256;   // S tile: 64 fp32 columns
 constexpr uint32_t kPCol = 320;   // P tile: 64 fp16 = 32 columns
 constexpr uint32_t kQCol = 352;   // Q part: 288 fp16 = 144 columns
+constexpr uint32_t kRefCol = 496; // references of a row's two threads, 2 buffers
 constexpr uint32_t kTmemCols = 512;
+
+// N consecutive columns of a warp's lanes.
+template <int N>
+__device__ __forceinline__ void tmem_ldn(uint32_t addr, uint32_t* r) {
+  if constexpr (N == 32) tmem_ld32(addr, r);
+  else tmem_ld16(addr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_stn(uint32_t addr, const uint32_t* r) {
+  if constexpr (N == 16) tmem_st16(addr, r);
+  else tmem_st8(addr, r);
+}
 
 // shared-memory layout (offsets from a 1024-byte aligned base)
 constexpr int kKBlockBytes = kTileN * 128;          // 64 keys x 64 fp16, 128-byte swizzle
@@ -125,7 +137,7 @@ struct __align__(16) ShardMeta {
 
 struct Ctl {
   uint64_t q_tma, q_ready, full[kStages], freed[kStages], raw_full[kRawStages], raw_empty[kRawStages],
-      s_full, s_free, pv_done, p_full, xa[2], xb[2], end;
+      s_full, s_free, pv_done, p_full, xa[2], xb[2], sums, end;
   uint32_t tbase;
   int n_list;
   int abort;
@@ -294,6 +306,7 @@ __device__ __forceinline__ HalfRt half_of(uint32_t c) {
 // keys times this; the softmax's scale and O's factor take it out again.
 struct Fp8Rows {
   static constexpr bool kFp4 = false;
+  static constexpr int kRowThreads = 1;
   static constexpr float kKeyScale = 1.f;
   static constexpr int kRowBytes = SMLA_ROW_BYTES;
   // pieces 0..15: codes [256c, 256c + 256) -> raw [0, 256); piece 16: the
@@ -311,6 +324,7 @@ struct Fp8Rows {
 
 struct Fp4Rows {
   static constexpr bool kFp4 = true;
+  static constexpr int kRowThreads = 2;
   static constexpr float kKeyScale = 1.f / 128.f;
   static constexpr int kRowBytes = SMLA_FP4_ROW_BYTES;
   // pieces 0..7: codes [128c, 128c + 128) -> raw [0, 128); piece 8: sixteen
@@ -324,6 +338,24 @@ struct Fp4Rows {
   static __device__ __forceinline__ int piece_src(int c, int j) {
     return j < 8 ? 128 * c + 16 * j : j == 8 ? 256 + 16 * c : 288 + 64 * c + 16 * (j - 9);
   }
+};
+
+// The warps of a CTA: 4 or 8 softmax warps (kRowThreads threads a head row,
+// each finishing kCols of a tile's key columns), 4 converter warps, the MMA
+// warp, 3 loader warps.  Two threads a row shorten the softmax's chain, which
+// bounds the fp4 kernels (sparse step of 4 pools, 72 rows of 2048 entries,
+// H = 128: 58.2 -> 54.3 us; 8 rows 9.5 -> 8.4), but leave the loaders 128
+// instead of 168 registers, and fp8's rows, half again as long, then arrive
+// late (fused step 62.8 -> 66.9 us, dense decode 649 -> 690): one thread there.
+template <class F>
+struct Roles {
+  static constexpr int kSoftmaxWarps = 4 * F::kRowThreads;
+  static constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+  static constexpr int kConvWarp0 = kSoftmaxWarps;
+  static constexpr int kMmaWarp = kConvWarp0 + 4;
+  static constexpr int kLoaderWarp0 = kMmaWarp + 1;
+  static constexpr int kThreads = 32 * (kLoaderWarp0 + 3);
+  static constexpr int kCols = kTileN / 2 / F::kRowThreads;
 };
 
 // The fp4 operand tile holds each run of 8 latent dims in the order 0 4 1 5 2
@@ -583,60 +615,166 @@ __device__ void convert_loop(Ctl* ctl, uint8_t* sm, int n, int ntiles, int key, 
   if (out_of_range) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
 }
 
-// Split-K epilogue (softmax warps): write this split's unnormalised O half,
-// its log2-domain reference maximum and its sum (-inf and 0 when it holds
-// no partial).  With the in-kernel combine the split then counts itself in:
-// the CTA whose split arrives last for its row and value half learns so in
+// Rows of up to kDirectTiles tiles (fp4): the converters load them themselves,
+// straight into registers and a tile ahead, which takes the trip through the
+// raw stage off a short row's chain.  Measured for 1 to 3 tiles: 0.1 to 0.3
+// us sooner (8 rows of 128 entries: 8.5 -> 8.3 us); from 4 tiles on the loads
+// hold the converters up (76 rows of 1024 entries: 32.6 -> 41.5 us).
+// Threads 2k and 2k + 1 own key k's pieces
+// 2i + part: a load instruction reads whole 32-byte sectors, and the eight
+// lanes of four keys store to eight different bank groups.
+constexpr int kDirectTiles = 3;
+
+struct Fp4Regs {
+  uint4 code[4], rope[2], scale;
+};
+
+__device__ __forceinline__ void load_fp4(const uint8_t* row, int c, int part, Fp4Regs& r) {
+  if (row != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.code[i] = ldg_stream(row + 128 * c + 32 * i + 16 * part);
+    r.scale = ldg_stream(row + 256 + 16 * c);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r.rope[i] = ldg_stream(row + 288 + 64 * c + 32 * i + 16 * part);
+  } else {
+    const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.code[i] = z;
+    r.scale = r.rope[0] = r.rope[1] = z;
+  }
+}
+
+__device__ __forceinline__ bool convert_fp4(const Fp4Regs& r, uint32_t op, int key, int part) {
+  uint32_t nan = 0;
+  const uint32_t sw[4] = {r.scale.x, r.scale.y, r.scale.z, r.scale.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // piece 2i + part: dims 32 (2i + part) .., two scale groups
+    const uint32_t s2 = (sw[i] >> (16 * part)) & 0xffffu;
+    const __half2 ss = __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(s2), __NV_E4M3));
+    const uint32_t sb = h2_bits(ss);
+    nan |= (sb & 0x7fffu) > 0x7c00u || (sb & 0x7fff0000u) > 0x7c000000u;
+    const __half2 up = __float2half2_rn(128.f);
+    const __half2 s0 = __hmul2(__low2half2(ss), up), s1 = __hmul2(__high2half2(ss), up);
+    const uint32_t blk = op + i * kKBlockBytes;
+    sts128(blk + sw128_offset(key, 4 * part), e2m1x8_scaled(r.code[i].x, s0));
+    sts128(blk + sw128_offset(key, 4 * part + 1), e2m1x8_scaled(r.code[i].y, s0));
+    sts128(blk + sw128_offset(key, 4 * part + 2), e2m1x8_scaled(r.code[i].z, s1));
+    sts128(blk + sw128_offset(key, 4 * part + 3), e2m1x8_scaled(r.code[i].w, s1));
+  }
+  uint32_t over = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    over |= bf16x8_over_fp16(r.rope[i]);
+    sts128(op + kRopeBlock + sw64_offset(key, 2 * i + part), bf16x8_to_f16x8(r.rope[i], Fp4Rows::kKeyScale));
+  }
+  return over != 0 || nan != 0;
+}
+
+template <int kMode>
+__device__ void convert_direct(const DecodeArgs& a, Ctl* ctl, uint8_t* sm, int n, int ntiles, int c,
+                               int d, volatile int* abort) {
+  const int* list = reinterpret_cast<const int*>(sm + kOffList);
+  const uint8_t* list_shard = sm + kOffListShard;
+  const uint32_t op0 = smem_u32(sm + kOffOp);
+  const int key = d >> 1, part = d & 1;
+  auto row_of = [&](int tile) -> const uint8_t* {
+    const int idx = tile * kTileN + key;
+    return idx < n ? row_ptr<kMode, Fp4Rows>(a, ctl, list, list_shard, idx) : nullptr;
+  };
+  Fp4Regs cur, next;
+  if (ntiles > 0) load_fp4(row_of(0), c, part, cur);
+  bool bad = false;
+#pragma unroll 1
+  for (int i = 0; i < ntiles; ++i) {
+    if (i + 1 < ntiles) load_fp4(row_of(i + 1), c, part, next);
+    if (i >= kStages &&
+        !wait_bar(&ctl->freed[i % kStages], ((i - kStages) / kStages) & 1, abort, kWsFreed))
+      break;
+    bad |= convert_fp4(cur, op0 + (i % kStages) * kOpTileBytes, key, part);
+    fence_async_shared();
+    mbar_arrive(&ctl->full[i % kStages]);
+    cur = next;
+  }
+  if (bad) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
+}
+
+// The softmax warps' epilogue: each thread of a head row stores its share of
+// the columns of the CTA's O half (thread g of two: [128 g, 128 g + 128)), O / l as bf16 into the output or, with
+// split-K, as this split's partial in fp16 (its own softmax average, so
+// within the range of the fp16 value rows; 2^-11 relative), whose log2-domain
+// reference maximum and sum (-inf and 0 when it holds no partial) go beside
+// it.  With the in-kernel combine the split then counts itself in: the CTA
+// whose split arrives last for its row and value half learns so in
 // `ctl->is_last` and combines the row once all its warps are free (see
 // combine_splits).  A split whose CTA gave up on a wait (`ok` false,
 // SMLA_DEVERR_TIMEOUT set) still arrives, contributing nothing, so the
 // counter always completes and the workspace stays valid for the next call.
 template <class F>
-__device__ void split_epilogue(const DecodeArgs& a, Ctl* ctl, int C, int64_t t, int split, int ntiles,
-                               float m_ref, float l, uint32_t tb, int warp, int h, bool ok) {
-  const int S = a.splits;
+__device__ __forceinline__ void row_epilogue(const DecodeArgs& a, Ctl* ctl, int C, int64_t t,
+                                             int split, int ntiles, float m_ref, float l,
+                                             uint32_t tb, int quad, int g, int h, bool live_warp,
+                                             bool ok) {
+  constexpr int kShare = 256 / F::kRowThreads;
   const bool live = h < a.H;
-  const int64_t row = (t * S + split) * a.H + (live ? h : 0);
-  // the split's own normalised output O / l, in fp16: an average of the
-  // fp16 value rows, so within their range, rounded once (2^-11 relative)
-  uint4* wo = reinterpret_cast<uint4*>(a.ws_o + row * SMLA_V_DIM + C * 256);
-  const bool has = ok && ntiles > 0;
+  const bool partial = a.splits > 1;
+  const bool has = ok && ntiles > 0 && live_warp;
+  if (partial) {
+    float* ml = a.ws_ml + ((t * a.splits + split) * 2 + C) * 2 * a.H;
+    if (live && g == 0) {
+      ml[h] = has ? m_ref : -INFINITY;
+      ml[a.H + h] = has ? l : 0.f;
+    }
+  } else if (ok && live && C == 0 && g == 0) {
+    a.lse[t * a.H + h] = (ntiles == 0) ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+  }
+  const int64_t row = (partial ? t * a.splits + split : t) * a.H + (live ? h : 0);
+  uint4* dst = reinterpret_cast<uint4*>((partial ? a.ws_o : a.out) + row * SMLA_V_DIM + C * 256 + g * kShare);
   if (has) {
-    const float inv = l > 0.f ? 1.f / (l * F::kKeyScale) : 0.f;
+    // tcgen05.ld is warp-collective: every lane loads, only live heads store
+    const float inv = partial && !(l > 0.f) ? 0.f : 1.f / (l * F::kKeyScale);
+    // 32-byte stores fill whole sectors (`out` itself may be 16-byte aligned)
+    const bool whole = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
 #pragma unroll 1
-    for (int cc = 0; cc < 8; ++cc) {
-      uint32_t r[32];
-      tmem_ld32(tmem_addr(tb, 32 * warp, kOCol + 32 * cc), r);
+    for (int cc = 0; cc < kShare / 32; ++cc) {
+      uint32_t r[32], o[16];
+      tmem_ld32(tmem_addr(tb, 32 * quad, kOCol + kShare * g + 32 * cc), r);
       tmem_ld_wait();
-      if (live) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            w[q] = h2_bits(
-                __floats2half2_rn(__uint_as_float(r[o_col<F>(8 * k + 2 * q)]) * inv,
-                                  __uint_as_float(r[o_col<F>(8 * k + 2 * q + 1)]) * inv));
-          wo[cc * 4 + k] = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int j = 0; j < 16; ++j) {
+        const float x0 = __uint_as_float(r[o_col<F>(2 * j)]) * inv;
+        const float x1 = __uint_as_float(r[o_col<F>(2 * j + 1)]) * inv;
+        if (partial) {
+          o[j] = h2_bits(__floats2half2_rn(x0, x1));
+        } else {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(x0, x1);
+          o[j] = *reinterpret_cast<const uint32_t*>(&v);
         }
       }
+      if (live && whole) {
+        stg256(dst + cc * 4, o);
+        stg256(dst + cc * 4 + 2, o + 8);
+      } else if (live) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          dst[cc * 4 + k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      }
     }
+  } else if (!partial && ok && ntiles == 0 && live) {
+#pragma unroll 1
+    for (int k = 0; k < kShare / 8; ++k) dst[k] = make_uint4(0, 0, 0, 0);
   }
-  float* ml = a.ws_ml + ((t * S + split) * 2 + C) * 2 * a.H;
-  if (live) {
-    ml[h] = has ? m_ref : -INFINITY;
-    ml[a.H + h] = has ? l : 0.f;
-  }
+  if (!partial) return;
   if (!a.combine_in_kernel) {  // split_combine_kernel merges after this grid
-    if (h == 0) ctl->is_last = 0;
+    if (h == 0 && g == 0) ctl->is_last = 0;
     return;
   }
   __threadfence();
-  named_bar_sync(2, 128);
-  if (h == 0) ctl->is_last = (atomicAdd(a.ws_tick + t * 2 + C, 1) == S - 1);
+  named_bar_sync(2, Roles<F>::kSoftmaxThreads);
+  if (h == 0 && g == 0) ctl->is_last = (atomicAdd(a.ws_tick + t * 2 + C, 1) == a.splits - 1);
 }
 
-// Split-K combine of one row's value half, run by all 384 threads of the CTA
+// Split-K combine of one row's value half, run by all threads of the CTA
 // whose split arrived last, after the roles have finished (TMEM released,
 // the peer no longer writing into this CTA's shared memory).  With m_s and
 // l_s the splits' log2-domain maxima and sums, M = max m_s over the splits
@@ -649,16 +787,18 @@ __device__ void split_epilogue(const DecodeArgs& a, Ctl* ctl, int C, int64_t t, 
 // non-empty splits are listed once, from head 0's sums.  Each thread owns
 // fixed float4 columns of the output (a warp covers 512 contiguous bytes of
 // one head row) and accumulates them over the listed splits with independent
-// loads, 11 columns per pass, two passes; the per-(split, head) weights sit
+// loads, 11 or 8 columns per pass, two passes; the per-(split, head) weights sit
 // in the operand stages, per head M and 1 / L beside the exchange buffers.
 // Splits are taken kCombChunk at a time.  The sums run in split order, as
 // the per-head M and L do.
-constexpr int kCombItems = 11;                                      // float4 columns per pass
 constexpr int kCombChunk = (kStages * kOpTileBytes) / (128 * 4);  // splits whose weights fit
-static_assert(2 * kCombItems * kThreads >= 128 * (SMLA_V_DIM / 2) / 4, "two passes cover a value half");
 static_assert(kCombChunk * 4 + 1024 + 16 <= 2 * kXBytes, "split list and head stats fit");
 
+template <class F>
 __device__ void combine_splits(const DecodeArgs& a, uint8_t* sm, int C, int64_t t) {
+  constexpr int kThreads = Roles<F>::kThreads;
+  constexpr int kCombItems = (4096 + kThreads - 1) / kThreads;  // float4 columns per pass
+  static_assert(2 * kCombItems * kThreads >= 128 * (SMLA_V_DIM / 2) / 4, "two passes cover a value half");
   const int S = a.splits;
   const int H = a.H;
   const int tid = threadIdx.x;
@@ -841,15 +981,16 @@ __device__ __forceinline__ void issue_q_tma(const DecodeArgs& a, int64_t t, int 
 // Convert head row h of the staged q into tensor memory as fp16 pairs (the
 // A operand of QK^T), 64 dims per group of 32 columns; reads follow the
 // boxes' swizzles, so 8 consecutive rows hit 8 different bank groups.
+// (thread g of two takes groups 3 g ..).
 // Returns true when a q value of the row does not fit fp16 (the operand
 // precision of QK^T).
 template <class F>
-__device__ bool q_to_tmem(uint32_t tb, int warp, int h, bool live, uint32_t src) {
-  const uint32_t base = tmem_addr(tb, 32 * warp, kQCol);
+__device__ bool q_to_tmem(uint32_t tb, int quad, int g, int h, bool live, uint32_t src) {
+  const uint32_t base = tmem_addr(tb, 32 * quad, kQCol);
   uint32_t over = 0;
 #pragma unroll 1
-  for (int grp = 0; grp < 5; ++grp) {
-    uint4 g[8];
+  for (int grp = 3 * g; grp < (g || F::kRowThreads == 1 ? 5 : 3); ++grp) {
+    uint4 raw[8];
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
       uint32_t addr;
@@ -857,10 +998,10 @@ __device__ bool q_to_tmem(uint32_t tb, int warp, int h, bool live, uint32_t src)
         addr = src + grp * kQLatBox + sw128_offset(h, v);
       else
         addr = src + 4 * kQLatBox + sw64_offset(h, v & 3);
-      g[v] = (live && (grp < 4 || v < 4)) ? lds128(addr) : make_uint4(0, 0, 0, 0);
-      over |= bf16x8_over_fp16(g[v]);
+      raw[v] = (live && (grp < 4 || v < 4)) ? lds128(addr) : make_uint4(0, 0, 0, 0);
+      over |= bf16x8_over_fp16(raw[v]);
     }
-    q_store_group<F>(g, base + 32 * grp, grp < 4);
+    q_store_group<F>(raw, base + 32 * grp, grp < 4);
   }
   tmem_st_wait();
   return over != 0;
@@ -904,117 +1045,118 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
   volatile int* abort = &ctl->abort;
   const int n = ctl->n_list;
   const int ntiles = (n + kTileN - 1) / kTileN;
+  using R = Roles<F>;
   const uint32_t tb = ctl->tbase;
 
-  if (warp < 4) {
+  if (warp < R::kSoftmaxWarps) {
     // ------------------------------------------------ softmax + epilogue
-    cluster_wait();     // the peer's barriers are initialised
-    const int h = tid;  // head row == TMEM lane
-    const bool live_warp = warp < softmax_warps(a.H);
+    cluster_wait();  // the peer's barriers are initialised
+    constexpr int G = F::kRowThreads;
+    constexpr int kCols = R::kCols;
+    const int h = tid & 127;      // head row == TMEM lane
+    const int quad = warp & 3;    // the warp's 32 lanes of TMEM
+    const int g = G == 1 ? 0 : warp >> 2;  // which of the row's threads
+    const bool live_warp = quad < softmax_warps(a.H);
     const uint32_t xa_bytes = softmax_warps(a.H) * (kXABytes / 4);
     const uint32_t xb_bytes = softmax_warps(a.H) * (kXBBytes / 4);
+    const uint32_t lanes = tmem_addr(tb, 32 * quad, 0);
     const float scale_log2 = a.sm_scale * kLog2e / F::kKeyScale;
     float m_ref = -INFINITY;  // log2-domain reference maximum
-    float l = 0.f;
+    float l = 0.f;            // the sum (two threads a row: this one's columns' share)
     // Key-column split of the softmax: CTA c finishes the scores of keys
     // [32c, 32c + 32) of each tile (its own partial plus the peer's, XA),
-    // computes their P against a reference maximum, and sends that P, the
-    // reference and the partial sum to the peer (XB); P of all 64 keys then
-    // sits in both CTAs.  Both sides move the shared reference R to the same
-    // max(own reference, peer reference), so O, l and P stay consistent.
+    // each of the row's G threads kCols of them, computes their P against a
+    // reference maximum, and sends that P and the reference (XB, to the row's
+    // thread g of the peer); P of all 64 keys then sits in both CTAs.  With
+    // one thread a row the partial sum goes along and both CTAs add it up;
+    // with two, each leaves its reference in tensor memory for the other, and
+    // the sums meet once, after the last tile.  All of a row's threads move
+    // the shared reference R to the same largest of theirs, so O, l and P
+    // stay consistent.
     // Buffers alternate by tile parity: the peer writes tile i into buffer
     // set i % 2 only after it has received this CTA's tile-i partial scores,
     // which this CTA sent after it had read tile i - 2 out of that set.
-    const int oc0 = 32 * C;  // this CTA's key columns (the peer's: 32 (1 - C) ..)
-    uint8_t* xbase = sm + kOffX;
-    const uint32_t peer_x = map_to_cta(smem_u32(xbase), peer);
+    const int own0 = 32 * C + kCols * g, peer0 = 32 * (1 - C) + kCols * g;  // key columns
+    const uint32_t x_l = smem_u32(sm + kOffX);
+    const uint32_t peer_x = map_to_cta(x_l, peer);
     const uint32_t peer_xa0 = map_to_cta(smem_u32(&ctl->xa[0]), peer);
     const uint32_t peer_xa1 = map_to_cta(smem_u32(&ctl->xa[1]), peer);
     const uint32_t peer_xb0 = map_to_cta(smem_u32(&ctl->xb[0]), peer);
     const uint32_t peer_xb1 = map_to_cta(smem_u32(&ctl->xb[1]), peer);
-    if (h == 0) {
+    if (tid == 0 && ntiles > 0) {
       for (int b = 0; b < 2 && b < ntiles; ++b) {
         mbar_arrive_expect_tx(&ctl->xa[b], xa_bytes);
         mbar_arrive_expect_tx(&ctl->xb[b], xb_bytes);
       }
+      if (G == 2) mbar_arrive_expect_tx(&ctl->sums, softmax_warps(a.H) * 512);
     }
     // The loop is software-pipelined across tiles: while the P of tile i is
     // in flight between the CTAs, the scores of tile i + 1 are read and the
     // peer's half of them sent, so the two exchanges of consecutive tiles
     // overlap.
-    float sown[32];  // this CTA's partial scores of its own columns, next tile
+    float sown[kCols];  // this thread's partial scores of its own columns, next tile
     // Read tile t's partial scores (QK^T of tile t done), release S for the
-    // next QK^T, send the peer's columns, keep this CTA's.
+    // next QK^T, send the peer's columns, keep the own.
     auto start_tile = [&](int t) -> bool {
       if (!__all_sync(0xffffffffu, wait_bar(&ctl->s_full, t & 1, abort, kWsSFull))) return false;
       tc_fence_after();
-      float s[64];
-      {
-        uint32_t r[32];
-        tmem_ld32(tmem_addr(tb, 32 * warp, kSCol), r);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(r[j]);
-        tmem_ld32(tmem_addr(tb, 32 * warp, kSCol + 32), r);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) s[32 + j] = __uint_as_float(r[j]);
-      }
+      uint32_t r[kCols], o[kCols];
+      tmem_ldn<kCols>(lanes + kSCol + peer0, r);
+      tmem_ldn<kCols>(lanes + kSCol + own0, o);
+      tmem_ld_wait();
       tc_fence_before();
       mbar_arrive(&ctl->s_free);
       const int b = t & 1;
       const uint32_t xa_p = peer_x + b * kXBytes;
 #pragma unroll
-      for (int j4 = 0; j4 < 8; ++j4) {
-        // columns 32 (1 - C) + 4 j4 ..: a select between two static indices
-        const int lo = 4 * j4, hi = 32 + 4 * j4;
-        st_async_v4(xa_p + (j4 * 128 + h) * 16, C ? s[lo] : s[hi], C ? s[lo + 1] : s[hi + 1],
-                    C ? s[lo + 2] : s[hi + 2], C ? s[lo + 3] : s[hi + 3], b ? peer_xa1 : peer_xa0);
-      }
+      for (int j4 = 0; j4 < kCols / 4; ++j4)
+        st_async_v4(xa_p + ((kCols / 4 * g + j4) * 128 + h) * 16, __uint_as_float(r[4 * j4]),
+                    __uint_as_float(r[4 * j4 + 1]), __uint_as_float(r[4 * j4 + 2]),
+                    __uint_as_float(r[4 * j4 + 3]), b ? peer_xa1 : peer_xa0);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) sown[j] = C ? s[32 + j] : s[j];
+      for (int j = 0; j < kCols; ++j) sown[j] = __uint_as_float(o[j]);
       return true;
     };
     // A warp whose wait gave up leaves the loop (at give_up below); the
     // others' waits give up too, since every wait is an mbarrier wait that
-    // sees the CTA's abort flag.  The four warps enter the loop on one
+    // sees the CTA's abort flag.  The softmax warps enter the loop on one
     // reduced decision and meet again only at the epilogue's barrier.
     bool ok = ntiles == 0 || !live_warp || start_tile(0);
-    ok = !named_bar_or(5, 128, !ok);
+    ok = !named_bar_or(5, R::kSoftmaxThreads, !ok);
     int i = 0;
     for (; i < ntiles && ok && live_warp; ++i) {
       const int b = i & 1;
-      const uint32_t xa_l = smem_u32(xbase) + b * kXBytes;  // this CTA's buffer set b
-      const uint32_t xa_p = peer_x + b * kXBytes;           // the peer's
-      // 1) full scores of this CTA's columns of tile i
+      const uint32_t xa_l = x_l + b * kXBytes;     // this CTA's buffer set b
+      const uint32_t xa_p = peer_x + b * kXBytes;  // the peer's
+      // 1) full scores of this thread's columns of tile i
       ok = __all_sync(0xffffffffu, wait_bar_cluster(&ctl->xa[b], (i >> 1) & 1, abort, kWsExchange));
       if (!ok) goto give_up;
-      float f[32];
+      float f[kCols];
 #pragma unroll
-      for (int j4 = 0; j4 < 8; ++j4) {
-        const float4 v = ld_shared_f4(xa_l + (j4 * 128 + h) * 16);
+      for (int j4 = 0; j4 < kCols / 4; ++j4) {
+        const float4 v = ld_shared_f4(xa_l + ((kCols / 4 * g + j4) * 128 + h) * 16);
         f[4 * j4] = sown[4 * j4] + v.x;
         f[4 * j4 + 1] = sown[4 * j4 + 1] + v.y;
         f[4 * j4 + 2] = sown[4 * j4 + 2] + v.z;
         f[4 * j4 + 3] = sown[4 * j4 + 3] + v.w;
       }
-      if (h == 0 && i + 2 < ntiles) mbar_arrive_expect_tx(&ctl->xa[b], xa_bytes);
-      const int valid = min(kTileN, n - i * kTileN) - oc0;  // valid columns of this CTA's 32
-      if (valid < 32) {
+      if (tid == 0 && i + 2 < ntiles) mbar_arrive_expect_tx(&ctl->xa[b], xa_bytes);
+      const int valid = min(kTileN, n - i * kTileN) - own0;  // valid columns of this thread's
+      if (valid < kCols) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) f[j] = (j < valid) ? f[j] : -INFINITY;
+        for (int j = 0; j < kCols; ++j) f[j] = (j < valid) ? f[j] : -INFINITY;
       }
       float mq[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) mq[k] = f[k];
 #pragma unroll
-      for (int j = 8; j < 32; ++j) mq[j & 7] = fmaxf(mq[j & 7], f[j]);
+      for (int j = 8; j < kCols; ++j) mq[j & 7] = fmaxf(mq[j & 7], f[j]);
       const float mx = scale_log2 * fmaxf(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])),
                                           fmaxf(fmaxf(mq[4], mq[5]), fmaxf(mq[6], mq[7])));
-      // 2) P of this CTA's columns against its reference (R, or its own
+      // 2) P of this thread's columns against its reference (R, or its own
       //    maximum when that exceeds R by more than 2^8)
       const float my_ref = (mx > m_ref + 8.f) ? mx : m_ref;
-      uint32_t pk[16];
+      uint32_t pk[kCols / 2];
       float l_part = 0.f;
       // P against reference `ref` (fp16 pairs, one rounding) and its sum;
       // nothing valid yet: zeros
@@ -1022,13 +1164,13 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
         l_part = 0.f;
         if (ref == -INFINITY) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) pk[j] = 0u;
+          for (int j = 0; j < kCols / 2; ++j) pk[j] = 0u;
           return;
         }
         float sums[4] = {0.f, 0.f, 0.f, 0.f};
         const float neg_m = -ref;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < kCols / 2; ++j) {
           const float p0 = ex2(fmaf(f[2 * j], scale_log2, neg_m));
           const float p1 = ex2(fmaf(f[2 * j + 1], scale_log2, neg_m));
           sums[j & 3] += p0 + p1;
@@ -1037,36 +1179,60 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
         l_part = (sums[0] + sums[1]) + (sums[2] + sums[3]);
       };
       own_p(my_ref);
-      // 3) P, reference and partial sum go to the peer
+      // 3) P and reference go to the peer: with the partial sum, or, with two
+      //    threads a row, the reference also to the other (whose wait on XB
+      //    counts this thread's arrival)
       const uint32_t xb_p = xa_p + kXABytes;
       const uint32_t xbb = b ? peer_xb1 : peer_xb0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        st_async_v4(xb_p + (q * 128 + h) * 16, __uint_as_float(pk[4 * q]),
+      for (int q = 0; q < kCols / 8; ++q)
+        st_async_v4(xb_p + ((kCols / 8 * g + q) * 128 + h) * 16, __uint_as_float(pk[4 * q]),
                     __uint_as_float(pk[4 * q + 1]), __uint_as_float(pk[4 * q + 2]),
                     __uint_as_float(pk[4 * q + 3]), xbb);
-      st_async_v2(xb_p + kXBPBytes + h * 8, my_ref, l_part, xbb);
+      if constexpr (G == 1) {
+        st_async_v2(xb_p + kXBPBytes + h * 8, my_ref, l_part, xbb);
+      } else {
+        st_async_f32(xb_p + kXBPBytes + (g * 128 + h) * 4, my_ref, xbb);
+        tmem_st1(lanes + kRefCol + 2 * b + g, __float_as_uint(my_ref));
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&ctl->xb[b]);
+      }
       // 4) while that is in flight: tile i + 1's scores (its QK^T could start
       //    once S(i) was read)
       if (i + 1 < ntiles && !start_tile(i + 1)) goto give_up;
-      // 5) the peer's P of tile i
+      // 5) the peer's P of tile i and the row's references
       ok = __all_sync(0xffffffffu, wait_bar_cluster(&ctl->xb[b], (i >> 1) & 1, abort, kWsExchangeP));
       if (!ok) goto give_up;
       const uint32_t xb_l = xa_l + kXABytes;
-      uint32_t pp[16];
+      uint32_t pp[kCols / 2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint4 v = lds128(xb_l + (q * 128 + h) * 16);
+      for (int q = 0; q < kCols / 8; ++q) {
+        const uint4 v = lds128(xb_l + ((kCols / 8 * g + q) * 128 + h) * 16);
         pp[4 * q] = v.x;
         pp[4 * q + 1] = v.y;
         pp[4 * q + 2] = v.z;
         pp[4 * q + 3] = v.w;
       }
-      const float2 peer_rl = ld_shared_f2(xb_l + kXBPBytes + h * 8);
-      if (h == 0 && i + 2 < ntiles) mbar_arrive_expect_tx(&ctl->xb[b], xb_bytes);
-      // 6) the shared reference moves to the larger of the two (identically
-      //    on both CTAs); what was computed against a smaller one is redone
-      const float r_new = fmaxf(my_ref, peer_rl.x);
+      // 6) the shared reference moves to the largest of the row's (identically
+      //    in all its threads); what was computed against a smaller one is
+      //    redone
+      float peer_ref, l_peer = 0.f, r_new;
+      if constexpr (G == 1) {
+        const float2 peer_rl = ld_shared_f2(xb_l + kXBPBytes + h * 8);
+        peer_ref = peer_rl.x;
+        l_peer = peer_rl.y;
+        r_new = fmaxf(my_ref, peer_ref);
+      } else {
+        uint32_t other;
+        tc_fence_after();
+        tmem_ld1(lanes + kRefCol + 2 * b + (1 - g), other);
+        peer_ref = ld_shared_f32(xb_l + kXBPBytes + (g * 128 + h) * 4);
+        const float peer_other = ld_shared_f32(xb_l + kXBPBytes + ((1 - g) * 128 + h) * 4);
+        tmem_ld_wait();
+        r_new = fmaxf(fmaxf(my_ref, __uint_as_float(other)), fmaxf(peer_ref, peer_other));
+      }
+      if (tid == 0 && i + 2 < ntiles) mbar_arrive_expect_tx(&ctl->xb[b], xb_bytes);
       float alpha = 1.f;  // O and l
       bool rescale = false;
       if (r_new != m_ref) {
@@ -1076,50 +1242,48 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
       // own P against a smaller reference: recomputed from the fp32 scores
       // (one rounding); the peer's: scaled in fp32 and rounded once more
       if (my_ref != r_new) own_p(r_new);
-      float l_peer = peer_rl.y;
-      if (peer_rl.x != r_new) {
-        const float fp = (peer_rl.x == -INFINITY) ? 0.f : ex2(peer_rl.x - r_new);
+      if (peer_ref != r_new) {
+        const float fp = (peer_ref == -INFINITY) ? 0.f : ex2(peer_ref - r_new);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < kCols / 2; ++j) {
           const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&pp[j]));
           pp[j] = h2_bits(__floats2half2_rn(v.x * fp, v.y * fp));
         }
         l_peer *= fp;
       }
-      const float l_own = l_part;
       m_ref = r_new;
-      // the same sum on both CTAs: keys 0..31 first, then 32..63
-      l = l * alpha + (C ? l_peer + l_own : l_own + l_peer);
+      // one thread a row: the same sum on both CTAs, keys 0..31 first
+      l = l * alpha + (G == 2 ? l_part : C ? l_peer + l_part : l_part + l_peer);
       if (i > 0) {
         ok = __all_sync(0xffffffffu, wait_bar(&ctl->pv_done, (i - 1) & 1, abort, kWsPvDone));
         if (!ok) goto give_up;
         tc_fence_after();
       }
-      // P(i) replaces P(i-1), which PV(i-1) has finished reading: keys
-      // 0..31 in columns 0..15, keys 32..63 in columns 16..31
-      tmem_st16(tmem_addr(tb, 32 * warp, kPCol + 16 * C), pk);
-      tmem_st16(tmem_addr(tb, 32 * warp, kPCol + 16 * (1 - C)), pp);
+      // P(i) replaces P(i-1), which PV(i-1) has finished reading: two keys a
+      // column
+      tmem_stn<kCols / 2>(lanes + kPCol + own0 / 2, pk);
+      tmem_stn<kCols / 2>(lanes + kPCol + peer0 / 2, pp);
       if (i > 0) {
         // tcgen05.ld/st are warp-collective: the warp rescales together when
-        // any of its rows needs it, each lane by its own factor (1 if none)
+        // any of its rows needs it, each lane by its own factor (1 if none),
+        // a row's threads each their share of O's columns
         if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
-          for (int cc = 0; cc < 8; ++cc) {
+          for (int cc = 8 / G * g; cc < 8 / G * (g + 1); ++cc) {
             uint32_t r[32];
-            const uint32_t addr = tmem_addr(tb, 32 * warp, kOCol + 32 * cc);
-            tmem_ld32(addr, r);
+            tmem_ld32(lanes + kOCol + 32 * cc, r);
             tmem_ld_wait();
 #pragma unroll
             for (int jj = 0; jj < 32; ++jj) r[jj] = __float_as_uint(__uint_as_float(r[jj]) * alpha);
-            tmem_st32(addr, r);
+            tmem_st32(lanes + kOCol + 32 * cc, r);
           }
         }
       }
       tmem_st_wait();
       tc_fence_before();
-      // this thread's row of P(i) is in TMEM: once all 128 have arrived the
-      // MMA thread issues PV(i); its completion releases the operand stage
-      // and lets the next P overwrite this one
+      // this thread's share of P(i) is in TMEM: once all have arrived the MMA
+      // warp issues PV(i); its completion releases the operand stage and lets
+      // the next P overwrite this one
       mbar_arrive(&ctl->p_full);
     }
     if (false) {
@@ -1130,64 +1294,42 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
     }
     // epilogue
     if (ok && ntiles > 0 && live_warp) {
-      ok = __all_sync(0xffffffffu, wait_bar(&ctl->pv_done, (ntiles - 1) & 1, abort, kWsPvLast));
+      if constexpr (G == 2) {
+        // the row's four shares of the sum meet in its own slot of the first
+        // exchange buffer (every reader of that slot has sent its P, or
+        // arrived, after reading it) and are added in one order
+        const uint32_t slot = h * 16 + (2 * C + g) * 4;
+        st_async_f32(map_to_cta(x_l, uint32_t(C)) + slot, l,
+                     map_to_cta(smem_u32(&ctl->sums), uint32_t(C)));
+        st_async_f32(peer_x + slot, l, map_to_cta(smem_u32(&ctl->sums), peer));
+        ok = __all_sync(0xffffffffu, wait_bar_cluster(&ctl->sums, 0, abort, kWsExchange));
+        const float4 v = ld_shared_f4(x_l + h * 16);
+        l = (v.x + v.y) + (v.z + v.w);
+      }
+      ok = __all_sync(0xffffffffu,
+                      ok && wait_bar(&ctl->pv_done, (ntiles - 1) & 1, abort, kWsPvLast));
       tc_fence_after();
     }
-    // one decision for all four softmax warps (the split epilogue below uses a
-    // 128-thread named barrier)
-    ok = !named_bar_or(4, 128, !ok);
-    if (a.splits > 1) {
-      split_epilogue<F>(a, ctl, C, t, split, ntiles, m_ref, l, tb, warp, h, ok && live_warp);
-    } else if (ok && live_warp) {
-      // tcgen05.ld is warp-collective: every lane loads, only live heads store
-      const bool live = h < a.H;
-      uint4* dst = reinterpret_cast<uint4*>(a.out + (t * a.H + (live ? h : 0)) * SMLA_V_DIM +
-                                            C * 256);
-      if (ntiles == 0) {
-        if (live) {
-#pragma unroll 1
-          for (int k = 0; k < 32; ++k) dst[k] = make_uint4(0, 0, 0, 0);
-        }
-      } else {
-        const float inv = 1.f / (l * F::kKeyScale);
-        // 32-byte stores fill whole sectors (`out` itself may be 16-byte aligned)
-        const bool whole = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
-#pragma unroll 1
-        for (int cc = 0; cc < 8; ++cc) {
-          uint32_t r[32];
-          tmem_ld32(tmem_addr(tb, 32 * warp, kOCol + 32 * cc), r);
-          tmem_ld_wait();
-          uint32_t o[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            __nv_bfloat162 v =
-                __floats2bfloat162_rn(__uint_as_float(r[o_col<F>(2 * j)]) * inv,
-                                      __uint_as_float(r[o_col<F>(2 * j + 1)]) * inv);
-            o[j] = *reinterpret_cast<uint32_t*>(&v);
-          }
-          if (live && whole) {
-            stg256(dst + cc * 4, o);
-            stg256(dst + cc * 4 + 2, o + 8);
-          } else if (live) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              dst[cc * 4 + k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          }
-        }
-      }
-      if (C == 0 && live)
-        a.lse[t * a.H + h] = (ntiles == 0) ? -INFINITY : (m_ref + log2f(l)) * kLn2;
-    }
-  } else if (warp < 8) {
+    // one decision for all softmax warps (the epilogue below uses a named
+    // barrier of theirs)
+    ok = !named_bar_or(4, R::kSoftmaxThreads, !ok);
+    row_epilogue<F>(a, ctl, C, t, split, ntiles, m_ref, l, tb, quad, g, h, live_warp, ok);
+  } else if (warp < R::kMmaWarp) {
     // ------------------------------------------------ dequantise
     // Converter d owns key d % 64 of every tile and half d / 64 of its
     // pieces, so each warp stores 32 consecutive rows of one chunk column
     // (conflict-free under the 128-byte swizzle).
-    const int d = tid - 128;
+    const int d = tid - 32 * R::kConvWarp0;
+    if constexpr (F::kFp4) {
+      if (ntiles <= kDirectTiles) {
+        convert_direct<kMode>(a, ctl, sm, n, ntiles, C, d, abort);
+        return;
+      }
+    }
     convert_loop<F>(ctl, sm, n, ntiles, d & (kTileN - 1), C, d >> 6, lane, abort);
-  } else if (warp >= kLoaderWarp0) {
+  } else if (warp >= R::kLoaderWarp0) {
     // ------------------------------------------------ stage cache rows
-    loader_loop<kMode, F>(a, ctl, sm, n, ntiles, pieces, abort);
+    if (!F::kFp4 || ntiles > kDirectTiles) loader_loop<kMode, F>(a, ctl, sm, n, ntiles, pieces, abort);
   } else {
     // ------------------------------------------------ MMA issue (one thread)
     // QK(i) needs its operand stage converted and S(i - 1) read by the
@@ -1356,8 +1498,10 @@ __device__ __forceinline__ bool dense_row(const DecodeArgs& a, int64_t t, int32_
 // that counts in like any other split.  Both CTAs of the pair take this path
 // together (the test depends only on the row and the split); it touches no
 // tensor memory and no peer shared memory.
+template <class F>
 __device__ void publish_empty_split(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, int64_t t, int split,
                                     int C) {
+  constexpr int kThreads = Roles<F>::kThreads;
   const int tid = threadIdx.x;
   if (a.splits == 1) {
     for (int idx = tid; idx < a.H * 32; idx += kThreads) {  // 32 x 16 bytes per head half
@@ -1378,7 +1522,7 @@ __device__ void publish_empty_split(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, 
   __syncthreads();
   if (tid == 0) ctl->is_last = (atomicAdd(a.ws_tick + t * 2 + C, 1) == a.splits - 1);
   __syncthreads();
-  if (ctl->is_last) combine_splits(a, sm, C, t);
+  if (ctl->is_last) combine_splits<F>(a, sm, C, t);
 }
 
 // Decodes of the serving step are launched behind the step's short kernels.
@@ -1386,8 +1530,12 @@ template <int kMode, class F>
 constexpr bool overlapped() { return F::kFp4 || kMode == kModeWindow; }
 
 template <int kMode, class F>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 1)
     sparse_mla_decode_kernel(const __grid_constant__ DecodeArgs a) {
+  constexpr int kSoftmaxWarps = Roles<F>::kSoftmaxWarps;
+  constexpr int kMmaWarp = Roles<F>::kMmaWarp;
+  constexpr int kLoaderWarp0 = Roles<F>::kLoaderWarp0;
+  constexpr int kRowThreads = F::kRowThreads;
   constexpr bool kPools = kMode != kModeSlots;  // entries resolve through D pools
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(
@@ -1417,7 +1565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const bool row_ok = dense_row<kMode>(a, t, r, range, e2);
     if (row_ok && min(e_end, range.limit) > e_begin) return false;
     if (tid == 0 && e2) atomicOr(&g_decode_error, e2);
-    publish_empty_split(a, sm, ctl, t, split, hr.c);
+    publish_empty_split<F>(a, sm, ctl, t, split, hr.c);
     return true;
   };
   if (kMode == kModeDense && empty_split()) return;
@@ -1427,23 +1575,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     mbar_init(&ctl->q_tma, 1);
-    mbar_init(&ctl->q_ready, 128);
+    mbar_init(&ctl->q_ready, 32 * kSoftmaxWarps);
     for (int st = 0; st < kStages; ++st) {
       mbar_init(&ctl->full[st], 128);
       mbar_init(&ctl->freed[st], 1);
     }
     mbar_init(&ctl->s_full, 1);
-    mbar_init(&ctl->s_free, 32 * softmax_warps(a.H));  // one arrival per softmax thread
+    mbar_init(&ctl->s_free, 32 * kRowThreads * softmax_warps(a.H));  // one arrival per softmax thread
     mbar_init(&ctl->pv_done, 1);
-    mbar_init(&ctl->p_full, 32 * softmax_warps(a.H));
+    mbar_init(&ctl->p_full, 32 * kRowThreads * softmax_warps(a.H));
     for (int st = 0; st < kRawStages; ++st) {
       mbar_init(&ctl->raw_full[st], kLoaders);  // one arrival per loader
       mbar_init(&ctl->raw_empty[st], 4);        // one arrival per converter warp
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctl->xa[b], 1);  // one expect_tx arrival per phase
-      mbar_init(&ctl->xb[b], 1);
+      // with two threads a row, also one arrival per reference left in tensor memory
+      mbar_init(&ctl->xb[b], 1 + (kRowThreads == 2 ? 64 * softmax_warps(a.H) : 0));
     }
+    mbar_init(&ctl->sums, 1);
     mbar_init(&ctl->end, 1);
     ctl->abort = 0;
     fence_mbar_init_cluster();
@@ -1465,12 +1615,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // The compacting warps' raw entries (kPer each of the row's split, see the
   // compaction below) are loaded before the set-up barrier, so that their
   // memory round trip overlaps the request id's.
-  constexpr int kListThreads = kThreads - 128;  // every warp but the softmax warps
+  constexpr int kListThreads = Roles<F>::kThreads - 32 * kSoftmaxWarps;  // every warp but the softmax warps
   constexpr int kPer =
       ((kMode == kModeWindow ? kWindowList : kMaxList) + kListThreads - 1) / kListThreads;
   int32_t vs[kPer];
-  if (!generated(kMode) && warp >= 4) {
-    const int j0 = e_begin + (tid - 128) * kPer;
+  if (!generated(kMode) && warp >= kSoftmaxWarps) {
+    const int j0 = e_begin + (tid - 32 * kSoftmaxWarps) * kPer;
     const int32_t* src = (kMode == kModeTopk ? a.topk : a.slots) + t * a.K;
     if (j0 + kPer <= e_end && (reinterpret_cast<uintptr_t>(src + j0) & 15u) == 0) {
 #pragma unroll
@@ -1510,23 +1660,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
 
-  if (warp < 4) {
+  if (warp < kSoftmaxWarps) {
     // Q half -> TMEM, overlapping the compaction below
     // the whole q tile landed (issued by thread 0 before the set-up barrier)
     bool qok = wait_bar(&ctl->q_tma, 0, &ctl->abort, kWsQReady);
-    if (warp < softmax_warps(a.H) &&
-        q_to_tmem<F>(ctl->tbase, warp, tid, qok && tid < a.H, smem_u32(sm + kOffOp)))
+    const int quad = warp & 3, h = tid & 127;
+    if (quad < softmax_warps(a.H) &&
+        q_to_tmem<F>(ctl->tbase, quad, kRowThreads == 1 ? 0 : warp >> 2, h, qok && h < a.H, smem_u32(sm + kOffOp)))
       atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
     tc_fence_before();
     mbar_arrive(&ctl->q_ready);
   } else {
     // Ordered compaction of the split's valid entries by the 256 threads of
-    // warps 4-11 (idle until the tile loop): thread d owns the contiguous
+    // the other warps (idle until the tile loop): thread d owns the contiguous
     // entries [e_begin + 8d, e_begin + 8d + 8), resolves them with all loads
     // in flight at once, and a block scan gives each thread its output
     // offset.  Both CTAs of the pair build the same list, so their tiles hold
     // the same keys.
-    const int d = tid - 128;
+    const int d = tid - 32 * kSoftmaxWarps;
     int* list = reinterpret_cast<int*>(sm + kOffList);
     uint8_t* list_shard = sm + kOffListShard;
     unsigned err = 0;
@@ -1605,13 +1756,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int y = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += y;
       }
-      if (lane == 31) ctl->warp_cnt[warp - 4] = incl;
+      if (lane == 31) ctl->warp_cnt[warp - kSoftmaxWarps] = incl;
       named_bar_sync(3, kListThreads);
       int wbase = 0, total = 0;
 #pragma unroll
       for (int w = 0; w < kListThreads / 32; ++w) {
         const int x = ctl->warp_cnt[w];
-        wbase += (w < warp - 4) ? x : 0;
+        wbase += (w < warp - kSoftmaxWarps) ? x : 0;
         total += x;
       }
       int pos = wbase + incl - cnt;
@@ -1636,7 +1787,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   run_cta<kMode, F>(a, sm, ctl, hr, t, split, peer, pieces);
 
-  if (warp >= 4) {
+  if (warp >= kSoftmaxWarps) {
     __syncwarp();
     cluster_wait();
   }
@@ -1647,7 +1798,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(ctl->tbase, kTmemCols);
   }
-  if (a.splits > 1 && ctl->is_last) combine_splits(a, sm, hr.c, t);
+  if (a.splits > 1 && ctl->is_last) combine_splits<F>(a, sm, hr.c, t);
 }
 
 // Split-K combine of one row's value half for eight heads, one warp per
@@ -1785,10 +1936,12 @@ int decode_splits(int32_t T, int32_t K) {
 // of a launch of one wave of pairs, in 1/100 us, fitted to fp4 decodes of 1-64
 // rows of 128-2048 entries (H = 128): 950 for a pair's set-up and epilogue,
 // 145 a tile of 64 keys, 7 a pair at work on the GPU, and 420 + 12 a split for
-// the kernel that merges splits.  Measured against at least 256 entries a
-// split: 1 row of 512 entries 8 splits 15.8 us (2: 22.8), 1 of 2048 16 splits
-// 18.3 (8: 19.7), 16 of 512 4 splits 19.5 (2: 24.3).  Splits that need a second
-// wave never won (80 rows of 2048: 1 split 117 us, 2 119).  Like decode_splits
+// the kernel that merges splits; the counts it picks are within 4% of the best
+// and 0.1% on average.  Measured against at least 256 entries a split: 1 row
+// of 512 entries 8 splits 13.8 us (2: 16.8), 1 of 2048 16 splits 15.9 (8:
+// 17.3), 16 of 512 4 splits 16.9 (2: 19.0).  Splits that need a second wave
+// gain little or lose (2 against 1: 80 rows of 2048 101.8 us, 105.0; 100 rows
+// 109.9, 105.9).  Like decode_splits
 // a function of the shape alone, with at most `list` entries per split.
 int model_splits(int32_t T, int32_t K, int list) {
   const int lo = (K + list - 1) / list;
@@ -1907,14 +2060,17 @@ cudaError_t launch_impl(const DecodeArgs& args, cudaStream_t s) {
   int sms = 0;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // The serving step's decodes merge in a second kernel whenever the grid
-  // leaves SMs idle for it (25 rows of 2048 in 3 splits: 35.7 us against 38.0;
-  // 38 rows in 2, which fill the GPU: 46.8 against 45.1).
-  a.combine_in_kernel = overlapped<kMode, F>() ? ctas >= sms : combine_in_kernel(ctas, a.splits, sms);
+  // The serving step's decodes merge in a second kernel unless the last CTAs
+  // can merge behind others' work (more than a wave), or two splits fill most
+  // of the GPU, which the second kernel would wait for (rows of 2048 entries,
+  // second kernel against last CTA: 25 rows in 3 splits 32.7 us, 34.5; 19 in 4
+  // 26.6, 30.5; 20 in 2 38.5, 39.2; 34 in 2 40.8, 39.7; 80 in 2 109.8, 101.8).
+  const bool last_merges = ctas > sms || (a.splits == 2 && 4 * ctas >= 3 * sms);
+  a.combine_in_kernel = overlapped<kMode, F>() ? last_merges : combine_in_kernel(ctas, a.splits, sms);
   if (overlapped<kMode, F>()) {
-    e = launch_overlapped(sparse_mla_decode_kernel<kMode, F>, unsigned(ctas), kThreads, kSmemBytes, s, a);
+    e = launch_overlapped(sparse_mla_decode_kernel<kMode, F>, unsigned(ctas), Roles<F>::kThreads, kSmemBytes, s, a);
   } else {
-    sparse_mla_decode_kernel<kMode, F><<<dim3(unsigned(ctas)), dim3(kThreads), kSmemBytes, s>>>(a);
+    sparse_mla_decode_kernel<kMode, F><<<dim3(unsigned(ctas)), dim3(Roles<F>::kThreads), kSmemBytes, s>>>(a);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || a.splits == 1 || a.T == 0 || a.combine_in_kernel) return e;
