@@ -604,6 +604,8 @@ __device__ void convert_loop(Ctl* ctl, uint8_t* sm, int n, int ntiles, int key, 
     // they refill it while this tile is converted
     __syncwarp();
     if (lane == 0) mbar_arrive(&ctl->raw_empty[st]);
+    // q was staged in the operand stages
+    if (i == 0 && !wait_bar(&ctl->q_ready, 0, abort, kWsQReady)) break;
     if (i >= kStages &&
         !wait_bar(&ctl->freed[i % kStages], ((i - kStages) / kStages) & 1, abort, kWsFreed))
       break;
@@ -691,6 +693,8 @@ __device__ void convert_direct(const DecodeArgs& a, Ctl* ctl, uint8_t* sm, int n
     if (i >= kStages &&
         !wait_bar(&ctl->freed[i % kStages], ((i - kStages) / kStages) & 1, abort, kWsFreed))
       break;
+    // q was staged in the operand stages
+    if (i == 0 && !wait_bar(&ctl->q_ready, 0, abort, kWsQReady)) break;
     bad |= convert_fp4(cur, op0 + (i % kStages) * kOpTileBytes, key, part);
     fence_async_shared();
     mbar_arrive(&ctl->full[i % kStages]);
@@ -1670,6 +1674,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
       atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
     tc_fence_before();
     mbar_arrive(&ctl->q_ready);
+    named_bar_sync(6, Roles<F>::kThreads);  // the list's length is known
   } else {
     // Ordered compaction of the split's valid entries by the 256 threads of
     // the other warps (idle until the tile loop): thread d owns the contiguous
@@ -1777,13 +1782,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
       if (d == 0) ctl->n_list = total;
     }
     if (err) atomicOr(&g_decode_error, err);
+    // the list is complete: its readers start on the first rows while q is
+    // still on its way into tensor memory
+    named_bar_arrive(6, Roles<F>::kThreads);
+    named_bar_sync(3, kListThreads);
   }
-  tc_fence_before();
-  __syncthreads();
-  // The peer's barriers are initialised before any remote store: only the
-  // softmax warps, which send them, wait for that before their loop.
+  // The peer's barriers are initialised, and its staged block tables read,
+  // before any remote store: only the softmax warps, which send them, wait
+  // for that before their loop.
+  __syncwarp();
   cluster_arrive();
-  tc_fence_after();
 
   run_cta<kMode, F>(a, sm, ctl, hr, t, split, peer, pieces);
 
@@ -1793,7 +1801,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // the peer no longer writes into this CTA's shared memory
+  // A CTA that finished has received everything its peer sends; one that gave
+  // up leaves only after the peer no longer writes into its shared memory.
+  if (ctl->abort) cluster_sync();
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(ctl->tbase, kTmemCols);

@@ -218,6 +218,10 @@ __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Count this thread in on barrier `id` without waiting for the others.
+__device__ __forceinline__ void named_bar_arrive(int id, int n) {
+  asm volatile("barrier.cta.arrive %0, %1;" :: "r"(id), "r"(n) : "memory");
+}
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(nthreads) : "memory");
 }
