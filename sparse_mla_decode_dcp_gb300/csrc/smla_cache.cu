@@ -16,11 +16,19 @@
 // value).  fp64 would do too but runs at about 1/60 of the fp32 rate here.
 //
 // One warp per row: a lane owns 16 consecutive latent dims (one fp4 group, an
-// eighth of an fp8 group) and one rope pair.
+// eighth of an fp8 group) and one rope pair.  Measured with norm and rotation:
+// 64 rows 1.8 us (fp4) and 2.2 (fp8), what a launch takes; 16,384 rows 8.5 and
+// 12.3; 65,536 rows 32.7 and 44.7, 3.7 and 3.0 TB/s, where the issue slots are
+// 73-76% busy with the exact sums and quotients (ALU and FMA pipes 50-57%),
+// not HBM.  Four rows a warp, the next one's loads ahead, gained nothing (fp4,
+// 16,384 rows: 10.4 us).
 //
 // Gather.  One warp per row, 8 dims per lane and step, so that every store is
 // 16 consecutive bytes a lane; kRows rows at once keep their loads in flight
 // together.  Bound by HBM: row + 4 bytes in, 1152 (bf16) or 2304 (fp32) out.
+// Measured on random rows: 4,001 to bf16 2.6 us (fp8 and fp4), 131,072 38.3
+// and 33.4 us, 262,144 73.8 and 64.5 (6.4 TB/s, 96% of a plain copy's rate); to
+// fp32 138 and 131 (5.5 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
@@ -36,6 +44,37 @@ __device__ unsigned int g_cache_error;
 
 constexpr int kWarps = 8;
 
+// Two fp32 side by side, in the packed instructions that issue once for both:
+// a write is bound by its instructions (fp4: 424 a row instead of 505, 16,384
+// rows 9.4 -> 8.5 us).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void f2_split(F2 a, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_sub(F2 a, F2 b) { return f2_fma(b, f2(-1.f, -1.f), a); }
+
 // A value as the unevaluated sum of two fp32.
 struct Pair {
   float hi, lo;
@@ -48,11 +87,16 @@ __device__ __forceinline__ Pair two_sum(float a, float b) {
   return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
 }
 
+// a + b, hi not rounded again: lo stays the sum of the parts cut off so far.
 __device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
   const Pair s = two_sum(a.hi, b.hi);
-  const float lo = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo));
-  const float hi = __fadd_rn(s.hi, lo);
-  return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
+  return {s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo))};
+}
+
+// hi + lo with hi the nearest fp32 (|lo| well below |hi|).
+__device__ __forceinline__ Pair pair_norm(Pair a) {
+  const float hi = __fadd_rn(a.hi, a.lo);
+  return {hi, __fsub_rn(a.lo, __fsub_rn(hi, a.hi))};
 }
 
 // a / d for an fp32 divisor; hi is the nearest fp32.
@@ -103,23 +147,27 @@ __device__ __forceinline__ Pair pair_rsqrt(Pair m) {
 // The codes of a lane's 16 values y r / d, packed into kWords words by
 // pack(v0, v1, pair index).  In fp32 alone a quotient is within 2^-21 of its
 // exact value, so where the codes of v (1 - 2^-20) and v (1 + 2^-20) agree they
-// are the exact quotient's; a warp with a value that close to a border (one
-// row in some thousands) takes the exact quotients.  Called by whole warps.
+// are the exact quotient's; a warp with a value that close to a border (about
+// one fp8 row in 100, one fp4 row in 500) takes the exact quotients.  Called by
+// whole warps.
 template <int kWords, class Pack>
-__device__ __forceinline__ void quantise(const float* y, Pair r, float d, float inv, uint32_t* w,
+__device__ __forceinline__ void quantise(const F2* y, Pair r, float d, float inv, uint32_t* w,
                                          Pack pack) {
   constexpr int kPairs = 8 / kWords;  // pairs of values a word
   const float t = __fmul_rn(r.hi, inv);
-  const float below = __fmul_rn(t, 1.f - 0x1p-20f), above = __fmul_rn(t, 1.f + 0x1p-20f);
+  const float tb = __fmul_rn(t, 1.f - 0x1p-20f), ta = __fmul_rn(t, 1.f + 0x1p-20f);
+  const F2 below = f2(tb, tb), above = f2(ta, ta);
   uint32_t near = 0;
 #pragma unroll
   for (int k = 0; k < kWords; ++k) {
     uint32_t lo = 0, hi = 0;
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      const float a = y[2 * (kPairs * k + i)], b = y[2 * (kPairs * k + i) + 1];
-      lo |= pack(__fmul_rn(a, below), __fmul_rn(b, below), i);
-      hi |= pack(__fmul_rn(a, above), __fmul_rn(b, above), i);
+      float a, b;
+      f2_split(f2_mul(y[kPairs * k + i], below), a, b);
+      lo |= pack(a, b, i);
+      f2_split(f2_mul(y[kPairs * k + i], above), a, b);
+      hi |= pack(a, b, i);
     }
     w[k] = lo;
     near |= lo ^ hi;
@@ -130,7 +178,8 @@ __device__ __forceinline__ void quantise(const float* y, Pair r, float d, float 
     w[k] = 0;
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      const float a = y[2 * (kPairs * k + i)], b = y[2 * (kPairs * k + i) + 1];
+      float a, b;
+      f2_split(y[kPairs * k + i], a, b);
       w[k] |= pack(quotient_odd(pair_mul(a, r), d, inv), quotient_odd(pair_mul(b, r), d, inv), i);
     }
   }
@@ -194,40 +243,49 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(const CacheWri
     g[4] = v1.x, g[5] = v1.y, g[6] = v1.z, g[7] = v1.w;
   }
 
-  float y[16];  // x g, exact
+  F2 y[8];  // x g, exact
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    y[2 * k] = bf16_lo(x[k]);
-    y[2 * k + 1] = bf16_hi(x[k]);
-  }
+  for (int k = 0; k < 8; ++k) y[k] = f2(bf16_lo(x[k]), bf16_hi(x[k]));
   Pair r = {1.f, 0.f};
   if (a.gamma) {
-    Pair ss = {0.f, 0.f};
+    // the even and the odd values' sums of squares, each with what its
+    // additions cut off
+    F2 sum = f2_mul(y[0], y[0]), cut = f2(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const Pair s = two_sum(ss.hi, __fmul_rn(y[k], y[k]));
-      ss = {s.hi, __fadd_rn(ss.lo, s.lo)};
+    for (int k = 1; k < 8; ++k) {
+      const F2 q = f2_mul(y[k], y[k]);
+      const F2 s = f2_add(sum, q);
+      const F2 qq = f2_sub(s, sum);
+      cut = f2_add(cut, f2_add(f2_sub(sum, f2_sub(s, qq)), f2_sub(q, qq)));
+      sum = s;
     }
+    Pair even, odd;
+    f2_split(sum, even.hi, odd.hi);
+    f2_split(cut, even.lo, odd.lo);
+    Pair ss = pair_add(even, odd);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
       ss = pair_add(ss, {__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
+    ss = pair_norm(ss);
     const Pair m = two_sum(__fmul_rn(ss.hi, 1.f / 512.f), a.eps);
     r = pair_rsqrt({m.hi, __fadd_rn(m.lo, __fmul_rn(ss.lo, 1.f / 512.f))});
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      y[2 * k] = __fmul_rn(y[2 * k], bf16_lo(g[k]));
-      y[2 * k + 1] = __fmul_rn(y[2 * k + 1], bf16_hi(g[k]));
-    }
+    for (int k = 0; k < 8; ++k) y[k] = f2_mul(y[k], f2(bf16_lo(g[k]), bf16_hi(g[k])));
   }
   // the group's largest magnitude; a value that is not finite (an infinite
   // or NaN input, or a sum of squares past fp32) makes the group's scale NaN
   float amax = 0.f;
-  bool finite = isfinite(r.hi) && isfinite(r.lo);
+  F2 zero = f2(0.f, 0.f);  // stays zero unless a value is not finite
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    amax = fmaxf(amax, fabsf(y[k]));
-    finite = finite && isfinite(y[k]);
+  for (int k = 0; k < 8; ++k) {
+    float u, v;
+    f2_split(y[k], u, v);
+    amax = fmaxf(amax, fmaxf(fabsf(u), fabsf(v)));
+    zero = f2_fma(y[k], f2(0.f, 0.f), zero);
   }
+  float z0, z1;
+  f2_split(zero, z0, z1);
+  bool finite = isfinite(r.hi) && isfinite(r.lo) && z0 == 0.f && z1 == 0.f;
   if (!kFp4) {
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
