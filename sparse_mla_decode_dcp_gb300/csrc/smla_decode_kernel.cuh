@@ -343,8 +343,8 @@ struct Fp4Rows {
 // The warps of a CTA: 4 or 8 softmax warps (kRowThreads threads a head row,
 // each finishing kCols of a tile's key columns), 4 converter warps, the MMA
 // warp, 3 loader warps.  Two threads a row shorten the softmax's chain, which
-// bounds the fp4 kernels (sparse step of 4 pools, 72 rows of 2048 entries,
-// H = 128: 58.2 -> 54.3 us; 8 rows 9.5 -> 8.4), but leave the loaders 128
+// bounds the fp4 kernels (sparse step of 4 pools, 64 rows of 2048 entries,
+// H = 128: 58.2 -> 54.3 us; 2 rows of 64 9.5 -> 8.4), but leave the loaders 128
 // instead of 168 registers, and fp8's rows, half again as long, then arrive
 // late (fused step 62.8 -> 66.9 us, dense decode 649 -> 690): one thread there.
 template <class F>
@@ -620,7 +620,7 @@ __device__ void convert_loop(Ctl* ctl, uint8_t* sm, int n, int ntiles, int key, 
 // Rows of up to kDirectTiles tiles (fp4): the converters load them themselves,
 // straight into registers and a tile ahead, which takes the trip through the
 // raw stage off a short row's chain.  Measured for 1 to 3 tiles: 0.1 to 0.3
-// us sooner (8 rows of 128 entries: 8.5 -> 8.3 us); from 4 tiles on the loads
+// us sooner (2 rows of 64 entries: 8.5 -> 8.3 us); from 4 tiles on the loads
 // hold the converters up (76 rows of 1024 entries: 32.6 -> 41.5 us).
 // Threads 2k and 2k + 1 own key k's pieces
 // 2i + part: a load instruction reads whole 32-byte sectors, and the eight
@@ -1335,12 +1335,12 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
     // ------------------------------------------------ stage cache rows
     if (!F::kFp4 || ntiles > kDirectTiles) loader_loop<kMode, F>(a, ctl, sm, n, ntiles, pieces, abort);
   } else {
-    // ------------------------------------------------ MMA issue (one thread)
+    // ------------------------------------------------ MMA issue
     // QK(i) needs its operand stage converted and S(i - 1) read by the
     // softmax, PV(i) the softmax's P(i); the warp sleeps on each barrier
     // until the hardware wakes it at the phase change.  Issuing PV here
     // rather than from a softmax thread keeps the MMA issue and a per-tile
-    // barrier of the four softmax warps off the softmax's chain.
+    // barrier of the softmax warps off the softmax's chain.
     // The whole warp runs the loop on values that are the same in every lane
     // and one elected lane issues: descriptors then stay in uniform registers,
     // and the 18 instructions of QK^T take ~400 clocks to issue (1200 when one
