@@ -42,6 +42,7 @@ QK_DIM, V_DIM, ROW_BYTES = 576, 512, 656
 HOST_CHUNKS = 4  # row groups of the host-buffer step (fastest of 1-8 on dcp4_long)
 # hashed to decide whether a committed ncu traffic figure still applies
 DECODE_SOURCES = ["sparse_mla_decode_dcp_gb300/csrc/smla_decode.cu",
+                  "sparse_mla_decode_dcp_gb300/csrc/smla_decode_kernel.cuh",
                   "sparse_mla_decode_dcp_gb300/csrc/smla_sm100.cuh"]
 KERNEL_SOURCES = {
     "smla_dcp_sparse_mla_decode_fused": DECODE_SOURCES,
