@@ -35,9 +35,10 @@
 //     row's code x scale has at most 6 significant bits and lies in [2^-10,
 //     2688] (or is 0), so its keys are exact in fp16.
 //   * Valid slots are compacted in order in the prologue (-1 never costs a
-//     load or an MMA).  Loader threads hold a tile's rows in registers while
-//     the tile before it is read out of a raw stage in shared memory; four
-//     operand tiles are in flight.
+//     load or an MMA).  Loader threads hold a tile's fp8 rows in registers
+//     while the tile before it is read out of a raw stage in shared memory;
+//     fp4 rows are converted from registers, loaded a tile ahead.  Four operand
+//     tiles are in flight.
 //   * The partial score tiles travel as asynchronous remote stores counted on
 //     the receiving CTA's mbarrier (st.async + expect_tx).
 //   * Softmax in the log2 domain with a lazily moved reference maximum: the
@@ -48,13 +49,14 @@
 // lanes 0-127, one or two threads a head row), 4 that dequantise, one that
 // allocates TMEM and issues every MMA (one elected lane: QK^T of a tile, then
 // PV of the tile two before it, once the softmax has stored that tile's P)
-// and 3 that load cache rows.
+// and 3 that load cache rows (fp8) or, two of them, convert rope values (fp4).
 // Every wait is bounded; a wait that runs out sets SMLA_DEVERR_TIMEOUT and
 // the CTA unwinds.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
 #include <atomic>
@@ -110,7 +112,7 @@ __device__ __forceinline__ void tmem_stn(uint32_t addr, const uint32_t* r) {
 constexpr int kKBlockBytes = kTileN * 128;          // 64 keys x 64 fp16, 128-byte swizzle
 constexpr int kRopeBlock = 4 * kKBlockBytes;        // 64 keys x 32 fp16, 64-byte swizzle
 constexpr int kOpTileBytes = kRopeBlock + kTileN * 64;  // 256 latent + 32 rope dims
-constexpr int kRawTileBytes = kTileN * 336;  // one tile of staged fp8 rows (fp4: 208 a row)
+constexpr int kRawTileBytes = kTileN * 336;  // one tile of staged fp8 rows
 // Per tile and direction the pair exchanges the fp32 partial scores of half
 // the tile's keys (XA) and then the fp16 P of the other half plus each row's
 // reference maximum and partial sum (XB).
@@ -120,6 +122,9 @@ constexpr int kXBBytes = kXBPBytes + 128 * 8;
 constexpr int kXBytes = kXABytes + kXBBytes;         // one buffer set
 constexpr int kOffOp = 0;
 constexpr int kOffRaw = kOffOp + kStages * kOpTileBytes;
+// fp4 rows have no raw stage: the list of their addresses takes its place
+constexpr int kOffRows = kOffRaw;
+static_assert(kWindowList * 8 <= kRawStages * kRawTileBytes && kMaxList <= kWindowList, "row addresses fit");
 constexpr int kOffX = kOffRaw + kRawStages * kRawTileBytes;
 constexpr int kOffList = kOffX + 2 * kXBytes;  // two buffer sets
 constexpr int kBtStageMax = 2 * kXBytes / 4;    // staged block-table entries (fused prologue)
@@ -225,15 +230,14 @@ __device__ __forceinline__ bool scale_out_of_range(float s) {
   return !(s <= 65504.f / 448.f) || (s != 0.f && s < 0x1p-22f);
 }
 
-// 8 bf16 -> 8 fp16 of value * up, up a power of two (exact where the product
-// is in fp16's normal range)
-__device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v, float up = 1.f) {
+// 8 bf16 -> 8 fp16 (exact in fp16's normal range)
+__device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t o[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    o[k] = h2_bits(__floats2half2_rn(__uint_as_float(w[k] << 16) * up,
-                                     __uint_as_float(w[k] & 0xffff0000u) * up));
+    o[k] = h2_bits(
+        __floats2half2_rn(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)));
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
@@ -299,16 +303,13 @@ __device__ __forceinline__ HalfRt half_of(uint32_t c) {
   return r;
 }
 
-// A cache row's format.  CTA c stages the bytes of its half of a row, at
-// kRawStride per row, in kPieces pieces of 16 bytes: its code pieces, then
-// its scales, then its four rope pieces.  kCodes: 16-byte code pieces of one
-// converter thread (its 128 dims).  kKeyScale: the operand tile holds the
-// keys times this; the softmax's scale and O's factor take it out again.
+// A cache row's format.
 struct Fp8Rows {
   static constexpr bool kFp4 = false;
   static constexpr int kRowThreads = 1;
-  static constexpr float kKeyScale = 1.f;
   static constexpr int kRowBytes = SMLA_ROW_BYTES;
+  // CTA c stages the bytes of its half of a row, at kRawStride per row, in
+  // kPieces pieces of 16 bytes.
   // pieces 0..15: codes [256c, 256c + 256) -> raw [0, 256); piece 16: the
   // four fp32 scales [512, 528) -> raw [256, 272); pieces 17..20: rope bf16
   // [528 + 64c, 592 + 64c) -> raw [272, 336)
@@ -316,33 +317,24 @@ struct Fp8Rows {
   static constexpr int kRawStride = 336;
   static constexpr int kRawScales = 256;
   static constexpr int kRawRope = 272;
-  static constexpr int kCodes = 8;
+  static constexpr int kCodes = 8;  // 16-byte code pieces of one converter thread (its 128 dims)
   static __device__ __forceinline__ int piece_src(int c, int j) {
     return j < 16 ? 256 * c + 16 * j : j == 16 ? 512 : 528 + 64 * c + 16 * (j - 17);
   }
 };
 
+// CTA c's half of a 4-bit row: codes [128c, 128c + 128), sixteen e4m3 scales
+// [256 + 16c, 272 + 16c), rope bf16 [288 + 64c, 352 + 64c).
 struct Fp4Rows {
   static constexpr bool kFp4 = true;
   static constexpr int kRowThreads = 2;
-  static constexpr float kKeyScale = 1.f / 128.f;
   static constexpr int kRowBytes = SMLA_FP4_ROW_BYTES;
-  // pieces 0..7: codes [128c, 128c + 128) -> raw [0, 128); piece 8: sixteen
-  // e4m3 scales [256 + 16c, 272 + 16c) -> raw [128, 144); pieces 9..12: rope
-  // bf16 [288 + 64c, 352 + 64c) -> raw [144, 208)
-  static constexpr int kPieces = 13;
-  static constexpr int kRawStride = 208;
-  static constexpr int kRawScales = 128;
-  static constexpr int kRawRope = 144;
-  static constexpr int kCodes = 4;
-  static __device__ __forceinline__ int piece_src(int c, int j) {
-    return j < 8 ? 128 * c + 16 * j : j == 8 ? 256 + 16 * c : 288 + 64 * c + 16 * (j - 9);
-  }
 };
 
 // The warps of a CTA: 4 or 8 softmax warps (kRowThreads threads a head row,
 // each finishing kCols of a tile's key columns), 4 converter warps, the MMA
-// warp, 3 loader warps.  Two threads a row shorten the softmax's chain, which
+// warp, 3 warps that load fp8 rows or, two of them, convert fp4 rows' rope
+// values.  Two threads a row shorten the softmax's chain, which
 // bounds the fp4 kernels (sparse step of 4 pools, 64 rows of 2048 entries,
 // H = 128: 58.2 -> 54.3 us; 2 rows of 64 9.5 -> 8.4), but leave the loaders 128
 // instead of 168 registers, and fp8's rows, half again as long, then arrive
@@ -358,28 +350,19 @@ struct Roles {
   static constexpr int kCols = kTileN / 2 / F::kRowThreads;
 };
 
-// The fp4 operand tile holds each run of 8 latent dims in the order 0 4 1 5 2
-// 6 3 7 (the pairs one 32-bit word of codes unpacks to with one shift and two
-// masks a pair); q is stored in that order too, so QK^T is unaffected, and
-// the columns of O are read back through this map.
-template <class F>
-__device__ __forceinline__ constexpr int o_col(int d) {
-  return F::kFp4 ? (d & ~7) + ((d & 3) << 1) + ((d >> 2) & 1) : d;
-}
-
-// Converter thread (key, part) of CTA c converts its key's code pieces
-// [kCodes part, kCodes (part + 1)) (tile dims 128 part .. 128 part + 127: one
-// fp8 scale group 2c + part, or eight fp4 groups) and rope pieces 2 part,
-// 2 part + 1 (tile dims 256 + 16 part .. 256 + 16 part + 15).
+// fp8 rows: converter thread (key, part) of CTA c converts its key's code
+// pieces [8 part, 8 part + 8) (tile dims 128 part .. 128 part + 127: scale
+// group 2c + part) and rope pieces 2 part, 2 part + 1 (tile dims 256 + 16 part
+// .. 256 + 16 part + 15).
 constexpr int kRopePerPart = 2;
 
-// Cache row of entry `idx` of the compacted list.
-template <int kMode, class F>
+// Cache row of entry `idx` of the compacted list (fp8 rows).
+template <int kMode>
 __device__ __forceinline__ const uint8_t* row_ptr(const DecodeArgs& a, const Ctl* ctl,
                                                   const int* list, const uint8_t* shard,
                                                   int idx) {
   const uint8_t* pool = kMode != kModeSlots ? ctl->pool[shard[idx]] : a.kv;
-  return pool + int64_t(list[idx]) * F::kRowBytes;
+  return pool + int64_t(list[idx]) * Fp8Rows::kRowBytes;
 }
 
 __device__ __forceinline__ void split_scale(float s, __half2& hi, __half2& lo) {
@@ -409,42 +392,36 @@ __device__ __forceinline__ uint32_t op_addr(uint32_t op, int key, int ldim) {
                     : op + kRopeBlock + sw64_offset(key, (ldim - 256) >> 3);
 }
 
-// 8 e2m1 codes (one 32-bit word, dim i in nibble i) -> 8 fp16 values code *
-// scale * 2^-7, in the order of o_col; scale7 = scale * 2^7.  A nibble's sign
-// moves to fp16's sign bit and its exponent and mantissa bits to fp16's bits
-// 11..9, which makes normal and subnormal codes alike land on code * 2^-14
-// (bias 1 against 15); scale * 2^14 itself would overflow fp16, so 2^-7 stays
-// on the keys, and one product does.  It is exact: at most 6 significant
-// bits, a multiple of 2^-17.  (Rope values times 2^-7 are exact down to 2^-10
-// and within 2^-18 of the value below.)
-__device__ __forceinline__ uint4 e2m1x8_scaled(uint32_t w, __half2 scale7) {
+// 8 e2m1 codes (one 32-bit word, dim i in nibble i) times their group's scale,
+// exact in fp16: at most 6 significant bits, 2^-10 to 2688.  The conversion
+// instruction keeps a tile's dims in their order; unpacking by shifts and masks
+// would leave them in another, which q and O would have to follow, and measured
+// 0.3 us slower (2 rows of 64 entries: 6.8 against 6.5; 32 rows of 2048 in two
+// splits 30.3, 29.9) to 0.8 us faster (64 rows of 2048: 52.8, 53.6).
+__device__ __forceinline__ uint4 e2m1x8_scaled(uint32_t w, __half2 scale) {
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t mag = i < 3 ? w << (9 - 4 * i) : w >> 3;
-    const uint32_t bits = (mag & 0x0E000E00u) | ((w << (12 - 4 * i)) & 0x80008000u);
-    o[i] = h2_bits(__hmul2(*reinterpret_cast<const __half2*>(&bits), scale7));
+    const __half2_raw h =
+        __nv_cvt_fp4x2_to_halfraw2(__nv_fp4x2_storage_t((w >> (8 * i)) & 0xffu), __NV_E2M1);
+    o[i] = h2_bits(__hmul2(__half2(h), scale));
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // One converter thread's staged pieces of its key: its code pieces, 2 rope
-// pieces and the scales of its codes' groups (fp8: one fp32; fp4: eight
-// e4m3).
-template <class F>
+// pieces and the scale of its codes' group.
 struct ConvRegs {
-  uint4 cur[F::kCodes + kRopePerPart];
+  uint4 cur[Fp8Rows::kCodes + kRopePerPart];
   float scale;
-  uint2 scale8;
 };
 
 // Read this thread's staged pieces of its key (`row` = the key's staged row;
 // zeros for a key past the row's valid count).  Lanes read rows kRawStride
 // apart, an odd number of 16-byte units: 8 consecutive keys hit 8 different
 // bank groups.
-template <class F>
-__device__ __forceinline__ void read_row(uint32_t row, bool live, int c, int part,
-                                         ConvRegs<F>& r) {
+__device__ __forceinline__ void read_row(uint32_t row, bool live, int c, int part, ConvRegs& r) {
+  using F = Fp8Rows;
   const uint32_t code0 = row + 16 * F::kCodes * part;
   const uint32_t rope0 = row + F::kRawRope + 32 * part;
 #pragma unroll
@@ -453,67 +430,37 @@ __device__ __forceinline__ void read_row(uint32_t row, bool live, int c, int par
 #pragma unroll
   for (int q = 0; q < kRopePerPart; ++q)
     r.cur[F::kCodes + q] = live ? lds128(rope0 + 16 * q) : make_uint4(0, 0, 0, 0);
-  if constexpr (F::kFp4) {
-    r.scale8 = live ? lds64(row + F::kRawScales + 8 * part) : make_uint2(0, 0);
-  } else {
-    // the one scale group of this thread's codes
-    r.scale = live ? ld_shared_f32(row + F::kRawScales + 4 * (2 * c + part)) : 0.f;
-  }
+  // the one scale group of this thread's codes
+  r.scale = live ? ld_shared_f32(row + F::kRawScales + 4 * (2 * c + part)) : 0.f;
 }
 
 // Convert the read pieces into the swizzled fp16 operand tile at `op` (the
 // same code path for both CTA ranks and parts).
 // Returns true when the key's scale or rope values do not fit the fp16 keys.
-template <class F>
-__device__ __forceinline__ bool convert_row(const ConvRegs<F>& r, uint32_t op, int key, int part) {
-  bool bad_scale;
-  if constexpr (F::kFp4) {
-    uint32_t nan = 0;
+__device__ __forceinline__ bool convert_row(const ConvRegs& r, uint32_t op, int key, int part) {
+  using F = Fp8Rows;
+  __half2 hi, lo;
+  split_scale(r.scale, hi, lo);
 #pragma unroll
-    for (int k = 0; k < F::kCodes; ++k) {
-      // two scale groups of 16 dims per code piece
-      const uint32_t s2 = ((k < 2 ? r.scale8.x : r.scale8.y) >> (16 * (k & 1))) & 0xffffu;
-      const __half2_raw sr = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(s2), __NV_E4M3);
-      const __half2 ss = __half2(sr);
-      const uint32_t sb = h2_bits(ss);
-      nan |= (sb & 0x7fffu) > 0x7c00u || (sb & 0x7fff0000u) > 0x7c000000u;
-      const __half2 up = __float2half2_rn(128.f);
-      const __half2 s0 = __hmul2(__low2half2(ss), up), s1 = __hmul2(__high2half2(ss), up);
-      const int ldim = 128 * part + 32 * k;
-      sts128(op_addr(op, key, ldim), e2m1x8_scaled(r.cur[k].x, s0));
-      sts128(op_addr(op, key, ldim + 8), e2m1x8_scaled(r.cur[k].y, s0));
-      sts128(op_addr(op, key, ldim + 16), e2m1x8_scaled(r.cur[k].z, s1));
-      sts128(op_addr(op, key, ldim + 24), e2m1x8_scaled(r.cur[k].w, s1));
-    }
-    bad_scale = nan != 0;
-  } else {
-    __half2 hi, lo;
-    split_scale(r.scale, hi, lo);
-#pragma unroll
-    for (int k = 0; k < F::kCodes; ++k) {
-      const int ldim = 128 * part + 16 * k;
-      sts128(op_addr(op, key, ldim), e4m3x8_scaled(make_uint2(r.cur[k].x, r.cur[k].y), hi, lo));
-      sts128(op_addr(op, key, ldim + 8), e4m3x8_scaled(make_uint2(r.cur[k].z, r.cur[k].w), hi, lo));
-    }
-    bad_scale = scale_out_of_range(r.scale);
+  for (int k = 0; k < F::kCodes; ++k) {
+    const int ldim = 128 * part + 16 * k;
+    sts128(op_addr(op, key, ldim), e4m3x8_scaled(make_uint2(r.cur[k].x, r.cur[k].y), hi, lo));
+    sts128(op_addr(op, key, ldim + 8), e4m3x8_scaled(make_uint2(r.cur[k].z, r.cur[k].w), hi, lo));
   }
   uint32_t over = 0;
 #pragma unroll
   for (int q = 0; q < kRopePerPart; ++q) {
     over |= bf16x8_over_fp16(r.cur[F::kCodes + q]);
-    sts128(op_addr(op, key, 256 + 16 * part + 8 * q), 
-           bf16x8_to_f16x8(r.cur[F::kCodes + q], F::kKeyScale));
+    sts128(op_addr(op, key, 256 + 16 * part + 8 * q), bf16x8_to_f16x8(r.cur[F::kCodes + q]));
   }
-  return over != 0 || bad_scale;
+  return over != 0 || scale_out_of_range(r.scale);
 }
 
-// The loader warps' loop.  Loader ld owns pieces ld + 96k of every tile (fp8:
-// 64 rows x 21 pieces = 14 x 96; fp4: 64 x 13, the last round two thirds
-// full), so consecutive lanes read consecutive 16 bytes of a row (whole
-// sectors, few transactions).  A tile's
-// pieces are loaded into registers while the raw stage holds the tile before
-// it, and stored once the converter warps have read that tile out of the
-// stage.  Load-issue stalls (the memory system's request slots) fall on these
+// The loader warps' loop (fp8 rows).  Loader ld owns pieces ld + 96k of every
+// tile (64 rows x 21 pieces = 14 x 96), so consecutive lanes read consecutive
+// 16 bytes of a row (whole sectors, few transactions).  A tile's pieces are
+// loaded into registers while the raw stage holds the tile before it, and
+// stored once the converter warps have read that tile out of the stage.  Load-issue stalls (the memory system's request slots) fall on these
 // warps, not on the converters.
 static_assert(kTileN * Fp8Rows::kRawStride <= (1 << 15) && Fp8Rows::kRowBytes <= (1 << 10) &&
                   kTileN <= (1 << 7),
@@ -524,33 +471,29 @@ static_assert(kTileN * Fp8Rows::kRawStride <= (1 << 15) && Fp8Rows::kRowBytes <=
 // stage, packed once as r << 25 | src << 15 | dst (dst < 2^15, src < 2^10).
 // A loader forms its pieces' places before the set-up barrier, while other
 // warps' first loads are on the way.
-template <class F>
 struct Pieces {
-  static constexpr int kCount = kTileN * F::kPieces;
-  static constexpr int kPer = (kCount + kLoaders - 1) / kLoaders;
+  static constexpr int kPer = kTileN * Fp8Rows::kPieces / kLoaders;
+  static_assert(kPer * kLoaders == kTileN * Fp8Rows::kPieces, "a tile's pieces fill the rounds");
   uint32_t pk[kPer];
   __device__ __forceinline__ void place(int c, int ld) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int p = ld + kLoaders * k;
-      // p / 21 or p / 13, exact for p < 64 * 21 (p < 9 * 96)
-      const int r = int((uint32_t(p) * (F::kFp4 ? 5042u : 3121u)) >> 16);
-      const int j = p - r * F::kPieces;
-      // a piece past the tile (fp4's last round): row 64, never below a row count
-      pk[k] = uint32_t(r) << 25 | uint32_t(F::piece_src(c, j)) << 15 |
-              uint32_t(r * F::kRawStride + 16 * j);
-      if (kCount % kLoaders != 0 && p >= kCount) pk[k] = uint32_t(kTileN) << 25;
+      const int r = int((uint32_t(p) * 3121u) >> 16);  // p / 21, exact for p < 64 * 21
+      const int j = p - r * Fp8Rows::kPieces;
+      pk[k] = uint32_t(r) << 25 | uint32_t(Fp8Rows::piece_src(c, j)) << 15 |
+              uint32_t(r * Fp8Rows::kRawStride + 16 * j);
     }
   }
 };
 
-template <int kMode, class F>
+template <int kMode>
 __device__ void loader_loop(const DecodeArgs& a, Ctl* ctl, uint8_t* sm, int n, int ntiles,
-                            const Pieces<F>& pieces, volatile int* abort) {
+                            const Pieces& pieces, volatile int* abort) {
   const int* list = reinterpret_cast<const int*>(sm + kOffList);
   const uint8_t* list_shard = sm + kOffListShard;
   const uint32_t raw0 = smem_u32(sm + kOffRaw);
-  constexpr int kPiecesPerLoader = Pieces<F>::kPer;
+  constexpr int kPiecesPerLoader = Pieces::kPer;
   const uint32_t (&pk)[kPiecesPerLoader] = pieces.pk;
   uint4 buf[kPiecesPerLoader];
   auto load = [&](int tile) {
@@ -560,7 +503,7 @@ __device__ void loader_loop(const DecodeArgs& a, Ctl* ctl, uint8_t* sm, int n, i
     for (int k = 0; k < kPiecesPerLoader; ++k) {
       const uint32_t r = pk[k] >> 25;
       if (r < rows) {
-        const uint8_t* row = row_ptr<kMode, F>(a, ctl, list, list_shard, base + int(r));
+        const uint8_t* row = row_ptr<kMode>(a, ctl, list, list_shard, base + int(r));
         buf[k] = ldg_stream(row + ((pk[k] >> 15) & 1023u));
       }
     }
@@ -584,10 +527,9 @@ __device__ void loader_loop(const DecodeArgs& a, Ctl* ctl, uint8_t* sm, int n, i
   }
 }
 
-// The converter threads' tile loop: each staged tile is converted into the
+// The converter threads' tile loop (fp8 rows): each staged tile is converted into the
 // fp16 operand stage once the MMAs of the tile two back have released it,
 // then handed back to the loaders (one arrival per warp).
-template <class F>
 __device__ void convert_loop(Ctl* ctl, uint8_t* sm, int n, int ntiles, int key, int c, int part,
                              int lane, volatile int* abort) {
   const uint32_t raw0 = smem_u32(sm + kOffRaw);
@@ -597,8 +539,8 @@ __device__ void convert_loop(Ctl* ctl, uint8_t* sm, int n, int ntiles, int key, 
   for (int i = 0; i < ntiles; ++i) {
     const int st = i % kRawStages;
     if (!wait_bar(&ctl->raw_full[st], (i / kRawStages) & 1, abort, kWsRaw)) break;
-    ConvRegs<F> r;
-    read_row<F>(raw0 + st * kRawTileBytes + key * F::kRawStride, key < n - i * kTileN, c, part, r);
+    ConvRegs r;
+    read_row(raw0 + st * kRawTileBytes + key * Fp8Rows::kRawStride, key < n - i * kTileN, c, part, r);
     // the raw stage goes back to the loaders as soon as the warp has read it
     // (the warp barrier orders the lanes' reads before lane 0's release), so
     // they refill it while this tile is converted
@@ -609,7 +551,7 @@ __device__ void convert_loop(Ctl* ctl, uint8_t* sm, int n, int ntiles, int key, 
     if (i >= kStages &&
         !wait_bar(&ctl->freed[i % kStages], ((i - kStages) / kStages) & 1, abort, kWsFreed))
       break;
-    out_of_range |= convert_row<F>(r, op0 + (i % kStages) * kOpTileBytes, key, part) &&
+    out_of_range |= convert_row(r, op0 + (i % kStages) * kOpTileBytes, key, part) &&
                     key < n - i * kTileN;
     fence_async_shared();
     mbar_arrive(&ctl->full[i % kStages]);
@@ -617,90 +559,124 @@ __device__ void convert_loop(Ctl* ctl, uint8_t* sm, int n, int ntiles, int key, 
   if (out_of_range) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
 }
 
-// Rows of up to kDirectTiles tiles (fp4): the converters load them themselves,
-// straight into registers and a tile ahead, which takes the trip through the
-// raw stage off a short row's chain.  Measured for 1 to 3 tiles: 0.1 to 0.3
-// us sooner (2 rows of 64 entries: 8.5 -> 8.3 us); from 4 tiles on the loads
-// hold the converters up (76 rows of 1024 entries: 32.6 -> 41.5 us).
-// Threads 2k and 2k + 1 own key k's pieces
-// 2i + part: a load instruction reads whole 32-byte sectors, and the eight
-// lanes of four keys store to eight different bank groups.
-constexpr int kDirectTiles = 3;
+// fp4 rows go straight from global memory into registers and from there into
+// the operand stages: with 13 pieces of 16 bytes a half row two threads' worth
+// of registers hold a tile ahead, and the trip through a raw stage (208 of some
+// 1100 wavefronts of shared memory a tile) is saved.  The converter warps take
+// the codes, warp w keys [16 w, 16 w + 16) of a tile: eight lanes read the 128
+// bytes of a key's codes (lane j piece j: dims 32 j .. of the CTA's half, two
+// scale groups), so that a load instruction reads whole lines.  Two more warps
+// take the rope values, four lanes a key.  Against loader warps and a raw
+// stage: 2 rows of 64 entries 7.6 -> 6.5 us, one pool's 32 rows of 2048 (two
+// splits) 32.0 -> 29.9, four pools' 64 rows 55.1 -> 53.6, windows of 1088
+// entries 66.2 -> 63.0.  Two threads a key with 32-byte loads were slower (61
+// us on the four pools), two tiles ahead too (53.5; one 53.1), and so were
+// addresses formed from slot and shard per load (60.8): the list holds the
+// rows' addresses, and each tile's are read a tile early.
+constexpr int kRopeThreads = 64;
 
 struct Fp4Regs {
-  uint4 code[4], rope[2], scale;
+  uint4 code[4];
+  uint32_t scale[4];
 };
 
-__device__ __forceinline__ void load_fp4(const uint8_t* row, int c, int part, Fp4Regs& r) {
-  if (row != nullptr) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.code[i] = ldg_stream(row + 128 * c + 32 * i + 16 * part);
-    r.scale = ldg_stream(row + 256 + 16 * c);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) r.rope[i] = ldg_stream(row + 288 + 64 * c + 32 * i + 16 * part);
-  } else {
-    const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.code[i] = z;
-    r.scale = r.rope[0] = r.rope[1] = z;
-  }
-}
-
-__device__ __forceinline__ bool convert_fp4(const Fp4Regs& r, uint32_t op, int key, int part) {
-  uint32_t nan = 0;
-  const uint32_t sw[4] = {r.scale.x, r.scale.y, r.scale.z, r.scale.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // piece 2i + part: dims 32 (2i + part) .., two scale groups
-    const uint32_t s2 = (sw[i] >> (16 * part)) & 0xffffu;
-    const __half2 ss = __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(s2), __NV_E4M3));
-    const uint32_t sb = h2_bits(ss);
-    nan |= (sb & 0x7fffu) > 0x7c00u || (sb & 0x7fff0000u) > 0x7c000000u;
-    const __half2 up = __float2half2_rn(128.f);
-    const __half2 s0 = __hmul2(__low2half2(ss), up), s1 = __hmul2(__high2half2(ss), up);
-    const uint32_t blk = op + i * kKBlockBytes;
-    sts128(blk + sw128_offset(key, 4 * part), e2m1x8_scaled(r.code[i].x, s0));
-    sts128(blk + sw128_offset(key, 4 * part + 1), e2m1x8_scaled(r.code[i].y, s0));
-    sts128(blk + sw128_offset(key, 4 * part + 2), e2m1x8_scaled(r.code[i].z, s1));
-    sts128(blk + sw128_offset(key, 4 * part + 3), e2m1x8_scaled(r.code[i].w, s1));
-  }
-  uint32_t over = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    over |= bf16x8_over_fp16(r.rope[i]);
-    sts128(op + kRopeBlock + sw64_offset(key, 2 * i + part), bf16x8_to_f16x8(r.rope[i], Fp4Rows::kKeyScale));
-  }
-  return over != 0 || nan != 0;
-}
-
-template <int kMode>
-__device__ void convert_direct(const DecodeArgs& a, Ctl* ctl, uint8_t* sm, int n, int ntiles, int c,
-                               int d, volatile int* abort) {
-  const int* list = reinterpret_cast<const int*>(sm + kOffList);
-  const uint8_t* list_shard = sm + kOffListShard;
+__device__ void convert_codes(Ctl* ctl, uint8_t* sm, int n, int ntiles, int c, int d,
+                              volatile int* abort) {
+  const uint8_t* const* rows = reinterpret_cast<const uint8_t* const*>(sm + kOffRows);
   const uint32_t op0 = smem_u32(sm + kOffOp);
-  const int key = d >> 1, part = d & 1;
-  auto row_of = [&](int tile) -> const uint8_t* {
-    const int idx = tile * kTileN + key;
-    return idx < n ? row_ptr<kMode, Fp4Rows>(a, ctl, list, list_shard, idx) : nullptr;
+  const int lane = d & 31;
+  const int j = lane & 7;
+  const int key0 = (d >> 5) * 16 + (lane >> 3);  // this lane's keys: key0 + 4 i
+  const uint8_t* row[4];
+  auto place = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int idx = tile * kTileN + key0 + 4 * i;
+      row[i] = idx < n ? rows[idx] : nullptr;
+    }
   };
+  auto load = [&](int tile, Fp4Regs& r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.code[i] = row[i] ? ldg_stream(row[i] + 128 * c + 16 * j) : make_uint4(0, 0, 0, 0);
+      r.scale[i] = row[i] ? __ldg(reinterpret_cast<const uint16_t*>(row[i] + 256 + 16 * c) + j) : 0;
+    }
+    place(tile + 1);
+  };
+  // Lane j stores its four 16-byte chunks from chunk j / 2 on, so that a key's
+  // eight lanes (two to each of four K-blocks) hit eight bank groups at a time.
+  const int rot = j >> 1;
   Fp4Regs cur, next;
-  if (ntiles > 0) load_fp4(row_of(0), c, part, cur);
-  bool bad = false;
+  place(0);
+  if (ntiles > 0) load(0, cur);
+  bool nan = false;
 #pragma unroll 1
   for (int i = 0; i < ntiles; ++i) {
-    if (i + 1 < ntiles) load_fp4(row_of(i + 1), c, part, next);
+    if (i + 1 < ntiles) load(i + 1, next);
+    // q was staged in the operand stages
+    if (i == 0 && !wait_bar(&ctl->q_ready, 0, abort, kWsQReady)) break;
     if (i >= kStages &&
         !wait_bar(&ctl->freed[i % kStages], ((i - kStages) / kStages) & 1, abort, kWsFreed))
       break;
-    // q was staged in the operand stages
-    if (i == 0 && !wait_bar(&ctl->q_ready, 0, abort, kWsQReady)) break;
-    bad |= convert_fp4(cur, op0 + (i % kStages) * kOpTileBytes, key, part);
+    const uint32_t blk = op0 + (i % kStages) * kOpTileBytes + (j >> 1) * kKBlockBytes;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __half2 ss =
+          __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(cur.scale[k]), __NV_E4M3));
+      const uint32_t sb = h2_bits(ss);
+      nan |= (sb & 0x7fffu) > 0x7c00u || (sb & 0x7fff0000u) > 0x7c000000u;
+      const __half2 s0 = __low2half2(ss), s1 = __high2half2(ss);
+      uint4 v = cur.code[k];
+      if (rot & 1) v = make_uint4(v.y, v.z, v.w, v.x);
+      if (rot & 2) v = make_uint4(v.z, v.w, v.x, v.y);
+      const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int chunk = (m + rot) & 3;
+        sts128(blk + sw128_offset(key0 + 4 * k, 4 * (j & 1) + chunk),
+               e2m1x8_scaled(word[m], chunk < 2 ? s0 : s1));
+      }
+    }
     fence_async_shared();
     mbar_arrive(&ctl->full[i % kStages]);
     cur = next;
   }
-  if (bad) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
+  if (nan) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
+}
+
+__device__ void convert_rope(Ctl* ctl, uint8_t* sm, int n, int ntiles, int c, int d,
+                             volatile int* abort) {
+  const uint8_t* const* rows = reinterpret_cast<const uint8_t* const*>(sm + kOffRows);
+  const uint32_t op0 = smem_u32(sm + kOffOp) + kRopeBlock;
+  uint4 cur[4], next[4];
+  auto load = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int idx = tile * kTileN + 16 * i + (d >> 2);
+      next[i] = idx < n ? ldg_stream(rows[idx] + 288 + 64 * c + 16 * (d & 3)) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (ntiles > 0) load(0);
+  uint32_t over = 0;
+#pragma unroll 1
+  for (int i = 0; i < ntiles; ++i) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) cur[k] = next[k];
+    if (i + 1 < ntiles) load(i + 1);
+    if (i == 0 && !wait_bar(&ctl->q_ready, 0, abort, kWsQReady)) break;
+    if (i >= kStages &&
+        !wait_bar(&ctl->freed[i % kStages], ((i - kStages) / kStages) & 1, abort, kWsFreed))
+      break;
+    const uint32_t op = op0 + (i % kStages) * kOpTileBytes;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      over |= bf16x8_over_fp16(cur[k]);
+      sts128(op + sw64_offset(16 * k + (d >> 2), d & 3), bf16x8_to_f16x8(cur[k]));
+    }
+    fence_async_shared();
+    mbar_arrive(&ctl->full[i % kStages]);
+  }
+  if (over) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
 }
 
 // The softmax warps' epilogue: each thread of a head row stores its share of
@@ -736,7 +712,7 @@ __device__ __forceinline__ void row_epilogue(const DecodeArgs& a, Ctl* ctl, int 
   uint4* dst = reinterpret_cast<uint4*>((partial ? a.ws_o : a.out) + row * SMLA_V_DIM + C * 256 + g * kShare);
   if (has) {
     // tcgen05.ld is warp-collective: every lane loads, only live heads store
-    const float inv = partial && !(l > 0.f) ? 0.f : 1.f / (l * F::kKeyScale);
+    const float inv = partial && !(l > 0.f) ? 0.f : 1.f / l;
     // 32-byte stores fill whole sectors (`out` itself may be 16-byte aligned)
     const bool whole = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
 #pragma unroll 1
@@ -746,8 +722,8 @@ __device__ __forceinline__ void row_epilogue(const DecodeArgs& a, Ctl* ctl, int 
       tmem_ld_wait();
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const float x0 = __uint_as_float(r[o_col<F>(2 * j)]) * inv;
-        const float x1 = __uint_as_float(r[o_col<F>(2 * j + 1)]) * inv;
+        const float x0 = __uint_as_float(r[2 * j]) * inv;
+        const float x1 = __uint_as_float(r[2 * j + 1]) * inv;
         if (partial) {
           o[j] = h2_bits(__floats2half2_rn(x0, x1));
         } else {
@@ -937,21 +913,12 @@ __device__ void combine_splits(const DecodeArgs& a, uint8_t* sm, int C, int64_t 
   if (tid == 0) a.ws_tick[t * 2 + C] = 0;
 }
 
-// 8 dims in the order of o_col: pairs (0, 4), (1, 5), (2, 6), (3, 7).
-__device__ __forceinline__ uint4 pair_halves(uint4 v) {
-  return make_uint4(__byte_perm(v.x, v.z, 0x5410u), __byte_perm(v.x, v.z, 0x7632u),
-                    __byte_perm(v.y, v.w, 0x5410u), __byte_perm(v.y, v.w, 0x7632u));
-}
-
-// Store 8 q loads (64 dims) as fp16 pairs into 32 (or 16) TMEM columns; the
-// latent dims in the operand tile's order.
-template <class F>
+// Store 8 q loads (64 dims) as fp16 pairs into 32 (or 16) TMEM columns.
 __device__ __forceinline__ void q_store_group(const uint4* raw, uint32_t addr, bool full) {
   uint32_t qr[32];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     uint4 v = bf16x8_to_f16x8(raw[k]);
-    if (F::kFp4 && full) v = pair_halves(v);
     qr[4 * k + 0] = v.x;
     qr[4 * k + 1] = v.y;
     qr[4 * k + 2] = v.z;
@@ -1005,7 +972,7 @@ __device__ bool q_to_tmem(uint32_t tb, int quad, int g, int h, bool live, uint32
       raw[v] = (live && (grp < 4 || v < 4)) ? lds128(addr) : make_uint4(0, 0, 0, 0);
       over |= bf16x8_over_fp16(raw[v]);
     }
-    q_store_group<F>(raw, base + 32 * grp, grp < 4);
+    q_store_group(raw, base + 32 * grp, grp < 4);
   }
   tmem_st_wait();
   return over != 0;
@@ -1041,7 +1008,7 @@ __device__ __forceinline__ void issue_pv(uint32_t tb, uint32_t op, bool accumula
 
 template <int kMode, class F>
 __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt& hr, int64_t t,
-                        int split, uint32_t peer, const Pieces<F>& pieces) {
+                        int split, uint32_t peer, const Pieces& pieces) {
   const int C = hr.c;
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -1064,7 +1031,7 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
     const uint32_t xa_bytes = softmax_warps(a.H) * (kXABytes / 4);
     const uint32_t xb_bytes = softmax_warps(a.H) * (kXBBytes / 4);
     const uint32_t lanes = tmem_addr(tb, 32 * quad, 0);
-    const float scale_log2 = a.sm_scale * kLog2e / F::kKeyScale;
+    const float scale_log2 = a.sm_scale * kLog2e;
     float m_ref = -INFINITY;  // log2-domain reference maximum
     float l = 0.f;            // the sum (two threads a row: this one's columns' share)
     // Key-column split of the softmax: CTA c finishes the scores of keys
@@ -1324,16 +1291,17 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
     // pieces, so each warp stores 32 consecutive rows of one chunk column
     // (conflict-free under the 128-byte swizzle).
     const int d = tid - 32 * R::kConvWarp0;
-    if constexpr (F::kFp4) {
-      if (ntiles <= kDirectTiles) {
-        convert_direct<kMode>(a, ctl, sm, n, ntiles, C, d, abort);
-        return;
-      }
-    }
-    convert_loop<F>(ctl, sm, n, ntiles, d & (kTileN - 1), C, d >> 6, lane, abort);
+    if constexpr (F::kFp4)
+      convert_codes(ctl, sm, n, ntiles, C, d, abort);
+    else
+      convert_loop(ctl, sm, n, ntiles, d & (kTileN - 1), C, d >> 6, lane, abort);
   } else if (warp >= R::kLoaderWarp0) {
-    // ------------------------------------------------ stage cache rows
-    if (!F::kFp4 || ntiles > kDirectTiles) loader_loop<kMode, F>(a, ctl, sm, n, ntiles, pieces, abort);
+    // ------------------------------------------------ stage cache rows, or rope
+    if constexpr (!F::kFp4) {
+      loader_loop<kMode>(a, ctl, sm, n, ntiles, pieces, abort);
+    } else if (tid < 32 * R::kLoaderWarp0 + kRopeThreads) {
+      convert_rope(ctl, sm, n, ntiles, C, tid - 32 * R::kLoaderWarp0, abort);
+    }
   } else {
     // ------------------------------------------------ MMA issue
     // QK(i) needs its operand stage converted and S(i - 1) read by the
@@ -1581,7 +1549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
     mbar_init(&ctl->q_tma, 1);
     mbar_init(&ctl->q_ready, 32 * kSoftmaxWarps);
     for (int st = 0; st < kStages; ++st) {
-      mbar_init(&ctl->full[st], 128);
+      mbar_init(&ctl->full[st], F::kFp4 ? 128 + kRopeThreads : 128);
       mbar_init(&ctl->freed[st], 1);
     }
     mbar_init(&ctl->s_full, 1);
@@ -1614,8 +1582,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
   }
   // q lands in the (still idle) operand stages while the CTA sets up
   if (tid == 0) issue_q_tma(a, t, hr.c, smem_u32(sm + kOffOp), &ctl->q_tma);
-  Pieces<F> pieces;
-  if (warp >= kLoaderWarp0) pieces.place(hr.c, tid - 32 * kLoaderWarp0);
+  Pieces pieces;
+  if (!F::kFp4 && warp >= kLoaderWarp0) pieces.place(hr.c, tid - 32 * kLoaderWarp0);
   // The compacting warps' raw entries (kPer each of the row's split, see the
   // compaction below) are loaded before the set-up barrier, so that their
   // memory round trip overlaps the request id's.
@@ -1685,6 +1653,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
     const int d = tid - 32 * kSoftmaxWarps;
     int* list = reinterpret_cast<int*>(sm + kOffList);
     uint8_t* list_shard = sm + kOffListShard;
+    const uint8_t** rows = reinterpret_cast<const uint8_t**>(sm + kOffRows);
     unsigned err = 0;
     bool req_ok = true;
     RowRange range;
@@ -1712,8 +1681,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
         unsigned e1 = 0;
         all = resolve_entry<kMode>(a, ctl, nullptr, false, req_ok, range, e_begin + j, slot, sh, e1) &&
               all;
-        list[j] = slot;
-        list_shard[j] = uint8_t(sh);
+        if constexpr (F::kFp4) {
+          rows[j] = ctl->pool[sh] + int64_t(slot) * F::kRowBytes;
+        } else {
+          list[j] = slot;
+          list_shard[j] = uint8_t(sh);
+        }
       }
       listed = !named_bar_or(3, kListThreads, !all);
       if (listed && d == 0) ctl->n_list = max(cnt, 0);
@@ -1774,8 +1747,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         if (keep & (1u << k)) {
-          list[pos] = vs[k];
-          list_shard[pos] = uint8_t(shards[k]);
+          if constexpr (F::kFp4) {
+            rows[pos] = (kPools ? ctl->pool[shards[k]] : a.kv) + int64_t(vs[k]) * F::kRowBytes;
+          } else {
+            list[pos] = vs[k];
+            list_shard[pos] = uint8_t(shards[k]);
+          }
           ++pos;
         }
       }
