@@ -1925,10 +1925,10 @@ int decode_splits(int32_t T, int32_t K) {
 // 145 a tile of 64 keys, 7 a pair at work on the GPU, and 420 + 12 a split for
 // the kernel that merges splits; the counts it picks are within 4% of the best
 // and 0.1% on average.  Measured against at least 256 entries a split: 1 row
-// of 512 entries 8 splits 13.8 us (2: 16.8), 1 of 2048 16 splits 15.9 (8:
-// 17.3), 16 of 512 4 splits 16.9 (2: 19.0).  Splits that need a second wave
-// gain little or lose (2 against 1: 80 rows of 2048 101.8 us, 105.0; 100 rows
-// 109.9, 105.9).  Like decode_splits
+// of 512 entries 8 splits 12.2 us (2: 15.1), 1 of 2048 16 splits 14.3 (8:
+// 15.5), 16 of 512 4 splits 15.3 (2: 17.0).  Splits that need a second wave
+// gain little or lose (2 against 1: 80 rows of 2048 94.2 us, 99.4; 100 rows
+// 102.6, 100.1).  Like decode_splits
 // a function of the shape alone, with at most `list` entries per split.
 int model_splits(int32_t T, int32_t K, int list) {
   const int lo = (K + list - 1) / list;
@@ -2050,8 +2050,8 @@ cudaError_t launch_impl(const DecodeArgs& args, cudaStream_t s) {
   // The serving step's decodes merge in a second kernel unless the last CTAs
   // can merge behind others' work (more than a wave), or two splits fill most
   // of the GPU, which the second kernel would wait for (rows of 2048 entries,
-  // second kernel against last CTA: 25 rows in 3 splits 32.7 us, 34.5; 19 in 4
-  // 26.6, 30.5; 20 in 2 38.5, 39.2; 34 in 2 40.8, 39.7; 80 in 2 109.8, 101.8).
+  // second kernel against last CTA: 25 rows in 3 splits 29.7 us, 31.4; 19 in 4
+  // 23.7, 27.6; 20 in 2 35.2, 35.9; 34 in 2 37.7, 36.4; 80 in 2 102.0, 94.2).
   const bool last_merges = ctas > sms || (a.splits == 2 && 4 * ctas >= 3 * sms);
   a.combine_in_kernel = overlapped<kMode, F>() ? last_merges : combine_in_kernel(ctas, a.splits, sms);
   if (overlapped<kMode, F>()) {
