@@ -133,8 +133,8 @@ def attend(q, rows, sm_scale, key_step=0.0):
     fp16's step is 2^-24, so each of those fp16 roundings is off by up to
     2^-25 as well: a p against a sum that is at least 1 (a key's p is 2^0
     when it sets the reference), a key (where key_step is not 0) and a
-    partial output.  The kernel holds fp4 rows' keys times 2^-7, which puts
-    a rope value within 2^-18."""
+    partial output.  fp4 rows' codes times scales are exact in fp16; their
+    rope values round as other keys do below 2^-14."""
     H = q.shape[0]
     if len(rows) == 0:
         return np.zeros((H, 512)), np.full(H, -np.inf), np.zeros((H, 512)), np.zeros(H)
@@ -148,7 +148,7 @@ def attend(q, rows, sm_scale, key_step=0.0):
     tiny = 2.0 ** -25
     lse_tol = size.max(axis=1) * (42 * 2.0 ** -23 + key_step) + 2.0 ** -19
     if rows.shape[1] == FP4_ROW_BYTES:
-        lse_tol = lse_tol + sm_scale * np.abs(q[:, 512:]).sum(axis=1) * 2.0 ** -18
+        lse_tol = lse_tol + sm_scale * np.abs(q[:, 512:]).sum(axis=1) * tiny
     if key_step:
         lse_tol = lse_tol + sm_scale * np.abs(q).sum(axis=1) * tiny
     out = p @ lat
