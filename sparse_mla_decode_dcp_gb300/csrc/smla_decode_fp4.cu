@@ -5,7 +5,7 @@
 namespace smla {
 
 size_t fp4_decode_workspace_bytes(int32_t T, int32_t H, int32_t K) {
-  return ws_layout(T, H, model_splits(T, K, kMaxList)).total;
+  return ws_layout(T, H, plan_splits(T, K, kMaxList).splits).total;
 }
 
 cudaError_t launch_decode_fp4(const DecodeArgs& a, cudaStream_t s) {

@@ -1518,12 +1518,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
   const int lane = tid & 31;
   const uint32_t c = cluster_ctarank();
   const uint32_t peer = c ^ 1u;
-  const int64_t item = blockIdx.x >> 1;
-  const int64_t t = item / a.splits;
-  const int split = int(item - t * a.splits);
-  const int per_split = (a.K + a.splits - 1) / a.splits;
-  const int e_begin = split * per_split;
-  const int e_end = min(a.K, e_begin + per_split);
+  const uint32_t item = blockIdx.x >> 1;
+  // serving-step decodes: every row's first split, then every row's second ...
+  const uint32_t inner = overlapped<kMode, F>() ? a.T : a.splits;
+  const uint32_t outer = item / inner;
+  const int64_t t = overlapped<kMode, F>() ? item - outer * inner : outer;
+  const int split = int(overlapped<kMode, F>() ? outer : item - outer * inner);
+  const int e_begin = split * a.split_entries;
+  const int e_end = min(a.K, e_begin + a.split_entries);
 
   const HalfRt hr = half_of(c);
   // a separate split combine (if any) may be scheduled on SMs this grid
@@ -1919,30 +1921,72 @@ int decode_splits(int32_t T, int32_t K) {
   return max(s, 1);
 }
 
-// The serving step's decodes take the split count that ends first by a model
-// of a launch of one wave of pairs, in 1/100 us, fitted to fp4 decodes of 1-64
-// rows of 128-2048 entries (H = 128): 950 for a pair's set-up and epilogue,
-// 145 a tile of 64 keys, 7 a pair at work on the GPU, and 420 + 12 a split for
-// the kernel that merges splits; the counts it picks are within 4% of the best
-// and 0.1% on average.  Measured against at least 256 entries a split: 1 row
-// of 512 entries 8 splits 12.2 us (2: 15.1), 1 of 2048 16 splits 14.3 (8:
-// 15.5), 16 of 512 4 splits 15.3 (2: 17.0).  Splits that need a second wave
-// gain little or lose (2 against 1: 80 rows of 2048 94.2 us, 99.4; 100 rows
-// 102.6, 100.1).  Like decode_splits
-// a function of the shape alone, with at most `list` entries per split.
-int model_splits(int32_t T, int32_t K, int list) {
-  const int lo = (K + list - 1) / list;
-  int best = 1;
-  int64_t best_cost = INT64_MAX;
-  for (int s = 1; T > 0 && int64_t(T) * s <= kClusterSlots && (s - 1) * kTileN < K; ++s) {
-    const int tiles = ((K + s - 1) / s + kTileN - 1) / kTileN;
-    const int64_t cost = 950 + 145 * int64_t(tiles) + 7 * T * s + (s > 1 ? 420 + 12 * s : 0);
+// The serving step's decodes take the splits that end first by a model of a
+// launch, in 1/100 us, like decode_splits a function of the shape alone, with
+// at most `list` entries per split.
+//
+// Within one wave of pairs, fitted to fp4 decodes of 1-64 rows of 128-2048
+// entries (H = 128): 950 for a pair's set-up and epilogue, 145 a tile of 64
+// keys, 7 a pair at work on the GPU, and 420 + 12 a split for the kernel that
+// merges splits; the counts it picks are within 4% of the best and 0.1% on
+// average.  Measured against at least 256 entries a split: 1 row of 512
+// entries 8 splits 12.2 us (2: 15.1), 1 of 2048 16 splits 14.3 (8: 15.5), 16 of
+// 512 4 splits 15.3 (2: 17.0).
+//
+// Past one wave a pair takes 810 (with splits 1100) and 135 a tile, and the
+// places the last wave of large splits leaves free take one small split a row,
+// counted as a tenth longer: 80 rows of 2048 entries 99.6 -> 90 us, 100 rows
+// 100.5 -> 94, 8-bit windows of 4,112 entries, 64 rows, 125.5 -> 121.6 (131
+// with a row's splits one after the other).  110 and 160 rows stay whole (100.7
+// us, 101.4 at best; 150.2, 155.4).
+struct SplitPlan {
+  int splits, entries;  // of a row, and of every split but the last
+};
+
+SplitPlan plan_splits(int32_t T, int32_t K, int list) {
+  const int lo = max((K + list - 1) / list, 1);
+  auto equal = [&](int s) { return SplitPlan{s, max((K + s - 1) / s, 1)}; };
+  if (T <= 0) return equal(lo);
+  if (int64_t(T) * lo <= kClusterSlots) {
+    int best = 1;
+    int64_t best_cost = INT64_MAX;
+    for (int s = 1; int64_t(T) * s <= kClusterSlots && (s - 1) * kTileN < K; ++s) {
+      const int tiles = ((K + s - 1) / s + kTileN - 1) / kTileN;
+      const int64_t cost = 950 + 145 * int64_t(tiles) + 7 * T * s + (s > 1 ? 420 + 12 * s : 0);
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = s;
+      }
+    }
+    return equal(max(best, lo));
+  }
+  // More than a wave: the splits of equal size, or larger ones first and a
+  // small one of each row in the places the last wave leaves free.
+  const int n = (K + kTileN - 1) / kTileN;
+  auto pair = [](int tiles, bool split) { return (split ? 1100 : 810) + 135 * int64_t(tiles); };
+  SplitPlan best = equal(lo);
+  int64_t best_cost = (int64_t(T) * lo + kClusterSlots - 1) / kClusterSlots *
+                      pair((best.entries + kTileN - 1) / kTileN, lo > 1);
+  for (int p = min(list / kTileN, n - 1); p > n / (lo + 1); --p) {
+    const int s = (n + p - 1) / p;
+    const int64_t large = pair(p, true), small = pair(n - (s - 1) * p, true) * 11 / 10;
+    const int64_t count = int64_t(T) * (s - 1);
+    const int64_t waves = count / kClusterSlots;     // full ones
+    const int64_t over = count - waves * kClusterSlots;
+    const int64_t room = kClusterSlots - over;       // places for small splits beside the last large ones
+    const int64_t beside = room * (large / small);
+    const int64_t end = (waves + (over > 0)) * large;
+    const int64_t left = max(T - beside, int64_t(0));
+    const int64_t cost =
+        (lo == 1 ? 500 : 0) +  // rows that were whole are merged
+        max(end, min(waves * large + (T + room - 1) / room * small,
+                     (waves + 1) * large + (left + kClusterSlots - 1) / kClusterSlots * small));
     if (cost < best_cost) {
       best_cost = cost;
-      best = s;
+      best = {s, p * kTileN};
     }
   }
-  return max(best, lo);
+  return best;
 }
 
 struct WsLayout {
@@ -2030,9 +2074,14 @@ cudaError_t launch_impl(const DecodeArgs& args, cudaStream_t s) {
     const cudaError_t e = encode_q_maps(a);
     if (e != cudaSuccess) return e;
   }
-  a.splits = a.single_split          ? 1
-             : overlapped<kMode, F>() ? model_splits(a.T, a.K, kMode == kModeWindow ? kWindowList : kMaxList)
-                                      : decode_splits(a.T, a.K);
+  if (overlapped<kMode, F>()) {
+    const SplitPlan plan = plan_splits(a.T, a.K, kMode == kModeWindow ? kWindowList : kMaxList);
+    a.splits = plan.splits;
+    a.split_entries = plan.entries;
+  } else {
+    a.splits = a.single_split ? 1 : decode_splits(a.T, a.K);
+    a.split_entries = (a.K + a.splits - 1) / a.splits;
+  }
   const WsLayout w = ws_layout(a.T, a.H, a.splits);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   a.ws_o = w.total ? reinterpret_cast<uint16_t*>(ws + w.o_off) : nullptr;

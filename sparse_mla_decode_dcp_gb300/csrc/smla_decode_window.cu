@@ -5,7 +5,7 @@
 namespace smla {
 
 size_t window_decode_workspace_bytes(int32_t T, int32_t H, int32_t K) {
-  return ws_layout(T, H, model_splits(T, K, kWindowList)).total;
+  return ws_layout(T, H, plan_splits(T, K, kWindowList).splits).total;
 }
 
 cudaError_t launch_decode_window(const DecodeArgs& args, bool fp4, cudaStream_t s) {

@@ -62,6 +62,7 @@ struct DecodeArgs {
   size_t workspace_bytes;
   // filled by the launcher from the workspace (split-K partials)
   int32_t splits;
+  int32_t split_entries;  // raw entries of every split of a row but the last
   uint16_t* ws_o;    // [T, splits, H, 512] fp16: each split's O / l (its own softmax average)
   float* ws_ml;      // [T, splits, 2 halves, 2, H]: log2-domain max, then sum
   int32_t* ws_tick;  // [T, 2] arrival counters, left at zero by every call

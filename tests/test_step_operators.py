@@ -684,6 +684,56 @@ def test_window_rows_longer_than_a_pairs_list(cuda_device, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,K", [(77, 2048), (90, 2047), (100, 1985), (153, 2048)])
+def test_fp4_sparse_decode_past_one_wave_of_pairs(cuda_device, T, K):
+    """Rows cut into a large and a small key range; a workspace serves call
+    after call, with the same bits."""
+    dev, H = cuda_device, 5
+    rng = np.random.default_rng(T)
+    cache = _random_cache(700, "fp4", 3, dev)
+    slots = rng.integers(0, 700, (T, K)).astype(np.int32)
+    slots[rng.random((T, K)) < 0.1] = -1
+    slots[7] = -1
+    slots[16, :1900] = -1  # its keys are all in the last range
+    slots[25, 64:] = -1
+    q = _q(T, H, dev, T)
+    ws = capi.alloc_fp4_decode_workspace(T, H, K, dev)
+    _err()
+    out, lse = capi.sparse_mla_decode_fp4(q, cache, _i32(slots, dev), SCALE, workspace=ws)
+    for _ in range(3):
+        out2, lse2 = capi.sparse_mla_decode_fp4(q, cache, _i32(slots, dev), SCALE, workspace=ws)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    assert _err() == 0
+    rows, qf = _np(cache), _f64(q)
+    at = list(range(7, T, 9))
+    _check(out[at], lse[at], [so.attend(qf[t], rows[slots[t][slots[t] >= 0]], SCALE) for t in at])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_long_windows_past_one_wave_of_pairs(cuda_device, fmt):
+    """64 rows of up to 4112 keys, short contexts among them (ranges without
+    a key)."""
+    dev = cuda_device
+    B, S, H, D, bs, window, sinks = 32, 2, 4, 2, 64, 4096, 16
+    ctx = [4300 if b % 3 == 0 else 2 + 130 * b for b in range(B)]
+    pools, tables = _paged(ctx, D, bs, 1, fmt, 8, dev)
+    q = _q(B * S, H, dev, 3)
+    ws = capi.alloc_window_decode_workspace(B * S, H, 4300, window, sinks, D, 1, -1, dev)
+    _err()
+    for _ in range(2):
+        out, lse = capi.dcp_window_mla_decode(q, _i32(ctx, dev), 4300, S, window, sinks, pools, tables, bs,
+                                              SCALE, workspace=ws)
+    assert _err() == 0
+    npools, ntables, qf = [_np(p) for p in pools], [_np(t) for t in tables], _f64(q)
+    at = list(range(0, B * S, 5))
+    refs = [so.attend(qf[t], _rows_at(npools, ntables, t // S, so.window_positions(
+        ctx[t // S] - S + t % S, window, sinks), D, bs, 1), SCALE, 2.0 ** -11 if fmt == "fp8" else 0.0)
+            for t in at]
+    _check(out[at], lse[at], refs)
+
+
+@pytest.mark.gpu
 def test_window_wide_enough_is_the_dense_decode(cuda_device):
     """Two kernels, one definition: both within its bounds."""
     dev = cuda_device
