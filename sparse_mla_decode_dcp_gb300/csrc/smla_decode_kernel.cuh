@@ -1521,7 +1521,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
   const uint32_t item = blockIdx.x >> 1;
   // serving-step decodes: every row's first split, then every row's second ...
   const uint32_t inner = overlapped<kMode, F>() ? a.T : a.splits;
-  const uint32_t outer = item / inner;
+  uint32_t outer = overlapped<kMode, F>() ? 0 : item;
+  if (a.splits > 1) outer = item / inner;
   const int64_t t = overlapped<kMode, F>() ? item - outer * inner : outer;
   const int split = int(overlapped<kMode, F>() ? outer : item - outer * inner);
   const int e_begin = split * a.split_entries;
