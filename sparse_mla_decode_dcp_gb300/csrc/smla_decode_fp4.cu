@@ -1,5 +1,6 @@
 // Sparse decode over the 416-byte fp4 cache: the launchers of the kernel in
 // smla_decode_kernel.cuh for that row format.
+#define SMLA_WAITS_OUT_OF_LINE  // see wait_phase
 #include "smla_decode_kernel.cuh"
 
 namespace smla {

@@ -179,15 +179,16 @@ enum WaitSite : uint32_t {
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 template <bool kCluster>
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                           uint32_t site) {
-  auto probe = [&]() {
-    return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
-  };
-  if (probe()) return true;
+__device__ __forceinline__ bool probe_phase(uint64_t* bar, uint32_t parity) {
+  return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+}
+
+template <bool kCluster>
+__device__ __forceinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                            uint32_t site) {
   const uint64_t t0 = globaltimer_ns();
   uint32_t it = 0;
-  while (!probe()) {
+  while (!probe_phase<kCluster>(bar, parity)) {
     if (*abort) return false;
     if ((++it & 63u) == 0 && globaltimer_ns() - t0 > kWaitNs) {
       atomicOr(&g_decode_error, SMLA_DEVERR_TIMEOUT | (1u << (8 + site)));
@@ -196,6 +197,30 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
     }
   }
   return true;
+}
+
+#ifdef SMLA_WAITS_OUT_OF_LINE
+// The waiting itself as one function, where the including file asks for it:
+// the code of sixteen warps in five roles is smaller by its copies.  Measured
+// both ways: 4-bit decodes 2-3% sooner (four pools 52.2 -> 51.2 us, one rank
+// 29.8 -> 29.0), windows 0.4-1.6%; but dense decode 635 -> 647 us, the 8-bit
+// fused step 61.7 -> 61.8, so those keep the copies.
+template <bool kCluster>
+__noinline__ __device__ bool wait_longer_called(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                uint32_t site) {
+  return wait_longer<kCluster>(bar, parity, abort, site);
+}
+#endif
+
+template <bool kCluster>
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                           uint32_t site) {
+  if (probe_phase<kCluster>(bar, parity)) return true;
+#ifdef SMLA_WAITS_OUT_OF_LINE
+  return wait_longer_called<kCluster>(bar, parity, abort, site);
+#else
+  return wait_longer<kCluster>(bar, parity, abort, site);
+#endif
 }
 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort,

@@ -1,5 +1,6 @@
 // Windowed decode with sinks over either cache: the launcher of the kernel in
 // smla_decode_kernel.cuh for generated rows with a gap.
+#define SMLA_WAITS_OUT_OF_LINE  // see wait_phase
 #include "smla_decode_kernel.cuh"
 
 namespace smla {
