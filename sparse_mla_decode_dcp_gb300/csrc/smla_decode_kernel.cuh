@@ -585,19 +585,20 @@ __device__ void convert_loop(Ctl* ctl, uint8_t* sm, int n, int ntiles, int key, 
 }
 
 // fp4 rows go straight from global memory into registers and from there into
-// the operand stages: with 13 pieces of 16 bytes a half row two threads' worth
-// of registers hold a tile ahead, and the trip through a raw stage (208 of some
-// 1100 wavefronts of shared memory a tile) is saved.  The converter warps take
+// the operand stages: a half row is 13 pieces of 16 bytes, few enough for the
+// converters to hold a tile of them ahead, and the trip through a raw stage
+// (208 of some 1100 wavefronts of shared memory a tile) is saved.  The converter warps take
 // the codes, warp w keys [16 w, 16 w + 16) of a tile: eight lanes read the 128
 // bytes of a key's codes (lane j piece j: dims 32 j .. of the CTA's half, two
 // scale groups), so that a load instruction reads whole lines.  Two more warps
 // take the rope values, four lanes a key.  Against loader warps and a raw
 // stage: 2 rows of 64 entries 7.6 -> 6.5 us, one pool's 32 rows of 2048 (two
 // splits) 32.0 -> 29.9, four pools' 64 rows 55.1 -> 53.6, windows of 1088
-// entries 66.2 -> 63.0.  Two threads a key with 32-byte loads were slower (61
-// us on the four pools), two tiles ahead too (53.5; one 53.1), and so were
-// addresses formed from slot and shard per load (60.8): the list holds the
-// rows' addresses, and each tile's are read a tile early.
+// entries 66.2 -> 63.0.  Slower were two threads a key, 32 bytes of it a load
+// (76 rows of 1024 entries 41.5 us, with loader warps 32.6), two tiles ahead
+// (four pools 53.5 us; one 53.1) and addresses formed from slot and shard at
+// each load (60.8): the list holds the rows' addresses, and each tile's are
+// read a tile early.
 constexpr int kRopeThreads = 64;
 
 struct Fp4Regs {
