@@ -1310,6 +1310,10 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
     // one decision for all softmax warps (the epilogue below uses a named
     // barrier of theirs)
     ok = !named_bar_or(4, R::kSoftmaxThreads, !ok);
+    // this CTA sends nothing more: the peer may leave once it has arrived too
+    // (each waits for that at its very end, behind the stores below)
+    __syncwarp();
+    cluster_arrive_relaxed();
     row_epilogue<F>(a, ctl, C, t, split, ntiles, m_ref, l, tb, quad, g, h, live_warp, ok);
   } else if (warp < R::kMmaWarp) {
     // ------------------------------------------------ dequantise
@@ -1804,12 +1808,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
   if (warp >= kSoftmaxWarps) {
     __syncwarp();
     cluster_wait();
+    cluster_arrive_relaxed();
   }
   tc_fence_before();
   __syncthreads();
-  // A CTA that finished has received everything its peer sends; one that gave
-  // up leaves only after the peer no longer writes into its shared memory.
-  if (ctl->abort) cluster_sync();
+  cluster_wait();  // the peer no longer writes into this CTA's shared memory
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(ctl->tbase, kTmemCols);
