@@ -190,9 +190,12 @@ smla_status smla_dcp_filter_convert_index(
 /*
  * Bytes of caller-owned workspace smla_sparse_mla_decode needs for (T, H,
  * K); 0 means none.  The size follows from the shape alone, so a caller can
- * allocate it once at start-up for its largest batch [P1 Implementation
- * Notes: per-device scratch allocated at initialisation; P2 "FlashInfer
- * sparse-MLA DCP workspace": size derived from tokens x gathered heads].
+ * allocate the workspace once at start-up [P1 Implementation Notes:
+ * per-device scratch allocated at initialisation; P2 "FlashInfer sparse-MLA
+ * DCP workspace": size derived from tokens x gathered heads].  Few rows are
+ * split over more key ranges than many, so a smaller batch may need more than
+ * a larger one: a workspace for batches of several sizes has the largest of
+ * their sizes.
  * Returns 0 for invalid shapes.
  */
 size_t smla_decode_workspace_size(int32_t T, int32_t H, int32_t K);
@@ -222,15 +225,18 @@ size_t smla_decode_workspace_size(int32_t T, int32_t H, int32_t K);
  *               smla_decode_workspace_size(T, H, K) bytes, 256-byte aligned,
  *               zero-filled before its first use (every call, including one
  *               that sets SMLA_DEVERR_TIMEOUT, leaves its arrival counters
- *               zero again); may be NULL when that size is 0.  Calls that
- *               run concurrently need distinct workspaces.
+ *               zero again); may be NULL when that size is 0.  One
+ *               workspace serves calls of any shapes in turn, of this and of
+ *               every other decode that takes one, as long as nothing else
+ *               writes to it in between.  Calls that run concurrently need
+ *               distinct workspaces.
  * When the size is not 0 the rows are split over several key ranges
  * (split-K) and each range's partial (its normalised output in fp16, its
  * maximum and sum in fp32) goes through the workspace.  The
  * partials are merged by their LSE in the decode kernel (the last range of
  * a row to finish merges it) when the decode grid is larger than one wave
- * on the GPU or there are fewer than four ranges per row; otherwise by a
- * second kernel launched on `stream` with programmatic stream
+ * on the GPU or there are fewer than four ranges per row, up to 16,384 rows;
+ * otherwise by a second kernel launched on `stream` with programmatic stream
  * serialisation.  Without split-K the call is a single kernel launch.
  * Errors: INVALID_ARG for null pointers, T < 0, K < 1, H < 1, num_slots < 0,
  * sm_scale not finite and positive, misaligned q/kv_cache/out; UNSUPPORTED
@@ -266,7 +272,7 @@ smla_status smla_sparse_mla_decode(
  * contents, so calls that overlap on the GPU (e.g. on two streams at once)
  * race and must be serialised by the caller.
  */
-#define SMLA_NOALLOC_SCRATCH_BYTES ((size_t)32 << 20)
+#define SMLA_NOALLOC_SCRATCH_BYTES (((size_t)32 << 20) + 131328)
 smla_status smla_sparse_mla_decode_noalloc(
     const uint16_t* q, const uint8_t* kv_cache, int64_t num_slots,
     const int32_t* local_slots, int32_t T, int32_t H, int32_t K,

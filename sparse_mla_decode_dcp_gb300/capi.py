@@ -238,7 +238,7 @@ def sparse_mla_decode(q: torch.Tensor, kv_cache: torch.Tensor, local_slots: torc
     return out, lse
 
 
-NOALLOC_SCRATCH_BYTES = 32 << 20
+NOALLOC_SCRATCH_BYTES = (32 << 20) + 131328
 
 
 def sparse_mla_decode_noalloc(q: torch.Tensor, kv_cache: torch.Tensor, local_slots: torch.Tensor,

@@ -69,7 +69,8 @@ cudaError_t launch_decode_noalloc(const DecodeArgs& args, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // the arrival counters must start at zero; a call that gave up part-way
     // could have left them otherwise
-    e = cudaMemsetAsync(static_cast<uint8_t*>(scratch) + w.tick_off, 0, w.total - w.tick_off, s);
+    const size_t rows = size_t(args.T < kTickRows ? args.T : kTickRows);
+    e = cudaMemsetAsync(scratch, 0, rows * 2 * sizeof(int32_t), s);
     if (e != cudaSuccess) return e;
     a.workspace = scratch;
     a.workspace_bytes = w.total;

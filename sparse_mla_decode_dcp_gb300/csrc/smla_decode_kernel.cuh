@@ -2019,18 +2019,21 @@ SplitPlan plan_splits(int32_t T, int32_t K, int list) {
   return best;
 }
 
+// The arrival counters come first, in a region of one size whatever the shape:
+// a workspace serves calls of any shapes in turn, and no call's partials may
+// lie where another's counters do.  The last 256 bytes are not written, so
+// that a workspace of a call's own size ends in zeros, as it always has.
 struct WsLayout {
-  size_t o_off, ml_off, tick_off, total;
+  size_t o_off, ml_off, total;
 };
 
 WsLayout ws_layout(int32_t T, int32_t H, int32_t S) {
-  WsLayout w{0, 0, 0, 0};
+  WsLayout w{0, 0, 0};
   if (S == 1 || T <= 0) return w;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  w.o_off = 0;
-  w.ml_off = up(size_t(T) * S * H * SMLA_V_DIM * sizeof(uint16_t));
-  w.tick_off = w.ml_off + up(size_t(T) * S * 2 * 2 * H * sizeof(float));
-  w.total = w.tick_off + up(size_t(T) * 2 * sizeof(int32_t));
+  w.o_off = kTickBytes;
+  w.ml_off = w.o_off + up(size_t(T) * S * H * SMLA_V_DIM * sizeof(uint16_t));
+  w.total = w.ml_off + up(size_t(T) * S * 2 * 2 * H * sizeof(float)) + 256;
   return w;
 }
 
@@ -2116,7 +2119,7 @@ cudaError_t launch_impl(const DecodeArgs& args, cudaStream_t s) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   a.ws_o = w.total ? reinterpret_cast<uint16_t*>(ws + w.o_off) : nullptr;
   a.ws_ml = w.total ? reinterpret_cast<float*>(ws + w.ml_off) : nullptr;
-  a.ws_tick = w.total ? reinterpret_cast<int32_t*>(ws + w.tick_off) : nullptr;
+  a.ws_tick = w.total ? reinterpret_cast<int32_t*>(ws) : nullptr;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -2132,7 +2135,8 @@ cudaError_t launch_impl(const DecodeArgs& args, cudaStream_t s) {
   // second kernel against last CTA: 25 rows in 3 splits 29.7 us, 31.4; 19 in 4
   // 23.7, 27.6; 20 in 2 35.2, 35.9; 34 in 2 37.7, 36.4; 80 in 2 102.0, 94.2).
   const bool last_merges = ctas > sms || (a.splits == 2 && 4 * ctas >= 3 * sms);
-  a.combine_in_kernel = overlapped<kMode, F>() ? last_merges : combine_in_kernel(ctas, a.splits, sms);
+  a.combine_in_kernel = a.T <= kTickRows &&  // rows that have counters
+                        (overlapped<kMode, F>() ? last_merges : combine_in_kernel(ctas, a.splits, sms));
   if (overlapped<kMode, F>()) {
     e = launch_overlapped(sparse_mla_decode_kernel<kMode, F>, unsigned(ctas), Roles<F>::kThreads, kSmemBytes, s, a);
   } else {

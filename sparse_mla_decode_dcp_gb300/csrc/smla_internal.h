@@ -65,7 +65,7 @@ struct DecodeArgs {
   int32_t split_entries;  // raw entries of every split of a row but the last
   uint16_t* ws_o;    // [T, splits, H, 512] fp16: each split's O / l (its own softmax average)
   float* ws_ml;      // [T, splits, 2 halves, 2, H]: log2-domain max, then sum
-  int32_t* ws_tick;  // [T, 2] arrival counters, left at zero by every call
+  int32_t* ws_tick;  // [kTickRows, 2] arrival counters, left at zero by every call
   int32_t combine_in_kernel;  // 1: the last split to arrive merges the row; 0: a second kernel
   int32_t single_split;       // set by the caller: no split-K whatever T (needs K <= 2048)
   // Fused DCP step only (D > 0): global top-k ids are converted per shard in
@@ -197,8 +197,12 @@ cudaError_t launch_decode_dense(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_fp4(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_fused_fp4(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_window(const DecodeArgs& a, bool fp4, cudaStream_t s);
+// The split-K workspace begins with two arrival counters for each of up to
+// this many rows; calls with more rows merge their splits in a second kernel.
+constexpr int32_t kTickRows = 16384;
+constexpr size_t kTickBytes = size_t(kTickRows) * 2 * sizeof(int32_t);
 // Library-owned split-K scratch (no allocation by anyone at call time).
-constexpr size_t kNoAllocScratchBytes = size_t(32) << 20;
+constexpr size_t kNoAllocScratchBytes = (size_t(32) << 20) + kTickBytes + 256;
 // compacted entries one decode cluster handles (the key list in its shared
 // memory): a decode without split-K needs K at most this
 constexpr int32_t kDecodeMaxList = 2048;
