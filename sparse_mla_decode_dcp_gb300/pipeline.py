@@ -93,7 +93,10 @@ class DcpServingStep:
     ``run`` brings ``tokens_per_req`` new tokens of every request, writes
     them and attends each token's window and sinks over all D pools.  Both
     take device tensors, launch on one stream and read nothing back: the
-    block tables grow on the device from each rank's free list.
+    block tables grow on the device from each rank's free list.  With a
+    ``stream``, everything runs on it, the constructor's fills too; what the
+    caller passes in is made ready on it, and results are read behind it, by
+    the caller (``stream.wait_stream``).
     ``take_blocks`` then drops the blocks taken since the last call from the
     front of the free lists (it reads their counts, so it synchronises); a
     server that keeps the lengths on the host can do that from them instead.
@@ -114,19 +117,22 @@ class DcpServingStep:
         row = {"fp8": capi.ROW_BYTES, "fp4": capi.FP4_ROW_BYTES}[fmt]
         width = -(-max_ctx // (interleave * dcp)) * interleave
         width = max(1, -(-width // block_size))
-        self.pools = [torch.zeros((blocks_per_rank * block_size, row), dtype=torch.uint8, device=dev)
-                      for _ in range(dcp)]
-        self.block_tables = [torch.full((num_reqs, width), -1, dtype=torch.int32, device=dev)
-                             for _ in range(dcp)]
-        self.free_blocks = [torch.arange(blocks_per_rank, dtype=torch.int32, device=dev)
-                            for _ in range(dcp)]
         T = num_reqs * tokens_per_req
-        self.q_lens = torch.full((num_reqs,), tokens_per_req, dtype=torch.int32, device=dev)
-        self.maps = [capi.alloc_step_maps(num_reqs, T, dev) for _ in range(dcp)]
-        self.out = torch.empty((T, heads, capi.V_DIM), dtype=torch.bfloat16, device=dev)
-        self.lse = torch.empty((T, heads), dtype=torch.float32, device=dev)
-        self.workspace = capi.alloc_window_decode_workspace(T, heads, max_ctx, window, sinks, dcp,
-                                                            interleave, -1, dev)
+        # Allocated and filled on the stream the steps run on (the current one
+        # without a stream), which alone orders the fills before the steps.
+        with torch.cuda.stream(stream):
+            self.pools = [torch.zeros((blocks_per_rank * block_size, row), dtype=torch.uint8, device=dev)
+                          for _ in range(dcp)]
+            self.block_tables = [torch.full((num_reqs, width), -1, dtype=torch.int32, device=dev)
+                                 for _ in range(dcp)]
+            self.free_blocks = [torch.arange(blocks_per_rank, dtype=torch.int32, device=dev)
+                                for _ in range(dcp)]
+            self.q_lens = torch.full((num_reqs,), tokens_per_req, dtype=torch.int32, device=dev)
+            self.maps = [capi.alloc_step_maps(num_reqs, T, dev, stream) for _ in range(dcp)]
+            self.out = torch.empty((T, heads, capi.V_DIM), dtype=torch.bfloat16, device=dev)
+            self.lse = torch.empty((T, heads), dtype=torch.float32, device=dev)
+            self.workspace = capi.alloc_window_decode_workspace(T, heads, max_ctx, window, sinks, dcp,
+                                                                interleave, -1, dev, stream)
         self._taken: List[torch.Tensor] = []
 
     def _append(self, ctx_lens, q_lens, kv, outs):
@@ -156,8 +162,7 @@ class DcpServingStep:
 
     def take_blocks(self):
         """Drop the blocks the last prefill or run took from the free lists."""
-        if self.stream is not None:
-            self.stream.synchronize()
-        for d, taken in enumerate(self._taken):
-            self.free_blocks[d] = self.free_blocks[d][int(taken.item()):]
+        with torch.cuda.stream(self.stream):
+            for d, taken in enumerate(self._taken):
+                self.free_blocks[d] = self.free_blocks[d][int(taken.item()):]
         self._taken = []

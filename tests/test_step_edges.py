@@ -118,3 +118,48 @@ def test_workspace_sizes_hold_the_counters_of_any_call(lib):
             # some count of splits accounts for the whole size
             assert n == 0 or any(n == counters + up(T * s * H * 1024) + up(T * s * H * 16) + 256 for s in range(2, 77))
     assert capi.fp4_decode_workspace_size(38, 128, 2048) > 0
+
+
+# ---------------------------------------------------------------- streams
+def _steps(dev, fmt, stream, ctx, kv, steps):
+    """A prefill and decode steps at once behind the constructor: the results
+    and everything the steps have written."""
+    from sparse_mla_decode_dcp_gb300.pipeline import DcpServingStep
+    step = DcpServingStep(num_reqs=3, tokens_per_req=2, heads=16, dcp=3, block_size=8, blocks_per_rank=20000,
+                          max_ctx=3100, window=2500, sinks=5, fmt=fmt, sm_scale=SCALE, device=dev, stream=stream)
+    step.prefill(ctx, ctx, kv)
+    step.take_blocks()
+    got = []
+    for c, k, q in steps:
+        out, lse = step.run(c, k, q)
+        with torch.cuda.stream(stream):
+            got += [out.clone(), lse.clone()]
+        step.take_blocks()
+    return got + step.block_tables + step.pools
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_serving_step_on_a_stream_behind_a_busy_one(cuda_device, fmt):
+    """Constructed with a stream while the current stream has work queued, and
+    used at once: the same results as on the current stream."""
+    dev = cuda_device
+    ctx = [2400, 1, 33]
+    g = torch.Generator(device=dev).manual_seed(3)
+
+    def rows(n):
+        return torch.randn((n, 576), generator=g, device=dev).to(torch.bfloat16)
+
+    inputs = (_i32(ctx, dev), rows(sum(ctx)),
+              [(_i32([c + 2 * (i + 1) for c in ctx], dev), rows(6), _q(6, 16, dev, i)) for i in range(2)])
+    want = _steps(dev, fmt, None, *inputs)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream(dev)
+    torch.cuda._sleep(400_000_000)  # about 0.2 s on the current stream
+    got = _steps(dev, fmt, s, *inputs)
+    s.synchronize()
+    still_busy = not torch.cuda.current_stream(dev).query()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert still_busy  # nothing of the steps had waited for the current stream
