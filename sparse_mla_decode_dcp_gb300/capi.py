@@ -139,6 +139,14 @@ def _stream_ptr(stream: Optional[torch.cuda.Stream], device) -> int:
     return int(s.cuda_stream)
 
 
+def _new(shape, dtype, dev, stream: Optional[torch.cuda.Stream], zero: bool = False):
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):  # the block belongs to the launching stream
+        return make(shape, dtype=dtype, device=dev)
+
+
 def _need(t: torch.Tensor, name: str, dtype, device):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -194,12 +202,12 @@ def decode_workspace_size(T: int, H: int, K: int) -> int:
     return int(load().smla_decode_workspace_size(T, H, K))
 
 
-def alloc_decode_workspace(T: int, H: int, K: int, device) -> Optional[torch.Tensor]:
-    """Zero-filled workspace for smla_sparse_mla_decode (None if none needed)."""
+def alloc_decode_workspace(T: int, H: int, K: int, device,
+                           stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """Zero-filled workspace for smla_sparse_mla_decode (None if none needed),
+    allocated and filled on `stream` (the current one without)."""
     n = decode_workspace_size(T, H, K)
-    if n == 0:
-        return None
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return _new(n, torch.uint8, device, stream, zero=True) if n else None
 
 
 def sparse_mla_decode(q: torch.Tensor, kv_cache: torch.Tensor, local_slots: torch.Tensor,
@@ -227,7 +235,7 @@ def sparse_mla_decode(q: torch.Tensor, kv_cache: torch.Tensor, local_slots: torc
     _need(out, "out", torch.bfloat16, dev)
     _need(lse, "lse", torch.float32, dev)
     if workspace is None:
-        workspace = alloc_decode_workspace(T, H, K, dev)
+        workspace = alloc_decode_workspace(T, H, K, dev, stream)
     ws_ptr = workspace.data_ptr() if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = load().smla_sparse_mla_decode(
@@ -311,7 +319,7 @@ def dcp_sparse_mla_decode_fused(q: torch.Tensor, req_id_per_token: torch.Tensor,
     _need(out, "out", torch.bfloat16, dev)
     _need(lse, "lse", torch.float32, dev)
     if workspace is None:
-        workspace = alloc_decode_workspace(T, H, K, dev)
+        workspace = alloc_decode_workspace(T, H, K, dev, stream)
     widths = [bt.shape[1] for bt in block_tables] if bt_widths is None else list(bt_widths)
     pools = (ctypes.c_void_p * D)(*[kv.data_ptr() for kv in kv_caches])
     nslots = (ctypes.c_int64 * D)(*[kv.shape[0] for kv in kv_caches])
@@ -390,7 +398,7 @@ def dcp_sparse_mla_decode_fused_host(q_host: torch.Tensor, topk_host: torch.Tens
     _need(out_dev, "out_dev", torch.bfloat16, dev)
     _need(lse_dev, "lse_dev", torch.float32, dev)
     if workspace is None and min(chunks, T) == 1:
-        workspace = alloc_decode_workspace(T, H, K, dev)
+        workspace = alloc_decode_workspace(T, H, K, dev, stream)
     widths = [bt.shape[1] for bt in block_tables] if bt_widths is None else list(bt_widths)
     pools = (ctypes.c_void_p * D)(*[kv.data_ptr() for kv in kv_caches])
     nslots = (ctypes.c_int64 * D)(*[kv.shape[0] for kv in kv_caches])
@@ -452,7 +460,7 @@ def dcp_dense_mla_decode(q: torch.Tensor, ctx_lens: torch.Tensor, max_ctx: int, 
     _need(lse, "lse", torch.float32, dev)
     if workspace is None:
         n = dense_decode_workspace_size(T, H, max_ctx, D, interleave, rank)
-        workspace = torch.zeros(n, dtype=torch.uint8, device=dev) if n else None
+        workspace = _new(n, torch.uint8, dev, stream, zero=True) if n else None
     widths = [0] * D
     for d in used:
         widths[d] = block_tables[d].shape[1] if bt_widths is None else int(bt_widths[d])
@@ -500,7 +508,7 @@ def topk_select(scores: torch.Tensor, n_cand: torch.Tensor, K: int, *, D: int = 
     sc = torch.empty((T, K), dtype=torch.float32, device=dev) if with_scores else None
     if workspace is True:
         need = topk_select_workspace_size(T, L, K) if 1 <= K <= MAX_TOPK else 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        workspace = _new(need, torch.uint8, dev, stream) if need else None
     elif workspace is False:
         workspace = None
     if workspace is not None:
@@ -579,14 +587,6 @@ def _native():
         from . import _smla_torch
         _binding = _smla_torch
     return _binding
-
-
-def _new(shape, dtype, dev, stream: Optional[torch.cuda.Stream], zero: bool = False):
-    make = torch.zeros if zero else torch.empty
-    if stream is None:
-        return make(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):  # the block belongs to the launching stream
-        return make(shape, dtype=dtype, device=dev)
 
 
 def _out_lse(q: torch.Tensor, out, lse, stream):

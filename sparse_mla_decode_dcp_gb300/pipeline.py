@@ -26,20 +26,21 @@ class DcpDecodeStep:
         self.stream = stream
         T, H, K, D = wl.T, wl.H, wl.K, wl.D
         dev = self.device
-        self.q = wl.q.to(dev).contiguous()
-        self.req_id = torch.from_numpy(wl.req_id).to(dev)
-        self.topk = torch.from_numpy(wl.topk).to(dev)
-        self.pools: List[torch.Tensor] = [s.pool.to(dev) for s in wl.shards]
-        self.block_tables = [torch.from_numpy(s.block_table).to(dev) for s in wl.shards]
-        self.bt_widths = [s.width for s in wl.shards]
-        self.local_slots = [torch.empty((T, K), dtype=torch.int32, device=dev) for _ in range(D)]
-        self.valid_count = [torch.empty((T,), dtype=torch.int32, device=dev) for _ in range(D)]
-        self.part_out = [torch.empty((T, H, capi.V_DIM), dtype=torch.bfloat16, device=dev)
-                         for _ in range(D)]
-        self.part_lse = [torch.empty((T, H), dtype=torch.float32, device=dev) for _ in range(D)]
-        self.out = torch.empty((T, H, capi.V_DIM), dtype=torch.bfloat16, device=dev)
-        self.lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-        self.workspace = capi.alloc_decode_workspace(T, H, K, dev)
+        with torch.cuda.stream(stream):  # copied and filled where the step runs
+            self.q = wl.q.to(dev).contiguous()
+            self.req_id = torch.from_numpy(wl.req_id).to(dev)
+            self.topk = torch.from_numpy(wl.topk).to(dev)
+            self.pools: List[torch.Tensor] = [s.pool.to(dev) for s in wl.shards]
+            self.block_tables = [torch.from_numpy(s.block_table).to(dev) for s in wl.shards]
+            self.bt_widths = [s.width for s in wl.shards]
+            self.local_slots = [torch.empty((T, K), dtype=torch.int32, device=dev) for _ in range(D)]
+            self.valid_count = [torch.empty((T,), dtype=torch.int32, device=dev) for _ in range(D)]
+            self.part_out = [torch.empty((T, H, capi.V_DIM), dtype=torch.bfloat16, device=dev)
+                             for _ in range(D)]
+            self.part_lse = [torch.empty((T, H), dtype=torch.float32, device=dev) for _ in range(D)]
+            self.out = torch.empty((T, H, capi.V_DIM), dtype=torch.bfloat16, device=dev)
+            self.lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+            self.workspace = capi.alloc_decode_workspace(T, H, K, dev, stream)
 
     @property
     def launches_per_step(self) -> int:

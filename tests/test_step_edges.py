@@ -163,3 +163,56 @@ def test_serving_step_on_a_stream_behind_a_busy_one(cuda_device, fmt):
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     assert still_busy  # nothing of the steps had waited for the current stream
+
+
+@pytest.mark.gpu
+def test_decodes_on_a_stream_with_their_own_workspace(cuda_device):
+    """Workspaces that a call allocates for itself are filled, and belong to,
+    the stream it launches on, while the current stream is busy."""
+    dev = cuda_device
+    ctx, H = [2300, 60, 2300], 16
+    pools, tables = _paged(ctx, 1, 16, 1, "fp8", 3, dev)
+    q, c, req = _q(3, H, dev), _i32(ctx, dev), _i32(range(3), dev)
+    ids = _i32(np.stack([np.random.default_rng(b).permutation(2048) % n for b, n in enumerate(ctx)]), dev)
+    scores = torch.randn((2, 1 << 18), generator=torch.Generator(device=dev).manual_seed(1), device=dev)
+    n_cand = _i32([1 << 18, 200000], dev)
+    cache4 = _random_cache(2400, "fp4", 1, dev)
+    calls = [
+        lambda **k: capi.sparse_mla_decode(q, pools[0], ids, SCALE, **k),
+        lambda **k: capi.dcp_sparse_mla_decode_fused(q, req, ids, pools, tables, 16, SCALE, **k),
+        lambda **k: capi.dcp_dense_mla_decode(q, c, 2300, 1, pools, tables, 16, SCALE, **k),
+        lambda **k: capi.sparse_mla_decode_fp4(q, cache4, ids, SCALE, **k),
+    ]
+    want = [call() for call in calls]
+    top = capi.topk_select(scores, n_cand, 64, workspace=True)
+    outs = [(torch.empty_like(o), torch.empty_like(l)) for o, l in want]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream(dev)
+    torch.cuda._sleep(200_000_000)
+    noise = []
+    for call, (o, l) in zip(calls, outs):
+        call(out=o, lse=l, stream=s)
+        noise.append(torch.full((4 << 20,), 255, dtype=torch.uint8, device=dev))  # a reused block would show
+    got = capi.topk_select(scores, n_cand, 64, workspace=True, stream=s)
+    torch.cuda.synchronize()
+    for (o, l), (wo, wl) in zip(outs, want):  # bit by bit: slots nobody holds give NaN
+        assert torch.equal(o.view(torch.int16), wo.view(torch.int16))
+        assert torch.equal(l.view(torch.int32), wl.view(torch.int32))
+    assert torch.equal(got, top)
+
+
+@pytest.mark.gpu
+def test_decode_step_on_a_stream_behind_a_busy_one(cuda_device):
+    from sparse_mla_decode_dcp_gb300 import inputs
+    from sparse_mla_decode_dcp_gb300.pipeline import DcpDecodeStep
+    dev = cuda_device
+    wl = inputs.make_workload("tiny", seed=0, device=dev)
+    want = [t.clone() for t in DcpDecodeStep(wl, device=dev).run()]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream(dev)
+    torch.cuda._sleep(200_000_000)
+    got = DcpDecodeStep(wl, device=dev, stream=s).run()
+    s.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    torch.cuda.synchronize()
