@@ -621,10 +621,11 @@ smla_status smla_dcp_step_maps(
  *            32 + j] for pair j (cos_sin NULL: copied as it is); pair j is
  *            values (2j, 2j + 1) when rope_pairs != 0, else (j, j + 32)
  * Scales and codes are rounded once, from the quotients above computed to
- * about 45 bits; a group whose scale is 0 (fp8: or below 2^-126) has zero
- * codes.  A group with a value that is not finite, and every group of a
- * normalised row with a latent that is not finite or a sum of squares past
- * fp32, gets a NaN scale.  Rows with slot -1 write nothing; the slots of one
+ * about 45 bits (with a norm, where mean(x^2) + eps is at least 2^-100); a
+ * group whose scale is 0 (fp8: or below 2^-126) has zero codes.  A group with
+ * a value y that is not finite in fp32, and every group of a normalised row
+ * with a latent that is not finite or a sum of squares past fp32, gets a NaN
+ * scale.  Rows with slot -1 write nothing; the slots of one
  * call are distinct (a slot given twice ends with an undefined mix of its
  * rows).
  *

@@ -216,3 +216,92 @@ def test_decode_step_on_a_stream_behind_a_busy_one(cuda_device):
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------ ends of fp32
+def _fp8_rows(y):
+    """Codes and scales of float64 latents y as the header defines them: a
+    group whose scale is below 2^-126 is stored as zeros."""
+    code, scale = so.quantise_fp8(y)
+    low = scale < 2.0 ** -126
+    return np.where(np.repeat(low, 128, axis=1), 0, code), np.where(low, np.float32(0), scale)
+
+
+def _write_latents(x, gamma, fmt, eps=1e-6):
+    dev = x.device
+    kv = torch.cat([x, torch.zeros((x.shape[0], 64), dtype=x.dtype, device=dev)], 1).contiguous()
+    cache = torch.full((x.shape[0], FORMATS[fmt]), 0x5A, dtype=torch.uint8, device=dev)
+    capi.mla_cache_write(kv, torch.arange(x.shape[0], dtype=torch.int32, device=dev), cache, gamma=gamma, eps=eps)
+    return _np(cache)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rms", [2.0 ** -40, 2.0 ** -10, 1.0, 2.0 ** 40])
+def test_write_tiny_groups(cuda_device, rms):
+    """Groups of a normalised row from ordinary size down to below the least
+    scale, exact zeros among their values, by small gammas and small latents."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(7)
+    T = 40
+    x = torch.randn((T, 512), generator=g, dtype=torch.float64)
+    x[:, 5::37] = 0
+    x = (x * rms).to(torch.bfloat16)
+    steps = torch.arange(T * 4, dtype=torch.float64).view(T, 4) * -0.85  # 2^0 .. 2^-135 in all
+    for t in range(T):
+        row = (1 + 0.3 * torch.randn(512, generator=g, dtype=torch.float64))
+        gamma = (row * torch.exp2(steps[t]).repeat_interleave(128)).to(torch.bfloat16)
+        got = _write_latents(x[t:t + 1].to(dev), gamma.to(dev), "fp8", eps=1e-30)
+        y = so.normalise(_f64(x[t:t + 1]), _f64(gamma), 1e-30)
+        code, scale = _fp8_rows(y)
+        assert np.array_equal(got[:, 512:528].copy().view("<f4"), scale), t
+        assert np.array_equal(got[:, :512], code), t
+
+
+@pytest.mark.gpu
+def test_write_tiny_latents(cuda_device):
+    """The same from the latents' side: groups of one row far apart, with and
+    without a norm."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(8)
+    T = 160
+    x = torch.randn((T, 4, 128), generator=g, dtype=torch.float64)
+    x[:, :, 3::29] = 0
+    x[:, 1] *= torch.exp2(-torch.arange(T, dtype=torch.float64)[:, None] * 0.85)
+    x[:, 2] *= 2.0 ** -100
+    x[:, 3] *= 2.0 ** -60
+    x = x.view(T, 512).to(torch.bfloat16)
+    gamma = torch.full((512,), 1.25, dtype=torch.bfloat16)
+    gamma[400:] = 2.0 ** -55
+    for gm in (None, gamma):
+        got = _write_latents(x.to(dev), None if gm is None else gm.to(dev), "fp8")
+        y = so.normalise(_f64(x), None if gm is None else _f64(gm), 1e-6)
+        code, scale = _fp8_rows(y)
+        assert np.array_equal(got[:, 512:528].copy().view("<f4"), scale)
+        assert np.array_equal(got[:, :512], code)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_write_past_fp32(cuda_device, fmt):
+    """A normalised value past fp32 makes its group's scale NaN, as an
+    infinite one does; the row's other groups are as they are."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn((8, 512), generator=g, dtype=torch.float64) * 0.01
+    x[:, 37] = 0.5  # 50 times the others: 2^127 times its norm does not fit
+    x = x.to(torch.bfloat16)
+    gamma = torch.ones(512, dtype=torch.bfloat16)
+    gamma[:128] = 2.0 ** 127
+    gamma[0:16] = 2.0 ** 100
+    got = _write_latents(x.to(dev), gamma.to(dev), fmt)
+    y = so.normalise(_f64(x), _f64(gamma), 1e-6)
+    assert (np.abs(y) > np.finfo(np.float32).max).any(axis=1).all()
+    with np.errstate(invalid="ignore"):
+        lat = so.parse(got)[0]
+    size = 128 if fmt == "fp8" else 16
+    past = np.repeat((np.abs(y) > np.finfo(np.float32).max).reshape(8, -1, size).any(axis=2), size, axis=1)
+    assert np.array_equal(np.isnan(lat), past)
+    if fmt == "fp8":
+        code, scale = _fp8_rows(np.where(past, 0, y))
+        assert np.array_equal(got[:, :512][~past], code[~past])
+        assert np.array_equal(got[:, 512:528].copy().view("<f4")[:, 1:], scale[:, 1:])
