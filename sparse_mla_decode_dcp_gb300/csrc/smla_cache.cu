@@ -185,6 +185,12 @@ __device__ __forceinline__ void quantise(const F2* y, Pair r, float d, float inv
   }
 }
 
+// A plain load, not through the read-only path (see launch_overlapped).
+template <class T>
+__device__ __forceinline__ T load(const T* p) {
+  return *p;
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -270,8 +276,8 @@ __global__ void __launch_bounds__(kWarps * 32, 5) cache_write_kernel(const Cache
   griddep_launch_dependents();
   if (t >= a.T) return;
   griddep_wait();
-  const int32_t slot = __ldg(a.slots + t);
-  const int32_t pos = a.cos_sin ? __ldg(a.positions + t) : 0;
+  const int32_t slot = load(a.slots + t);
+  const int32_t pos = a.cos_sin ? load(a.positions + t) : 0;
   if (slot < 0) return;
   const bool bad_slot = slot >= a.num_slots;
   const bool bad_pos = a.cos_sin && (pos < 0 || pos >= a.num_positions);
@@ -287,8 +293,8 @@ __global__ void __launch_bounds__(kWarps * 32, 5) cache_write_kernel(const Cache
   // every load of the row first
   uint32_t x[8], g[8];
   {
-    const uint4 v0 = __ldg(reinterpret_cast<const uint4*>(src) + 2 * lane);
-    const uint4 v1 = __ldg(reinterpret_cast<const uint4*>(src) + 2 * lane + 1);
+    const uint4 v0 = load(reinterpret_cast<const uint4*>(src) + 2 * lane);
+    const uint4 v1 = load(reinterpret_cast<const uint4*>(src) + 2 * lane + 1);
     x[0] = v0.x, x[1] = v0.y, x[2] = v0.z, x[3] = v0.w;
     x[4] = v1.x, x[5] = v1.y, x[6] = v1.z, x[7] = v1.w;
   }
@@ -296,17 +302,17 @@ __global__ void __launch_bounds__(kWarps * 32, 5) cache_write_kernel(const Cache
   const uint16_t* zs = src + SMLA_V_DIM;
   uint32_t z;
   if (a.rope_pairs)
-    z = __ldg(reinterpret_cast<const uint32_t*>(zs) + lane);
+    z = load(reinterpret_cast<const uint32_t*>(zs) + lane);
   else
-    z = uint32_t(__ldg(zs + lane)) | uint32_t(__ldg(zs + 32 + lane)) << 16;
+    z = uint32_t(load(zs + lane)) | uint32_t(load(zs + 32 + lane)) << 16;
   float co = 1.f, si = 0.f;
   if (a.cos_sin) {
-    co = __ldg(a.cos_sin + int64_t(pos) * 64 + lane);
-    si = __ldg(a.cos_sin + int64_t(pos) * 64 + 32 + lane);
+    co = load(a.cos_sin + int64_t(pos) * 64 + lane);
+    si = load(a.cos_sin + int64_t(pos) * 64 + 32 + lane);
   }
   if (a.gamma) {
-    const uint4 v0 = __ldg(reinterpret_cast<const uint4*>(a.gamma) + 2 * lane);
-    const uint4 v1 = __ldg(reinterpret_cast<const uint4*>(a.gamma) + 2 * lane + 1);
+    const uint4 v0 = load(reinterpret_cast<const uint4*>(a.gamma) + 2 * lane);
+    const uint4 v1 = load(reinterpret_cast<const uint4*>(a.gamma) + 2 * lane + 1);
     g[0] = v0.x, g[1] = v0.y, g[2] = v0.z, g[3] = v0.w;
     g[4] = v1.x, g[5] = v1.y, g[6] = v1.z, g[7] = v1.w;
   }
@@ -435,7 +441,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache_gather_kernel(const CacheGa
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    slot[i] = n0 + i < a.N ? __ldg(a.slots + n0 + i) : -1;
+    slot[i] = n0 + i < a.N ? load(a.slots + n0 + i) : -1;
     if (slot[i] >= a.num_slots) {
       bad = true;
       slot[i] = -1;
@@ -455,15 +461,15 @@ __global__ void __launch_bounds__(kWarps * 32) cache_gather_kernel(const CacheGa
       for (int h = 0; h < 2; ++h) {
         const uint8_t* p = src + kCodeBytes * (32 * h + lane);
         if (kFp4) {
-          code[i][h].x = __ldg(reinterpret_cast<const uint32_t*>(p));
+          code[i][h].x = load(reinterpret_cast<const uint32_t*>(p));
           scale[i][h] = __half2float(
-              __half(__nv_cvt_fp8_to_halfraw(__ldg(src + 256 + 16 * h + (lane >> 1)), __NV_E4M3)));
+              __half(__nv_cvt_fp8_to_halfraw(load(src + 256 + 16 * h + (lane >> 1)), __NV_E4M3)));
         } else {
-          code[i][h] = __ldg(reinterpret_cast<const uint2*>(p));
-          scale[i][h] = __ldg(reinterpret_cast<const float*>(src + 512) + 2 * h + (lane >> 4));
+          code[i][h] = load(reinterpret_cast<const uint2*>(p));
+          scale[i][h] = load(reinterpret_cast<const float*>(src + 512) + 2 * h + (lane >> 4));
         }
       }
-      rope[i] = __ldg(reinterpret_cast<const uint32_t*>(src + kRope) + lane);
+      rope[i] = load(reinterpret_cast<const uint32_t*>(src + kRope) + lane);
     }
   }
 #pragma unroll

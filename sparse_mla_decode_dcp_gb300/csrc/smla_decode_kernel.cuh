@@ -625,7 +625,7 @@ __device__ void convert_codes(Ctl* ctl, uint8_t* sm, int n, int ntiles, int c, i
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       r.code[i] = row[i] ? ldg_stream(row[i] + 128 * c + 16 * j) : make_uint4(0, 0, 0, 0);
-      r.scale[i] = row[i] ? __ldg(reinterpret_cast<const uint16_t*>(row[i] + 256 + 16 * c) + j) : 0;
+      r.scale[i] = row[i] ? reinterpret_cast<const uint16_t*>(row[i] + 256 + 16 * c)[j] : 0;
     }
     place(tile + 1);
   };
@@ -1445,7 +1445,7 @@ __device__ __forceinline__ bool resolve_entry(const DecodeArgs& a, const Ctl* ct
   const int32_t col = int32_t(fastdiv(uint32_t(lp), a.div_bs));
   const bool in_table = col < m.bt_width;
   const int32_t colc = in_table ? col : 0;  // every table has a column 0
-  const int32_t blk = staged ? bt[m.bt_off + colc] : __ldg(ctl->bt_row[d] + colc);
+  const int32_t blk = staged ? bt[m.bt_off + colc] : ctl->bt_row[d][colc];
   const int64_t s64 = int64_t(blk) * a.block_size + (lp - col * a.block_size);
   const bool in_pool = s64 < m.pool_slots;
   err |= (live && (!in_table || blk < 0)) ? unsigned(SMLA_DEVERR_BLOCK_TABLE) : 0u;
@@ -1630,7 +1630,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
     if (j0 + kPer <= e_end && (reinterpret_cast<uintptr_t>(src + j0) & 15u) == 0) {
 #pragma unroll
       for (int q4 = 0; q4 < kPer / 4; ++q4) {
-        const int4 w = __ldg(reinterpret_cast<const int4*>(src + j0) + q4);
+        const int4 w = reinterpret_cast<const int4*>(src + j0)[q4];
         vs[4 * q4] = w.x;
         vs[4 * q4 + 1] = w.y;
         vs[4 * q4 + 2] = w.z;
@@ -1638,7 +1638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) vs[k] = (j0 + k < e_end) ? __ldg(src + j0 + k) : -1;
+      for (int k = 0; k < kPer; ++k) vs[k] = (j0 + k < e_end) ? src[j0 + k] : -1;
     }
   }
   if (kPools && tid < a.D) {

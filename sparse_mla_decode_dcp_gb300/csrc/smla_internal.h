@@ -166,7 +166,9 @@ struct MergeArgs {
 // signalled (griddep_launch_dependents) or exited, so that its launch
 // overlaps that kernel's end; griddep_wait then holds it until that kernel
 // has completed and its writes are visible.  Every such kernel waits before
-// it touches global memory.
+// it touches global memory, and reads it by plain loads, never through the
+// read-only path (__ldg, ld.global.nc): that is for memory nobody writes while
+// the kernel runs, and this one runs from before the other's end.
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

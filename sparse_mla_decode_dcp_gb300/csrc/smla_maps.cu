@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapsArgs a) {
         } else if (col >= sp.old_blocks) {
           const int64_t f = int64_t(sp.first_free) + (col - sp.old_blocks);
           if (f < a.num_free)
-            blk = __ldg(a.free_blocks + f);
+            blk = a.free_blocks[f];
           else
             err |= SMLA_DEVERR_FREE_BLOCKS;
           if (at == 0) *entry = blk;

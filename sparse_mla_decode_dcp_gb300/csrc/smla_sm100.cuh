@@ -146,11 +146,12 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
   return v;
 }
 
-// 16-byte read-only global load that does not allocate in L1 (streamed
-// data read once).
+// 16-byte global load that does not allocate in L1 (streamed data read once).
+// Not the read-only form: the cache rows may have been written by the kernel
+// before this one on the stream while this one was already starting.
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }

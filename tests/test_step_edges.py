@@ -305,3 +305,63 @@ def test_write_past_fp32(cuda_device, fmt):
         code, scale = _fp8_rows(np.where(past, 0, y))
         assert np.array_equal(got[:, :512][~past], code[~past])
         assert np.array_equal(got[:, 512:528].copy().view("<f4")[:, 1:], scale[:, 1:])
+
+
+# ------------------------------------------------- overlapping launches
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_rows_overwritten_and_read_again_without_a_wait(cuda_device, fmt):
+    """Step maps, cache write, gather and decodes in one chain of overlapping
+    launches, over and over on the same slots with other rows, other tables
+    and other lists each time: every reader sees what the writer before it
+    wrote, as when the host waits in between."""
+    dev = cuda_device
+    B, H, bs, n, rounds = 4, 16, 16, 70, 24
+    N = B * n
+    g = torch.Generator(device=dev).manual_seed(2)
+    kv = [torch.randn((N, 576), generator=g, device=dev).to(torch.bfloat16) for _ in range(rounds)]
+    free = [torch.randperm(B * 5, generator=g, device=dev).to(torch.int32) for _ in range(rounds)]
+    ctx, ql = _i32([n] * B, dev), _i32([n] * B, dev)
+    req, topk = _i32(range(B), dev), _i32([list(range(n))] * B, dev)
+    cos_sin, q = torch.rand((n, 64), generator=g, device=dev), _q(B, H, dev)
+    cache = torch.zeros((B * 5 * bs, FORMATS[fmt]), dtype=torch.uint8, device=dev)
+    table = torch.full((B, 5), -1, dtype=torch.int32, device=dev)
+    maps = capi.alloc_step_maps(B, N, dev)
+    ws = [capi.alloc_window_decode_workspace(B, H, n, n, 0, 1, 1, -1, dev),
+          capi.alloc_fp4_decode_workspace(B, H, n, dev)]
+
+    def outs():
+        return (torch.empty((N, 576), dtype=torch.bfloat16, device=dev),
+                *(torch.empty(s, dtype=t, device=dev) for _ in range(2)
+                  for s, t in (((B, H, 512), torch.bfloat16), ((B, H), torch.float32))))
+
+    def chain(i, o, wait):
+        capi.dcp_step_maps(ctx, ql, free[i], table, N, 1, 0, bs, out=maps)
+        wait()
+        capi.mla_cache_write(kv[i], maps.slots, cache, positions=maps.positions, cos_sin=cos_sin)
+        wait()
+        capi.mla_cache_gather(cache, maps.slots, out=o[0])
+        wait()
+        capi.dcp_window_mla_decode(q, ctx, n, 1, n, 0, [cache], [table], bs, SCALE, out=o[1], lse=o[2],
+                                   workspace=ws[0])
+        wait()
+        if fmt == "fp4":
+            capi.dcp_sparse_mla_decode_fused_fp4(q, req, topk, [cache], [table], bs, SCALE, out=o[3], lse=o[4],
+                                                 workspace=ws[1])
+        else:
+            o[3].zero_()
+            o[4].zero_()
+        wait()
+
+    got, want = [outs() for _ in range(rounds)], [outs() for _ in range(rounds)]
+    _err()
+    for i in range(rounds):
+        chain(i, want[i], torch.cuda.synchronize)
+    for i in range(rounds):
+        chain(i, got[i], lambda: None)
+    torch.cuda.synchronize()
+    assert _err() == 0
+    for i in range(rounds):
+        for a, b in zip(got[i], want[i]):
+            assert torch.equal(a, b), i
+    assert not torch.equal(want[0][1], want[1][1])
