@@ -21,6 +21,8 @@
 // 3.8 us.  Up to there a launch's own latency and, past 256 requests, one more
 // scan bound it; 8,192 requests take 32 scans and 19 us, little beside the
 // attention of as many requests.
+#include <atomic>
+
 #include "../../include/smla.h"
 #include "smla_internal.h"
 
@@ -189,6 +191,24 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapsArgs a) {
 
 }  // namespace
 
+// The kernel's shared-memory limit, once per device and for the largest batch:
+// a limit set for each launch's own batch would be lowered by another host
+// thread between the setting and the launch.
+static cudaError_t allow_all_spans() {
+  constexpr int kDevices = 64;
+  constexpr int kBytes = SMLA_MAX_STEP_REQS * int(sizeof(ReqSpan));
+  static_assert(kBytes <= 227 * 1024 - 4096, "spans fit shared memory");
+  static std::atomic<bool> done[kDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool tracked = dev >= 0 && dev < kDevices;
+  if (tracked && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(step_maps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (e == cudaSuccess && tracked) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
 cudaError_t launch_step_maps(const MapsArgs& args, cudaStream_t s) {
   MapsArgs a = args;
   a.div_I = make_fastdiv(uint32_t(a.interleave));
@@ -198,10 +218,8 @@ cudaError_t launch_step_maps(const MapsArgs& args, cudaStream_t s) {
   const uint64_t round = uint64_t(a.interleave) * uint32_t(a.D);
   a.div_ID = make_fastdiv(uint32_t(round > (1ull << 31) ? (1ull << 31) : round));
   const size_t smem = size_t(a.B) * sizeof(ReqSpan);
-  static_assert(SMLA_MAX_STEP_REQS * sizeof(ReqSpan) <= 227 * 1024 - 4096, "spans fit shared memory");
   if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        step_maps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const cudaError_t e = allow_all_spans();
     if (e != cudaSuccess) return e;
   }
   const int64_t need = (int64_t(a.T) + kThreads - 1) / kThreads;

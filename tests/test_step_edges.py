@@ -365,3 +365,35 @@ def test_rows_overwritten_and_read_again_without_a_wait(cuda_device, fmt):
         for a, b in zip(got[i], want[i]):
             assert torch.equal(a, b), i
     assert not torch.equal(want[0][1], want[1][1])
+
+
+# ------------------------------------------------------------ host threads
+@pytest.mark.gpu
+def test_step_maps_from_host_threads_with_large_batches(cuda_device):
+    """Batches that need different amounts of shared memory, from several host
+    threads and streams: no launch is refused, and every map is right."""
+    dev = cuda_device
+    failed = []
+
+    def work(B, rounds):
+        try:
+            s = torch.cuda.Stream(dev)
+            with torch.cuda.stream(s):
+                ctx, ql = _i32([5] * B, dev), _i32([1] * B, dev)
+                free, bt = _i32(range(B), dev), _i32([[7]] * B, dev)
+                out = capi.alloc_step_maps(B, B, dev, s)
+                want = _i32([7 * 8 + 4] * B, dev)
+                for _ in range(rounds):
+                    capi.dcp_step_maps(ctx, ql, free, bt, B, 1, 0, 8, out=out, stream=s)
+                s.synchronize()
+                assert torch.equal(out.slots, want)
+        except Exception as e:  # noqa: BLE001
+            failed.append((B, e))
+
+    threads = [threading.Thread(target=work, args=(B, 4000)) for B in (8192, 3000, 5000, 100)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    assert _err() == 0
