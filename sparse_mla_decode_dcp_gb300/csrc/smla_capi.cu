@@ -15,8 +15,12 @@ inline bool misaligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) != 0;
 }
 
+// A call's status.  A failed call also clears the error that the runtime keeps
+// for the thread: the next call's launch asks for it and would report this one.
 inline smla_status from_cuda(cudaError_t e) {
-  return e == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+  if (e == cudaSuccess) return SMLA_OK;
+  cudaGetLastError();
+  return SMLA_ERR_CUDA;
 }
 
 }  // namespace

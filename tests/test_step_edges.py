@@ -397,3 +397,44 @@ def test_step_maps_from_host_threads_with_large_batches(cuda_device):
         t.join()
     assert not failed
     assert _err() == 0
+
+
+# ---------------------------------------------------------- refused launches
+@pytest.mark.gpu
+def test_a_refused_launch_is_reported_once(cuda_device):
+    """A launch refused on the host (on a stream whose capture has become
+    invalid) fails its own call and no later one."""
+    dev = cuda_device
+    drv = ctypes.CDLL("libcuda.so.1")
+    handle = ctypes.c_void_p
+    cache = _random_cache(8, "fp4", 1, dev)
+    slots, out = _i32(range(8), dev), torch.empty((8, 576), dtype=torch.bfloat16, device=dev)
+    ids, table = _i32([[0, 5, 3, -1]], dev), _i32([[1]], dev)
+    req = _i32([0], dev)
+    ctx, ql, free, maps = _i32([8], dev), _i32([0], dev), _i32([], dev), capi.alloc_step_maps(1, 1, dev)
+    q = _q(1, 4, dev)
+    o, l = torch.empty((1, 4, 512), dtype=torch.bfloat16, device=dev), torch.empty((1, 4), device=dev)
+
+    def healthy():
+        return capi.dcp_filter_convert_index(req, table, ids, 1, 0, 8)[0]
+
+    want = healthy()
+    capi.mla_cache_gather(cache, slots, out=out)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream(dev)
+    for call in (lambda: capi.mla_cache_gather(cache, slots, out=out, stream=s),
+                 lambda: capi.dcp_step_maps(ctx, ql, free, table, 1, 1, 0, 8, out=maps, stream=s),
+                 lambda: capi.sparse_mla_decode_fp4(q, cache, ids, SCALE, out=o, lse=l, stream=s)):
+        st = handle(s.cuda_stream)
+        assert drv.cuStreamBeginCapture_v2(st, 2) == 0  # of this stream alone
+        assert drv.cuStreamSynchronize(st) != 0  # not allowed in a capture: it is invalid from here on
+        with pytest.raises(capi.SmlaError):
+            call()
+        got = healthy()
+        graph = handle()
+        assert drv.cuStreamEndCapture(st, ctypes.byref(graph)) != 0
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    capi.mla_cache_gather(cache, slots, out=out, stream=s)  # and the stream works again
+    torch.cuda.synchronize()
+    assert _err() == 0
