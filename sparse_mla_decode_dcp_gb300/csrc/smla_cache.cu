@@ -425,6 +425,16 @@ __device__ __forceinline__ void e4m3x2(uint32_t c, float& a, float& b) {
   b = __high2float(h);
 }
 
+// c s, rounded to fp32, or (kOdd, where bf16 follows) rounded to odd, so that
+// the rounding to bf16 is of the product itself: the product is exact, or lies
+// between two neighbouring fp32 of which one has an odd last bit.
+template <bool kOdd>
+__device__ __forceinline__ float times(float c, float s) {
+  if (!kOdd) return __fmul_rn(c, s);
+  const float lo = __fmul_rd(c, s), hi = __fmul_ru(c, s);
+  return (__float_as_uint(lo) & 1u) ? lo : hi;
+}
+
 constexpr int kRows = 4;
 
 template <bool kFp4, bool kFp32>
@@ -492,8 +502,8 @@ __global__ void __launch_bounds__(kWarps * 32) cache_gather_kernel(const CacheGa
         for (int k = 0; k < 4; ++k) {
           const uint32_t w = k < 2 ? code[i][h].x : code[i][h].y;
           e4m3x2(w >> (16 * (k & 1)), v[2 * k], v[2 * k + 1]);
-          v[2 * k] *= scale[i][h];
-          v[2 * k + 1] *= scale[i][h];
+          v[2 * k] = times<!kFp32>(v[2 * k], scale[i][h]);
+          v[2 * k + 1] = times<!kFp32>(v[2 * k + 1], scale[i][h]);
         }
       }
       store8<kFp32>(a.out, row + 256 * h + 8 * lane, v);

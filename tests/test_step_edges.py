@@ -438,3 +438,36 @@ def test_a_refused_launch_is_reported_once(cuda_device):
     capi.mla_cache_gather(cache, slots, out=out, stream=s)  # and the stream works again
     torch.cuda.synchronize()
     assert _err() == 0
+
+
+# ---------------------------------------------------------------- rounding
+def _bf16_once(x):
+    """float64 to bf16 (as float64), one rounding, ties to even (normal values)."""
+    m, e = np.frexp(x)
+    return np.ldexp(np.rint(m * 256.0) / 256.0, e)
+
+
+@pytest.mark.gpu
+def test_gather_of_8_bit_rows_rounds_to_bf16_once(cuda_device):
+    """Scales whose products with a code lie so close to the middle of two
+    bf16 that fp32 would round them onto it."""
+    dev = cuda_device
+    rng = np.random.default_rng(4)
+    # e4m3 codes 1.875, 1.625, 1.125 and their multiples by powers of two
+    codes = np.array([0x3F, 0x3D, 0x39, 0xBF, 0x47, 0x35], dtype=np.uint8)
+    value = np.array([1.875, 1.625, 1.125, -1.875, 3.75, 0.8125])
+    n = 6000
+    at = rng.integers(0, len(codes), (n, 4))
+    middle = (rng.integers(128, 256, (n, 4)) + 0.5) * 2.0 ** rng.integers(-20, 10, (n, 4))
+    scale = (middle / np.abs(value[at])).astype(np.float32)
+    rows = np.zeros((n, 656), dtype=np.uint8)
+    rows[:, :512] = np.repeat(codes[at], 128, axis=1)
+    rows[:, 512:528] = scale.view(np.uint8).reshape(n, 16)
+    got = capi.mla_cache_gather(torch.from_numpy(rows).to(dev), _i32(range(n), dev))
+    exact = value[at] * scale.astype(np.float64)  # 4 + 24 bits
+    twice = _bf16_once(exact.astype(np.float32).astype(np.float64))
+    want = _bf16_once(exact)
+    assert (want != twice).sum() > 1000  # the inputs tell one rounding from two
+    assert np.array_equal(_f64(got)[:, :512], np.repeat(want, 128, axis=1))
+    full = capi.mla_cache_gather(torch.from_numpy(rows).to(dev), _i32(range(n), dev), dtype=torch.float32)
+    assert np.array_equal(_np(full)[:, :512], np.repeat(exact.astype(np.float32), 128, axis=1))
