@@ -4,13 +4,16 @@ compiled part of its Python binding (``_smla_torch.so``) with the host compiler.
 Each ``csrc/*.cu`` translation unit compiles in its own nvcc process (in
 parallel), then nvcc links the shared library next to this file.  A unit is
 rebuilt only when it, a header under ``csrc/`` or ``include/smla.h`` is newer
-than its object.  The binding compiles beside them, against the installed
-torch's headers.
+than its object.  The library needs nvcc alone and is linked whatever becomes
+of the binding, which compiles beside it against the installed torch's headers,
+again when another torch or Python is installed; without a torch there is
+none.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -49,6 +52,13 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _read(path: str) -> str:
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read()
+
+
 def _compile(nvcc, src, obj, log_dir):
     cmd = [nvcc] + NVCC_FLAGS + ["-c", src, "-o", obj]
     p = subprocess.run(cmd, capture_output=True, text=True)
@@ -59,10 +69,20 @@ def _compile(nvcc, src, obj, log_dir):
     return obj
 
 
+def _torch_dir():
+    """The installed torch's folder (None without one), not imported."""
+    spec = importlib.util.find_spec("torch")
+    return list(spec.submodule_search_locations)[0] if spec else None
+
+
+def _torch_key() -> str:
+    """What the binding's object is compiled against."""
+    return f"{sys.version}\n{_torch_dir()}\n" + _read(os.path.join(_torch_dir(), "version.py"))
+
+
 def _compile_binding(obj, log_dir):
-    import torch
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
-    inc = [os.path.join(os.path.dirname(torch.__file__), "include"),
+    inc = [os.path.join(_torch_dir(), "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden"]
     cmd += ["-I" + p for p in inc] + ["-c", BINDING_SRC, "-o", obj]
@@ -81,7 +101,7 @@ def _link(cmd):
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
-    """Compile every CUDA unit and link libsmla.so, and compile and link its
+    """Compile every CUDA unit and link libsmla.so, then compile and link its
     Python binding; returns the library path."""
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -96,11 +116,16 @@ def build(verbose: bool = False, force: bool = False) -> str:
             jobs.append((src, obj))
     binding_obj = os.path.join(BUILD_DIR, "smla_torch.o")
     header = os.path.join(ROOT, "include", "smla.h")
-    binding_job = force or _stale(binding_obj, [BINDING_SRC, header])
+    with_binding = _torch_dir() is not None
+    stamp = os.path.join(BUILD_DIR, "smla_torch.key")
+    binding_job = with_binding and (force or _stale(binding_obj, [BINDING_SRC, header])
+                                    or _read(stamp) != _torch_key())
+    binding = None
     if jobs or binding_job:
         with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
-            futs = [ex.submit(_compile_binding, binding_obj, BUILD_DIR)] if binding_job else []
-            futs += [ex.submit(_compile, nvcc, s, o, BUILD_DIR) for s, o in jobs]
+            if binding_job:
+                binding = ex.submit(_compile_binding, binding_obj, BUILD_DIR)
+            futs = [ex.submit(_compile, nvcc, s, o, BUILD_DIR) for s, o in jobs]
             for f in futs:
                 f.result()
         if verbose:
@@ -109,11 +134,14 @@ def build(verbose: bool = False, force: bool = False) -> str:
                     sys.stdout.write(f.read())
     if force or jobs or _stale(LIB_PATH, objs):
         _link([nvcc] + ARCH + ["-shared", "-o", LIB_PATH] + objs)
-    if force or jobs or binding_job or _stale(BINDING_PATH, [binding_obj, LIB_PATH]):
-        import torch
+    if binding is not None:
+        binding.result()  # the library is there even when this raises
+        with open(stamp, "w") as f:
+            f.write(_torch_key())
+    if with_binding and (force or jobs or binding_job or _stale(BINDING_PATH, [binding_obj, LIB_PATH])):
         _link([os.environ.get("CXX", "g++"), "-shared", "-o", BINDING_PATH, binding_obj,
                "-L" + PKG_DIR, "-l:libsmla.so", "-Wl,-rpath,$ORIGIN",
-               "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python",
+               "-L" + os.path.join(_torch_dir(), "lib"), "-ltorch_python",
                "-ltorch_cpu", "-lc10_cuda", "-lc10"])
     return LIB_PATH
 
