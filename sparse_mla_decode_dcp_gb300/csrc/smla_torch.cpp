@@ -240,10 +240,15 @@ Query query_of(PyObject* q_, PyObject* out_, PyObject* lse_, PyObject* ws_) {
 }
 
 // ids [T, K] of a row's entries.
-const at::Tensor& entries(PyObject* o, const char* name, const Query& q) {
+struct Entries {
+  const int32_t* data;
+  int32_t K;
+};
+
+Entries entries(PyObject* o, const char* name, const Query& q) {
   const at::Tensor& t = need(o, name, at::kInt, q.dev);
   if (t.dim() != 2 || t.size(0) != q.T) refuse(PyExc_ValueError, "%s must be [T, K]", name);
-  return t;
+  return {ptr<int32_t>(t), size32(t.size(1), name)};
 }
 
 // (q, kv_cache, local_slots, sm_scale, out, lse, workspace, stream)
@@ -253,11 +258,11 @@ PyObject* decode_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& kv = tensor(a[1], "kv_cache");
     if (cache_format(kv, "kv_cache", q.dev) != SMLA_CACHE_FP4)
       refuse(PyExc_ValueError, "%s must be [num_slots, 416]", "kv_cache");
-    const at::Tensor& slots = entries(a[2], "local_slots", q);
+    const Entries slots = entries(a[2], "local_slots", q);
     const float scale = f32(a[3]);
     return launch(q.dev, a[7], [&](void* s) {
-      return smla_sparse_mla_decode_fp4(q.q, ptr<uint8_t>(kv), kv.size(0), ptr<int32_t>(slots), q.T, q.H,
-                                        int32_t(slots.size(1)), scale, q.out, q.lse, q.ws, q.ws_bytes, s);
+      return smla_sparse_mla_decode_fp4(q.q, ptr<uint8_t>(kv), kv.size(0), slots.data, q.T, q.H, slots.K,
+                                        scale, q.out, q.lse, q.ws, q.ws_bytes, s);
     });
   });
 }
@@ -268,15 +273,15 @@ PyObject* decode_fused_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 13, [&] {
     const Query q = query_of(a[0], a[9], a[10], a[11]);
     const at::Tensor& req = vec(a[1], "req_id_per_token", at::kInt, q.dev, q.T);
-    const at::Tensor& topk = entries(a[2], "topk_global", q);
+    const Entries topk = entries(a[2], "topk_global", q);
     const Pools p = pools_of(a[3], a[4], a[8], q.dev, -1);
     if (p.format != SMLA_CACHE_FP4) refuse(PyExc_ValueError, "%s must be [num_slots, 416]", "kv_caches[d]");
     const int32_t bs = i32(a[5]), I = i32(a[7]), reqs = size32(p.rows, "block_tables");
     const float scale = f32(a[6]);
     return launch(q.dev, a[12], [&](void* s) {
       return smla_dcp_sparse_mla_decode_fused_fp4(
-          q.q, q.T, q.H, int32_t(topk.size(1)), scale, ptr<int32_t>(req), ptr<int32_t>(topk), reqs, p.D,
-          bs, I, p.kv, p.slots, p.bt, p.stride, p.width, q.out, q.lse, q.ws, q.ws_bytes, s);
+          q.q, q.T, q.H, topk.K, scale, ptr<int32_t>(req), topk.data, reqs, p.D, bs, I, p.kv, p.slots,
+          p.bt, p.stride, p.width, q.out, q.lse, q.ws, q.ws_bytes, s);
     });
   });
 }

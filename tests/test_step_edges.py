@@ -471,3 +471,18 @@ def test_gather_of_8_bit_rows_rounds_to_bf16_once(cuda_device):
     assert np.array_equal(_f64(got)[:, :512], np.repeat(want, 128, axis=1))
     full = capi.mla_cache_gather(torch.from_numpy(rows).to(dev), _i32(range(n), dev), dtype=torch.float32)
     assert np.array_equal(_np(full)[:, :512], np.repeat(exact.astype(np.float32), 128, axis=1))
+
+
+# ---------------------------------------------------------------- refusals
+def test_rows_of_more_entries_than_32_bits_count_are_refused(lib):
+    """Not taken as the low 32 bits of their count (of which 64 would run)."""
+    q = torch.zeros((0, 4, 576), dtype=torch.bfloat16)
+    out, lse = torch.zeros((0, 4, 512), dtype=torch.bfloat16), torch.zeros((0, 4))
+    ids = torch.zeros((0, (1 << 32) + 64), dtype=torch.int32)
+    cache, table = torch.zeros((8, 416), dtype=torch.uint8), torch.zeros((1, 1), dtype=torch.int32)
+    ws = torch.zeros(1, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="too many entries"):
+        capi.sparse_mla_decode_fp4(q, cache, ids, SCALE, out=out, lse=lse, workspace=ws)
+    with pytest.raises(ValueError, match="too many entries"):
+        capi.dcp_sparse_mla_decode_fused_fp4(q, torch.zeros(0, dtype=torch.int32), ids, [cache], [table], 8,
+                                             SCALE, out=out, lse=lse, workspace=ws)
