@@ -1349,10 +1349,11 @@ __device__ void run_cta(const DecodeArgs& a, uint8_t* sm, Ctl* ctl, const HalfRt
     const int nt = __shfl_sync(0xffffffffu, ntiles, 0);
     const bool leader = elect_one();
     bool ok = wait_bar(&ctl->q_ready, 0, abort, kWsQReady);
+    const int steps = __all_sync(0xffffffffu, ok) ? nt + 2 : 0;
     // QK(j), then PV(j - 2): the softmax stores P(j - 2) after it has read
     // S(j - 1), which frees S for QK(j)
 #pragma unroll 1
-    for (int j = 0; j < nt + 2; ++j) {
+    for (int j = 0; j < steps; ++j) {
       if (j < nt) {
         ok = wait_bar(&ctl->full[j % kStages], (j / kStages) & 1, abort, kWsFull) &&
              (j == 0 || wait_bar(&ctl->s_free, (j - 1) & 1, abort, kWsSFree));
