@@ -485,8 +485,9 @@ __device__ __forceinline__ bool convert_row(const ConvRegs& r, uint32_t op, int 
 // tile (64 rows x 21 pieces = 14 x 96), so consecutive lanes read consecutive
 // 16 bytes of a row (whole sectors, few transactions).  A tile's pieces are
 // loaded into registers while the raw stage holds the tile before it, and
-// stored once the converter warps have read that tile out of the stage.  Load-issue stalls (the memory system's request slots) fall on these
-// warps, not on the converters.
+// stored once the converter warps have read that tile out of the stage.
+// Load-issue stalls (the memory system's request slots) fall on these warps,
+// not on the converters.
 static_assert(kTileN * Fp8Rows::kRawStride <= (1 << 15) && Fp8Rows::kRowBytes <= (1 << 10) &&
                   kTileN <= (1 << 7),
               "packed piece offsets fit their fields");
@@ -1428,7 +1429,7 @@ __device__ __forceinline__ bool resolve_entry(const DecodeArgs& a, const Ctl* ct
     return v >= 0;
   }
   // Pools: every entry takes the same straight-line path (no branch per
-  // check), so the 16 entries of a thread overlap their shared-memory reads.
+  // check), so the entries of a thread overlap their shared-memory reads.
   const bool live = v >= 0 && req_ok && !(generated(kMode) && v >= range.limit);
   const int32_t vv = place_entry<kMode>(live ? v : 0, range);
   int d;
@@ -1679,8 +1680,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
     named_bar_sync(6, Roles<F>::kThreads);  // the list's length is known
   } else {
     // Ordered compaction of the split's valid entries by the 256 threads of
-    // the other warps (idle until the tile loop): thread d owns the contiguous
-    // entries [e_begin + 8d, e_begin + 8d + 8), resolves them with all loads
+    // the other warps (idle until the tile loop): thread d owns the kPer
+    // contiguous entries from e_begin + kPer d on, resolves them with all loads
     // in flight at once, and a block scan gives each thread its output
     // offset.  Both CTAs of the pair build the same list, so their tiles hold
     // the same keys.
@@ -1727,7 +1728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
     }
     if (!listed) {
       // 1) this thread's kPer raw entries (loaded before the set-up barrier,
-      //    four 16-byte loads when the row allows; a dense row's entries are
+      //    by 16-byte loads when the row allows; a generated row's entries are
       //    just their indices), and, with D pools, the request's block-table
       //    rows copied into shared memory by all the compacting threads
       const int j0 = e_begin + d * kPer;
@@ -1749,7 +1750,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
         cp_async_wait<0>();
         named_bar_sync(3, kListThreads);  // every thread's copies are visible
       }
-      // 2) resolve the 16 entries from registers and shared memory
+      // 2) resolve them from registers and shared memory
       int shards[kPer];
       unsigned keep = 0;
 #pragma unroll
