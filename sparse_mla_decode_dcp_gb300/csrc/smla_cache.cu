@@ -130,6 +130,7 @@ __device__ __forceinline__ float round_odd(Pair p) {
 __device__ __forceinline__ float quotient_odd(Pair a, float d, float inv) {
   const float v = __fmul_rn(a.hi, inv);
   const float q = __fmaf_rn(__fadd_rn(__fmaf_rn(-v, d, a.hi), a.lo), inv, v);
+  if (q == 0.f) return a.hi;  // zero, or too small for fp32: its sign is what counts
   return round_odd({q, __fadd_rn(__fmaf_rn(-q, d, a.hi), a.lo)});
 }
 

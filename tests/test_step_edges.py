@@ -307,6 +307,32 @@ def test_write_past_fp32(cuda_device, fmt):
         assert np.array_equal(got[:, 512:528].copy().view("<f4")[:, 1:], scale[:, 1:])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_write_of_values_far_below_their_group(cuda_device, fmt):
+    """Quotients too small for fp32, of either sign, beside ones on a rounding
+    border (which send the row through the exact quotients)."""
+    dev = cuda_device
+    x = torch.zeros((8, 512), dtype=torch.float64)
+    top = 448.0 * 2.0 ** 52 if fmt == "fp8" else 6.0 * 256
+    unit = 2.0 ** 52 if fmt == "fp8" else 256.0
+    x[:, ::16] = top
+    x[:, 1::16] = 8.5 * unit if fmt == "fp8" else 2.5 * unit  # ties
+    x[:, 2::16] = -2.0 ** -110
+    x[:, 3::16] = 2.0 ** -110
+    x[:, 4::16] = -2.0 ** -133
+    x[:, 5::16] = -2.0 ** -130
+    x = x.to(torch.bfloat16)
+    got = _write_latents(x.to(dev), None, fmt)
+    code, scale = so.quantise_fp8(_f64(x)) if fmt == "fp8" else so.quantise_fp4(_f64(x))
+    if fmt == "fp8":
+        assert np.array_equal(got[:, 512:528].copy().view("<f4"), scale)
+        assert np.array_equal(got[:, :512], code)
+    else:
+        assert np.array_equal(got[:, 256:288], scale)
+        assert np.array_equal(got[:, :256], code[:, 0::2] | (code[:, 1::2] << 4))
+
+
 # ------------------------------------------------- overlapping launches
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
