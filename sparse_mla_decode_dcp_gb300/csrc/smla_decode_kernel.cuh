@@ -1460,9 +1460,11 @@ __device__ __forceinline__ bool resolve_entry(const DecodeArgs& a, const Ctl* ct
 // How many of the first n positions rank `dense_rank` holds: whole rounds of
 // I*D positions give I each, then the partial round.
 __device__ __forceinline__ int32_t rank_rows(const DecodeArgs& a, int32_t n) {
-  const int32_t ID = a.interleave * a.D;
-  const int32_t full = n / ID, rem = n - full * ID;
-  return full * a.interleave + min(max(rem - a.dense_rank * a.interleave, 0), a.interleave);
+  // a round that does not fit 32 bits never completes
+  const int64_t ID = int64_t(a.interleave) * a.D;
+  const int32_t full = ID > n ? 0 : n / int32_t(ID);
+  const int64_t mine = int64_t(n) - full * ID - int64_t(a.dense_rank) * a.interleave;
+  return full * a.interleave + int32_t(min(max(mine, int64_t(0)), int64_t(a.interleave)));
 }
 
 // Dense and windowed decode: the request of row t and the range of its raw

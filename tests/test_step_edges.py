@@ -333,6 +333,31 @@ def test_write_of_values_far_below_their_group(cuda_device, fmt):
         assert np.array_equal(got[:, :256], code[:, 0::2] | (code[:, 1::2] << 4))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,I", [(16, 1 << 28), (16, (1 << 27) + 1), (9, 1 << 28)])
+def test_dense_decode_of_one_rank_with_rounds_past_32_bits(cuda_device, D, I):
+    """One rank holds the whole context, the others nothing: runs of I
+    positions, D runs a round, more than 32 bits count."""
+    dev = cuda_device
+    ctx, bs = [150], 16
+    pools, tables = _paged(ctx, 1, bs, 1, "fp8", 1, dev)
+    q, c = _q(1, 1, dev), _i32(ctx, dev)
+    want = so.attend(_f64(q)[0], _np(pools[0])[[int(tables[0][0, t // bs]) * bs + t % bs for t in range(150)]],
+                     SCALE, 2.0 ** -11)
+    ws = torch.zeros(capi.dense_decode_workspace_size(1, 1, 150, D, I, 0), dtype=torch.uint8, device=dev)
+    _err()
+    for rank in (0, 1, D - 1):
+        use = [pools[0] if d == rank else None for d in range(D)]
+        tab = [tables[0] if d == rank else None for d in range(D)]
+        out, lse = capi.dcp_dense_mla_decode(q, c, 150, 1, use, tab, bs, SCALE, rank=rank, interleave=I,
+                                             workspace=ws)
+        if rank == 0:
+            _check(out, lse, [want])
+        else:
+            assert torch.isneginf(lse).all() and not out.any()
+    assert _err() == 0
+
+
 # ------------------------------------------------- overlapping launches
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
