@@ -101,6 +101,8 @@ class DcpServingStep:
     ``take_blocks`` then drops the blocks taken since the last call from the
     front of the free lists (it reads their counts, so it synchronises); a
     server that keeps the lengths on the host can do that from them instead.
+    A ``prefill`` or ``run`` that raises has taken nothing: called again with
+    the same lengths it takes the same blocks.
     """
 
     def __init__(self, num_reqs: int, tokens_per_req: int, heads: int, dcp: int, block_size: int,
@@ -139,27 +141,31 @@ class DcpServingStep:
     def _append(self, ctx_lens, q_lens, kv, outs):
         if self._taken:
             raise RuntimeError("the last step's blocks are still in the free lists: take_blocks() first")
+        taken = []
         for d in range(self.D):
             m = capi.dcp_step_maps(ctx_lens, q_lens, self.free_blocks[d], self.block_tables[d],
                                    kv.shape[0], self.D, d, self.block_size,
                                    interleave=self.interleave, out=outs[d], stream=self.stream)
-            self._taken.append(m.blocks_taken)
+            taken.append(m.blocks_taken)
             capi.mla_cache_write(kv, m.slots, self.pools[d], gamma=self.gamma, eps=self.eps,
                                  positions=m.positions, cos_sin=self.cos_sin,
                                  rope_pairs=self.rope_pairs, stream=self.stream)
+        return taken
 
     def prefill(self, ctx_lens: torch.Tensor, q_lens: torch.Tensor, kv: torch.Tensor):
         """Write the rows kv [sum(q_lens), 576] of the requests' new tokens."""
-        self._append(ctx_lens, q_lens, kv, [None] * self.D)
+        self._taken = self._append(ctx_lens, q_lens, kv, [None] * self.D)
 
     def run(self, ctx_lens: torch.Tensor, kv: torch.Tensor, q: torch.Tensor):
         """One decode step: rows kv [B*S, 576] go into the caches, q
         [B*S, H, 576] attends.  Returns (out, lse), reused by the next step."""
-        self._append(ctx_lens, self.q_lens, kv, self.maps)
-        return capi.dcp_window_mla_decode(
+        taken = self._append(ctx_lens, self.q_lens, kv, self.maps)
+        result = capi.dcp_window_mla_decode(
             q, ctx_lens, self.max_ctx, self.S, self.window, self.sinks, self.pools,
             self.block_tables, self.block_size, self.sm_scale, interleave=self.interleave,
             out=self.out, lse=self.lse, workspace=self.workspace, stream=self.stream)
+        self._taken = taken
+        return result
 
     def take_blocks(self):
         """Drop the blocks the last prefill or run took from the free lists."""

@@ -218,6 +218,44 @@ def test_decode_step_on_a_stream_behind_a_busy_one(cuda_device):
     torch.cuda.synchronize()
 
 
+@pytest.mark.gpu
+def test_serving_step_called_again_after_a_refusal(cuda_device):
+    """A prefill and a step that are refused half-way (rows of a wrong width, a
+    query of a wrong shape) take no blocks: called again they do what they
+    would have done."""
+    from sparse_mla_decode_dcp_gb300.pipeline import DcpServingStep
+    dev = cuda_device
+    g = torch.Generator(device=dev).manual_seed(4)
+    ctx, more = _i32([60, 9], dev), _i32([61, 10], dev)
+    kv, kv1 = (torch.randn((n, 576), generator=g, device=dev).to(torch.bfloat16) for n in (69, 2))
+    q = _q(2, 4, dev)
+
+    def make():
+        return DcpServingStep(num_reqs=2, tokens_per_req=1, heads=4, dcp=2, block_size=4, blocks_per_rank=40,
+                              max_ctx=100, window=50, sinks=3, device=dev)
+
+    want = make()
+    want.prefill(ctx, ctx, kv)
+    want.take_blocks()
+    out, lse = (t.clone() for t in want.run(more, kv1, q))
+    want.take_blocks()
+    step = make()
+    with pytest.raises(ValueError):
+        step.prefill(ctx, ctx, kv[:, :568].contiguous())
+    step.prefill(ctx, ctx, kv)
+    step.take_blocks()
+    with pytest.raises(ValueError):
+        step.run(more, kv1, q[:, :, :512].contiguous())
+    with pytest.raises(ValueError):
+        step.run(more, kv1.float(), q)
+    o, l = step.run(more, kv1, q)
+    assert torch.equal(o, out) and torch.equal(l, lse)
+    step.take_blocks()
+    for a, b in zip(step.free_blocks + step.block_tables + step.pools,
+                    want.free_blocks + want.block_tables + want.pools):
+        assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------ ends of fp32
 def _fp8_rows(y):
     """Codes and scales of float64 latents y as the header defines them: a
