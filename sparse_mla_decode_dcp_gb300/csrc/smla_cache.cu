@@ -16,12 +16,12 @@
 // value).  fp64 would do too but runs at about 1/60 of the fp32 rate here.
 //
 // One warp per row: a lane owns 16 consecutive latent dims (one fp4 group, an
-// eighth of an fp8 group) and one rope pair.  Measured with norm and rotation:
-// 64 rows 1.8 us (fp4) and 2.2 (fp8), what a launch takes; 16,384 rows 8.5 and
-// 12.3; 65,536 rows 32.7 and 44.7, 3.7 and 3.0 TB/s, where the issue slots are
-// 73-76% busy with the exact sums and quotients (ALU and FMA pipes 50-57%),
-// not HBM.  Four rows a warp, the next one's loads ahead, gained nothing (fp4,
-// 16,384 rows: 10.4 us).
+// eighth of an fp8 group) and one rope pair.  Measured with norm and rotation,
+// rows to random slots: 64 rows 2.0 us (fp4) and 2.6 (fp8), about a launch;
+// 16,384 rows 9.4 and 11.1; 65,536 rows 33.1 and 39.2, 3.6 and 3.5 TB/s, where
+// the issue slots are 73-75% busy with the exact sums and quotients, not HBM.
+// Rows without a slot leave their warps' places empty: 16,384 of which one in
+// four is written 4.9 and 5.5, 4,096 that all are 4.3 and 5.1.
 //
 // Gather.  One warp per row, 8 dims per lane and step, so that every store is
 // 16 consecutive bytes a lane; kRows rows at once keep their loads in flight

@@ -204,7 +204,7 @@ __device__ __forceinline__ bool wait_longer(uint64_t* bar, uint32_t parity, vola
 // the code of sixteen warps in five roles is smaller by its copies.  Measured
 // both ways: 4-bit decodes 2-3% sooner (four pools 52.2 -> 51.2 us, one rank
 // 29.8 -> 29.0), windows 0.4-1.6%; but dense decode 635 -> 647 us, the 8-bit
-// fused step 61.7 -> 61.8, so those keep the copies.
+// fused step (inputs in L2) 61.7 -> 61.8, so those keep the copies.
 template <bool kCluster>
 __noinline__ __device__ bool wait_longer_called(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                 uint32_t site) {
@@ -363,7 +363,8 @@ struct Fp4Rows {
 // bounds the fp4 kernels (sparse step of 4 pools, 64 rows of 2048 entries,
 // H = 128: 58.2 -> 54.3 us; 2 rows of 64 9.5 -> 8.4), but leave the loaders 128
 // instead of 168 registers, and fp8's rows, half again as long, then arrive
-// late (fused step 62.8 -> 66.9 us, dense decode 649 -> 690): one thread there.
+// late (fused step, inputs in L2, 62.8 -> 66.9 us, dense decode 649 -> 690): one
+// thread there.
 template <class F>
 struct Roles {
   static constexpr int kSoftmaxWarps = 4 * F::kRowThreads;
@@ -419,10 +420,9 @@ __device__ __forceinline__ uint32_t op_addr(uint32_t op, int key, int ldim) {
 
 // 8 e2m1 codes (one 32-bit word, dim i in nibble i) times their group's scale,
 // exact in fp16: at most 6 significant bits, 2^-10 to 2688.  The conversion
-// instruction keeps a tile's dims in their order; unpacking by shifts and masks
-// would leave them in another, which q and O would have to follow, and measured
-// 0.3 us slower (2 rows of 64 entries: 6.8 against 6.5; 32 rows of 2048 in two
-// splits 30.3, 29.9) to 0.8 us faster (64 rows of 2048: 52.8, 53.6).
+// instruction keeps a tile's dims in their order; shifts and masks would leave
+// them in another, for no clear gain (2 rows of 64 entries 6.8 against 6.5 us, 64
+// rows of 2048 52.8 against 53.6).
 __device__ __forceinline__ uint4 e2m1x8_scaled(uint32_t w, __half2 scale) {
   uint32_t o[4];
 #pragma unroll
@@ -595,11 +595,9 @@ __device__ void convert_loop(Ctl* ctl, uint8_t* sm, int n, int ntiles, int key, 
 // take the rope values, four lanes a key.  Against loader warps and a raw
 // stage: 2 rows of 64 entries 7.6 -> 6.5 us, one pool's 32 rows of 2048 (two
 // splits) 32.0 -> 29.9, four pools' 64 rows 55.1 -> 53.6, windows of 1088
-// entries 66.2 -> 63.0.  Slower were two threads a key, 32 bytes of it a load
-// (76 rows of 1024 entries 41.5 us, with loader warps 32.6), two tiles ahead
-// (four pools 53.5 us; one 53.1) and addresses formed from slot and shard at
-// each load (60.8): the list holds the rows' addresses, and each tile's are
-// read a tile early.
+// entries 66.2 -> 63.0.  The list holds the rows' addresses (formed from slot
+// and shard at each load: four pools 60.8 us), and each tile's are read a tile
+// early.
 constexpr int kRopeThreads = 64;
 
 struct Fp4Regs {
