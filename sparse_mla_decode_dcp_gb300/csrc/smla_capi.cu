@@ -311,7 +311,8 @@ smla_status smla_dcp_sparse_mla_decode_fused_host(
 static int32_t dense_entries(int32_t max_ctx, int32_t D, int32_t interleave, int32_t rank) {
   if (rank < 0) return max_ctx;
   const int64_t id = int64_t(interleave) * D;
-  return int32_t(((int64_t(max_ctx) + id - 1) / id) * interleave);
+  const int64_t held = ((int64_t(max_ctx) + id - 1) / id) * interleave;
+  return int32_t(held < INT32_MAX ? held : INT32_MAX);
 }
 
 size_t smla_dense_decode_workspace_size(int32_t T, int32_t H, int32_t max_ctx, int32_t D,

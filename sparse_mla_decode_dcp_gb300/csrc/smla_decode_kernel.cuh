@@ -1558,7 +1558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
   const int64_t t = overlapped<kMode, F>() ? item - outer * inner : outer;
   const int split = int(overlapped<kMode, F>() ? outer : item - outer * inner);
   const int e_begin = split * a.split_entries;
-  const int e_end = min(a.K, e_begin + a.split_entries);
+  const int e_end = a.K - e_begin < a.split_entries ? a.K : e_begin + a.split_entries;
 
   const HalfRt hr = half_of(c);
   // a separate split combine (if any) may be scheduled on SMs this grid
@@ -1947,10 +1947,11 @@ bool combine_in_kernel(int64_t decode_ctas, int splits, int sms) {
 constexpr int kClusterSlots = 76;
 
 int decode_splits(int32_t T, int32_t K) {
-  int s = (T > 0) ? kClusterSlots / T : 1;
-  s = min(s, (K + 255) / 256);
-  s = max(s, (K + kMaxList - 1) / kMaxList);
-  return max(s, 1);
+  const int64_t k = K;  // K may be close to 2^31
+  int64_t s = (T > 0) ? kClusterSlots / T : 1;
+  s = min(s, (k + 255) / 256);
+  s = max(s, (k + kMaxList - 1) / kMaxList);
+  return int(max(s, int64_t(1)));
 }
 
 // The serving step's decodes take the splits that end first by a model of a
@@ -2115,7 +2116,7 @@ cudaError_t launch_impl(const DecodeArgs& args, cudaStream_t s) {
     a.split_entries = plan.entries;
   } else {
     a.splits = a.single_split ? 1 : decode_splits(a.T, a.K);
-    a.split_entries = (a.K + a.splits - 1) / a.splits;
+    a.split_entries = int32_t((int64_t(a.K) + a.splits - 1) / a.splits);
   }
   const WsLayout w = ws_layout(a.T, a.H, a.splits);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);

@@ -104,6 +104,22 @@ def test_splits_merge_on_both_sides_of_the_rows_with_counters(cuda_device, T):
     _check(out[at], lse[at], [so.attend(qf[t], rows[slots[t][slots[t] >= 0]], SCALE) for t in at])
 
 
+@pytest.mark.parametrize("ctx", [2 ** 31 - 1, 2 ** 31 - 100, 2 ** 31 - 2048, 2 ** 31 - 2049])
+def test_dense_contexts_up_to_31_bits_are_split(lib, ctx):
+    """A bound of 2^31 - 1 positions takes as many key ranges as one of a few
+    thousand fewer, and the workspace they need, not a single range of 2048."""
+    counters = 16384 * 2 * 4 + 256
+    for D, I, rank, held in [(4, 1, -1, ctx), (1, 1000, 0, ctx), (1, 2 ** 30, 0, ctx), (2, 16, 1, ctx // 2)]:
+        n = capi.dense_decode_workspace_size(1, 1, ctx, D, I, rank)
+        assert n >= counters + -(-held // 2048) * (1024 + 16), (D, I)
+    arr = lambda typ, x: (typ * 1)(x)  # noqa: E731
+    st = lib.smla_dcp_dense_mla_decode(
+        0x10000, 1, 1, 1, ctypes.c_float(0.07), 0x10000, ctx, 1, -1, 16, 1, arr(ctypes.c_void_p, 0x10000),
+        arr(ctypes.c_int64, 100), arr(ctypes.c_void_p, 0x10000), arr(ctypes.c_int64, 4),
+        arr(ctypes.c_int32, 4), 0x10000, 0x10000, None, 0, None)
+    assert st == capi.SMLA_ERR_WORKSPACE
+
+
 def test_workspace_sizes_hold_the_counters_of_any_call(lib):
     """Every size that is not 0 begins with the same counters' region, so no
     call's partials reach into it."""
