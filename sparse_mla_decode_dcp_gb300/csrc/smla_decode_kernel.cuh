@@ -1558,7 +1558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<F>::kThreads, 
   const int64_t t = overlapped<kMode, F>() ? item - outer * inner : outer;
   const int split = int(overlapped<kMode, F>() ? outer : item - outer * inner);
   const int e_begin = split * a.split_entries;
-  const int e_end = a.K - e_begin < a.split_entries ? a.K : e_begin + a.split_entries;
+  const int e_end = int(min(uint32_t(a.K), uint32_t(e_begin) + uint32_t(a.split_entries)));
 
   const HalfRt hr = half_of(c);
   // a separate split combine (if any) may be scheduled on SMs this grid
