@@ -1,0 +1,599 @@
+"""A drafted tree's verification and the 8-bit projections around it, as
+measured work.
+
+Tree maps (visibility masks and rotary positions from parents), attention of
+a tree of drafted tokens over a paged latent cache, the greedy walk of the
+tree with the accepted rows' move to their slots, and the block-scaled 8-bit
+matrix product with the quantisation of its activations.  ``own`` selects the
+library's calls; otherwise ``run`` is their plain form in torch.
+
+Cache rows: fp8 656 bytes = 512 e4m3 codes | 4 fp32 scales | 64 bf16;
+fp4 416 bytes = 256 bytes of e2m1 codes (low nibble = even dim) | 32 e4m3
+scales, one per 16 dims | 64 bf16.
+"""
+import math
+
+import torch
+
+own = False
+
+ROW = {"fp8": 656, "fp4": 416}
+SCALE = 1.0 / math.sqrt(192.0)
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+NEG_INF = float("-inf")
+VOCAB = 128000
+
+
+# --------------------------------------------------------------------------
+# cases
+# --------------------------------------------------------------------------
+def listed():
+    return [
+        # masks and positions of a serving batch's trees: latency
+        dict(name="maps_step", op="maps", B=64, n_lo=16, n_hi=16, pad=0),
+        # thousands of requests with ragged trees, padded to a captured row count
+        dict(name="maps_ragged", op="maps", B=4096, n_lo=1, n_hi=64, pad=77),
+        # one short request on a tensor-parallel rank's heads: latency
+        dict(name="tree_small", op="tree", fmt="fp8", B=1, n_lo=8, n_hi=8, H=16, ctx_lo=300,
+             ctx_hi=300, D=2, rank=-1, bs=16, I=1),
+        # one rank's partial of two very long contexts, ragged trees
+        dict(name="tree_long_rank", op="tree", fmt="fp8", B=2, n_lo=11, n_hi=60, H=64,
+             ctx_lo=50000, ctx_hi=131072, D=4, rank=2, bs=64, I=1),
+        # the long-context serving batch over four pools
+        dict(name="tree_batch_fp8", op="tree", fmt="fp8", B=32, n_lo=16, n_hi=16, H=128,
+             ctx_lo=2048, ctx_hi=32768, D=4, rank=-1, bs=64, I=1),
+        # ragged trees over the 4-bit cache
+        dict(name="tree_ragged_fp4", op="tree", fmt="fp4", B=16, n_lo=5, n_hi=33, H=128,
+             ctx_lo=512, ctx_hi=16384, D=2, rank=-1, bs=64, I=4),
+        # a serving batch's accepted tokens into the 8-bit cache: latency
+        dict(name="commit_step_fp8", op="commit", fmt="fp8", B=32, n_lo=16, n_hi=16),
+        # thousands of ragged trees, 4-bit cache
+        dict(name="commit_ragged_fp4", op="commit", fmt="fp4", B=2048, n_lo=1, n_hi=64),
+        # one token through a small projection (the latent of its cache row): latency
+        dict(name="linear_token", op="linear", G=1, M=1, N=576, K=2048),
+        # a verification step's rows through the query's up-projection (128 heads of 192)
+        dict(name="linear_query_up", op="linear", G=1, M=64, N=24576, K=1536),
+        # the same rows' queries into the latent space, a product for each head
+        dict(name="linear_absorb", op="linear", G=128, M=64, N=512, K=128),
+        # a prefill chunk through the output projection (128 heads of 128)
+        dict(name="linear_prefill_out", op="linear", G=1, M=4001, N=4096, K=16384),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["maps", "tree", "tree", "commit", "linear", "linear"])
+    n_hi = _log(rng, 1, 64)
+    n_lo = rng.choice([n_hi, max(1, n_hi // 4)])
+    if op == "maps":
+        return dict(op=op, B=_log(rng, 1, 4000), n_lo=n_lo, n_hi=n_hi, pad=rng.choice([0, 0, 13]))
+    if op == "commit":
+        return dict(op=op, fmt=rng.choice(["fp8", "fp4"]), B=_log(rng, 1, 1000), n_lo=n_lo, n_hi=n_hi)
+    if op == "tree":
+        D = rng.choice([1, 2, 3, 4, 8])
+        ctx = _log(rng, 1, 100000)
+        case = dict(op=op, fmt=rng.choice(["fp8", "fp4"]), B=_log(rng, 1, 32), n_lo=n_lo, n_hi=n_hi,
+                    H=rng.choice([1, 8, 16, 37, 64, 128]), ctx_lo=max(1, ctx // 16), ctx_hi=ctx,
+                    D=D, rank=rng.choice([-1, -1, rng.randrange(D)]), bs=rng.choice([1, 16, 48, 64, 128]),
+                    I=rng.choice([1, 1, 4]))
+        while work(case)["flops"] > 1e12 or case["B"] * case["ctx_hi"] > 600000:
+            case["B"] = max(1, case["B"] // 2)
+            case["ctx_hi"] = max(1, case["ctx_hi"] // 2)
+            case["ctx_lo"] = max(1, case["ctx_lo"] // 2)
+        return case
+    if rng.random() < 0.3:
+        N, K = rng.choice([(512, 128), (128, 512)])
+        return dict(op=op, G=rng.choice([8, 16, 128]), M=_log(rng, 1, 700), N=N, K=K)
+    case = dict(op=op, G=1, M=_log(rng, 1, 8192), N=_log(rng, 16, 24576), K=16 * _log(rng, 1, 1024))
+    while work(case)["flops"] > 5e11:
+        case["M"] = case["M"] // 2 + 1
+    return case
+
+
+# --------------------------------------------------------------------------
+# sizes that follow from a case
+# --------------------------------------------------------------------------
+def _ladder(lo, hi, n):
+    """n lengths from lo to hi, evenly spaced in their logarithm."""
+    if n == 1:
+        return [hi]
+    return [min(hi, max(lo, int(lo * (hi / lo) ** (i / (n - 1))))) for i in range(n)]
+
+
+def _nodes(case):
+    """Nodes of every request's tree, from n_lo to n_hi in a mixed order."""
+    span = case["n_hi"] - case["n_lo"] + 1
+    return [case["n_hi"] - (b * 37) % span for b in range(case["B"])]
+
+
+def _rows(c, D, r, I):
+    """Of the first c positions, how many rank r holds."""
+    full, rem = divmod(c, I * D)
+    return full * I + min(max(rem - r * I, 0), I)
+
+
+def work(case):
+    op = case["op"]
+    if op == "linear":
+        G, M, N, K = case["G"], case["M"], case["N"], case["K"]
+        # activations, weights and their scales in, results out
+        blocks = -(-K // 128) * -(-N // 128)
+        return {"bytes": G * (2 * M * K + N * K + 4 * blocks + 2 * M * N), "flops": 2 * G * M * N * K}
+    n = _nodes(case)
+    T = sum(n)
+    if op == "maps":
+        W = -(-case["n_hi"] // 64)
+        return {"bytes": 4 * T + 8 * case["B"] + (T + case["pad"]) * (8 * W + 4), "flops": 8 * T}
+    if op == "commit":
+        # tree in; rows, counts and tokens out; about a sixth of the rows moved,
+        # and every row read once through the gather that hands back its values
+        moved = min(T, 4 * case["B"])
+        return {"bytes": 16 * T + 8 * case["B"] + 2 * moved * ROW[case["fmt"]]
+                + T * (4 + ROW[case["fmt"]] + 1152), "flops": T * 512}
+    H = case["H"]
+    keys = pairs = 0
+    for c, m in zip(_ladder(case["ctx_lo"], case["ctx_hi"], case["B"]), n):
+        if case["rank"] >= 0:
+            c, d = _rows(c, case["D"], case["rank"], case["I"]), -(-m // case["D"])
+        else:
+            d = m
+        keys += c + d
+        pairs += (c + min(d, 8)) * m
+    return {"bytes": keys * ROW[case["fmt"]] + T * H * (1152 + 1024 + 4) + 16 * T,
+            "flops": pairs * 2 * H * (576 + 512)}
+
+
+# --------------------------------------------------------------------------
+# inputs
+# --------------------------------------------------------------------------
+def _e2m1_codes(v):
+    """Nearest e2m1 code (ties to the even code) of v, |v| <= 6."""
+    a = v.abs()
+    c = torch.zeros_like(a, dtype=torch.uint8)
+    for b, even_below in [(0.25, True), (0.75, False), (1.25, True), (1.75, False),
+                          (2.5, True), (3.5, False), (5.0, True)]:
+        c += (a > b) if even_below else (a >= b)
+    return c + (torch.signbit(v)).to(torch.uint8) * 8
+
+
+def _quantised_rows(n, fmt, g, dev):
+    """n rows of normalised latents N(0, 1) and rope values N(0, 1)."""
+    out = torch.empty((n, ROW[fmt]), dtype=torch.uint8, device=dev)
+    for s in range(0, n, 1 << 17):
+        m = min(1 << 17, n - s)
+        y = torch.randn((m, 512), generator=g, device=dev)
+        rope = torch.randn((m, 64), generator=g, device=dev).to(torch.bfloat16)
+        o = out[s:s + m]
+        if fmt == "fp8":
+            y = y.view(m, 4, 128)
+            sc = y.abs().amax(2, keepdim=True) / 448.0
+            o[:, :512] = (y / sc).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8).view(m, 512)
+            o[:, 512:528] = sc.reshape(m, 4).contiguous().view(torch.uint8)
+        else:
+            y = y.view(m, 32, 16)
+            sc = (y.abs().amax(2, keepdim=True) / 6.0).to(torch.float8_e4m3fn)
+            c = _e2m1_codes((y / sc.float()).clamp(-6, 6)).view(m, 256, 2)
+            o[:, :256] = c[:, :, 0] | (c[:, :, 1] << 4)
+            o[:, 256:288] = sc.view(torch.uint8).view(m, 32)
+        o[:, -128:] = rope.view(torch.uint8).view(m, 128)
+    return out
+
+
+def _paged_pools(ctx, D, bs, I, fmt, extra, seed, g, dev):
+    """D pools of one tensor and their block tables: request b's blocks are a
+    random choice of its pool's; ~10% of the blocks belong to nobody, and each
+    pool ends in `extra` rows outside every block."""
+    cg = torch.Generator().manual_seed(seed)
+    c = torch.tensor(ctx, dtype=torch.int64)
+    tables, counts, scratch = [], [], []
+    for d in range(D):
+        n = (c // (I * D)) * I + (c % (I * D) - d * I).clamp(0, I)
+        nb = (n + bs - 1) // bs
+        total = int(nb.sum()) + max(1, int(nb.sum()) // 10)
+        perm = torch.randperm(total, generator=cg).to(torch.int32)
+        W = max(1, int(nb.max()))
+        col = torch.arange(W)[None]
+        at = (torch.cumsum(nb, 0) - nb)[:, None] + col
+        tables.append(torch.where(col < nb[:, None], perm[at.clamp(max=total - 1)],
+                                  torch.tensor(-1, dtype=torch.int32)))
+        scratch.append(total * bs)
+        counts.append(total * bs + extra)
+    W = max(t.shape[1] for t in tables)
+    bt = torch.full((D, len(ctx), W), -1, dtype=torch.int32)
+    for d, t in enumerate(tables):
+        bt[d, :, :t.shape[1]] = t
+    pool = _quantised_rows(sum(counts), fmt, g, dev)
+    base = [0]
+    for n in counts:
+        base.append(base[-1] + n)
+    bt = bt.to(dev)
+    return dict(pool=pool, bt=bt, base=torch.tensor(base[:-1], device=dev), scratch=scratch,
+                pools=[pool[base[d]:base[d + 1]] for d in range(D)], tables=[bt[d] for d in range(D)])
+
+
+def _shuffled(values, seed):
+    p = torch.randperm(len(values), generator=torch.Generator().manual_seed(seed)).tolist()
+    return [values[i] for i in p]
+
+
+def _trees(n, seed):
+    """Ragged random trees: (row_start, each row's request, its node's index,
+    its parent's index); a node hangs on one of the few before it."""
+    cg = torch.Generator().manual_seed(seed)
+    n = torch.tensor(n, dtype=torch.int64)
+    starts = torch.cat([torch.zeros(1, dtype=torch.int64), torch.cumsum(n, 0)])
+    req = torch.repeat_interleave(torch.arange(len(n)), n)
+    j = torch.arange(int(starts[-1])) - starts[req]
+    back = torch.floor(torch.rand(j.shape, generator=cg) * j.clamp(max=5)).long()
+    parent = torch.where(j > 0, j - 1 - back, -1)
+    return starts, req, j, parent
+
+
+def prepare(case, seed):
+    dev = torch.device("cuda")
+    g = torch.Generator(device=dev).manual_seed(seed)
+    op = case["op"]
+    s = {"case": case, "op": op}
+    if op == "linear":
+        G, M, N, K = case["G"], case["M"], case["N"], case["K"]
+        # rows of a norm's or an attention's output, a few channels larger than the rest
+        x = torch.randn((M, G, K + 64 * (G > 1)), generator=g, device=dev)
+        x *= 1.0 + 7.0 * (torch.rand((1, 1, x.shape[2]), generator=g, device=dev) < 0.02)
+        x = x.to(torch.bfloat16)[:, :, :K]
+        s["x"] = x.transpose(0, 1) if G > 1 else x[:, 0]
+        nb, kb = -(-N // 128), -(-K // 128)
+        codes = torch.empty((G, N, K), dtype=torch.float8_e4m3fn, device=dev)
+        scales = torch.empty((G, nb, kb), device=dev)
+        for i in range(G):
+            w = torch.zeros((nb * 128, kb * 128), device=dev)
+            w[:N, :K] = torch.randn((N, K), generator=g, device=dev) / math.sqrt(K)
+            w = w.view(nb, 128, kb, 128)
+            sc = w.abs().amax((1, 3)) / 448.0
+            c = (w / sc[:, None, :, None]).clamp(-448, 448).view(nb * 128, kb * 128)[:N, :K]
+            codes[i], scales[i] = c.to(torch.float8_e4m3fn), sc
+        s["w"], s["w_scale"] = (codes, scales) if G > 1 else (codes[0], scales[0])
+        # a head's result goes into its part of the decode's query or output rows
+        s["out"] = (torch.zeros((M, G, N + 64), dtype=torch.bfloat16, device=dev)[:, :, :N].transpose(0, 1)
+                    if G > 1 else torch.zeros((M, N), dtype=torch.bfloat16, device=dev))
+        return s
+    n = _nodes(case)
+    starts, req, j, parent = _trees(n, seed)
+    T = int(starts[-1])
+    cg = torch.Generator().manual_seed(seed + 1)
+    s["row_start"] = starts.to(torch.int32).to(dev)
+    s["T"] = T
+    i32 = torch.int32
+    if op == "maps":
+        fill = torch.zeros(case["pad"], dtype=torch.int64)
+        s["parents"] = torch.cat([parent, fill]).to(i32).to(dev)
+        s["prefix"] = torch.randint(0, 60000, (case["B"],), generator=cg).to(i32).to(dev)
+    elif op == "commit":
+        tokens = torch.randint(0, VOCAB, (T,), generator=cg)
+        targets = torch.randint(0, VOCAB, (T,), generator=cg)
+        # four of five nodes have a drafted child that the model agrees with
+        agree = (j > 0) & (torch.rand(T, generator=cg) < 0.8)
+        at = (starts[req] + parent)[agree]
+        targets[at] = tokens[agree]
+        s["parents"], s["tokens"], s["targets"] = (v.to(i32).to(dev) for v in (parent, tokens, targets))
+        perm = torch.randperm(2 * T + 5, generator=cg).to(i32).to(dev)
+        s["src"], s["dst"] = perm[:T].contiguous(), perm[T:2 * T].contiguous()
+        s["pool"] = _quantised_rows(2 * T + 5, case["fmt"], g, dev)
+    else:
+        D, I, H = case["D"], case["I"], case["H"]
+        ctx = _shuffled(_ladder(case["ctx_lo"], case["ctx_hi"], case["B"]), seed)
+        s.update(_paged_pools(ctx, D, case["bs"], I, case["fmt"], T, seed, g, dev))
+        s["ctx"], s["n"], s["parent_list"] = ctx, n, parent.tolist()
+        s["prefix"] = torch.tensor(ctx, dtype=i32, device=dev)
+        s["q"] = torch.randn((T, H, 576), generator=g, device=dev).to(torch.bfloat16)
+        # a drafted token's row lies behind its rank's blocks
+        owner = ((torch.tensor(ctx)[req] + j) // I) % D
+        s["draft_slots"] = [torch.where(owner == d, s["scratch"][d] + torch.arange(T), -1).to(i32).to(dev)
+                            for d in range(D)]
+        s["masks"] = _plain_maps(parent.to(dev), starts.to(dev), torch.zeros(case["B"], dtype=torch.int64,
+                                                                             device=dev), case["n_hi"])[0]
+    return s
+
+
+# --------------------------------------------------------------------------
+# the library's calls
+# --------------------------------------------------------------------------
+def _run_own(s):
+    from sparse_mla_decode_dcp_gb300 import capi
+    c, op, b = s["case"], s["op"], s.setdefault("buffers", {})
+    if op == "maps":
+        b["out"] = capi.tree_maps(s["parents"], s["row_start"], s["prefix"], c["n_hi"], out=b.get("out"))
+        return list(b["out"])
+    if op == "commit":
+        b["walk"] = capi.tree_accept(s["parents"], s["tokens"], s["targets"], s["row_start"],
+                                     out=b.get("walk"))
+        capi.mla_cache_move(s["pool"], b["walk"].rows, s["src"], s["dst"])
+        b["out"] = capi.mla_cache_gather(s["pool"], s["dst"], out=b.get("out"))
+        return list(b["walk"]) + [b["out"]]
+    if op == "linear":
+        if not b:  # what a program allocates once for its batch shape
+            b["a"] = capi.alloc_fp8_rows(s["x"].shape, s["x"].device)
+            b["workspace"] = capi.alloc_fp8_matmul_workspace(c["G"], c["M"], c["N"], c["K"], s["x"].device)
+        a = capi.fp8_quantise(s["x"], out=b["a"])
+        return capi.fp8_matmul(a.codes, a.scales, s["w"], s["w_scale"], out=s["out"],
+                               workspace=b["workspace"])
+    T, H = s["q"].shape[:2]
+    if not b:  # what a serving loop allocates once for its batch shape
+        b["out"] = torch.empty((T, H, 512), dtype=torch.bfloat16, device=s["q"].device)
+        b["lse"] = torch.empty((T, H), dtype=torch.float32, device=s["q"].device)
+        b["workspace"] = capi.alloc_tree_decode_workspace(
+            T, H, c["B"], c["ctx_hi"], c["n_hi"], c["D"], c["I"], c["rank"], s["q"].device)
+    return capi.dcp_tree_mla_decode(s["q"], s["row_start"], s["prefix"], c["ctx_hi"], s["masks"],
+                                    c["n_hi"], s["draft_slots"], s["pools"], s["tables"], c["bs"], SCALE,
+                                    rank=c["rank"], interleave=c["I"], **b)
+
+
+# --------------------------------------------------------------------------
+# the plain forms
+# --------------------------------------------------------------------------
+def _plain_maps(parent, starts, prefix, max_nodes):
+    dev = parent.device
+    T, B = parent.shape[0], starts.shape[0] - 1
+    W = -(-max_nodes // 64)
+    i = torch.arange(T, device=dev)
+    live = i < starts[-1]
+    req = torch.searchsorted(starts[1:].contiguous(), i, right=True).clamp(max=B - 1)
+    first = torch.where(live, starts[req], 0)
+    at = torch.where(live, i - first, -1)
+    seen = torch.zeros((T, 64 * W + 1), dtype=torch.bool, device=dev)  # the last column takes the rest
+    depth = torch.full((T,), -1, dtype=torch.int64, device=dev)
+    for _ in range(max_nodes):
+        seen.scatter_(1, torch.where(at >= 0, at, 64 * W)[:, None], True)
+        depth += at >= 0
+        at = torch.where(at >= 0, parent[first + at.clamp(min=0)], -1)
+    bits = seen[:, :64 * W].view(T, W, 64).long() << torch.arange(64, device=dev)
+    pos = torch.where(live, prefix[req] + depth, 0)
+    return bits.sum(2), pos.to(torch.int32)
+
+
+def _plain_accept(s):
+    starts = s["row_start"].long()
+    dev = starts.device
+    T, B = s["T"], starts.shape[0] - 1
+    i = torch.arange(T, device=dev)
+    req = torch.searchsorted(starts[1:].contiguous(), i, right=True)
+    parent = s["parents"].long() + starts[req]  # as rows
+    root = s["parents"] < 0
+    n = starts[1:] - starts[:-1]
+    cur = torch.where(n > 0, starts[:-1], -1)
+    steps, alive = [cur], cur
+    for _ in range(s["case"]["n_hi"] - 1):
+        u = alive.clamp(min=0)
+        fits = (alive[req] >= 0) & ~root & (parent == u[req]) & (s["tokens"] == s["targets"][u][req])
+        child = torch.full((B,), T, dtype=torch.int64, device=dev)
+        child.scatter_reduce_(0, req, torch.where(fits, i, T), "amin")
+        alive = torch.where(child < T, child, -1)
+        steps.append(alive)
+        cur = torch.where(alive >= 0, alive, cur)
+    path = torch.stack(steps, 1)
+    count = (path >= 0).sum(1)
+    out = torch.full((T + 1,), -1, dtype=torch.int64, device=dev)
+    at = (torch.cumsum(count, 0) - count)[:, None] + torch.arange(path.shape[1], device=dev)
+    out.scatter_(0, torch.where(path >= 0, at, T).reshape(-1), path.reshape(-1))
+    token = torch.where(cur >= 0, s["targets"][cur.clamp(min=0)], -1)
+    return count.to(torch.int32), out[:T].to(torch.int32), token.to(torch.int32)
+
+
+def _values(rows, fmt):
+    """fp32 [..., 576] of packed rows."""
+    shape = rows.shape[:-1]
+    rope = rows[..., -128:].contiguous().view(torch.bfloat16).float()
+    if fmt == "fp8":
+        v = rows[..., :512].contiguous().view(torch.float8_e4m3fn).float().view(*shape, 4, 128)
+        sc = rows[..., 512:528].contiguous().view(torch.float32)
+    else:
+        lut = torch.tensor(E2M1 + tuple(-x for x in E2M1), device=rows.device)
+        codes = rows[..., :256].int()
+        v = lut[torch.stack([codes & 15, codes >> 4], -1)].view(*shape, 32, 16)
+        sc = rows[..., 256:288].contiguous().view(torch.float8_e4m3fn).float()
+    return torch.cat([(v * sc[..., None]).view(*shape, 512), rope], -1)
+
+
+def _plain_commit(s):
+    count, rows, token = _plain_accept(s)
+    src = s["src"].long()[rows.clamp(min=0).long()]
+    dst = torch.where(rows >= 0, s["dst"].long(), src)
+    s["pool"][dst] = s["pool"][src]
+    return [count, rows, token, _values(s["pool"][s["dst"].long()], s["case"]["fmt"]).to(torch.bfloat16)]
+
+
+def _plain_tree(s):
+    c = s["case"]
+    D, I, bs, H, fmt = c["D"], c["I"], c["bs"], c["H"], c["fmt"]
+    dev = s["q"].device
+    ranks = range(D) if c["rank"] < 0 else [c["rank"]]
+    out = torch.empty((s["T"], H, 512), dtype=torch.bfloat16, device=dev)
+    lse = torch.empty((s["T"], H), dtype=torch.float32, device=dev)
+    t0 = 0
+    for b, (ctx, n) in enumerate(zip(s["ctx"], s["n"])):
+        p = torch.arange(ctx, device=dev)
+        d = (p // I) % D
+        if c["rank"] >= 0:
+            p, d = p[d == c["rank"]], c["rank"]
+        lp = (p // (I * D)) * I + p % I
+        slot = s["base"][d] + s["bt"][d, b, lp // bs].long() * bs + lp % bs
+        drafts = torch.full((n,), -1, dtype=torch.int64, device=dev)
+        for r in ranks:
+            own_slot = s["draft_slots"][r][t0:t0 + n].long()
+            drafts = torch.where((drafts < 0) & (own_slot >= 0), s["base"][r] + own_slot, drafts)
+        k = _values(s["pool"][torch.cat([slot, drafts.clamp(min=0)])], fmt)
+        q = s["q"][t0:t0 + n].reshape(n * H, 576).float()
+        sc = torch.matmul(q, k.T) * SCALE
+        j = torch.arange(n, device=dev)
+        see = ((s["masks"][t0:t0 + n][:, j // 64] >> (j % 64)) & 1).bool() & (drafts >= 0)
+        tail = sc[:, k.shape[0] - n:].view(n, H, n)
+        tail.masked_fill_(~see[:, None], NEG_INF)
+        m = sc.amax(1, keepdim=True)
+        e = torch.exp(sc - torch.where(m > NEG_INF, m, 0.0))
+        l = e.sum(1, keepdim=True)
+        o = torch.matmul(e, k[:, :512]) / torch.where(l > 0, l, 1.0)
+        out[t0:t0 + n] = o.view(n, H, 512).to(torch.bfloat16)
+        lse[t0:t0 + n] = (m + torch.log(l)).view(n, H)
+        t0 += n
+    return out, lse
+
+
+def _plain_linear(s):
+    c = s["case"]
+    N, K, kb = c["N"], c["K"], -(-c["K"] // 128)
+    x = torch.nn.functional.pad(s["x"].double(), (0, kb * 128 - K))  # codes sit next to rounding borders
+    x = x.view(*x.shape[:-1], kb, 128)
+    sc = (x.abs().amax(-1, keepdim=True) / 448.0).float()
+    v = (x / torch.where(sc > 0, sc, 1.0).double()).clamp(-448, 448)
+    # one step of e4m3 at v's magnitude; rounded half to even in 64 bits
+    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+    v = ((v / step).round() * step).float() * sc
+    a = v.flatten(-2)[..., :K]
+    sw = s["w_scale"].repeat_interleave(128, -1)[..., :K].repeat_interleave(128, -2)[..., :N, :]
+    s["out"].copy_(torch.matmul(a, (s["w"].float() * sw).transpose(-1, -2)))
+    return s["out"]
+
+
+def run(s):
+    if own:
+        return _run_own(s)
+    c, op = s["case"], s["op"]
+    if op == "maps":
+        return list(_plain_maps(s["parents"].long(), s["row_start"].long(), s["prefix"].long(), c["n_hi"]))
+    if op == "commit":
+        return _plain_commit(s)
+    if op == "linear":
+        return _plain_linear(s)
+    return _plain_tree(s)
+
+
+# --------------------------------------------------------------------------
+# the definitions in 64 bits, row by row
+# --------------------------------------------------------------------------
+def _e4m3_table(dev):
+    v = []
+    for code in range(256):
+        e, m = (code >> 3) & 15, code & 7
+        x = m / 8 * 2.0 ** -6 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7)
+        v.append(math.nan if code & 127 == 127 else -x if code & 128 else x)
+    return torch.tensor(v, dtype=torch.float64, device=dev)
+
+
+def _exact_rows(rows, fmt):
+    dev, n = rows.device, rows.shape[0]
+    e4m3 = _e4m3_table(dev)
+    if fmt == "fp8":
+        sc = rows[:, 512:528].contiguous().view(torch.float32).double()
+        lat = e4m3[rows[:, :512].long()] * sc.repeat_interleave(128, 1)
+    else:
+        mag = torch.tensor(E2M1, dtype=torch.float64, device=dev)
+        nib = torch.empty((n, 512), dtype=torch.int64, device=dev)
+        nib[:, 0::2] = rows[:, :256].long() % 16
+        nib[:, 1::2] = rows[:, :256].long() // 16
+        lat = mag[nib % 8] * torch.where(nib >= 8, -1.0, 1.0)
+        lat = lat * e4m3[rows[:, 256:288].long()].repeat_interleave(16, 1)
+    rope = (rows[:, -128::2].int() + rows[:, -127::2].int() * 256).to(torch.int32)
+    rope = (rope << 16).view(torch.float32).double()
+    return torch.cat([lat, rope], 1)
+
+
+def _nearest(values, x):
+    """The entry of the ascending table `values` nearest to x >= 0, ties to
+    the even index."""
+    at = torch.searchsorted(values, x.contiguous()).clamp(1, values.numel() - 1)
+    lo, hi = values[at - 1], values[at]
+    up = (x - lo > hi - x) | ((x - lo == hi - x) & (at % 2 == 0))
+    return torch.where(up, hi, lo)
+
+
+def _exact_linear(s, case):
+    G, M, N, K = case["G"], case["M"], case["N"], case["K"]
+    dev = s["x"].device
+    full = _e4m3_table(dev)
+    xs = s["x"] if G > 1 else s["x"][None]
+    ws, scs = (s["w"], s["w_scale"]) if G > 1 else (s["w"][None], s["w_scale"][None])
+    outs = []
+    for g in range(G):
+        acc = torch.zeros((M, N), dtype=torch.float64, device=dev)
+        for k0 in range(0, K, 128):
+            x = xs[g, :, k0:k0 + 128].double()
+            sc = (x.abs().amax(1, keepdim=True) / 448).float().double()
+            safe = torch.where(sc > 0, sc, 1.0)
+            a = _nearest(full[:127], x.abs() / safe) * x.sign() * sc
+            w = full[ws[g, :, k0:k0 + 128].contiguous().view(torch.uint8).long()]
+            w *= scs[g, :, k0 // 128].double().repeat_interleave(128)[:N, None]
+            acc.addmm_(a, w.T)
+        outs.append(acc)
+    return torch.stack(outs) if G > 1 else outs[0]
+
+
+def _exact_tree(s, case):
+    D, I, bs, H, fmt = case["D"], case["I"], case["bs"], case["H"], case["fmt"]
+    dev = s["q"].device
+    bt = s["bt"].cpu()
+    base = s["base"].tolist()
+    slots = [v.tolist() for v in s["draft_slots"]]
+    outs, lses = [], []
+    t0 = 0
+    for b, (ctx, n) in enumerate(zip(s["ctx"], s["n"])):
+        p = torch.arange(ctx)
+        d = torch.div(p, I, rounding_mode="floor") % D
+        lp = torch.div(p, I * D, rounding_mode="floor") * I + p % I
+        row = torch.tensor(base)[d] + bt[d, b, torch.div(lp, bs, rounding_mode="floor")].long() * bs + lp % bs
+        if case["rank"] >= 0:
+            row = row[d == case["rank"]]
+        keys = _exact_rows(s["pool"][row.to(dev)], fmt)
+        where = []
+        for j in range(n):
+            held = [base[r] + slots[r][t0 + j] for r in range(D)
+                    if slots[r][t0 + j] >= 0 and case["rank"] in (-1, r)]
+            where.append(held[0] if held else -1)
+        drafts = _exact_rows(s["pool"][torch.tensor([max(w, 0) for w in where], device=dev)], fmt)
+        for j in range(n):
+            line, u = [], j
+            while u >= 0:
+                line.append(u)
+                u = s["parent_list"][t0 + u]
+            line = [u for u in line if where[u] >= 0]
+            q = s["q"][t0 + j].double()
+            sc = torch.cat([q @ keys.T, q @ drafts[line].T], 1) * SCALE
+            if sc.shape[1] == 0:
+                outs.append(q.new_zeros((H, 512)))
+                lses.append(q.new_full((H,), NEG_INF))
+                continue
+            w = torch.softmax(sc, 1)
+            outs.append(w[:, :keys.shape[0]] @ keys[:, :512] + w[:, keys.shape[0]:] @ drafts[line, :512])
+            lses.append(torch.logsumexp(sc, 1))
+        t0 += n
+    return torch.stack(outs), torch.stack(lses)
+
+
+def _exact_commit(s, case):
+    starts, parent = s["row_start"].tolist(), s["parents"].tolist()
+    token, target = s["tokens"].tolist(), s["targets"].tolist()
+    src, dst = s["src"].tolist(), s["dst"].tolist()
+    held = list(range(s["pool"].shape[0]))  # whose row a slot ends with
+    i = 0
+    for t0, t1 in zip(starts, starts[1:]):
+        u = t0
+        while u is not None:
+            held[dst[i]] = src[u]
+            i += 1
+            u = next((v for v in range(u + 1, t1)
+                      if parent[v] == u - t0 and token[v] == target[u]), None)
+    at = torch.tensor([held[d] for d in dst], device=s["pool"].device)
+    return [None, None, None, _exact_rows(s["pool"][at], case["fmt"])]
+
+
+def exact(case, seed):
+    op = case["op"]
+    if op == "maps":
+        return None  # whole numbers
+    s = prepare(case, seed)
+    if op == "commit":
+        return _exact_commit(s, case)
+    if op == "linear":
+        return _exact_linear(s, case)
+    return _exact_tree(s, case)
