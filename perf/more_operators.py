@@ -315,10 +315,8 @@ def _run_own(s):
     if op == "linear":
         if not b:  # what a program allocates once for its batch shape
             b["a"] = capi.alloc_fp8_rows(s["x"].shape, s["x"].device)
-            b["workspace"] = capi.alloc_fp8_matmul_workspace(c["G"], c["M"], c["N"], c["K"], s["x"].device)
         a = capi.fp8_quantise(s["x"], out=b["a"])
-        return capi.fp8_matmul(a.codes, a.scales, s["w"], s["w_scale"], out=s["out"],
-                               workspace=b["workspace"])
+        return capi.fp8_matmul(a.codes, a.scales, s["w"], s["w_scale"], out=s["out"])
     T, H = s["q"].shape[:2]
     if not b:  # what a serving loop allocates once for its batch shape
         b["out"] = torch.empty((T, H, 512), dtype=torch.bfloat16, device=s["q"].device)
