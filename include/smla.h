@@ -42,6 +42,13 @@
  *   smla_dcp_window_mla_decode        the dense decode limited to a sliding
  *                                     window and a few first tokens (sinks)
  *
+ * and the verification of drafted trees of tokens:
+ *
+ *   smla_tree_maps                    who sees whom, and rotary positions,
+ *                                     from the nodes' parents
+ *   smla_tree_accept                  the nodes the model agrees with
+ *   smla_mla_cache_move               their cache rows, to their own slots
+ *
  * Sources (page title, then section):
  *   [P1] "[eldritch] attention: support DCP in SM120 FlashInfer sparse MLA"
  *   [P2] "[Bugfix][Attention] Stabilize sparse-MLA DCP for GLM PCP evals"
@@ -70,7 +77,7 @@
  *     treated as -1 and a bit is set in the device error word, readable with
  *     smla_get_device_error.  No kernel traps.
  *   - Index tensors are int32, row-major and contiguous.
- *   - The serving step's calls (the last list above) launch with programmatic
+ *   - The serving step's calls (the last lists above) launch with programmatic
  *     stream serialisation: their launch overlaps the end of the kernel before
  *     them on the stream, and they wait for its completion before they touch
  *     memory.
@@ -107,7 +114,10 @@ enum {
   SMLA_DEVERR_RANGE = 32u,      /* a q or rope value, or a latent group scale,
                                    that the fp16 keys cannot carry (below)    */
   SMLA_DEVERR_FREE_BLOCKS = 64u, /* step maps: the free list is too short     */
-  SMLA_DEVERR_POSITION = 128u   /* cache write: a position outside the table  */
+  SMLA_DEVERR_POSITION = 128u,  /* cache write: a position outside the table  */
+  SMLA_DEVERR_TREE = 1u << 30   /* a drafted tree whose rows lie outside T or
+                                   are too many, or a parent that does not
+                                   come before its node                       */
 };
 /* The decode kernels compute QK^T and PV on fp16 operands: q and the rope
  * values are converted from bf16 and each latent value is dequantised as
@@ -119,7 +129,7 @@ enum {
  * it may be outside the stated tolerances.  An fp4 row's latent values are
  * exact in the kernel's keys and its rope values within 2^-18; for those rows
  * the bit stands for the q and rope values and for a NaN scale. */
-/* With SMLA_DEVERR_TIMEOUT, bits 8..31 of the word tell which of the decode
+/* With SMLA_DEVERR_TIMEOUT, bits 8..29 of the word tell which of the decode
  * kernel's internal waits gave up (a diagnostic bitmask, one bit per site). */
 
 /* Largest gathered head count the decode kernel takes [P3 implementation
@@ -663,6 +673,86 @@ smla_status smla_mla_cache_write(
 smla_status smla_mla_cache_gather(const uint8_t* kv_cache, int64_t num_slots, int32_t format,
                                   const int32_t* slots, int32_t N, void* out,
                                   int64_t out_row_stride, int32_t out_fp32, void* stream);
+
+/*
+ * Drafted trees.  A verification step brings, for request b, the n_b nodes of
+ * a tree of drafted tokens as its rows row_start[b] .. row_start[b + 1] - 1;
+ * node j is row row_start[b] + j.  parents[row] is the index (in the tree) of
+ * the node before it, less than its own, or -1 for a node that follows the
+ * prefix (the request's cached positions) directly.  By custom node 0 is the
+ * last token sampled and the only such node.  n_b is 0 .. max_nodes, at most
+ * SMLA_MAX_TREE_NODES; rows from row_start[B] up to T are padding.
+ *
+ * smla_tree_maps writes, with W = ceil(max_nodes / 64):
+ *   masks [T, W]    bit m mod 64 of word m div 64 is set when node m is the
+ *                   row's own or one of its ancestors
+ *   positions [T]   prefix_lens[b] + the node's depth (its number of
+ *                   ancestors), the place of its token if it is accepted
+ * and zeros in both for the padding rows.
+ *
+ *   parents         device int32 [T]
+ *   row_start       device int32 [B + 1]
+ *   prefix_lens     device int32 [B] (may be NULL without positions)
+ *   masks           device uint64 [T, W] output, 8-byte aligned
+ *   positions       device int32 [T] output or NULL
+ * Errors: INVALID_ARG for B < 0, T < 0, max_nodes < 1, a NULL array that is
+ * needed, misaligned arrays; UNSUPPORTED for max_nodes > SMLA_MAX_TREE_NODES.
+ * T = 0 is a no-op.  On the device a parent that is below -1 or not before
+ * its node counts as -1, a request whose rows are more than max_nodes or lie
+ * outside [0, T) writes nothing; both set SMLA_DEVERR_TREE.
+ */
+#define SMLA_MAX_TREE_NODES 256
+smla_status smla_tree_maps(const int32_t* parents, const int32_t* row_start,
+                           const int32_t* prefix_lens, int32_t B, int32_t T, int32_t max_nodes,
+                           uint64_t* masks, int32_t* positions, void* stream);
+
+/*
+ * smla_tree_accept walks each tree greedily: node 0 is accepted, and from an
+ * accepted node the walk goes on to its lowest child whose token is the
+ * node's target (the token the model chose after it), until there is none.
+ *   accepted[b]     the number of accepted nodes (0 for an empty tree)
+ *   rows            the accepted nodes' rows, of request 0 from its node 0
+ *                   on, then of request 1 and so on; -1 behind the last one
+ *                   up to T.  With q_lens = accepted and ctx_lens = the
+ *                   prefix + accepted, row i of smla_dcp_step_maps is the
+ *                   place of the token in rows[i].
+ *   next_tokens[b]  the last accepted node's target (-1 for an empty tree)
+ *
+ *   parents, tokens, targets   device int32 [T]
+ *   row_start                  device int32 [B + 1]
+ *   accepted [B], rows [T], next_tokens [B]   device int32 outputs
+ * No output may alias an input or another output.
+ * Errors: INVALID_ARG for B < 0, T < 0, a NULL array that is needed,
+ * misaligned arrays; UNSUPPORTED for B > SMLA_MAX_STEP_REQS.  B = 0 and T = 0
+ * is a no-op.  On the device a request of more than SMLA_MAX_TREE_NODES rows,
+ * or with rows outside [0, T), counts as empty and sets SMLA_DEVERR_TREE.
+ * Above 64 requests the call is two launches, the second with programmatic
+ * stream serialisation behind the first.
+ */
+smla_status smla_tree_accept(const int32_t* parents, const int32_t* tokens, const int32_t* targets,
+                             const int32_t* row_start, int32_t B, int32_t T, int32_t* accepted,
+                             int32_t* rows, int32_t* next_tokens, void* stream);
+
+/*
+ * Cache move: for i < N with rows[i] != -1 and dst_slots[i] >= 0, the cache
+ * row in slot src_slots[rows[i]] is copied, byte for byte, to slot
+ * dst_slots[i].  With smla_tree_accept's rows, the drafts' slots and
+ * smla_dcp_step_maps' slots it brings the accepted tokens to their places.
+ * A slot that is written is not read by the same call, nor written twice
+ * (else it ends with an undefined mix).
+ *
+ *   kv_cache     device uint8 [num_slots, 656 or 416], 16-byte aligned
+ *   rows         device int32 [N]
+ *   src_slots    device int32 [T]
+ *   dst_slots    device int32 [N]
+ * Errors: INVALID_ARG for N < 0, T < 0, num_slots < 0, another format, NULL or
+ * misaligned arrays.  N = 0 is a no-op.  On the device a row outside [0, T),
+ * a negative source slot or a slot >= num_slots moves nothing and sets
+ * SMLA_DEVERR_SLOT_RANGE.
+ */
+smla_status smla_mla_cache_move(int32_t format, uint8_t* kv_cache, int64_t num_slots,
+                                const int32_t* rows, int32_t N, const int32_t* src_slots, int32_t T,
+                                const int32_t* dst_slots, void* stream);
 
 #ifdef __cplusplus
 } /* extern "C" */

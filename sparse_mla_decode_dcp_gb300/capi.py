@@ -30,6 +30,7 @@ DEVERR_CONTEXT = 16
 DEVERR_RANGE = 32
 DEVERR_FREE_BLOCKS = 64
 DEVERR_POSITION = 128
+DEVERR_TREE = 1 << 30
 
 MAX_HEADS = 128
 MAX_DCP = 16
@@ -39,6 +40,7 @@ V_DIM = 512
 FP4_ROW_BYTES = 416
 CACHE_FP8, CACHE_FP4 = 0, 1
 MAX_STEP_REQS = 8192
+MAX_TREE_NODES = 256
 
 _c_i32, _c_i64, _c_sz, _c_vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
 
@@ -97,6 +99,12 @@ SIGNATURES = {
         _c_i32, _c_vp, _c_i64, _c_vp]),
     "smla_mla_cache_gather": (ctypes.c_int, [
         _c_vp, _c_i64, _c_i32, _c_vp, _c_i32, _c_vp, _c_i64, _c_i32, _c_vp]),
+    "smla_tree_maps": (ctypes.c_int, [
+        _c_vp, _c_vp, _c_vp, _c_i32, _c_i32, _c_i32, _c_vp, _c_vp, _c_vp]),
+    "smla_tree_accept": (ctypes.c_int, [
+        _c_vp, _c_vp, _c_vp, _c_vp, _c_i32, _c_i32, _c_vp, _c_vp, _c_vp, _c_vp]),
+    "smla_mla_cache_move": (ctypes.c_int, [
+        _c_i32, _c_vp, _c_i64, _c_vp, _c_i32, _c_vp, _c_i32, _c_vp, _c_vp]),
 }
 
 _lib = None
@@ -746,3 +754,61 @@ def mla_cache_gather(kv_cache: torch.Tensor, slots: torch.Tensor, *,
         out = _new((slots.shape[0], QK_DIM), dtype, kv_cache.device, stream)
     _check("smla_mla_cache_gather", _native().cache_gather(kv_cache, slots, out, stream))
     return out
+
+
+# --------------------------------------------------------------------------
+# Verification of drafted trees: a step's rows are the nodes of its requests'
+# trees, request b's at row_start[b] .. row_start[b + 1] - 1.
+# --------------------------------------------------------------------------
+class TreeMaps(NamedTuple):
+    """What tree_maps writes: masks int64 [T, ceil(max_nodes / 64)] (bit m:
+    node m of the tree is the row's own or an ancestor), positions int32 [T]."""
+    masks: torch.Tensor
+    positions: torch.Tensor
+
+
+def tree_maps(parents: torch.Tensor, row_start: torch.Tensor, prefix_lens: torch.Tensor,
+              max_nodes: int, *, out: Optional[TreeMaps] = None,
+              stream: Optional[torch.cuda.Stream] = None) -> TreeMaps:
+    """Visibility masks and rotary positions of drafted trees of at most
+    max_nodes nodes; parents[T] are indices in their tree (-1: a node that
+    follows the prefix), each less than its node's."""
+    if out is None:
+        T, dev = parents.shape[0], parents.device
+        out = TreeMaps(_new((T, -(-max_nodes // 64)), torch.int64, dev, stream),
+                       _new((T,), torch.int32, dev, stream))
+    _check("smla_tree_maps",
+           _native().tree_maps(parents, row_start, prefix_lens, max_nodes, out, stream))
+    return out
+
+
+class TreeWalk(NamedTuple):
+    """What tree_accept writes (int32): accepted [B], rows [T] (the accepted
+    nodes' rows in request order, then -1), next_tokens [B]."""
+    accepted: torch.Tensor
+    rows: torch.Tensor
+    next_tokens: torch.Tensor
+
+
+def tree_accept(parents: torch.Tensor, tokens: torch.Tensor, targets: torch.Tensor,
+                row_start: torch.Tensor, *, out: Optional[TreeWalk] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> TreeWalk:
+    """Walk each tree from its node 0 to the lowest child whose token is the
+    node's target, as long as there is one."""
+    if out is None:
+        T, B, dev = parents.shape[0], row_start.shape[0] - 1, parents.device
+        out = TreeWalk(*(_new((n,), torch.int32, dev, stream) for n in (B, T, B)))
+    _check("smla_tree_accept",
+           _native().tree_accept(parents, tokens, targets, row_start, out, stream))
+    return out
+
+
+def mla_cache_move(kv_cache: torch.Tensor, rows: torch.Tensor, src_slots: torch.Tensor,
+                   dst_slots: torch.Tensor, *,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Copy the cache rows src_slots[rows[i]] to dst_slots[i] (either -1:
+    skipped); what is written is not read by the same call.  Returns
+    kv_cache."""
+    _check("smla_mla_cache_move",
+           _native().cache_move(kv_cache, rows, src_slots, dst_slots, stream))
+    return kv_cache

@@ -8,6 +8,7 @@
 
 #include "../../include/smla.h"
 #include "smla_internal.h"
+#include "smla_verify.h"
 
 namespace {
 
@@ -50,6 +51,7 @@ smla_status smla_get_device_error(uint32_t* flags, int clear) {
   if (e == cudaSuccess) e = smla::decode_window_error_word(flags, clear != 0);
   if (e == cudaSuccess) e = smla::maps_error_word(flags, clear != 0);
   if (e == cudaSuccess) e = smla::cache_error_word(flags, clear != 0);
+  if (e == cudaSuccess) e = smla::tree_error_word(flags, clear != 0);
   return from_cuda(e);
 }
 
@@ -543,6 +545,53 @@ smla_status smla_mla_cache_gather(const uint8_t* kv_cache, int64_t num_slots, in
   a.out_row_stride = out_row_stride;
   return from_cuda(smla::launch_cache_gather(a, format == SMLA_CACHE_FP4, out_fp32 != 0,
                                              static_cast<cudaStream_t>(stream)));
+}
+
+static_assert(SMLA_MAX_TREE_NODES == smla::kMaxTreeNodes, "header and kernels agree on a tree's size");
+
+smla_status smla_tree_maps(const int32_t* parents, const int32_t* row_start,
+                           const int32_t* prefix_lens, int32_t B, int32_t T, int32_t max_nodes,
+                           uint64_t* masks, int32_t* positions, void* stream) {
+  if (B < 0 || T < 0 || max_nodes < 1) return SMLA_ERR_INVALID_ARG;
+  if (max_nodes > SMLA_MAX_TREE_NODES) return SMLA_ERR_UNSUPPORTED;
+  if (T == 0) return SMLA_OK;
+  if (!parents || !row_start || !masks || (positions && B > 0 && !prefix_lens)) return SMLA_ERR_INVALID_ARG;
+  if (misaligned(parents, 4) || misaligned(row_start, 4) || misaligned(prefix_lens, 4) ||
+      misaligned(masks, 8) || misaligned(positions, 4))
+    return SMLA_ERR_INVALID_ARG;
+  const smla::TreeMapsArgs a = {parents, row_start, prefix_lens, B, T, max_nodes, masks, positions};
+  return from_cuda(smla::launch_tree_maps(a, static_cast<cudaStream_t>(stream)));
+}
+
+smla_status smla_tree_accept(const int32_t* parents, const int32_t* tokens, const int32_t* targets,
+                             const int32_t* row_start, int32_t B, int32_t T, int32_t* accepted,
+                             int32_t* rows, int32_t* next_tokens, void* stream) {
+  if (B < 0 || T < 0) return SMLA_ERR_INVALID_ARG;
+  if (B > SMLA_MAX_STEP_REQS) return SMLA_ERR_UNSUPPORTED;
+  if (B == 0 && T == 0) return SMLA_OK;
+  if ((T > 0 && (!parents || !tokens || !targets || !rows)) || !row_start ||
+      (B > 0 && (!accepted || !next_tokens)))
+    return SMLA_ERR_INVALID_ARG;
+  if (misaligned(parents, 4) || misaligned(tokens, 4) || misaligned(targets, 4) ||
+      misaligned(row_start, 4) || misaligned(accepted, 4) || misaligned(rows, 4) ||
+      misaligned(next_tokens, 4))
+    return SMLA_ERR_INVALID_ARG;
+  const smla::TreeAcceptArgs a = {parents, tokens, targets, row_start, B, T, accepted, rows, next_tokens};
+  return from_cuda(smla::launch_tree_accept(a, static_cast<cudaStream_t>(stream)));
+}
+
+smla_status smla_mla_cache_move(int32_t format, uint8_t* kv_cache, int64_t num_slots,
+                                const int32_t* rows, int32_t N, const int32_t* src_slots, int32_t T,
+                                const int32_t* dst_slots, void* stream) {
+  if (N < 0 || T < 0 || num_slots < 0 || (format != SMLA_CACHE_FP8 && format != SMLA_CACHE_FP4))
+    return SMLA_ERR_INVALID_ARG;
+  if (N == 0) return SMLA_OK;
+  if (!kv_cache || !rows || (T > 0 && !src_slots) || !dst_slots) return SMLA_ERR_INVALID_ARG;
+  if (misaligned(kv_cache, 16) || misaligned(rows, 4) || misaligned(src_slots, 4) ||
+      misaligned(dst_slots, 4))
+    return SMLA_ERR_INVALID_ARG;
+  const smla::CacheMoveArgs a = {kv_cache, num_slots, rows, N, src_slots, T, dst_slots};
+  return from_cuda(smla::launch_cache_move(a, format == SMLA_CACHE_FP4, static_cast<cudaStream_t>(stream)));
 }
 
 size_t smla_topk_select_workspace_size(int32_t T, int32_t L, int32_t K) {

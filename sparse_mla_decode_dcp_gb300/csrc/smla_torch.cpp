@@ -389,10 +389,75 @@ PyObject* cache_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (parents, row_start, prefix_lens, max_nodes, (masks, positions), stream)
+PyObject* tree_maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&] {
+    const at::Device dev = tensor(a[0], "parents").device();
+    const at::Tensor& parents = vec(a[0], "parents", at::kInt, dev, -1);
+    const int32_t T = size32(parents.size(0), "parents");
+    const at::Tensor& prefix = vec(a[2], "prefix_lens", at::kInt, dev, -1);
+    const int32_t B = size32(prefix.size(0), "prefix_lens"), nodes = i32(a[3]);
+    const at::Tensor& starts = vec(a[1], "row_start", at::kInt, dev, int64_t(B) + 1);
+    const Seq out(a[4], "out must be a sequence");
+    if (out.size() != 2) refuse(PyExc_ValueError, "%s must hold two tensors", "out");
+    const at::Tensor& masks = need(out[0], "masks", at::kLong, dev);
+    if (masks.dim() != 2 || masks.size(0) != T || masks.size(1) != (int64_t(nodes) + 63) / 64)
+      refuse(PyExc_ValueError, "%s must be [T, ceil(max_nodes / 64)]", "masks");
+    const at::Tensor& pos = vec(out[1], "positions", at::kInt, dev, T);
+    return launch(dev, a[5], [&](void* s) {
+      return smla_tree_maps(ptr<int32_t>(parents), ptr<int32_t>(starts), ptr<int32_t>(prefix), B, T, nodes,
+                            ptr<uint64_t>(masks), ptr<int32_t>(pos), s);
+    });
+  });
+}
+
+// (parents, tokens, targets, row_start, (accepted, rows, next_tokens), stream)
+PyObject* tree_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&] {
+    const at::Device dev = tensor(a[0], "parents").device();
+    const at::Tensor& parents = vec(a[0], "parents", at::kInt, dev, -1);
+    const int32_t T = size32(parents.size(0), "parents");
+    const at::Tensor& tokens = vec(a[1], "tokens", at::kInt, dev, T);
+    const at::Tensor& targets = vec(a[2], "targets", at::kInt, dev, T);
+    const at::Tensor& starts = vec(a[3], "row_start", at::kInt, dev, -1);
+    if (starts.size(0) < 1) refuse(PyExc_ValueError, "%s must be [B + 1]", "row_start");
+    const int32_t B = size32(starts.size(0) - 1, "row_start");
+    const Seq out(a[4], "out must be a sequence");
+    if (out.size() != 3) refuse(PyExc_ValueError, "%s must hold three tensors", "out");
+    const at::Tensor& accepted = vec(out[0], "accepted", at::kInt, dev, B);
+    const at::Tensor& rows = vec(out[1], "rows", at::kInt, dev, T);
+    const at::Tensor& next = vec(out[2], "next_tokens", at::kInt, dev, B);
+    return launch(dev, a[5], [&](void* s) {
+      return smla_tree_accept(ptr<int32_t>(parents), ptr<int32_t>(tokens), ptr<int32_t>(targets),
+                              ptr<int32_t>(starts), B, T, ptr<int32_t>(accepted), ptr<int32_t>(rows),
+                              ptr<int32_t>(next), s);
+    });
+  });
+}
+
+// (kv_cache, rows, src_slots, dst_slots, stream)
+PyObject* cache_move(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 5, [&] {
+    const at::Tensor& cache = tensor(a[0], "kv_cache");
+    const at::Device dev = cache.device();
+    const int32_t fmt = cache_format(cache, "kv_cache", dev);
+    const at::Tensor& rows = vec(a[1], "rows", at::kInt, dev, -1);
+    const int32_t N = size32(rows.size(0), "rows");
+    const at::Tensor& src = vec(a[2], "src_slots", at::kInt, dev, -1);
+    const int32_t T = size32(src.size(0), "src_slots");
+    const at::Tensor& dst = vec(a[3], "dst_slots", at::kInt, dev, N);
+    return launch(dev, a[4], [&](void* s) {
+      return smla_mla_cache_move(fmt, ptr<uint8_t>(cache), cache.size(0), ptr<int32_t>(rows), N,
+                                 ptr<int32_t>(src), T, ptr<int32_t>(dst), s);
+    });
+  });
+}
+
 #define SMLA_FN(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {SMLA_FN(decode_fp4), SMLA_FN(decode_fused_fp4), SMLA_FN(decode_window),
                           SMLA_FN(step_maps),  SMLA_FN(cache_write),      SMLA_FN(cache_gather),
+                          SMLA_FN(tree_maps),  SMLA_FN(tree_accept),      SMLA_FN(cache_move),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_smla_torch", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

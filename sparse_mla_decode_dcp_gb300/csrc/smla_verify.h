@@ -1,0 +1,49 @@
+// Internal launcher interface of the verification step's operators (drafted
+// trees) and of the 8-bit products.  Not installed; the public surface is
+// include/smla.h.
+#pragma once
+
+#include "smla_internal.h"
+
+namespace smla {
+
+// Nodes of one request's tree; the walk and the masks hold a node's index in
+// 8 bits and in up to four 64-bit words.
+constexpr int kMaxTreeNodes = 256;
+
+struct TreeMapsArgs {
+  const int32_t* parents;      // [T]
+  const int32_t* row_start;    // [B + 1]
+  const int32_t* prefix_lens;  // [B] (with positions)
+  int32_t B, T, max_nodes;
+  uint64_t* masks;             // [T, ceil(max_nodes / 64)]
+  int32_t* positions;          // [T] or null
+};
+
+struct TreeAcceptArgs {
+  const int32_t* parents;      // [T]
+  const int32_t* tokens;       // [T]
+  const int32_t* targets;      // [T]
+  const int32_t* row_start;    // [B + 1]
+  int32_t B, T;
+  int32_t* accepted;           // [B]
+  int32_t* rows;               // [T]
+  int32_t* next_tokens;        // [B]
+};
+
+struct CacheMoveArgs {
+  uint8_t* kv_cache;
+  int64_t num_slots;
+  const int32_t* rows;         // [N], -1 = nothing
+  int32_t N;
+  const int32_t* src_slots;    // [T]
+  int32_t T;
+  const int32_t* dst_slots;    // [N], -1 = another cache's
+};
+
+cudaError_t launch_tree_maps(const TreeMapsArgs& a, cudaStream_t s);
+cudaError_t launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t s);
+cudaError_t launch_cache_move(const CacheMoveArgs& a, bool fp4, cudaStream_t s);
+cudaError_t tree_error_word(uint32_t* flags, bool clear);
+
+}  // namespace smla
