@@ -49,6 +49,12 @@
  *   smla_tree_accept                  the nodes the model agrees with
  *   smla_mla_cache_move               their cache rows, to their own slots
  *
+ * and the projections around the attention, in 8 bits:
+ *
+ *   smla_fp8_quantise                 bf16 rows to e4m3, a scale for 128
+ *   smla_fp8_matmul                   their product with e4m3 weights that
+ *                                     have a scale for 128 x 128
+ *
  * Sources (page title, then section):
  *   [P1] "[eldritch] attention: support DCP in SM120 FlashInfer sparse MLA"
  *   [P2] "[Bugfix][Attention] Stabilize sparse-MLA DCP for GLM PCP evals"
@@ -753,6 +759,62 @@ smla_status smla_tree_accept(const int32_t* parents, const int32_t* tokens, cons
 smla_status smla_mla_cache_move(int32_t format, uint8_t* kv_cache, int64_t num_slots,
                                 const int32_t* rows, int32_t N, const int32_t* src_slots, int32_t T,
                                 const int32_t* dst_slots, void* stream);
+
+/*
+ * Rows to 8 bits: for each of G batches' M rows and each group of 128 columns
+ * (the last may be shorter),
+ *   scales[g, m, j] = fp32(max |x| / 448) over columns 128 j .. 128 j + 127
+ *   codes[g, m, k]  = e4m3(x[g, m, k] / scale), nearest, ties to even
+ * each rounded once.  A group whose scale is 0 or below 2^-126 has zero codes;
+ * a group with a value that is not finite has a NaN scale and zero codes.
+ *
+ *   x        device bf16; entry (g, m, k) at g * batch + m * row + k (strides
+ *            in elements; 16-byte aligned rows load fastest)
+ *   codes    device uint8 (e4m3) output, the same with its own strides
+ *   scales   device fp32 output, entry (g, m, j) at g * batch + m * row +
+ *            j * col
+ * Errors: INVALID_ARG for G < 0, M < 0, K < 1, a negative stride, NULL or
+ * misaligned arrays.  G = 0 or M = 0 is a no-op.
+ */
+smla_status smla_fp8_quantise(const uint16_t* x, int64_t x_batch_stride, int64_t x_row_stride, int32_t G,
+                              int32_t M, int32_t K, uint8_t* codes, int64_t codes_batch_stride,
+                              int64_t codes_row_stride, float* scales, int64_t scales_batch_stride,
+                              int64_t scales_row_stride, int64_t scales_col_stride, void* stream);
+
+/*
+ * 8-bit matrix product with block scales, for each of G batches (the heads of
+ * an absorbed projection, for instance; G = 1: one product):
+ *   out[g, m, n] = sum_j a_scales[g, m, j] b_scales[g, n div 128, j]
+ *                  sum_{k = 128 j .. 128 j + 127} a[g, m, k] b[g, n, k]
+ * A group's products are summed by the tensor cores in fp32, the groups in
+ * fp32, and the result is rounded once.  M, N and K are any sizes.  A row's
+ * result does not depend on the other rows' values, and a repeated call gives
+ * the same bits.
+ *
+ *   a          device uint8 (e4m3), entry (g, m, k) at g * batch + m * row + k
+ *   a_scales   device fp32, entry (g, m, j) at g * batch + m * row + j * col
+ *              (with a col stride of M, as a [K / 128, M] matrix, they are
+ *              fetched fastest)
+ *   b          device uint8 (e4m3), entry (g, n, k) at g * batch + n * row + k
+ *   b_scales   device fp32, entry (g, n div 128, j) by their strides
+ *   out        device bf16 (out_fp32 = 0) or fp32, entry (g, m, n) at
+ *              g * batch + m * row + n
+ * a and b are 16-byte aligned, with row strides of at least K and row and
+ * (G > 1) batch strides that are positive multiples of 16.  Strides of
+ * scales may be 0 (a shared scale).  out may not alias an input, nor its own
+ * entries each other.
+ * Errors: INVALID_ARG for G < 0, M < 0, N < 0, K < 1, a bad stride, NULL or
+ * misaligned arrays; UNSUPPORTED for strides of 2^40 bytes and more and for
+ * more than 2^27 tiles of 16 x 128 results.  G, M or N = 0 is a no-op.
+ */
+smla_status smla_fp8_matmul(const uint8_t* a, int64_t a_batch_stride, int64_t a_row_stride,
+                            const float* a_scales, int64_t a_scales_batch_stride,
+                            int64_t a_scales_row_stride, int64_t a_scales_col_stride, const uint8_t* b,
+                            int64_t b_batch_stride, int64_t b_row_stride, const float* b_scales,
+                            int64_t b_scales_batch_stride, int64_t b_scales_row_stride,
+                            int64_t b_scales_col_stride, int32_t G, int32_t M, int32_t N, int32_t K,
+                            void* out, int64_t out_batch_stride, int64_t out_row_stride, int32_t out_fp32,
+                            void* stream);
 
 #ifdef __cplusplus
 } /* extern "C" */

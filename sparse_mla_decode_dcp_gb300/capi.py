@@ -105,6 +105,12 @@ SIGNATURES = {
         _c_vp, _c_vp, _c_vp, _c_vp, _c_i32, _c_i32, _c_vp, _c_vp, _c_vp, _c_vp]),
     "smla_mla_cache_move": (ctypes.c_int, [
         _c_i32, _c_vp, _c_i64, _c_vp, _c_i32, _c_vp, _c_i32, _c_vp, _c_vp]),
+    "smla_fp8_quantise": (ctypes.c_int, [
+        _c_vp, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64,
+        _c_i64, _c_vp]),
+    "smla_fp8_matmul": (ctypes.c_int, [
+        _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64,
+        _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _c_vp, _c_i64, _c_i64, _c_i32, _c_vp]),
 }
 
 _lib = None
@@ -812,3 +818,52 @@ def mla_cache_move(kv_cache: torch.Tensor, rows: torch.Tensor, src_slots: torch.
     _check("smla_mla_cache_move",
            _native().cache_move(kv_cache, rows, src_slots, dst_slots, stream))
     return kv_cache
+
+
+# --------------------------------------------------------------------------
+# The projections around the attention in 8 bits: matrices [M, K], or batches
+# of them [G, M, K] (a product for each head, say), with contiguous rows.
+# --------------------------------------------------------------------------
+class Fp8Rows(NamedTuple):
+    """Rows in 8 bits: codes float8_e4m3fn [.., M, K], scales fp32
+    [.., M, ceil(K / 128)], one for each 128 columns."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def alloc_fp8_rows(shape: Sequence[int], device,
+                   stream: Optional[torch.cuda.Stream] = None) -> Fp8Rows:
+    """Buffers for rows of shape [M, K] or [G, M, K], laid out as fp8_matmul
+    takes them fastest: code rows a multiple of 16 bytes apart, scales with
+    neighbouring rows side by side."""
+    *batch, M, K = shape
+    codes = _new((*batch, M, -(-K // 16) * 16), torch.float8_e4m3fn, device, stream)[..., :K]
+    scales = _new((*batch, -(-K // 128), M), torch.float32, device, stream).transpose(-1, -2)
+    return Fp8Rows(codes, scales)
+
+
+def fp8_quantise(x: torch.Tensor, *, out: Optional[Fp8Rows] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> Fp8Rows:
+    """Rows x (bf16, [M, K] or [G, M, K], any row and batch strides) in 8 bits:
+    scale = max |x| / 448 of each 128 columns, code = e4m3(x / scale)."""
+    if out is None:
+        if x.dim() not in (2, 3):
+            raise ValueError("x must be a matrix or a batch of them")
+        out = alloc_fp8_rows(x.shape, x.device, stream)
+    _check("smla_fp8_quantise", _native().fp8_quantise(x, out[0], out[1], stream))
+    return out
+
+
+def fp8_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor, *,
+               out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """a [M, K] times b [N, K] transposed (or batches of them), both
+    float8_e4m3fn with rows a multiple of 16 bytes apart; a_scales [M,
+    ceil(K / 128)], b_scales [ceil(N / 128), ceil(K / 128)].  Returns bf16 or
+    fp32 [M, N]; `out` may have any row and batch strides."""
+    if out is None:
+        if a.dim() not in (2, 3) or b.dim() != a.dim():
+            raise ValueError("a and b must be matrices or batches of them")
+        out = _new((*a.shape[:-1], b.shape[-2]), dtype, a.device, stream)
+    _check("smla_fp8_matmul", _native().fp8_matmul(a, a_scales, b, b_scales, out, stream))
+    return out

@@ -52,6 +52,7 @@ smla_status smla_get_device_error(uint32_t* flags, int clear) {
   if (e == cudaSuccess) e = smla::maps_error_word(flags, clear != 0);
   if (e == cudaSuccess) e = smla::cache_error_word(flags, clear != 0);
   if (e == cudaSuccess) e = smla::tree_error_word(flags, clear != 0);
+  if (e == cudaSuccess) e = smla::matmul_error_word(flags, clear != 0);
   return from_cuda(e);
 }
 
@@ -592,6 +593,69 @@ smla_status smla_mla_cache_move(int32_t format, uint8_t* kv_cache, int64_t num_s
     return SMLA_ERR_INVALID_ARG;
   const smla::CacheMoveArgs a = {kv_cache, num_slots, rows, N, src_slots, T, dst_slots};
   return from_cuda(smla::launch_cache_move(a, format == SMLA_CACHE_FP4, static_cast<cudaStream_t>(stream)));
+}
+
+smla_status smla_fp8_quantise(const uint16_t* x, int64_t x_batch_stride, int64_t x_row_stride, int32_t G,
+                              int32_t M, int32_t K, uint8_t* codes, int64_t codes_batch_stride,
+                              int64_t codes_row_stride, float* scales, int64_t scales_batch_stride,
+                              int64_t scales_row_stride, int64_t scales_col_stride, void* stream) {
+  if (G < 0 || M < 0 || K < 1 || x_batch_stride < 0 || x_row_stride < 0 || codes_batch_stride < 0 ||
+      codes_row_stride < 0 || scales_batch_stride < 0 || scales_row_stride < 0 || scales_col_stride < 0)
+    return SMLA_ERR_INVALID_ARG;
+  if (G == 0 || M == 0) return SMLA_OK;
+  if (!x || !codes || !scales || misaligned(x, 2) || misaligned(scales, 4)) return SMLA_ERR_INVALID_ARG;
+  const smla::QuantiseArgs a = {x, {x_batch_stride, x_row_stride, 1}, G, M, K,
+                                codes, {codes_batch_stride, codes_row_stride, 1},
+                                scales, {scales_batch_stride, scales_row_stride, scales_col_stride}};
+  return from_cuda(smla::launch_fp8_quantise(a, static_cast<cudaStream_t>(stream)));
+}
+
+// Strides of a batch of code matrices that the tensor maps take.
+static smla_status code_strides(const uint8_t* p, int64_t batch, int64_t row, int32_t G, int32_t K) {
+  if (!p || misaligned(p, 16) || row < K || row % 16 != 0 || (G > 1 && (batch < 1 || batch % 16 != 0)))
+    return SMLA_ERR_INVALID_ARG;
+  constexpr int64_t kMost = int64_t(1) << 40;
+  return row >= kMost || (G > 1 && batch >= kMost) ? SMLA_ERR_UNSUPPORTED : SMLA_OK;
+}
+
+smla_status smla_fp8_matmul(const uint8_t* a, int64_t a_batch_stride, int64_t a_row_stride,
+                            const float* a_scales, int64_t a_scales_batch_stride,
+                            int64_t a_scales_row_stride, int64_t a_scales_col_stride, const uint8_t* b,
+                            int64_t b_batch_stride, int64_t b_row_stride, const float* b_scales,
+                            int64_t b_scales_batch_stride, int64_t b_scales_row_stride,
+                            int64_t b_scales_col_stride, int32_t G, int32_t M, int32_t N, int32_t K,
+                            void* out, int64_t out_batch_stride, int64_t out_row_stride, int32_t out_fp32,
+                            void* stream) {
+  if (G < 0 || M < 0 || N < 0 || K < 1 || a_scales_batch_stride < 0 || a_scales_row_stride < 0 ||
+      a_scales_col_stride < 0 || b_scales_batch_stride < 0 || b_scales_row_stride < 0 ||
+      b_scales_col_stride < 0 || out_batch_stride < 0 || out_row_stride < 0)
+    return SMLA_ERR_INVALID_ARG;
+  if (G == 0 || M == 0 || N == 0) return SMLA_OK;
+  smla_status st = code_strides(a, a_batch_stride, a_row_stride, G, K);
+  if (st == SMLA_OK) st = code_strides(b, b_batch_stride, b_row_stride, G, K);
+  if (st != SMLA_OK) return st;
+  if (!a_scales || !b_scales || !out || misaligned(a_scales, 4) || misaligned(b_scales, 4) ||
+      misaligned(out, out_fp32 ? 4 : 2) || (M > 1 && out_row_stride < 1) || (G > 1 && out_batch_stride < 1))
+    return SMLA_ERR_INVALID_ARG;
+  if (int64_t(G) * (int64_t(M) / 16 + 1) * (int64_t(N) / 128 + 1) > (int64_t(1) << 27))
+    return SMLA_ERR_UNSUPPORTED;
+  smla::MatmulArgs m{};
+  m.a = a;
+  m.as = {a_batch_stride, a_row_stride, 1};
+  m.a_scales = a_scales;
+  m.ass = {a_scales_batch_stride, a_scales_row_stride, a_scales_col_stride};
+  m.b = b;
+  m.bs = {b_batch_stride, b_row_stride, 1};
+  m.b_scales = b_scales;
+  m.bss = {b_scales_batch_stride, b_scales_row_stride, b_scales_col_stride};
+  m.G = G;
+  m.M = M;
+  m.N = N;
+  m.K = K;
+  m.out = out;
+  m.os = {out_batch_stride, out_row_stride, 1};
+  m.out_fp32 = out_fp32 != 0;
+  return from_cuda(smla::launch_fp8_matmul(m, static_cast<cudaStream_t>(stream)));
 }
 
 size_t smla_topk_select_workspace_size(int32_t T, int32_t L, int32_t K) {

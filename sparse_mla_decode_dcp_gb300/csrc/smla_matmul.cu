@@ -1,0 +1,504 @@
+// 8-bit matrix product with a scale for each block of 128: for each batch
+// entry,
+//   out[m, n] = sum_g sa[m, g] sb[n / 128, g] sum_{k in group g} a[m, k] b[n, k]
+// with e4m3 codes a (rows of activations, one scale for 128 columns) and b
+// (weights, one scale for 128 x 128), groups of 128 k.
+//
+// The tensor cores sum one group at a time: a scale is any fp32 number, so the
+// group's sums come back from tensor memory and are added, times their scale,
+// to fp32 sums in registers while the next group's MMAs run (two accumulators
+// in turn).  TMA brings a group's codes as 128-byte rows in the MMA's
+// swizzle, several groups ahead.
+//
+// One operand's rows are the MMA's 128 lanes, the other's its columns.  Many
+// activation rows lie along the lanes (kSwap false, tiles of 128 x 128); up to
+// 64 of them along the columns, where a tile of 16, 32 or 64 wastes little,
+// and the weights' rows along the lanes: such a call is bound by the weights'
+// bytes.  A weight tile of 128 rows has one scale a group either way.
+//
+// With few tiles the groups are split over the CTAs of a cluster, whose sums
+// meet through distributed shared memory in the order of their groups.
+//
+// Warps: 0 loads (one lane), 1 issues the MMAs (one lane), 2 holds tensor
+// memory, 4 and up read the sums.  Every wait is bounded; one that gives up
+// sets SMLA_DEVERR_TIMEOUT and the CTA unwinds.
+#include <cuda_bf16.h>
+
+#include <atomic>
+#include <mutex>
+
+#include "../../include/smla.h"
+#include "smla_pair.cuh"
+#include "smla_verify.h"
+
+namespace smla {
+namespace {
+
+using namespace sm100;
+
+__device__ unsigned int g_matmul_error;
+
+constexpr int kGroup = 128;        // k of a scale, bytes of a tile's row
+constexpr int kLaneRows = 128;
+constexpr int kScaleChunk = 16;    // groups whose scales are fetched together
+constexpr int kMaxStages = 8;
+constexpr int kMaxSplits = 8;
+
+struct Ctl {
+  uint64_t full[kMaxStages], empty[kMaxStages], sum_full[2], sum_empty[2], end;
+  uint32_t tbase;
+  int abort;
+};
+
+template <bool kSwap, int kCols>
+struct Shape {
+  static constexpr int kSumWarps = kSwap ? 4 : 8;
+  static constexpr int kThreads = 32 * (4 + kSumWarps);
+  static constexpr int kPerThread = kCols * 4 / kSumWarps;  // sums of a thread
+  static constexpr int kStageBytes = (kLaneRows + kCols) * kGroup;
+  static constexpr int kScaled = kSwap ? kCols : kLaneRows;  // activation rows of a tile
+  static constexpr int kScaleBytes = 2 * kScaleChunk * kScaled * 4;
+  static constexpr int kPitch = kSwap ? kLaneRows : kCols + 4;  // of the exchanged sums
+  static constexpr int kExchange = (kSwap ? kCols : kLaneRows) * kPitch * 4;
+  static constexpr uint32_t kTmemCols = 2 * kCols < 32 ? 32 : 2 * kCols;
+};
+
+template <int kCount>
+__device__ __forceinline__ void load_sums(uint32_t addr, uint32_t* r) {
+  if constexpr (kCount == 32) tmem_ld32(addr, r);
+  else tmem_ld16(addr, r);
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float x, float y) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// kN consecutive results of row m from column n (a multiple of kN) on.  A
+// single one is stored by itself; more as wide as a.vec says the rows are
+// aligned (2: to 32 bytes, 1: to 16), one by one at the end of a row.
+template <int kN>
+__device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t g, int32_t m, int32_t n,
+                                          const float* v) {
+  static_assert(kN == 1 || kN == 4 || kN % 16 == 0, "whole vectors");
+  const int64_t at = g * a.os.batch + int64_t(m) * a.os.rows + n;
+  float* of = static_cast<float*>(a.out) + at;
+  __nv_bfloat16* oh = static_cast<__nv_bfloat16*>(a.out) + at;
+  if constexpr (kN >= 4) {
+    if (a.vec && n + kN <= a.N) {
+      if (a.out_fp32) {
+#pragma unroll
+        for (int j = 0; j < kN; j += 4)
+          *reinterpret_cast<float4*>(of + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        return;
+      }
+      if constexpr (kN >= 16) {
+        if (a.vec == 2) {  // whole sectors
+#pragma unroll
+          for (int j = 0; j < kN; j += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = bf16x2(v[j + 2 * i], v[j + 2 * i + 1]);
+            stg256(oh + j, w);
+          }
+          return;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kN; j += 4)
+        *reinterpret_cast<uint2*>(oh + j) = make_uint2(bf16x2(v[j], v[j + 1]), bf16x2(v[j + 2], v[j + 3]));
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kN; ++j) {
+    if (n + j >= a.N) continue;
+    if (a.out_fp32) of[j] = v[j];
+    else oh[j] = __float2bfloat16_rn(v[j]);
+  }
+}
+
+template <bool kSwap, int kCols>
+__global__ void __launch_bounds__(Shape<kSwap, kCols>::kThreads, kSwap ? 2 : 1)
+    fp8_matmul_kernel(const __grid_constant__ MatmulArgs a) {
+  using S = Shape<kSwap, kCols>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Ctl ctl;
+  __shared__ __align__(16) float scales[2][kScaleChunk][S::kScaled];
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  volatile int* abort = &ctl.abort;
+
+  // this CTA's tile and its share of the groups
+  const uint32_t split = blockIdx.x % uint32_t(a.splits);
+  const uint32_t tile = blockIdx.x / uint32_t(a.splits);
+  const uint32_t per_batch = uint32_t(a.m_tiles) * uint32_t(a.n_tiles);
+  const uint32_t g = tile / per_batch;
+  const uint32_t in_batch = tile - g * per_batch;
+  const int32_t n_tile = int32_t(in_batch / uint32_t(a.m_tiles));
+  const int32_t m_tile = int32_t(in_batch - uint32_t(n_tile) * uint32_t(a.m_tiles));
+  const int32_t m0 = m_tile * (kSwap ? kCols : kLaneRows);
+  const int32_t n0 = n_tile * 128;
+  const int kb0 = int(int64_t(a.k_blocks) * split / a.splits);
+  const int kbs = int(int64_t(a.k_blocks) * (split + 1) / a.splits) - kb0;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&a.a_map);
+    prefetch_tensormap(&a.b_map);
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.sum_full[i], 1);
+      mbar_init(&ctl.sum_empty[i], S::kSumWarps);
+    }
+    mbar_init(&ctl.end, 1);
+    ctl.abort = 0;
+    fence_mbar_init_cluster();
+  }
+  if (warp == 2) {
+    tmem_alloc(&ctl.tbase, S::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = ctl.tbase;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  float acc[S::kPerThread];
+  bool ok = true;
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t sm0 = smem_u32(sm);
+      int s = 0;
+      uint32_t lap = 0;  // of the stages
+      int i = 0;
+      for (; i < kbs; ++i) {
+        if (lap > 0 && !wait_bounded(&ctl.empty[s], (lap - 1) & 1, abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT))
+          break;
+        const uint32_t at = sm0 + s * S::kStageBytes;
+        mbar_arrive_expect_tx(&ctl.full[s], S::kStageBytes);
+        const int32_t x = (kb0 + i) * kGroup;
+        tma_load_3d(at, kSwap ? &a.b_map : &a.a_map, x, kSwap ? n0 : m0, int32_t(g), &ctl.full[s]);
+        tma_load_3d(at + kLaneRows * kGroup, kSwap ? &a.a_map : &a.b_map, x, kSwap ? m0 : n0, int32_t(g),
+                    &ctl.full[s]);
+        if (++s == a.stages) {
+          s = 0;
+          ++lap;
+        }
+      }
+      // the CTA leaves when its loads have landed, whatever became of the rest
+      int no_abort = 0;
+      for (int j = max(0, i - a.stages); j < i; ++j)
+        wait_bounded(&ctl.full[j % a.stages], (j / a.stages) & 1, &no_abort, &g_matmul_error,
+                     SMLA_DEVERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = idesc_f16_f32(128, kCols, false, false);
+    const bool leader = elect_one();
+    int issued = 0;
+    int s = 0;
+    uint32_t lap = 0;
+    for (int i = 0; i < kbs; ++i) {
+      const int b = i & 1;
+      bool go = wait_bounded(&ctl.full[s], lap & 1, abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT);
+      if (go && i >= 2)
+        go = wait_bounded(&ctl.sum_empty[b], ((i >> 1) - 1) & 1, abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT);
+      if (!__all_sync(0xffffffffu, go)) break;
+      tc_fence_after();
+      if (leader) {
+        const uint32_t at = smem_u32(sm) + s * S::kStageBytes;
+        const uint64_t ad = sdesc_sw128(at, 16, 1024);
+        const uint64_t bd = sdesc_sw128(at + kLaneRows * kGroup, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < kGroup / 32; ++k)
+          mma_ss_f8(tb + b * kCols, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+        mma_commit(&ctl.empty[s]);
+        mma_commit(&ctl.sum_full[b]);
+      }
+      __syncwarp();
+      ++issued;
+      if (++s == a.stages) {
+        s = 0;
+        ++lap;
+      }
+    }
+    // every MMA has completed before tensor memory is given back
+    if (issued > 0) {
+      if (leader) mma_commit(&ctl.end);
+      __syncwarp();
+      int no_abort = 0;
+      wait_bounded(&ctl.end, 0, &no_abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT);
+    }
+  } else if (warp >= 4) {
+    const int t = tid - 128;
+    const int quad = warp & 3;
+    const int half = (warp - 4) >> 2;  // which columns, with eight warps
+    const int row = 32 * quad + lane;
+    uint64_t sum[S::kPerThread / 2];
+#pragma unroll
+    for (int j = 0; j < S::kPerThread / 2; ++j) sum[j] = 0;
+    // a chunk's scales sa sb are fetched into registers while the chunk before
+    // it is summed
+    constexpr int kSumThreads = 32 * S::kSumWarps;
+    constexpr int kFetch = (kScaleChunk * S::kScaled + kSumThreads - 1) / kSumThreads;
+    float next[kFetch];
+    auto fetch = [&](int i0) {
+#pragma unroll
+      for (int f = 0; f < kFetch; ++f) {
+        const int e = t + kSumThreads * f;
+        const int k = i0 + e / S::kScaled;
+        const int m = m0 + e % S::kScaled;
+        next[f] = 0.f;
+        if (e < kScaleChunk * S::kScaled && k < kbs && m < a.M)
+          next[f] = a.a_scales[int64_t(g) * a.ass.batch + int64_t(m) * a.ass.rows + (kb0 + k) * a.ass.cols] *
+                    a.b_scales[int64_t(g) * a.bss.batch + n_tile * a.bss.rows + (kb0 + k) * a.bss.cols];
+      }
+    };
+    fetch(0);
+    for (int i = 0; i < kbs; ++i) {
+      const int chunk = i / kScaleChunk;
+      if (i % kScaleChunk == 0) {
+        // the buffer's last readers are two chunks back, before the barrier of
+        // the chunk between
+#pragma unroll
+        for (int f = 0; f < kFetch; ++f) {
+          const int e = t + kSumThreads * f;
+          if (e < kScaleChunk * S::kScaled) (&scales[chunk & 1][0][0])[e] = next[f];
+        }
+        named_bar_sync(1, kSumThreads);
+        fetch(i + kScaleChunk);
+      }
+      const int b = i & 1;
+      ok = __all_sync(0xffffffffu, wait_bounded(&ctl.sum_full[b], (i >> 1) & 1, abort, &g_matmul_error,
+                                                SMLA_DEVERR_TIMEOUT));
+      // a warp that gives up goes on to the barriers with what it has
+      if (ok) {
+        tc_fence_after();
+        const uint32_t at = tmem_addr(tb, 32 * quad, b * kCols + half * S::kPerThread);
+        const float* sc = scales[chunk & 1][i % kScaleChunk];
+        constexpr int kStep = S::kPerThread < 32 ? S::kPerThread : 32;
+#pragma unroll
+        for (int c = 0; c < S::kPerThread; c += kStep) {
+          uint32_t r[kStep];
+          load_sums<kStep>(at + c, r);
+          tmem_ld_wait();
+          if (c + kStep == S::kPerThread) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.sum_empty[b]);
+          }
+#pragma unroll
+          for (int j = 0; j < kStep / 2; ++j) {
+            uint64_t s2;
+            if constexpr (kSwap) {
+              const float2 f = *reinterpret_cast<const float2*>(sc + c + 2 * j);
+              s2 = pack2(f.x, f.y);
+            } else {
+              s2 = pack2(sc[row], sc[row]);
+            }
+            sum[c / 2 + j] = fma2(pack2(r[2 * j], r[2 * j + 1]), s2, sum[c / 2 + j]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < S::kPerThread / 2; ++j) {
+      const float2 f = unpack2(sum[j]);
+      acc[2 * j] = f.x;
+      acc[2 * j + 1] = f.y;
+    }
+    if (a.splits == 1) {
+      if constexpr (kSwap) {
+        const int32_t n = n0 + row;
+        if (n < a.N) {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            if (m0 + j < a.M) store_row<1>(a, g, m0 + j, n, acc + j);
+        }
+      } else if (m0 + row < a.M) {
+        store_row<S::kPerThread>(a, g, m0 + row, n0 + half * S::kPerThread, acc);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) tmem_dealloc(tb, S::kTmemCols);
+  if (a.splits == 1) return;
+
+  // the cluster's sums, through the operand stages (every load of theirs has
+  // been consumed)
+  const uint32_t mine = smem_u32(sm);
+  if (warp >= 4) {
+    const int row = 32 * (warp & 3) + lane;
+    const int half = (warp - 4) >> 2;
+    float* x = reinterpret_cast<float*>(sm);
+    if constexpr (kSwap) {
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) x[j * S::kPitch + row] = acc[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < S::kPerThread; j += 4)
+        *reinterpret_cast<float4*>(x + row * S::kPitch + half * S::kPerThread + j) =
+            make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+    }
+  }
+  cluster_sync();
+  // four columns of the output a thread, this CTA's share of the tile
+  constexpr int kRowsOut = kSwap ? kCols : kLaneRows;   // output rows of the tile
+  constexpr int kQuads = (kSwap ? kLaneRows : kCols) / 4;
+  for (int e = int(split) * S::kThreads + tid; e < kRowsOut * kQuads; e += a.splits * S::kThreads) {
+    const int i = e / kQuads;
+    const int c = 4 * (e % kQuads);
+    float v[4] = {};
+    for (int s = 0; s < a.splits; ++s) {
+      const float4 p = ld_cluster_f4(map_to_cta(mine + uint32_t(i * S::kPitch + c) * 4, uint32_t(s)));
+      v[0] += p.x;
+      v[1] += p.y;
+      v[2] += p.z;
+      v[3] += p.w;
+    }
+    if (m0 + i < a.M && n0 + c < a.N) store_row<4>(a, g, m0 + i, n0 + c, v);
+  }
+  cluster_sync();  // nobody's sums go while they are read
+}
+
+// cuTensorMapEncodeTiled, looked up once through the runtime.
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+cudaError_t encode_fn(EncodeFn* fn) {
+  static std::mutex m;
+  static EncodeFn cached = nullptr;
+  std::lock_guard<std::mutex> lock(m);
+  if (cached == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || p == nullptr) return cudaErrorNotSupported;
+    cached = reinterpret_cast<EncodeFn>(p);
+  }
+  *fn = cached;
+  return cudaSuccess;
+}
+
+// Boxes of 128 columns x `box_rows` rows of a batch of code matrices, in the
+// 128-byte swizzle; columns and rows past the end read as zeros.
+cudaError_t encode_codes(CUtensorMap* map, const uint8_t* p, const Strides& st, int32_t G, int32_t rows,
+                         int32_t K, uint32_t box_rows) {
+  EncodeFn enc = nullptr;
+  const cudaError_t e = encode_fn(&enc);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t dims[3] = {cuuint64_t(K), cuuint64_t(rows), cuuint64_t(G)};
+  const cuuint64_t strides[2] = {cuuint64_t(st.rows), cuuint64_t(G > 1 ? st.batch : st.rows)};
+  const cuuint32_t box[3] = {kGroup, box_rows, 1}, ones[3] = {1, 1, 1};
+  if (enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(p), dims, strides, box, ones,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  return cudaSuccess;
+}
+
+constexpr int kSms = 152;
+
+template <bool kSwap, int kCols>
+cudaError_t launch(MatmulArgs& a, cudaStream_t s) {
+  using S = Shape<kSwap, kCols>;
+  constexpr int kMaxSmem = kMaxStages * S::kStageBytes < 180 * 1024 ? kMaxStages * S::kStageBytes : 180 * 1024;
+  static_assert(S::kExchange <= kMaxSmem, "the exchanged sums fit");
+  // shared-memory limit, once per device
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool tracked = dev >= 0 && dev < 64;
+  if (!tracked || !done[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(fp8_matmul_kernel<kSwap, kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMaxSmem + 1024);
+    if (e != cudaSuccess) return e;
+    if (tracked) done[dev].store(true, std::memory_order_release);
+  }
+  a.m_tiles = int32_t((int64_t(a.M) + (kSwap ? kCols : kLaneRows) - 1) / (kSwap ? kCols : kLaneRows));
+  const int64_t tiles = int64_t(a.G) * a.m_tiles * a.n_tiles;
+  a.splits = 1;
+  while (a.splits < kMaxSplits && tiles * a.splits * 2 <= kSms && a.k_blocks >= 4 * a.splits) a.splits *= 2;
+  if (tiles * a.splits > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int per_split = (a.k_blocks + a.splits - 1) / a.splits;
+  const int most = kMaxSmem / S::kStageBytes;
+  a.stages = per_split < most ? per_split : most;
+  size_t smem = size_t(a.stages) * S::kStageBytes;
+  if (a.splits > 1 && smem < size_t(S::kExchange)) smem = S::kExchange;
+  // As many CTAs on an SM as tensor memory holds and no more: one that waited
+  // for another's would hold up its cluster, which may hold up that one.
+  constexpr size_t kResident = 512 / S::kTmemCols;
+  constexpr size_t kStatic = S::kScaleBytes + sizeof(Ctl);
+  const size_t least = size_t(228 * 1024) / (kResident + 1) + 1;
+  if (smem + 1024 + kStatic < least) smem = least - 1024 - kStatic;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(tiles * a.splits));
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = smem + 1024;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(a.splits);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, fp8_matmul_kernel<kSwap, kCols>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_matmul(const MatmulArgs& args, cudaStream_t s) {
+  MatmulArgs a = args;
+  a.k_blocks = int32_t((int64_t(a.K) + kGroup - 1) / kGroup);
+  a.n_tiles = int32_t((int64_t(a.N) + 127) / 128);
+  const int cols = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
+  cudaError_t e = encode_codes(&a.a_map, a.a, a.as, a.G, a.M, a.K, uint32_t(cols));
+  if (e == cudaSuccess) e = encode_codes(&a.b_map, a.b, a.bs, a.G, a.N, a.K, 128);
+  if (e != cudaSuccess) return e;
+  const uint64_t bytes = a.out_fp32 ? 4 : 2;
+  const uint64_t ends = reinterpret_cast<uintptr_t>(a.out) | (uint64_t(a.os.rows) * bytes) |
+                        (a.G > 1 ? uint64_t(a.os.batch) * bytes : 0);
+  a.vec = ends % 32 == 0 ? 2 : ends % 16 == 0 ? 1 : 0;
+  switch (cols) {
+    case 16: return launch<true, 16>(a, s);
+    case 32: return launch<true, 32>(a, s);
+    case 64: return launch<true, 64>(a, s);
+    default: return launch<false, 128>(a, s);
+  }
+}
+
+cudaError_t matmul_error_word(uint32_t* flags, bool clear) {
+  unsigned int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_matmul_error, sizeof(v));
+  if (e != cudaSuccess) return e;
+  *flags |= v;
+  if (clear) {
+    v = 0;
+    e = cudaMemcpyToSymbol(g_matmul_error, &v, sizeof(v));
+  }
+  return e;
+}
+
+}  // namespace smla

@@ -453,11 +453,101 @@ PyObject* cache_move(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A matrix [M, K] or a batch of them [G, M, K]; strides of one-entry
+// dimensions mean nothing.
+struct Matrix {
+  void* data;
+  int64_t G, rows, cols, batch, row, col;
+};
+
+Matrix matrix(PyObject* o, const char* name, at::Device dev, int64_t dims) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.device() != dev) refuse(PyExc_ValueError, "%s is on another device than the other tensors", name);
+  if (t.dim() != dims) refuse(PyExc_ValueError, "%s must have as many dimensions as the other tensors", name);
+  Matrix m{};
+  m.data = t.data_ptr();
+  m.G = dims == 3 ? t.size(0) : 1;
+  m.rows = t.size(dims - 2);
+  m.cols = t.size(dims - 1);
+  m.col = m.cols > 1 ? t.stride(dims - 1) : 1;
+  m.row = m.rows > 1 ? t.stride(dims - 2) : (m.cols * m.col + 15) / 16 * 16;
+  m.batch = m.G > 1 ? t.stride(0) : (m.rows * m.row + 15) / 16 * 16;
+  return m;
+}
+
+Matrix rows_of(PyObject* o, const char* name, at::ScalarType type, at::Device dev, int64_t dims) {
+  need_dtype(tensor(o, name), name, type);
+  const Matrix m = matrix(o, name, dev, dims);
+  if (m.col != 1) refuse(PyExc_ValueError, "%s must have contiguous rows", name);
+  return m;
+}
+
+Matrix scales_of(PyObject* o, const char* name, at::Device dev, int64_t dims, int64_t G, int64_t rows,
+                 int64_t cols) {
+  need_dtype(tensor(o, name), name, at::kFloat);
+  const Matrix m = matrix(o, name, dev, dims);
+  if (m.G != G || m.rows != rows || m.cols != cols)
+    refuse(PyExc_ValueError, "%s must have one entry for each block of 128", name);
+  return m;
+}
+
+int64_t dims_of(PyObject* o, const char* name) {
+  const int64_t d = tensor(o, name).dim();
+  if (d != 2 && d != 3) refuse(PyExc_ValueError, "%s must be a matrix or a batch of them", name);
+  return d;
+}
+
+int64_t blocks(int64_t n) { return (n + 127) / 128; }
+
+// (x, codes, scales, stream)
+PyObject* fp8_quantise(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 4, [&] {
+    const at::Device dev = tensor(a[0], "x").device();
+    const int64_t dims = dims_of(a[0], "x");
+    const Matrix x = rows_of(a[0], "x", at::kBFloat16, dev, dims);
+    const Matrix c = rows_of(a[1], "codes", at::kFloat8_e4m3fn, dev, dims);
+    if (c.G != x.G || c.rows != x.rows || c.cols != x.cols) refuse(PyExc_ValueError, "%s must be x's shape", "codes");
+    const Matrix s = scales_of(a[2], "scales", dev, dims, x.G, x.rows, blocks(x.cols));
+    const int32_t G = size32(x.G, "x"), M = size32(x.rows, "x"), K = size32(x.cols, "x");
+    return launch(dev, a[3], [&](void* st) {
+      return smla_fp8_quantise(static_cast<uint16_t*>(x.data), x.batch, x.row, G, M, K,
+                               static_cast<uint8_t*>(c.data), c.batch, c.row, static_cast<float*>(s.data),
+                               s.batch, s.row, s.col, st);
+    });
+  });
+}
+
+// (a, a_scales, b, b_scales, out, stream)
+PyObject* fp8_matmul(PyObject*, PyObject* const* p, Py_ssize_t n) {
+  return guarded(n, 6, [&] {
+    const at::Device dev = tensor(p[0], "a").device();
+    const int64_t dims = dims_of(p[0], "a");
+    const Matrix a = rows_of(p[0], "a", at::kFloat8_e4m3fn, dev, dims);
+    const Matrix b = rows_of(p[2], "b", at::kFloat8_e4m3fn, dev, dims);
+    if (b.G != a.G || b.cols != a.cols) refuse(PyExc_ValueError, "%s must have a's batches and columns", "b");
+    const Matrix as = scales_of(p[1], "a_scales", dev, dims, a.G, a.rows, blocks(a.cols));
+    const Matrix bs = scales_of(p[3], "b_scales", dev, dims, a.G, blocks(b.rows), blocks(a.cols));
+    const bool fp32 = tensor(p[4], "out").scalar_type() == at::kFloat;
+    const Matrix o = rows_of(p[4], "out", fp32 ? at::kFloat : at::kBFloat16, dev, dims);
+    if (o.G != a.G || o.rows != a.rows || o.cols != b.rows)
+      refuse(PyExc_ValueError, "%s must be [.., M, N]", "out");
+    const int32_t G = size32(a.G, "a"), M = size32(a.rows, "a"), N = size32(b.rows, "b"),
+                  K = size32(a.cols, "a");
+    return launch(dev, p[5], [&](void* st) {
+      return smla_fp8_matmul(static_cast<uint8_t*>(a.data), a.batch, a.row, static_cast<float*>(as.data),
+                             as.batch, as.row, as.col, static_cast<uint8_t*>(b.data), b.batch, b.row,
+                             static_cast<float*>(bs.data), bs.batch, bs.row, bs.col, G, M, N, K, o.data,
+                             o.batch, o.row, fp32, st);
+    });
+  });
+}
+
 #define SMLA_FN(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {SMLA_FN(decode_fp4), SMLA_FN(decode_fused_fp4), SMLA_FN(decode_window),
                           SMLA_FN(step_maps),  SMLA_FN(cache_write),      SMLA_FN(cache_gather),
                           SMLA_FN(tree_maps),  SMLA_FN(tree_accept),      SMLA_FN(cache_move),
+                          SMLA_FN(fp8_quantise), SMLA_FN(fp8_matmul),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_smla_torch", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

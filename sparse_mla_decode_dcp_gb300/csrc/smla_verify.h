@@ -41,6 +41,44 @@ struct CacheMoveArgs {
   const int32_t* dst_slots;    // [N], -1 = another cache's
 };
 
+// A batch of matrices: entry (g, row, col) is at g * batch + row * rows + col
+// * cols, in elements.
+struct Strides {
+  int64_t batch, rows, cols;
+};
+
+struct QuantiseArgs {
+  const uint16_t* x;  // bf16, columns contiguous
+  Strides xs;
+  int32_t G, M, K;
+  uint8_t* codes;     // columns contiguous
+  Strides cs;
+  float* scales;      // [G, M, ceil(K / 128)]
+  Strides ss;
+};
+
+struct MatmulArgs {
+  CUtensorMap a_map, b_map;  // set by the launcher
+  const uint8_t* a;          // [G, M, K], columns contiguous
+  Strides as;
+  const float* a_scales;     // [G, M, ceil(K / 128)]
+  Strides ass;
+  const uint8_t* b;          // [G, N, K], columns contiguous
+  Strides bs;
+  const float* b_scales;     // [G, ceil(N / 128), ceil(K / 128)]
+  Strides bss;
+  int32_t G, M, N, K;
+  void* out;                 // [G, M, N], columns contiguous
+  Strides os;
+  int32_t out_fp32;
+  // set by the launcher
+  int32_t m_tiles, n_tiles, k_blocks, splits, stages, vec;
+};
+
+cudaError_t launch_fp8_quantise(const QuantiseArgs& a, cudaStream_t s);
+cudaError_t launch_fp8_matmul(const MatmulArgs& a, cudaStream_t s);
+cudaError_t matmul_error_word(uint32_t* flags, bool clear);
+
 cudaError_t launch_tree_maps(const TreeMapsArgs& a, cudaStream_t s);
 cudaError_t launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t s);
 cudaError_t launch_cache_move(const CacheMoveArgs& a, bool fp4, cudaStream_t s);
