@@ -46,6 +46,8 @@
  *
  *   smla_tree_maps                    who sees whom, and rotary positions,
  *                                     from the nodes' parents
+ *   smla_dcp_tree_mla_decode          attention of a tree's nodes over the
+ *                                     cached prefix and each other
  *   smla_tree_accept                  the nodes the model agrees with
  *   smla_mla_cache_move               their cache rows, to their own slots
  *
@@ -711,6 +713,67 @@ smla_status smla_mla_cache_gather(const uint8_t* kv_cache, int64_t num_slots, in
 smla_status smla_tree_maps(const int32_t* parents, const int32_t* row_start,
                            const int32_t* prefix_lens, int32_t B, int32_t T, int32_t max_nodes,
                            uint64_t* masks, int32_t* positions, void* stream);
+
+/*
+ * Tree attention with LSE return: row row_start[b] + j (node j of request b),
+ * each head, attends
+ *   - the request's prefix, positions 0 .. prefix_lens[b] - 1, through its
+ *     block-table rows: of all D pools (rank = -1: out and lse are the merged
+ *     result) or of one rank (rank >= 0: its partial, for smla_dcp_lse_merge);
+ *     position t lives on rank (t div I) mod D, as in
+ *     smla_dcp_filter_convert_index
+ *   - each node m of its tree whose bit is set in the row's mask (bit m mod 64
+ *     of word m div 64, as smla_tree_maps writes them; any mask is taken) and
+ *     which some pool holds: draft_slots[d][row of m] >= 0 is its cache slot
+ *     in pool d, -1 where that pool does not hold it.  Merged, the lowest pool
+ *     that holds it counts; with rank >= 0 only draft_slots[rank] is read.
+ *     The slots may be a smla_dcp_step_maps call's (the drafts lie where their
+ *     positions' blocks are) or rows outside every block (a scratch area, from
+ *     which smla_mla_cache_move brings the accepted ones).
+ * with the attention of smla_sparse_mla_decode over those cache rows.  A row
+ * with nothing to attend is written as (0, -inf).  Rows of out and lse that
+ * belong to no request (behind row_start[B], padding) are left as they were.
+ *
+ *   q              device bf16 [T, H, 576], 16-byte aligned
+ *   row_start      device int32 [B + 1]
+ *   prefix_lens    device int32 [B], each in [0, max_prefix]
+ *   max_prefix     host bound on every prefix_lens[b], at least 0
+ *   masks          device uint64 [T, ceil(max_nodes / 64)]
+ *   max_nodes      host bound on every request's rows
+ *   draft_slots    host array of D device pointers, int32 [T] each
+ *   format         SMLA_CACHE_FP8 or SMLA_CACHE_FP4: the rows of every pool
+ *   kv_caches, num_slots, block_tables, bt_row_strides, bt_widths
+ *                  host arrays of D entries as in smla_dcp_dense_mla_decode;
+ *                  with rank >= 0 only entry [rank] is read
+ *   out            device bf16 [T, H, 512], 16-byte aligned
+ *   lse            device fp32 [T, H]
+ *   workspace      >= smla_tree_decode_workspace_size(T, H, B, max_prefix,
+ *                  max_nodes, D, interleave, rank) bytes, 256-byte aligned;
+ *                  needs no initial contents.  Calls that run concurrently
+ *                  need distinct workspaces.
+ * Errors: INVALID_ARG for T < 0, H < 1, B < 0, max_prefix < 0, max_nodes < 1,
+ * D < 1, rank outside [-1, D), block_size < 1, interleave < 1, another format,
+ * sm_scale not finite and positive, NULL or misaligned arrays, a bad pool or
+ * table entry that is read; UNSUPPORTED for H > SMLA_MAX_HEADS, D >
+ * SMLA_MAX_DCP, max_nodes > SMLA_MAX_TREE_NODES, max_prefix > 2^30 or T * H >
+ * 2^31 - 1; WORKSPACE as for smla_sparse_mla_decode.  T = 0 and B = 0 are
+ * no-ops.
+ * On the device a request whose rows are more than max_nodes or lie outside
+ * [0, T) writes nothing and sets SMLA_DEVERR_TREE; a prefix outside [0,
+ * max_prefix] gives (0, -inf) in all the request's rows and sets
+ * SMLA_DEVERR_CONTEXT; a position past a block table or in an unallocated
+ * block, and a slot past its pool, are not attended and set
+ * SMLA_DEVERR_BLOCK_TABLE and SMLA_DEVERR_SLOT_RANGE.
+ */
+size_t smla_tree_decode_workspace_size(int32_t T, int32_t H, int32_t B, int32_t max_prefix,
+                                       int32_t max_nodes, int32_t D, int32_t interleave, int32_t rank);
+smla_status smla_dcp_tree_mla_decode(
+    const uint16_t* q, int32_t T, int32_t H, float sm_scale, const int32_t* row_start,
+    const int32_t* prefix_lens, int32_t B, int32_t max_prefix, const uint64_t* masks, int32_t max_nodes,
+    const int32_t* const* draft_slots, int32_t D, int32_t rank, int32_t block_size, int32_t interleave,
+    int32_t format, const uint8_t* const* kv_caches, const int64_t* num_slots,
+    const int32_t* const* block_tables, const int64_t* bt_row_strides, const int32_t* bt_widths,
+    uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * smla_tree_accept walks each tree greedily: node 0 is accepted, and from an

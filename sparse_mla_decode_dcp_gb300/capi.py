@@ -101,6 +101,11 @@ SIGNATURES = {
         _c_vp, _c_i64, _c_i32, _c_vp, _c_i32, _c_vp, _c_i64, _c_i32, _c_vp]),
     "smla_tree_maps": (ctypes.c_int, [
         _c_vp, _c_vp, _c_vp, _c_i32, _c_i32, _c_i32, _c_vp, _c_vp, _c_vp]),
+    "smla_tree_decode_workspace_size": (_c_sz, [_c_i32] * 8),
+    "smla_dcp_tree_mla_decode": (ctypes.c_int, [
+        _c_vp, _c_i32, _c_i32, ctypes.c_float, _c_vp, _c_vp, _c_i32, _c_i32, _c_vp, _c_i32, _c_vp,
+        _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp,
+        _c_vp, _c_sz, _c_vp]),
     "smla_tree_accept": (ctypes.c_int, [
         _c_vp, _c_vp, _c_vp, _c_vp, _c_i32, _c_i32, _c_vp, _c_vp, _c_vp, _c_vp]),
     "smla_mla_cache_move": (ctypes.c_int, [
@@ -786,6 +791,51 @@ def tree_maps(parents: torch.Tensor, row_start: torch.Tensor, prefix_lens: torch
     _check("smla_tree_maps",
            _native().tree_maps(parents, row_start, prefix_lens, max_nodes, out, stream))
     return out
+
+
+def tree_decode_workspace_size(T: int, H: int, B: int, max_prefix: int, max_nodes: int, D: int,
+                               interleave: int = 1, rank: int = -1) -> int:
+    return int(load().smla_tree_decode_workspace_size(T, H, B, max_prefix, max_nodes, D, interleave,
+                                                      rank))
+
+
+def alloc_tree_decode_workspace(T: int, H: int, B: int, max_prefix: int, max_nodes: int, D: int,
+                                interleave: int, rank: int, device,
+                                stream: Optional[torch.cuda.Stream] = None
+                                ) -> Optional[torch.Tensor]:
+    """Workspace of dcp_tree_mla_decode (None if none needed)."""
+    n = tree_decode_workspace_size(T, H, B, max_prefix, max_nodes, D, interleave, rank)
+    return _new(n, torch.uint8, device, stream) if n else None
+
+
+def dcp_tree_mla_decode(q: torch.Tensor, row_start: torch.Tensor, prefix_lens: torch.Tensor,
+                        max_prefix: int, masks: torch.Tensor, max_nodes: int,
+                        draft_slots: Sequence[Optional[torch.Tensor]],
+                        kv_caches: Sequence[Optional[torch.Tensor]],
+                        block_tables: Sequence[Optional[torch.Tensor]], block_size: int,
+                        sm_scale: float, *, rank: int = -1, interleave: int = 1,
+                        bt_widths: Optional[Sequence[int]] = None,
+                        out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None
+                        ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of drafted trees' nodes (rows q [T, H, 576]) over their
+    requests' cached prefixes and the nodes their masks name, over 8- or 4-bit
+    pools: merged over the D pools (rank = -1) or one rank's partial (only its
+    pool, table and draft slots are read).  draft_slots[d] [T]: each node's
+    slot in pool d, -1 where it is not held.  Rows of no request are left as
+    they were (uninitialised in an `out` and `lse` allocated here)."""
+    if out is None or lse is None:
+        out, lse = _out_lse(q, out, lse, stream)
+    if workspace is None and q.dim() == 3:
+        workspace = alloc_tree_decode_workspace(q.shape[0], q.shape[1], prefix_lens.shape[0], max_prefix,
+                                                max_nodes, len(kv_caches), interleave, rank, q.device,
+                                                stream)
+    _check("smla_dcp_tree_mla_decode",
+           _native().decode_tree(q, row_start, prefix_lens, max_prefix, masks, max_nodes, draft_slots,
+                                 kv_caches, block_tables, block_size, sm_scale, rank, interleave,
+                                 bt_widths, out, lse, workspace, stream))
+    return out, lse
 
 
 class TreeWalk(NamedTuple):

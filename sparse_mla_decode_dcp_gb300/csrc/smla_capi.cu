@@ -53,6 +53,7 @@ smla_status smla_get_device_error(uint32_t* flags, int clear) {
   if (e == cudaSuccess) e = smla::cache_error_word(flags, clear != 0);
   if (e == cudaSuccess) e = smla::tree_error_word(flags, clear != 0);
   if (e == cudaSuccess) e = smla::matmul_error_word(flags, clear != 0);
+  if (e == cudaSuccess) e = smla::tree_decode_error_word(flags, clear != 0);
   return from_cuda(e);
 }
 
@@ -562,6 +563,85 @@ smla_status smla_tree_maps(const int32_t* parents, const int32_t* row_start,
     return SMLA_ERR_INVALID_ARG;
   const smla::TreeMapsArgs a = {parents, row_start, prefix_lens, B, T, max_nodes, masks, positions};
   return from_cuda(smla::launch_tree_maps(a, static_cast<cudaStream_t>(stream)));
+}
+
+// The most keys of a request: its prefix, or one rank's share of it, and its
+// tree's nodes.
+static int64_t tree_keys(int32_t max_prefix, int32_t max_nodes, int32_t D, int32_t interleave, int32_t rank) {
+  return held_at_most(max_prefix, D, interleave, rank) + max_nodes;
+}
+
+static bool tree_unsupported(int32_t H, int32_t max_prefix, int32_t max_nodes, int32_t D) {
+  return H > SMLA_MAX_HEADS || D > SMLA_MAX_DCP || max_prefix > kMaxEntries ||
+         max_nodes > SMLA_MAX_TREE_NODES;
+}
+
+size_t smla_tree_decode_workspace_size(int32_t T, int32_t H, int32_t B, int32_t max_prefix,
+                                       int32_t max_nodes, int32_t D, int32_t interleave, int32_t rank) {
+  if (T < 0 || H < 1 || B < 0 || max_prefix < 0 || max_nodes < 1 || D < 1 || interleave < 1 || rank < -1 ||
+      rank >= D || tree_unsupported(H, max_prefix, max_nodes, D))
+    return 0;
+  return smla::tree_decode_workspace_bytes(T, B, H, tree_keys(max_prefix, max_nodes, D, interleave, rank));
+}
+
+smla_status smla_dcp_tree_mla_decode(
+    const uint16_t* q, int32_t T, int32_t H, float sm_scale, const int32_t* row_start,
+    const int32_t* prefix_lens, int32_t B, int32_t max_prefix, const uint64_t* masks, int32_t max_nodes,
+    const int32_t* const* draft_slots, int32_t D, int32_t rank, int32_t block_size, int32_t interleave,
+    int32_t format, const uint8_t* const* kv_caches, const int64_t* num_slots,
+    const int32_t* const* block_tables, const int64_t* bt_row_strides, const int32_t* bt_widths,
+    uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (T < 0 || H < 1 || B < 0 || max_prefix < 0 || max_nodes < 1 || D < 1 || rank < -1 || rank >= D ||
+      block_size < 1 || interleave < 1 || (format != SMLA_CACHE_FP8 && format != SMLA_CACHE_FP4) ||
+      !std::isfinite(sm_scale) || !(sm_scale > 0.f))
+    return SMLA_ERR_INVALID_ARG;
+  if (tree_unsupported(H, max_prefix, max_nodes, D) || int64_t(T) * H > INT32_MAX)
+    return SMLA_ERR_UNSUPPORTED;
+  if (T == 0 || B == 0) return SMLA_OK;
+  if (!q || !row_start || !prefix_lens || !masks || !draft_slots || !kv_caches || !num_slots ||
+      !block_tables || !bt_row_strides || !bt_widths || !out || !lse)
+    return SMLA_ERR_INVALID_ARG;
+  if (misaligned(q, 16) || misaligned(out, 16) || misaligned(lse, 4) || misaligned(row_start, 4) ||
+      misaligned(prefix_lens, 4) || misaligned(masks, 8))
+    return SMLA_ERR_INVALID_ARG;
+  smla::TreeDecodeArgs a{};
+  for (int d = 0; d < D; ++d) {
+    if (rank >= 0 && d != rank) continue;
+    if (!kv_caches[d] || misaligned(kv_caches[d], 16) || num_slots[d] < 0 || !block_tables[d] ||
+        misaligned(block_tables[d], 4) || bt_widths[d] < 1 || bt_row_strides[d] < bt_widths[d] ||
+        !draft_slots[d] || misaligned(draft_slots[d], 4))
+      return SMLA_ERR_INVALID_ARG;
+    a.pools[d] = kv_caches[d];
+    a.pool_slots[d] = num_slots[d];
+    a.bts[d] = block_tables[d];
+    a.bt_stride[d] = bt_row_strides[d];
+    a.bt_width[d] = bt_widths[d];
+    a.draft_slots[d] = draft_slots[d];
+  }
+  const size_t need =
+      smla::tree_decode_workspace_bytes(T, B, H, tree_keys(max_prefix, max_nodes, D, interleave, rank));
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || misaligned(workspace, 256)))
+    return SMLA_ERR_WORKSPACE;
+  a.q = q;
+  a.T = T;
+  a.B = B;
+  a.H = H;
+  a.sm_scale = sm_scale;
+  a.row_start = row_start;
+  a.prefix_lens = prefix_lens;
+  a.max_prefix = max_prefix;
+  a.masks = masks;
+  a.max_nodes = max_nodes;
+  a.mask_words = (max_nodes + 63) / 64;
+  a.D = D;
+  a.rank = rank;
+  a.block_size = block_size;
+  a.interleave = interleave;
+  a.out = out;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  return from_cuda(smla::launch_tree_decode(a, format == SMLA_CACHE_FP4, static_cast<cudaStream_t>(stream)));
 }
 
 smla_status smla_tree_accept(const int32_t* parents, const int32_t* tokens, const int32_t* targets,

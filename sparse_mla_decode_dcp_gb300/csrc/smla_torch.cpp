@@ -411,6 +411,35 @@ PyObject* tree_maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (q, row_start, prefix_lens, max_prefix, masks, max_nodes, draft_slots,
+//  kv_caches, block_tables, block_size, sm_scale, rank, interleave, bt_widths,
+//  out, lse, workspace, stream)
+PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 18, [&] {
+    const Query q = query_of(a[0], a[14], a[15], a[16]);
+    const at::Tensor& prefix = vec(a[2], "prefix_lens", at::kInt, q.dev, -1);
+    const int32_t B = size32(prefix.size(0), "prefix_lens");
+    const at::Tensor& starts = vec(a[1], "row_start", at::kInt, q.dev, int64_t(B) + 1);
+    const int32_t max_prefix = i32(a[3]), nodes = i32(a[5]), bs = i32(a[9]), rank = i32(a[11]), I = i32(a[12]);
+    const float scale = f32(a[10]);
+    const at::Tensor& masks = need(a[4], "masks", at::kLong, q.dev);
+    if (masks.dim() != 2 || masks.size(0) != q.T || masks.size(1) != (int64_t(nodes) + 63) / 64)
+      refuse(PyExc_ValueError, "%s must be [T, ceil(max_nodes / 64)]", "masks");
+    const Pools p = pools_of(a[7], a[8], a[13], q.dev, rank);
+    if (p.rows < B) refuse(PyExc_ValueError, "%s need a row per request", "block_tables");
+    const Seq drafts(a[6], "draft_slots must be a sequence");
+    if (drafts.size() != p.D) refuse(PyExc_ValueError, "%s must have an entry for each pool", "draft_slots");
+    const int32_t* slots[SMLA_MAX_DCP] = {};
+    for (int32_t d = 0; d < p.D; ++d)
+      if (rank < 0 || d == rank) slots[d] = ptr<int32_t>(vec(drafts[d], "draft_slots[d]", at::kInt, q.dev, q.T));
+    return launch(q.dev, a[17], [&](void* s) {
+      return smla_dcp_tree_mla_decode(q.q, q.T, q.H, scale, ptr<int32_t>(starts), ptr<int32_t>(prefix), B,
+                                      max_prefix, ptr<uint64_t>(masks), nodes, slots, p.D, rank, bs, I, p.format,
+                                      p.kv, p.slots, p.bt, p.stride, p.width, q.out, q.lse, q.ws, q.ws_bytes, s);
+    });
+  });
+}
+
 // (parents, tokens, targets, row_start, (accepted, rows, next_tokens), stream)
 PyObject* tree_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 6, [&] {
@@ -547,7 +576,7 @@ PyObject* fp8_matmul(PyObject*, PyObject* const* p, Py_ssize_t n) {
 PyMethodDef kMethods[] = {SMLA_FN(decode_fp4), SMLA_FN(decode_fused_fp4), SMLA_FN(decode_window),
                           SMLA_FN(step_maps),  SMLA_FN(cache_write),      SMLA_FN(cache_gather),
                           SMLA_FN(tree_maps),  SMLA_FN(tree_accept),      SMLA_FN(cache_move),
-                          SMLA_FN(fp8_quantise), SMLA_FN(fp8_matmul),
+                          SMLA_FN(decode_tree), SMLA_FN(fp8_quantise),    SMLA_FN(fp8_matmul),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_smla_torch", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -41,6 +41,29 @@ struct CacheMoveArgs {
   const int32_t* dst_slots;    // [N], -1 = another cache's
 };
 
+struct TreeDecodeArgs {
+  const uint16_t* q;           // bf16 [T, H, 576]
+  int32_t T, B, H;
+  float sm_scale;
+  const int32_t* row_start;    // [B + 1]
+  const int32_t* prefix_lens;  // [B]
+  int32_t max_prefix;
+  const uint64_t* masks;       // [T, mask_words]
+  int32_t max_nodes, mask_words;
+  int32_t D, rank, block_size, interleave;  // rank -1: all pools
+  FastDiv div_ID, div_bs;      // set by the launcher
+  const uint8_t* pools[kMaxMerge];
+  int64_t pool_slots[kMaxMerge];
+  const int32_t* bts[kMaxMerge];
+  int64_t bt_stride[kMaxMerge];
+  int32_t bt_width[kMaxMerge];
+  const int32_t* draft_slots[kMaxMerge];  // [T] each
+  uint16_t* out;               // bf16 [T, H, 512]
+  float* lse;                  // [T, H]
+  void* workspace;
+  size_t workspace_bytes;
+};
+
 // A batch of matrices: entry (g, row, col) is at g * batch + row * rows + col
 // * cols, in elements.
 struct Strides {
@@ -74,6 +97,10 @@ struct MatmulArgs {
   // set by the launcher
   int32_t m_tiles, n_tiles, k_blocks, splits, stages, vec;
 };
+
+cudaError_t launch_tree_decode(const TreeDecodeArgs& a, bool fp4, cudaStream_t s);
+size_t tree_decode_workspace_bytes(int32_t T, int32_t B, int32_t H, int64_t max_keys);
+cudaError_t tree_decode_error_word(uint32_t* flags, bool clear);
 
 cudaError_t launch_fp8_quantise(const QuantiseArgs& a, cudaStream_t s);
 cudaError_t launch_fp8_matmul(const MatmulArgs& a, cudaStream_t s);
