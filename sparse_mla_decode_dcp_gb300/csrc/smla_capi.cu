@@ -618,8 +618,8 @@ smla_status smla_dcp_tree_mla_decode(
     a.bt_width[d] = bt_widths[d];
     a.draft_slots[d] = draft_slots[d];
   }
-  const size_t need =
-      smla::tree_decode_workspace_bytes(T, B, H, tree_keys(max_prefix, max_nodes, D, interleave, rank));
+  const int64_t keys = tree_keys(max_prefix, max_nodes, D, interleave, rank);
+  const size_t need = smla::tree_decode_workspace_bytes(T, B, H, keys);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || misaligned(workspace, 256)))
     return SMLA_ERR_WORKSPACE;
   a.q = q;
@@ -641,7 +641,7 @@ smla_status smla_dcp_tree_mla_decode(
   a.lse = lse;
   a.workspace = workspace;
   a.workspace_bytes = workspace_bytes;
-  return from_cuda(smla::launch_tree_decode(a, format == SMLA_CACHE_FP4, static_cast<cudaStream_t>(stream)));
+  return from_cuda(smla::launch_tree_decode(a, keys, format == SMLA_CACHE_FP4, static_cast<cudaStream_t>(stream)));
 }
 
 smla_status smla_tree_accept(const int32_t* parents, const int32_t* tokens, const int32_t* targets,

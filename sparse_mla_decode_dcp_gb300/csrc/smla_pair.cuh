@@ -1,6 +1,6 @@
 // Inline-PTX wrappers beside smla_sm100.cuh's: batched TMA tile loads, 8-bit
-// MMAs with both operands in shared memory, packed fp32 arithmetic, and a
-// wait that is bounded in time.
+// MMAs with both operands in shared memory, MMAs of a CTA pair, packed fp32
+// arithmetic, and a wait that is bounded in time.
 #pragma once
 
 #include "smla_sm100.cuh"
@@ -31,6 +31,63 @@ __device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
       :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// ------------------------------------------------------------- CTA pairs
+// Tensor memory of both CTAs of a pair (a warp of each takes part).
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+               :: "r"(smem_u32(dst_smem)), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(taddr), "r"(ncols)
+               : "memory");
+}
+
+// D (+)= A * B^T over a pair's shared and tensor memories, fp16 operands,
+// issued by its first CTA: each CTA holds half of A's rows and half of B's at
+// the same offsets.  With M = 128 a CTA's 64 rows of D lie in its lanes 0..63
+// (the first half of the columns) and 64..127 (the second).
+__device__ __forceinline__ void mma_ss_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// The same on e4m3 operands (K = 32), and on bf16 ones by idesc_bf16_f32.
+__device__ __forceinline__ void mma_ss_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+__host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
+  return idesc_f16_f32(M, N, false, false) | (1u << 7) | (1u << 10);
+}
+
+// Arrive on the barrier at `bar`'s offset in both CTAs when every MMA this
+// thread issued so far has completed.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+      :: "r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
+}
+
+// Arrive on a barrier of a CTA of the cluster (an address from map_to_cta),
+// behind this thread's writes to its own CTA's shared memory.  The release is
+// the CTA's: nothing but such writes and tensor-memory accesses is handed over.
+// (At cluster scope it waits for every load in flight: 6 us a tile of the tree
+// decode instead of 1.)
+__device__ __forceinline__ void mbar_arrive_at(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
 }
 
 // Two fp32 at once: a * b + c, each rounded once.

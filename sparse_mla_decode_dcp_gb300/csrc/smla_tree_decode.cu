@@ -1,4 +1,5 @@
-// Attention of drafted trees over the packed latent cache (8- or 4-bit rows).
+// Attention of drafted trees over the packed latent cache (8- or 4-bit rows)
+// on tcgen05 tensor cores.
 //
 // Row (t, h) of request b attends the request's prefix (this rank's share of
 // its positions, or all pools') and those nodes of its tree that its mask
@@ -6,19 +7,130 @@
 //   s_k = sm_scale <q, k>,  lse = ln sum exp s_k,  out = sum exp(s_k - lse) latent_k
 // A row with no key is written as (0, -inf).
 //
-// One CTA a row: four warps take keys in turn, one score a warp at a time,
-// and keep their own running maximum, sum and output, which meet at the end.
-#include <cuda_bf16.h>
-#include <cuda_fp4.h>
-#include <cuda_fp8.h>
+// Design (a cluster of two CTAs works on 128 rows and 64 keys at a time):
+//   * A request's rows, its nodes times the heads, share its keys, so they are
+//     taken as one list and cut into tiles of 128 whatever the head count: 16
+//     heads of 8 nodes fill a tile as 128 heads of one do.
+//   * MMAs of the pair (cta_group::2, M = 128): each CTA holds 64 of the rows,
+//     all 512 value columns of their accumulator (256 tensor-memory columns,
+//     two halves of the columns in the two halves of the lanes) and 64 scores,
+//     and every CTA's score and output is whole: no partial scores travel.
+//     For QK^T each CTA supplies half of the tile's keys (32, all 576 dims),
+//     for PV half of the value dims (256, of all 64 keys), so that only
+//     signals, no data, go between the CTAs.
+//   * fp8 rows: QK^T takes the cache's codes as they are, copied into the
+//     MMA's layout asynchronously (cp.async).  The query's latent part is an
+//     e4m3 sum hi + lo of each row's values times a power of two: bf16 has 8
+//     significant bits, hi the first 4 and lo the rest, exactly down to 2^-10
+//     of the row's largest value and within 2^-19 of it below.  The four scale
+//     groups and the rope part (bf16 as it is) have score accumulators of
+//     their own, which meet, times the fp32 scales, in the softmax: the log
+//     sum is as exact as fp32 sums are.  Values are codes times scales,
+//     rounded once to fp16.
+//   * fp4 rows: codes times scales are exact in fp16, for keys and values.
+//   * A row's 64 scores lie in two lanes, 32 each, whose threads agree on the
+//     maximum through shared memory.  Softmax in the log2 domain against a
+//     reference that moves only when a row's maximum grows by more than 2^8.
+//   * Masks are looked at in the tiles that hold nodes or missing rows; a
+//     node's row that is not finite is kept out of the value tile (its score
+//     spoils the rows that see it), so that masked places do not show.
+//   * All requests' (row tile, key tile) units form one line that is cut into
+//     equal ranges, one a pair, so that ragged batches fill the GPU.  A row
+//     tile that a cut falls into leaves partial results (fp16, with their
+//     maximum and sum), which a second kernel merges.
+//
+// Warps: 0-7 softmax and output (two threads a lane of tensor memory), 8-15
+// load cache rows ahead and convert them, 16 issues the MMAs (the first CTA's,
+// for both; the second's tells it of its keys), 17 lists the pair's work, 18
+// looks up the keys' rows.  Every wait is bounded; one that
+// gives up sets SMLA_DEVERR_TIMEOUT and the CTA unwinds.
+#define SMLA_WAITS_OUT_OF_LINE
+#include "smla_decode_kernel.cuh"
 
-#include "../../include/smla.h"
+#include "smla_pair.cuh"
 #include "smla_verify.h"
 
 namespace smla {
 namespace {
 
-__device__ unsigned int g_tree_decode_error;
+constexpr int kPairRows = 128, kCtaRows = 64;
+constexpr int kTileKeys = 64, kCtaKeys = 32;
+constexpr int kSoftWarps = 8, kConvWarps = 8;
+constexpr int kIssueWarp = kSoftWarps + kConvWarps;
+constexpr int kTreeWarps = kIssueWarp + 3;
+constexpr int kTreeThreads = 32 * kTreeWarps;
+constexpr int kWarpKeys = kCtaKeys / kConvWarps;  // of each CTA, a converter warp's
+constexpr int kItems = 8;   // work items listed ahead
+constexpr int kPlaces = 4;  // tiles whose rows are looked up ahead
+constexpr int kPairs = 76;
+
+// Shared memory: operand tiles in blocks of 128 bytes a row, Q and P by this
+// CTA's 64 rows, K by its 32 keys, V by 64 keys (64 dims a block).
+constexpr int kQBlock = kCtaRows * 128, kKBlock = kCtaKeys * 128, kVBlock = kTileKeys * 128;
+constexpr int kQSize = 9 * kQBlock, kVSize = 4 * kVBlock;
+// fp8 rows: Q is hi (4 blocks of 128 codes), lo (4) and the rope part (64
+// bf16), a K tile 4 blocks of codes and the rope block, three tiles ahead.
+// fp4 rows: 8 blocks of 64 fp16 and the rope block, two tiles.
+template <bool kFp4> struct Shared {
+  static constexpr int kStages = kFp4 ? 2 : 3;
+  static constexpr int kKSize = (kFp4 ? 9 : 5) * kKBlock;
+  static constexpr int kOffV = kQSize + kStages * kKSize;
+  static constexpr int kOffP = kOffV + 2 * kVSize;
+  static constexpr int kOffCtl = kOffP + kCtaRows * 128;
+};
+
+// tensor memory: the output's 2 x 128 columns, a tile's scores (32 columns for
+// each of up to five accumulators)
+constexpr uint32_t kOutCol = 0, kScoreCol = 256;
+
+// A request's keys in their order: the prefix positions of pool 0, of pool 1
+// and so on (or of one rank), then the tree's nodes.
+struct Keys {
+  int32_t first, nodes;           // the request's rows (no nodes when its prefix is out of range)
+  int32_t before[kMaxMerge + 1];  // prefix keys before pool d
+  int32_t prefix, total;
+};
+
+// A row tile of a request over a range of its key tiles.
+struct Item {
+  int32_t req;
+  int32_t rows;          // of the tile that exist; 0: the end of the list
+  int32_t skip;          // rows of the request before the tile
+  int32_t tile0, tiles;  // key tiles
+  int32_t part;          // -1: all of the row tile's keys; else the partial result's place
+  Keys keys;
+};
+
+struct TreeCtl {
+  uint64_t qk[2], pv[2], k_free[3], k_full[3], k_peer[3], v_full[2], q_full, s_read, p_full, out_read, top[2],
+      sum, item_full[kItems], item_empty[kItems], place_full[kPlaces], place_empty[kPlaces], end;
+  uint32_t tbase;
+  int abort;
+  uint64_t valid[16];                     // per tile (mod 16): which of its keys exist
+  const uint8_t* row[kPlaces][kTileKeys];  // the keys' cache rows
+  float row_scale[2][kCtaRows];           // fp8 rows, per item (mod 2): a row's score times this is its own
+  float tops[2][32 * kSoftWarps], sums[32 * kSoftWarps];
+  Item items[kItems];
+  int64_t warp_units[kTreeWarps];
+  int64_t start;                          // of the pair's range, within its first request
+  int32_t start_req;
+  // fp8 rows only, so last: per tile (mod 4), the keys' scales by group
+  alignas(16) float scales[4][4][kTileKeys];
+};
+template <bool kFp4>
+constexpr int tree_smem() {
+  return Shared<kFp4>::kOffCtl + int(kFp4 ? offsetof(TreeCtl, scales) : sizeof(TreeCtl)) + 1024;
+}
+static_assert(tree_smem<false>() <= 227 * 1024 && tree_smem<true>() <= 227 * 1024, "shared memory per CTA");
+
+struct SplitTile {
+  int32_t row, rows;     // first row (of T * H) and how many
+  int32_t parts, place;  // partial results: `place`, then the first of each pair behind
+};
+
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, TreeCtl* ctl, uint32_t site) {
+  return wait_phase<false>(bar, parity, &ctl->abort, site);
+}
 
 // Of the first n positions, how many pool d holds.
 __device__ __forceinline__ int32_t pool_rows(const TreeDecodeArgs& a, int32_t n, int32_t d) {
@@ -27,188 +139,1108 @@ __device__ __forceinline__ int32_t pool_rows(const TreeDecodeArgs& a, int32_t n,
   return full * a.interleave + int32_t(min(max(rest, int64_t(0)), int64_t(a.interleave)));
 }
 
-// A request's keys in their order: the prefix positions of pool 0, of pool 1
-// and so on (or of one rank), then the tree's nodes.
-struct Keys {
-  int32_t first, nodes;        // the request's rows
-  int32_t before[kMaxMerge + 1];  // prefix keys before pool d
-  int32_t total;               // prefix keys and nodes
+// What a request brings: its rows and keys.  No rows (and an error bit) when
+// they lie outside T or are too many; no keys when its prefix is out of range.
+struct Request {
+  int32_t first, nodes, prefix, keys;  // prefix: as given, -1 when out of range
 };
 
-__device__ __forceinline__ int32_t prefix_keys(const Keys& k) { return k.total - k.nodes; }
-
-// Address of key i's cache row, or null (and an error bit, where it is one)
-// for a node no pool holds and an entry that is out of range.
-__device__ __forceinline__ const uint8_t* key_row(const TreeDecodeArgs& a, const Keys& keys, int32_t req,
-                                                  int32_t i, int row_bytes, unsigned& err) {
-  int d = max(a.rank, 0);
-  int64_t slot;
-  if (i < prefix_keys(keys)) {
-    if (a.rank < 0)
-      while (i >= keys.before[d + 1]) ++d;
-    const int32_t lp = i - keys.before[d];
-    const int32_t col = int32_t(fastdiv(uint32_t(lp), a.div_bs));
-    const int32_t blk = col < a.bt_width[d] ? a.bts[d][req * a.bt_stride[d] + col] : -1;
-    if (blk < 0) {
-      err |= SMLA_DEVERR_BLOCK_TABLE;
-      return nullptr;
-    }
-    slot = int64_t(blk) * a.block_size + (lp - col * a.block_size);
+__device__ __forceinline__ Request load_request(const TreeDecodeArgs& a, int32_t b, unsigned& err) {
+  Request r;
+  r.first = a.row_start[b];
+  const int64_t n = int64_t(a.row_start[b + 1]) - r.first;
+  r.prefix = a.prefix_lens[b];
+  const bool rows_ok = r.first >= 0 && n >= 0 && n <= a.max_nodes && r.first + n <= a.T;
+  if (!rows_ok) err |= SMLA_DEVERR_TREE;
+  r.nodes = rows_ok ? int32_t(n) : 0;
+  r.keys = 0;
+  if (r.prefix < 0 || r.prefix > a.max_prefix) {
+    if (rows_ok && n > 0) err |= SMLA_DEVERR_CONTEXT;
+    r.prefix = -1;
   } else {
-    const int32_t row = keys.first + (i - prefix_keys(keys));
-    slot = a.draft_slots[d][row];
-    if (a.rank < 0)
-      while (slot < 0 && d + 1 < a.D) slot = a.draft_slots[++d][row];
-    if (slot < 0) return nullptr;
+    r.keys = (a.rank < 0 ? r.prefix : pool_rows(a, r.prefix, a.rank)) + r.nodes;
   }
-  if (slot >= a.pool_slots[d]) {
+  return r;
+}
+
+__device__ __forceinline__ int32_t row_tiles(const TreeDecodeArgs& a, const Request& r) {
+  return int32_t((int64_t(r.nodes) * a.H + kPairRows - 1) / kPairRows);
+}
+// A request without keys has one tile of none.
+__device__ __forceinline__ int32_t key_tiles(const Request& r) {
+  return max((r.keys + kTileKeys - 1) / kTileKeys, 1);
+}
+// Units of a row tile: its key tiles where it may be cut, else one.
+__device__ __forceinline__ int32_t tile_units(const TreeDecodeArgs& a, const Request& r) {
+  return a.split ? key_tiles(r) : 1;
+}
+
+// A key's place while its table entry is on the way.
+struct Place {
+  int32_t d, offset, entry;
+  bool prefix, live;
+};
+
+__device__ __forceinline__ Place find_key(const TreeDecodeArgs& a, const Keys& keys, int32_t req, int32_t i) {
+  Place p;
+  p.live = i < keys.total;
+  p.prefix = i < keys.prefix;
+  p.d = max(a.rank, 0);
+  p.offset = 0;
+  p.entry = -1;
+  if (p.prefix) {
+    if (a.rank < 0)
+      while (i >= keys.before[p.d + 1]) ++p.d;
+    const int32_t lp = i - keys.before[p.d];
+    const int32_t col = int32_t(fastdiv(uint32_t(lp), a.div_bs));
+    p.offset = lp - col * a.block_size;
+    if (col < a.bt_width[p.d]) p.entry = a.bts[p.d][req * a.bt_stride[p.d] + col];
+  } else if (p.live) {
+    const int32_t row = keys.first + (i - keys.prefix);
+    p.entry = a.draft_slots[p.d][row];
+    if (a.rank < 0)
+      while (p.entry < 0 && p.d + 1 < a.D) p.entry = a.draft_slots[++p.d][row];
+  }
+  return p;
+}
+
+// Address of the key's cache row, or null (with an error bit, where it is
+// one).
+__device__ __forceinline__ const uint8_t* key_row(const TreeDecodeArgs& a, const Place& p, int row_bytes,
+                                                  unsigned& err) {
+  if (!p.live) return nullptr;
+  if (p.entry < 0) {
+    if (p.prefix) err |= SMLA_DEVERR_BLOCK_TABLE;
+    return nullptr;
+  }
+  const int64_t slot = p.prefix ? int64_t(p.entry) * a.block_size + p.offset : p.entry;
+  if (slot >= a.pool_slots[p.d]) {
     err |= SMLA_DEVERR_SLOT_RANGE;
     return nullptr;
   }
-  return a.pools[d] + slot * row_bytes;
+  return a.pools[p.d] + slot * row_bytes;
 }
 
-// Fills `keys` for request b; false (and an error bit) for rows that lie
-// outside T or are too many.  A prefix out of range leaves no keys.
-__device__ bool request_keys(const TreeDecodeArgs& a, int32_t b, Keys& keys, unsigned& err) {
-  const int32_t first = a.row_start[b];
-  const int64_t n = int64_t(a.row_start[b + 1]) - first;
-  if (first < 0 || n < 0 || n > a.max_nodes || first + n > a.T) {
-    err |= SMLA_DEVERR_TREE;
-    return false;
-  }
-  const int32_t prefix = a.prefix_lens[b];
-  const bool ok = prefix >= 0 && prefix <= a.max_prefix;
-  if (!ok) err |= SMLA_DEVERR_CONTEXT;
-  keys.first = first;
-  keys.nodes = ok ? int32_t(n) : 0;
-  int32_t sum = 0;
-  for (int d = 0; d < a.D; ++d) {
-    keys.before[d] = a.rank < 0 ? sum : 0;
-    if (ok && (a.rank < 0 || a.rank == d)) sum += pool_rows(a, prefix, d);
-  }
-  keys.before[a.D] = sum;
-  keys.total = sum + keys.nodes;
-  return true;
+// fp16 values that are not finite, to zero.
+__device__ __forceinline__ uint32_t only_finite(uint32_t w) {
+  if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u;
+  if ((w & 0x7c000000u) == 0x7c000000u) w &= 0xffffu;
+  return w;
+}
+__device__ __forceinline__ uint4 only_finite(uint4 v) {
+  return make_uint4(only_finite(v.x), only_finite(v.y), only_finite(v.z), only_finite(v.w));
 }
 
-template <bool kFp4>
-__device__ __forceinline__ float key_value(const uint8_t* row, int c) {
-  constexpr int kRope = kFp4 ? 288 : 528;
-  if (c >= SMLA_V_DIM)
-    return __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(row + kRope)[c - SMLA_V_DIM]) << 16);
-  if constexpr (kFp4) {
-    const float s = float(*reinterpret_cast<const __nv_fp8_e4m3*>(row + 256 + c / 16));
-    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(__nv_fp4x2_storage_t(row[c / 2]), __NV_E2M1);
-    const float2 f = __half22float2(__half2(h));
-    return s * (c & 1 ? f.y : f.x);
-  } else {
-    return reinterpret_cast<const float*>(row + SMLA_V_DIM)[c / 128] *
-           float(*reinterpret_cast<const __nv_fp8_e4m3*>(row + c));
+// A consumer's place in the pair's list of items.
+struct Cursor {
+  int item = -1, tile = 0, tiles = 0;
+  bool end = false;
+  __device__ __forceinline__ const Item& at(const TreeCtl* ctl) const { return ctl->items[item % kItems]; }
+  // To the next item's first tile; false at the end of the list.
+  __device__ __forceinline__ bool next_item(TreeCtl* ctl) {
+    ++item;
+    tile = 0;
+    const bool ok = tree_wait(&ctl->item_full[item % kItems], (item / kItems) & 1, ctl, kWsRaw);
+    end = !__all_sync(0xffffffffu, ok) || at(ctl).rows == 0;
+    tiles = end ? 0 : at(ctl).tiles;
+    return !end;
+  }
+  __device__ __forceinline__ void next_tile(TreeCtl* ctl) {
+    if (!end && (item < 0 || ++tile == tiles)) next_item(ctl);
+  }
+};
+
+// Hands an item's place back to the list (one arrival a warp).
+__device__ __forceinline__ void leave_item(TreeCtl* ctl, int item, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&ctl->item_empty[item % kItems]);
+}
+
+// ---------------------------------------------------------------- work list
+__device__ void list_work(const TreeDecodeArgs& a, TreeCtl* ctl, int C, int64_t units, int64_t per_pair,
+                          int lane) {
+  const int pair = int(blockIdx.x >> 1);
+  const int64_t u_begin = per_pair * pair;
+  const int64_t u_end = min(u_begin + per_pair, units);
+  int64_t u = u_begin;
+  int32_t req = ctl->start_req;
+  int64_t in_req = ctl->start;  // units of `req` before u
+  int item = 0;
+  SplitTile begun = {0, 0, 0, 0};
+  bool ok = true;
+  while (ok && u < u_end && req < a.B) {
+    unsigned ignored = 0;
+    const Request r = load_request(a, req, ignored);
+    const int32_t per_tile = tile_units(a, r);
+    const int64_t all = int64_t(row_tiles(a, r)) * per_tile;
+    // this lane's pool and the prefix keys up to it
+    const int32_t held =
+        r.prefix >= 0 && lane < a.D && (a.rank < 0 || lane == a.rank) ? pool_rows(a, r.prefix, lane) : 0;
+    int32_t upto = held;
+#pragma unroll
+    for (int o = 1; o < kMaxMerge; o <<= 1) {
+      const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    while (in_req < all && u < u_end) {
+      const int32_t tile = int32_t(in_req / per_tile);
+      const int32_t k0 = int32_t(in_req - int64_t(tile) * per_tile);
+      const int32_t take = int32_t(min(int64_t(per_tile - k0), u_end - u));
+      const bool whole = take == per_tile;
+      const int slot = item % kItems;
+      if (item >= kItems)
+        ok = tree_wait(&ctl->item_empty[slot], (item / kItems - 1) & 1, ctl, kWsRawEmpty);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      Item& it = ctl->items[slot];
+      if (lane < a.D) it.keys.before[lane] = a.rank < 0 ? upto - held : 0;
+      if (lane == a.D - 1) it.keys.before[a.D] = upto;
+      const int32_t skip = tile * kPairRows;
+      const int32_t rows = min(kPairRows, r.nodes * a.H - skip);
+      if (lane == 0) {
+        it.keys.first = r.first;
+        it.keys.nodes = r.prefix >= 0 ? r.nodes : 0;
+        it.keys.total = r.keys;
+        it.keys.prefix = r.keys - it.keys.nodes;
+        it.req = req;
+        it.rows = rows;
+        it.skip = skip;
+        it.tile0 = a.split ? k0 : 0;
+        it.tiles = a.split ? take : key_tiles(r);
+        it.part = whole ? -1 : 2 * pair + (item > 0);
+      }
+      if (!whole && k0 == 0) {
+        begun.row = r.first * a.H + skip;
+        begun.rows = rows;
+        begun.parts = int32_t((u + per_tile - 1) / per_pair) - pair + 1;
+        begun.place = 2 * pair + (item > 0);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->item_full[slot]);
+      ++item;
+      u += take;
+      in_req += take;
+    }
+    ++req;
+    in_req = 0;
+  }
+  // the end of the list
+  const int slot = item % kItems;
+  if (ok && item >= kItems) ok = tree_wait(&ctl->item_empty[slot], (item / kItems - 1) & 1, ctl, kWsRawEmpty);
+  if (__all_sync(0xffffffffu, ok) && lane == 0) {
+    ctl->items[slot].rows = 0;
+    mbar_arrive(&ctl->item_full[slot]);
+  }
+  if (a.split && C == 0 && lane == 0) static_cast<SplitTile*>(a.ws_desc)[pair] = begun;
+}
+
+// --------------------------------------------------------------- the keys' rows
+// One warp, two keys a lane, a tile ahead.  A missing key's row is read from
+// somewhere else (a row of q is longer than a cache row): its score is masked,
+// and what goes into the value tile is made finite.
+__device__ void look_up_rows(const TreeDecodeArgs& a, TreeCtl* ctl, int row_bytes, int lane) {
+  const uint8_t* elsewhere = reinterpret_cast<const uint8_t*>(a.q);
+  unsigned err = 0;
+  Cursor ahead;
+  Place place[2];
+  auto find = [&](int before) {
+    if (before >= 0 && ahead.item != before) leave_item(ctl, before, lane);
+    if (ahead.end) return;
+    const Item& it = ahead.at(ctl);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      place[i] = find_key(a, it.keys, it.req, (it.tile0 + ahead.tile) * kTileKeys + 32 * i + lane);
+  };
+  ahead.next_tile(ctl);
+  find(-1);
+  for (int t = 0; !ahead.end; ++t) {
+    const int slot = t % kPlaces;
+    if (t >= kPlaces && !__all_sync(0xffffffffu, tree_wait(&ctl->place_empty[slot], (t / kPlaces - 1) & 1, ctl,
+                                                           kWsRawEmpty)))
+      break;
+    const uint8_t* row[2] = {key_row(a, place[0], row_bytes, err), key_row(a, place[1], row_bytes, err)};
+    const uint32_t lo = __ballot_sync(0xffffffffu, row[0] != nullptr);
+    const uint32_t hi = __ballot_sync(0xffffffffu, row[1] != nullptr);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) ctl->row[slot][32 * i + lane] = row[i] ? row[i] : elsewhere;
+    if (lane == 0) ctl->valid[t & 15] = uint64_t(hi) << 32 | lo;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->place_full[slot]);
+    const int before = ahead.item;
+    ahead.next_tile(ctl);
+    find(before);
+  }
+  if (err) atomicOr(&g_decode_error, err);
+}
+
+// --------------------------------------------------------------- converters
+// Whether any of a tile's keys may hold what a masked place must not show.
+__device__ __forceinline__ bool must_mend(const TreeCtl* ctl, const Item& it, int tile, int g) {
+  return (it.tile0 + tile + 1) * kTileKeys > it.keys.prefix || ctl->valid[g & 15] != ~0ull;
+}
+
+// 8-bit rows.  A warp copies four keys of this CTA into the K tile (codes,
+// rope) two tiles ahead, and makes value rows of those four and of four of the
+// peer's: the former's codes come back from the K tile, the latter's from
+// global memory through registers, a tile ahead.  16 lanes take a key's half
+// of the codes, 16 each; the eight chunks that a quarter of a warp stores
+// together lie in eight bank groups.
+struct Fp8Keys {
+  static constexpr bool kFp4 = false;
+  static constexpr int kRowBytes = SMLA_ROW_BYTES;
+  using Sm = Shared<false>;
+
+  // Rows of the request's list as the A operands of QK^T, eight a warp.
+  static __device__ void load_queries(const TreeDecodeArgs& a, const Item& it, uint32_t q0, float* row_scale, int C,
+                                      int w, int lane) {
+    const int64_t row0 = int64_t(it.keys.first) * a.H + it.skip + kCtaRows * C;
+    const int live = it.rows - kCtaRows * C;
+#pragma unroll 4
+    for (int i = 0; i < 8; ++i) {
+      const int r = 8 * w + i;
+      uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, rope = make_uint4(0, 0, 0, 0);
+      if (r < live) {
+        const uint16_t* q = a.q + (row0 + r) * SMLA_QK_DIM;
+        v[0] = ldg_stream(q + 16 * lane);
+        v[1] = ldg_stream(q + 16 * lane + 8);
+        if (lane < 8) rope = ldg_stream(q + SMLA_V_DIM + 8 * lane);
+      }
+      const uint32_t x[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = max(top, max(x[k] & 0x7fffu, (x[k] >> 16) & 0x7fffu));
+      top = __reduce_max_sync(0xffffffffu, top);
+      // the row times 2^up has its largest value in [2^7, 2^8)
+      const int exponent = int(top >> 7);
+      const int up = top == 0 ? 0 : max(min(134 - exponent, 120), -120);
+      const float by = __uint_as_float(uint32_t(127 + up) << 23);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t h = 0, l = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t w2 = x[2 * k + j];
+          const float2 f = make_float2(__uint_as_float(w2 << 16) * by, __uint_as_float(w2 & 0xffff0000u) * by);
+          const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+          const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+          h |= uint32_t(c) << (16 * j);
+          l |= uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(f.x - b.x, f.y - b.y), __NV_SATFINITE, __NV_E4M3))
+               << (16 * j);
+        }
+        hi[k] = h;
+        lo[k] = l;
+      }
+      const uint32_t at = q0 + (lane >> 3) * kQBlock + sw128_offset(r, lane & 7);
+      sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      sts128(at + 4 * kQBlock, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      if (lane < 8) {
+        const uint32_t z[4] = {rope.x, rope.y, rope.z, rope.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __nv_bfloat162 p =
+              __floats2bfloat162_rn(__uint_as_float(z[k] << 16) * by, __uint_as_float(z[k] & 0xffff0000u) * by);
+          o[k] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        sts128(q0 + 8 * kQBlock + sw128_offset(r, lane), make_uint4(o[0], o[1], o[2], o[3]));
+      }
+      // a query that is not finite has no score that is
+      if (lane == 0) row_scale[r] = exponent == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(uint32_t(127 - up) << 23);
+      if (exponent == 255 && lane == 0) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
+    }
+  }
+
+  static __device__ void run(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl, int C, int w, int lane) {
+    const uint32_t base = smem_u32(sm);
+    const uint32_t v_full = map_to_cta(smem_u32(&ctl->v_full[0]), 0), q_full = map_to_cta(smem_u32(&ctl->q_full), 0);
+    const int own_keys = kCtaKeys * C + kWarpKeys * w, peer_keys = kCtaKeys * (1 - C) + kWarpKeys * w;
+    const int j = lane & 15, pair = lane >> 4;  // 16 codes from 16 j on; of two keys
+    const uint32_t k0 = base + kQSize;
+    // this lane's places in a tile: where its copies go, where it reads codes
+    // of the tile's own half, where its value chunks go
+    const uint32_t to_k = (lane >> 3) * kKBlock;
+    const uint32_t rope_at = 4 * kKBlock + sw128_offset(kWarpKeys * w + (lane >> 3), lane & 7);
+    const uint32_t from_k = (2 * C + (j >> 3)) * kKBlock;
+    const int turn = (j >> 2) & 1;  // which chunk first
+    const int scale_key = (lane >> 2) < kWarpKeys ? own_keys + (lane >> 2) : peer_keys + (lane >> 2) - kWarpKeys;
+    bool bad = false, ok = true;
+    // copies of tile t
+    auto copy = [&](int t) {
+      const int slot = t % kPlaces, st = t % 3;
+      // the K tile is free once QK^T of the tile three before is done
+      const bool ready = tree_wait(&ctl->place_full[slot], (t / kPlaces) & 1, ctl, kWsRaw) &&
+                         (t < 3 || tree_wait(&ctl->k_free[st], (t / 3 - 1) & 1, ctl, kWsFreed));
+      if (!__all_sync(0xffffffffu, ready)) return false;
+      const uint32_t k_tile = k0 + st * Sm::kKSize;
+#pragma unroll
+      for (int i = 0; i < kWarpKeys; ++i)
+        cp_async_16(k_tile + to_k + sw128_offset(kWarpKeys * w + i, lane & 7), ctl->row[slot][own_keys + i] + 16 * lane);
+      cp_async_16(k_tile + rope_at, ctl->row[slot][own_keys + (lane >> 3)] + 528 + 16 * (lane & 7));
+      cp_async_4(smem_u32(&ctl->scales[t & 3][lane & 3][scale_key]), ctl->row[slot][scale_key] + 512 + 4 * (lane & 3));
+      cp_async_arrive(&ctl->k_full[st]);
+      cp_async_commit();
+      return true;
+    };
+    // the peer's keys of tile t
+    uint4 peer[2];
+    auto load_peer = [&](int t) {
+      const int slot = t % kPlaces;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        peer[i] = ldg_stream(ctl->row[slot][peer_keys + 2 * i + pair] + 256 * C + 16 * j);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->place_empty[slot]);
+    };
+    // ahead: the tile copied next
+    Cursor ahead, now;
+    int t = 0, g = 0;  // tiles copied, converted
+    for (int i = 0; i < 2 && ok; ++i) {
+      ahead.next_tile(ctl);
+      if (!ahead.end) ok = copy(t++);
+      else cp_async_commit();
+    }
+    if (ok && t > 0) load_peer(0);
+    while (ok) {
+      // to the next tile; an item is handed back when it is left
+      const int before = now.item;
+      now.next_tile(ctl);
+      if (before >= 0 && now.item != before) leave_item(ctl, before, lane);
+      if (now.end) break;
+      const Item& it = now.at(ctl);
+      if (now.tile == 0) {  // the item's rows, in place of the last one's
+        if (g > 0 && !__all_sync(0xffffffffu, tree_wait(&ctl->k_free[(g - 1) % 3], ((g - 1) / 3) & 1, ctl, kWsFreed)))
+          break;
+        load_queries(a, it, base, ctl->row_scale[now.item & 1], C, w, lane);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(q_full);
+      }
+      // V is free once PV of the tile two before is done (and QK^T of the tile
+      // one before, which was issued earlier: copies two ahead need not wait)
+      if (g >= 2 && !__all_sync(0xffffffffu, tree_wait(&ctl->pv[g & 1], ((g >> 1) - 1) & 1, ctl, kWsPvDone))) break;
+      ahead.next_tile(ctl);
+      if (!ahead.end) ok = copy(t++);
+      else cp_async_commit();
+      if (!ok) break;
+      cp_async_wait<2>();  // this warp's copies of the tile
+      __syncwarp();
+      const uint32_t k_tile = k0 + (g % 3) * Sm::kKSize, v_tile = base + Sm::kOffV + (g & 1) * kVSize;
+      const float* table = &ctl->scales[g & 3][2 * C + (j >> 3)][0];
+      const bool mend = must_mend(ctl, it, now.tile, g);
+      uint4 x[8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int key = 2 * i + pair;
+        const uint4 own = lds128(k_tile + from_k + sw128_offset(kWarpKeys * w + key, j & 7));
+        const float s = table[own_keys + key], s_peer = ctl->scales[g & 3][2 * C + (j >> 3)][peer_keys + key];
+        __half2 hi, lo;
+        split_scale(s, hi, lo);
+        x[2 * i] = e4m3x8_scaled(turn ? make_uint2(own.z, own.w) : make_uint2(own.x, own.y), hi, lo);
+        x[2 * i + 1] = e4m3x8_scaled(turn ? make_uint2(own.x, own.y) : make_uint2(own.z, own.w), hi, lo);
+        bad |= scale_out_of_range(s) && ((ctl->valid[g & 15] >> (own_keys + key)) & 1);
+        split_scale(s_peer, hi, lo);
+        const uint4 p = peer[i];
+        x[4 + 2 * i] = e4m3x8_scaled(turn ? make_uint2(p.z, p.w) : make_uint2(p.x, p.y), hi, lo);
+        x[5 + 2 * i] = e4m3x8_scaled(turn ? make_uint2(p.x, p.y) : make_uint2(p.z, p.w), hi, lo);
+      }
+      if (mend) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = only_finite(x[i]);
+      }
+      const uint32_t block = v_tile + (j >> 2) * kVBlock;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int key = (i < 4 ? own_keys : peer_keys) + 2 * ((i >> 1) & 1) + pair;
+        sts128(block + sw128_offset(key, 2 * (j & 3) + ((i & 1) ^ turn)), x[i]);
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(v_full + 8 * (g & 1));
+      ++g;
+      if (g < t) load_peer(g);
+    }
+    cp_async_wait_all();
+    if (bad) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
+  }
+};
+
+// 4-bit rows: K and V tiles from registers, loaded a tile ahead.  8 lanes take
+// a key's half of the codes, 32 each.
+struct Fp4Keys {
+  static constexpr bool kFp4 = true;
+  static constexpr int kRowBytes = SMLA_FP4_ROW_BYTES;
+  using Sm = Shared<true>;
+
+  static __device__ void load_queries(const TreeDecodeArgs& a, const Item& it, uint32_t q0, float*, int C, int w,
+                                      int lane) {
+    uint32_t over = 0;
+    const int64_t row0 = int64_t(it.keys.first) * a.H + it.skip + kCtaRows * C;
+    const int live = it.rows - kCtaRows * C;
+#pragma unroll 9
+    for (int k = 0; k < 8 * 72 / 32; ++k) {
+      const int e = 32 * k + lane;
+      const int r = 8 * w + e / 72, chunk = e % 72;  // 8 dims each
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < live) v = ldg_stream(a.q + (row0 + r) * SMLA_QK_DIM + 8 * chunk);
+      over |= bf16x8_over_fp16(v);
+      sts128(q0 + (chunk >> 3) * kQBlock + sw128_offset(r, chunk & 7), bf16x8_to_f16x8(v));
+    }
+    if (over) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
+  }
+
+  struct Half {
+    uint4 code;
+    uint32_t scale;
+    __device__ __forceinline__ void load(const uint8_t* row, int half, int lane) {
+      code = ldg_stream(row + 128 * half + 16 * (lane & 7));
+      scale = reinterpret_cast<const uint16_t*>(row + 256 + 16 * half)[lane & 7];
+    }
+    // the lane's four chunks, in the order it stores them
+    __device__ __forceinline__ void values(uint4* v, int lane) const {
+      const int rot = (lane >> 1) & 3;
+      const __half2 s = __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(scale), __NV_E4M3));
+      const __half2 s0 = __low2half2(s), s1 = __high2half2(s);
+      uint4 c = code;
+      if (rot & 1) c = make_uint4(c.y, c.z, c.w, c.x);
+      if (rot & 2) c = make_uint4(c.z, c.w, c.x, c.y);
+      const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int m = 0; m < 4; ++m) v[m] = e2m1x8_scaled(word[m], ((m + rot) & 3) < 2 ? s0 : s1);
+    }
+    __device__ __forceinline__ bool nan() const { return (((scale & 0x7f7fu) + 0x0101u) & 0x8080u) != 0; }
+  };
+
+  static __device__ void run(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl, int C, int w, int lane) {
+    const uint32_t base = smem_u32(sm);
+    const uint32_t k_full = map_to_cta(smem_u32(&ctl->k_full[0]), 0), v_full = map_to_cta(smem_u32(&ctl->v_full[0]), 0),
+                   q_full = map_to_cta(smem_u32(&ctl->q_full), 0);
+    const int own_keys = kCtaKeys * C + kWarpKeys * w, peer_keys = kCtaKeys * (1 - C) + kWarpKeys * w;
+    const int j = lane & 7, key = lane >> 3, rot = (lane >> 1) & 3;
+    uint32_t over = 0;
+    bool bad = false;
+    Half own, other, peer;
+    uint4 rope;
+    auto load = [&](int t) {
+      const int slot = t % kPlaces;
+      if (!__all_sync(0xffffffffu, tree_wait(&ctl->place_full[slot], (t / kPlaces) & 1, ctl, kWsRaw))) return false;
+      const uint8_t* row = ctl->row[slot][own_keys + key];
+      own.load(row, C, lane);
+      other.load(row, 1 - C, lane);
+      rope = ldg_stream(row + 288 + 16 * j);
+      peer.load(ctl->row[slot][peer_keys + key], C, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->place_empty[slot]);
+      return true;
+    };
+    Cursor ahead, now;
+    int g = 0;
+    ahead.next_tile(ctl);
+    bool ok = ahead.end || load(0);
+    while (ok) {
+      const int before = now.item;
+      now.next_tile(ctl);
+      if (before >= 0 && now.item != before) leave_item(ctl, before, lane);
+      if (now.end) break;
+      const Item& it = now.at(ctl);
+      const int st = g & 1;
+      if (now.tile == 0) {  // the item's rows, in place of the last one's
+        if (g > 0 && !__all_sync(0xffffffffu, tree_wait(&ctl->k_free[(g - 1) & 1], ((g - 1) >> 1) & 1, ctl, kWsFreed)))
+          break;
+        load_queries(a, it, base, nullptr, C, w, lane);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(q_full);
+      }
+      const uint64_t valid = ctl->valid[g & 15];
+      const bool live = (valid >> (own_keys + key)) & 1;
+      bad |= live && (own.nan() || other.nan());
+      if (live) over |= bf16x8_over_fp16(rope);
+      // K: free once QK^T of the tile two before is done
+      if (g >= 2 && !__all_sync(0xffffffffu, tree_wait(&ctl->k_free[st], ((g >> 1) - 1) & 1, ctl, kWsFreed))) break;
+      const uint32_t k_tile = base + kQSize + st * Sm::kKSize;
+      uint4 x[4], y[4];
+      own.values(x, lane);
+      other.values(y, lane);
+      const uint32_t k_block = k_tile + (j >> 1) * kKBlock;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const uint32_t at = k_block + sw128_offset(kWarpKeys * w + key, 4 * (j & 1) + ((m + rot) & 3));
+        sts128(at + 4 * C * kKBlock, x[m]);
+        sts128(at + 4 * (1 - C) * kKBlock, y[m]);
+      }
+      sts128(k_tile + 8 * kKBlock + sw128_offset(kWarpKeys * w + key, j), bf16x8_to_f16x8(rope));
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(k_full + 8 * st);
+      // V: free once PV of the tile two before is done
+      if (g >= 2 && !__all_sync(0xffffffffu, tree_wait(&ctl->pv[st], ((g >> 1) - 1) & 1, ctl, kWsPvDone))) break;
+      peer.values(y, lane);
+      if (must_mend(ctl, it, now.tile, g)) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          x[m] = only_finite(x[m]);
+          y[m] = only_finite(y[m]);
+        }
+      }
+      const uint32_t v_block = base + Sm::kOffV + st * kVSize + (j >> 1) * kVBlock;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int c = 4 * (j & 1) + ((m + rot) & 3);
+        sts128(v_block + sw128_offset(own_keys + key, c), x[m]);
+        sts128(v_block + sw128_offset(peer_keys + key, c), y[m]);
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(v_full + 8 * st);
+      ++g;
+      ahead.next_tile(ctl);
+      if (!ahead.end) ok = load(g);
+    }
+    if (bad || over) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
+  }
+};
+
+// ------------------------------------------------------------------- MMAs
+// The first CTA's warp; the peer's keys have landed when its own says so.
+template <class F>
+__device__ void issue_mmas(uint8_t* sm, TreeCtl* ctl, uint32_t tb, int lane) {
+  using Sm = Shared<F::kFp4>;
+  constexpr int kSt = Sm::kStages;
+  constexpr uint32_t qk_desc = idesc_f16_f32(128, kTileKeys, false, false);  // fp16, and e4m3 in its kind
+  constexpr uint32_t rope_desc = idesc_bf16_f32(128, kTileKeys);
+  constexpr uint32_t pv_desc = idesc_f16_f32(128, 256, false, true);
+  const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0);
+  const uint32_t tbu = __shfl_sync(0xffffffffu, tb, 0);
+  const bool leader = elect_one();
+  Cursor cur;
+  int g = 0;  // tiles so far
+  bool ok = true;
+  while (ok && cur.next_item(ctl)) {
+    const int n = cur.tiles;
+    leave_item(ctl, cur.item, lane);
+    for (int j = 0; j <= n; ++j) {
+      if (j < n) {
+        const int t = g + j, st = t % kSt;
+        ok = tree_wait(&ctl->k_full[st], (t / kSt) & 1, ctl, kWsFull);
+        if (!F::kFp4) ok = ok && tree_wait(&ctl->k_peer[st], (t / kSt) & 1, ctl, kWsFull);
+        ok = ok && (j > 0 || tree_wait(&ctl->q_full, cur.item & 1, ctl, kWsQReady)) &&
+             (t == 0 || tree_wait(&ctl->s_read, (t - 1) & 1, ctl, kWsSFree));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t ad = sdesc_sw128(base, 16, 1024);
+          const uint64_t bd = sdesc_sw128(base + kQSize + st * Sm::kKSize, 16, 1024);
+          if constexpr (F::kFp4) {
+#pragma unroll
+            for (int k = 0; k < 36; ++k)
+              mma_ss_f16_pair(tbu + kScoreCol, ad + uint64_t((k >> 2) * (kQBlock >> 4) + 2 * (k & 3)),
+                              bd + uint64_t((k >> 2) * (kKBlock >> 4) + 2 * (k & 3)), qk_desc, k > 0);
+          } else {
+            fence_async_shared();  // the copies were generic writes
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {  // group k / 4: 128 codes, 32 an MMA
+              const uint64_t q = ad + uint64_t((k >> 2) * (kQBlock >> 4) + 2 * (k & 3));
+              const uint64_t b = bd + uint64_t((k >> 2) * (kKBlock >> 4) + 2 * (k & 3));
+              mma_ss_f8_pair(tbu + kScoreCol + 32 * (k >> 2), q, b, qk_desc, (k & 3) > 0);
+              mma_ss_f8_pair(tbu + kScoreCol + 32 * (k >> 2), q + 4 * (kQBlock >> 4), b, qk_desc, 1);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ss_f16_pair(tbu + kScoreCol + 128, ad + uint64_t(8 * (kQBlock >> 4) + 2 * k),
+                              bd + uint64_t(4 * (kKBlock >> 4) + 2 * k), rope_desc, k > 0);
+          }
+          mma_commit_pair(&ctl->qk[t & 1]);
+          mma_commit_pair(&ctl->k_free[st]);
+        }
+        __syncwarp();
+      }
+      if (j > 0) {
+        const int t = g + j - 1;
+        ok = tree_wait(&ctl->v_full[t & 1], (t >> 1) & 1, ctl, kWsFull) &&
+             tree_wait(&ctl->p_full, t & 1, ctl, kWsPFull) &&
+             (j > 1 || cur.item == 0 || tree_wait(&ctl->out_read, (cur.item - 1) & 1, ctl, kWsSFree));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t ad = sdesc_sw128(base + Sm::kOffP, 16, 1024);
+          const uint32_t v = base + Sm::kOffV + (t & 1) * kVSize;
+#pragma unroll
+          for (int k = 0; k < kTileKeys / 16; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              mma_ss_f16_pair(tbu + kOutCol + 128 * i, ad + 2 * k,
+                              sdesc_sw128(v + 2 * i * kVBlock, kVBlock, 1024) + uint64_t(k * (2048 >> 4)), pv_desc,
+                              j > 1 || k > 0);
+          mma_commit_pair(&ctl->pv[t & 1]);
+        }
+        __syncwarp();
+      }
+    }
+    g += n;
+  }
+  // every MMA has completed before tensor memory is given back
+  if (leader) mma_commit_pair(&ctl->end);
+  __syncwarp();
+}
+
+// The second CTA's: tells the first's when its copies of a K tile have landed.
+template <class F>
+__device__ void tell_peer(TreeCtl* ctl, int lane) {
+  const uint32_t k_peer = map_to_cta(smem_u32(&ctl->k_peer[0]), 0);
+  Cursor cur;
+  int t = 0;
+  while (cur.next_item(ctl)) {
+    const int n = cur.tiles;
+    leave_item(ctl, cur.item, lane);
+    for (int j = 0; !F::kFp4 && j < n; ++j, ++t) {
+      if (!__all_sync(0xffffffffu, tree_wait(&ctl->k_full[t % 3], (t / 3) & 1, ctl, kWsFull))) return;
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(k_peer + 8 * (t % 3));
+    }
   }
 }
 
-constexpr int kWarps = 4;
+// ------------------------------------------------------- softmax and output
+// 32 bits of a row's mask from node j0 on; nodes before 0 are prefix keys,
+// which every row sees.
+__device__ __forceinline__ uint32_t seen_from(const uint64_t* mask, int words, int j0) {
+  if (j0 <= -32) return 0xffffffffu;
+  if (j0 < 0) return (uint32_t(mask[0]) << -j0) | ((1u << -j0) - 1u);
+  const int w = j0 >> 6, s = j0 & 63;
+  if (w >= words) return 0;
+  uint64_t x = mask[w] >> s;
+  if (s > 32 && w + 1 < words) x |= mask[w + 1] << (64 - s);
+  return uint32_t(x);
+}
 
-template <bool kFp4>
-__global__ void __launch_bounds__(32 * kWarps) tree_decode_kernel(const __grid_constant__ TreeDecodeArgs a) {
-  constexpr int kRowBytes = kFp4 ? SMLA_FP4_ROW_BYTES : SMLA_ROW_BYTES;
-  __shared__ Keys keys;
-  __shared__ int s_req;
-  __shared__ float s_out[kWarps][SMLA_V_DIM], s_m[kWarps], s_l[kWarps];
+template <class F>
+__device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl, uint32_t tb, int C, int tid) {
+  const int warp = tid >> 5, lane = tid & 31;
+  // the thread's row; which 32 keys and 256 value dims its lane holds, and
+  // which half of those are the thread's
+  const int r = tid & 63, half = (tid >> 6) & 1, part = tid >> 7;
+  const uint32_t lanes = tmem_addr(tb, 32 * (warp & 3), 0);
+  const uint32_t p_row = smem_u32(sm) + Shared<F::kFp4>::kOffP;
+  const uint32_t s_read = map_to_cta(smem_u32(&ctl->s_read), 0), p_full = map_to_cta(smem_u32(&ctl->p_full), 0),
+                 out_read = map_to_cta(smem_u32(&ctl->out_read), 0);
+  Cursor cur;
+  int g = 0;
+  bool ok = true;
+  while (ok && cur.next_item(ctl)) {
+    const Item& it = cur.at(ctl);
+    const int n = cur.tiles;
+    const int row = kCtaRows * C + r;  // of the tile
+    const bool live = row < it.rows;
+    const int64_t out_row = int64_t(it.keys.first) * a.H + it.skip + row;
+    const uint64_t* mask =
+        a.masks + (live ? int64_t(it.keys.first) + (it.skip + row) / a.H : it.keys.first) * a.mask_words;
+    float m_ref = -INFINITY, l = 0.f;  // log2 domain
+    float c2 = a.sm_scale * kLog2e;
+    for (int j = 0; j < n; ++j, ++g) {
+      const int b = g & 1;
+      ok = __all_sync(0xffffffffu, tree_wait(&ctl->qk[b], (g >> 1) & 1, ctl, kWsSFull));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t scores = lanes + kScoreCol + 16 * part;
+      uint32_t s[16];
+      tmem_ld16(scores + (F::kFp4 ? 0 : 128), s);
+      if constexpr (!F::kFp4) {
+        if (j == 0) c2 *= ctl->row_scale[cur.item & 1][r];
+        uint32_t x[2][16];
+        uint64_t sum[8];
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          tmem_ld16(scores + 32 * q, x[0]);
+          tmem_ld16(scores + 32 * (q + 1), x[1]);
+          tmem_ld_wait();
+          if (q == 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum[k] = pack2(s[2 * k], s[2 * k + 1]);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float4* sc = reinterpret_cast<const float4*>(&ctl->scales[g & 3][q + i][kCtaKeys * half + 16 * part]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float4 f = sc[k];
+              sum[2 * k] = fma2(pack2(x[i][4 * k], x[i][4 * k + 1]), pack2(f.x, f.y), sum[2 * k]);
+              sum[2 * k + 1] = fma2(pack2(x[i][4 * k + 2], x[i][4 * k + 3]), pack2(f.z, f.w), sum[2 * k + 1]);
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 f = unpack2(sum[k]);
+          s[2 * k] = __float_as_uint(f.x);
+          s[2 * k + 1] = __float_as_uint(f.y);
+        }
+      }
+      const int first = (it.tile0 + j) * kTileKeys + kCtaKeys * half + 16 * part;  // key of s[0]
+      uint32_t see = uint32_t(ctl->valid[g & 15] >> (kCtaKeys * half + 16 * part)) & 0xffffu;
+      if (first + 16 > it.keys.prefix) see &= seen_from(mask, a.mask_words, first - it.keys.prefix);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(s_read);
+      if (see != 0xffffu) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (!((see >> k) & 1)) s[k] = 0xff800000u;
+      }
+      float top = __uint_as_float(s[0]);
+#pragma unroll
+      for (int k = 1; k < 16; ++k) top = fmaxf(top, __uint_as_float(s[k]));
+      ctl->tops[b][tid] = top;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->top[b]);
+      ok = __all_sync(0xffffffffu, tree_wait(&ctl->top[b], (g >> 1) & 1, ctl, kWsExchange));
+      if (!ok) break;
+      top = fmaxf(fmaxf(ctl->tops[b][r], ctl->tops[b][64 + r]), fmaxf(ctl->tops[b][128 + r], ctl->tops[b][192 + r])) * c2;
+      float alpha = 1.f;
+      const bool moves = top > m_ref + 8.f;
+      if (moves) {
+        alpha = ex2(m_ref - top);
+        m_ref = top;
+      }
+      const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+      float sum = 0.f;
+      uint32_t p[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float x = ex2(fmaf(__uint_as_float(s[2 * k]), c2, -ref));
+        const float y = ex2(fmaf(__uint_as_float(s[2 * k + 1]), c2, -ref));
+        sum += x + y;
+        p[k] = h2_bits(__floats2half2_rn(x, y));
+      }
+      l = l * alpha + sum;
+      if (j > 0) {
+        // PV of the tile before has read its P and stored its output
+        ok = __all_sync(0xffffffffu, tree_wait(&ctl->pv[b ^ 1], ((g - 1) >> 1) & 1, ctl, kWsPvDone));
+        if (!ok) break;
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll 1
+          for (int cc = 4 * part; cc < 4 * part + 4; ++cc) {
+            uint32_t o[32];
+            tmem_ld32(lanes + kOutCol + 32 * cc, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st32(lanes + kOutCol + 32 * cc, o);
+          }
+          tmem_st_wait();
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        sts128(p_row + sw128_offset(r, 4 * half + 2 * part + q),
+               make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]));
+      fence_async_shared();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(p_full);
+    }
+    if (!ok) break;
+    ctl->sums[tid] = l;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->sum);
+    ok = __all_sync(0xffffffffu, tree_wait(&ctl->sum, cur.item & 1, ctl, kWsExchange) &&
+                                     tree_wait(&ctl->pv[(g - 1) & 1], ((g - 1) >> 1) & 1, ctl, kWsPvLast));
+    if (!ok) break;
+    tc_fence_after();
+    l = (ctl->sums[r] + ctl->sums[64 + r]) + (ctl->sums[128 + r] + ctl->sums[192 + r]);
+    const bool partial = it.part >= 0;
+    const int64_t place = partial ? int64_t(it.part) * kPairRows + row : out_row;
+    if (live && half == 0 && part == 0) {
+      if (partial) {
+        a.ws_ml[2 * place] = m_ref;
+        a.ws_ml[2 * place + 1] = l;
+      } else {
+        a.lse[place] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+      }
+    }
+    uint16_t* dst = (partial ? a.ws_o : a.out) + place * SMLA_V_DIM + 256 * half;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const bool aligned = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
+#pragma unroll 1
+    for (int cc = 4 * part; cc < 4 * part + 4; ++cc) {
+      uint32_t x[32], o[16];
+      tmem_ld32(lanes + kOutCol + 32 * cc, x);
+      tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        // a row with no key has no output, whatever its tile's other rows hold
+        const float y = l == 0.f ? 0.f : __uint_as_float(x[2 * k]) * inv;
+        const float z = l == 0.f ? 0.f : __uint_as_float(x[2 * k + 1]) * inv;
+        if (partial) {
+          o[k] = h2_bits(__floats2half2_rn(y, z));
+        } else {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(y, z);
+          o[k] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+      }
+      if (live && aligned) {
+        stg256(dst + 32 * cc, o);
+        stg256(dst + 32 * cc + 16, o + 8);
+      } else if (live) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          reinterpret_cast<uint4*>(dst + 32 * cc)[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_at(out_read);
+    leave_item(ctl, cur.item, lane);
+  }
+}
+
+template <class F>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
+    tree_decode_kernel(const __grid_constant__ TreeDecodeArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  TreeCtl* ctl = reinterpret_cast<TreeCtl*>(sm + Shared<F::kFp4>::kOffCtl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int32_t t = int32_t(blockIdx.x) / a.H, h = int32_t(blockIdx.x) % a.H;
+  const int C = int(cluster_ctarank());
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->qk[i], 1);
+      mbar_init(&ctl->pv[i], 1);
+      mbar_init(&ctl->v_full[i], 2 * kConvWarps);  // both CTAs'
+      mbar_init(&ctl->top[i], kSoftWarps);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&ctl->k_free[i], 1);
+      mbar_init(&ctl->k_full[i], F::kFp4 ? 2 * kConvWarps : 32 * kConvWarps);  // fp8: this CTA's copying threads
+      mbar_init(&ctl->k_peer[i], 1);
+    }
+    for (int i = 0; i < kPlaces; ++i) {
+      mbar_init(&ctl->place_full[i], 1);
+      mbar_init(&ctl->place_empty[i], kConvWarps);
+    }
+    mbar_init(&ctl->q_full, 2 * kConvWarps);
+    mbar_init(&ctl->s_read, 2 * kSoftWarps);
+    mbar_init(&ctl->p_full, 2 * kSoftWarps);
+    mbar_init(&ctl->out_read, 2 * kSoftWarps);
+    mbar_init(&ctl->sum, kSoftWarps);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&ctl->item_full[i], 1);
+      mbar_init(&ctl->item_empty[i], kSoftWarps + kConvWarps + 2);  // all but the list's own
+    }
+    mbar_init(&ctl->end, 1);
+    ctl->abort = 0;
+    fence_mbar_init_cluster();
+  }
+  if (warp == kIssueWarp) {
+    tmem_alloc_pair(&ctl->tbase, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = ctl->tbase;
   griddep_launch_dependents();
   griddep_wait();
+
+  // all requests' units, and where this pair's range begins
   unsigned err = 0;
-  if (tid == 0) {
-    int lo = 0, hi = a.B;  // the last request that starts at or before t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.row_start[mid] <= t) lo = mid;
-      else hi = mid;
+  int64_t mine = 0;
+  for (int32_t b = tid; b < a.B; b += kTreeThreads) {
+    const Request r = load_request(a, b, err);
+    mine += int64_t(row_tiles(a, r)) * tile_units(a, r);
+  }
+  if (err && blockIdx.x == 0) atomicOr(&g_decode_error, err);
+  int64_t total = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) ctl->warp_units[warp] = total;
+  __syncthreads();
+  int64_t units = 0;
+  for (int w = 0; w < kTreeWarps; ++w) units += ctl->warp_units[w];
+  const int64_t pairs = gridDim.x >> 1;
+  const int64_t per_pair = max((units + pairs - 1) / pairs, int64_t(a.min_units));
+  const int64_t u0 = per_pair * (blockIdx.x >> 1);
+  int64_t base = 0;
+  for (int32_t b0 = 0; b0 < a.B && base <= u0; b0 += kTreeThreads) {
+    const int32_t b = b0 + tid;
+    int64_t v = 0;
+    if (b < a.B) {
+      unsigned ignored = 0;
+      const Request r = load_request(a, b, ignored);
+      v = int64_t(row_tiles(a, r)) * tile_units(a, r);
     }
-    const bool ok = t >= a.row_start[lo] && t < a.row_start[lo + 1] && request_keys(a, lo, keys, err);
-    s_req = ok ? lo : -1;
+    int64_t upto = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    __syncthreads();  // the sums before have been read
+    if (lane == 31) ctl->warp_units[warp] = upto;
+    __syncthreads();
+    int64_t begin = base + upto - v;
+    for (int w = 0; w < kTreeWarps; ++w) {
+      if (w < warp) begin += ctl->warp_units[w];
+      base += ctl->warp_units[w];
+    }
+    if (begin <= u0 && u0 < begin + v) {
+      ctl->start_req = b;
+      ctl->start = u0 - begin;
+    }
   }
   __syncthreads();
-  if (err) atomicOr(&g_tree_decode_error, err);
-  if (s_req < 0) return;
-  err = 0;
-  const uint16_t* q = a.q + (int64_t(t) * a.H + h) * SMLA_QK_DIM;
-  float qv[SMLA_QK_DIM / 32], o[SMLA_V_DIM / 32] = {};
+  cluster_sync();  // the peer's barriers are initialised
+
+  if (warp < kSoftWarps) {
+    softmax_rows<F>(a, sm, ctl, tb, C, tid);
+  } else if (warp < kIssueWarp) {
+    F::run(a, sm, ctl, C, warp - kSoftWarps, lane);
+  } else if (warp == kIssueWarp) {
+    if (C == 0) issue_mmas<F>(sm, ctl, tb, lane);
+    else tell_peer<F>(ctl, lane);
+    // also after a wait that gave up: the pair's MMAs have completed
+    int no_abort = 0;
+    wait_phase<false>(&ctl->end, 0, &no_abort, kWsDrain);
+  } else if (warp == kIssueWarp + 1) {
+    list_work(a, ctl, C, units, per_pair, lane);
+  } else {
+    look_up_rows(a, ctl, F::kRowBytes, lane);
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // neither CTA reaches into the other any more
+  tc_fence_after();
+  if (warp == kIssueWarp) tmem_dealloc_pair(tb, 512);
+  __syncwarp();
+  cluster_sync();
+}
+
+// Merges the row tiles that were cut: with m and l the parts' log2-domain
+// references and sums, M = max m over the parts that hold a key, out = sum l
+// 2^(m - M) O / sum l 2^(m - M).  One warp a row, 16 value dims a lane, parts
+// in the order of their keys.
+constexpr int kMergeWarps = 8;
+constexpr int kMergeBlocks = kPairRows / kMergeWarps;
+
+__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const TreeDecodeArgs a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pair = int(blockIdx.x) / kMergeBlocks;
+  const int row = int(blockIdx.x) % kMergeBlocks * kMergeWarps + warp;
+  griddep_launch_dependents();
+  griddep_wait();
+  const SplitTile t = static_cast<const SplitTile*>(a.ws_desc)[pair];
+  if (row >= t.rows) return;
+  auto place = [&](int i) { return int64_t(i == 0 ? t.place : 2 * (pair + i)) * kPairRows + row; };
+  float top = -INFINITY;
+  for (int i = lane; i < t.parts; i += 32) {
+    const float m = a.ws_ml[2 * place(i)];
+    if (a.ws_ml[2 * place(i) + 1] != 0.f) top = fmaxf(top, m);
+  }
 #pragma unroll
-  for (int k = 0; k < SMLA_QK_DIM / 32; ++k) qv[k] = __uint_as_float(uint32_t(q[32 * k + lane]) << 16);
-  float m = -INFINITY, l = 0.f;
-  for (int32_t i = warp; i < keys.total; i += kWarps) {
-    const int32_t j = i - prefix_keys(keys);
-    if (j >= 0 && !((a.masks[int64_t(t) * a.mask_words + (j >> 6)] >> (j & 63)) & 1)) continue;
-    const uint8_t* row = key_row(a, keys, s_req, i, kRowBytes, err);
-    if (row == nullptr) continue;
-    float k[SMLA_QK_DIM / 32], s = 0.f;
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float sum = 0.f, acc[16] = {};
+#pragma unroll 4
+  for (int i = 0; i < t.parts; ++i) {
+    const int64_t p = place(i);
+    const float m = a.ws_ml[2 * p], l = a.ws_ml[2 * p + 1];
+    const uint4* src = reinterpret_cast<const uint4*>(a.ws_o + p * SMLA_V_DIM + 16 * lane);
+    const uint4 lo = src[0], hi = src[1];
+    const float w = l == 0.f ? 0.f : l * exp2f(m - top);
+    sum += w;
+    const uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-    for (int c = 0; c < SMLA_QK_DIM / 32; ++c) {
-      k[c] = key_value<kFp4>(row, 32 * c + lane);
-      s = fmaf(qv[c], k[c], s);
+    for (int k = 0; k < 8; ++k) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[k]));
+      acc[2 * k] = fmaf(w, f.x, acc[2 * k]);
+      acc[2 * k + 1] = fmaf(w, f.y, acc[2 * k + 1]);
     }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t o[8];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.sm_scale;
-    const float top = fmaxf(m, s);
-    const float keep = expf(m - top), p = expf(s - top);
-    l = l * keep + p;
-    m = top;
-#pragma unroll
-    for (int c = 0; c < SMLA_V_DIM / 32; ++c) o[c] = fmaf(p, k[c], o[c] * keep);
+  for (int k = 0; k < 8; ++k) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    o[k] = *reinterpret_cast<const uint32_t*>(&v);
   }
-  if (err) atomicOr(&g_tree_decode_error, err);
-#pragma unroll
-  for (int c = 0; c < SMLA_V_DIM / 32; ++c) s_out[warp][32 * c + lane] = o[c];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  __syncthreads();
-  float top = -INFINITY, sum = 0.f, w[kWarps];
-  for (int x = 0; x < kWarps; ++x) top = fmaxf(top, s_m[x]);
-  for (int x = 0; x < kWarps; ++x) {
-    w[x] = s_m[x] == -INFINITY ? (s_l[x] == s_l[x] ? 0.f : 1.f) : expf(s_m[x] - top);
-    sum += s_l[x] * w[x];
-  }
-  for (int c = tid; c < SMLA_V_DIM; c += 32 * kWarps) {
-    float v = 0.f;
-    for (int x = 0; x < kWarps; ++x) v += w[x] * s_out[x][c];
-    reinterpret_cast<__nv_bfloat16*>(a.out)[(int64_t(t) * a.H + h) * SMLA_V_DIM + c] =
-        __float2bfloat16_rn(sum == 0.f ? 0.f : v / sum);
-  }
-  if (tid == 0) a.lse[int64_t(t) * a.H + h] = sum == 0.f ? -INFINITY : top + logf(sum);
+  uint4* dst = reinterpret_cast<uint4*>(a.out + (int64_t(t.row) + row) * SMLA_V_DIM + 16 * lane);
+  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  if (lane == 0) a.lse[int64_t(t.row) + row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// How a call is laid out, from its shape alone: its pairs, and whether a row
+// tile may be cut (never when one pair's least range holds all its keys).
+struct TreePlan {
+  int pairs, min_units;
+  bool split;
+  size_t ml_off, o_off, bytes;
+};
+
+constexpr int kMinUnits = 4;
+
+TreePlan plan_tree(int32_t T, int32_t B, int32_t H, int64_t max_keys) {
+  TreePlan p;
+  const int64_t key_tiles = (max_keys + kTileKeys - 1) / kTileKeys;
+  const int64_t row_tiles = int64_t(T) * H / kPairRows + (B < T ? B : T);
+  p.split = key_tiles > 8;
+  p.min_units = p.split ? kMinUnits : 1;
+  const int64_t units = p.split ? row_tiles * key_tiles : row_tiles;
+  const int64_t need = (units + p.min_units - 1) / p.min_units;
+  p.pairs = int(need < 1 ? 1 : need < kPairs ? need : kPairs);
+  p.ml_off = 4096;
+  p.o_off = p.ml_off + size_t(2) * p.pairs * kPairRows * 2 * sizeof(float);
+  p.bytes = p.split ? p.o_off + size_t(2) * p.pairs * kPairRows * SMLA_V_DIM * sizeof(uint16_t) : 0;
+  static_assert(kPairs * sizeof(SplitTile) <= 4096, "descriptors fit");
+  return p;
 }
 
 }  // namespace
 
-size_t tree_decode_workspace_bytes(int32_t, int32_t, int32_t, int64_t) { return 0; }
+size_t tree_decode_workspace_bytes(int32_t T, int32_t B, int32_t H, int64_t max_keys) {
+  return T > 0 && B > 0 ? plan_tree(T, B, H, max_keys).bytes : 0;
+}
 
-cudaError_t launch_tree_decode(const TreeDecodeArgs& args, bool fp4, cudaStream_t s) {
+template <class F>
+static cudaError_t launch_tree(const TreeDecodeArgs& a, int pairs, cudaStream_t s) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool tracked = dev >= 0 && dev < 64;
+  if (!tracked || !done[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(tree_decode_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             tree_smem<F::kFp4>());
+    if (e != cudaSuccess) return e;
+    if (tracked) done[dev].store(true, std::memory_order_release);
+  }
+  return launch_overlapped(tree_decode_kernel<F>, unsigned(2 * pairs), kTreeThreads, tree_smem<F::kFp4>(), s, a);
+}
+
+cudaError_t launch_tree_decode(const TreeDecodeArgs& args, int64_t max_keys, bool fp4, cudaStream_t s) {
   TreeDecodeArgs a = args;
   // a round past 2^31 positions never completes
   const uint64_t round = uint64_t(a.interleave) * uint32_t(a.D);
   a.div_ID = make_fastdiv(uint32_t(round > (1ull << 31) ? (1ull << 31) : round));
   a.div_bs = make_fastdiv(uint32_t(a.block_size));
-  const unsigned grid = unsigned(a.T) * unsigned(a.H);
-  return fp4 ? launch_overlapped(tree_decode_kernel<true>, grid, 32 * kWarps, 0, s, a)
-             : launch_overlapped(tree_decode_kernel<false>, grid, 32 * kWarps, 0, s, a);
+  const TreePlan p = plan_tree(a.T, a.B, a.H, max_keys);
+  a.split = p.split;
+  a.min_units = p.min_units;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  a.ws_desc = ws;
+  a.ws_ml = p.split ? reinterpret_cast<float*>(ws + p.ml_off) : nullptr;
+  a.ws_o = p.split ? reinterpret_cast<uint16_t*>(ws + p.o_off) : nullptr;
+  const cudaError_t e = fp4 ? launch_tree<Fp4Keys>(a, p.pairs, s) : launch_tree<Fp8Keys>(a, p.pairs, s);
+  if (e != cudaSuccess || !p.split) return e;
+  return launch_overlapped(tree_merge_kernel, unsigned(p.pairs * kMergeBlocks), 32 * kMergeWarps, 0, s, a);
 }
 
-cudaError_t tree_decode_error_word(uint32_t* flags, bool clear) {
-  unsigned int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_tree_decode_error, sizeof(v));
-  if (e != cudaSuccess) return e;
-  *flags |= v;
-  if (clear) {
-    v = 0;
-    e = cudaMemcpyToSymbol(g_tree_decode_error, &v, sizeof(v));
-  }
-  return e;
-}
+cudaError_t tree_decode_error_word(uint32_t* flags, bool clear) { return read_error_word(flags, clear); }
 
 }  // namespace smla

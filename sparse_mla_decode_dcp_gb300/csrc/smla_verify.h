@@ -62,6 +62,12 @@ struct TreeDecodeArgs {
   float* lse;                  // [T, H]
   void* workspace;
   size_t workspace_bytes;
+  // set by the launcher
+  int32_t split;               // a tile of rows may be cut into key ranges
+  int32_t min_units;           // key tiles a pair takes at least
+  void* ws_desc;               // per pair: the cut tile it begins
+  float* ws_ml;                // [2 pairs, 128, 2]
+  uint16_t* ws_o;              // fp16 [2 pairs, 128, 512]
 };
 
 // A batch of matrices: entry (g, row, col) is at g * batch + row * rows + col
@@ -98,7 +104,8 @@ struct MatmulArgs {
   int32_t m_tiles, n_tiles, k_blocks, splits, stages, vec;
 };
 
-cudaError_t launch_tree_decode(const TreeDecodeArgs& a, bool fp4, cudaStream_t s);
+// max_keys: of a request
+cudaError_t launch_tree_decode(const TreeDecodeArgs& a, int64_t max_keys, bool fp4, cudaStream_t s);
 size_t tree_decode_workspace_bytes(int32_t T, int32_t B, int32_t H, int64_t max_keys);
 cudaError_t tree_decode_error_word(uint32_t* flags, bool clear);
 
