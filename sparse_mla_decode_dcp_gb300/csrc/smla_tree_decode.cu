@@ -40,11 +40,10 @@
 //     maximum and sum), which a second kernel merges.
 //
 // Warps: 0-7 softmax and output (two threads a lane of tensor memory), 8-15
-// load cache rows ahead and convert them, 16 issues the MMAs (the first CTA's,
-// for both; the second's tells it of its keys), 17 lists the pair's work, 18
-// looks up the keys' rows.  Every wait is bounded; one that
+// convert cache rows, 16 issues the MMAs (the first CTA's, for both; the
+// second's tells it of its keys), 17 lists the pair's work, 18 looks up the
+// keys' rows, 19 copies fp8 rows into the K tiles.  Every wait is bounded; one that
 // gives up sets SMLA_DEVERR_TIMEOUT and the CTA unwinds.
-#define SMLA_WAITS_OUT_OF_LINE
 #include "smla_decode_kernel.cuh"
 
 #include "smla_pair.cuh"
@@ -57,7 +56,7 @@ constexpr int kPairRows = 128, kCtaRows = 64;
 constexpr int kTileKeys = 64, kCtaKeys = 32;
 constexpr int kSoftWarps = 8, kConvWarps = 8;
 constexpr int kIssueWarp = kSoftWarps + kConvWarps;
-constexpr int kTreeWarps = kIssueWarp + 3;
+constexpr int kTreeWarps = kIssueWarp + 4;
 constexpr int kTreeThreads = 32 * kTreeWarps;
 constexpr int kWarpKeys = kCtaKeys / kConvWarps;  // of each CTA, a converter warp's
 constexpr int kItems = 8;   // work items listed ahead
@@ -76,7 +75,10 @@ template <bool kFp4> struct Shared {
   static constexpr int kKSize = (kFp4 ? 9 : 5) * kKBlock;
   static constexpr int kOffV = kQSize + kStages * kKSize;
   static constexpr int kOffP = kOffV + 2 * kVSize;
-  static constexpr int kOffCtl = kOffP + kCtaRows * 128;
+  static constexpr int kPSize = kCtaRows * 128;
+  // P tiles, and how many tiles PV stays behind QK^T
+  static constexpr int kProbs = kFp4 ? 1 : 2;
+  static constexpr int kOffCtl = kOffP + kProbs * kPSize;
 };
 
 // tensor memory: the output's 2 x 128 columns, a tile's scores (32 columns for
@@ -102,8 +104,10 @@ struct Item {
 };
 
 struct TreeCtl {
-  uint64_t qk[2], pv[2], k_free[3], k_full[3], k_peer[3], v_full[2], q_full, s_read, p_full, out_read, top[2],
-      sum, item_full[kItems], item_empty[kItems], place_full[kPlaces], place_empty[kPlaces], end;
+  // qk, s_read: fp8 rows, of the scores of groups 0 and 1 and of the rest; fp4
+  // rows, of even and odd tiles' scores
+  uint64_t qk[2], s_read[2], pv[2], k_free[3], k_full[3], k_read[3], k_peer[3], v_full[2], q_full, p_full[2],
+      out_read, top[2], sum, item_full[kItems], item_empty[kItems], place_full[kPlaces], place_empty[kPlaces], end;
   uint32_t tbase;
   int abort;
   uint64_t valid[16];                     // per tile (mod 16): which of its keys exist
@@ -128,8 +132,25 @@ struct SplitTile {
   int32_t parts, place;  // partial results: `place`, then the first of each pair behind
 };
 
-__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, TreeCtl* ctl, uint32_t site) {
-  return wait_phase<false>(bar, parity, &ctl->abort, site);
+// Every wait is bounded: it gives up after so many looks, each of which
+// suspends the thread for up to kSuspendNs (2.6 s in all), or when another wait
+// of the CTA has; the first to do so leaves its site in ctl->abort, which the
+// CTA reports at its end.  A few instructions a wait matter: the roles' code
+// runs once a tile each, and past some 128 KB of it warps wait for instructions
+// (waits that read the timer, and every loop unrolled, 154 KB: 5.1 ms for a
+// batch of 32 requests; without 2.6 and less).
+constexpr int kLooks = 1 << 17;
+
+__noinline__ __device__ bool look_again(uint64_t* bar, uint32_t parity, volatile int* abort, int site) {
+#pragma unroll 1
+  for (int n = kLooks; n > 0 && *abort == 0; --n)
+    if (mbar_try_wait(bar, parity)) return true;
+  if (*abort == 0) *abort = site + 1;
+  return false;
+}
+
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, TreeCtl* ctl, int site) {
+  return mbar_try_wait(bar, parity) || look_again(bar, parity, &ctl->abort, site);
 }
 
 // Of the first n positions, how many pool d holds.
@@ -223,9 +244,8 @@ __device__ __forceinline__ const uint8_t* key_row(const TreeDecodeArgs& a, const
 
 // fp16 values that are not finite, to zero.
 __device__ __forceinline__ uint32_t only_finite(uint32_t w) {
-  if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u;
-  if ((w & 0x7c000000u) == 0x7c000000u) w &= 0xffffu;
-  return w;
+  const __half2 v = *reinterpret_cast<const __half2*>(&w);
+  return w & __heq2_mask(__hsub2(v, v), __half2half2(__ushort_as_half(0)));
 }
 __device__ __forceinline__ uint4 only_finite(uint4 v) {
   return make_uint4(only_finite(v.x), only_finite(v.y), only_finite(v.z), only_finite(v.w));
@@ -337,40 +357,45 @@ __device__ void list_work(const TreeDecodeArgs& a, TreeCtl* ctl, int C, int64_t 
 }
 
 // --------------------------------------------------------------- the keys' rows
-// One warp, two keys a lane, a tile ahead.  A missing key's row is read from
-// somewhere else (a row of q is longer than a cache row): its score is masked,
-// and what goes into the value tile is made finite.
+// One warp, half a tile at a time, a key a lane, and half a tile ahead.  A
+// missing key's row is read from somewhere else (a row of q is longer than a
+// cache row): its score is masked, and what goes into the value tile is made
+// finite.
 __device__ void look_up_rows(const TreeDecodeArgs& a, TreeCtl* ctl, int row_bytes, int lane) {
   const uint8_t* elsewhere = reinterpret_cast<const uint8_t*>(a.q);
   unsigned err = 0;
   Cursor ahead;
-  Place place[2];
-  auto find = [&](int before) {
-    if (before >= 0 && ahead.item != before) leave_item(ctl, before, lane);
-    if (ahead.end) return;
-    const Item& it = ahead.at(ctl);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      place[i] = find_key(a, it.keys, it.req, (it.tile0 + ahead.tile) * kTileKeys + 32 * i + lane);
-  };
-  ahead.next_tile(ctl);
-  find(-1);
-  for (int t = 0; !ahead.end; ++t) {
-    const int slot = t % kPlaces;
-    if (t >= kPlaces && !__all_sync(0xffffffffu, tree_wait(&ctl->place_empty[slot], (t / kPlaces - 1) & 1, ctl,
-                                                           kWsRawEmpty)))
-      break;
-    const uint8_t* row[2] = {key_row(a, place[0], row_bytes, err), key_row(a, place[1], row_bytes, err)};
-    const uint32_t lo = __ballot_sync(0xffffffffu, row[0] != nullptr);
-    const uint32_t hi = __ballot_sync(0xffffffffu, row[1] != nullptr);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) ctl->row[slot][32 * i + lane] = row[i] ? row[i] : elsewhere;
-    if (lane == 0) ctl->valid[t & 15] = uint64_t(hi) << 32 | lo;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ctl->place_full[slot]);
-    const int before = ahead.item;
-    ahead.next_tile(ctl);
-    find(before);
+  Place place;
+  uint32_t low = 0;  // which of the tile's first keys exist
+#pragma unroll 1
+  for (int h = -1;; ++h) {  // half tile h is stored, h + 1 looked up
+    const uint8_t* row = h < 0 ? nullptr : key_row(a, place, row_bytes, err);
+    const bool stores = h >= 0;
+    if (((h + 1) & 1) == 0) {
+      const int before = ahead.item;
+      ahead.next_tile(ctl);
+      if (before >= 0 && ahead.item != before) leave_item(ctl, before, lane);
+    }
+    if (!ahead.end) {
+      const Item& it = ahead.at(ctl);
+      place = find_key(a, it.keys, it.req, (it.tile0 + ahead.tile) * kTileKeys + 32 * ((h + 1) & 1) + lane);
+    }
+    if (stores) {
+      const int t = h >> 1, slot = t % kPlaces;
+      if ((h & 1) == 0 && t >= kPlaces &&
+          !__all_sync(0xffffffffu, tree_wait(&ctl->place_empty[slot], (t / kPlaces - 1) & 1, ctl, kWsRawEmpty)))
+        break;
+      const uint32_t have = __ballot_sync(0xffffffffu, row != nullptr);
+      ctl->row[slot][32 * (h & 1) + lane] = row ? row : elsewhere;
+      if (h & 1) {
+        if (lane == 0) ctl->valid[t & 15] = uint64_t(have) << 32 | low;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->place_full[slot]);
+        if (ahead.end) break;
+      }
+      low = have;
+    }
+    if (ahead.end && (h & 1) != 0) break;  // no tile at all, or the last stored
   }
   if (err) atomicOr(&g_decode_error, err);
 }
@@ -381,33 +406,129 @@ __device__ __forceinline__ bool must_mend(const TreeCtl* ctl, const Item& it, in
   return (it.tile0 + tile + 1) * kTileKeys > it.keys.prefix || ctl->valid[g & 15] != ~0ull;
 }
 
-// 8-bit rows.  A warp copies four keys of this CTA into the K tile (codes,
-// rope) two tiles ahead, and makes value rows of those four and of four of the
-// peer's: the former's codes come back from the K tile, the latter's from
-// global memory through registers, a tile ahead.  16 lanes take a key's half
-// of the codes, 16 each; the eight chunks that a quarter of a warp stores
-// together lie in eight bank groups.
+// A warp's eight rows of q to their places in the Q operand (a row's 1,152
+// bytes as nine pieces of 128, one in each block), rows past the tile's as
+// zeros; each format then converts them in place.
+__device__ __forceinline__ void stage_queries(const TreeDecodeArgs& a, const Item& it, uint32_t q0, int C, int w,
+                                              int lane) {
+  const int64_t row0 = int64_t(it.keys.first) * a.H + it.skip + kCtaRows * C;
+  const int live = it.rows - kCtaRows * C;
+#pragma unroll 6
+  for (int k = 0; k < 8 * 72 / 32; ++k) {
+    const int e = 32 * k + lane;
+    const int r = 8 * w + e / 72, chunk = e % 72;  // 8 dims each
+    const uint32_t at = q0 + (chunk >> 3) * kQBlock + sw128_offset(r, chunk & 7);
+    if (r < live) cp_async_16(at, a.q + (row0 + r) * SMLA_QK_DIM + 8 * chunk);
+    else sts128(at, make_uint4(0, 0, 0, 0));
+  }
+  cp_async_wait_all();
+  __syncwarp();
+}
+
+// 8-bit rows.  The copying warp brings this CTA's keys (codes, rope) into the
+// K tiles, three tiles ahead, and both CTAs' scales.  A converter warp makes
+// value rows of four keys of this CTA, whose codes come from the K tile, and
+// of four of the peer's, whose half of the codes it loads a tile ahead.  16
+// lanes take a key's half of the codes, 16 each; the eight chunks that a
+// quarter of a warp stores together lie in eight bank groups.
 struct Fp8Keys {
   static constexpr bool kFp4 = false;
   static constexpr int kRowBytes = SMLA_ROW_BYTES;
   using Sm = Shared<false>;
 
-  // Rows of the request's list as the A operands of QK^T, eight a warp.
-  static __device__ void load_queries(const TreeDecodeArgs& a, const Item& it, uint32_t q0, float* row_scale, int C,
-                                      int w, int lane) {
-    const int64_t row0 = int64_t(it.keys.first) * a.H + it.skip + kCtaRows * C;
-    const int live = it.rows - kCtaRows * C;
-#pragma unroll 4
-    for (int i = 0; i < 8; ++i) {
-      const int r = 8 * w + i;
-      uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, rope = make_uint4(0, 0, 0, 0);
-      if (r < live) {
-        const uint16_t* q = a.q + (row0 + r) * SMLA_QK_DIM;
-        v[0] = ldg_stream(q + 16 * lane);
-        v[1] = ldg_stream(q + 16 * lane + 8);
-        if (lane < 8) rope = ldg_stream(q + SMLA_V_DIM + 8 * lane);
+  // 16 codes times their scale, rounded once.  Scales from 2^-10 on split into
+  // fp16 hi + lo as they are (lo is good to 2^-25, 2^-15 of the scale); any
+  // scale, as 2^8 times itself against codes times 2^-8.
+  static __device__ __forceinline__ void values(uint4 c, float scale, uint4* v) {
+    const __half h = __float2half_rn(scale);
+    const __half2 hi = __half2half2(h), lo = __half2half2(__float2half_rn(scale - __half2float(h)));
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __half2 a = __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[k]), __NV_E4M3));
+      const __half2 b = __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[k] >> 16), __NV_E4M3));
+      o[2 * k] = h2_bits(__hfma2(a, hi, __hmul2(a, lo)));
+      o[2 * k + 1] = h2_bits(__hfma2(b, hi, __hmul2(b, lo)));
+    }
+    v[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    v[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+  static __device__ __forceinline__ void any_values(uint4 c, float scale, bool mend, uint4* v) {
+    __half2 hi, lo;
+    split_scale(scale, hi, lo);
+    v[0] = e4m3x8_scaled(make_uint2(c.x, c.y), hi, lo);
+    v[1] = e4m3x8_scaled(make_uint2(c.z, c.w), hi, lo);
+    if (mend) {
+      v[0] = only_finite(v[0]);
+      v[1] = only_finite(v[1]);
+    }
+  }
+
+  // The copying warp.
+  static __device__ void copy_rows(uint8_t* sm, TreeCtl* ctl, int C, int lane) {
+    const uint32_t k0 = smem_u32(sm) + kQSize;
+    const uint32_t to = (lane >> 3) * kKBlock;
+    Cursor cur;
+    for (int t = 0;; ++t) {
+      const int before = cur.item;
+      cur.next_tile(ctl);
+      if (before >= 0 && cur.item != before) leave_item(ctl, before, lane);
+      if (cur.end) break;
+      const int slot = t % kPlaces, st = t % 3;
+      // the K tile is free once QK^T and the converters of the tile three
+      // before have read it
+      const bool ready =
+          tree_wait(&ctl->place_full[slot], (t / kPlaces) & 1, ctl, kWsRaw) &&
+          (t < 3 || (tree_wait(&ctl->k_free[st], (t / 3 - 1) & 1, ctl, kWsFreed) &&
+                     tree_wait(&ctl->k_read[st], (t / 3 - 1) & 1, ctl, kWsRawEmpty)));
+      if (!__all_sync(0xffffffffu, ready)) break;
+      const uint8_t* const* row = ctl->row[slot];
+      const uint32_t k_tile = k0 + st * Sm::kKSize;
+#pragma unroll 1
+      for (int i0 = 0; i0 < kCtaKeys; i0 += 8) {
+        const uint8_t* p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = row[kCtaKeys * C + i0 + i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          cp_async_16(k_tile + to + sw128_offset(i0 + i, lane & 7), p[i] + 16 * lane);
       }
-      const uint32_t x[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+      const uint32_t table = smem_u32(&ctl->scales[t & 3][lane & 3][lane >> 2]);
+#pragma unroll 1
+      for (int i0 = 0; i0 < 8; i0 += 4) {
+        const uint8_t *rope[4], *scale[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          rope[i] = row[kCtaKeys * C + 4 * (i0 + i) + (lane >> 3)];
+          scale[i] = row[8 * (i0 + i) + (lane >> 2)];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          cp_async_16(k_tile + 4 * kKBlock + sw128_offset(4 * (i0 + i) + (lane >> 3), lane & 7),
+                      rope[i] + 528 + 16 * (lane & 7));
+          cp_async_4(table + 32 * (i0 + i), scale[i] + 512 + 4 * (lane & 3));
+        }
+      }
+      cp_async_arrive(&ctl->k_full[st]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->place_empty[slot]);
+    }
+    cp_async_wait_all();
+  }
+
+  // Rows of the request's list as the A operands of QK^T, eight a warp.
+  static __device__ __forceinline__ void load_queries(const TreeDecodeArgs& a, const Item& it, uint32_t q0,
+                                                      float* row_scale, int C, int w, int lane) {
+    stage_queries(a, it, q0, C, w, lane);
+#pragma unroll 1
+    for (int r = 8 * w; r < 8 * w + 8; ++r) {
+      const uint32_t at = q0 + (lane >> 2) * kQBlock;  // dims 16 lane ..
+      const uint4 v0 = lds128(at + sw128_offset(r, 2 * (lane & 3)));
+      const uint4 v1 = lds128(at + sw128_offset(r, 2 * (lane & 3) + 1));
+      const uint32_t rope_at = q0 + 8 * kQBlock + sw128_offset(r, lane & 7);
+      const uint4 rope = lds128(rope_at);
+      const uint32_t x[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
       uint32_t top = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) top = max(top, max(x[k] & 0x7fffu, (x[k] >> 16) & 0x7fffu));
@@ -419,91 +540,68 @@ struct Fp8Keys {
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        uint32_t h = 0, l = 0;
+        hi[k] = lo[k] = 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint32_t w2 = x[2 * k + j];
           const float2 f = make_float2(__uint_as_float(w2 << 16) * by, __uint_as_float(w2 & 0xffff0000u) * by);
           const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
           const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
-          h |= uint32_t(c) << (16 * j);
-          l |= uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(f.x - b.x, f.y - b.y), __NV_SATFINITE, __NV_E4M3))
-               << (16 * j);
+          hi[k] |= uint32_t(c) << (16 * j);
+          lo[k] |= uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(f.x - b.x, f.y - b.y), __NV_SATFINITE, __NV_E4M3))
+                   << (16 * j);
         }
-        hi[k] = h;
-        lo[k] = l;
       }
-      const uint32_t at = q0 + (lane >> 3) * kQBlock + sw128_offset(r, lane & 7);
-      sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-      sts128(at + 4 * kQBlock, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-      if (lane < 8) {
-        const uint32_t z[4] = {rope.x, rope.y, rope.z, rope.w};
-        uint32_t o[4];
+      const uint32_t z[4] = {rope.x, rope.y, rope.z, rope.w};
+      uint32_t o[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __nv_bfloat162 p =
-              __floats2bfloat162_rn(__uint_as_float(z[k] << 16) * by, __uint_as_float(z[k] & 0xffff0000u) * by);
-          o[k] = *reinterpret_cast<const uint32_t*>(&p);
-        }
-        sts128(q0 + 8 * kQBlock + sw128_offset(r, lane), make_uint4(o[0], o[1], o[2], o[3]));
+      for (int k = 0; k < 4; ++k) {
+        const __nv_bfloat162 p =
+            __floats2bfloat162_rn(__uint_as_float(z[k] << 16) * by, __uint_as_float(z[k] & 0xffff0000u) * by);
+        o[k] = *reinterpret_cast<const uint32_t*>(&p);
       }
+      __syncwarp();  // every lane has read the row
+      const uint32_t to = q0 + (lane >> 3) * kQBlock + sw128_offset(r, lane & 7);
+      sts128(to, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      sts128(to + 4 * kQBlock, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      if (lane < 8) sts128(rope_at, make_uint4(o[0], o[1], o[2], o[3]));
       // a query that is not finite has no score that is
-      if (lane == 0) row_scale[r] = exponent == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(uint32_t(127 - up) << 23);
-      if (exponent == 255 && lane == 0) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
+      if (lane == 0) {
+        row_scale[r] = __uint_as_float(exponent == 255 ? 0x7fc00000u : uint32_t(127 - up) << 23);
+        if (exponent == 255) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
+      }
     }
   }
 
   static __device__ void run(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl, int C, int w, int lane) {
+    constexpr int kPer = kWarpKeys / 2;  // keys of a half warp
     const uint32_t base = smem_u32(sm);
     const uint32_t v_full = map_to_cta(smem_u32(&ctl->v_full[0]), 0), q_full = map_to_cta(smem_u32(&ctl->q_full), 0);
-    const int own_keys = kCtaKeys * C + kWarpKeys * w, peer_keys = kCtaKeys * (1 - C) + kWarpKeys * w;
-    const int j = lane & 15, pair = lane >> 4;  // 16 codes from 16 j on; of two keys
-    const uint32_t k0 = base + kQSize;
-    // this lane's places in a tile: where its copies go, where it reads codes
-    // of the tile's own half, where its value chunks go
-    const uint32_t to_k = (lane >> 3) * kKBlock;
-    const uint32_t rope_at = 4 * kKBlock + sw128_offset(kWarpKeys * w + (lane >> 3), lane & 7);
-    const uint32_t from_k = (2 * C + (j >> 3)) * kKBlock;
-    const int turn = (j >> 2) & 1;  // which chunk first
-    const int scale_key = (lane >> 2) < kWarpKeys ? own_keys + (lane >> 2) : peer_keys + (lane >> 2) - kWarpKeys;
+    const int first = kWarpKeys * w;
+    const int own_keys = kCtaKeys * C + first, peer_keys = kCtaKeys * (1 - C) + first;
+    const int j = lane & 15, key = lane >> 4;  // 16 codes from 16 j on; of keys key, key + 2, ...
+    const int swap = (j >> 2) & 1, group = 2 * C + (j >> 3);
+    const uint32_t from = base + kQSize + group * kKBlock;
+    const uint32_t to = base + Sm::kOffV + (j >> 2) * kVBlock;
     bool bad = false, ok = true;
-    // copies of tile t
-    auto copy = [&](int t) {
-      const int slot = t % kPlaces, st = t % 3;
-      // the K tile is free once QK^T of the tile three before is done
-      const bool ready = tree_wait(&ctl->place_full[slot], (t / kPlaces) & 1, ctl, kWsRaw) &&
-                         (t < 3 || tree_wait(&ctl->k_free[st], (t / 3 - 1) & 1, ctl, kWsFreed));
-      if (!__all_sync(0xffffffffu, ready)) return false;
-      const uint32_t k_tile = k0 + st * Sm::kKSize;
-#pragma unroll
-      for (int i = 0; i < kWarpKeys; ++i)
-        cp_async_16(k_tile + to_k + sw128_offset(kWarpKeys * w + i, lane & 7), ctl->row[slot][own_keys + i] + 16 * lane);
-      cp_async_16(k_tile + rope_at, ctl->row[slot][own_keys + (lane >> 3)] + 528 + 16 * (lane & 7));
-      cp_async_4(smem_u32(&ctl->scales[t & 3][lane & 3][scale_key]), ctl->row[slot][scale_key] + 512 + 4 * (lane & 3));
-      cp_async_arrive(&ctl->k_full[st]);
-      cp_async_commit();
-      return true;
-    };
-    // the peer's keys of tile t
-    uint4 peer[2];
+    uint4 peer[kPer];
     auto load_peer = [&](int t) {
       const int slot = t % kPlaces;
+      if (!__all_sync(0xffffffffu, tree_wait(&ctl->place_full[slot], (t / kPlaces) & 1, ctl, kWsRaw))) return false;
+      const uint8_t* p[kPer];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        peer[i] = ldg_stream(ctl->row[slot][peer_keys + 2 * i + pair] + 256 * C + 16 * j);
+      for (int i = 0; i < kPer; ++i) p[i] = ctl->row[slot][peer_keys + 2 * i + key];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) peer[i] = ldg_stream(p[i] + 256 * C + 16 * j);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->place_empty[slot]);
+      return true;
     };
-    // ahead: the tile copied next
     Cursor ahead, now;
-    int t = 0, g = 0;  // tiles copied, converted
-    for (int i = 0; i < 2 && ok; ++i) {
-      ahead.next_tile(ctl);
-      if (!ahead.end) ok = copy(t++);
-      else cp_async_commit();
-    }
-    if (ok && t > 0) load_peer(0);
-    while (ok) {
+    ahead.next_tile(ctl);
+    if (!ahead.end) ok = load_peer(0);
+    int st = 0, lap = 0;  // the K tile and its uses
+    for (int g = 0; ok; ++g) {
       // to the next tile; an item is handed back when it is left
       const int before = now.item;
       now.next_tile(ctl);
@@ -518,51 +616,80 @@ struct Fp8Keys {
         __syncwarp();
         if (lane == 0) mbar_arrive_at(q_full);
       }
-      // V is free once PV of the tile two before is done (and QK^T of the tile
-      // one before, which was issued earlier: copies two ahead need not wait)
-      if (g >= 2 && !__all_sync(0xffffffffu, tree_wait(&ctl->pv[g & 1], ((g >> 1) - 1) & 1, ctl, kWsPvDone))) break;
-      ahead.next_tile(ctl);
-      if (!ahead.end) ok = copy(t++);
-      else cp_async_commit();
-      if (!ok) break;
-      cp_async_wait<2>();  // this warp's copies of the tile
-      __syncwarp();
-      const uint32_t k_tile = k0 + (g % 3) * Sm::kKSize, v_tile = base + Sm::kOffV + (g & 1) * kVSize;
-      const float* table = &ctl->scales[g & 3][2 * C + (j >> 3)][0];
-      const bool mend = must_mend(ctl, it, now.tile, g);
-      uint4 x[8];
+      {
+        // V: free once PV of the tile two before is done
+        ok = tree_wait(&ctl->k_full[st], lap & 1, ctl, kWsRaw) &&
+             (g < 2 || tree_wait(&ctl->pv[g & 1], ((g >> 1) - 1) & 1, ctl, kWsPvDone));
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t k_tile = from + st * Sm::kKSize, v_tile = to + (g & 1) * kVSize;
+        const float* scales = ctl->scales[g & 3][group];
+        const bool mend = must_mend(ctl, it, now.tile, g);
+        uint4 own[kPer];
+        float s_own[kPer], s_peer[kPer];
+        float least = INFINITY, most = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int key = 2 * i + pair;
-        const uint4 own = lds128(k_tile + from_k + sw128_offset(kWarpKeys * w + key, j & 7));
-        const float s = table[own_keys + key], s_peer = ctl->scales[g & 3][2 * C + (j >> 3)][peer_keys + key];
-        __half2 hi, lo;
-        split_scale(s, hi, lo);
-        x[2 * i] = e4m3x8_scaled(turn ? make_uint2(own.z, own.w) : make_uint2(own.x, own.y), hi, lo);
-        x[2 * i + 1] = e4m3x8_scaled(turn ? make_uint2(own.x, own.y) : make_uint2(own.z, own.w), hi, lo);
-        bad |= scale_out_of_range(s) && ((ctl->valid[g & 15] >> (own_keys + key)) & 1);
-        split_scale(s_peer, hi, lo);
-        const uint4 p = peer[i];
-        x[4 + 2 * i] = e4m3x8_scaled(turn ? make_uint2(p.z, p.w) : make_uint2(p.x, p.y), hi, lo);
-        x[5 + 2 * i] = e4m3x8_scaled(turn ? make_uint2(p.x, p.y) : make_uint2(p.z, p.w), hi, lo);
-      }
-      if (mend) {
+        for (int i = 0; i < kPer; ++i) {
+          own[i] = lds128(k_tile + sw128_offset(first + 2 * i + key, j & 7));
+          s_own[i] = scales[own_keys + 2 * i + key];
+          s_peer[i] = scales[peer_keys + 2 * i + key];
+          // (a NaN is neither, but most of them is the largest's or one)
+          least = fminf(least, fminf(s_own[i], s_peer[i]));
+          most = s_own[i] <= most ? most : s_own[i];
+          most = s_peer[i] <= most ? most : s_peer[i];
+        }
+        // chunks in the order this lane stores them
+        auto turned = [&](uint4 c) { return swap ? make_uint4(c.z, c.w, c.x, c.y) : c; };
+        auto store = [&](int i, const uint4* x, const uint4* y) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = only_finite(x[i]);
-      }
-      const uint32_t block = v_tile + (j >> 2) * kVBlock;
+          for (int s = 0; s < 2; ++s) {
+            const uint32_t c = 2 * (j & 3) + (s ^ swap);
+            sts128(v_tile + sw128_offset(own_keys + 2 * i + key, c), x[s]);
+            sts128(v_tile + sw128_offset(peer_keys + 2 * i + key, c), y[s]);
+          }
+        };
+        if (__all_sync(0xffffffffu, least >= 0x1p-10f && most <= 65504.f / 448.f) && !mend) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int key = (i < 4 ? own_keys : peer_keys) + 2 * ((i >> 1) & 1) + pair;
-        sts128(block + sw128_offset(key, 2 * (j & 3) + ((i & 1) ^ turn)), x[i]);
+          for (int i = 0; i < kPer; ++i) {
+            uint4 x[2], y[2];
+            values(turned(own[i]), s_own[i], x);
+            values(turned(peer[i]), s_peer[i], y);
+            store(i, x, y);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < kPer; ++i) {
+            uint4 c = own[0], d = peer[0];
+            float s = s_own[0], s2 = s_peer[0];
+#pragma unroll
+            for (int k = 1; k < kPer; ++k) {
+              if (i == k) {
+                c = own[k];
+                d = peer[k];
+                s = s_own[k];
+                s2 = s_peer[k];
+              }
+            }
+            uint4 x[2], y[2];
+            any_values(turned(c), s, mend, x);
+            any_values(turned(d), s2, mend, y);
+            bad |= scale_out_of_range(s) && ((ctl->valid[g & 15] >> (own_keys + 2 * i + key)) & 1);
+            store(i, x, y);
+          }
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_at(v_full + 8 * (g & 1));
+          mbar_arrive(&ctl->k_read[st]);
+        }
+        ahead.next_tile(ctl);
+        if (!ahead.end) ok = load_peer(g + 1);
       }
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_at(v_full + 8 * (g & 1));
-      ++g;
-      if (g < t) load_peer(g);
+      if (++st == 3) {
+        st = 0;
+        ++lap;
+      }
     }
-    cp_async_wait_all();
     if (bad) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
   }
 };
@@ -574,19 +701,18 @@ struct Fp4Keys {
   static constexpr int kRowBytes = SMLA_FP4_ROW_BYTES;
   using Sm = Shared<true>;
 
-  static __device__ void load_queries(const TreeDecodeArgs& a, const Item& it, uint32_t q0, float*, int C, int w,
-                                      int lane) {
+  static __device__ __forceinline__ void load_queries(const TreeDecodeArgs& a, const Item& it, uint32_t q0, int C,
+                                                      int w, int lane) {
+    stage_queries(a, it, q0, C, w, lane);
     uint32_t over = 0;
-    const int64_t row0 = int64_t(it.keys.first) * a.H + it.skip + kCtaRows * C;
-    const int live = it.rows - kCtaRows * C;
-#pragma unroll 9
+#pragma unroll 2
     for (int k = 0; k < 8 * 72 / 32; ++k) {
       const int e = 32 * k + lane;
-      const int r = 8 * w + e / 72, chunk = e % 72;  // 8 dims each
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < live) v = ldg_stream(a.q + (row0 + r) * SMLA_QK_DIM + 8 * chunk);
+      const int r = 8 * w + e / 72, chunk = e % 72;
+      const uint32_t at = q0 + (chunk >> 3) * kQBlock + sw128_offset(r, chunk & 7);
+      const uint4 v = lds128(at);
       over |= bf16x8_over_fp16(v);
-      sts128(q0 + (chunk >> 3) * kQBlock + sw128_offset(r, chunk & 7), bf16x8_to_f16x8(v));
+      sts128(at, bf16x8_to_f16x8(v));
     }
     if (over) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
   }
@@ -614,32 +740,41 @@ struct Fp4Keys {
   };
 
   static __device__ void run(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl, int C, int w, int lane) {
+    constexpr int kPer = kWarpKeys / 4;  // keys of a quarter warp
     const uint32_t base = smem_u32(sm);
     const uint32_t k_full = map_to_cta(smem_u32(&ctl->k_full[0]), 0), v_full = map_to_cta(smem_u32(&ctl->v_full[0]), 0),
                    q_full = map_to_cta(smem_u32(&ctl->q_full), 0);
-    const int own_keys = kCtaKeys * C + kWarpKeys * w, peer_keys = kCtaKeys * (1 - C) + kWarpKeys * w;
+    const int first = kWarpKeys * w;
+    const int own_keys = kCtaKeys * C + first, peer_keys = kCtaKeys * (1 - C) + first;
     const int j = lane & 7, key = lane >> 3, rot = (lane >> 1) & 3;
     uint32_t over = 0;
-    bool bad = false;
-    Half own, other, peer;
-    uint4 rope;
+    bool bad = false, ok = true;
+    Half own[kPer], other[kPer], peer[kPer];
+    uint4 rope[kPer];
     auto load = [&](int t) {
       const int slot = t % kPlaces;
       if (!__all_sync(0xffffffffu, tree_wait(&ctl->place_full[slot], (t / kPlaces) & 1, ctl, kWsRaw))) return false;
-      const uint8_t* row = ctl->row[slot][own_keys + key];
-      own.load(row, C, lane);
-      other.load(row, 1 - C, lane);
-      rope = ldg_stream(row + 288 + 16 * j);
-      peer.load(ctl->row[slot][peer_keys + key], C, lane);
+      const uint8_t *p[kPer], *q[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        p[i] = ctl->row[slot][own_keys + 4 * i + key];
+        q[i] = ctl->row[slot][peer_keys + 4 * i + key];
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        own[i].load(p[i], C, lane);
+        other[i].load(p[i], 1 - C, lane);
+        rope[i] = ldg_stream(p[i] + 288 + 16 * j);
+        peer[i].load(q[i], C, lane);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->place_empty[slot]);
       return true;
     };
     Cursor ahead, now;
-    int g = 0;
     ahead.next_tile(ctl);
-    bool ok = ahead.end || load(0);
-    while (ok) {
+    if (!ahead.end) ok = load(0);
+    for (int g = 0; ok; ++g) {
       const int before = now.item;
       now.next_tile(ctl);
       if (before >= 0 && now.item != before) leave_item(ctl, before, lane);
@@ -649,55 +784,65 @@ struct Fp4Keys {
       if (now.tile == 0) {  // the item's rows, in place of the last one's
         if (g > 0 && !__all_sync(0xffffffffu, tree_wait(&ctl->k_free[(g - 1) & 1], ((g - 1) >> 1) & 1, ctl, kWsFreed)))
           break;
-        load_queries(a, it, base, nullptr, C, w, lane);
+        load_queries(a, it, base, C, w, lane);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive_at(q_full);
       }
       const uint64_t valid = ctl->valid[g & 15];
-      const bool live = (valid >> (own_keys + key)) & 1;
-      bad |= live && (own.nan() || other.nan());
-      if (live) over |= bf16x8_over_fp16(rope);
       // K: free once QK^T of the tile two before is done
       if (g >= 2 && !__all_sync(0xffffffffu, tree_wait(&ctl->k_free[st], ((g >> 1) - 1) & 1, ctl, kWsFreed))) break;
       const uint32_t k_tile = base + kQSize + st * Sm::kKSize;
-      uint4 x[4], y[4];
-      own.values(x, lane);
-      other.values(y, lane);
       const uint32_t k_block = k_tile + (j >> 1) * kKBlock;
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const uint32_t at = k_block + sw128_offset(kWarpKeys * w + key, 4 * (j & 1) + ((m + rot) & 3));
-        sts128(at + 4 * C * kKBlock, x[m]);
-        sts128(at + 4 * (1 - C) * kKBlock, y[m]);
+      for (int i = 0; i < kPer; ++i) {
+        const int row = first + 4 * i + key;
+        if ((valid >> (own_keys + 4 * i + key)) & 1) {
+          bad |= own[i].nan() || other[i].nan();
+          over |= bf16x8_over_fp16(rope[i]);
+        }
+        uint4 x[4], y[4];
+        own[i].values(x, lane);
+        other[i].values(y, lane);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const uint32_t at = k_block + sw128_offset(row, 4 * (j & 1) + ((m + rot) & 3));
+          sts128(at + 4 * C * kKBlock, x[m]);
+          sts128(at + 4 * (1 - C) * kKBlock, y[m]);
+        }
+        sts128(k_tile + 8 * kKBlock + sw128_offset(row, j), bf16x8_to_f16x8(rope[i]));
       }
-      sts128(k_tile + 8 * kKBlock + sw128_offset(kWarpKeys * w + key, j), bf16x8_to_f16x8(rope));
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive_at(k_full + 8 * st);
       // V: free once PV of the tile two before is done
       if (g >= 2 && !__all_sync(0xffffffffu, tree_wait(&ctl->pv[st], ((g >> 1) - 1) & 1, ctl, kWsPvDone))) break;
-      peer.values(y, lane);
-      if (must_mend(ctl, it, now.tile, g)) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          x[m] = only_finite(x[m]);
-          y[m] = only_finite(y[m]);
-        }
-      }
+      const bool mend = must_mend(ctl, it, now.tile, g);
       const uint32_t v_block = base + Sm::kOffV + st * kVSize + (j >> 1) * kVBlock;
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int c = 4 * (j & 1) + ((m + rot) & 3);
-        sts128(v_block + sw128_offset(own_keys + key, c), x[m]);
-        sts128(v_block + sw128_offset(peer_keys + key, c), y[m]);
+      for (int i = 0; i < kPer; ++i) {
+        uint4 x[4], y[4];
+        own[i].values(x, lane);
+        peer[i].values(y, lane);
+        if (mend) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            x[m] = only_finite(x[m]);
+            y[m] = only_finite(y[m]);
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const int c = 4 * (j & 1) + ((m + rot) & 3);
+          sts128(v_block + sw128_offset(own_keys + 4 * i + key, c), x[m]);
+          sts128(v_block + sw128_offset(peer_keys + 4 * i + key, c), y[m]);
+        }
       }
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive_at(v_full + 8 * st);
-      ++g;
       ahead.next_tile(ctl);
-      if (!ahead.end) ok = load(g);
+      if (!ahead.end) ok = load(g + 1);
     }
     if (bad || over) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
   }
@@ -721,61 +866,85 @@ __device__ void issue_mmas(uint8_t* sm, TreeCtl* ctl, uint32_t tb, int lane) {
   while (ok && cur.next_item(ctl)) {
     const int n = cur.tiles;
     leave_item(ctl, cur.item, lane);
-    for (int j = 0; j <= n; ++j) {
+    for (int j = 0; j < n + Sm::kProbs; ++j) {
       if (j < n) {
         const int t = g + j, st = t % kSt;
         ok = tree_wait(&ctl->k_full[st], (t / kSt) & 1, ctl, kWsFull);
         if (!F::kFp4) ok = ok && tree_wait(&ctl->k_peer[st], (t / kSt) & 1, ctl, kWsFull);
-        ok = ok && (j > 0 || tree_wait(&ctl->q_full, cur.item & 1, ctl, kWsQReady)) &&
-             (t == 0 || tree_wait(&ctl->s_read, (t - 1) & 1, ctl, kWsSFree));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          const uint64_t ad = sdesc_sw128(base, 16, 1024);
-          const uint64_t bd = sdesc_sw128(base + kQSize + st * Sm::kKSize, 16, 1024);
-          if constexpr (F::kFp4) {
+        ok = ok && (j > 0 || tree_wait(&ctl->q_full, cur.item & 1, ctl, kWsQReady));
+        const uint64_t ad = sdesc_sw128(base, 16, 1024);
+        const uint64_t bd = sdesc_sw128(base + kQSize + st * Sm::kKSize, 16, 1024);
+        if constexpr (F::kFp4) {
+          ok = ok && (t < 2 || tree_wait(&ctl->s_read[t & 1], ((t >> 1) - 1) & 1, ctl, kWsSFree));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll 1
+            for (int q = 0; q < 9; ++q)
 #pragma unroll
-            for (int k = 0; k < 36; ++k)
-              mma_ss_f16_pair(tbu + kScoreCol, ad + uint64_t((k >> 2) * (kQBlock >> 4) + 2 * (k & 3)),
-                              bd + uint64_t((k >> 2) * (kKBlock >> 4) + 2 * (k & 3)), qk_desc, k > 0);
-          } else {
-            fence_async_shared();  // the copies were generic writes
+              for (int k = 0; k < 4; ++k)
+                mma_ss_f16_pair(tbu + kScoreCol + 32 * (t & 1), ad + uint64_t(q * (kQBlock >> 4) + 2 * k),
+                                bd + uint64_t(q * (kKBlock >> 4) + 2 * k), qk_desc, q > 0 || k > 0);
+            mma_commit_pair(&ctl->qk[t & 1]);
+          }
+        } else {
+          // Groups of 128 codes, 32 an MMA, in two halves, so that the
+          // softmax reads the one while the other is made.
+          auto groups = [&](int q0) {
+#pragma unroll 1
+            for (int q = q0; q < q0 + 2; ++q) {
+              const uint64_t qd = ad + uint64_t(q * (kQBlock >> 4)), kd = bd + uint64_t(q * (kKBlock >> 4));
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {  // group k / 4: 128 codes, 32 an MMA
-              const uint64_t q = ad + uint64_t((k >> 2) * (kQBlock >> 4) + 2 * (k & 3));
-              const uint64_t b = bd + uint64_t((k >> 2) * (kKBlock >> 4) + 2 * (k & 3));
-              mma_ss_f8_pair(tbu + kScoreCol + 32 * (k >> 2), q, b, qk_desc, (k & 3) > 0);
-              mma_ss_f8_pair(tbu + kScoreCol + 32 * (k >> 2), q + 4 * (kQBlock >> 4), b, qk_desc, 1);
+              for (int k = 0; k < 4; ++k) {
+                mma_ss_f8_pair(tbu + kScoreCol + 32 * q, qd + 2 * k, kd + 2 * k, qk_desc, k > 0);
+                mma_ss_f8_pair(tbu + kScoreCol + 32 * q, qd + 4 * (kQBlock >> 4) + 2 * k, kd + 2 * k, qk_desc, 1);
+              }
             }
+          };
+          ok = ok && (t == 0 || tree_wait(&ctl->s_read[0], (t - 1) & 1, ctl, kWsSFree));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            fence_async_shared();  // the copies were generic writes
+            groups(0);
+            mma_commit_pair(&ctl->qk[0]);
+          }
+          __syncwarp();
+          ok = __all_sync(0xffffffffu, t == 0 || tree_wait(&ctl->s_read[1], (t - 1) & 1, ctl, kWsSFree));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            groups(2);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_ss_f16_pair(tbu + kScoreCol + 128, ad + uint64_t(8 * (kQBlock >> 4) + 2 * k),
                               bd + uint64_t(4 * (kKBlock >> 4) + 2 * k), rope_desc, k > 0);
+            mma_commit_pair(&ctl->qk[1]);
           }
-          mma_commit_pair(&ctl->qk[t & 1]);
-          mma_commit_pair(&ctl->k_free[st]);
         }
+        if (leader) mma_commit_pair(&ctl->k_free[st]);
         __syncwarp();
       }
-      if (j > 0) {
-        const int t = g + j - 1;
+      if (j >= Sm::kProbs) {
+        const int t = g + j - Sm::kProbs, pb = t % Sm::kProbs;
         ok = tree_wait(&ctl->v_full[t & 1], (t >> 1) & 1, ctl, kWsFull) &&
-             tree_wait(&ctl->p_full, t & 1, ctl, kWsPFull) &&
-             (j > 1 || cur.item == 0 || tree_wait(&ctl->out_read, (cur.item - 1) & 1, ctl, kWsSFree));
+             tree_wait(&ctl->p_full[pb], (t / Sm::kProbs) & 1, ctl, kWsPFull) &&
+             (j > Sm::kProbs || cur.item == 0 || tree_wait(&ctl->out_read, (cur.item - 1) & 1, ctl, kWsSFree));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-          const uint64_t ad = sdesc_sw128(base + Sm::kOffP, 16, 1024);
+          const uint64_t ad = sdesc_sw128(base + Sm::kOffP + pb * Sm::kPSize, 16, 1024);
           const uint32_t v = base + Sm::kOffV + (t & 1) * kVSize;
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < kTileKeys / 16; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               mma_ss_f16_pair(tbu + kOutCol + 128 * i, ad + 2 * k,
                               sdesc_sw128(v + 2 * i * kVBlock, kVBlock, 1024) + uint64_t(k * (2048 >> 4)), pv_desc,
-                              j > 1 || k > 0);
+                              j > Sm::kProbs || k > 0);
           mma_commit_pair(&ctl->pv[t & 1]);
         }
         __syncwarp();
@@ -827,7 +996,7 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
   const int r = tid & 63, half = (tid >> 6) & 1, part = tid >> 7;
   const uint32_t lanes = tmem_addr(tb, 32 * (warp & 3), 0);
   const uint32_t p_row = smem_u32(sm) + Shared<F::kFp4>::kOffP;
-  const uint32_t s_read = map_to_cta(smem_u32(&ctl->s_read), 0), p_full = map_to_cta(smem_u32(&ctl->p_full), 0),
+  const uint32_t s_read = map_to_cta(smem_u32(&ctl->s_read[0]), 0), p_full = map_to_cta(smem_u32(&ctl->p_full[0]), 0),
                  out_read = map_to_cta(smem_u32(&ctl->out_read), 0);
   Cursor cur;
   int g = 0;
@@ -844,50 +1013,64 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
     float c2 = a.sm_scale * kLog2e;
     for (int j = 0; j < n; ++j, ++g) {
       const int b = g & 1;
-      ok = __all_sync(0xffffffffu, tree_wait(&ctl->qk[b], (g >> 1) & 1, ctl, kWsSFull));
-      if (!ok) break;
-      tc_fence_after();
       const uint32_t scores = lanes + kScoreCol + 16 * part;
       uint32_t s[16];
-      tmem_ld16(scores + (F::kFp4 ? 0 : 128), s);
-      if constexpr (!F::kFp4) {
-        if (j == 0) c2 *= ctl->row_scale[cur.item & 1][r];
-        uint32_t x[2][16];
+      if constexpr (F::kFp4) {
+        ok = __all_sync(0xffffffffu, tree_wait(&ctl->qk[b], (g >> 1) & 1, ctl, kWsSFull));
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld16(scores + 32 * b, s);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(s_read + 8 * b);
+      } else {
+        // sum = scores of groups 0, 1 by their scales, then of 2, 3 and the rope
         uint64_t sum[8];
+        auto add = [&](const uint32_t* x, int q, bool set) {
+          const float4* sc = reinterpret_cast<const float4*>(&ctl->scales[g & 3][q][kCtaKeys * half + 16 * part]);
 #pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-          tmem_ld16(scores + 32 * q, x[0]);
-          tmem_ld16(scores + 32 * (q + 1), x[1]);
-          tmem_ld_wait();
-          if (q == 0) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum[k] = pack2(s[2 * k], s[2 * k + 1]);
+          for (int k = 0; k < 4; ++k) {
+            const float4 f = sc[k];
+            sum[2 * k] = fma2(pack2(x[4 * k], x[4 * k + 1]), pack2(f.x, f.y), set ? 0 : sum[2 * k]);
+            sum[2 * k + 1] = fma2(pack2(x[4 * k + 2], x[4 * k + 3]), pack2(f.z, f.w), set ? 0 : sum[2 * k + 1]);
           }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float4* sc = reinterpret_cast<const float4*>(&ctl->scales[g & 3][q + i][kCtaKeys * half + 16 * part]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float4 f = sc[k];
-              sum[2 * k] = fma2(pack2(x[i][4 * k], x[i][4 * k + 1]), pack2(f.x, f.y), sum[2 * k]);
-              sum[2 * k + 1] = fma2(pack2(x[i][4 * k + 2], x[i][4 * k + 3]), pack2(f.z, f.w), sum[2 * k + 1]);
-            }
-          }
-        }
+        };
+        uint32_t x[2][16];
+        ok = __all_sync(0xffffffffu, tree_wait(&ctl->qk[0], g & 1, ctl, kWsSFull));
+        if (!ok) break;
+        if (j == 0) c2 *= ctl->row_scale[cur.item & 1][r];
+        tc_fence_after();
+        tmem_ld16(scores, x[0]);
+        tmem_ld16(scores + 32, x[1]);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(s_read);
+        add(x[0], 0, true);
+        add(x[1], 1, false);
+        ok = __all_sync(0xffffffffu, tree_wait(&ctl->qk[1], g & 1, ctl, kWsSFull));
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld16(scores + 64, x[0]);
+        tmem_ld16(scores + 96, x[1]);
+        tmem_ld16(scores + 128, s);
+        tmem_ld_wait();
+        tc_fence_before();
+        add(x[0], 2, false);
+        add(x[1], 3, false);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(s_read + 8);  // the scales have been read, too
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float2 f = unpack2(sum[k]);
-          s[2 * k] = __float_as_uint(f.x);
-          s[2 * k + 1] = __float_as_uint(f.y);
+          s[2 * k] = __float_as_uint(f.x + __uint_as_float(s[2 * k]));
+          s[2 * k + 1] = __float_as_uint(f.y + __uint_as_float(s[2 * k + 1]));
         }
       }
       const int first = (it.tile0 + j) * kTileKeys + kCtaKeys * half + 16 * part;  // key of s[0]
       uint32_t see = uint32_t(ctl->valid[g & 15] >> (kCtaKeys * half + 16 * part)) & 0xffffu;
       if (first + 16 > it.keys.prefix) see &= seen_from(mask, a.mask_words, first - it.keys.prefix);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_at(s_read);
       if (see != 0xffffu) {
 #pragma unroll
         for (int k = 0; k < 16; ++k)
@@ -919,32 +1102,36 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
         p[k] = h2_bits(__floats2half2_rn(x, y));
       }
       l = l * alpha + sum;
-      if (j > 0) {
-        // PV of the tile before has read its P and stored its output
+      // the output moves once PV of the tile before has been added to it; P's
+      // place is free once PV of its last tile has read it
+      const bool any = j > 0 && __any_sync(0xffffffffu, moves);
+      if (any || (F::kFp4 && j > 0))
         ok = __all_sync(0xffffffffu, tree_wait(&ctl->pv[b ^ 1], ((g - 1) >> 1) & 1, ctl, kWsPvDone));
-        if (!ok) break;
+      if (!F::kFp4 && ok && g >= 2)
+        ok = __all_sync(0xffffffffu, tree_wait(&ctl->pv[b], ((g >> 1) - 1) & 1, ctl, kWsPvDone));
+      if (!ok) break;
+      if (any) {
         tc_fence_after();
-        if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll 1
-          for (int cc = 4 * part; cc < 4 * part + 4; ++cc) {
-            uint32_t o[32];
-            tmem_ld32(lanes + kOutCol + 32 * cc, o);
-            tmem_ld_wait();
+        for (int cc = 4 * part; cc < 4 * part + 4; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(lanes + kOutCol + 32 * cc, o);
+          tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tmem_st32(lanes + kOutCol + 32 * cc, o);
-          }
-          tmem_st_wait();
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+          tmem_st32(lanes + kOutCol + 32 * cc, o);
         }
+        tmem_st_wait();
       }
+      const int pb = F::kFp4 ? 0 : b;
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        sts128(p_row + sw128_offset(r, 4 * half + 2 * part + q),
+        sts128(p_row + pb * Shared<F::kFp4>::kPSize + sw128_offset(r, 4 * half + 2 * part + q),
                make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]));
       fence_async_shared();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_at(p_full);
+      if (lane == 0) mbar_arrive_at(p_full + 8 * pb);
     }
     if (!ok) break;
     ctl->sums[tid] = l;
@@ -1015,24 +1202,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
       mbar_init(&ctl->pv[i], 1);
       mbar_init(&ctl->v_full[i], 2 * kConvWarps);  // both CTAs'
       mbar_init(&ctl->top[i], kSoftWarps);
+      mbar_init(&ctl->s_read[i], 2 * kSoftWarps);
+      mbar_init(&ctl->p_full[i], 2 * kSoftWarps);
     }
     for (int i = 0; i < 3; ++i) {
       mbar_init(&ctl->k_free[i], 1);
-      mbar_init(&ctl->k_full[i], F::kFp4 ? 2 * kConvWarps : 32 * kConvWarps);  // fp8: this CTA's copying threads
+      mbar_init(&ctl->k_full[i], F::kFp4 ? 2 * kConvWarps : 32);  // fp8: the copying warp's threads
+      mbar_init(&ctl->k_read[i], kConvWarps);
       mbar_init(&ctl->k_peer[i], 1);
     }
     for (int i = 0; i < kPlaces; ++i) {
       mbar_init(&ctl->place_full[i], 1);
-      mbar_init(&ctl->place_empty[i], kConvWarps);
+      mbar_init(&ctl->place_empty[i], kConvWarps + !F::kFp4);  // and the copying warp
     }
     mbar_init(&ctl->q_full, 2 * kConvWarps);
-    mbar_init(&ctl->s_read, 2 * kSoftWarps);
-    mbar_init(&ctl->p_full, 2 * kSoftWarps);
     mbar_init(&ctl->out_read, 2 * kSoftWarps);
     mbar_init(&ctl->sum, kSoftWarps);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&ctl->item_full[i], 1);
-      mbar_init(&ctl->item_empty[i], kSoftWarps + kConvWarps + 2);  // all but the list's own
+      mbar_init(&ctl->item_empty[i], kSoftWarps + kConvWarps + 2 + !F::kFp4);  // all but the list's own
     }
     mbar_init(&ctl->end, 1);
     ctl->abort = 0;
@@ -1102,21 +1290,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
     softmax_rows<F>(a, sm, ctl, tb, C, tid);
   } else if (warp < kIssueWarp) {
     F::run(a, sm, ctl, C, warp - kSoftWarps, lane);
-  } else if (warp == kIssueWarp) {
-    if (C == 0) issue_mmas<F>(sm, ctl, tb, lane);
-    else tell_peer<F>(ctl, lane);
-    // also after a wait that gave up: the pair's MMAs have completed
-    int no_abort = 0;
-    wait_phase<false>(&ctl->end, 0, &no_abort, kWsDrain);
-  } else if (warp == kIssueWarp + 1) {
-    list_work(a, ctl, C, units, per_pair, lane);
   } else {
-    look_up_rows(a, ctl, F::kRowBytes, lane);
+    if (warp == kIssueWarp) {
+      if (C == 0) issue_mmas<F>(sm, ctl, tb, lane);
+      else tell_peer<F>(ctl, lane);
+      // also after a wait that gave up: the pair's MMAs have completed
+      for (int n = kLooks; n > 0 && !mbar_try_wait(&ctl->end, 0); --n) {
+      }
+    } else if (warp == kIssueWarp + 1) {
+      list_work(a, ctl, C, units, per_pair, lane);
+    } else if (warp == kIssueWarp + 2) {
+      look_up_rows(a, ctl, F::kRowBytes, lane);
+    } else if constexpr (!F::kFp4) {
+      F::copy_rows(sm, ctl, C, lane);
+    }
   }
   tc_fence_before();
   __syncwarp();
   cluster_sync();  // neither CTA reaches into the other any more
   tc_fence_after();
+  if (tid == 0 && ctl->abort) atomicOr(&g_decode_error, SMLA_DEVERR_TIMEOUT | (1u << (7 + ctl->abort)));
   if (warp == kIssueWarp) tmem_dealloc_pair(tb, 512);
   __syncwarp();
   cluster_sync();
