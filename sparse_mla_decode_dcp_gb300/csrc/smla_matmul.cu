@@ -11,10 +11,11 @@
 // swizzle, several groups ahead.
 //
 // One operand's rows are the MMA's 128 lanes, the other's its columns.  Many
-// activation rows lie along the lanes (kSwap false, tiles of 128 x 128); up to
-// 64 of them along the columns, where a tile of 16, 32 or 64 wastes little,
-// and the weights' rows along the lanes: such a call is bound by the weights'
-// bytes.  A weight tile of 128 rows has one scale a group either way.
+// activation rows lie along the lanes (kSwap false, tiles of 128 x 128, and with
+// enough of them the pairs' 256 x 256 below); up to 64 of them along the
+// columns, where a tile of 16, 32 or 64 wastes little, and the weights' rows
+// along the lanes: such a call is bound by the weights' bytes.  A weight tile of
+// 128 rows has one scale a group either way.
 //
 // With few tiles the groups are split over the CTAs of a cluster, whose sums
 // meet through distributed shared memory in the order of their groups.
@@ -138,18 +139,21 @@ __global__ void __launch_bounds__(Shape<kSwap, kCols>::kThreads, kSwap ? 2 : 1)
   const int lane = tid & 31;
   volatile int* abort = &ctl.abort;
 
-  // this CTA's tile and its share of the groups
+  // this CTA's tiles and its share of their groups; split tiles are one a CTA
   const uint32_t split = blockIdx.x % uint32_t(a.splits);
-  const uint32_t tile = blockIdx.x / uint32_t(a.splits);
-  const uint32_t per_batch = uint32_t(a.m_tiles) * uint32_t(a.n_tiles);
-  const uint32_t g = tile / per_batch;
-  const uint32_t in_batch = tile - g * per_batch;
-  const int32_t n_tile = int32_t(in_batch / uint32_t(a.m_tiles));
-  const int32_t m_tile = int32_t(in_batch - uint32_t(n_tile) * uint32_t(a.m_tiles));
-  const int32_t m0 = m_tile * (kSwap ? kCols : kLaneRows);
-  const int32_t n0 = n_tile * 128;
+  const uint32_t tile0 = blockIdx.x / uint32_t(a.splits), step = gridDim.x / uint32_t(a.splits);
   const int kb0 = int(int64_t(a.k_blocks) * split / a.splits);
   const int kbs = int(int64_t(a.k_blocks) * (split + 1) / a.splits) - kb0;
+  struct Place {
+    int32_t g, n_tile, m0;
+  };
+  auto place = [&](uint32_t tile) {
+    const uint32_t per_batch = uint32_t(a.m_tiles) * uint32_t(a.n_tiles);
+    const uint32_t g = tile / per_batch, in_batch = tile - g * per_batch;
+    const uint32_t n_tile = in_batch / uint32_t(a.m_tiles);
+    return Place{int32_t(g), int32_t(n_tile),
+                 int32_t(in_batch - n_tile * uint32_t(a.m_tiles)) * (kSwap ? kCols : kLaneRows)};
+  };
 
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&a.a_map);
@@ -184,56 +188,67 @@ __global__ void __launch_bounds__(Shape<kSwap, kCols>::kThreads, kSwap ? 2 : 1)
       const uint32_t sm0 = smem_u32(sm);
       int s = 0;
       uint32_t lap = 0;  // of the stages
-      int i = 0;
-      for (; i < kbs; ++i) {
-        if (lap > 0 && !wait_bounded(&ctl.empty[s], (lap - 1) & 1, abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT))
-          break;
-        const uint32_t at = sm0 + s * S::kStageBytes;
-        mbar_arrive_expect_tx(&ctl.full[s], S::kStageBytes);
-        const int32_t x = (kb0 + i) * kGroup;
-        tma_load_3d(at, kSwap ? &a.b_map : &a.a_map, x, kSwap ? n0 : m0, int32_t(g), &ctl.full[s]);
-        tma_load_3d(at + kLaneRows * kGroup, kSwap ? &a.a_map : &a.b_map, x, kSwap ? m0 : n0, int32_t(g),
-                    &ctl.full[s]);
-        if (++s == a.stages) {
-          s = 0;
-          ++lap;
+      bool ok = true;
+      for (uint32_t tile = tile0; ok && tile < a.tiles; tile += step) {
+        const Place p = place(tile);
+        const int32_t l_row = kSwap ? p.n_tile * 128 : p.m0, c_row = kSwap ? p.m0 : p.n_tile * 128;
+        for (int i = 0; i < kbs; ++i) {
+          if (lap > 0 && !wait_bounded(&ctl.empty[s], (lap - 1) & 1, abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT)) {
+            ok = false;
+            break;
+          }
+          const uint32_t at = sm0 + s * S::kStageBytes;
+          mbar_arrive_expect_tx(&ctl.full[s], S::kStageBytes);
+          const int32_t x = (kb0 + i) * kGroup;
+          tma_load_3d(at, kSwap ? &a.b_map : &a.a_map, x, l_row, p.g, &ctl.full[s]);
+          tma_load_3d(at + kLaneRows * kGroup, kSwap ? &a.a_map : &a.b_map, x, c_row, p.g, &ctl.full[s]);
+          if (++s == a.stages) {
+            s = 0;
+            ++lap;
+          }
         }
       }
       // the CTA leaves when its loads have landed, whatever became of the rest
       int no_abort = 0;
-      for (int j = max(0, i - a.stages); j < i; ++j)
-        wait_bounded(&ctl.full[j % a.stages], (j / a.stages) & 1, &no_abort, &g_matmul_error,
-                     SMLA_DEVERR_TIMEOUT);
+      for (int j = 0; j < a.stages; ++j) {
+        const uint32_t used = lap + (j < s);  // loads of stage j
+        if (used > 0)
+          wait_bounded(&ctl.full[j], (used - 1) & 1, &no_abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
     constexpr uint32_t idesc = idesc_f16_f32(128, kCols, false, false);
     const bool leader = elect_one();
-    int issued = 0;
+    uint32_t issued = 0;
     int s = 0;
     uint32_t lap = 0;
-    for (int i = 0; i < kbs; ++i) {
-      const int b = i & 1;
-      bool go = wait_bounded(&ctl.full[s], lap & 1, abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT);
-      if (go && i >= 2)
-        go = wait_bounded(&ctl.sum_empty[b], ((i >> 1) - 1) & 1, abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT);
-      if (!__all_sync(0xffffffffu, go)) break;
-      tc_fence_after();
-      if (leader) {
-        const uint32_t at = smem_u32(sm) + s * S::kStageBytes;
-        const uint64_t ad = sdesc_sw128(at, 16, 1024);
-        const uint64_t bd = sdesc_sw128(at + kLaneRows * kGroup, 16, 1024);
+    bool ok = true;
+    for (uint32_t tile = tile0; ok && tile < a.tiles; tile += step) {
+      for (int i = 0; i < kbs; ++i) {
+        const int b = issued & 1;
+        bool go = wait_bounded(&ctl.full[s], lap & 1, abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT);
+        if (go && issued >= 2)
+          go = wait_bounded(&ctl.sum_empty[b], ((issued >> 1) - 1) & 1, abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT);
+        ok = __all_sync(0xffffffffu, go);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t at = smem_u32(sm) + s * S::kStageBytes;
+          const uint64_t ad = sdesc_sw128(at, 16, 1024);
+          const uint64_t bd = sdesc_sw128(at + kLaneRows * kGroup, 16, 1024);
 #pragma unroll
-        for (int k = 0; k < kGroup / 32; ++k)
-          mma_ss_f8(tb + b * kCols, ad + 2 * k, bd + 2 * k, idesc, k > 0);
-        mma_commit(&ctl.empty[s]);
-        mma_commit(&ctl.sum_full[b]);
-      }
-      __syncwarp();
-      ++issued;
-      if (++s == a.stages) {
-        s = 0;
-        ++lap;
+          for (int k = 0; k < kGroup / 32; ++k)
+            mma_ss_f8(tb + b * kCols, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+          mma_commit(&ctl.empty[s]);
+          mma_commit(&ctl.sum_full[b]);
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == a.stages) {
+          s = 0;
+          ++lap;
+        }
       }
     }
     // every MMA has completed before tensor memory is given back
@@ -249,88 +264,94 @@ __global__ void __launch_bounds__(Shape<kSwap, kCols>::kThreads, kSwap ? 2 : 1)
     const int half = (warp - 4) >> 2;  // which columns, with eight warps
     const int row = 32 * quad + lane;
     uint64_t sum[S::kPerThread / 2];
-#pragma unroll
-    for (int j = 0; j < S::kPerThread / 2; ++j) sum[j] = 0;
-    // a chunk's scales sa sb are fetched into registers while the chunk before
-    // it is summed
+    // A chunk's scales sa sb are fetched into registers while the chunk before
+    // it (of the tile before, at a tile's begin) is summed.
     constexpr int kSumThreads = 32 * S::kSumWarps;
     constexpr int kFetch = (kScaleChunk * S::kScaled + kSumThreads - 1) / kSumThreads;
     float next[kFetch];
-    auto fetch = [&](int i0) {
+    auto fetch = [&](const Place& p, int i0) {
 #pragma unroll
       for (int f = 0; f < kFetch; ++f) {
         const int e = t + kSumThreads * f;
         const int k = i0 + e / S::kScaled;
-        const int m = m0 + e % S::kScaled;
+        const int m = p.m0 + e % S::kScaled;
         next[f] = 0.f;
         if (e < kScaleChunk * S::kScaled && k < kbs && m < a.M)
-          next[f] = a.a_scales[int64_t(g) * a.ass.batch + int64_t(m) * a.ass.rows + (kb0 + k) * a.ass.cols] *
-                    a.b_scales[int64_t(g) * a.bss.batch + n_tile * a.bss.rows + (kb0 + k) * a.bss.cols];
+          next[f] = a.a_scales[p.g * a.ass.batch + m * a.ass.rows + (kb0 + k) * a.ass.cols] *
+                    a.b_scales[p.g * a.bss.batch + p.n_tile * a.bss.rows + (kb0 + k) * a.bss.cols];
       }
     };
-    fetch(0);
-    for (int i = 0; i < kbs; ++i) {
-      const int chunk = i / kScaleChunk;
-      if (i % kScaleChunk == 0) {
-        // the buffer's last readers are two chunks back, before the barrier of
-        // the chunk between
+    if (tile0 < a.tiles) fetch(place(tile0), 0);
+    uint32_t done = 0, chunks = 0;  // groups, and chunks of scales, so far
+    for (uint32_t tile = tile0; tile < a.tiles; tile += step) {
+      const Place p = place(tile);
 #pragma unroll
-        for (int f = 0; f < kFetch; ++f) {
-          const int e = t + kSumThreads * f;
-          if (e < kScaleChunk * S::kScaled) (&scales[chunk & 1][0][0])[e] = next[f];
-        }
-        named_bar_sync(1, kSumThreads);
-        fetch(i + kScaleChunk);
-      }
-      const int b = i & 1;
-      ok = __all_sync(0xffffffffu, wait_bounded(&ctl.sum_full[b], (i >> 1) & 1, abort, &g_matmul_error,
-                                                SMLA_DEVERR_TIMEOUT));
-      // a warp that gives up goes on to the barriers with what it has
-      if (ok) {
-        tc_fence_after();
-        const uint32_t at = tmem_addr(tb, 32 * quad, b * kCols + half * S::kPerThread);
-        const float* sc = scales[chunk & 1][i % kScaleChunk];
-        constexpr int kStep = S::kPerThread < 32 ? S::kPerThread : 32;
+      for (int j = 0; j < S::kPerThread / 2; ++j) sum[j] = 0;
+      for (int i = 0; i < kbs; ++i, ++done) {
+        if (i % kScaleChunk == 0) {
+          // the buffer's last readers are two chunks back, before the barrier of
+          // the chunk between
+          float* buffer = &scales[chunks & 1][0][0];
 #pragma unroll
-        for (int c = 0; c < S::kPerThread; c += kStep) {
-          uint32_t r[kStep];
-          load_sums<kStep>(at + c, r);
-          tmem_ld_wait();
-          if (c + kStep == S::kPerThread) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.sum_empty[b]);
+          for (int f = 0; f < kFetch; ++f) {
+            const int e = t + kSumThreads * f;
+            if (e < kScaleChunk * S::kScaled) buffer[e] = next[f];
           }
+          named_bar_sync(1, kSumThreads);
+          ++chunks;
+          if (i + kScaleChunk < kbs) fetch(p, i + kScaleChunk);
+          else if (tile + step < a.tiles) fetch(place(tile + step), 0);
+        }
+        const int b = done & 1;
+        ok = __all_sync(0xffffffffu, wait_bounded(&ctl.sum_full[b], (done >> 1) & 1, abort, &g_matmul_error,
+                                                  SMLA_DEVERR_TIMEOUT));
+        // a warp that gives up goes on to the barriers with what it has
+        if (ok) {
+          tc_fence_after();
+          const uint32_t at = tmem_addr(tb, 32 * quad, b * kCols + half * S::kPerThread);
+          const float* sc = scales[(chunks - 1) & 1][i % kScaleChunk];
+          constexpr int kStep = S::kPerThread < 32 ? S::kPerThread : 32;
 #pragma unroll
-          for (int j = 0; j < kStep / 2; ++j) {
-            uint64_t s2;
-            if constexpr (kSwap) {
-              const float2 f = *reinterpret_cast<const float2*>(sc + c + 2 * j);
-              s2 = pack2(f.x, f.y);
-            } else {
-              s2 = pack2(sc[row], sc[row]);
+          for (int c = 0; c < S::kPerThread; c += kStep) {
+            uint32_t r[kStep];
+            load_sums<kStep>(at + c, r);
+            tmem_ld_wait();
+            if (c + kStep == S::kPerThread) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&ctl.sum_empty[b]);
             }
-            sum[c / 2 + j] = fma2(pack2(r[2 * j], r[2 * j + 1]), s2, sum[c / 2 + j]);
+#pragma unroll
+            for (int j = 0; j < kStep / 2; ++j) {
+              uint64_t s2;
+              if constexpr (kSwap) {
+                const float2 f = *reinterpret_cast<const float2*>(sc + c + 2 * j);
+                s2 = pack2(f.x, f.y);
+              } else {
+                s2 = pack2(sc[row], sc[row]);
+              }
+              sum[c / 2 + j] = fma2(pack2(r[2 * j], r[2 * j + 1]), s2, sum[c / 2 + j]);
+            }
           }
         }
       }
-    }
 #pragma unroll
-    for (int j = 0; j < S::kPerThread / 2; ++j) {
-      const float2 f = unpack2(sum[j]);
-      acc[2 * j] = f.x;
-      acc[2 * j + 1] = f.y;
-    }
-    if (a.splits == 1) {
-      if constexpr (kSwap) {
-        const int32_t n = n0 + row;
-        if (n < a.N) {
+      for (int j = 0; j < S::kPerThread / 2; ++j) {
+        const float2 f = unpack2(sum[j]);
+        acc[2 * j] = f.x;
+        acc[2 * j + 1] = f.y;
+      }
+      if (a.splits == 1) {
+        if constexpr (kSwap) {
+          const int32_t n = p.n_tile * 128 + row;
+          if (n < a.N) {
 #pragma unroll
-          for (int j = 0; j < kCols; ++j)
-            if (m0 + j < a.M) store_row<1>(a, g, m0 + j, n, acc + j);
+            for (int j = 0; j < kCols; ++j)
+              if (p.m0 + j < a.M) store_row<1>(a, p.g, p.m0 + j, n, acc + j);
+          }
+        } else if (p.m0 + row < a.M) {
+          store_row<S::kPerThread>(a, p.g, p.m0 + row, p.n_tile * 128 + half * S::kPerThread, acc);
         }
-      } else if (m0 + row < a.M) {
-        store_row<S::kPerThread>(a, g, m0 + row, n0 + half * S::kPerThread, acc);
       }
     }
   }
@@ -338,6 +359,7 @@ __global__ void __launch_bounds__(Shape<kSwap, kCols>::kThreads, kSwap ? 2 : 1)
   __syncthreads();
   if (warp == 2) tmem_dealloc(tb, S::kTmemCols);
   if (a.splits == 1) return;
+  const Place p = place(tile0);
 
   // the cluster's sums, through the operand stages (every load of theirs has
   // been consumed)
@@ -371,9 +393,248 @@ __global__ void __launch_bounds__(Shape<kSwap, kCols>::kThreads, kSwap ? 2 : 1)
       v[2] += p.z;
       v[3] += p.w;
     }
-    if (m0 + i < a.M && n0 + c < a.N) store_row<4>(a, g, m0 + i, n0 + c, v);
+    if (p.m0 + i < a.M && p.n_tile * 128 + c < a.N) store_row<4>(a, p.g, p.m0 + i, p.n_tile * 128 + c, v);
   }
   cluster_sync();  // nobody's sums go while they are read
+}
+
+// Many rows: a CTA pair (cta_group::2) makes 256 x 256 results a tile, each CTA
+// 128 of the activation rows, in 256 columns of its tensor memory; each holds
+// half of both operands (the pair's MMAs read the other's half of the
+// weights), so a byte of shared memory serves twice the products of a 128 x 128
+// tile.  Two accumulators fill tensor memory: while one's group is summed into
+// registers (eight warps, 128 columns a thread), the next group's MMAs fill the
+// other.  Pairs take tiles in turn, rows first.
+struct PairCtl {
+  uint64_t full[kMaxStages], peer_full[kMaxStages], empty[kMaxStages], sum_full[2], sum_empty[2], end;
+  uint32_t tbase;
+  int abort;
+};
+constexpr int kPairThreads = 384;
+constexpr int kPairStageBytes = 2 * 128 * kGroup;
+constexpr int kPairStages = 6;
+constexpr int kPairSmem = kPairStages * kPairStageBytes + 1024;
+constexpr int kPairChunk = 8;  // groups whose scales are fetched together
+// registers a thread: launched with 168, then shared out by groups of four warps
+constexpr int kPairSumRegs = 224, kPairOtherRegs = 56;
+static_assert(8 * kPairSumRegs + 4 * kPairOtherRegs <= 12 * 168, "no more than the launch has");
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    fp8_matmul_pair_kernel(const __grid_constant__ MatmulArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ PairCtl ctl;
+  __shared__ float sa[2][kPairChunk][128], sb[2][kPairChunk][2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = int(cluster_ctarank());
+  volatile int* abort = &ctl.abort;
+  const int kbs = a.k_blocks;
+  const uint32_t tile0 = blockIdx.x >> 1, step = gridDim.x >> 1;
+  struct Place {
+    int32_t g, n_tile, m0;  // n_tile: of 256; m0: this CTA's first row
+  };
+  auto place = [&](uint32_t tile) {
+    const uint32_t per_batch = uint32_t(a.m_tiles) * uint32_t(a.n_tiles);
+    const uint32_t g = tile / per_batch, in_batch = tile - g * per_batch;
+    const uint32_t n_tile = in_batch / uint32_t(a.m_tiles);
+    return Place{int32_t(g), int32_t(n_tile), int32_t(in_batch - n_tile * uint32_t(a.m_tiles)) * 256 + 128 * C};
+  };
+  if (tid == 0) {
+    prefetch_tensormap(&a.a_map);
+    prefetch_tensormap(&a.b_map);
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.peer_full[i], 1);
+      mbar_init(&ctl.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.sum_full[i], 1);
+      mbar_init(&ctl.sum_empty[i], 16);  // both CTAs' summing warps
+    }
+    mbar_init(&ctl.end, 1);
+    ctl.abort = 0;
+    fence_mbar_init_cluster();
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(&ctl.tbase, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers are initialised
+  tc_fence_after();
+  const uint32_t tb = ctl.tbase;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  if (warp < 4) {
+    regs_decrease<kPairOtherRegs>();
+    if (warp == 0) {
+      if (lane == 0) {
+        const uint32_t sm0 = smem_u32(sm);
+        int s = 0;
+        uint32_t lap = 0;
+        bool ok = true;
+        for (uint32_t tile = tile0; ok && tile < a.tiles; tile += step) {
+          const Place p = place(tile);
+          for (int i = 0; i < kbs; ++i) {
+            if (lap > 0 &&
+                !wait_bounded(&ctl.empty[s], (lap - 1) & 1, abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT)) {
+              ok = false;
+              break;
+            }
+            const uint32_t at = sm0 + s * kPairStageBytes;
+            mbar_arrive_expect_tx(&ctl.full[s], kPairStageBytes);
+            tma_load_3d(at, &a.a_map, i * kGroup, p.m0, p.g, &ctl.full[s]);
+            tma_load_3d(at + 128 * kGroup, &a.b_map, i * kGroup, p.n_tile * 256 + 128 * C, p.g, &ctl.full[s]);
+            if (++s == kPairStages) {
+              s = 0;
+              ++lap;
+            }
+          }
+        }
+        // the CTA leaves when its loads have landed, whatever became of the rest
+        int no_abort = 0;
+        for (int j = 0; j < kPairStages; ++j) {
+          const uint32_t used = lap + (j < s);
+          if (used > 0)
+            wait_bounded(&ctl.full[j], (used - 1) & 1, &no_abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      constexpr uint32_t idesc = idesc_f16_f32(256, 256, false, false);
+      const bool leader = elect_one();
+      uint32_t issued = 0;
+      int s = 0;
+      uint32_t lap = 0;
+      bool ok = true;
+      for (uint32_t tile = tile0; ok && tile < a.tiles; tile += step) {
+        for (int i = 0; i < kbs; ++i) {
+          ok = wait_bounded(&ctl.full[s], lap & 1, abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT);
+          if (C == 1) {  // tells the first CTA that this one's half has landed
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (leader) mbar_arrive_at(map_to_cta(smem_u32(&ctl.peer_full[s]), 0));
+            __syncwarp();
+          } else {
+            const int b = issued & 1;
+            ok = ok && wait_bounded(&ctl.peer_full[s], lap & 1, abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT) &&
+                 (issued < 2 || wait_bounded(&ctl.sum_empty[b], ((issued >> 1) - 1) & 1, abort, &g_matmul_error,
+                                             SMLA_DEVERR_TIMEOUT));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+              const uint32_t at = smem_u32(sm) + s * kPairStageBytes;
+              const uint64_t ad = sdesc_sw128(at, 16, 1024);
+              const uint64_t bd = sdesc_sw128(at + 128 * kGroup, 16, 1024);
+#pragma unroll
+              for (int k = 0; k < kGroup / 32; ++k)
+                mma_ss_f8_pair(tb + 256 * b, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+              mma_commit_pair(&ctl.empty[s]);
+              mma_commit_pair(&ctl.sum_full[b]);
+            }
+            __syncwarp();
+          }
+          ++issued;
+          if (++s == kPairStages) {
+            s = 0;
+            ++lap;
+          }
+        }
+      }
+      // every MMA has completed before tensor memory is given back
+      if (C == 0 && leader) mma_commit_pair(&ctl.end);
+      __syncwarp();
+      int no_abort = 0;
+      wait_bounded(&ctl.end, 0, &no_abort, &g_matmul_error, SMLA_DEVERR_TIMEOUT);
+    }
+  } else {
+    regs_increase<kPairSumRegs>();
+    const int t = tid - 128, quad = warp & 3, half = (warp - 4) >> 2;
+    const int row = 32 * quad + lane;
+    const uint32_t sum_empty = map_to_cta(smem_u32(&ctl.sum_empty[0]), 0);
+    uint64_t sum[64];
+    float next[kPairChunk / 2], next_b = 0.f;
+    auto fetch = [&](const Place& p, int i0) {
+      const int m = p.m0 + (t & 127);
+#pragma unroll
+      for (int f = 0; f < kPairChunk / 2; ++f) {
+        const int k = i0 + 2 * f + (t >> 7);
+        next[f] = k < kbs && m < a.M ? a.a_scales[p.g * a.ass.batch + m * a.ass.rows + k * a.ass.cols] : 0.f;
+      }
+      const int k = i0 + (t >> 1), n = 2 * p.n_tile + (t & 1);
+      if (t < 2 * kPairChunk)
+        next_b = k < kbs && n * 128 < a.N ? a.b_scales[p.g * a.bss.batch + n * a.bss.rows + k * a.bss.cols] : 0.f;
+    };
+    if (tile0 < a.tiles) fetch(place(tile0), 0);
+    uint32_t done = 0, chunks = 0;
+    bool ok = true;
+    for (uint32_t tile = tile0; tile < a.tiles; tile += step) {
+      const Place p = place(tile);
+#pragma unroll
+      for (int j = 0; j < 64; ++j) sum[j] = 0;
+      for (int i = 0; i < kbs; ++i, ++done) {
+        if (i % kPairChunk == 0) {
+          // the buffer's last readers are two chunks back, before the barrier of
+          // the chunk between
+#pragma unroll
+          for (int f = 0; f < kPairChunk / 2; ++f) sa[chunks & 1][2 * f + (t >> 7)][t & 127] = next[f];
+          if (t < 2 * kPairChunk) sb[chunks & 1][t >> 1][t & 1] = next_b;
+          named_bar_sync(1, 256);
+          ++chunks;
+          if (i + kPairChunk < kbs) fetch(p, i + kPairChunk);
+          else if (tile + step < a.tiles) fetch(place(tile + step), 0);
+        }
+        const int b = done & 1;
+        ok = __all_sync(0xffffffffu, wait_bounded(&ctl.sum_full[b], (done >> 1) & 1, abort, &g_matmul_error,
+                                                  SMLA_DEVERR_TIMEOUT));
+        // a warp that gives up goes on to the barriers with what it has
+        if (ok) {
+          tc_fence_after();
+          const float f = sa[(chunks - 1) & 1][i % kPairChunk][row] * sb[(chunks - 1) & 1][i % kPairChunk][half];
+          const uint64_t s2 = pack2(f, f);
+          const uint32_t at = tmem_addr(tb, 32 * quad, 256 * b + 128 * half);
+          uint32_t r[2][32];
+          tmem_ld32(at, r[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait();
+            if (c < 3) tmem_ld32(at + 32 * (c + 1), r[(c + 1) & 1]);
+            if (c == 3) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_at(sum_empty + 8 * b);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              sum[16 * c + j] = fma2(pack2(r[c & 1][2 * j], r[c & 1][2 * j + 1]), s2, sum[16 * c + j]);
+          }
+        }
+      }
+      if (p.m0 + row < a.M) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          float v[16];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 f = unpack2(sum[8 * c + j]);
+            v[2 * j] = f.x;
+            v[2 * j + 1] = f.y;
+          }
+          store_row<16>(a, p.g, p.m0 + row, p.n_tile * 256 + 128 * half + 16 * c, v);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // neither CTA reaches into the other any more
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc_pair(tb, 512);
+  __syncwarp();
+  cluster_sync();
 }
 
 // cuTensorMapEncodeTiled, looked up once through the runtime.
@@ -416,6 +677,8 @@ cudaError_t encode_codes(CUtensorMap* map, const uint8_t* p, const Strides& st, 
 }
 
 constexpr int kSms = 152;
+// tiles from which pairs take them
+constexpr int64_t kPairTiles = 38;
 
 template <bool kSwap, int kCols>
 cudaError_t launch(MatmulArgs& a, cudaStream_t s) {
@@ -436,12 +699,16 @@ cudaError_t launch(MatmulArgs& a, cudaStream_t s) {
   }
   a.m_tiles = int32_t((int64_t(a.M) + (kSwap ? kCols : kLaneRows) - 1) / (kSwap ? kCols : kLaneRows));
   const int64_t tiles = int64_t(a.G) * a.m_tiles * a.n_tiles;
+  a.tiles = uint32_t(tiles);
   a.splits = 1;
   while (a.splits < kMaxSplits && tiles * a.splits * 2 <= kSms && a.k_blocks >= 4 * a.splits) a.splits *= 2;
-  if (tiles * a.splits > INT32_MAX) return cudaErrorInvalidConfiguration;
   const int per_split = (a.k_blocks + a.splits - 1) / a.splits;
-  const int most = kMaxSmem / S::kStageBytes;
-  a.stages = per_split < most ? per_split : most;
+  // two CTAs an SM along the columns: one's loads run while the other starts or
+  // ends
+  const int most = (kSwap && a.splits == 1 ? kMaxSmem / 2 : kMaxSmem) / S::kStageBytes;
+  const int64_t total = tiles > kSms * 2 ? (tiles + 2 * kSms - 1) / (2 * kSms) * per_split : per_split;
+  a.stages = int(total < most ? total : most);
+  const int64_t ctas = kSwap && a.splits == 1 && tiles > 2 * kSms ? 2 * kSms : tiles * a.splits;
   size_t smem = size_t(a.stages) * S::kStageBytes;
   if (a.splits > 1 && smem < size_t(S::kExchange)) smem = S::kExchange;
   // As many CTAs on an SM as tensor memory holds and no more: one that waited
@@ -451,7 +718,7 @@ cudaError_t launch(MatmulArgs& a, cudaStream_t s) {
   const size_t least = size_t(228 * 1024) / (kResident + 1) + 1;
   if (smem + 1024 + kStatic < least) smem = least - 1024 - kStatic;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(tiles * a.splits));
+  cfg.gridDim = dim3(unsigned(ctas));
   cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = smem + 1024;
   cfg.stream = s;
@@ -465,6 +732,25 @@ cudaError_t launch(MatmulArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, fp8_matmul_kernel<kSwap, kCols>, a);
+}
+
+cudaError_t launch_pairs(MatmulArgs& a, cudaStream_t s) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool tracked = dev >= 0 && dev < 64;
+  if (!tracked || !done[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(fp8_matmul_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+    if (e != cudaSuccess) return e;
+    if (tracked) done[dev].store(true, std::memory_order_release);
+  }
+  a.m_tiles = int32_t((int64_t(a.M) + 255) / 256);
+  a.n_tiles = int32_t((int64_t(a.N) + 255) / 256);
+  a.tiles = uint32_t(int64_t(a.G) * a.m_tiles * a.n_tiles);
+  a.splits = 1;
+  const unsigned pairs = a.tiles < kSms / 2 ? a.tiles : kSms / 2;
+  return launch_overlapped(fp8_matmul_pair_kernel, 2 * pairs, kPairThreads, kPairSmem, s, a);
 }
 
 }  // namespace
@@ -485,8 +771,10 @@ cudaError_t launch_fp8_matmul(const MatmulArgs& args, cudaStream_t s) {
     case 16: return launch<true, 16>(a, s);
     case 32: return launch<true, 32>(a, s);
     case 64: return launch<true, 64>(a, s);
-    default: return launch<false, 128>(a, s);
+    default: break;
   }
+  const int64_t pair_tiles = int64_t(a.G) * ((int64_t(a.M) + 255) / 256) * ((int64_t(a.N) + 255) / 256);
+  return a.M > 128 && pair_tiles >= kPairTiles ? launch_pairs(a, s) : launch<false, 128>(a, s);
 }
 
 cudaError_t matmul_error_word(uint32_t* flags, bool clear) {

@@ -102,6 +102,7 @@ struct MatmulArgs {
   int32_t out_fp32;
   // set by the launcher
   int32_t m_tiles, n_tiles, k_blocks, splits, stages, vec;
+  uint32_t tiles;            // of all batches
 };
 
 // max_keys: of a request

@@ -202,7 +202,9 @@ def _check_product(got, a, sa, b, sb):
 
 SIZES = [(1, 1, 1), (1, 1, 16), (1, 576, 2048), (2, 5, 127), (3, 200, 130), (16, 129, 128), (17, 128, 1000),
          (33, 300, 272), (64, 257, 640), (65, 128, 384), (128, 130, 129), (130, 64, 16), (200, 300, 2176),
-         (257, 513, 1152), (5, 40, 16384), (64, 128, 8192), (100, 128, 4112)]
+         (257, 513, 1152), (5, 40, 16384), (64, 128, 8192), (100, 128, 4112),
+         (20, 45000, 130), (50, 40001, 300),                             # columns' tiles in turn
+         (300, 4990, 400), (1100, 2049, 144), (259, 9000, 1300), (2000, 3000, 48)]  # pairs' tiles
 
 
 @pytest.mark.gpu
@@ -220,7 +222,8 @@ def test_product_matches_the_definition(cuda_device, M, N, K):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("G,M,N,K", [(3, 1, 512, 128), (5, 64, 128, 512), (128, 2, 16, 128), (2, 100, 300, 400),
-                                     (7, 129, 33, 48), (2, 20, 60, 4096)])
+                                     (7, 129, 33, 48), (2, 20, 60, 4096),
+                                     (40, 130, 33, 176), (20, 300, 260, 272)])
 def test_batches_in_and_out_of_interleaved_rows(cuda_device, G, M, N, K):
     """A product for each head, from and into the heads' parts of wider rows."""
     a0, sa = _operand((M, G, K), G + M, 1, cuda_device)
