@@ -2,13 +2,19 @@
 // e4m3 codes and an fp32 scale, in the rounding of the 8-bit cache's rows:
 //   scale = fp32(max |x| / 448),   code = e4m3(x / scale), each rounded once.
 //
-// Three bytes move for an element, so memory bounds it; sixteen lanes take a
-// group, eight values each.  The quotient is rounded to e4m3 from fp32: with
-// y = 1 / scale, q = x y corrected by its residual is within an ulp of x /
-// scale and equal to it where that is an fp32 number.  Rounding q would go
-// wrong only where q is halfway between two codes and the quotient is not;
-// there the sign of the residual x - q scale tells its side, and q moves one
-// ulp to it.
+// Three bytes move for an element, so memory should bound it, and a value may
+// cost few instructions: a product and half a conversion.  That is enough
+// because x and the largest value, top, have 8 significant bits: let the
+// quotient of x and top / 448 be compared with a number halfway between two
+// codes, whose significand M has at most 5 bits.  With the significands X and T
+// that is 7 X 2^k against M T: if they differ, the quotient is at least 2^-13 of
+// itself away from the halfway number, far more than any rounding here.  If they
+// are equal, x / scale is as far from it as the rounded scale is from top / 448:
+//   * the scale is below: the quotient is above, by less than 2^-23 (and below
+//     it the other way): the reciprocal is taken 2^-20 larger (smaller),
+//     which decides these and no others;
+//   * the scale is exact (7 divides T): the quotient is the halfway number
+//     itself and goes to the even code: the product is rounded to 14 bits first.
 #include <cuda_fp8.h>
 
 #include "../../include/smla.h"
@@ -18,43 +24,57 @@ namespace smla {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kLanes = 16;   // of a group
-constexpr int kPer = 8;      // values of a lane
+// Lanes of a group, values of a lane.  What a lane does once for its group (its
+// place, the maximum, scale and reciprocal) costs as much as several values.
+constexpr int kLanes = 8;
+constexpr int kPer = 16;
 
-__device__ __forceinline__ float quotient(float x, float scale, float inv) {
-  float q = x * inv;
-  q = fmaf(fmaf(-q, scale, x), inv, q);
-  // halves between codes have at most five significant bits
-  if ((__float_as_uint(q) & 0x3ffffu) == 0) {
-    const float r = fmaf(-q, scale, x);
-    if (r != 0.f && q != 0.f)
-      q = __uint_as_float(__float_as_uint(q) + ((r < 0.f) == (q < 0.f) ? 1u : ~0u));
-  }
-  return q;
+// top / 448, rounded once: a product by the rounded reciprocal, corrected by its
+// residual, is that for every bf16 top (all 256 significands were tried)
+// whose quotient is normal.
+__device__ __forceinline__ float over_448(float top) {
+  if (top < 0x1p-116f) return __fdiv_rn(top, 448.f);
+  constexpr float kInv = 1.f / 448.f;
+  const float s = top * kInv;
+  return fmaf(fmaf(-s, 448.f, top), kInv, s);
 }
 
-__global__ void __launch_bounds__(kThreads) fp8_quantise_kernel(const QuantiseArgs a, int64_t groups,
-                                                                int32_t row_groups, bool vec) {
+// A thread block's groups lie `step` apart in the list of all of them; the
+// place of the next (column block, row, batch) follows by carries.
+struct Walk {
+  int64_t groups, step;
+  int32_t row_groups, d_kb, d_m, d_g;  // step as column blocks, rows, batches
+};
+
+__global__ void __launch_bounds__(kThreads) fp8_quantise_kernel(const QuantiseArgs a, const Walk walk, bool vec) {
   const int sub = threadIdx.x & (kLanes - 1);
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t step = int64_t(gridDim.x) * (kThreads / kLanes);
-  for (int64_t i0 = int64_t(blockIdx.x) * (kThreads / kLanes); i0 < groups; i0 += step) {
-    const int64_t i = i0 + threadIdx.x / kLanes;
-    const bool live = i < groups;
-    const int64_t row = live ? i / row_groups : 0;
-    const int32_t kb = int32_t(live ? i - row * row_groups : 0);
-    const int64_t g = row / a.M;
-    const int64_t m = row - g * a.M;
+  int64_t i = int64_t(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes;
+  int32_t kb, m, g;
+  if (walk.groups <= INT32_MAX) {
+    const uint32_t row = uint32_t(i) / uint32_t(walk.row_groups);
+    kb = int32_t(uint32_t(i) - row * uint32_t(walk.row_groups));
+    g = int32_t(row / uint32_t(a.M));
+    m = int32_t(row - uint32_t(g) * uint32_t(a.M));
+  } else {
+    const int64_t row = i / walk.row_groups;
+    kb = int32_t(i - row * walk.row_groups);
+    g = int32_t(row / a.M);
+    m = int32_t(row - int64_t(g) * a.M);
+  }
+  // both halves of a warp stay while either has a group
+  for (; __any_sync(0xffffffffu, i < walk.groups); i += walk.step) {
+    const bool live = i < walk.groups;
     const int32_t col = kb * 128 + sub * kPer;
     const int32_t n = live ? min(max(a.K - col, 0), kPer) : 0;
     const uint16_t* x = a.x + g * a.xs.batch + m * a.xs.rows + col;
     float v[kPer];
     if (vec && n == kPer) {
-      const uint4 w = *reinterpret_cast<const uint4*>(x);
-      const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+      const uint4 w0 = reinterpret_cast<const uint4*>(x)[0], w1 = reinterpret_cast<const uint4*>(x)[1];
+      const uint32_t p[kPer / 2] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kPer / 2; ++j) {
         v[2 * j] = __uint_as_float(p[j] << 16);
         v[2 * j + 1] = __uint_as_float(p[j] & 0xffff0000u);
       }
@@ -69,24 +89,31 @@ __global__ void __launch_bounds__(kThreads) fp8_quantise_kernel(const QuantiseAr
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const bool finite = top < 0x7f800000u;
-    const float scale = finite ? __fdiv_rn(__uint_as_float(top), 448.f) : __uint_as_float(0x7fc00000u);
-    const bool coded = finite && scale >= 0x1p-126f;
+    const float scale = finite ? over_448(__uint_as_float(top)) : __uint_as_float(0x7fc00000u);
     uint32_t code[kPer / 4] = {};
-    if (coded) {
-      // small groups are taken 2^64 larger, where residuals are exact too
-      const float up = scale < 0x1p-60f ? 0x1p64f : 1.f;
-      const float unit = scale * up;
-      const float inv = __frcp_rn(unit);
+    if (finite && scale >= 0x1p-126f) {
+      const float off = fmaf(-scale, 448.f, __uint_as_float(top));  // exact
+      float inv = __fdividef(1.f, scale);
+      if (off == 0.f) {
 #pragma unroll
-      for (int j = 0; j < kPer; j += 2) {
-        const float2 q = make_float2(quotient(v[j] * up, unit, inv), quotient(v[j + 1] * up, unit, inv));
-        code[j / 4] |= uint32_t(__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3)) << (8 * (j & 2));
+        for (int j = 0; j < kPer; ++j) {
+          const float q = __fmul_rn(v[j], inv), c = __fmul_rn(q, 1025.f);
+          v[j] = __fsub_rn(c, __fsub_rn(c, q));
+        }
+        inv = 1.f;
+      } else {
+        inv = fmaf(inv, copysignf(0x1p-20f, off), inv);
       }
+#pragma unroll
+      for (int j = 0; j < kPer; j += 2)
+        code[j / 4] |= uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(v[j] * inv, v[j + 1] * inv), __NV_SATFINITE,
+                                                         __NV_E4M3))
+                       << (8 * (j & 2));
     }
     if (n > 0) {
       uint8_t* c = a.codes + g * a.cs.batch + m * a.cs.rows + col;
-      if (n == kPer && (reinterpret_cast<uintptr_t>(c) & 7) == 0) {
-        *reinterpret_cast<uint2*>(c) = make_uint2(code[0], code[1]);
+      if (n == kPer && (reinterpret_cast<uintptr_t>(c) & 15) == 0) {
+        *reinterpret_cast<uint4*>(c) = make_uint4(code[0], code[1], code[2], code[3]);
       } else {
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
@@ -94,19 +121,32 @@ __global__ void __launch_bounds__(kThreads) fp8_quantise_kernel(const QuantiseAr
       }
     }
     if (live && sub == 0) a.scales[g * a.ss.batch + m * a.ss.rows + kb * a.ss.cols] = scale;
+    kb += walk.d_kb;
+    int32_t carry = kb >= walk.row_groups;
+    kb -= carry ? walk.row_groups : 0;
+    m += walk.d_m + carry;
+    carry = m >= a.M;
+    m -= carry ? a.M : 0;
+    g += walk.d_g + carry;
   }
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_quantise(const QuantiseArgs& a, cudaStream_t s) {
-  const int32_t row_groups = int32_t((int64_t(a.K) + 127) / 128);
-  const int64_t groups = int64_t(a.G) * a.M * row_groups;
+  Walk w;
+  w.row_groups = int32_t((int64_t(a.K) + 127) / 128);
+  w.groups = int64_t(a.G) * a.M * w.row_groups;
   const int64_t per = kThreads / kLanes;
-  const int64_t need = (groups + per - 1) / per;
-  const unsigned grid = unsigned(need < 152 * 64 ? need : 152 * 64);
+  const int64_t need = (w.groups + per - 1) / per;
+  const unsigned grid = unsigned(need < 152 * 6 ? need : 152 * 6);
+  w.step = int64_t(grid) * per;
+  const int64_t rows = w.step / w.row_groups;
+  w.d_kb = int32_t(w.step - rows * w.row_groups);
+  w.d_g = int32_t(rows / a.M);
+  w.d_m = int32_t(rows - int64_t(w.d_g) * a.M);
   const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.xs.batch % 8 == 0 && a.xs.rows % 8 == 0;
-  return launch_overlapped(fp8_quantise_kernel, grid, kThreads, 0, s, a, groups, row_groups, vec);
+  return launch_overlapped(fp8_quantise_kernel, grid, kThreads, 0, s, a, w, vec);
 }
 
 }  // namespace smla
