@@ -126,6 +126,19 @@ __device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t g, int32_
   }
 }
 
+// Results of consecutive rows, `stride` apart.  Instructions bound it: with an
+// address and the output's type looked at for each result a tile of 64 rows
+// took 2.4 us more (128 heads' 64 x 512 x 128 11.8 us instead of 5.7, 64 rows
+// through 24576 x 1536 13.4 instead of 10.7).
+template <int kN, class T>
+__device__ __forceinline__ void store_column(T* o, int64_t stride, int32_t rows, const float* v) {
+#pragma unroll
+  for (int j = 0; j < kN; ++j) {
+    if (j < rows) *o = T(v[j]);
+    o += stride;
+  }
+}
+
 template <bool kSwap, int kCols>
 __global__ void __launch_bounds__(Shape<kSwap, kCols>::kThreads, kSwap ? 2 : 1)
     fp8_matmul_kernel(const __grid_constant__ MatmulArgs a) {
@@ -343,11 +356,13 @@ __global__ void __launch_bounds__(Shape<kSwap, kCols>::kThreads, kSwap ? 2 : 1)
       }
       if (a.splits == 1) {
         if constexpr (kSwap) {
+          // a warp stores 32 columns of a row at a time
           const int32_t n = p.n_tile * 128 + row;
           if (n < a.N) {
-#pragma unroll
-            for (int j = 0; j < kCols; ++j)
-              if (p.m0 + j < a.M) store_row<1>(a, p.g, p.m0 + j, n, acc + j);
+            const int64_t at = p.g * a.os.batch + p.m0 * a.os.rows + n;
+            const int32_t rows = min(a.M - p.m0, kCols);
+            if (a.out_fp32) store_column<kCols>(static_cast<float*>(a.out) + at, a.os.rows, rows, acc);
+            else store_column<kCols>(static_cast<__nv_bfloat16*>(a.out) + at, a.os.rows, rows, acc);
           }
         } else if (p.m0 + row < a.M) {
           store_row<S::kPerThread>(a, p.g, p.m0 + row, p.n_tile * 128 + half * S::kPerThread, acc);
