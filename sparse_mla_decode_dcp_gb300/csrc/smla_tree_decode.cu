@@ -22,7 +22,7 @@
 //     MMA's layout asynchronously (cp.async).  The query's latent part is an
 //     e4m3 sum hi + lo of each row's values times a power of two: bf16 has 8
 //     significant bits, hi the first 4 and lo the rest, exactly down to 2^-10
-//     of the row's largest value and within 2^-19 of it below.  The four scale
+//     of the row's largest value and within 2^-17 of it below.  The four scale
 //     groups and the rope part (bf16 as it is) have score accumulators of
 //     their own, which meet, times the fp32 scales, in the softmax: the log
 //     sum is as exact as fp32 sums are.  Values are codes times scales,
@@ -115,7 +115,7 @@ struct TreeCtl {
   float row_scale[2][kCtaRows];           // fp8 rows, per item (mod 2): a row's score times this is its own
   float tops[2][32 * kSoftWarps], sums[32 * kSoftWarps];
   Item items[kItems];
-  int64_t warp_units[kTreeWarps];
+  int64_t warp_units[kTreeWarps], warp_later[kTreeWarps];
   int64_t start;                          // of the pair's range, within its first request
   int32_t start_req;
   // fp8 rows only, so last: per tile (mod 4), the keys' scales by group
@@ -194,6 +194,12 @@ __device__ __forceinline__ int32_t key_tiles(const Request& r) {
 // Units of a row tile: its key tiles where it may be cut, else one.
 __device__ __forceinline__ int32_t tile_units(const TreeDecodeArgs& a, const Request& r) {
   return a.split ? key_tiles(r) : 1;
+}
+
+// x / y of numbers that seldom need 64 bits.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return uint32_t(x) / uint32_t(y);
+  return x / y;
 }
 
 // A key's place while its table entry is on the way.
@@ -302,9 +308,12 @@ __device__ void list_work(const TreeDecodeArgs& a, TreeCtl* ctl, int C, int64_t 
       const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += x;
     }
-    while (in_req < all && u < u_end) {
-      const int32_t tile = int32_t(in_req / per_tile);
-      const int32_t k0 = int32_t(in_req - int64_t(tile) * per_tile);
+    int32_t tile = 0, k0 = 0;
+    if (in_req != 0) {
+      tile = int32_t(quotient(in_req, per_tile));
+      k0 = int32_t(in_req - int64_t(tile) * per_tile);
+    }
+    for (; in_req < all && u < u_end; ++tile, k0 = 0) {
       const int32_t take = int32_t(min(int64_t(per_tile - k0), u_end - u));
       const bool whole = take == per_tile;
       const int slot = item % kItems;
@@ -334,7 +343,7 @@ __device__ void list_work(const TreeDecodeArgs& a, TreeCtl* ctl, int C, int64_t 
       if (!whole && k0 == 0) {
         begun.row = r.first * a.H + skip;
         begun.rows = rows;
-        begun.parts = int32_t((u + per_tile - 1) / per_pair) - pair + 1;
+        begun.parts = int32_t(quotient(u + per_tile - 1, per_pair)) - pair + 1;
         begun.place = 2 * pair + (item > 0);
       }
       __syncwarp();
@@ -357,45 +366,46 @@ __device__ void list_work(const TreeDecodeArgs& a, TreeCtl* ctl, int C, int64_t 
 }
 
 // --------------------------------------------------------------- the keys' rows
-// One warp, half a tile at a time, a key a lane, and half a tile ahead.  A
-// missing key's row is read from somewhere else (a row of q is longer than a
-// cache row): its score is masked, and what goes into the value tile is made
-// finite.
+// One warp, two keys a lane, and a tile ahead.  A missing key's row is read
+// from somewhere else (a row of q is longer than a cache row): its score is
+// masked, and what goes into the value tile is made finite.
 __device__ void look_up_rows(const TreeDecodeArgs& a, TreeCtl* ctl, int row_bytes, int lane) {
   const uint8_t* elsewhere = reinterpret_cast<const uint8_t*>(a.q);
   unsigned err = 0;
   Cursor ahead;
-  Place place;
-  uint32_t low = 0;  // which of the tile's first keys exist
+  Place place[2];
 #pragma unroll 1
-  for (int h = -1;; ++h) {  // half tile h is stored, h + 1 looked up
-    const uint8_t* row = h < 0 ? nullptr : key_row(a, place, row_bytes, err);
-    const bool stores = h >= 0;
-    if (((h + 1) & 1) == 0) {
-      const int before = ahead.item;
-      ahead.next_tile(ctl);
-      if (before >= 0 && ahead.item != before) leave_item(ctl, before, lane);
+  for (int t = -1;; ++t) {  // tile t is stored, t + 1 looked up
+    const uint8_t* row[2];
+    if (t >= 0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) row[h] = key_row(a, place[h], row_bytes, err);
     }
+    const int before = ahead.item;
+    ahead.next_tile(ctl);
+    if (before >= 0 && ahead.item != before) leave_item(ctl, before, lane);
     if (!ahead.end) {
       const Item& it = ahead.at(ctl);
-      place = find_key(a, it.keys, it.req, (it.tile0 + ahead.tile) * kTileKeys + 32 * ((h + 1) & 1) + lane);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        place[h] = find_key(a, it.keys, it.req, (it.tile0 + ahead.tile) * kTileKeys + 32 * h + lane);
     }
-    if (stores) {
-      const int t = h >> 1, slot = t % kPlaces;
-      if ((h & 1) == 0 && t >= kPlaces &&
+    if (t >= 0) {
+      const int slot = t % kPlaces;
+      if (t >= kPlaces &&
           !__all_sync(0xffffffffu, tree_wait(&ctl->place_empty[slot], (t / kPlaces - 1) & 1, ctl, kWsRawEmpty)))
         break;
-      const uint32_t have = __ballot_sync(0xffffffffu, row != nullptr);
-      ctl->row[slot][32 * (h & 1) + lane] = row ? row : elsewhere;
-      if (h & 1) {
-        if (lane == 0) ctl->valid[t & 15] = uint64_t(have) << 32 | low;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->place_full[slot]);
-        if (ahead.end) break;
+      uint32_t have[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        have[h] = __ballot_sync(0xffffffffu, row[h] != nullptr);
+        ctl->row[slot][32 * h + lane] = row[h] ? row[h] : elsewhere;
       }
-      low = have;
+      if (lane == 0) ctl->valid[t & 15] = uint64_t(have[1]) << 32 | have[0];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->place_full[slot]);
     }
-    if (ahead.end && (h & 1) != 0) break;  // no tile at all, or the last stored
+    if (ahead.end) break;
   }
   if (err) atomicOr(&g_decode_error, err);
 }
@@ -406,9 +416,9 @@ __device__ __forceinline__ bool must_mend(const TreeCtl* ctl, const Item& it, in
   return (it.tile0 + tile + 1) * kTileKeys > it.keys.prefix || ctl->valid[g & 15] != ~0ull;
 }
 
-// A warp's eight rows of q to their places in the Q operand (a row's 1,152
-// bytes as nine pieces of 128, one in each block), rows past the tile's as
-// zeros; each format then converts them in place.
+// A warp's eight rows of q on their way to the Q operand (a row's 1,152 bytes
+// as nine pieces of 128, one in each block), rows past the tile's as zeros;
+// each format then converts them in place.
 __device__ __forceinline__ void stage_queries(const TreeDecodeArgs& a, const Item& it, uint32_t q0, int C, int w,
                                               int lane) {
   const int64_t row0 = int64_t(it.keys.first) * a.H + it.skip + kCtaRows * C;
@@ -421,8 +431,6 @@ __device__ __forceinline__ void stage_queries(const TreeDecodeArgs& a, const Ite
     if (r < live) cp_async_16(at, a.q + (row0 + r) * SMLA_QK_DIM + 8 * chunk);
     else sts128(at, make_uint4(0, 0, 0, 0));
   }
-  cp_async_wait_all();
-  __syncwarp();
 }
 
 // 8-bit rows.  The copying warp brings this CTA's keys (codes, rope) into the
@@ -517,58 +525,74 @@ struct Fp8Keys {
     cp_async_wait_all();
   }
 
-  // Rows of the request's list as the A operands of QK^T, eight a warp.
-  static __device__ __forceinline__ void load_queries(const TreeDecodeArgs& a, const Item& it, uint32_t q0,
-                                                      float* row_scale, int C, int w, int lane) {
-    stage_queries(a, it, q0, C, w, lane);
+  static __device__ __forceinline__ __nv_bfloat162 magnitudes(uint32_t w) {
+    return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+  }
+  // The staged rows as the A operands of QK^T, eight a warp, two at a time.
+  static __device__ __forceinline__ void convert_queries(uint32_t q0, float* row_scale, int w, int lane) {
+    const uint32_t at = q0 + (lane >> 2) * kQBlock;  // dims 16 lane ..
+    const uint32_t to = q0 + (lane >> 3) * kQBlock;
 #pragma unroll 1
-    for (int r = 8 * w; r < 8 * w + 8; ++r) {
-      const uint32_t at = q0 + (lane >> 2) * kQBlock;  // dims 16 lane ..
-      const uint4 v0 = lds128(at + sw128_offset(r, 2 * (lane & 3)));
-      const uint4 v1 = lds128(at + sw128_offset(r, 2 * (lane & 3) + 1));
-      const uint32_t rope_at = q0 + 8 * kQBlock + sw128_offset(r, lane & 7);
-      const uint4 rope = lds128(rope_at);
-      const uint32_t x[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-      uint32_t top = 0;
+    for (int r0 = 8 * w; r0 < 8 * w + 8; r0 += 2) {
+      uint4 v[2][2], rope[2];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) top = max(top, max(x[k] & 0x7fffu, (x[k] >> 16) & 0x7fffu));
-      top = __reduce_max_sync(0xffffffffu, top);
-      // the row times 2^up has its largest value in [2^7, 2^8)
-      const int exponent = int(top >> 7);
-      const int up = top == 0 ? 0 : max(min(134 - exponent, 120), -120);
-      const float by = __uint_as_float(uint32_t(127 + up) << 23);
-      uint32_t hi[4], lo[4];
+      for (int i = 0; i < 2; ++i) {
+        v[i][0] = lds128(at + sw128_offset(r0 + i, 2 * (lane & 3)));
+        v[i][1] = lds128(at + sw128_offset(r0 + i, 2 * (lane & 3) + 1));
+        rope[i] = lds128(q0 + 8 * kQBlock + sw128_offset(r0 + i, lane & 7));
+      }
+      uint32_t top[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        hi[k] = lo[k] = 0;
+      for (int i = 0; i < 2; ++i) {
+        auto most = [](uint4 x) {
+          return __hmax2_nan(__hmax2_nan(magnitudes(x.x), magnitudes(x.y)), __hmax2_nan(magnitudes(x.z), magnitudes(x.w)));
+        };
+        const __nv_bfloat162 m = __hmax2_nan(most(v[i][0]), most(v[i][1]));
+        const uint32_t bits = *reinterpret_cast<const uint32_t*>(&m);
+        top[i] = max(bits & 0xffffu, bits >> 16);  // a NaN's bits are above infinity's
+      }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t w2 = x[2 * k + j];
-          const float2 f = make_float2(__uint_as_float(w2 << 16) * by, __uint_as_float(w2 & 0xffff0000u) * by);
-          const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-          const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
-          hi[k] |= uint32_t(c) << (16 * j);
-          lo[k] |= uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(f.x - b.x, f.y - b.y), __NV_SATFINITE, __NV_E4M3))
-                   << (16 * j);
+      for (int i = 0; i < 2; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
+      __syncwarp();  // every lane has read the rows
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = r0 + i;
+        const uint32_t x[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+        // the row times 2^up has its largest value in [2^7, 2^8)
+        const int exponent = int(top[i] >> 7);
+        const int up = top[i] == 0 ? 0 : max(min(134 - exponent, 120), -120);
+        const float by = __uint_as_float(uint32_t(127 + up) << 23);
+        const __nv_bfloat162 by2 = __float2bfloat162_rn(by);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          hi[k] = lo[k] = 0;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            // times 2^up as fp16: exact from 2^-17 on, within 2^-25 below
+            const uint32_t w2 = x[2 * k + j];
+            const __half2 f = __floats2half2_rn(__uint_as_float(w2 << 16) * by, __uint_as_float(w2 & 0xffff0000u) * by);
+            const __nv_fp8x2_storage_t c = __nv_cvt_halfraw2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+            const __half2 b = __half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3));
+            hi[k] |= uint32_t(c) << (16 * j);
+            lo[k] |= uint32_t(__nv_cvt_halfraw2_to_fp8x2(__hsub2(f, b), __NV_SATFINITE, __NV_E4M3)) << (16 * j);
+          }
         }
-      }
-      const uint32_t z[4] = {rope.x, rope.y, rope.z, rope.w};
-      uint32_t o[4];
+        const uint32_t z[4] = {rope[i].x, rope[i].y, rope[i].z, rope[i].w};
+        uint32_t o[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const __nv_bfloat162 p =
-            __floats2bfloat162_rn(__uint_as_float(z[k] << 16) * by, __uint_as_float(z[k] & 0xffff0000u) * by);
-        o[k] = *reinterpret_cast<const uint32_t*>(&p);
-      }
-      __syncwarp();  // every lane has read the row
-      const uint32_t to = q0 + (lane >> 3) * kQBlock + sw128_offset(r, lane & 7);
-      sts128(to, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-      sts128(to + 4 * kQBlock, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-      if (lane < 8) sts128(rope_at, make_uint4(o[0], o[1], o[2], o[3]));
-      // a query that is not finite has no score that is
-      if (lane == 0) {
-        row_scale[r] = __uint_as_float(exponent == 255 ? 0x7fc00000u : uint32_t(127 - up) << 23);
-        if (exponent == 255) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
+        for (int k = 0; k < 4; ++k) {
+          const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&z[k]), by2);
+          o[k] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        sts128(to + sw128_offset(r, lane & 7), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        sts128(to + 4 * kQBlock + sw128_offset(r, lane & 7), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        if (lane < 8) sts128(q0 + 8 * kQBlock + sw128_offset(r, lane), make_uint4(o[0], o[1], o[2], o[3]));
+        // a query that is not finite has no score that is
+        if (lane == 0) {
+          row_scale[r] = __uint_as_float(exponent == 255 ? 0x7fc00000u : uint32_t(127 - up) << 23);
+          if (exponent == 255) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
+        }
       }
     }
   }
@@ -599,7 +623,10 @@ struct Fp8Keys {
     };
     Cursor ahead, now;
     ahead.next_tile(ctl);
-    if (!ahead.end) ok = load_peer(0);
+    if (!ahead.end) {
+      stage_queries(a, ahead.at(ctl), base, C, w, lane);  // while the keys are looked up
+      ok = load_peer(0);
+    }
     int st = 0, lap = 0;  // the K tile and its uses
     for (int g = 0; ok; ++g) {
       // to the next tile; an item is handed back when it is left
@@ -609,9 +636,13 @@ struct Fp8Keys {
       if (now.end) break;
       const Item& it = now.at(ctl);
       if (now.tile == 0) {  // the item's rows, in place of the last one's
-        if (g > 0 && !__all_sync(0xffffffffu, tree_wait(&ctl->k_free[(g - 1) % 3], ((g - 1) / 3) & 1, ctl, kWsFreed)))
-          break;
-        load_queries(a, it, base, ctl->row_scale[now.item & 1], C, w, lane);
+        if (g > 0) {
+          if (!__all_sync(0xffffffffu, tree_wait(&ctl->k_free[(g - 1) % 3], ((g - 1) / 3) & 1, ctl, kWsFreed))) break;
+          stage_queries(a, it, base, C, w, lane);
+        }
+        cp_async_wait_all();
+        __syncwarp();
+        convert_queries(base, ctl->row_scale[now.item & 1], w, lane);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive_at(q_full);
@@ -701,9 +732,7 @@ struct Fp4Keys {
   static constexpr int kRowBytes = SMLA_FP4_ROW_BYTES;
   using Sm = Shared<true>;
 
-  static __device__ __forceinline__ void load_queries(const TreeDecodeArgs& a, const Item& it, uint32_t q0, int C,
-                                                      int w, int lane) {
-    stage_queries(a, it, q0, C, w, lane);
+  static __device__ __forceinline__ void convert_queries(uint32_t q0, int w, int lane) {
     uint32_t over = 0;
 #pragma unroll 2
     for (int k = 0; k < 8 * 72 / 32; ++k) {
@@ -773,7 +802,10 @@ struct Fp4Keys {
     };
     Cursor ahead, now;
     ahead.next_tile(ctl);
-    if (!ahead.end) ok = load(0);
+    if (!ahead.end) {
+      stage_queries(a, ahead.at(ctl), base, C, w, lane);  // while the keys are looked up
+      ok = load(0);
+    }
     for (int g = 0; ok; ++g) {
       const int before = now.item;
       now.next_tile(ctl);
@@ -782,9 +814,13 @@ struct Fp4Keys {
       const Item& it = now.at(ctl);
       const int st = g & 1;
       if (now.tile == 0) {  // the item's rows, in place of the last one's
-        if (g > 0 && !__all_sync(0xffffffffu, tree_wait(&ctl->k_free[(g - 1) & 1], ((g - 1) >> 1) & 1, ctl, kWsFreed)))
-          break;
-        load_queries(a, it, base, C, w, lane);
+        if (g > 0) {
+          if (!__all_sync(0xffffffffu, tree_wait(&ctl->k_free[(g - 1) & 1], ((g - 1) >> 1) & 1, ctl, kWsFreed))) break;
+          stage_queries(a, it, base, C, w, lane);
+        }
+        cp_async_wait_all();
+        __syncwarp();
+        convert_queries(base, w, lane);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive_at(q_full);
@@ -1014,6 +1050,9 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
     for (int j = 0; j < n; ++j, ++g) {
       const int b = g & 1;
       const uint32_t scores = lanes + kScoreCol + 16 * part;
+      const int first = (it.tile0 + j) * kTileKeys + kCtaKeys * half + 16 * part;  // key of s[0]
+      // the mask's words are on their way while the scores are computed
+      const uint32_t seen = first + 16 > it.keys.prefix ? seen_from(mask, a.mask_words, first - it.keys.prefix) : 0xffffu;
       uint32_t s[16];
       if constexpr (F::kFp4) {
         ok = __all_sync(0xffffffffu, tree_wait(&ctl->qk[b], (g >> 1) & 1, ctl, kWsSFull));
@@ -1068,9 +1107,7 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
           s[2 * k + 1] = __float_as_uint(f.y + __uint_as_float(s[2 * k + 1]));
         }
       }
-      const int first = (it.tile0 + j) * kTileKeys + kCtaKeys * half + 16 * part;  // key of s[0]
-      uint32_t see = uint32_t(ctl->valid[g & 15] >> (kCtaKeys * half + 16 * part)) & 0xffffu;
-      if (first + 16 > it.keys.prefix) see &= seen_from(mask, a.mask_words, first - it.keys.prefix);
+      const uint32_t see = seen & uint32_t(ctl->valid[g & 15] >> (kCtaKeys * half + 16 * part)) & 0xffffu;
       if (see != 0xffffu) {
 #pragma unroll
         for (int k = 0; k < 16; ++k)
@@ -1188,6 +1225,12 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
   }
 }
 
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
 template <class F>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
     tree_decode_kernel(const __grid_constant__ TreeDecodeArgs a) {
@@ -1234,37 +1277,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = ctl->tbase;
+  cluster_arrive();
   griddep_launch_dependents();
   griddep_wait();
 
-  // all requests' units, and where this pair's range begins
+  // all requests' units, and where this pair's range begins: a request a
+  // thread, and the later ones (of batches past the block's threads) in turn
   unsigned err = 0;
-  int64_t mine = 0;
+  int64_t v = 0, later = 0;
   for (int32_t b = tid; b < a.B; b += kTreeThreads) {
     const Request r = load_request(a, b, err);
-    mine += int64_t(row_tiles(a, r)) * tile_units(a, r);
+    const int64_t n = int64_t(row_tiles(a, r)) * tile_units(a, r);
+    if (b == tid) v = n;
+    else later += n;
   }
   if (err && blockIdx.x == 0) atomicOr(&g_decode_error, err);
-  int64_t total = mine;
+  int64_t upto = v;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) ctl->warp_units[warp] = total;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (a.B > kTreeThreads) later = warp_sum(later);
+  if (lane == 31) {
+    ctl->warp_units[warp] = upto;
+    ctl->warp_later[warp] = later;
+  }
   __syncthreads();
-  int64_t units = 0;
-  for (int w = 0; w < kTreeWarps; ++w) units += ctl->warp_units[w];
+  const int64_t of_warp = lane < kTreeWarps ? ctl->warp_units[lane] : 0;
+  int64_t base = warp_sum(of_warp);  // of the block's first requests
+  int64_t begin = warp_sum(lane < warp ? of_warp : 0) + upto - v;
+  int64_t units = base;
+  if (a.B > kTreeThreads) units += warp_sum(lane < kTreeWarps ? ctl->warp_later[lane] : 0);
   const int64_t pairs = gridDim.x >> 1;
-  const int64_t per_pair = max((units + pairs - 1) / pairs, int64_t(a.min_units));
+  const int64_t per_pair = max(quotient(units + pairs - 1, pairs), int64_t(a.min_units));
   const int64_t u0 = per_pair * (blockIdx.x >> 1);
-  int64_t base = 0;
-  for (int32_t b0 = 0; b0 < a.B && base <= u0; b0 += kTreeThreads) {
+  for (int32_t b0 = 0;;) {
+    if (begin <= u0 && u0 < begin + v) {
+      ctl->start_req = b0 + tid;
+      ctl->start = u0 - begin;
+    }
+    b0 += kTreeThreads;
+    if (b0 >= a.B || base > u0) break;
     const int32_t b = b0 + tid;
-    int64_t v = 0;
+    v = 0;
     if (b < a.B) {
       unsigned ignored = 0;
       const Request r = load_request(a, b, ignored);
       v = int64_t(row_tiles(a, r)) * tile_units(a, r);
     }
-    int64_t upto = v;
+    upto = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
@@ -1273,18 +1335,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
     __syncthreads();  // the sums before have been read
     if (lane == 31) ctl->warp_units[warp] = upto;
     __syncthreads();
-    int64_t begin = base + upto - v;
+    begin = base + upto - v;
     for (int w = 0; w < kTreeWarps; ++w) {
       if (w < warp) begin += ctl->warp_units[w];
       base += ctl->warp_units[w];
     }
-    if (begin <= u0 && u0 < begin + v) {
-      ctl->start_req = b;
-      ctl->start = u0 - begin;
-    }
   }
   __syncthreads();
-  cluster_sync();  // the peer's barriers are initialised
+  cluster_wait();  // the peer's barriers are initialised
 
   if (warp < kSoftWarps) {
     softmax_rows<F>(a, sm, ctl, tb, C, tid);
@@ -1369,20 +1427,31 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
 }
 
 // How a call is laid out, from its shape alone: its pairs, and whether a row
-// tile may be cut (never when one pair's least range holds all its keys).
+// tile may be cut.
 struct TreePlan {
   int pairs, min_units;
   bool split;
   size_t ml_off, o_off, bytes;
 };
 
-constexpr int kMinUnits = 4;
+// Key tiles that a pair takes at least.  One request of 8 nodes and 16 heads
+// over 300 / 2,000 / 4,000 positions, 8-bit rows: 18.1 / 24.3 / 46 us with 1
+// (the merge then reads a part a tile), 18.7 / 23.3 / 26.4 with 2, 20.6 / 22.6 /
+// 26.5 with 3.
+constexpr int kMinUnits = 2;
+// Row tiles of more key tiles than this are cut.  Where there are fewer than
+// half as many row tiles as pairs: the request above over 300 / 500 positions
+// 21.4 / 26.6 us whole, 18.7 / 20.1 cut.  Else the merge and the second loads of
+// the queries cost more than an even share gives: 8 and 32 requests of 128
+// heads over 300 positions 23.0 and 67.4 us whole, 25.1 and 75.5 cut; from 600
+// on there is no difference.
+constexpr int kWholeOfFew = 2, kWholeOfMany = 8;
 
 TreePlan plan_tree(int32_t T, int32_t B, int32_t H, int64_t max_keys) {
   TreePlan p;
   const int64_t key_tiles = (max_keys + kTileKeys - 1) / kTileKeys;
   const int64_t row_tiles = int64_t(T) * H / kPairRows + (B < T ? B : T);
-  p.split = key_tiles > 8;
+  p.split = key_tiles > (2 * row_tiles <= kPairs ? kWholeOfFew : kWholeOfMany);
   p.min_units = p.split ? kMinUnits : 1;
   const int64_t units = p.split ? row_tiles * key_tiles : row_tiles;
   const int64_t need = (units + p.min_units - 1) / p.min_units;
