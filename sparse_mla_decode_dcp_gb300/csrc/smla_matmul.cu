@@ -12,9 +12,9 @@
 //
 // One operand's rows are the MMA's 128 lanes, the other's its columns.  Many
 // activation rows lie along the lanes (kSwap false, tiles of 128 x 128, and with
-// enough of them the pairs' 256 x 256 below); up to 64 of them along the
-// columns, where a tile of 16, 32 or 64 wastes little, and the weights' rows
-// along the lanes: such a call is bound by the weights' bytes.  A weight tile of
+// enough of them the pairs' of 256 x 160 to 256 x 256 below); up to 64 of them
+// along the columns, where a tile of 16, 32 or 64 wastes little, and the
+// weights' rows along the lanes: such a call is bound by the weights' bytes.  A weight tile of
 // 128 rows has one scale a group either way.
 //
 // With few tiles the groups are split over the CTAs of a cluster, whose sums
@@ -413,46 +413,60 @@ __global__ void __launch_bounds__(Shape<kSwap, kCols>::kThreads, kSwap ? 2 : 1)
   cluster_sync();  // nobody's sums go while they are read
 }
 
-// Many rows: a CTA pair (cta_group::2) makes 256 x 256 results a tile, each CTA
-// 128 of the activation rows, in 256 columns of its tensor memory; each holds
-// half of both operands (the pair's MMAs read the other's half of the
+// Many rows: a CTA pair (cta_group::2) makes 256 x kCols results a tile, each
+// CTA 128 of the activation rows, in kCols columns of its tensor memory; each
+// holds half of both operands (the pair's MMAs read the other's half of the
 // weights), so a byte of shared memory serves twice the products of a 128 x 128
-// tile.  Two accumulators fill tensor memory: while one's group is summed into
-// registers (eight warps, 128 columns a thread), the next group's MMAs fill the
-// other.  Pairs take tiles in turn, rows first.
+// tile.  Of two accumulators one's group is summed into registers (eight warps,
+// half of the columns a thread) while the next group's MMAs fill the other.
+// Pairs take tiles in turn, rows first.
+//
+// What bounds it is the way from L2: with 160, 192, 224 and 256 columns a group
+// takes 364, 388, 423 and 434 ns, 11.1 to 11.5 TB/s of operands over all SMs,
+// while the MMAs need less (56% of the tensor cores' time with 224).  4001 rows
+// through 4096 x 16384: 217 us, 2.5 PFLOP/s.  16 columns are read from tensor
+// memory at a time: 32 (and with 256 columns a few spilled registers) took 267 us
+// with 256 columns instead of 222 and 227 with 224; a third and fourth
+// accumulator (160, 128 columns) nothing less.
 struct PairCtl {
   uint64_t full[kMaxStages], peer_full[kMaxStages], empty[kMaxStages], sum_full[2], sum_empty[2], end;
   uint32_t tbase;
   int abort;
 };
 constexpr int kPairThreads = 384;
-constexpr int kPairStageBytes = 2 * 128 * kGroup;
 constexpr int kPairStages = 6;
-constexpr int kPairSmem = kPairStages * kPairStageBytes + 1024;
+// of a CTA: 128 activation rows, half of the tile's columns
+template <int kCols> constexpr int kPairStageBytes = (128 + kCols / 2) * kGroup;
+template <int kCols> constexpr int kPairSmem = kPairStages * kPairStageBytes<kCols> + 1024;
 constexpr int kPairChunk = 8;  // groups whose scales are fetched together
 // registers a thread: launched with 168, then shared out by groups of four warps
 constexpr int kPairSumRegs = 224, kPairOtherRegs = 56;
 static_assert(8 * kPairSumRegs + 4 * kPairOtherRegs <= 12 * 168, "no more than the launch has");
 
+template <int kCols>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     fp8_matmul_pair_kernel(const __grid_constant__ MatmulArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ PairCtl ctl;
-  __shared__ float sa[2][kPairChunk][128], sb[2][kPairChunk][2];
+  // a thread's sums: half of the tile's columns, 16 read at a time; those have
+  // one weight scale, the tile's columns up to three
+  constexpr int kHalf = kCols / 2, kReads = kHalf / 16, kScales = 4;
+  static_assert(kCols % 32 == 0 && kCols <= 256, "halves are whole reads, and a read lies in one block of 128");
+  __shared__ float sa[2][kPairChunk][128], sb[2][kPairChunk][kScales];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = int(cluster_ctarank());
   volatile int* abort = &ctl.abort;
   const int kbs = a.k_blocks;
   const uint32_t tile0 = blockIdx.x >> 1, step = gridDim.x >> 1;
   struct Place {
-    int32_t g, n_tile, m0;  // n_tile: of 256; m0: this CTA's first row
+    int32_t g, n0, m0;  // the tile's first column, this CTA's first row
   };
   auto place = [&](uint32_t tile) {
     const uint32_t per_batch = uint32_t(a.m_tiles) * uint32_t(a.n_tiles);
     const uint32_t g = tile / per_batch, in_batch = tile - g * per_batch;
     const uint32_t n_tile = in_batch / uint32_t(a.m_tiles);
-    return Place{int32_t(g), int32_t(n_tile), int32_t(in_batch - n_tile * uint32_t(a.m_tiles)) * 256 + 128 * C};
+    return Place{int32_t(g), int32_t(n_tile) * kCols, int32_t(in_batch - n_tile * uint32_t(a.m_tiles)) * 256 + 128 * C};
   };
   if (tid == 0) {
     prefetch_tensormap(&a.a_map);
@@ -498,10 +512,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               ok = false;
               break;
             }
-            const uint32_t at = sm0 + s * kPairStageBytes;
-            mbar_arrive_expect_tx(&ctl.full[s], kPairStageBytes);
+            const uint32_t at = sm0 + s * kPairStageBytes<kCols>;
+            mbar_arrive_expect_tx(&ctl.full[s], kPairStageBytes<kCols>);
             tma_load_3d(at, &a.a_map, i * kGroup, p.m0, p.g, &ctl.full[s]);
-            tma_load_3d(at + 128 * kGroup, &a.b_map, i * kGroup, p.n_tile * 256 + 128 * C, p.g, &ctl.full[s]);
+            tma_load_3d(at + 128 * kGroup, &a.b_map, i * kGroup, p.n0 + kHalf * C, p.g, &ctl.full[s]);
             if (++s == kPairStages) {
               s = 0;
               ++lap;
@@ -518,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      constexpr uint32_t idesc = idesc_f16_f32(256, 256, false, false);
+      constexpr uint32_t idesc = idesc_f16_f32(256, kCols, false, false);
       const bool leader = elect_one();
       uint32_t issued = 0;
       int s = 0;
@@ -541,7 +555,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (!ok) break;
             tc_fence_after();
             if (leader) {
-              const uint32_t at = smem_u32(sm) + s * kPairStageBytes;
+              const uint32_t at = smem_u32(sm) + s * kPairStageBytes<kCols>;
               const uint64_t ad = sdesc_sw128(at, 16, 1024);
               const uint64_t bd = sdesc_sw128(at + 128 * kGroup, 16, 1024);
 #pragma unroll
@@ -570,7 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int t = tid - 128, quad = warp & 3, half = (warp - 4) >> 2;
     const int row = 32 * quad + lane;
     const uint32_t sum_empty = map_to_cta(smem_u32(&ctl.sum_empty[0]), 0);
-    uint64_t sum[64];
+    uint64_t sum[kHalf / 2];
     float next[kPairChunk / 2], next_b = 0.f;
     auto fetch = [&](const Place& p, int i0) {
       const int m = p.m0 + (t & 127);
@@ -579,8 +593,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int k = i0 + 2 * f + (t >> 7);
         next[f] = k < kbs && m < a.M ? a.a_scales[p.g * a.ass.batch + m * a.ass.rows + k * a.ass.cols] : 0.f;
       }
-      const int k = i0 + (t >> 1), n = 2 * p.n_tile + (t & 1);
-      if (t < 2 * kPairChunk)
+      const int k = i0 + t / kScales, n = p.n0 / 128 + t % kScales;
+      if (t < kScales * kPairChunk)
         next_b = k < kbs && n * 128 < a.N ? a.b_scales[p.g * a.bss.batch + n * a.bss.rows + k * a.bss.cols] : 0.f;
     };
     if (tile0 < a.tiles) fetch(place(tile0), 0);
@@ -589,14 +603,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     for (uint32_t tile = tile0; tile < a.tiles; tile += step) {
       const Place p = place(tile);
 #pragma unroll
-      for (int j = 0; j < 64; ++j) sum[j] = 0;
+      for (int j = 0; j < kHalf / 2; ++j) sum[j] = 0;
+      // the scales of this half's first reads, and of those from `cut` on
+      const int first = p.n0 % 128 + kHalf * half, block = first / 128;
+      const int cut = kCols == 256 ? kReads : (128 - first % 128) / 16;
       for (int i = 0; i < kbs; ++i, ++done) {
         if (i % kPairChunk == 0) {
           // the buffer's last readers are two chunks back, before the barrier of
           // the chunk between
 #pragma unroll
           for (int f = 0; f < kPairChunk / 2; ++f) sa[chunks & 1][2 * f + (t >> 7)][t & 127] = next[f];
-          if (t < 2 * kPairChunk) sb[chunks & 1][t >> 1][t & 1] = next_b;
+          if (t < kScales * kPairChunk) sb[chunks & 1][t / kScales][t % kScales] = next_b;
           named_bar_sync(1, 256);
           ++chunks;
           if (i + kPairChunk < kbs) fetch(p, i + kPairChunk);
@@ -608,29 +625,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // a warp that gives up goes on to the barriers with what it has
         if (ok) {
           tc_fence_after();
-          const float f = sa[(chunks - 1) & 1][i % kPairChunk][row] * sb[(chunks - 1) & 1][i % kPairChunk][half];
-          const uint64_t s2 = pack2(f, f);
-          const uint32_t at = tmem_addr(tb, 32 * quad, 256 * b + 128 * half);
-          uint32_t r[2][32];
-          tmem_ld32(at, r[0]);
+          const float f = sa[(chunks - 1) & 1][i % kPairChunk][row];
+          const float* fb = &sb[(chunks - 1) & 1][i % kPairChunk][block];
+          const float f0 = f * fb[0], f1 = kCols == 256 ? f0 : f * fb[1];
+          const uint64_t s0 = pack2(f0, f0), s1 = pack2(f1, f1);
+          const uint32_t at = tmem_addr(tb, 32 * quad, 256 * b + kHalf * half);
+          uint32_t r[2][16];
+          tmem_ld16(at, r[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < kReads; ++c) {
             tmem_ld_wait();
-            if (c < 3) tmem_ld32(at + 32 * (c + 1), r[(c + 1) & 1]);
-            if (c == 3) {
+            if (c + 1 < kReads) tmem_ld16(at + 16 * (c + 1), r[(c + 1) & 1]);
+            if (c + 1 == kReads) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive_at(sum_empty + 8 * b);
             }
+            const uint64_t s2 = c < cut ? s0 : s1;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              sum[16 * c + j] = fma2(pack2(r[c & 1][2 * j], r[c & 1][2 * j + 1]), s2, sum[16 * c + j]);
+            for (int j = 0; j < 8; ++j)
+              sum[8 * c + j] = fma2(pack2(r[c & 1][2 * j], r[c & 1][2 * j + 1]), s2, sum[8 * c + j]);
           }
         }
       }
       if (p.m0 + row < a.M) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < kHalf / 16; ++c) {
           float v[16];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -638,7 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             v[2 * j] = f.x;
             v[2 * j + 1] = f.y;
           }
-          store_row<16>(a, p.g, p.m0 + row, p.n_tile * 256 + 128 * half + 16 * c, v);
+          store_row<16>(a, p.g, p.m0 + row, p.n0 + kHalf * half + 16 * c, v);
         }
       }
     }
@@ -749,6 +769,7 @@ cudaError_t launch(MatmulArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, fp8_matmul_kernel<kSwap, kCols>, a);
 }
 
+template <int kCols>
 cudaError_t launch_pairs(MatmulArgs& a, cudaStream_t s) {
   static std::atomic<bool> done[64];
   int dev = 0;
@@ -756,16 +777,37 @@ cudaError_t launch_pairs(MatmulArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const bool tracked = dev >= 0 && dev < 64;
   if (!tracked || !done[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(fp8_matmul_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+    e = cudaFuncSetAttribute(fp8_matmul_pair_kernel<kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kPairSmem<kCols>);
     if (e != cudaSuccess) return e;
     if (tracked) done[dev].store(true, std::memory_order_release);
   }
   a.m_tiles = int32_t((int64_t(a.M) + 255) / 256);
-  a.n_tiles = int32_t((int64_t(a.N) + 255) / 256);
+  a.n_tiles = int32_t((int64_t(a.N) + kCols - 1) / kCols);
   a.tiles = uint32_t(int64_t(a.G) * a.m_tiles * a.n_tiles);
   a.splits = 1;
   const unsigned pairs = a.tiles < kSms / 2 ? a.tiles : kSms / 2;
-  return launch_overlapped(fp8_matmul_pair_kernel, 2 * pairs, kPairThreads, kPairSmem, s, a);
+  return launch_overlapped(fp8_matmul_pair_kernel<kCols>, 2 * pairs, kPairThreads, kPairSmem<kCols>, s, a);
+}
+
+// The pairs' tile width, 0 for a call with too few tiles: the one whose rounds
+// of 76 tiles bring the least bytes, 128 + cols / 2 rows a CTA.  4001 x 4096 x
+// 16384 takes 222 us with 256 columns, 217 with 224, 248 with 192 and 280 with
+// 160; 4096 x 7168 x 2048 57.5, 62.4, 66.1 and 75.0; 300 x 7168 x 16384 57.6,
+// 56.2, 53.1 and 95.3; 2000 x 3000 x 1024 21.1, 19.9, 18.2 and 17.3.
+int pair_width(const MatmulArgs& a) {
+  int best = 0;
+  int64_t least = INT64_MAX;
+  for (const int cols : {256, 224, 192, 160}) {
+    const int64_t tiles = int64_t(a.G) * ((int64_t(a.M) + 255) / 256) * ((int64_t(a.N) + cols - 1) / cols);
+    if (cols == 256 && tiles < kPairTiles) return 0;
+    const int64_t time = (tiles + kSms / 2 - 1) / (kSms / 2) * (256 + cols);
+    if (time < least) {
+      least = time;
+      best = cols;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -776,7 +818,8 @@ cudaError_t launch_fp8_matmul(const MatmulArgs& args, cudaStream_t s) {
   a.n_tiles = int32_t((int64_t(a.N) + 127) / 128);
   const int cols = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
   cudaError_t e = encode_codes(&a.a_map, a.a, a.as, a.G, a.M, a.K, uint32_t(cols));
-  if (e == cudaSuccess) e = encode_codes(&a.b_map, a.b, a.bs, a.G, a.N, a.K, 128);
+  const int width = a.M > 128 ? pair_width(a) : 0;
+  if (e == cudaSuccess) e = encode_codes(&a.b_map, a.b, a.bs, a.G, a.N, a.K, width ? width / 2 : 128);
   if (e != cudaSuccess) return e;
   const uint64_t bytes = a.out_fp32 ? 4 : 2;
   const uint64_t ends = reinterpret_cast<uintptr_t>(a.out) | (uint64_t(a.os.rows) * bytes) |
@@ -788,8 +831,13 @@ cudaError_t launch_fp8_matmul(const MatmulArgs& args, cudaStream_t s) {
     case 64: return launch<true, 64>(a, s);
     default: break;
   }
-  const int64_t pair_tiles = int64_t(a.G) * ((int64_t(a.M) + 255) / 256) * ((int64_t(a.N) + 255) / 256);
-  return a.M > 128 && pair_tiles >= kPairTiles ? launch_pairs(a, s) : launch<false, 128>(a, s);
+  switch (width) {
+    case 160: return launch_pairs<160>(a, s);
+    case 192: return launch_pairs<192>(a, s);
+    case 224: return launch_pairs<224>(a, s);
+    case 256: return launch_pairs<256>(a, s);
+    default: return launch<false, 128>(a, s);
+  }
 }
 
 cudaError_t matmul_error_word(uint32_t* flags, bool clear) {

@@ -242,6 +242,21 @@ def test_batches_in_and_out_of_interleaved_rows(cuda_device, G, M, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("G,M,N,K", [(1, 1500, 3300, 400), (1, 300, 7168, 272), (1, 257, 8400, 300),
+                                     (9, 513, 500, 144), (5, 300, 1000, 1040)])
+def test_each_width_of_the_pairs_tiles(cuda_device, G, M, N, K):
+    """Tiles of 160, 192, 224 and 256 columns, whose weight scales change at
+    other columns than they end; rows and columns past the end untouched."""
+    shape = lambda *s: s if G > 1 else s[1:]  # noqa: E731
+    a, sa = _operand(shape(G, M, K), M + K, 1, cuda_device)
+    b, sb = _operand(shape(G, N, K), N + K, 128, cuda_device)
+    wide = torch.full(shape(G, M + 1, N + 16), 7.0, dtype=torch.bfloat16, device=cuda_device)
+    got = capi.fp8_matmul(a, sa, b, sb, out=wide[..., :M, :N])
+    _check_product(got, a, sa, b, sb)
+    assert torch.all(wide[..., M:, :] == 7) and torch.all(wide[..., N:] == 7)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [3, 40, 150])
 def test_whole_numbers_come_out_exactly(cuda_device, M):
     """Sums of whole numbers below 2^24 are exact in fp32, so any lost bit of
