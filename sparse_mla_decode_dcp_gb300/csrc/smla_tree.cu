@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(32 * kOneCtaWarps) tree_accept_small_kernel(co
     if (b >= a.B) continue;
     int at = 0;
     for (int o = 0; o < b; ++o) at += count[o];
-    for (int k = lane; k < count[b]; k += 32) a.rows[at + k] = first[i] + path[b][k];
+    // (spans that overlap may hold more than T accepted rows)
+    for (int k = lane; k < count[b] && at + k < a.T; k += 32) a.rows[at + k] = first[i] + path[b][k];
   }
   for (int t = total + int(threadIdx.x); t < a.T; t += 32 * kOneCtaWarps) a.rows[t] = -1;
   if (err && lane == 0) atomicOr(&g_tree_error, err);
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps) tree_rows_kernel(const TreeAc
     int32_t n, target;
     const int32_t first = tree_span(a.row_start, b, a.T, kMaxTreeNodes, n, err);
     walk(a, first, n, lane, target, [&](int at, int32_t row) {
-      if (lane == 0) a.rows[before + at] = row;
+      if (lane == 0 && before + at < a.T) a.rows[before + at] = row;  // (spans may overlap)
     });
   }
   for (int64_t t = total + int64_t(blockIdx.x) * 32 * kWalkWarps + threadIdx.x; t < a.T;

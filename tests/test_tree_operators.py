@@ -223,6 +223,23 @@ def test_accept_reports_bad_trees(cuda_device, B):
     assert _err() == capi.DEVERR_TREE
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [5, 101])
+def test_accepted_rows_of_overlapping_spans_stay_inside(cuda_device, B):
+    """Spans that go back over the same rows hold more accepted nodes than there
+    are rows: what is behind the last row stays as it was."""
+    dev, n = cuda_device, 6
+    starts = np.arange(B + 1) % 2 * n  # rows 0 .. 5, then -6 of them, and so on
+    par, z = _i32(np.arange(n) - 1, dev), torch.zeros(n, dtype=torch.int32, device=dev)
+    rows = torch.full((n + 4000,), 77, dtype=torch.int32, device=dev)
+    out = capi.TreeWalk(_i32(np.zeros(B), dev), rows[:n], _i32(np.zeros(B), dev))
+    _err()
+    capi.tree_accept(par, z, z, _i32(starts, dev), out=out)
+    assert _np(out.accepted).tolist() == [n if b % 2 == 0 else 0 for b in range(B)]
+    assert _np(out.rows).tolist() == list(range(n))
+    assert rows[n:].eq(77).all() and _err() == capi.DEVERR_TREE
+
+
 # -------------------------------------------------------------------- move
 @pytest.mark.gpu
 @pytest.mark.parametrize("row", [656, 416])
