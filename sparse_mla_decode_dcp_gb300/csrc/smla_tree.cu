@@ -289,7 +289,7 @@ cudaError_t launch_tree_maps(const TreeMapsArgs& a, cudaStream_t s) {
   int group = 32;
   while (group < a.max_nodes) group *= 2;
   const int64_t per = kMapThreads / group;
-  const unsigned grid = unsigned((a.B + per - 1) / per);
+  const unsigned grid = a.B > 0 ? unsigned((a.B + per - 1) / per) : 1;  // padding rows alone, too
   switch ((a.max_nodes + 63) / 64) {
     case 1: return launch_overlapped(tree_maps_kernel<1>, grid, kMapThreads, 0, s, a, group);
     case 2: return launch_overlapped(tree_maps_kernel<2>, grid, kMapThreads, 0, s, a, group);

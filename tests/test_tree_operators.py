@@ -151,6 +151,18 @@ def test_maps_match_the_definition(cuda_device, B, lo, hi, max_nodes, pad):
 
 
 @pytest.mark.gpu
+def test_no_request_is_all_padding(cuda_device):
+    dev, T = cuda_device, 300
+    par, none, start = _i32(np.full(T, -1), dev), _i32([], dev), _i32([0], dev)
+    out = capi.TreeMaps(torch.full((T, 2), 5, dtype=torch.int64, device=dev), _i32(np.full(T, 5), dev))
+    _err()
+    capi.tree_maps(par, start, none, 100, out=out)
+    walk = capi.tree_accept(par, par, par, start)
+    assert out.masks.eq(0).all() and out.positions.eq(0).all()
+    assert walk.rows.eq(-1).all() and len(walk.accepted) == 0 and _err() == 0
+
+
+@pytest.mark.gpu
 def test_maps_report_bad_trees(cuda_device):
     dev = cuda_device
 
