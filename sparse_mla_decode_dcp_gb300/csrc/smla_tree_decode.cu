@@ -139,18 +139,23 @@ struct SplitTile {
 // runs once a tile each, and past some 128 KB of it warps wait for instructions
 // (waits that read the timer, and every loop unrolled, 154 KB: 5.1 ms for a
 // batch of 32 requests; without 2.6 and less).
-constexpr int kLooks = 1 << 17;
+//
+// All but the list's wait for a place are for work on a few tiles.  That one is
+// for a whole item (2 us a key tile: 2.6 s at 80 M keys), so it looks longer;
+// when the items are not worked on, another wait gives up and ends it.
+constexpr int kLooks = 1 << 17, kLooksForItem = 1 << 28;
 
-__noinline__ __device__ bool look_again(uint64_t* bar, uint32_t parity, volatile int* abort, int site) {
+__noinline__ __device__ bool look_again(uint64_t* bar, uint32_t parity, volatile int* abort, int site, int looks) {
 #pragma unroll 1
-  for (int n = kLooks; n > 0 && *abort == 0; --n)
+  for (int n = looks; n > 0 && *abort == 0; --n)
     if (mbar_try_wait(bar, parity)) return true;
   if (*abort == 0) *abort = site + 1;
   return false;
 }
 
-__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, TreeCtl* ctl, int site) {
-  return mbar_try_wait(bar, parity) || look_again(bar, parity, &ctl->abort, site);
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, TreeCtl* ctl, int site,
+                                          int looks = kLooks) {
+  return mbar_try_wait(bar, parity) || look_again(bar, parity, &ctl->abort, site, looks);
 }
 
 // Of the first n positions, how many pool d holds.
@@ -318,7 +323,7 @@ __device__ void list_work(const TreeDecodeArgs& a, TreeCtl* ctl, int C, int64_t 
       const bool whole = take == per_tile;
       const int slot = item % kItems;
       if (item >= kItems)
-        ok = tree_wait(&ctl->item_empty[slot], (item / kItems - 1) & 1, ctl, kWsRawEmpty);
+        ok = tree_wait(&ctl->item_empty[slot], (item / kItems - 1) & 1, ctl, kWsRawEmpty, kLooksForItem);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
@@ -357,7 +362,8 @@ __device__ void list_work(const TreeDecodeArgs& a, TreeCtl* ctl, int C, int64_t 
   }
   // the end of the list
   const int slot = item % kItems;
-  if (ok && item >= kItems) ok = tree_wait(&ctl->item_empty[slot], (item / kItems - 1) & 1, ctl, kWsRawEmpty);
+  if (ok && item >= kItems)
+    ok = tree_wait(&ctl->item_empty[slot], (item / kItems - 1) & 1, ctl, kWsRawEmpty, kLooksForItem);
   if (__all_sync(0xffffffffu, ok) && lane == 0) {
     ctl->items[slot].rows = 0;
     mbar_arrive(&ctl->item_full[slot]);
@@ -657,16 +663,14 @@ struct Fp8Keys {
         const bool mend = must_mend(ctl, it, now.tile, g);
         uint4 own[kPer];
         float s_own[kPer], s_peer[kPer];
-        float least = INFINITY, most = 0.f;
+        bool plain = !mend;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           own[i] = lds128(k_tile + sw128_offset(first + 2 * i + key, j & 7));
           s_own[i] = scales[own_keys + 2 * i + key];
           s_peer[i] = scales[peer_keys + 2 * i + key];
-          // (a NaN is neither, but most of them is the largest's or one)
-          least = fminf(least, fminf(s_own[i], s_peer[i]));
-          most = s_own[i] <= most ? most : s_own[i];
-          most = s_peer[i] <= most ? most : s_peer[i];
+          plain &= s_own[i] >= 0x1p-10f && s_own[i] <= 65504.f / 448.f;
+          plain &= s_peer[i] >= 0x1p-10f && s_peer[i] <= 65504.f / 448.f;  // (a NaN is neither)
         }
         // chunks in the order this lane stores them
         auto turned = [&](uint4 c) { return swap ? make_uint4(c.z, c.w, c.x, c.y) : c; };
@@ -678,7 +682,7 @@ struct Fp8Keys {
             sts128(v_tile + sw128_offset(peer_keys + 2 * i + key, c), y[s]);
           }
         };
-        if (__all_sync(0xffffffffu, least >= 0x1p-10f && most <= 65504.f / 448.f) && !mend) {
+        if (__all_sync(0xffffffffu, plain)) {
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
             uint4 x[2], y[2];
@@ -704,6 +708,7 @@ struct Fp8Keys {
             any_values(turned(c), s, mend, x);
             any_values(turned(d), s2, mend, y);
             bad |= scale_out_of_range(s) && ((ctl->valid[g & 15] >> (own_keys + 2 * i + key)) & 1);
+            bad |= scale_out_of_range(s2) && ((ctl->valid[g & 15] >> (peer_keys + 2 * i + key)) & 1);
             store(i, x, y);
           }
         }

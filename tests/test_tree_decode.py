@@ -261,6 +261,67 @@ def test_many_short_requests(cuda_device):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("B,most", [(640, 40), (1500, 30), (1290, 700)])
+def test_more_requests_than_a_block_has_threads(cuda_device, fmt, B, most):
+    """Whole and cut row tiles, the longest request among the late ones."""
+    rng = np.random.default_rng(B)
+    nodes, ctx = rng.integers(0, 3, B), rng.integers(0, 30, B)
+    ctx[-7] = most
+    nodes[-7] = 2
+    c = Case(cuda_device, fmt, nodes=nodes.tolist(), ctx=ctx.tolist(), H=3, D=2, bs=16, seed=8).upload()
+    c.check(*c.run())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ctx", [20, 150])
+def test_scales_of_all_sizes(cuda_device, ctx):
+    """8-bit rows whose groups' scales reach from 2^-60 to 2^5, next to each other
+    and a whole tile of small ones."""
+    c = Case(cuda_device, "fp8", nodes=[9], ctx=[ctx], H=16, D=2, bs=16, seed=ctx)
+    rng = np.random.default_rng(2)
+    for pool in c.pools:
+        scale = np.exp2(rng.integers(-60, 6, (len(pool), 4)) * 1.0) * rng.uniform(0.6, 1, (len(pool), 4))
+        scale[:len(pool) // 3] = 2.0 ** -12
+        pool[:, 512:528] = scale.astype("<f4").view(np.uint8)
+    c.upload()
+    _err()
+    c.check(*c.run())
+    assert _err() == capi.DEVERR_RANGE  # the scales below 2^-22, as the header says
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("what", ["scale", "rope", "q"])
+def test_what_is_not_finite_stays_in_its_request(cuda_device, fmt, what):
+    """A prefix row spoils its request's rows, a query its own row."""
+    c = Case(cuda_device, fmt, nodes=[5, 4, 3], ctx=[70, 90, 10], H=16, bs=16, seed=7)
+    spoilt = set(range(5, 9))
+    slot = c.tables[0][1][4] * 16 + 3
+    row = c.pools[0][slot]
+    if what == "scale":
+        if fmt == "fp8":
+            row[520:524] = np.array([np.nan], dtype="<f4").view(np.uint8)
+        else:
+            row[270] = 0x7f
+    elif what == "rope":
+        row[-2:] = (0xc0, 0x7f)  # NaN
+    else:
+        c.q[6, 5, 100] = float("inf")
+        spoilt = {6}
+    c.upload()
+    _err()
+    out, lse = c.run()
+    # 8-bit rows' rope values go to the tensor cores as they are
+    assert _err() == (0 if (fmt, what) == ("fp8", "rope") else capi.DEVERR_RANGE)
+    c.check(out, lse, rows=set(range(c.T)) - spoilt)
+    if what == "q":
+        assert not lse[6, 5].isfinite() and not out[6, 5].isfinite().any()
+    else:
+        assert lse[5:9].isnan().all() and out[5:9].isnan().all()
+
+
+@pytest.mark.gpu
 def test_a_batch_of_uneven_requests(cuda_device):
     c = Case(cuda_device, "fp8", nodes=[16, 5, 30, 1], ctx=[1500, 9000, 10, 4000], H=128, D=4, bs=64, seed=9).upload()
     out, lse = c.run()
