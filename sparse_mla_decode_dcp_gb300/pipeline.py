@@ -119,6 +119,8 @@ class DcpServingStep:
                  cos_sin: Optional[torch.Tensor] = None, rope_pairs: bool = True,
                  sm_scale: float = 192 ** -0.5, interleave: int = 1, max_nodes: int = 0, device="cuda",
                  stream: Optional[torch.cuda.Stream] = None):
+        if not 0 <= max_nodes <= capi.MAX_TREE_NODES:
+            raise ValueError(f"max_nodes must be 0 .. {capi.MAX_TREE_NODES}, got {max_nodes}")
         dev = torch.device(device)
         self.B, self.S, self.H, self.D = num_reqs, tokens_per_req, heads, dcp
         self.block_size, self.interleave, self.max_ctx = block_size, interleave, max_ctx

@@ -306,6 +306,12 @@ def test_rounds_on_a_stream_behind_a_busy_one(cuda_device):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("max_nodes", [-1, 257])
+def test_trees_of_no_size_are_refused(max_nodes):
+    with pytest.raises(ValueError):
+        _server("cpu", "fp8", max_nodes=max_nodes)
+
+
 @pytest.mark.gpu
 def test_drafts_that_a_server_does_not_hold(cuda_device):
     dev = cuda_device
