@@ -907,7 +907,7 @@ __device__ void issue_mmas(uint8_t* sm, TreeCtl* ctl, uint32_t tb, int lane) {
   while (ok && cur.next_item(ctl)) {
     const int n = cur.tiles;
     leave_item(ctl, cur.item, lane);
-    for (int j = 0; j < n + Sm::kProbs; ++j) {
+    for (int j = 0; j <= n; ++j) {
       if (j < n) {
         const int t = g + j, st = t % kSt;
         ok = tree_wait(&ctl->k_full[st], (t / kSt) & 1, ctl, kWsFull);
@@ -950,7 +950,6 @@ __device__ void issue_mmas(uint8_t* sm, TreeCtl* ctl, uint32_t tb, int lane) {
           if (leader) {
             fence_async_shared();  // the copies were generic writes
             groups(0);
-            mma_commit_pair(&ctl->qk[0]);
           }
           __syncwarp();
           ok = __all_sync(0xffffffffu, t == 0 || tree_wait(&ctl->s_read[1], (t - 1) & 1, ctl, kWsSFree));
@@ -962,17 +961,17 @@ __device__ void issue_mmas(uint8_t* sm, TreeCtl* ctl, uint32_t tb, int lane) {
             for (int k = 0; k < 4; ++k)
               mma_ss_f16_pair(tbu + kScoreCol + 128, ad + uint64_t(8 * (kQBlock >> 4) + 2 * k),
                               bd + uint64_t(4 * (kKBlock >> 4) + 2 * k), rope_desc, k > 0);
-            mma_commit_pair(&ctl->qk[1]);
+            mma_commit_pair(&ctl->qk[0]);
           }
         }
         if (leader) mma_commit_pair(&ctl->k_free[st]);
         __syncwarp();
       }
-      if (j >= Sm::kProbs) {
-        const int t = g + j - Sm::kProbs, pb = t % Sm::kProbs;
+      if (j > 0) {
+        const int t = g + j - 1, pb = t % Sm::kProbs;
         ok = tree_wait(&ctl->v_full[t & 1], (t >> 1) & 1, ctl, kWsFull) &&
              tree_wait(&ctl->p_full[pb], (t / Sm::kProbs) & 1, ctl, kWsPFull) &&
-             (j > Sm::kProbs || cur.item == 0 || tree_wait(&ctl->out_read, (cur.item - 1) & 1, ctl, kWsSFree));
+             (j > 1 || cur.item == 0 || tree_wait(&ctl->out_read, (cur.item - 1) & 1, ctl, kWsSFree));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -985,7 +984,7 @@ __device__ void issue_mmas(uint8_t* sm, TreeCtl* ctl, uint32_t tb, int lane) {
             for (int i = 0; i < 2; ++i)
               mma_ss_f16_pair(tbu + kOutCol + 128 * i, ad + 2 * k,
                               sdesc_sw128(v + 2 * i * kVBlock, kVBlock, 1024) + uint64_t(k * (2048 >> 4)), pv_desc,
-                              j > Sm::kProbs || k > 0);
+                              j > 1 || k > 0);
           mma_commit_pair(&ctl->pv[t & 1]);
         }
         __syncwarp();
@@ -1052,12 +1051,13 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
         a.masks + (live ? int64_t(it.keys.first) + (it.skip + row) / a.H : it.keys.first) * a.mask_words;
     float m_ref = -INFINITY, l = 0.f;  // log2 domain
     float c2 = a.sm_scale * kLog2e;
-    for (int j = 0; j < n; ++j, ++g) {
+    const int prefix = it.keys.prefix;
+    int first = it.tile0 * kTileKeys + kCtaKeys * half + 16 * part;  // key of s[0]
+    for (int j = 0; j < n; ++j, ++g, first += kTileKeys) {
       const int b = g & 1;
       const uint32_t scores = lanes + kScoreCol + 16 * part;
-      const int first = (it.tile0 + j) * kTileKeys + kCtaKeys * half + 16 * part;  // key of s[0]
       // the mask's words are on their way while the scores are computed
-      const uint32_t seen = first + 16 > it.keys.prefix ? seen_from(mask, a.mask_words, first - it.keys.prefix) : 0xffffu;
+      const uint32_t seen = first + 16 > prefix ? seen_from(mask, a.mask_words, first - prefix) : 0xffffu;
       uint32_t s[16];
       if constexpr (F::kFp4) {
         ok = __all_sync(0xffffffffu, tree_wait(&ctl->qk[b], (g >> 1) & 1, ctl, kWsSFull));
@@ -1069,40 +1069,48 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
         __syncwarp();
         if (lane == 0) mbar_arrive_at(s_read + 8 * b);
       } else {
-        // sum = scores of groups 0, 1 by their scales, then of 2, 3 and the rope
+        // sum = scores of groups 0, 1 by their scales, then of 2, 3 and the rope;
+        // the scales are asked for while the scores are on their way
         uint64_t sum[8];
-        auto add = [&](const uint32_t* x, int q, bool set) {
-          const float4* sc = reinterpret_cast<const float4*>(&ctl->scales[g & 3][q][kCtaKeys * half + 16 * part]);
+        uint32_t x[2][16];
+        float4 f[2][4];
+        auto scales = [&](int q) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 f = sc[k];
-            sum[2 * k] = fma2(pack2(x[4 * k], x[4 * k + 1]), pack2(f.x, f.y), set ? 0 : sum[2 * k]);
-            sum[2 * k + 1] = fma2(pack2(x[4 * k + 2], x[4 * k + 3]), pack2(f.z, f.w), set ? 0 : sum[2 * k + 1]);
+          for (int i = 0; i < 2; ++i) {
+            const float4* sc = reinterpret_cast<const float4*>(&ctl->scales[g & 3][q + i][kCtaKeys * half + 16 * part]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[i][k] = sc[k];
           }
         };
-        uint32_t x[2][16];
+        auto add = [&](int i, bool set) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            sum[2 * k] = fma2(pack2(x[i][4 * k], x[i][4 * k + 1]), pack2(f[i][k].x, f[i][k].y), set ? 0 : sum[2 * k]);
+            sum[2 * k + 1] =
+                fma2(pack2(x[i][4 * k + 2], x[i][4 * k + 3]), pack2(f[i][k].z, f[i][k].w), set ? 0 : sum[2 * k + 1]);
+          }
+        };
         ok = __all_sync(0xffffffffu, tree_wait(&ctl->qk[0], g & 1, ctl, kWsSFull));
         if (!ok) break;
         if (j == 0) c2 *= ctl->row_scale[cur.item & 1][r];
         tc_fence_after();
         tmem_ld16(scores, x[0]);
         tmem_ld16(scores + 32, x[1]);
+        scales(0);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_at(s_read);
-        add(x[0], 0, true);
-        add(x[1], 1, false);
-        ok = __all_sync(0xffffffffu, tree_wait(&ctl->qk[1], g & 1, ctl, kWsSFull));
-        if (!ok) break;
-        tc_fence_after();
+        add(0, true);
+        add(1, false);
         tmem_ld16(scores + 64, x[0]);
         tmem_ld16(scores + 96, x[1]);
         tmem_ld16(scores + 128, s);
+        scales(2);
         tmem_ld_wait();
         tc_fence_before();
-        add(x[0], 2, false);
-        add(x[1], 3, false);
+        add(0, false);
+        add(1, false);
         __syncwarp();
         if (lane == 0) mbar_arrive_at(s_read + 8);  // the scales have been read, too
 #pragma unroll
@@ -1124,33 +1132,41 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
       ctl->tops[b][tid] = top;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->top[b]);
-      ok = __all_sync(0xffffffffu, tree_wait(&ctl->top[b], (g >> 1) & 1, ctl, kWsExchange));
-      if (!ok) break;
-      top = fmaxf(fmaxf(ctl->tops[b][r], ctl->tops[b][64 + r]), fmaxf(ctl->tops[b][128 + r], ctl->tops[b][192 + r])) * c2;
-      float alpha = 1.f;
-      const bool moves = top > m_ref + 8.f;
-      if (moves) {
-        alpha = ex2(m_ref - top);
-        m_ref = top;
-      }
-      const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-      float sum = 0.f;
+      // p by the reference so far, while the maxima travel; once more by the new
+      // one if a row's has moved
+      float alpha = 1.f, sum;
       uint32_t p[8];
+      bool any_moves = false;
+#pragma unroll 1
+      for (;;) {
+        const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+        sum = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float x = ex2(fmaf(__uint_as_float(s[2 * k]), c2, -ref));
-        const float y = ex2(fmaf(__uint_as_float(s[2 * k + 1]), c2, -ref));
-        sum += x + y;
-        p[k] = h2_bits(__floats2half2_rn(x, y));
+        for (int k = 0; k < 8; ++k) {
+          const float x = ex2(fmaf(__uint_as_float(s[2 * k]), c2, -ref));
+          const float y = ex2(fmaf(__uint_as_float(s[2 * k + 1]), c2, -ref));
+          sum += x + y;
+          p[k] = h2_bits(__floats2half2_rn(x, y));
+        }
+        if (any_moves) break;
+        ok = __all_sync(0xffffffffu, tree_wait(&ctl->top[b], (g >> 1) & 1, ctl, kWsExchange));
+        if (!ok) break;
+        top = fmaxf(fmaxf(ctl->tops[b][r], ctl->tops[b][64 + r]), fmaxf(ctl->tops[b][128 + r], ctl->tops[b][192 + r])) * c2;
+        const bool moves = top > m_ref + 8.f;
+        any_moves = __any_sync(0xffffffffu, moves);
+        if (!any_moves) break;
+        if (moves) {
+          alpha = ex2(m_ref - top);
+          m_ref = top;
+        }
       }
+      if (!ok) break;
       l = l * alpha + sum;
       // the output moves once PV of the tile before has been added to it; P's
       // place is free once PV of its last tile has read it
-      const bool any = j > 0 && __any_sync(0xffffffffu, moves);
+      const bool any = j > 0 && any_moves;
       if (any || (F::kFp4 && j > 0))
         ok = __all_sync(0xffffffffu, tree_wait(&ctl->pv[b ^ 1], ((g - 1) >> 1) & 1, ctl, kWsPvDone));
-      if (!F::kFp4 && ok && g >= 2)
-        ok = __all_sync(0xffffffffu, tree_wait(&ctl->pv[b], ((g >> 1) - 1) & 1, ctl, kWsPvDone));
       if (!ok) break;
       if (any) {
         tc_fence_after();
