@@ -136,7 +136,10 @@ enum {
  * subnormals and lose precision).  The result is still written; the bit says
  * it may be outside the stated tolerances.  An fp4 row's latent values are
  * exact in the kernel's keys and its rope values within 2^-18; for those rows
- * the bit stands for the q and rope values and for a NaN scale. */
+ * the bit stands for the q and rope values and for a NaN scale.
+ * smla_dcp_tree_mla_decode takes 8-bit rows' codes and rope values, and q, as
+ * they are into QK^T, so that there the bit stands for a scale as above (of
+ * the values) and for a q that is not finite; over 4-bit rows it is as above. */
 /* With SMLA_DEVERR_TIMEOUT, bits 8..29 of the word tell which of the decode
  * kernel's internal waits gave up (a diagnostic bitmask, one bit per site). */
 
@@ -730,8 +733,11 @@ smla_status smla_tree_maps(const int32_t* parents, const int32_t* row_start,
  *     The slots may be a smla_dcp_step_maps call's (the drafts lie where their
  *     positions' blocks are) or rows outside every block (a scratch area, from
  *     which smla_mla_cache_move brings the accepted ones).
- * with the attention of smla_sparse_mla_decode over those cache rows.  A row
- * with nothing to attend is written as (0, -inf).  Rows of out and lse that
+ * with the attention of smla_sparse_mla_decode over those cache rows.  Over
+ * 8-bit rows the scores are sums of exact products (of q's latent values those
+ * below 2^-10 of the row's largest are taken to within 2^-17 of it), scaled in
+ * fp32, so lse is good to fp32 sums; values and probabilities round to fp16.
+ * A row with nothing to attend is written as (0, -inf).  Rows of out and lse that
  * belong to no request (behind row_start[B], padding) are left as they were.
  *
  *   q              device bf16 [T, H, 576], 16-byte aligned

@@ -712,8 +712,6 @@ cudaError_t encode_codes(CUtensorMap* map, const uint8_t* p, const Strides& st, 
 }
 
 constexpr int kSms = 152;
-// tiles from which pairs take them
-constexpr int64_t kPairTiles = 38;
 
 template <bool kSwap, int kCols>
 cudaError_t launch(MatmulArgs& a, cudaStream_t s) {
@@ -735,6 +733,8 @@ cudaError_t launch(MatmulArgs& a, cudaStream_t s) {
   a.m_tiles = int32_t((int64_t(a.M) + (kSwap ? kCols : kLaneRows) - 1) / (kSwap ? kCols : kLaneRows));
   const int64_t tiles = int64_t(a.G) * a.m_tiles * a.n_tiles;
   a.tiles = uint32_t(tiles);
+  // few tiles: 1 x 576 x 2048 takes 6.4 us by a CTA a tile, 4.0 by clusters; 64 x
+  // 576 x 7168 28.6 and 7.7, 128 x 512 x 16384 60.2 and 13.2
   a.splits = 1;
   while (a.splits < kMaxSplits && tiles * a.splits * 2 <= kSms && a.k_blocks >= 4 * a.splits) a.splits *= 2;
   const int per_split = (a.k_blocks + a.splits - 1) / a.splits;
@@ -790,17 +790,21 @@ cudaError_t launch_pairs(MatmulArgs& a, cudaStream_t s) {
   return launch_overlapped(fp8_matmul_pair_kernel<kCols>, 2 * pairs, kPairThreads, kPairSmem<kCols>, s, a);
 }
 
-// The pairs' tile width, 0 for a call with too few tiles: the one whose rounds
-// of 76 tiles bring the least bytes, 128 + cols / 2 rows a CTA.  4001 x 4096 x
+// The pairs' tile width, 0 for a call whose tiles of 128 x 128 are so few that
+// clusters share a tile's groups (300 x 2048 x 2048, 48 tiles: 9.5 us so, 9.9 by
+// pairs; 130 x 4096 x 7168, 64: 18.8, 23.6; 512 x 2560 x 2048, 80: 10.3, 9.8;
+// 1024 x 2048 x 7168, 128: 28.9, 24.2; 512 x 6144 x 7168, 192: 56.8, 25.2).
+// Else the one whose rounds of 76 tiles bring the least bytes, 128 + cols / 2
+// rows a CTA.  4001 x 4096 x
 // 16384 takes 222 us with 256 columns, 217 with 224, 248 with 192 and 280 with
 // 160; 4096 x 7168 x 2048 57.5, 62.4, 66.1 and 75.0; 300 x 7168 x 16384 57.6,
 // 56.2, 53.1 and 95.3; 2000 x 3000 x 1024 21.1, 19.9, 18.2 and 17.3.
 int pair_width(const MatmulArgs& a) {
+  if (int64_t(a.G) * ((int64_t(a.M) + 127) / 128) * a.n_tiles <= kSms / 2) return 0;
   int best = 0;
   int64_t least = INT64_MAX;
   for (const int cols : {256, 224, 192, 160}) {
     const int64_t tiles = int64_t(a.G) * ((int64_t(a.M) + 255) / 256) * ((int64_t(a.N) + cols - 1) / cols);
-    if (cols == 256 && tiles < kPairTiles) return 0;
     const int64_t time = (tiles + kSms / 2 - 1) / (kSms / 2) * (256 + cols);
     if (time < least) {
       least = time;
@@ -816,6 +820,8 @@ cudaError_t launch_fp8_matmul(const MatmulArgs& args, cudaStream_t s) {
   MatmulArgs a = args;
   a.k_blocks = int32_t((int64_t(a.K) + kGroup - 1) / kGroup);
   a.n_tiles = int32_t((int64_t(a.N) + 127) / 128);
+  // 16 rows through 24576 x 1536 take 6.4 us with tiles of 16 columns, 11.6 with
+  // 64 and 16.3 along the lanes; 32 rows 7.1, 9.6 and 15.6; 64 rows 10.0 and 16.5
   const int cols = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
   cudaError_t e = encode_codes(&a.a_map, a.a, a.as, a.G, a.M, a.K, uint32_t(cols));
   const int width = a.M > 128 ? pair_width(a) : 0;

@@ -85,7 +85,7 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
 // behind this thread's writes to its own CTA's shared memory.  The release is
 // the CTA's: nothing but such writes and tensor-memory accesses is handed over.
 // (At cluster scope it waits for every load in flight: 6 us a tile of the tree
-// decode instead of 1.)
+// decode instead of 2.)
 __device__ __forceinline__ void mbar_arrive_at(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
 }

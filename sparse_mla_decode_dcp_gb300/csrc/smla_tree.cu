@@ -3,7 +3,9 @@
 // accepted nodes' cache rows going from their drafts' slots to their own.
 //
 // All three move a few bytes a node and are bound by launch and memory
-// latency, so each does its work in as few dependent steps as it can.
+// latency, so each does its work in as few dependent steps as it can.  64 trees
+// of 16 nodes: 3.0 us for the maps of a call among others (4,096 of up to 64
+// nodes: 3.9); walk, move and a gather of 512 rows 9.4 us.
 #include "../../include/smla.h"
 #include "smla_verify.h"
 
@@ -129,7 +131,9 @@ __device__ __forceinline__ int walk(const TreeAcceptArgs& a, int32_t first, int3
 }
 
 // Up to kOneCta requests: one CTA, whose warps keep their paths in shared
-// memory while the counts before them are summed.
+// memory while the counts before them are summed (1, 32 and 64 requests of 16
+// nodes: 2.0, 4.9 and 7.0 us, with walks of up to 16 steps; by the two launches
+// below 3.5, 5.9 and 7.4).
 constexpr int kOneCta = 64;
 constexpr int kOneCtaWarps = 32;
 
