@@ -39,16 +39,16 @@
 //     tile that a cut falls into leaves partial results (fp16, with their
 //     maximum and sum), which a second kernel merges.
 //
-// A key tile takes 1.8 us of a pair (8-bit rows; 4-bit ones 1.9): a batch of 32
-// requests of 16 nodes, 128 heads and 2,048 to 32,768 positions 2.19 ms, 740
+// A key tile takes 1.7 us of a pair (8-bit rows; 4-bit ones 1.9): a batch of 32
+// requests of 16 nodes, 128 heads and 2,048 to 32,768 positions 2.02 ms, 800
 // TFLOP/s.  Its MMAs alone take 0.75 us.  What bounds it is the shared-memory data
-// pipe, 95% of its time busy (62% for the warps: value tiles, scales, copies; 34%
-// for the tensor cores' operands; 4-bit rows 88%), and so the softmax, a chain of
-// steps that each wait in it: fewer dependent steps helped (scales asked for
-// with the scores, one wait a tile, exponentials while the maxima travel: 2.44
-// ms before), less traffic at the cost of longer chains did not (a quarter of the
-// scale loads by tensor-memory fragments and shuffles: 2.65; rows gathered by
-// TMA, 128 bytes a piece: 2.88).
+// pipe, nearly always busy (two thirds for the warps: value tiles, scales,
+// copies; a third for the tensor cores' operands), and so the softmax, a chain of
+// steps that each wait in it: fewer dependent steps helped (scales asked for with
+// the scores, one wait a tile, exponentials while the maxima travel: 2.18 ms
+// after 2.44), and so did less code (below), less traffic at the cost of longer
+// chains did not (a quarter of the scale loads by tensor-memory fragments and
+// shuffles: 2.65; rows gathered by TMA, 128 bytes a piece: 2.88).
 //
 // Warps: 0-7 softmax and output (two threads a lane of tensor memory), 8-15
 // convert cache rows, 16 issues the MMAs (the first CTA's, for both; the
@@ -147,9 +147,10 @@ struct SplitTile {
 // suspends the thread for up to kSuspendNs (2.6 s in all), or when another wait
 // of the CTA has; the first to do so leaves its site in ctl->abort, which the
 // CTA reports at its end.  A few instructions a wait matter: the roles' code
-// runs once a tile each, and past some 128 KB of it warps wait for instructions
-// (waits that read the timer, and every loop unrolled, 154 KB: 5.1 ms for a
-// batch of 32 requests; without 2.6 and less).
+// runs once a tile each, and from some 90 KB of it on warps wait for
+// instructions (the batch of 32 requests above: 5.1 ms with waits that read the
+// timer and every loop unrolled, 154 KB; 2.18 with 102 KB, 2.02 with 91, whose
+// loops that run once a launch or an item are not unrolled).
 //
 // All but the list's wait for a place are for work on a few tiles.  That one is
 // for a whole item (2 us a key tile: 2.6 s at 80 M keys), so it looks longer;
@@ -319,7 +320,7 @@ __device__ void list_work(const TreeDecodeArgs& a, TreeCtl* ctl, int C, int64_t 
     const int32_t held =
         r.prefix >= 0 && lane < a.D && (a.rank < 0 || lane == a.rank) ? pool_rows(a, r.prefix, lane) : 0;
     int32_t upto = held;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < kMaxMerge; o <<= 1) {
       const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += x;
@@ -943,31 +944,27 @@ __device__ void issue_mmas(uint8_t* sm, TreeCtl* ctl, uint32_t tb, int lane) {
         } else {
           // Groups of 128 codes, 32 an MMA, in two halves, so that the
           // softmax reads the one while the other is made.
-          auto groups = [&](int q0) {
 #pragma unroll 1
-            for (int q = q0; q < q0 + 2; ++q) {
-              const uint64_t qd = ad + uint64_t(q * (kQBlock >> 4)), kd = bd + uint64_t(q * (kKBlock >> 4));
+          for (int h = 0; h < 2; ++h) {
+            ok = __all_sync(0xffffffffu, ok && (t == 0 || tree_wait(&ctl->s_read[h], (t - 1) & 1, ctl, kWsSFree)));
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+              if (h == 0) fence_async_shared();  // the copies were generic writes
+#pragma unroll 1
+              for (int q = 2 * h; q < 2 * h + 2; ++q) {
+                const uint64_t qd = ad + uint64_t(q * (kQBlock >> 4)), kd = bd + uint64_t(q * (kKBlock >> 4));
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                mma_ss_f8_pair(tbu + kScoreCol + 32 * q, qd + 2 * k, kd + 2 * k, qk_desc, k > 0);
-                mma_ss_f8_pair(tbu + kScoreCol + 32 * q, qd + 4 * (kQBlock >> 4) + 2 * k, kd + 2 * k, qk_desc, 1);
+                for (int k = 0; k < 4; ++k) {
+                  mma_ss_f8_pair(tbu + kScoreCol + 32 * q, qd + 2 * k, kd + 2 * k, qk_desc, k > 0);
+                  mma_ss_f8_pair(tbu + kScoreCol + 32 * q, qd + 4 * (kQBlock >> 4) + 2 * k, kd + 2 * k, qk_desc, 1);
+                }
               }
             }
-          };
-          ok = ok && (t == 0 || tree_wait(&ctl->s_read[0], (t - 1) & 1, ctl, kWsSFree));
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          if (leader) {
-            fence_async_shared();  // the copies were generic writes
-            groups(0);
+            __syncwarp();
           }
-          __syncwarp();
-          ok = __all_sync(0xffffffffu, t == 0 || tree_wait(&ctl->s_read[1], (t - 1) & 1, ctl, kWsSFree));
           if (!ok) break;
-          tc_fence_after();
           if (leader) {
-            groups(2);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_ss_f16_pair(tbu + kScoreCol + 128, ad + uint64_t(8 * (kQBlock >> 4) + 2 * k),
@@ -1317,6 +1314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
   // thread, and the later ones (of batches past the block's threads) in turn
   unsigned err = 0;
   int64_t v = 0, later = 0;
+#pragma unroll 1
   for (int32_t b = tid; b < a.B; b += kTreeThreads) {
     const Request r = load_request(a, b, err);
     const int64_t n = int64_t(row_tiles(a, r)) * tile_units(a, r);
@@ -1344,6 +1342,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
   const int64_t pairs = gridDim.x >> 1;
   const int64_t per_pair = max(quotient(units + pairs - 1, pairs), int64_t(a.min_units));
   const int64_t u0 = per_pair * (blockIdx.x >> 1);
+#pragma unroll 1
   for (int32_t b0 = 0;;) {
     if (begin <= u0 && u0 < begin + v) {
       ctl->start_req = b0 + tid;
@@ -1359,7 +1358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
       v = int64_t(row_tiles(a, r)) * tile_units(a, r);
     }
     upto = v;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += x;
@@ -1368,6 +1367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
     if (lane == 31) ctl->warp_units[warp] = upto;
     __syncthreads();
     begin = base + upto - v;
+#pragma unroll 1
     for (int w = 0; w < kTreeWarps; ++w) {
       if (w < warp) begin += ctl->warp_units[w];
       base += ctl->warp_units[w];
