@@ -314,10 +314,11 @@ class Fp8Projections:
     def query(self, x: torch.Tensor, positions: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Queries [T, H, 576] of rows x [T, C], in the latent space; their
         last 64 values rotated by cos_sin[positions] if this has a table (as
-        mla_cache_write rotates a row's)."""
+        mla_cache_write rotates a row's; a position outside it takes its
+        nearest entry, where that call reports an error)."""
         T, H, P = self._count(x.shape[0]), self.H, self.P
         heads, q = self.heads[:T], self.q[:T]
-        self._product(x, self._rows(self.x8, T), self.w_q, heads.view(T, -1))
+        self._product(x, self._rows(self.x8, T), self.w_q, heads.view(T, H * (P + self.rope)))
         self._product(heads[..., :P].transpose(0, 1), self._rows(self.part8, T), self.w_k,
                       q[..., :capi.V_DIM].transpose(0, 1))
         with torch.cuda.stream(self.stream):
@@ -325,7 +326,8 @@ class Fp8Projections:
             if self.cos_sin is None:
                 to.copy_(z)
             else:
-                c, s = self.cos_sin[positions.long()][:, None].chunk(2, -1)
+                at = positions.long().clamp(0, self.cos_sin.shape[0] - 1)
+                c, s = self.cos_sin[at][:, None].chunk(2, -1)
                 half = self.rope // 2
                 a, b = ((z[..., 0::2], z[..., 1::2]) if self.rope_pairs else (z[..., :half], z[..., half:]))
                 to_a, to_b = ((to[..., 0::2], to[..., 1::2]) if self.rope_pairs
@@ -340,4 +342,4 @@ class Fp8Projections:
         T = self._count(latent.shape[0])
         values = self.values[:T]
         self._product(latent.transpose(0, 1), self._rows(self.latent8, T), self.w_v, values.transpose(0, 1))
-        return self._product(values.view(T, -1), self._rows(self.values8, T), self.w_o, self.y[:T])
+        return self._product(values.view(T, self.H * self.V), self._rows(self.values8, T), self.w_o, self.y[:T])

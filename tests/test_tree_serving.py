@@ -146,6 +146,42 @@ def test_projections_match_their_definition(cuda_device, T, rope_pairs):
 
 
 @pytest.mark.gpu
+def test_projections_of_no_rows_and_of_positions_past_the_table(cuda_device):
+    p = _projections(cuda_device)
+    n = len(p.cos_sin)
+    assert p.query(_bf16((0, 200), 1, cuda_device), _i32([], cuda_device)).shape == (0, H, 576)
+    assert p.output(_bf16((0, H, 512), 1, cuda_device)).shape == (0, p.E)
+    x = _bf16((4, 200), 2, cuda_device)
+    got = p.query(x, _i32([n, -1, 2 ** 31 - 1, 5], cuda_device)).clone()
+    assert torch.equal(got, p.query(x, _i32([n - 1, 0, n - 1, 5], cuda_device)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_no_drafts_change_nothing(cuda_device, fmt):
+    """Trees of no nodes, all padding or no rows at all: nothing is accepted,
+    the cache and its block tables stay as they were."""
+    dev, ctx = cuda_device, [90, 5, 40]
+    step = _ready(dev, fmt, ctx)
+    keep = _cached(step, ctx)
+    pre, rs = _i32(ctx, dev), _i32([0] * (B + 1), dev)
+    _err()
+    for T in (7, 0):
+        par = _i32([-1] * T, dev)
+        step.tree_out.fill_(3)
+        out, lse = step.verify(pre, par, rs, _bf16((T, 576), 1, dev), _bf16((T, H, 576), 2, dev))
+        assert out.shape == (T, H, 512) and out.eq(3).all()
+        walk, after = step.commit(pre, par, par, par, rs)
+        assert walk.accepted.eq(0).all() and walk.rows.eq(-1).all() and walk.next_tokens.eq(-1).all()
+        assert torch.equal(after, pre)
+        assert all(int(t) == 0 for t in step._taken)
+        step.take_blocks()
+    for a, b in zip(_cached(step, ctx), keep):
+        assert np.array_equal(a, b)
+    assert _err() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
 def test_drafting_server(cuda_device, fmt):
     """Prefill, then rounds of trees: each part within its definition's bounds,
