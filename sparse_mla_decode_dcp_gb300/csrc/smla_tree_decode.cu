@@ -152,9 +152,10 @@ struct SplitTile {
 // timer and every loop unrolled, 154 KB; 2.18 with 102 KB, 2.02 with 91, whose
 // loops that run once a launch or an item are not unrolled).
 //
-// All but the list's wait for a place are for work on a few tiles.  That one is
-// for a whole item (2 us a key tile: 2.6 s at 80 M keys), so it looks longer;
-// when the items are not worked on, another wait gives up and ends it.
+// All but those of the list for a place and for the list's next item are for
+// work on a few tiles.  Those are for a whole item (2 us a key tile: 2.6 s at 80
+// M keys), so they look longer; when the items are not worked on, another wait
+// gives up and ends them.
 constexpr int kLooks = 1 << 17, kLooksForItem = 1 << 28;
 
 __noinline__ __device__ bool look_again(uint64_t* bar, uint32_t parity, volatile int* abort, int site, int looks) {
@@ -283,7 +284,7 @@ struct Cursor {
   __device__ __forceinline__ bool next_item(TreeCtl* ctl) {
     ++item;
     tile = 0;
-    const bool ok = tree_wait(&ctl->item_full[item % kItems], (item / kItems) & 1, ctl, kWsRaw);
+    const bool ok = tree_wait(&ctl->item_full[item % kItems], (item / kItems) & 1, ctl, kWsRaw, kLooksForItem);
     end = !__all_sync(0xffffffffu, ok) || at(ctl).rows == 0;
     tiles = end ? 0 : at(ctl).tiles;
     return !end;
