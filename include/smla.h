@@ -801,7 +801,7 @@ smla_status smla_dcp_tree_mla_decode(
  * misaligned arrays; UNSUPPORTED for B > SMLA_MAX_STEP_REQS.  B = 0 and T = 0
  * is a no-op.  On the device a request of more than SMLA_MAX_TREE_NODES rows,
  * or with rows outside [0, T), counts as empty and sets SMLA_DEVERR_TREE.
- * Above 64 requests the call is two launches, the second with programmatic
+ * Above 32 requests the call is two launches, the second with programmatic
  * stream serialisation behind the first.
  */
 smla_status smla_tree_accept(const int32_t* parents, const int32_t* tokens, const int32_t* targets,

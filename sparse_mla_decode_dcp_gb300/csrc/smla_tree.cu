@@ -5,7 +5,7 @@
 // All three move a few bytes a node and are bound by launch and memory
 // latency, so each does its work in as few dependent steps as it can.  64 trees
 // of 16 nodes: 3.0 us for the maps of a call among others (4,096 of up to 64
-// nodes: 3.9); walk, move and a gather of 512 rows 9.4 us.
+// nodes: 3.9); walk, move and a gather of 512 rows 7.9 us.
 #include "../../include/smla.h"
 #include "smla_verify.h"
 
@@ -92,88 +92,89 @@ __global__ void __launch_bounds__(kMapThreads) tree_maps_kernel(const TreeMapsAr
 // One warp walks one tree: from node 0, the accepted one, to the lowest child
 // whose token is the model's, and so on.  `visit(i, row)` is called by every
 // lane for the i-th accepted row; returns their number and the last one's
-// target.  A lane holds the nodes lane, lane + 32, ... in registers.
+// target.  Every node's way on is found at once (a lane looks at the nodes lane,
+// lane + 32, ... as children), so that a step of the walk is one load from shared
+// memory: `next` [kMaxTreeNodes] is the warp's, 0 where a node has no way on.
+// 64 chains of 64 nodes, four of five tokens right: 21.2 us when each step looked
+// for its child by ballots, 8.6 so.
 template <class Visit>
-__device__ __forceinline__ int walk(const TreeAcceptArgs& a, int32_t first, int32_t n, int lane,
+__device__ __forceinline__ int walk(const TreeAcceptArgs& a, int32_t first, int32_t n, int lane, uint8_t* next,
                                     int32_t& target, Visit visit) {
   constexpr int kPer = kMaxTreeNodes / 32;
+  target = -1;
+  if (n == 0) return 0;
   int32_t parent[kPer], token[kPer], goal[kPer];
+  __syncwarp();  // the last walk's reads
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int j = 32 * k + lane;
-    const bool in = j < n;
-    parent[k] = in ? a.parents[first + j] : -1;
-    token[k] = in ? a.tokens[first + j] : 0;
-    goal[k] = in ? a.targets[first + j] : 0;
+    parent[k] = j < n ? a.parents[first + j] : -1;
+    if (parent[k] >= j) parent[k] = -1;  // not a node before
+    token[k] = j < n ? a.tokens[first + j] : 0;
+    if (32 * k < n) next[j] = 0;
   }
-  target = -1;
-  if (n == 0) return 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) goal[k] = parent[k] >= 0 ? a.targets[first + parent[k]] : 0;
+#pragma unroll
+  for (int k = kPer - 1; k >= 0; --k) {  // the lowest child's is the last to be written
+    if (32 * k >= n) continue;
+    const bool fits = parent[k] >= 0 && token[k] == goal[k];
+    const unsigned same = __match_any_sync(0xffffffffu, fits ? parent[k] : -1 - lane);
+    __syncwarp();
+    if (fits && lane == __ffs(same) - 1) next[parent[k]] = uint8_t(32 * k + lane);
+  }
+  __syncwarp();
   int cur = 0, count = 0;
   while (true) {
     visit(count, first + cur);
     ++count;
-    int32_t t = goal[0];
-#pragma unroll
-    for (int k = 1; k < kPer; ++k) t = (cur >> 5) == k ? goal[k] : t;
-    target = __shfl_sync(0xffffffffu, t, cur & 31);
-    int next = -1;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      if (32 * k >= n || next >= 0) continue;
-      const int j = 32 * k + lane;
-      const unsigned fits =
-          __ballot_sync(0xffffffffu, j > cur && j < n && parent[k] == cur && token[k] == target);
-      if (fits) next = 32 * k + __ffs(fits) - 1;
-    }
-    if (next < 0) return count;
-    cur = next;
+    const int to = next[cur];
+    if (to == 0) break;
+    cur = to;
   }
+  target = a.targets[first + cur];
+  return count;
 }
 
-// Up to kOneCta requests: one CTA, whose warps keep their paths in shared
-// memory while the counts before them are summed (1, 32 and 64 requests of 16
-// nodes: 2.0, 4.9 and 7.0 us, with walks of up to 16 steps; by the two launches
-// below 3.5, 5.9 and 7.4).
-constexpr int kOneCta = 64;
-constexpr int kOneCtaWarps = 32;
+// Up to kOneCta requests: one CTA, a warp each, whose paths stay in shared memory
+// while the counts before them are summed.  1, 16 and 32 requests of 16 nodes:
+// 2.1, 2.8 and 3.5 us, by the two launches below 3.8, 4.7 and 4.8; 64 (two a
+// warp) 5.8 and 5.0.
+constexpr int kOneCta = 32;
 
-__global__ void __launch_bounds__(32 * kOneCtaWarps) tree_accept_small_kernel(const TreeAcceptArgs a) {
-  __shared__ uint8_t path[kOneCta][kMaxTreeNodes];
+__global__ void __launch_bounds__(32 * kOneCta) tree_accept_small_kernel(const TreeAcceptArgs a) {
+  __shared__ uint8_t path[kOneCta][kMaxTreeNodes], next[kOneCta][kMaxTreeNodes];
   __shared__ int count[kOneCta];
-  const int warp = threadIdx.x >> 5;
+  const int b = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   griddep_launch_dependents();
   griddep_wait();
   unsigned err = 0;
-  int32_t first[kOneCta / kOneCtaWarps];
-#pragma unroll
-  for (int i = 0; i < kOneCta / kOneCtaWarps; ++i) {
-    const int b = warp + kOneCtaWarps * i;
-    first[i] = 0;
-    if (b >= a.B) continue;
+  int32_t first = 0, accepted = 0;
+  if (b < a.B) {
     int32_t n, target;
-    first[i] = tree_span(a.row_start, b, a.T, kMaxTreeNodes, n, err);
-    const int c = walk(a, first[i], n, lane, target,
-                       [&](int at, int32_t row) { path[b][at] = uint8_t(row - first[i]); });
+    first = tree_span(a.row_start, b, a.T, kMaxTreeNodes, n, err);
+    accepted = walk(a, first, n, lane, next[b], target,
+                    [&](int at, int32_t row) { path[b][at] = uint8_t(row - first); });
     if (lane == 0) {
-      count[b] = c;
-      a.accepted[b] = c;
+      a.accepted[b] = accepted;
       a.next_tokens[b] = target;
     }
   }
+  if (lane == 0) count[b] = accepted;
   __syncthreads();
-  int total = 0;
-  for (int b = 0; b < a.B; ++b) total += count[b];
+  // every warp sums all counts
+  int upto = count[lane];
 #pragma unroll
-  for (int i = 0; i < kOneCta / kOneCtaWarps; ++i) {
-    const int b = warp + kOneCtaWarps * i;
-    if (b >= a.B) continue;
-    int at = 0;
-    for (int o = 0; o < b; ++o) at += count[o];
-    // (spans that overlap may hold more than T accepted rows)
-    for (int k = lane; k < count[b] && at + k < a.T; k += 32) a.rows[at + k] = first[i] + path[b][k];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
   }
-  for (int t = total + int(threadIdx.x); t < a.T; t += 32 * kOneCtaWarps) a.rows[t] = -1;
+  const int total = __shfl_sync(0xffffffffu, upto, 31);
+  const int at = __shfl_sync(0xffffffffu, upto, b) - accepted;
+  // (spans that overlap may hold more than T accepted rows)
+  for (int k = lane; k < accepted && at + k < a.T; k += 32) a.rows[at + k] = first + path[b][k];
+  for (int t = total + int(threadIdx.x); t < a.T; t += 32 * kOneCta) a.rows[t] = -1;
   if (err && lane == 0) atomicOr(&g_tree_error, err);
 }
 
@@ -182,6 +183,7 @@ __global__ void __launch_bounds__(32 * kOneCtaWarps) tree_accept_small_kernel(co
 constexpr int kWalkWarps = 8;
 
 __global__ void __launch_bounds__(32 * kWalkWarps) tree_count_kernel(const TreeAcceptArgs a) {
+  __shared__ uint8_t next[kWalkWarps][kMaxTreeNodes];
   const int lane = threadIdx.x & 31;
   const int b = int(blockIdx.x) * kWalkWarps + (threadIdx.x >> 5);
   griddep_launch_dependents();
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps) tree_count_kernel(const TreeA
   unsigned err = 0;
   int32_t n, target;
   const int32_t first = tree_span(a.row_start, b, a.T, kMaxTreeNodes, n, err);
-  const int c = walk(a, first, n, lane, target, [](int, int32_t) {});
+  const int c = walk(a, first, n, lane, next[threadIdx.x >> 5], target, [](int, int32_t) {});
   if (lane == 0) {
     a.accepted[b] = c;
     a.next_tokens[b] = target;
@@ -200,6 +202,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps) tree_count_kernel(const TreeA
 
 __global__ void __launch_bounds__(32 * kWalkWarps) tree_rows_kernel(const TreeAcceptArgs a) {
   __shared__ int s_before[kWalkWarps], s_total[kWalkWarps];
+  __shared__ uint8_t next[kWalkWarps][kMaxTreeNodes];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int b0 = int(blockIdx.x) * kWalkWarps;
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps) tree_rows_kernel(const TreeAc
     unsigned err = 0;
     int32_t n, target;
     const int32_t first = tree_span(a.row_start, b, a.T, kMaxTreeNodes, n, err);
-    walk(a, first, n, lane, target, [&](int at, int32_t row) {
+    walk(a, first, n, lane, next[warp], target, [&](int at, int32_t row) {
       if (lane == 0 && before + at < a.T) a.rows[before + at] = row;  // (spans may overlap)
     });
   }
@@ -303,7 +306,7 @@ cudaError_t launch_tree_maps(const TreeMapsArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t s) {
-  if (a.B <= kOneCta) return launch_overlapped(tree_accept_small_kernel, 1, 32 * kOneCtaWarps, 0, s, a);
+  if (a.B <= kOneCta) return launch_overlapped(tree_accept_small_kernel, 1, 32 * kOneCta, 0, s, a);
   const unsigned grid = unsigned((a.B + kWalkWarps - 1) / kWalkWarps);
   const cudaError_t e = launch_overlapped(tree_count_kernel, grid, 32 * kWalkWarps, 0, s, a);
   if (e != cudaSuccess) return e;

@@ -217,6 +217,31 @@ def test_a_chain_of_every_node_is_walked_to_its_end(cuda_device):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B", [1, 31, 32, 33])
+def test_walks_of_wide_and_deep_trees(cuda_device, B):
+    """Around the number of requests that one launch takes: many children with
+    the same token, the lowest of them far behind others' children; parents
+    that are no nodes before them."""
+    rng = np.random.default_rng(B)
+    starts, parents = _trees(rng, B, 200, 256, ("bushy", "chain", "star"))
+    T = len(parents)
+    inner = np.arange(T) - np.repeat(starts[:-1], np.diff(starts))  # node numbers
+    far = rng.random(T) < 0.3  # children of any node before, not of the nearest
+    parents = np.where(far & (inner > 0), rng.integers(0, np.maximum(inner, 1)), parents)
+    wrong = (rng.random(T) < 0.1) & (inner > 0)  # themselves, a later node, below -1
+    bad = np.where(wrong, np.where(rng.random(T) < 0.5, inner + rng.integers(0, 3, T), -2), parents)
+    tokens, targets = rng.integers(0, 2, T), rng.integers(0, 2, T)
+    got = capi.tree_accept(*(_i32(v, cuda_device) for v in (bad, tokens, targets, starts)))
+    want = to.tree_accept(np.where(wrong, -1, parents), tokens, targets, starts, T)
+    for x, y in zip(got, want):
+        assert np.array_equal(_np(x), y)
+    assert B == 1 or max(want[0]) > 3  # the walks go somewhere
+    got = capi.tree_accept(*(_i32(v, cuda_device) for v in (np.arange(T) - 1 - np.repeat(starts[:-1], np.diff(starts)),
+                                                            0 * tokens, 0 * tokens, starts)))
+    assert np.array_equal(_np(got.accepted), np.diff(starts)) and np.array_equal(_np(got.rows), np.arange(T))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("B", [3, 100])
 def test_accept_reports_bad_trees(cuda_device, B):
     """A tree too large or out of the rows counts as empty."""
