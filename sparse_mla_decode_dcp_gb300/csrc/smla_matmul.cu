@@ -712,6 +712,15 @@ cudaError_t encode_codes(CUtensorMap* map, const uint8_t* p, const Strides& st, 
 }
 
 constexpr int kSms = 152;
+// Clusters of CTAs, one an SM, that are resident together (as
+// cudaOccupancyMaxActiveClusters tells): one more waits for a whole tile of
+// another's (100 x 2048 x 2048, 16 tiles: 13.7 us by clusters of eight, of
+// which 15 fit, 7.2 by four; 1 x 2112 x 7168, 17 tiles: 10.8 and 7.1).
+constexpr int clusters_that_fit(int ctas) { return ctas == 2 ? 76 : ctas == 4 ? 36 : 15; }
+// Groups from which a tile's are split (64 x 4096 x 512, 4 groups: 5.6 us by
+// clusters of two, 4.2 by one CTA; x 1024, 8 groups: 6.0 and 6.2; 1 x 2048 x 1024
+// 3.8 and 4.2).
+constexpr int kLeastSplit = 8;
 
 template <bool kSwap, int kCols>
 cudaError_t launch(MatmulArgs& a, cudaStream_t s) {
@@ -736,7 +745,9 @@ cudaError_t launch(MatmulArgs& a, cudaStream_t s) {
   // few tiles: 1 x 576 x 2048 takes 6.4 us by a CTA a tile, 4.0 by clusters; 64 x
   // 576 x 7168 28.6 and 7.7, 128 x 512 x 16384 60.2 and 13.2
   a.splits = 1;
-  while (a.splits < kMaxSplits && tiles * a.splits * 2 <= kSms && a.k_blocks >= 4 * a.splits) a.splits *= 2;
+  while (a.splits < kMaxSplits && tiles <= clusters_that_fit(2 * a.splits) && a.k_blocks >= kLeastSplit &&
+         a.k_blocks >= 4 * a.splits)
+    a.splits *= 2;
   const int per_split = (a.k_blocks + a.splits - 1) / a.splits;
   // two CTAs an SM along the columns: one's loads run while the other starts or
   // ends
