@@ -742,16 +742,21 @@ cudaError_t launch(MatmulArgs& a, cudaStream_t s) {
   a.m_tiles = int32_t((int64_t(a.M) + (kSwap ? kCols : kLaneRows) - 1) / (kSwap ? kCols : kLaneRows));
   const int64_t tiles = int64_t(a.G) * a.m_tiles * a.n_tiles;
   a.tiles = uint32_t(tiles);
+  // Two CTAs an SM along the columns: one's loads run while the other starts or
+  // ends, and each of its groups' way through the tensor core and back (64 x 7168
+  // x 7168 in 112 CTAs of 28 groups 18.2 us, in 224 of 14 13.7; 64 x 18432 x 7168
+  // 40.5 and 30.8).  Clusters that fit without have all of the shared memory (64 x
+  // 4096 x 7168, 32 of four: 11.4 us with 7 stages, 12.6 with 3).
+  constexpr int kPerSm = kSwap ? 2 : 1;
   // few tiles: 1 x 576 x 2048 takes 6.4 us by a CTA a tile, 4.0 by clusters; 64 x
   // 576 x 7168 28.6 and 7.7, 128 x 512 x 16384 60.2 and 13.2
   a.splits = 1;
-  while (a.splits < kMaxSplits && tiles <= clusters_that_fit(2 * a.splits) && a.k_blocks >= kLeastSplit &&
+  while (a.splits < kMaxSplits && tiles <= kPerSm * clusters_that_fit(2 * a.splits) && a.k_blocks >= kLeastSplit &&
          a.k_blocks >= 4 * a.splits)
     a.splits *= 2;
   const int per_split = (a.k_blocks + a.splits - 1) / a.splits;
-  // two CTAs an SM along the columns: one's loads run while the other starts or
-  // ends
-  const int most = (kSwap && a.splits == 1 ? kMaxSmem / 2 : kMaxSmem) / S::kStageBytes;
+  const bool shared = kSwap && (a.splits == 1 || tiles > clusters_that_fit(a.splits));
+  const int most = (shared ? kMaxSmem / 2 : kMaxSmem) / S::kStageBytes;
   const int64_t total = tiles > kSms * 2 ? (tiles + 2 * kSms - 1) / (2 * kSms) * per_split : per_split;
   a.stages = int(total < most ? total : most);
   const int64_t ctas = kSwap && a.splits == 1 && tiles > 2 * kSms ? 2 * kSms : tiles * a.splits;
