@@ -122,12 +122,11 @@ __device__ __forceinline__ uint64_t timer_ns() {
 // flag, so that its other roles stop waiting too, and `*error` gets `bit`.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
-template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
                                              unsigned* error, unsigned bit) {
-  if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = timer_ns();
-  while (!(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
+  while (!mbar_try_wait(bar, parity)) {
     if (*abort) return false;
     if (timer_ns() - t0 > kWaitLimitNs) {
       atomicOr(error, bit);

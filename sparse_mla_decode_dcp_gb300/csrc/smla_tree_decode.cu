@@ -87,7 +87,8 @@ template <bool kFp4> struct Shared {
   static constexpr int kOffV = kQSize + kStages * kKSize;
   static constexpr int kOffP = kOffV + 2 * kVSize;
   static constexpr int kPSize = kCtaRows * 128;
-  // P tiles, and how many tiles PV stays behind QK^T
+  // P tiles.  PV is issued behind QK^T of the next tile, so that with two a
+  // tile's scores tell that PV of the tile two before has read its P
   static constexpr int kProbs = kFp4 ? 1 : 2;
   static constexpr int kOffCtl = kOffP + kProbs * kPSize;
 };
@@ -115,8 +116,8 @@ struct Item {
 };
 
 struct TreeCtl {
-  // qk, s_read: fp8 rows, of the scores of groups 0 and 1 and of the rest; fp4
-  // rows, of even and odd tiles' scores
+  // s_read: fp8 rows, of the scores of groups 0 and 1 and of the rest (qk: [0], of
+  // all); both, fp4 rows: of even and odd tiles' scores
   uint64_t qk[2], s_read[2], pv[2], k_free[3], k_full[3], k_read[3], k_peer[3], v_full[2], q_full, p_full[2],
       out_read, top[2], sum, item_full[kItems], item_empty[kItems], place_full[kPlaces], place_empty[kPlaces], end;
   uint32_t tbase;
@@ -943,8 +944,8 @@ __device__ void issue_mmas(uint8_t* sm, TreeCtl* ctl, uint32_t tb, int lane) {
             mma_commit_pair(&ctl->qk[t & 1]);
           }
         } else {
-          // Groups of 128 codes, 32 an MMA, in two halves, so that the
-          // softmax reads the one while the other is made.
+          // Groups of 128 codes, 32 an MMA, in two halves: the first is made
+          // while the softmax reads the second of the tile before.
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             ok = __all_sync(0xffffffffu, ok && (t == 0 || tree_wait(&ctl->s_read[h], (t - 1) & 1, ctl, kWsSFree)));
@@ -1171,8 +1172,8 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
       }
       if (!ok) break;
       l = l * alpha + sum;
-      // the output moves once PV of the tile before has been added to it; P's
-      // place is free once PV of its last tile has read it
+      // the output moves once PV of the tile before has been added to it; so is
+      // P's place free then, where there is one
       const bool any = j > 0 && any_moves;
       if (any || (F::kFp4 && j > 0))
         ok = __all_sync(0xffffffffu, tree_wait(&ctl->pv[b ^ 1], ((g - 1) >> 1) & 1, ctl, kWsPvDone));
