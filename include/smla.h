@@ -48,6 +48,8 @@
  *                                     from the nodes' parents
  *   smla_dcp_tree_mla_decode          attention of a tree's nodes over the
  *                                     cached prefix and each other
+ *   smla_dcp_tree_window_mla_decode   the same limited to a sliding window
+ *                                     and a few first tokens (sinks)
  *   smla_tree_accept                  the nodes the model agrees with
  *   smla_mla_cache_move               their cache rows, to their own slots
  *
@@ -137,7 +139,7 @@ enum {
  * it may be outside the stated tolerances.  An fp4 row's latent values are
  * exact in the kernel's keys and its rope values within 2^-18; for those rows
  * the bit stands for the q and rope values and for a NaN scale.
- * smla_dcp_tree_mla_decode takes 8-bit rows' codes and rope values, and q, as
+ * The tree decodes take 8-bit rows' codes and rope values, and q, as
  * they are into QK^T, so that there the bit stands for a scale as above (of
  * the values) and for a q that is not finite; over 4-bit rows it is as above. */
 /* With SMLA_DEVERR_TIMEOUT, bits 8..29 of the word tell which of the decode
@@ -780,6 +782,33 @@ smla_status smla_dcp_tree_mla_decode(
     int32_t format, const uint8_t* const* kv_caches, const int64_t* num_slots,
     const int32_t* const* block_tables, const int64_t* bt_row_strides, const int32_t* bt_widths,
     uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The same with a window and sinks, for a model whose steps run through
+ * smla_dcp_window_mla_decode: a node at position p = positions[its row] attends
+ * of the keys above those at positions t with t < sinks or t > p - window,
+ * where a prefix key's t is its place in the request and a drafted node's its
+ * own position.  A chain of nodes attends what smla_dcp_window_mla_decode gives
+ * the same tokens.  Only the block-table entries and cache rows of positions
+ * that a node at the prefix's end attends are read: blocks behind that window
+ * may have been given back.
+ *
+ *   positions    device int32 [T], as smla_tree_maps writes them: the prefix's
+ *                length plus the node's depth (outside [prefix_lens[b],
+ *                prefix_lens[b] + max_nodes) it counts as the nearest of these)
+ *   window       >= 1 (from max_prefix + max_nodes on nothing is left out)
+ *   sinks        >= 0
+ *   the rest     as for smla_dcp_tree_mla_decode; its workspace size serves
+ * Errors: as smla_dcp_tree_mla_decode, plus INVALID_ARG for window < 1, sinks <
+ * 0 and NULL or misaligned positions.
+ */
+smla_status smla_dcp_tree_window_mla_decode(
+    const uint16_t* q, int32_t T, int32_t H, float sm_scale, const int32_t* row_start,
+    const int32_t* prefix_lens, const int32_t* positions, int32_t B, int32_t max_prefix, const uint64_t* masks,
+    int32_t max_nodes, int32_t window, int32_t sinks, const int32_t* const* draft_slots, int32_t D, int32_t rank,
+    int32_t block_size, int32_t interleave, int32_t format, const uint8_t* const* kv_caches,
+    const int64_t* num_slots, const int32_t* const* block_tables, const int64_t* bt_row_strides,
+    const int32_t* bt_widths, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * smla_tree_accept walks each tree greedily: node 0 is accepted, and from an

@@ -106,6 +106,10 @@ SIGNATURES = {
         _c_vp, _c_i32, _c_i32, ctypes.c_float, _c_vp, _c_vp, _c_i32, _c_i32, _c_vp, _c_i32, _c_vp,
         _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp,
         _c_vp, _c_sz, _c_vp]),
+    "smla_dcp_tree_window_mla_decode": (ctypes.c_int, [
+        _c_vp, _c_i32, _c_i32, ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_i32, _c_i32, _c_vp, _c_i32, _c_i32,
+        _c_i32, _c_vp, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp,
+        _c_vp, _c_vp, _c_sz, _c_vp]),
     "smla_tree_accept": (ctypes.c_int, [
         _c_vp, _c_vp, _c_vp, _c_vp, _c_i32, _c_i32, _c_vp, _c_vp, _c_vp, _c_vp]),
     "smla_mla_cache_move": (ctypes.c_int, [
@@ -814,6 +818,8 @@ def dcp_tree_mla_decode(q: torch.Tensor, row_start: torch.Tensor, prefix_lens: t
                         kv_caches: Sequence[Optional[torch.Tensor]],
                         block_tables: Sequence[Optional[torch.Tensor]], block_size: int,
                         sm_scale: float, *, rank: int = -1, interleave: int = 1,
+                        window: Optional[int] = None, sinks: int = 0,
+                        positions: Optional[torch.Tensor] = None,
                         bt_widths: Optional[Sequence[int]] = None,
                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                         workspace: Optional[torch.Tensor] = None,
@@ -823,8 +829,13 @@ def dcp_tree_mla_decode(q: torch.Tensor, row_start: torch.Tensor, prefix_lens: t
     requests' cached prefixes and the nodes their masks name, over 8- or 4-bit
     pools: merged over the D pools (rank = -1) or one rank's partial (only its
     pool, table and draft slots are read).  draft_slots[d] [T]: each node's
-    slot in pool d, -1 where it is not held.  Rows of no request are left as
-    they were (uninitialised in an `out` and `lse` allocated here)."""
+    slot in pool d, -1 where it is not held.  With a `window`, a node at
+    positions[its row] (as tree_maps writes them) attends of these only the
+    keys at the last `window` positions up to its own and at the request's
+    first `sinks`, as dcp_window_mla_decode does.  Rows of no request are left
+    as they were (uninitialised in an `out` and `lse` allocated here)."""
+    if window is not None and positions is None:
+        raise ValueError("a window needs the nodes' positions")
     if out is None or lse is None:
         out, lse = _out_lse(q, out, lse, stream)
     if workspace is None and q.dim() == 3:
@@ -834,7 +845,7 @@ def dcp_tree_mla_decode(q: torch.Tensor, row_start: torch.Tensor, prefix_lens: t
     _check("smla_dcp_tree_mla_decode",
            _native().decode_tree(q, row_start, prefix_lens, max_prefix, masks, max_nodes, draft_slots,
                                  kv_caches, block_tables, block_size, sm_scale, rank, interleave,
-                                 bt_widths, out, lse, workspace, stream))
+                                 bt_widths, out, lse, workspace, stream, window, sinks, positions))
     return out, lse
 
 

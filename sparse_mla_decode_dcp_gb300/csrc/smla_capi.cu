@@ -584,10 +584,11 @@ size_t smla_tree_decode_workspace_size(int32_t T, int32_t H, int32_t B, int32_t 
   return smla::tree_decode_workspace_bytes(T, B, H, tree_keys(max_prefix, max_nodes, D, interleave, rank));
 }
 
-smla_status smla_dcp_tree_mla_decode(
+// Both forms; window 0: the whole prefix.
+static smla_status tree_decode(
     const uint16_t* q, int32_t T, int32_t H, float sm_scale, const int32_t* row_start,
-    const int32_t* prefix_lens, int32_t B, int32_t max_prefix, const uint64_t* masks, int32_t max_nodes,
-    const int32_t* const* draft_slots, int32_t D, int32_t rank, int32_t block_size, int32_t interleave,
+    const int32_t* prefix_lens, const int32_t* positions, int32_t B, int32_t max_prefix, const uint64_t* masks,
+    int32_t max_nodes, int32_t window, int32_t sinks, const int32_t* const* draft_slots, int32_t D, int32_t rank, int32_t block_size, int32_t interleave,
     int32_t format, const uint8_t* const* kv_caches, const int64_t* num_slots,
     const int32_t* const* block_tables, const int64_t* bt_row_strides, const int32_t* bt_widths,
     uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
@@ -602,7 +603,8 @@ smla_status smla_dcp_tree_mla_decode(
       !block_tables || !bt_row_strides || !bt_widths || !out || !lse)
     return SMLA_ERR_INVALID_ARG;
   if (misaligned(q, 16) || misaligned(out, 16) || misaligned(lse, 4) || misaligned(row_start, 4) ||
-      misaligned(prefix_lens, 4) || misaligned(masks, 8))
+      misaligned(prefix_lens, 4) || misaligned(masks, 8) ||
+      (window > 0 && (!positions || misaligned(positions, 4))))
     return SMLA_ERR_INVALID_ARG;
   smla::TreeDecodeArgs a{};
   for (int d = 0; d < D; ++d) {
@@ -618,7 +620,10 @@ smla_status smla_dcp_tree_mla_decode(
     a.bt_width[d] = bt_widths[d];
     a.draft_slots[d] = draft_slots[d];
   }
-  const int64_t keys = tree_keys(max_prefix, max_nodes, D, interleave, rank);
+  // a window that no node's position reaches past shuts out nothing
+  if (int64_t(window) >= int64_t(max_prefix) + max_nodes) window = 0;
+  const int64_t keys = window > 0 ? int64_t(window_entries(max_prefix, window, sinks, D, interleave, rank)) + max_nodes
+                                  : tree_keys(max_prefix, max_nodes, D, interleave, rank);
   const size_t need = smla::tree_decode_workspace_bytes(T, B, H, keys);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || misaligned(workspace, 256)))
     return SMLA_ERR_WORKSPACE;
@@ -633,6 +638,9 @@ smla_status smla_dcp_tree_mla_decode(
   a.masks = masks;
   a.max_nodes = max_nodes;
   a.mask_words = (max_nodes + 63) / 64;
+  a.positions = positions;
+  a.window = window;
+  a.sinks = sinks;
   a.D = D;
   a.rank = rank;
   a.block_size = block_size;
@@ -642,6 +650,31 @@ smla_status smla_dcp_tree_mla_decode(
   a.workspace = workspace;
   a.workspace_bytes = workspace_bytes;
   return from_cuda(smla::launch_tree_decode(a, keys, format == SMLA_CACHE_FP4, static_cast<cudaStream_t>(stream)));
+}
+
+smla_status smla_dcp_tree_mla_decode(
+    const uint16_t* q, int32_t T, int32_t H, float sm_scale, const int32_t* row_start,
+    const int32_t* prefix_lens, int32_t B, int32_t max_prefix, const uint64_t* masks, int32_t max_nodes,
+    const int32_t* const* draft_slots, int32_t D, int32_t rank, int32_t block_size, int32_t interleave,
+    int32_t format, const uint8_t* const* kv_caches, const int64_t* num_slots,
+    const int32_t* const* block_tables, const int64_t* bt_row_strides, const int32_t* bt_widths,
+    uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return tree_decode(q, T, H, sm_scale, row_start, prefix_lens, nullptr, B, max_prefix, masks, max_nodes, 0, 0,
+                     draft_slots, D, rank, block_size, interleave, format, kv_caches, num_slots, block_tables,
+                     bt_row_strides, bt_widths, out, lse, workspace, workspace_bytes, stream);
+}
+
+smla_status smla_dcp_tree_window_mla_decode(
+    const uint16_t* q, int32_t T, int32_t H, float sm_scale, const int32_t* row_start,
+    const int32_t* prefix_lens, const int32_t* positions, int32_t B, int32_t max_prefix, const uint64_t* masks,
+    int32_t max_nodes, int32_t window, int32_t sinks, const int32_t* const* draft_slots, int32_t D, int32_t rank,
+    int32_t block_size, int32_t interleave, int32_t format, const uint8_t* const* kv_caches,
+    const int64_t* num_slots, const int32_t* const* block_tables, const int64_t* bt_row_strides,
+    const int32_t* bt_widths, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (window < 1 || sinks < 0) return SMLA_ERR_INVALID_ARG;
+  return tree_decode(q, T, H, sm_scale, row_start, prefix_lens, positions, B, max_prefix, masks, max_nodes, window,
+                     sinks, draft_slots, D, rank, block_size, interleave, format, kv_caches, num_slots, block_tables,
+                     bt_row_strides, bt_widths, out, lse, workspace, workspace_bytes, stream);
 }
 
 smla_status smla_tree_accept(const int32_t* parents, const int32_t* tokens, const int32_t* targets,

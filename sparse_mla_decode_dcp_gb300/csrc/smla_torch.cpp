@@ -413,9 +413,9 @@ PyObject* tree_maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // (q, row_start, prefix_lens, max_prefix, masks, max_nodes, draft_slots,
 //  kv_caches, block_tables, block_size, sm_scale, rank, interleave, bt_widths,
-//  out, lse, workspace, stream)
+//  out, lse, workspace, stream, window or None, sinks, positions (with a window))
 PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 18, [&] {
+  return guarded(n, 21, [&] {
     const Query q = query_of(a[0], a[14], a[15], a[16]);
     const at::Tensor& prefix = vec(a[2], "prefix_lens", at::kInt, q.dev, -1);
     const int32_t B = size32(prefix.size(0), "prefix_lens");
@@ -432,6 +432,16 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* slots[SMLA_MAX_DCP] = {};
     for (int32_t d = 0; d < p.D; ++d)
       if (rank < 0 || d == rank) slots[d] = ptr<int32_t>(vec(drafts[d], "draft_slots[d]", at::kInt, q.dev, q.T));
+    if (a[18] != Py_None) {
+      const int32_t window = i32(a[18]), sinks = i32(a[19]);
+      const at::Tensor& positions = vec(a[20], "positions", at::kInt, q.dev, q.T);
+      return launch(q.dev, a[17], [&](void* s) {
+        return smla_dcp_tree_window_mla_decode(
+            q.q, q.T, q.H, scale, ptr<int32_t>(starts), ptr<int32_t>(prefix), ptr<int32_t>(positions), B, max_prefix,
+            ptr<uint64_t>(masks), nodes, window, sinks, slots, p.D, rank, bs, I, p.format, p.kv, p.slots, p.bt,
+            p.stride, p.width, q.out, q.lse, q.ws, q.ws_bytes, s);
+      });
+    }
     return launch(q.dev, a[17], [&](void* s) {
       return smla_dcp_tree_mla_decode(q.q, q.T, q.H, scale, ptr<int32_t>(starts), ptr<int32_t>(prefix), B,
                                       max_prefix, ptr<uint64_t>(masks), nodes, slots, p.D, rank, bs, I, p.format,

@@ -5,7 +5,8 @@
 // its positions, or all pools') and those nodes of its tree that its mask
 // names and some pool holds:
 //   s_k = sm_scale <q, k>,  lse = ln sum exp s_k,  out = sum exp(s_k - lse) latent_k
-// A row with no key is written as (0, -inf).
+// A row with no key is written as (0, -inf).  A windowed call's row, at position
+// p, attends of these the keys at positions t < sinks and t > p - window.
 //
 // Design (a cluster of two CTAs works on 128 rows and 64 keys at a time):
 //   * A request's rows, its nodes times the heads, share its keys, so they are
@@ -34,6 +35,11 @@
 //   * Masks are looked at in the tiles that hold nodes or missing rows; a
 //     node's row that is not finite is kept out of the value tile (its score
 //     spoils the rows that see it), so that masked places do not show.
+//   * With a window the list of a request's keys leaves out the positions that
+//     none of its nodes sees: a key has the last position that sees it, and only
+//     tiles with keys that some node no longer sees compare.  The batch below with
+//     a window of 4,096 and 4 sinks: 0.82 ms; with one that leaves out a node's
+//     last few keys alone 2.34 (the look-up of a key's row and the code cost 15%).
 //   * All requests' (row tile, key tile) units form one line that is cut into
 //     equal ranges, one a pair, so that ragged batches fill the GPU.  A row
 //     tile that a cut falls into leaves partial results (fp16, with their
@@ -103,6 +109,10 @@ struct Keys {
   int32_t first, nodes;           // the request's rows (no nodes when its prefix is out of range)
   int32_t before[kMaxMerge + 1];  // prefix keys before pool d
   int32_t prefix, total;
+  int32_t length;                 // the prefix's positions (more than its keys, with a window)
+  // windowed calls: of pool d's rows its listed keys are the first sinks and, from
+  // row sinks + gap on, those in the window; rows from edge on are seen by every node
+  int32_t sinks[kMaxMerge], gap[kMaxMerge], edge[kMaxMerge];
 };
 
 // A row tile of a request over a range of its key tiles.
@@ -123,6 +133,11 @@ struct TreeCtl {
   uint32_t tbase;
   int abort;
   uint64_t valid[16];                     // per tile (mod 16): which of its keys exist
+  // windowed calls, per tile: the last position that sees a key, counted from the
+  // prefix's end (255: every node does), and the first of these.  (A tile's are
+  // written when PV of the tile seven before is done.)
+  alignas(16) uint8_t until[8][kTileKeys];
+  int32_t soonest[16];
   const uint8_t* row[kPlaces][kTileKeys];  // the keys' cache rows
   float row_scale[2][kCtaRows];           // fp8 rows, per item (mod 2): a row's score times this is its own
   float tops[2][32 * kSoftWarps], sums[32 * kSoftWarps];
@@ -179,12 +194,39 @@ __device__ __forceinline__ int32_t pool_rows(const TreeDecodeArgs& a, int32_t n,
   return full * a.interleave + int32_t(min(max(rest, int64_t(0)), int64_t(a.interleave)));
 }
 
+// A windowed call lists, of a prefix's positions, the first sinks and those in
+// the window of a node that follows the prefix directly: from here on.
+__device__ __forceinline__ int32_t window_start(const TreeDecodeArgs& a, int32_t prefix) {
+  return max(prefix - a.window + 1, min(a.sinks, prefix));
+}
+
+// Keys of a prefix that are listed of pool d.
+template <bool kWindow>
+__device__ __forceinline__ int32_t pool_keys(const TreeDecodeArgs& a, int32_t prefix, int32_t d) {
+  const int32_t n = pool_rows(a, prefix, d);
+  if (!kWindow) return n;
+  return pool_rows(a, min(a.sinks, prefix), d) + n - pool_rows(a, window_start(a, prefix), d);
+}
+
+// The last position that sees a listed key at position t, counted from the
+// prefix's end at `length` (nodes' positions are less than 256 past it).
+__device__ __forceinline__ int32_t seen_until(const TreeDecodeArgs& a, int32_t t, int32_t length) {
+  return t < a.sinks ? 255 : int32_t(min(int64_t(t) + a.window - 1 - length, int64_t(255)));
+}
+
+// A node's position counted from there: as given, where a tree of max_nodes
+// nodes may have it.
+__device__ __forceinline__ int32_t node_position(const TreeDecodeArgs& a, int32_t row, int32_t length) {
+  return min(max(a.positions[row], length), length + a.max_nodes - 1) - length;
+}
+
 // What a request brings: its rows and keys.  No rows (and an error bit) when
 // they lie outside T or are too many; no keys when its prefix is out of range.
 struct Request {
   int32_t first, nodes, prefix, keys;  // prefix: as given, -1 when out of range
 };
 
+template <bool kWindow>
 __device__ __forceinline__ Request load_request(const TreeDecodeArgs& a, int32_t b, unsigned& err) {
   Request r;
   r.first = a.row_start[b];
@@ -198,7 +240,8 @@ __device__ __forceinline__ Request load_request(const TreeDecodeArgs& a, int32_t
     if (rows_ok && n > 0) err |= SMLA_DEVERR_CONTEXT;
     r.prefix = -1;
   } else {
-    r.keys = (a.rank < 0 ? r.prefix : pool_rows(a, r.prefix, a.rank)) + r.nodes;
+    const int32_t listed = kWindow ? min(a.sinks, r.prefix) + r.prefix - window_start(a, r.prefix) : r.prefix;
+    r.keys = (a.rank < 0 ? listed : pool_keys<kWindow>(a, r.prefix, a.rank)) + r.nodes;
   }
   return r;
 }
@@ -224,9 +267,11 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
 // A key's place while its table entry is on the way.
 struct Place {
   int32_t d, offset, entry;
+  int32_t until;  // windowed calls
   bool prefix, live;
 };
 
+template <bool kWindow>
 __device__ __forceinline__ Place find_key(const TreeDecodeArgs& a, const Keys& keys, int32_t req, int32_t i) {
   Place p;
   p.live = i < keys.total;
@@ -234,10 +279,19 @@ __device__ __forceinline__ Place find_key(const TreeDecodeArgs& a, const Keys& k
   p.d = max(a.rank, 0);
   p.offset = 0;
   p.entry = -1;
+  p.until = 255;
   if (p.prefix) {
     if (a.rank < 0)
       while (i >= keys.before[p.d + 1]) ++p.d;
-    const int32_t lp = i - keys.before[p.d];
+    int32_t lp = i - keys.before[p.d];
+    if (kWindow && lp >= keys.sinks[p.d]) {
+      lp += keys.gap[p.d];
+      if (lp < keys.edge[p.d]) {
+        const int32_t round = int32_t(uint32_t(lp) / uint32_t(a.interleave));
+        const int64_t t = (int64_t(round) * a.D + p.d) * a.interleave + (lp - round * a.interleave);
+        p.until = seen_until(a, int32_t(t), keys.length);
+      }
+    }
     const int32_t col = int32_t(fastdiv(uint32_t(lp), a.div_bs));
     p.offset = lp - col * a.block_size;
     if (col < a.bt_width[p.d]) p.entry = a.bts[p.d][req * a.bt_stride[p.d] + col];
@@ -246,6 +300,7 @@ __device__ __forceinline__ Place find_key(const TreeDecodeArgs& a, const Keys& k
     p.entry = a.draft_slots[p.d][row];
     if (a.rank < 0)
       while (p.entry < 0 && p.d + 1 < a.D) p.entry = a.draft_slots[++p.d][row];
+    if (kWindow) p.until = seen_until(a, keys.length + node_position(a, row, keys.length), keys.length);
   }
   return p;
 }
@@ -302,6 +357,7 @@ __device__ __forceinline__ void leave_item(TreeCtl* ctl, int item, int lane) {
 }
 
 // ---------------------------------------------------------------- work list
+template <bool kWindow>
 __device__ void list_work(const TreeDecodeArgs& a, TreeCtl* ctl, int C, int64_t units, int64_t per_pair,
                           int lane) {
   const int pair = int(blockIdx.x >> 1);
@@ -315,12 +371,12 @@ __device__ void list_work(const TreeDecodeArgs& a, TreeCtl* ctl, int C, int64_t 
   bool ok = true;
   while (ok && u < u_end && req < a.B) {
     unsigned ignored = 0;
-    const Request r = load_request(a, req, ignored);
+    const Request r = load_request<kWindow>(a, req, ignored);
     const int32_t per_tile = tile_units(a, r);
     const int64_t all = int64_t(row_tiles(a, r)) * per_tile;
     // this lane's pool and the prefix keys up to it
     const int32_t held =
-        r.prefix >= 0 && lane < a.D && (a.rank < 0 || lane == a.rank) ? pool_rows(a, r.prefix, lane) : 0;
+        r.prefix >= 0 && lane < a.D && (a.rank < 0 || lane == a.rank) ? pool_keys<kWindow>(a, r.prefix, lane) : 0;
     int32_t upto = held;
 #pragma unroll 1
     for (int o = 1; o < kMaxMerge; o <<= 1) {
@@ -345,6 +401,12 @@ __device__ void list_work(const TreeDecodeArgs& a, TreeCtl* ctl, int C, int64_t 
       Item& it = ctl->items[slot];
       if (lane < a.D) it.keys.before[lane] = a.rank < 0 ? upto - held : 0;
       if (lane == a.D - 1) it.keys.before[a.D] = upto;
+      if (kWindow && lane < a.D && r.prefix >= 0) {
+        const int32_t start = window_start(a, r.prefix);
+        it.keys.sinks[lane] = pool_rows(a, min(a.sinks, r.prefix), lane);
+        it.keys.gap[lane] = pool_rows(a, start, lane) - it.keys.sinks[lane];
+        it.keys.edge[lane] = pool_rows(a, min(max(start, r.prefix - a.window + a.max_nodes), r.prefix), lane);
+      }
       const int32_t skip = tile * kPairRows;
       const int32_t rows = min(kPairRows, r.nodes * a.H - skip);
       if (lane == 0) {
@@ -352,6 +414,7 @@ __device__ void list_work(const TreeDecodeArgs& a, TreeCtl* ctl, int C, int64_t 
         it.keys.nodes = r.prefix >= 0 ? r.nodes : 0;
         it.keys.total = r.keys;
         it.keys.prefix = r.keys - it.keys.nodes;
+        it.keys.length = r.prefix;
         it.req = req;
         it.rows = rows;
         it.skip = skip;
@@ -389,6 +452,7 @@ __device__ void list_work(const TreeDecodeArgs& a, TreeCtl* ctl, int C, int64_t 
 // One warp, two keys a lane, and a tile ahead.  A missing key's row is read
 // from somewhere else (a row of q is longer than a cache row): its score is
 // masked, and what goes into the value tile is made finite.
+template <bool kWindow>
 __device__ void look_up_rows(const TreeDecodeArgs& a, TreeCtl* ctl, int row_bytes, int lane) {
   const uint8_t* elsewhere = reinterpret_cast<const uint8_t*>(a.q);
   unsigned err = 0;
@@ -397,9 +461,13 @@ __device__ void look_up_rows(const TreeDecodeArgs& a, TreeCtl* ctl, int row_byte
 #pragma unroll 1
   for (int t = -1;; ++t) {  // tile t is stored, t + 1 looked up
     const uint8_t* row[2];
+    int32_t until[2];
     if (t >= 0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) row[h] = key_row(a, place[h], row_bytes, err);
+      for (int h = 0; h < 2; ++h) {
+        row[h] = key_row(a, place[h], row_bytes, err);
+        until[h] = place[h].until;
+      }
     }
     const int before = ahead.item;
     ahead.next_tile(ctl);
@@ -408,7 +476,7 @@ __device__ void look_up_rows(const TreeDecodeArgs& a, TreeCtl* ctl, int row_byte
       const Item& it = ahead.at(ctl);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        place[h] = find_key(a, it.keys, it.req, (it.tile0 + ahead.tile) * kTileKeys + 32 * h + lane);
+        place[h] = find_key<kWindow>(a, it.keys, it.req, (it.tile0 + ahead.tile) * kTileKeys + 32 * h + lane);
     }
     if (t >= 0) {
       const int slot = t % kPlaces;
@@ -420,6 +488,11 @@ __device__ void look_up_rows(const TreeDecodeArgs& a, TreeCtl* ctl, int row_byte
       for (int h = 0; h < 2; ++h) {
         have[h] = __ballot_sync(0xffffffffu, row[h] != nullptr);
         ctl->row[slot][32 * h + lane] = row[h] ? row[h] : elsewhere;
+        if (kWindow) ctl->until[t & 7][32 * h + lane] = uint8_t(until[h]);
+      }
+      if (kWindow) {
+        const int32_t soonest = __reduce_min_sync(0xffffffffu, min(until[0], until[1]));
+        if (lane == 0) ctl->soonest[t & 15] = soonest;
       }
       if (lane == 0) ctl->valid[t & 15] = uint64_t(have[1]) << 32 | have[0];
       __syncwarp();
@@ -432,8 +505,11 @@ __device__ void look_up_rows(const TreeDecodeArgs& a, TreeCtl* ctl, int row_byte
 
 // --------------------------------------------------------------- converters
 // Whether any of a tile's keys may hold what a masked place must not show.
-__device__ __forceinline__ bool must_mend(const TreeCtl* ctl, const Item& it, int tile, int g) {
-  return (it.tile0 + tile + 1) * kTileKeys > it.keys.prefix || ctl->valid[g & 15] != ~0ull;
+template <bool kWindow>
+__device__ __forceinline__ bool must_mend(const TreeDecodeArgs& a, const TreeCtl* ctl, const Item& it, int tile,
+                                          int g) {
+  return (it.tile0 + tile + 1) * kTileKeys > it.keys.prefix || ctl->valid[g & 15] != ~0ull ||
+         (kWindow && ctl->soonest[g & 15] < a.max_nodes - 1);
 }
 
 // A warp's eight rows of q on their way to the Q operand (a row's 1,152 bytes
@@ -617,6 +693,7 @@ struct Fp8Keys {
     }
   }
 
+  template <bool kWindow>
   static __device__ void run(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl, int C, int w, int lane) {
     constexpr int kPer = kWarpKeys / 2;  // keys of a half warp
     const uint32_t base = smem_u32(sm);
@@ -674,7 +751,7 @@ struct Fp8Keys {
         if (!__all_sync(0xffffffffu, ok)) break;
         const uint32_t k_tile = from + st * Sm::kKSize, v_tile = to + (g & 1) * kVSize;
         const float* scales = ctl->scales[g & 3][group];
-        const bool mend = must_mend(ctl, it, now.tile, g);
+        const bool mend = must_mend<kWindow>(a, ctl, it, now.tile, g);
         uint4 own[kPer];
         float s_own[kPer], s_peer[kPer];
         bool plain = !mend;
@@ -787,6 +864,7 @@ struct Fp4Keys {
     __device__ __forceinline__ bool nan() const { return (((scale & 0x7f7fu) + 0x0101u) & 0x8080u) != 0; }
   };
 
+  template <bool kWindow>
   static __device__ void run(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl, int C, int w, int lane) {
     constexpr int kPer = kWarpKeys / 4;  // keys of a quarter warp
     const uint32_t base = smem_u32(sm);
@@ -872,7 +950,7 @@ struct Fp4Keys {
       if (lane == 0) mbar_arrive_at(k_full + 8 * st);
       // V: free once PV of the tile two before is done
       if (g >= 2 && !__all_sync(0xffffffffu, tree_wait(&ctl->pv[st], ((g >> 1) - 1) & 1, ctl, kWsPvDone))) break;
-      const bool mend = must_mend(ctl, it, now.tile, g);
+      const bool mend = must_mend<kWindow>(a, ctl, it, now.tile, g);
       const uint32_t v_block = base + Sm::kOffV + st * kVSize + (j >> 1) * kVBlock;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
@@ -1038,7 +1116,17 @@ __device__ __forceinline__ uint32_t seen_from(const uint64_t* mask, int words, i
   return uint32_t(x);
 }
 
-template <class F>
+// Windowed calls, of a tile with keys that not every node sees: which of 16 keys
+// the item's row sees.
+__noinline__ __device__ uint32_t in_window(const TreeDecodeArgs& a, const Item& it, int row, const uint8_t* until) {
+  const int32_t position = node_position(a, it.keys.first + (it.skip + row) / a.H, it.keys.length);
+  uint32_t seen = 0;
+#pragma unroll 1
+  for (int k = 0; k < 16; ++k) seen |= uint32_t(position <= until[k]) << k;
+  return seen;
+}
+
+template <class F, bool kWindow>
 __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl, uint32_t tb, int C, int tid) {
   const int warp = tid >> 5, lane = tid & 31;
   // the thread's row; which 32 keys and 256 value dims its lane holds, and
@@ -1130,7 +1218,9 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
           s[2 * k + 1] = __float_as_uint(f.y + __uint_as_float(s[2 * k + 1]));
         }
       }
-      const uint32_t see = seen & uint32_t(ctl->valid[g & 15] >> (kCtaKeys * half + 16 * part)) & 0xffffu;
+      uint32_t see = seen & uint32_t(ctl->valid[g & 15] >> (kCtaKeys * half + 16 * part)) & 0xffffu;
+      if (kWindow && live && ctl->soonest[g & 15] < a.max_nodes - 1)
+        see &= in_window(a, it, row, &ctl->until[g & 7][kCtaKeys * half + 16 * part]);
       if (see != 0xffffu) {
 #pragma unroll
         for (int k = 0; k < 16; ++k)
@@ -1262,7 +1352,7 @@ __device__ __forceinline__ int64_t warp_sum(int64_t x) {
   return x;
 }
 
-template <class F>
+template <class F, bool kWindow>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
     tree_decode_kernel(const __grid_constant__ TreeDecodeArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -1318,7 +1408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
   int64_t v = 0, later = 0;
 #pragma unroll 1
   for (int32_t b = tid; b < a.B; b += kTreeThreads) {
-    const Request r = load_request(a, b, err);
+    const Request r = load_request<kWindow>(a, b, err);
     const int64_t n = int64_t(row_tiles(a, r)) * tile_units(a, r);
     if (b == tid) v = n;
     else later += n;
@@ -1356,7 +1446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
     v = 0;
     if (b < a.B) {
       unsigned ignored = 0;
-      const Request r = load_request(a, b, ignored);
+      const Request r = load_request<kWindow>(a, b, ignored);
       v = int64_t(row_tiles(a, r)) * tile_units(a, r);
     }
     upto = v;
@@ -1379,9 +1469,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
   cluster_wait();  // the peer's barriers are initialised
 
   if (warp < kSoftWarps) {
-    softmax_rows<F>(a, sm, ctl, tb, C, tid);
+    softmax_rows<F, kWindow>(a, sm, ctl, tb, C, tid);
   } else if (warp < kIssueWarp) {
-    F::run(a, sm, ctl, C, warp - kSoftWarps, lane);
+    F::template run<kWindow>(a, sm, ctl, C, warp - kSoftWarps, lane);
   } else {
     if (warp == kIssueWarp) {
       if (C == 0) issue_mmas<F>(sm, ctl, tb, lane);
@@ -1390,9 +1480,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
       for (int n = kLooks; n > 0 && !mbar_try_wait(&ctl->end, 0); --n) {
       }
     } else if (warp == kIssueWarp + 1) {
-      list_work(a, ctl, C, units, per_pair, lane);
+      list_work<kWindow>(a, ctl, C, units, per_pair, lane);
     } else if (warp == kIssueWarp + 2) {
-      look_up_rows(a, ctl, F::kRowBytes, lane);
+      look_up_rows<kWindow>(a, ctl, F::kRowBytes, lane);
     } else if constexpr (!F::kFp4) {
       F::copy_rows(sm, ctl, C, lane);
     }
@@ -1503,7 +1593,7 @@ size_t tree_decode_workspace_bytes(int32_t T, int32_t B, int32_t H, int64_t max_
   return T > 0 && B > 0 ? plan_tree(T, B, H, max_keys).bytes : 0;
 }
 
-template <class F>
+template <class F, bool kWindow>
 static cudaError_t launch_tree(const TreeDecodeArgs& a, int pairs, cudaStream_t s) {
   static std::atomic<bool> done[64];
   int dev = 0;
@@ -1511,12 +1601,12 @@ static cudaError_t launch_tree(const TreeDecodeArgs& a, int pairs, cudaStream_t 
   if (e != cudaSuccess) return e;
   const bool tracked = dev >= 0 && dev < 64;
   if (!tracked || !done[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(tree_decode_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(tree_decode_kernel<F, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              tree_smem<F::kFp4>());
     if (e != cudaSuccess) return e;
     if (tracked) done[dev].store(true, std::memory_order_release);
   }
-  return launch_overlapped(tree_decode_kernel<F>, unsigned(2 * pairs), kTreeThreads, tree_smem<F::kFp4>(), s, a);
+  return launch_overlapped(tree_decode_kernel<F, kWindow>, unsigned(2 * pairs), kTreeThreads, tree_smem<F::kFp4>(), s, a);
 }
 
 cudaError_t launch_tree_decode(const TreeDecodeArgs& args, int64_t max_keys, bool fp4, cudaStream_t s) {
@@ -1532,7 +1622,9 @@ cudaError_t launch_tree_decode(const TreeDecodeArgs& args, int64_t max_keys, boo
   a.ws_desc = ws;
   a.ws_ml = p.split ? reinterpret_cast<float*>(ws + p.ml_off) : nullptr;
   a.ws_o = p.split ? reinterpret_cast<uint16_t*>(ws + p.o_off) : nullptr;
-  const cudaError_t e = fp4 ? launch_tree<Fp4Keys>(a, p.pairs, s) : launch_tree<Fp8Keys>(a, p.pairs, s);
+  const bool window = a.window > 0;
+  const cudaError_t e = fp4 ? (window ? launch_tree<Fp4Keys, true>(a, p.pairs, s) : launch_tree<Fp4Keys, false>(a, p.pairs, s))
+                            : (window ? launch_tree<Fp8Keys, true>(a, p.pairs, s) : launch_tree<Fp8Keys, false>(a, p.pairs, s));
   if (e != cudaSuccess || !p.split) return e;
   return launch_overlapped(tree_merge_kernel, unsigned(p.pairs * kMergeBlocks), 32 * kMergeWarps, 0, s, a);
 }

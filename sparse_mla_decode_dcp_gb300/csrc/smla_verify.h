@@ -50,6 +50,8 @@ struct TreeDecodeArgs {
   int32_t max_prefix;
   const uint64_t* masks;       // [T, mask_words]
   int32_t max_nodes, mask_words;
+  const int32_t* positions;    // [T] (with a window)
+  int32_t window, sinks;       // window 0: none
   int32_t D, rank, block_size, interleave;  // rank -1: all pools
   FastDiv div_ID, div_bs;      // set by the launcher
   const uint8_t* pools[kMaxMerge];

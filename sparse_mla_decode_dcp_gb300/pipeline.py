@@ -107,7 +107,8 @@ class DcpServingStep:
 
     With ``max_nodes`` above 0 the server may draft trees of that many tokens
     a request at most: ``verify`` writes their rows into scratch slots that
-    each pool has behind its blocks and attends them; ``commit`` takes the
+    each pool has behind its blocks and attends each node's window and sinks
+    of its prefix and ancestors, as ``run`` does; ``commit`` takes the
     nodes the model agrees with into the cache.  ``commit`` takes blocks as
     ``run`` does.  Both reuse their results' buffers and allocate nothing; a
     CUDA graph may hold them, with the free lists of its capture.
@@ -201,7 +202,8 @@ class DcpServingStep:
 
     def verify(self, prefix_lens: torch.Tensor, parents: torch.Tensor, row_start: torch.Tensor,
                kv: torch.Tensor, q: torch.Tensor):
-        """Attention of drafted trees over the cached prefixes and themselves.
+        """Attention of drafted trees over the cached prefixes and themselves,
+        each node's window and sinks of them as ``run`` attends a token's.
         Rows kv [T, 576] and q [T, H, 576] are the nodes', request b's at
         row_start[b] .. row_start[b + 1] - 1; their positions (for q's
         rotation) come from ``tree_positions``.  Returns
@@ -216,7 +218,7 @@ class DcpServingStep:
         return capi.dcp_tree_mla_decode(
             q, row_start, prefix_lens, self.max_ctx, maps.masks, self.max_nodes, [slots] * self.D,
             self.pools, self.block_tables, self.block_size, self.sm_scale, interleave=self.interleave,
-            out=self.tree_out[:T], lse=self.tree_lse[:T], workspace=self.tree_workspace,
+            window=self.window, sinks=self.sinks, positions=maps.positions, out=self.tree_out[:T], lse=self.tree_lse[:T], workspace=self.tree_workspace,
             stream=self.stream)
 
     def tree_positions(self, prefix_lens: torch.Tensor, parents: torch.Tensor,

