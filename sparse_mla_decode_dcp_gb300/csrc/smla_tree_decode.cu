@@ -637,18 +637,24 @@ struct Fp8Keys {
         v[i][1] = lds128(at + sw128_offset(r0 + i, 2 * (lane & 3) + 1));
         rope[i] = lds128(q0 + 8 * kQBlock + sw128_offset(r0 + i, lane & 7));
       }
-      uint32_t top[2];
+      uint32_t top[2], top_rope[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         auto most = [](uint4 x) {
           return __hmax2_nan(__hmax2_nan(magnitudes(x.x), magnitudes(x.y)), __hmax2_nan(magnitudes(x.z), magnitudes(x.w)));
         };
-        const __nv_bfloat162 m = __hmax2_nan(most(v[i][0]), most(v[i][1]));
-        const uint32_t bits = *reinterpret_cast<const uint32_t*>(&m);
-        top[i] = max(bits & 0xffffu, bits >> 16);  // a NaN's bits are above infinity's
+        auto larger = [](__nv_bfloat162 m) {  // its bits: a NaN's are above infinity's
+          const uint32_t bits = *reinterpret_cast<const uint32_t*>(&m);
+          return max(bits & 0xffffu, bits >> 16);
+        };
+        top[i] = larger(__hmax2_nan(most(v[i][0]), most(v[i][1])));
+        top_rope[i] = larger(most(rope[i]));
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
+      for (int i = 0; i < 2; ++i) {
+        top[i] = __reduce_max_sync(0xffffffffu, top[i]);
+        top_rope[i] = __reduce_max_sync(0xffffffffu, top_rope[i]);
+      }
       __syncwarp();  // every lane has read the rows
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -686,8 +692,9 @@ struct Fp8Keys {
         if (lane < 8) sts128(q0 + 8 * kQBlock + sw128_offset(r, lane), make_uint4(o[0], o[1], o[2], o[3]));
         // a query that is not finite has no score that is
         if (lane == 0) {
-          row_scale[r] = __uint_as_float(exponent == 255 ? 0x7fc00000u : uint32_t(127 - up) << 23);
-          if (exponent == 255) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
+          const bool finite = max(top[i], top_rope[i]) < 0x7f80u;
+          row_scale[r] = __uint_as_float(finite ? uint32_t(127 - up) << 23 : 0x7fc00000u);
+          if (!finite) atomicOr(&g_decode_error, SMLA_DEVERR_RANGE);
         }
       }
     }
