@@ -23,7 +23,7 @@
 //     MMA's layout asynchronously (cp.async).  The query's latent part is an
 //     e4m3 sum hi + lo of each row's values times a power of two: bf16 has 8
 //     significant bits, hi the first 4 and lo the rest, exactly down to 2^-10
-//     of the row's largest value and within 2^-17 of it below.  The four scale
+//     of the row's largest latent and within 2^-17 of it below.  The four scale
 //     groups and the rope part (bf16 as it is) have score accumulators of
 //     their own, which meet, times the fp32 scales, in the softmax: the log
 //     sum is as exact as fp32 sums are.  Values are codes times scales,
@@ -139,7 +139,7 @@ struct TreeCtl {
   alignas(16) uint8_t until[8][kTileKeys];
   int32_t soonest[16];
   const uint8_t* row[kPlaces][kTileKeys];  // the keys' cache rows
-  float row_scale[2][kCtaRows];           // fp8 rows, per item (mod 2): a row's score times this is its own
+  float row_scale[2][kCtaRows];           // fp8 rows, per item (mod 2): 2^-up of a row's latents
   float tops[2][32 * kSoftWarps], sums[32 * kSoftWarps];
   Item items[kItems];
   int64_t warp_units[kTreeWarps], warp_later[kTreeWarps];
@@ -660,11 +660,11 @@ struct Fp8Keys {
       for (int i = 0; i < 2; ++i) {
         const int r = r0 + i;
         const uint32_t x[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
-        // the row times 2^up has its largest value in [2^7, 2^8)
+        // the latents times 2^up have their largest value in [2^7, 2^8); the rope
+        // part stays as it is (times 2^up it would overflow beside tiny latents)
         const int exponent = int(top[i] >> 7);
         const int up = top[i] == 0 ? 0 : max(min(134 - exponent, 120), -120);
         const float by = __uint_as_float(uint32_t(127 + up) << 23);
-        const __nv_bfloat162 by2 = __float2bfloat162_rn(by);
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -680,16 +680,8 @@ struct Fp8Keys {
             lo[k] |= uint32_t(__nv_cvt_halfraw2_to_fp8x2(__hsub2(f, b), __NV_SATFINITE, __NV_E4M3)) << (16 * j);
           }
         }
-        const uint32_t z[4] = {rope[i].x, rope[i].y, rope[i].z, rope[i].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&z[k]), by2);
-          o[k] = *reinterpret_cast<const uint32_t*>(&p);
-        }
         sts128(to + sw128_offset(r, lane & 7), make_uint4(hi[0], hi[1], hi[2], hi[3]));
         sts128(to + 4 * kQBlock + sw128_offset(r, lane & 7), make_uint4(lo[0], lo[1], lo[2], lo[3]));
-        if (lane < 8) sts128(q0 + 8 * kQBlock + sw128_offset(r, lane), make_uint4(o[0], o[1], o[2], o[3]));
         // a query that is not finite has no score that is
         if (lane == 0) {
           const bool finite = max(top[i], top_rope[i]) < 0x7f80u;
@@ -1155,7 +1147,8 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
     const uint64_t* mask =
         a.masks + (live ? int64_t(it.keys.first) + (it.skip + row) / a.H : it.keys.first) * a.mask_words;
     float m_ref = -INFINITY, l = 0.f;  // log2 domain
-    float c2 = a.sm_scale * kLog2e;
+    const float c2 = a.sm_scale * kLog2e;
+    float latents = 1.f;  // fp8 rows: the row's scale
     const int prefix = it.keys.prefix;
     int first = it.tile0 * kTileKeys + kCtaKeys * half + 16 * part;  // key of s[0]
     for (int j = 0; j < n; ++j, ++g, first += kTileKeys) {
@@ -1197,7 +1190,7 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
         };
         ok = __all_sync(0xffffffffu, tree_wait(&ctl->qk[0], g & 1, ctl, kWsSFull));
         if (!ok) break;
-        if (j == 0) c2 *= ctl->row_scale[cur.item & 1][r];
+        if (j == 0) latents = ctl->row_scale[cur.item & 1][r];
         tc_fence_after();
         tmem_ld16(scores, x[0]);
         tmem_ld16(scores + 32, x[1]);
@@ -1221,8 +1214,8 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float2 f = unpack2(sum[k]);
-          s[2 * k] = __float_as_uint(f.x + __uint_as_float(s[2 * k]));
-          s[2 * k + 1] = __float_as_uint(f.y + __uint_as_float(s[2 * k + 1]));
+          s[2 * k] = __float_as_uint(fmaf(f.x, latents, __uint_as_float(s[2 * k])));
+          s[2 * k + 1] = __float_as_uint(fmaf(f.y, latents, __uint_as_float(s[2 * k + 1])));
         }
       }
       uint32_t see = seen & uint32_t(ctl->valid[g & 15] >> (kCtaKeys * half + 16 * part)) & 0xffffu;
