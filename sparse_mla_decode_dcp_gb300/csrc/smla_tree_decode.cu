@@ -30,8 +30,8 @@
 //     rounded once to fp16.
 //   * fp4 rows: codes times scales are exact in fp16, for keys and values.
 //   * A row's 64 scores lie in two lanes, 32 each, whose threads agree on the
-//     maximum through shared memory.  Softmax in the log2 domain against a
-//     reference that moves only when a row's maximum grows by more than 2^8.
+//     maximum through shared memory.  Softmax by powers of two against a
+//     reference that moves only when p would grow past 2^8.
 //   * Masks are looked at in the tiles that hold nodes or missing rows; a
 //     node's row that is not finite is kept out of the value tile (its score
 //     spoils the rows that see it), so that masked places do not show.
@@ -1146,7 +1146,9 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
     const int64_t out_row = int64_t(it.keys.first) * a.H + it.skip + row;
     const uint64_t* mask =
         a.masks + (live ? int64_t(it.keys.first) + (it.skip + row) / a.H : it.keys.first) * a.mask_words;
-    float m_ref = -INFINITY, l = 0.f;  // log2 domain
+    // the reference is a score, not its product with c2: of scores so large that
+    // the product rounds by more than fp16's range, the largest still has p = 1
+    float m_ref = -INFINITY, l = 0.f;
     const float c2 = a.sm_scale * kLog2e;
     float latents = 1.f;  // fp8 rows: the row's scale
     const int prefix = it.keys.prefix;
@@ -1243,20 +1245,20 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
         sum = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float x = ex2(fmaf(__uint_as_float(s[2 * k]), c2, -ref));
-          const float y = ex2(fmaf(__uint_as_float(s[2 * k + 1]), c2, -ref));
+          const float2 below = unpack2(mul2(add2(pack2(s[2 * k], s[2 * k + 1]), pack2(-ref, -ref)), pack2(c2, c2)));
+          const float x = ex2(below.x), y = ex2(below.y);
           sum += x + y;
           p[k] = h2_bits(__floats2half2_rn(x, y));
         }
         if (any_moves) break;
         ok = __all_sync(0xffffffffu, tree_wait(&ctl->top[b], (g >> 1) & 1, ctl, kWsExchange));
         if (!ok) break;
-        top = fmaxf(fmaxf(ctl->tops[b][r], ctl->tops[b][64 + r]), fmaxf(ctl->tops[b][128 + r], ctl->tops[b][192 + r])) * c2;
-        const bool moves = top > m_ref + 8.f;
+        top = fmaxf(fmaxf(ctl->tops[b][r], ctl->tops[b][64 + r]), fmaxf(ctl->tops[b][128 + r], ctl->tops[b][192 + r]));
+        const bool moves = (top - m_ref) * c2 > 8.f;
         any_moves = __any_sync(0xffffffffu, moves);
         if (!any_moves) break;
         if (moves) {
-          alpha = ex2(m_ref - top);
+          alpha = ex2((m_ref - top) * c2);
           m_ref = top;
         }
       }
@@ -1304,10 +1306,10 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
     const int64_t place = partial ? int64_t(it.part) * kPairRows + row : out_row;
     if (live && half == 0 && part == 0) {
       if (partial) {
-        a.ws_ml[2 * place] = m_ref;
+        a.ws_ml[2 * place] = m_ref * c2;
         a.ws_ml[2 * place + 1] = l;
       } else {
-        a.lse[place] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+        a.lse[place] = l == 0.f ? -INFINITY : (m_ref * c2 + log2f(l)) * kLn2;
       }
     }
     uint16_t* dst = (partial ? a.ws_o : a.out) + place * SMLA_V_DIM + 256 * half;

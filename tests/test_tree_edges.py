@@ -3,8 +3,10 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import step_oracle as so
+from oracle.smla_oracle import bf16_bits_to_f64
 from sparse_mla_decode_dcp_gb300 import capi
-from test_tree_decode import FORMATS, Case, _err
+from test_tree_decode import FORMATS, SCALE, Case, _err
 
 
 @pytest.mark.gpu
@@ -51,3 +53,36 @@ def test_latents_of_all_sizes(cuda_device):
     assert _err() == 0
     assert out.isfinite().all() and lse.isfinite().all()
     c.check(out, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ctx", [70, 900])
+@pytest.mark.parametrize("fmt,low,high", [("fp8", 12, 100), ("fp4", 4, 12)])
+def test_scores_past_the_exponentials_range(cuda_device, fmt, low, high, ctx):
+    """Scores from some 2^13 to 2^100: the largest key alone counts, in whole
+    tiles and in merged ranges."""
+    c = Case(cuda_device, fmt, nodes=[8], ctx=[ctx], H=16, bs=16, seed=9)
+    by = torch.exp2(torch.linspace(low, high, 8).floor().double())[:, None, None]
+    c.q = (c.q.double() * by).bfloat16()
+    if fmt == "fp4":  # groups' scales as large as they may be
+        for pool in c.pools:
+            pool[:, 256:288] = 0x70
+    c.upload()
+    out, lse = c.run()
+    assert _err() == 0
+    assert out.isfinite().all() and lse.isfinite().all()
+    q = bf16_bits_to_f64(c.q.view(torch.int16).numpy().astype(np.uint16))
+    checked = 0
+    for j in range(8):
+        lat, rope = so.parse(np.stack([c.pools[d][s] for d, s in c.keys(0, j, -1)]))
+        s = SCALE * q[j] @ np.concatenate([lat, rope], axis=1).T
+        size = SCALE * (np.abs(q[j]) @ np.abs(np.concatenate([lat, rope], axis=1)).T).max(axis=1)
+        first, second = np.argmax(s, axis=1), np.sort(s, axis=1)[:, -2]
+        tol = size * 2.0 ** -17  # 42 steps of 2^-23 of the products' sum, as so.attend has it, and the keys' rope in fp16
+        assert np.all(np.abs(lse[j].cpu().double().numpy() - s.max(axis=1)) <= tol + np.log(ctx + 8))
+        for h in range(16):
+            if s[h].max() - second[h] > 2 * tol[h] + 20:  # another key's weight is below e^-20
+                want = lat[first[h]]
+                assert np.all(np.abs(out[j, h].cpu().double().numpy() - want) <= 2.0 ** -7 * np.abs(want) + 2.0 ** -12)
+                checked += 1
+    assert checked > 60
