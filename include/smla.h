@@ -757,8 +757,9 @@ smla_status smla_tree_maps(const int32_t* parents, const int32_t* row_start,
  *   lse            device fp32 [T, H]
  *   workspace      >= smla_tree_decode_workspace_size(T, H, B, max_prefix,
  *                  max_nodes, D, interleave, rank) bytes, 256-byte aligned;
- *                  needs no initial contents.  Calls that run concurrently
- *                  need distinct workspaces.
+ *                  needs no initial contents.  That size also serves every
+ *                  call of fewer rows, heads, requests, prefix or nodes.  Calls
+ *                  that run concurrently need distinct workspaces.
  * Errors: INVALID_ARG for T < 0, H < 1, B < 0, max_prefix < 0, max_nodes < 1,
  * D < 1, rank outside [-1, D), block_size < 1, interleave < 1, another format,
  * sm_scale not finite and positive, NULL or misaligned arrays, a bad pool or

@@ -581,7 +581,7 @@ size_t smla_tree_decode_workspace_size(int32_t T, int32_t H, int32_t B, int32_t 
   if (T < 0 || H < 1 || B < 0 || max_prefix < 0 || max_nodes < 1 || D < 1 || interleave < 1 || rank < -1 ||
       rank >= D || tree_unsupported(H, max_prefix, max_nodes, D))
     return 0;
-  return smla::tree_decode_workspace_bytes(T, B, H, tree_keys(max_prefix, max_nodes, D, interleave, rank));
+  return smla::tree_decode_most_workspace_bytes(T, B, H, tree_keys(max_prefix, max_nodes, D, interleave, rank));
 }
 
 // Both forms; window 0: the whole prefix.

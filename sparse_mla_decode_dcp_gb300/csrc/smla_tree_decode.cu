@@ -1558,6 +1558,7 @@ struct TreePlan {
   int pairs, min_units;
   bool split;
   size_t ml_off, o_off, bytes;
+  size_t most_bytes;  // of this call and any with fewer rows, requests or keys
 };
 
 // Key tiles that a pair takes at least.  One request of 8 nodes and 16 heads
@@ -1579,12 +1580,18 @@ TreePlan plan_tree(int32_t T, int32_t B, int32_t H, int64_t max_keys) {
   const int64_t row_tiles = int64_t(T) * H / kPairRows + (B < T ? B : T);
   p.split = key_tiles > (2 * row_tiles <= kPairs ? kWholeOfFew : kWholeOfMany);
   p.min_units = p.split ? kMinUnits : 1;
-  const int64_t units = p.split ? row_tiles * key_tiles : row_tiles;
-  const int64_t need = (units + p.min_units - 1) / p.min_units;
-  p.pairs = int(need < 1 ? 1 : need < kPairs ? need : kPairs);
+  auto pairs = [](int64_t units, int64_t least) {
+    const int64_t need = (units + least - 1) / least;
+    return int(need < 1 ? 1 : need < kPairs ? need : kPairs);
+  };
+  p.pairs = pairs(p.split ? row_tiles * key_tiles : row_tiles, p.min_units);
   p.ml_off = 4096;
-  p.o_off = p.ml_off + size_t(2) * p.pairs * kPairRows * 2 * sizeof(float);
-  p.bytes = p.split ? p.o_off + size_t(2) * p.pairs * kPairRows * SMLA_V_DIM * sizeof(uint16_t) : 0;
+  auto o_off = [&](int n) { return p.ml_off + size_t(2) * n * kPairRows * 2 * sizeof(float); };
+  auto bytes = [&](int n) { return o_off(n) + size_t(2) * n * kPairRows * SMLA_V_DIM * sizeof(uint16_t); };
+  p.o_off = o_off(p.pairs);
+  p.bytes = p.split ? bytes(p.pairs) : 0;
+  // fewer rows may be cut where these are not
+  p.most_bytes = key_tiles > kWholeOfFew ? bytes(pairs(row_tiles * key_tiles, kMinUnits)) : 0;
   static_assert(kPairs * sizeof(SplitTile) <= 4096, "descriptors fit");
   return p;
 }
@@ -1593,6 +1600,10 @@ TreePlan plan_tree(int32_t T, int32_t B, int32_t H, int64_t max_keys) {
 
 size_t tree_decode_workspace_bytes(int32_t T, int32_t B, int32_t H, int64_t max_keys) {
   return T > 0 && B > 0 ? plan_tree(T, B, H, max_keys).bytes : 0;
+}
+
+size_t tree_decode_most_workspace_bytes(int32_t T, int32_t B, int32_t H, int64_t max_keys) {
+  return T > 0 && B > 0 ? plan_tree(T, B, H, max_keys).most_bytes : 0;
 }
 
 template <class F, bool kWindow>

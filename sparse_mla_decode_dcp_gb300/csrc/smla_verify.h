@@ -109,7 +109,9 @@ struct MatmulArgs {
 
 // max_keys: of a request
 cudaError_t launch_tree_decode(const TreeDecodeArgs& a, int64_t max_keys, bool fp4, cudaStream_t s);
+// what the call needs, and what it and any of fewer rows, requests or keys need
 size_t tree_decode_workspace_bytes(int32_t T, int32_t B, int32_t H, int64_t max_keys);
+size_t tree_decode_most_workspace_bytes(int32_t T, int32_t B, int32_t H, int64_t max_keys);
 cudaError_t tree_decode_error_word(uint32_t* flags, bool clear);
 
 cudaError_t launch_fp8_quantise(const QuantiseArgs& a, cudaStream_t s);

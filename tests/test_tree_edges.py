@@ -1,11 +1,15 @@
 """Tree attention at the edges of what its queries, calls and buffers may be."""
+import itertools
+
 import numpy as np
 import pytest
 import torch
 
 from oracle import step_oracle as so
 from oracle.smla_oracle import bf16_bits_to_f64
+from sparse_mla_decode_dcp_gb300 import build as smla_build
 from sparse_mla_decode_dcp_gb300 import capi
+from sparse_mla_decode_dcp_gb300.pipeline import DcpServingStep
 from test_tree_decode import FORMATS, SCALE, Case, _err
 
 
@@ -86,3 +90,47 @@ def test_scores_past_the_exponentials_range(cuda_device, fmt, low, high, ctx):
                 assert np.all(np.abs(out[j, h].cpu().double().numpy() - want) <= 2.0 ** -7 * np.abs(want) + 2.0 ** -12)
                 checked += 1
     assert checked > 60
+
+
+# --------------------------------------------------------------- workspaces
+@pytest.mark.parametrize("H", [1, 16, 128])
+@pytest.mark.parametrize("B", [1, 5, 32, 200])
+@pytest.mark.parametrize("rank", [-1, 1])
+def test_a_workspace_serves_every_smaller_call(H, B, rank):
+    smla_build.build()
+    size = capi.tree_decode_workspace_size
+    rows, prefixes = [1, 2, 3, 8, 16, 17, 32, 64, 100, 256, 512, 3000], [0, 60, 130, 300, 400, 496, 600, 5000]
+    got = {(T, p): size(T, H, B, p, 16, 4, 1, rank) for T, p in itertools.product(rows, prefixes)}
+    for (T, p), n in got.items():
+        for (T2, p2), m in got.items():
+            assert T2 > T or p2 > p or m <= n, (T, p, T2, p2)
+    assert all(size(64, H, b, 300, 16, 4, 1, rank) <= size(64, H, B, 300, 16, 4, 1, rank) for b in range(1, B + 1))
+    assert all(size(64, h, B, 300, 16, 4, 1, rank) <= size(64, H, B, 300, 16, 4, 1, rank) for h in range(1, H + 1))
+    assert all(size(64, H, B, 300, n, 4, 1, rank) <= size(64, H, B, 300, 16, 4, 1, rank) for n in range(1, 17))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window", [150, 1000])
+def test_steps_of_any_rows_allocate_nothing(cuda_device, window):
+    """A server whose full steps are not cut into key ranges and whose small
+    ones are."""
+    dev, B, N, H = cuda_device, 32, 16, 128
+    step = DcpServingStep(B, 1, H, 2, 16, 700, 300, window, 4, fmt="fp8", max_nodes=N, device=dev)
+    ctx = torch.full((B,), 260, dtype=torch.int32, device=dev)
+    g = torch.Generator(device=dev).manual_seed(1)
+    step.prefill(ctx, ctx, torch.randn((260 * B, 576), generator=g, device=dev).bfloat16())
+    step.take_blocks()
+    for T in (512, 300, 64, 40, 32, 16, 3, 1):
+        par = torch.full((T,), -1, dtype=torch.int32, device=dev)
+        starts = torch.arange(B + 1, device=dev) * T // B
+        rs, tok = starts.to(torch.int32), torch.zeros_like(par)
+        kv = torch.randn((T, 576), generator=g, device=dev).bfloat16()
+        q = torch.randn((T, H, 576), generator=g, device=dev).bfloat16()
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_stats(dev)["allocation.all.allocated"]
+        out, lse = step.verify(ctx, par, rs, kv, q)
+        step.commit(ctx, par, tok, tok, rs)
+        torch.cuda.synchronize()
+        assert torch.cuda.memory_stats(dev)["allocation.all.allocated"] == before, T
+        assert lse.isfinite().all() and _err() == 0
+        step._taken = []  # the same lengths again
