@@ -872,8 +872,12 @@ smla_status smla_mla_cache_move(int32_t format, uint8_t* kv_cache, int64_t num_s
  *   codes    device uint8 (e4m3) output, the same with its own strides
  *   scales   device fp32 output, entry (g, m, j) at g * batch + m * row +
  *            j * col
- * Errors: INVALID_ARG for G < 0, M < 0, K < 1, a negative stride, NULL or
- * misaligned arrays.  G = 0 or M = 0 is a no-op.
+ * No output may alias x, the other output or its own entries: taken in the
+ * order of their strides, each dimension of more than one entry steps past all
+ * that the ones before it span.
+ * Errors: INVALID_ARG for G < 0, M < 0, K < 1, a negative stride, outputs whose
+ * own entries are not apart as above, NULL or misaligned arrays.  G = 0 or M =
+ * 0 is a no-op.
  */
 smla_status smla_fp8_quantise(const uint16_t* x, int64_t x_batch_stride, int64_t x_row_stride, int32_t G,
                               int32_t M, int32_t K, uint8_t* codes, int64_t codes_batch_stride,
@@ -901,9 +905,9 @@ smla_status smla_fp8_quantise(const uint16_t* x, int64_t x_batch_stride, int64_t
  * a and b are 16-byte aligned, with row strides of at least K and row and
  * (G > 1) batch strides that are positive multiples of 16.  Strides of
  * scales may be 0 (a shared scale).  out may not alias an input, nor its own
- * entries each other.
- * Errors: INVALID_ARG for G < 0, M < 0, N < 0, K < 1, a bad stride, NULL or
- * misaligned arrays; UNSUPPORTED for strides of 2^40 bytes and more and for
+ * entries each other (as smla_fp8_quantise's outputs).
+ * Errors: INVALID_ARG for G < 0, M < 0, N < 0, K < 1, a bad stride, an out whose
+ * own entries are not apart, NULL or misaligned arrays; UNSUPPORTED for strides of 2^40 bytes and more and for
  * more than 2^27 tiles of 16 x 128 results.  G, M or N = 0 is a no-op.
  */
 smla_status smla_fp8_matmul(const uint8_t* a, int64_t a_batch_stride, int64_t a_row_stride,

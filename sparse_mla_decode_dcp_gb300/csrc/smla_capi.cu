@@ -2,6 +2,7 @@
 // (the host-buffer form of the fused step: its copies and a launch per row
 // group).  Every check runs before anything touches the GPU, so a rejected
 // call has no side effect and needs no device.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -708,6 +709,24 @@ smla_status smla_mla_cache_move(int32_t format, uint8_t* kv_cache, int64_t num_s
   return from_cuda(smla::launch_cache_move(a, format == SMLA_CACHE_FP4, static_cast<cudaStream_t>(stream)));
 }
 
+// Whether an array's entries lie apart: with the dimensions in the order of
+// their strides, each steps past all that the ones before it span.
+struct Dim {
+  int64_t count, stride;
+};
+static bool apart(Dim x, Dim y, Dim z) {
+  Dim d[3] = {x, y, z};
+  std::sort(d, d + 3, [](const Dim& p, const Dim& q) { return p.stride < q.stride; });
+  int64_t span = 1;
+  for (const Dim& e : d) {
+    if (e.count <= 1) continue;
+    if (e.stride < span) return false;
+    const bool fits = e.count - 1 <= (INT64_MAX - span) / e.stride;
+    span = fits ? (e.count - 1) * e.stride + span : INT64_MAX;
+  }
+  return true;
+}
+
 smla_status smla_fp8_quantise(const uint16_t* x, int64_t x_batch_stride, int64_t x_row_stride, int32_t G,
                               int32_t M, int32_t K, uint8_t* codes, int64_t codes_batch_stride,
                               int64_t codes_row_stride, float* scales, int64_t scales_batch_stride,
@@ -717,6 +736,9 @@ smla_status smla_fp8_quantise(const uint16_t* x, int64_t x_batch_stride, int64_t
     return SMLA_ERR_INVALID_ARG;
   if (G == 0 || M == 0) return SMLA_OK;
   if (!x || !codes || !scales || misaligned(x, 2) || misaligned(scales, 4)) return SMLA_ERR_INVALID_ARG;
+  if (!apart({K, 1}, {M, codes_row_stride}, {G, codes_batch_stride}) ||
+      !apart({(int64_t(K) + 127) / 128, scales_col_stride}, {M, scales_row_stride}, {G, scales_batch_stride}))
+    return SMLA_ERR_INVALID_ARG;
   const smla::QuantiseArgs a = {x, {x_batch_stride, x_row_stride, 1}, G, M, K,
                                 codes, {codes_batch_stride, codes_row_stride, 1},
                                 scales, {scales_batch_stride, scales_row_stride, scales_col_stride}};
@@ -752,6 +774,7 @@ smla_status smla_fp8_matmul(const uint8_t* a, int64_t a_batch_stride, int64_t a_
     return SMLA_ERR_INVALID_ARG;
   if (int64_t(G) * (int64_t(M) / 16 + 1) * (int64_t(N) / 128 + 1) > (int64_t(1) << 27))
     return SMLA_ERR_UNSUPPORTED;
+  if (!apart({N, 1}, {M, out_row_stride}, {G, out_batch_stride})) return SMLA_ERR_INVALID_ARG;
   smla::MatmulArgs m{};
   m.a = a;
   m.as = {a_batch_stride, a_row_stride, 1};
