@@ -544,6 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (C == 1) {  // tells the first CTA that this one's half has landed
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
+            // (written by TMA, whose completion this warp has waited for)
             if (leader) mbar_arrive_at(map_to_cta(smem_u32(&ctl.peer_full[s]), 0));
             __syncwarp();
           } else {
@@ -639,7 +640,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (c + 1 == kReads) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive_at(sum_empty + 8 * b);
+              if (lane == 0) mbar_arrive_at(sum_empty + 8 * b);  // read: wait::ld, fence
             }
             const uint64_t s2 = c < cut ? s0 : s1;
 #pragma unroll

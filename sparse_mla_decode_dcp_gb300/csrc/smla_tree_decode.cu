@@ -741,7 +741,7 @@ struct Fp8Keys {
         convert_queries(base, ctl->row_scale[now.item & 1], w, lane);
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive_at(q_full);
+        if (lane == 0) mbar_arrive_at(q_full);  // written: every lane has fenced its part
       }
       {
         // V: free once PV of the tile two before is done
@@ -805,7 +805,7 @@ struct Fp8Keys {
         fence_async_shared();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_at(v_full + 8 * (g & 1));
+          mbar_arrive_at(v_full + 8 * (g & 1));  // written: every lane has fenced its part
           mbar_arrive(&ctl->k_read[st]);
         }
         ahead.next_tile(ctl);
@@ -946,7 +946,7 @@ struct Fp4Keys {
       }
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive_at(k_full + 8 * st);
+      if (lane == 0) mbar_arrive_at(k_full + 8 * st);  // (K, V and Q: as over 8-bit rows)
       // V: free once PV of the tile two before is done
       if (g >= 2 && !__all_sync(0xffffffffu, tree_wait(&ctl->pv[st], ((g >> 1) - 1) & 1, ctl, kWsPvDone))) break;
       const bool mend = must_mend<kWindow>(a, ctl, it, now.tile, g);
@@ -1097,7 +1097,7 @@ __device__ void tell_peer(TreeCtl* ctl, int lane) {
       if (!__all_sync(0xffffffffu, tree_wait(&ctl->k_full[t % 3], (t / 3) & 1, ctl, kWsFull))) return;
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive_at(k_peer + 8 * (t % 3));
+      if (lane == 0) mbar_arrive_at(k_peer + 8 * (t % 3));  // copied: this warp has waited for it and fenced
     }
   }
 }
@@ -1167,7 +1167,7 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_at(s_read + 8 * b);
+        if (lane == 0) mbar_arrive_at(s_read + 8 * b);  // read: wait::ld, fence
       } else {
         // sum = scores of groups 0, 1 by their scales, then of 2, 3 and the rope;
         // the scales are asked for while the scores are on their way
@@ -1200,7 +1200,7 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_at(s_read);
+        if (lane == 0) mbar_arrive_at(s_read);  // read: wait::ld, fence
         add(0, true);
         add(1, false);
         tmem_ld16(scores + 64, x[0]);
@@ -1291,7 +1291,7 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
       fence_async_shared();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_at(p_full + 8 * pb);
+      if (lane == 0) mbar_arrive_at(p_full + 8 * pb);  // written: every lane has fenced its part
     }
     if (!ok) break;
     ctl->sums[tid] = l;
@@ -1343,7 +1343,7 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive_at(out_read);
+    if (lane == 0) mbar_arrive_at(out_read);  // read: wait::ld, fence
     leave_item(ctl, cur.item, lane);
   }
 }
