@@ -134,3 +134,57 @@ def test_steps_of_any_rows_allocate_nothing(cuda_device, window):
         assert torch.cuda.memory_stats(dev)["allocation.all.allocated"] == before, T
         assert lse.isfinite().all() and _err() == 0
         step._taken = []  # the same lengths again
+
+
+# -------------------------------------------------- the log-sums of 8-bit rows
+def _bounds(q, raw):
+    """One node's log-sums and their tolerance, as the header promises them over
+    8-bit rows: exact products in fp32 sums (so.attend without a rounding of the
+    keys), but latents of q below 2^-10 of the row's largest to within 2^-17 of
+    it."""
+    _, lse, _, tol = so.attend(q, raw, SCALE, 0.0)
+    lat = np.abs(so.parse(raw)[0])
+    top = np.abs(q[:, :512]).max(axis=1, keepdims=True)
+    small = np.where(np.abs(q[:, :512]) < 2.0 ** -10 * top, 2.0 ** -17 * top, 0)
+    return lse, tol + SCALE * (small @ lat.T).max(axis=1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", [
+    dict(nodes=[9, 3], ctx=[65, 700], H=16, D=2), dict(nodes=[16], ctx=[130], H=128), dict(nodes=[5], ctx=[0], H=37),
+])
+@pytest.mark.parametrize("what", ["plain", "sizes of rows", "small latents", "scales"])
+def test_log_sums_are_as_good_as_fp32_sums(cuda_device, kw, what):
+    c = Case(cuda_device, "fp8", bs=16, seed=len(what), **kw)
+    g = torch.Generator().manual_seed(3)
+    if what == "sizes of rows":
+        c.q *= torch.exp2(torch.randint(-40, 7, (c.T, c.H, 1), generator=g)).bfloat16()
+    elif what == "small latents":  # down to 2^-20 of the row's largest
+        c.q[..., :512] *= torch.exp2(torch.randint(-20, 1, (c.T, c.H, 512), generator=g)).bfloat16()
+    elif what == "scales":
+        rng = np.random.default_rng(4)
+        for pool in c.pools:
+            by = np.exp2(rng.integers(-8, 4, (len(pool), 4))).astype("<f4")
+            pool[:, 512:528] = (pool[:, 512:528].copy().view("<f4") * by).view(np.uint8)
+    c.upload()
+    _, got = c.run()
+    assert _err() == 0
+    q = bf16_bits_to_f64(c.q.view(torch.int16).numpy().astype(np.uint16))
+    for b in range(c.B):
+        for j in range(c.nodes[b]):
+            t = c.starts[b] + j
+            want, tol = _bounds(q[t], np.stack([c.pools[d][s] for d, s in c.keys(b, j, -1)]))
+            err = np.abs(got[t].cpu().double().numpy() - want)
+            assert np.all(err <= tol), (b, j, (err / tol).max())
+
+
+def test_the_bounds_tell_rounded_keys_apart():
+    """Keys rounded to fp16 would be outside them."""
+    c = Case("cpu", "fp8", nodes=[2], ctx=[130], H=16, bs=16, seed=1)
+    q = bf16_bits_to_f64(c.q.view(torch.int16).numpy().astype(np.uint16))
+    raw = np.stack([c.pools[d][s] for d, s in c.keys(0, 1, -1)])
+    want, tol = _bounds(q[1], raw)
+    lat, rope = so.parse(raw)
+    s = SCALE * q[1] @ np.concatenate([lat.astype(np.float16), rope], axis=1).astype(np.float64).T
+    off = np.abs(np.log(np.exp(s - s.max(axis=1, keepdims=True)).sum(axis=1)) + s.max(axis=1) - want)
+    assert off.max() > 1.5 * tol.max()
