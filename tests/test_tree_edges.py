@@ -179,12 +179,16 @@ def test_log_sums_are_as_good_as_fp32_sums(cuda_device, kw, what):
 
 
 def test_the_bounds_tell_rounded_keys_apart():
-    """Keys rounded to fp16 would be outside them."""
-    c = Case("cpu", "fp8", nodes=[2], ctx=[130], H=16, bs=16, seed=1)
+    """Keys rounded to fp16 would be outside them where a node sees few keys (over
+    many their errors cancel, and the bounds' worst case does not)."""
+    c = Case("cpu", "fp8", nodes=[5], ctx=[0], H=37, bs=16, seed=5)  # as one of the cases above
     q = bf16_bits_to_f64(c.q.view(torch.int16).numpy().astype(np.uint16))
-    raw = np.stack([c.pools[d][s] for d, s in c.keys(0, 1, -1)])
-    want, tol = _bounds(q[1], raw)
-    lat, rope = so.parse(raw)
-    s = SCALE * q[1] @ np.concatenate([lat.astype(np.float16), rope], axis=1).astype(np.float64).T
-    off = np.abs(np.log(np.exp(s - s.max(axis=1, keepdims=True)).sum(axis=1)) + s.max(axis=1) - want)
-    assert off.max() > 1.5 * tol.max()
+    worst = 0
+    for j in range(5):
+        raw = np.stack([c.pools[d][s] for d, s in c.keys(0, j, -1)])
+        want, tol = _bounds(q[j], raw)
+        lat, rope = so.parse(raw)
+        s = SCALE * q[j] @ np.concatenate([lat.astype(np.float16), rope], axis=1).astype(np.float64).T
+        off = np.log(np.exp(s - s.max(axis=1, keepdims=True)).sum(axis=1)) + s.max(axis=1) - want
+        worst = max(worst, (np.abs(off) / tol).max())
+    assert worst > 2
