@@ -272,7 +272,9 @@ class Fp8Projections:
       w_o [E, H * V]          the heads' values together
 
     ``query`` and ``output`` launch on one stream, read nothing back and reuse
-    their results' buffers.
+    their results' buffers.  ``query`` rotates by torch's own operators, a dozen
+    launches with temporaries behind the products; the products and ``output``
+    allocate nothing.
     """
 
     def __init__(self, w_q: capi.Fp8Rows, w_k: capi.Fp8Rows, w_v: capi.Fp8Rows, w_o: capi.Fp8Rows,
@@ -319,6 +321,8 @@ class Fp8Projections:
         mla_cache_write rotates a row's; a position outside it takes its
         nearest entry, where that call reports an error)."""
         T, H, P = self._count(x.shape[0]), self.H, self.P
+        if self.cos_sin is not None and (positions is None or positions.shape != (T,)):
+            raise ValueError(f"a position for each of the {T} rows is needed to rotate them")
         heads, q = self.heads[:T], self.q[:T]
         self._product(x, self._rows(self.x8, T), self.w_q, heads.view(T, H * (P + self.rope)))
         self._product(heads[..., :P].transpose(0, 1), self._rows(self.part8, T), self.w_k,
