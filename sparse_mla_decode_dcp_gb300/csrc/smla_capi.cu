@@ -649,7 +649,6 @@ static smla_status tree_decode(
   a.out = out;
   a.lse = lse;
   a.workspace = workspace;
-  a.workspace_bytes = workspace_bytes;
   return from_cuda(smla::launch_tree_decode(a, keys, format == SMLA_CACHE_FP4, static_cast<cudaStream_t>(stream)));
 }
 

@@ -63,7 +63,6 @@ struct TreeDecodeArgs {
   uint16_t* out;               // bf16 [T, H, 512]
   float* lse;                  // [T, H]
   void* workspace;
-  size_t workspace_bytes;
   // set by the launcher
   int32_t split;               // a tile of rows may be cut into key ranges
   int32_t min_units;           // key tiles a pair takes at least
