@@ -737,7 +737,7 @@ smla_status smla_tree_maps(const int32_t* parents, const int32_t* row_start,
  *     which smla_mla_cache_move brings the accepted ones).
  * with the attention of smla_sparse_mla_decode over those cache rows.  Over
  * 8-bit rows the scores are sums of exact products (of q's latent values those
- * below 2^-10 of the row's largest are taken to within 2^-17 of it), scaled in
+ * below 2^-10 of the largest of them are taken to within 2^-17 of it), scaled in
  * fp32, so lse is good to fp32 sums; values and probabilities round to fp16.
  * A row with nothing to attend is written as (0, -inf).  Rows of out and lse that
  * belong to no request (behind row_start[B], padding) are left as they were.

@@ -46,7 +46,7 @@
 //     maximum and sum), which a second kernel merges.
 //
 // A key tile takes 1.7 us of a pair (8-bit rows; 4-bit ones 1.9): a batch of 32
-// requests of 16 nodes, 128 heads and 2,048 to 32,768 positions 2.02 ms, 800
+// requests of 16 nodes, 128 heads and 2,048 to 32,768 positions 2.07 ms, 780
 // TFLOP/s.  Its MMAs alone take 0.75 us.  What bounds it is the shared-memory data
 // pipe, nearly always busy (two thirds for the warps: value tiles, scales,
 // copies; a third for the tensor cores' operands), and so the softmax, a chain of
