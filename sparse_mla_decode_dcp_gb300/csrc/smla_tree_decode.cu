@@ -1306,7 +1306,7 @@ __device__ void softmax_rows(const TreeDecodeArgs& a, uint8_t* sm, TreeCtl* ctl,
     const int64_t place = partial ? int64_t(it.part) * kPairRows + row : out_row;
     if (live && half == 0 && part == 0) {
       if (partial) {
-        a.ws_ml[2 * place] = m_ref * c2;
+        a.ws_ml[2 * place] = m_ref;
         a.ws_ml[2 * place + 1] = l;
       } else {
         a.lse[place] = l == 0.f ? -INFINITY : (m_ref * c2 + log2f(l)) * kLn2;
@@ -1499,10 +1499,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTreeThreads, 1)
   cluster_sync();
 }
 
-// Merges the row tiles that were cut: with m and l the parts' log2-domain
-// references and sums, M = max m over the parts that hold a key, out = sum l
-// 2^(m - M) O / sum l 2^(m - M).  One warp a row, 16 value dims a lane, parts
-// in the order of their keys.
+// Merges the row tiles that were cut: with m and l the parts' references (scores)
+// and sums, M = max m over the parts that hold a key, out = sum l 2^(c2 (m - M)) O
+// / sum l 2^(c2 (m - M)).  One warp a row, 16 value dims a lane, parts in the order
+// of their keys.
 constexpr int kMergeWarps = 8;
 constexpr int kMergeBlocks = kPairRows / kMergeWarps;
 
@@ -1522,6 +1522,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float c2 = a.sm_scale * kLog2e;
   float sum = 0.f, acc[16] = {};
 #pragma unroll 4
   for (int i = 0; i < t.parts; ++i) {
@@ -1529,7 +1530,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
     const float m = a.ws_ml[2 * p], l = a.ws_ml[2 * p + 1];
     const uint4* src = reinterpret_cast<const uint4*>(a.ws_o + p * SMLA_V_DIM + 16 * lane);
     const uint4 lo = src[0], hi = src[1];
-    const float w = l == 0.f ? 0.f : l * exp2f(m - top);
+    const float w = l == 0.f ? 0.f : l * exp2f((m - top) * c2);
     sum += w;
     const uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
@@ -1549,7 +1550,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
   uint4* dst = reinterpret_cast<uint4*>(a.out + (int64_t(t.row) + row) * SMLA_V_DIM + 16 * lane);
   dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
   dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-  if (lane == 0) a.lse[int64_t(t.row) + row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  if (lane == 0) a.lse[int64_t(t.row) + row] = sum == 0.f ? -INFINITY : (top * c2 + log2f(sum)) * kLn2;
 }
 
 // How a call is laid out, from its shape alone: its pairs, and whether a row
