@@ -328,3 +328,45 @@ def test_drafting_server_under_its_window(cuda_device, fmt, first):
     got, want = (s.run(_i32(ctx + 1, dev), kv, q) for s in (step, other))
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert _err() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("length", [2 ** 30, 2 ** 30 - 37])
+@pytest.mark.parametrize("D,rank", [(1, -1), (4, -1), (4, 3)])
+def test_the_longest_prefix(cuda_device, fmt, length, D, rank):
+    """Only the sinks' and the window's blocks exist, far apart in the table."""
+    bs, window, sinks, H, n, I = 2 ** 18, 100, 9, 16, 5, 3
+    c = Windowed(cuda_device, fmt, window, sinks, nodes=[n], ctx=[40], H=H, D=D, bs=64, I=I, rank=rank, seed=1,
+                 shapes=("chain",))
+    rng = np.random.default_rng(2)
+    local = lambda p: (p // I % D, p // (I * D) * I + p % I)  # noqa: E731
+    cached = {p: c.pools[0][rng.integers(len(c.pools[0]))] for p in (*range(sinks), *range(length - window, length))}
+    width = 2 ** 30 // (D * bs) + 2
+    pools, tables, drafts = [], [], []
+    for d in range(D):
+        pool = torch.zeros((3 * bs + n, c.pools[0].shape[1]), dtype=torch.uint8, device=cuda_device)
+        table = np.full((1, width), -1, dtype=np.int32)
+        cols = sorted({local(p)[1] // bs for p in cached if local(p)[0] == d})
+        assert len(cols) <= 3
+        table[0, cols] = np.arange(len(cols))
+        for p, row in cached.items():
+            e, lp = local(p)
+            if e == d:
+                pool[int(table[0, lp // bs]) * bs + lp % bs] = torch.from_numpy(row.copy()).to(cuda_device)
+        own = np.array([3 * bs + j if local(length + j)[0] == d else -1 for j in range(n)])
+        for j in np.flatnonzero(own >= 0):
+            pool[own[j]] = torch.from_numpy(c.pools[0][j].copy()).to(cuda_device)
+        pools.append(pool), tables.append(_i32(table, cuda_device)), drafts.append(_i32(own, cuda_device))
+    _err()
+    out, lse = capi.dcp_tree_mla_decode(
+        c.q.to(cuda_device), _i32([0, n], cuda_device), _i32([length], cuda_device), 2 ** 30,
+        torch.from_numpy(c.masks.view(np.int64)).to(cuda_device), c.max_nodes, drafts, pools, tables, bs, SCALE,
+        rank=rank, interleave=I, window=window, sinks=sinks, positions=_i32(length + np.arange(n), cuda_device))
+    assert _err() == 0
+    for j in range(n):
+        mine = lambda t: rank < 0 or local(t)[0] == rank  # noqa: E731
+        rows = [row for t, row in cached.items() if mine(t) and (t < sinks or t > length + j - window)]
+        rows += [c.pools[0][m] for m in range(j + 1) if mine(length + m)]
+        o, l, o_tol, l_tol = so.attend(_f64(c.q[j]), np.stack(rows), SCALE, KEY_STEP[fmt])
+        assert np.all(np.abs(_f64(out[j]) - o) <= o_tol) and np.all(np.abs(_np(lse[j].double()) - l) <= l_tol), j
