@@ -39,7 +39,7 @@
 //     none of its nodes sees: a key has the last position that sees it, and only
 //     tiles with keys that some node no longer sees compare.  The batch below with
 //     a window of 4,096 and 4 sinks: 0.82 ms; with one that leaves out a node's
-//     last few keys alone 2.34 (the look-up of a key's row and the code cost 15%).
+//     last few keys alone 2.34 (the look-up of a key's row and the code cost 13%).
 //   * All requests' (row tile, key tile) units form one line that is cut into
 //     equal ranges, one a pair, so that ragged batches fill the GPU.  A row
 //     tile that a cut falls into leaves partial results (fp16, with their
